@@ -27,7 +27,9 @@ __all__ = ["TV_OK", "TV_ERR_BAD_TREE", "TV_ERR_OUT_OF_RANGE", "TV_ERR_UNSUPPORTE
            "tree_verify_attention",
            "tree_verify_attention_noalloc", "tree_verify_attention_noalloc_capacity",
            "tree_accept_workspace",
-           "tree_accept", "kv_compact", "draft_tree_workspace", "draft_tree_expand"]
+           "tree_accept", "kv_compact", "draft_tree_workspace", "draft_tree_expand",
+           "RopeTable", "rope_table", "chunk_kv_append", "chunk_attention_workspace",
+           "chunk_attention", "token_counts_update", "tree_logits_process"]
 
 (TV_OK, TV_ERR_INVALID_ARG, TV_ERR_BAD_TREE, TV_ERR_OUT_OF_RANGE, TV_ERR_UNSUPPORTED,
  TV_ERR_CUDA, TV_ERR_TIMEOUT, TV_ERR_BAD_VALUES, TV_ERR_WORKSPACE) = range(9)
@@ -83,6 +85,16 @@ _compact = _sig("kv_compact", _i,
 _draft_ws = _sig("draft_tree_workspace", _sz, [_i, _i, _i])
 _draft_expand = _sig("draft_tree_expand", _i, [_p, _p, _i, _i, _i, _i, _i, _i, _p, _p, _p, _p,
                                                _p, _p, _p, _sz, _p])
+
+_rope_init = _sig("rope_table_init", _i, [_p, _i, _i, ctypes.c_double, _i] + [ctypes.c_double] * 5)
+_chunk_append = _sig("chunk_kv_append", _i, [_p, _i64, _p, _i64, _p, _i64, _p, _i, _p, _p, _i, _i,
+                                             _i, _i, _p, _p, _i64, _p, _p, _p, _i, _i, _i, _i, _p,
+                                             _p])
+_chunk_attn_ws = _sig("chunk_attention_workspace", _sz, [_i, _i, _i, _i, _i, _i])
+_chunk_attn = _sig("chunk_attention", _i, [_p, _i64, _p, _p, _p, _i, _p, _p, _i, _i, _i, _i, _i,
+                                           _i, _i, _i, _f, _f, _i, _p, _i64, _p, _p, _sz, _p])
+_token_counts = _sig("token_counts_update", _i, [_p, _p, _p, _i, _i, _i, _i, _i, _p, _p])
+_tree_logits = _sig("tree_logits_process", _i, [_p, _i, _i, _i, _i] + [_p] * 10 + [_i, _p, _p, _p])
 
 assert _abi() == 2, "header / library ABI mismatch"
 
@@ -346,3 +358,196 @@ def draft_tree_expand(logits, layer, layers, status, workspace, *, topk, root_to
     _check(_draft_expand(_ptr(logits), _ptr(root_tokens), B, V, topk, layer, layers, N, _ptr(front_tokens),
                _ptr(front_src), _ptr(parents), _ptr(tokens), _ptr(scores), _ptr(status),
                _ptr(workspace), ws_bytes, _stream(stream)), "draft_tree_expand")
+
+
+# ---------------------------------------------------------------------------
+# chunks of new tokens, and the logits of a tree
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "bands": 2, "ramp": 3}
+
+
+class RopeTable(ctypes.Structure):
+    """Rotary frequencies (plain host data, see rope_table); dim columns are rotated."""
+    _fields_ = [("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("amplitude", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("turn", ctypes.c_uint64 * 128)]
+
+
+def rope_table(dim, *, theta: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+               factor: float = 1.0, original_len: float = 0.0, low: float = 0.0,
+               high: float = 0.0, amplitude: float = 0.0) -> RopeTable:
+    """The rotary positions of one model, made once: dim rotated columns of a head, pairs
+    (j, j + dim/2) or, interleaved, (2j, 2j + 1); scaling "none", "linear", "bands" or "ramp"
+    with its factor and original context length (formulas in the C header)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling is one of {sorted(ROPE_SCALINGS)}")
+    t = RopeTable()
+    _check(_rope_init(ctypes.addressof(t), dim, int(bool(interleaved)), float(theta),
+                      ROPE_SCALINGS[scaling], float(factor), float(original_len), float(low),
+                      float(high), float(amplitude)), "rope_table")
+    return t
+
+
+def _row_stride(t, dtype, name, heads, d, T):
+    """[T, heads, d] with contiguous heads and any row stride: the stride, in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != (T, heads, d):
+        raise ValueError(f"{name}: expected shape {(T, heads, d)}, got {tuple(t.shape)}")
+    s = t.stride()
+    if (d > 1 and s[2] != 1) or (heads > 1 and s[1] != d):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return s[0] if T > 1 else heads * d
+
+
+def _on_one_device(*tensors):
+    """The tensors' common device, which must be the current one (the library launches
+    there, and the caller's stream belongs to it)."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors passed to libtreeverify must live on the current CUDA device")
+
+
+def _paged(k_cache, v_cache, block_table, q_start, prefix_lens, status, dtype, Hkv, d):
+    """Checks shared by the chunk calls; returns (B, block size, blocks)."""
+    if k_cache.dim() != 4 or k_cache.shape[1] != Hkv or k_cache.shape[3] != d:
+        raise ValueError("the caches are [num_blocks, Hkv, block_size, d]")
+    _want(k_cache, dtype, "k_cache")
+    _want(v_cache, dtype, "v_cache", k_cache.shape)
+    _want(status, torch.int32, "status")
+    B = status.shape[0] if status.dim() == 1 else -1
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table is int32 [B, max_blocks_per_seq], status int32 [B]")
+    _want(block_table, torch.int32, "block_table")
+    _want(q_start, torch.int32, "q_start", (B + 1,))
+    _want(prefix_lens, torch.int32, "prefix_lens", (B,))
+    return B, k_cache.shape[2], k_cache.shape[0]
+
+
+def chunk_kv_append(q, k, v, k_cache, v_cache, block_table, q_start, prefix_lens, status, *,
+                    q_out=None, rope=None, positions=None, stream=None) -> None:
+    """A ragged batch of new tokens into the paged cache: k / v [T,Hkv,d] and (or None) q
+    [T,Hq,d], rows any stride apart; queries and keys rotated by ``rope`` (a RopeTable, or
+    None); q_out [T,Hq,d] (default: q in place); positions int32 [T] or None (prefix + row);
+    q_start int32 [B+1]; caches [num_blocks,Hkv,bs,d]; prefix_lens, status int32 [B]."""
+    if k.dim() != 3:
+        raise ValueError("k is [T, Hkv, d]")
+    T, Hkv, d = k.shape
+    dt = _dtype_code(k)
+    ks = _row_stride(k, k.dtype, "k", Hkv, d, T)
+    vs = _row_stride(v, k.dtype, "v", Hkv, d, T)
+    Hq, qs, qos = 1, 0, 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q is [T, Hq, d]")
+        Hq = q.shape[1]
+        q_out = q if q_out is None else q_out
+        qs = _row_stride(q, k.dtype, "q", Hq, d, T)
+        qos = _row_stride(q_out, k.dtype, "q_out", Hq, d, T)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    B, bs, blocks = _paged(k_cache, v_cache, block_table, q_start, prefix_lens, status, k.dtype,
+                           Hkv, d)
+    if positions is not None:
+        _want(positions, torch.int32, "positions", (T,))
+    if rope is not None and not isinstance(rope, RopeTable):
+        raise TypeError("rope: expected a RopeTable")
+    _on_one_device(q, k, v, q_out, k_cache, v_cache, block_table, q_start, prefix_lens, status,
+                   positions)
+    _check(_chunk_append(None if q is None else q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(),
+                         vs, _ptr(positions), T, _ptr(q_start), _ptr(prefix_lens), B, Hq, Hkv, d,
+                         None if rope is None else ctypes.addressof(rope),
+                         None if q is None else q_out.data_ptr(), qos, _ptr(k_cache),
+                         _ptr(v_cache), _ptr(block_table), block_table.shape[1], bs, blocks, dt,
+                         _ptr(status), _stream(stream)), "chunk_kv_append")
+
+
+def chunk_attention_workspace(T, B, Hq, Hkv, d, dtype=torch.bfloat16) -> int:
+    return int(_chunk_attn_ws(T, B, Hq, Hkv, d, TV_BF16 if dtype == torch.bfloat16 else TV_F32))
+
+
+def chunk_attention(q, k_cache, v_cache, block_table, q_start, prefix_lens, out, status,
+                    workspace=None, *, scale: float = 0.0, softcap: float = 0.0, window: int = 0,
+                    stream=None) -> None:
+    """Causal attention of a ragged batch of new tokens over the paged cache (prefix and the
+    chunk itself): q / out [T,Hq,d], rows any stride apart; caches [num_blocks,Hkv,bs,d];
+    q_start int32 [B+1]; prefix_lens, status int32 [B]; softcap > 0 caps the scores, window > 0
+    limits the keys of a token to itself and the window - 1 before it; workspace uint8 of
+    chunk_attention_workspace() bytes."""
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q is [T, Hq, d] and the caches [num_blocks, Hkv, block_size, d]")
+    T, Hq, d = q.shape
+    Hkv = k_cache.shape[1]
+    dt = _dtype_code(q)
+    qs = _row_stride(q, q.dtype, "q", Hq, d, T)
+    os_ = _row_stride(out, q.dtype, "out", Hq, d, T)
+    B, bs, blocks = _paged(k_cache, v_cache, block_table, q_start, prefix_lens, status, q.dtype,
+                           Hkv, d)
+    _on_one_device(q, k_cache, v_cache, block_table, q_start, prefix_lens, out, status, workspace)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_chunk_attn(q.data_ptr(), qs, _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
+                       block_table.shape[1], _ptr(q_start), _ptr(prefix_lens), T, B, Hq, Hkv, d,
+                       bs, blocks, dt, float(scale), float(softcap), int(window), out.data_ptr(),
+                       os_, _ptr(status), _ptr(workspace), ws_bytes, _stream(stream)),
+           "chunk_attention")
+
+
+def token_counts_update(counts, tokens, status, *, starts=None, clear: bool = False,
+                        prompt: bool = False, stream=None) -> None:
+    """Token histories counts int32 [B,V] (bit 31: in the prompt; below: times emitted):
+    tokens int32, [total] with starts int32 [B+1], or [B,W] without (-1 entries are skipped);
+    clear zeroes the rows first; prompt marks instead of counting; status int32 [B]."""
+    _want(counts, torch.int32, "counts")
+    if counts.dim() != 2:
+        raise ValueError("counts is int32 [B, V]")
+    B, V = counts.shape
+    _want(tokens, torch.int32, "tokens")
+    if starts is None:
+        if tokens.dim() != 2 or tokens.shape[0] != B:
+            raise ValueError("tokens is int32 [B, W], or [total] with starts")
+    else:
+        _want(starts, torch.int32, "starts", (B + 1,))
+        if tokens.dim() != 1:
+            raise ValueError("tokens is int32 [total] with starts")
+    _want(status, torch.int32, "status", (B,))
+    _on_one_device(counts, tokens, starts, status)
+    _check(_token_counts(_ptr(counts), _ptr(tokens), _ptr(starts), tokens.numel(), B, V,
+                         int(bool(clear)), int(bool(prompt)), _ptr(status), _stream(stream)),
+           "token_counts_update")
+
+
+def tree_logits_process(logits, out, status, *, probs: bool, mask=None, draft_tokens=None,
+                        counts=None, bias=None, grammar=None, repetition=None, frequency=None,
+                        presence=None, temperature=None, node_counts=None, stream=None) -> None:
+    """The target model's rows of a tree, logits float32 or bfloat16 [B,N,V], into what
+    tree_accept reads, out float32 [B,N,V]: probabilities (probs) or logits, after bias
+    [B,V], the penalties float32 [B] for tokens of the history (counts int32 [B,V]) and of
+    each node's path (mask int64 [B,N], draft_tokens int32 [B,N]), the temperature float32 [B]
+    and the grammar bits int32 [B,N,ceil(V/32)]; all of them optional; status int32 [B]."""
+    if logits.dim() != 3:
+        raise ValueError("logits is [B, N, V]")
+    B, N, V = logits.shape
+    dt = _dtype_code(logits)
+    _want(out, torch.float32, "out", (B, N, V))
+    _want(status, torch.int32, "status", (B,))
+    for t, n, dtype, shape in ((mask, "mask", torch.int64, (B, N)),
+                               (draft_tokens, "draft_tokens", torch.int32, (B, N)),
+                               (counts, "counts", torch.int32, (B, V)),
+                               (bias, "bias", torch.float32, (B, V)),
+                               (grammar, "grammar", torch.int32, (B, N, (V + 31) // 32)),
+                               (repetition, "repetition", torch.float32, (B,)),
+                               (frequency, "frequency", torch.float32, (B,)),
+                               (presence, "presence", torch.float32, (B,)),
+                               (temperature, "temperature", torch.float32, (B,))):
+        if t is not None:
+            _want(t, dtype, n, shape)
+    _on_one_device(logits, out, status, mask, draft_tokens, counts, bias, grammar, repetition,
+                   frequency, presence, temperature, node_counts)
+    _check(_tree_logits(_ptr(logits), dt, B, N, V, _counts(node_counts, B), _ptr(mask),
+                        _ptr(draft_tokens), _ptr(counts), _ptr(bias), _ptr(grammar),
+                        _ptr(repetition), _ptr(frequency), _ptr(presence), _ptr(temperature),
+                        int(bool(probs)), _ptr(out), _ptr(status), _stream(stream)),
+           "tree_logits_process")

@@ -292,4 +292,187 @@ tv_status draft_tree_expand(const float* logits, const int32_t* root_tokens, int
     return launch_draft_expand(a);
 }
 
+static bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+
+tv_status rope_table_init(tv_rope_table* table, int dim, int interleaved, double theta,
+                          tv_rope_scaling scaling, double factor, double original_len, double low,
+                          double high, double amplitude) {
+    return make_rope_table(table, dim, interleaved, theta, scaling, factor, original_len, low, high,
+                           amplitude);
+}
+
+tv_status chunk_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                          const void* v, int64_t v_stride, const int32_t* positions, int T,
+                          const int32_t* q_start, const int32_t* prefix_lens, int B, int Hq,
+                          int Hkv, int d, const tv_rope_table* rope, void* q_out,
+                          int64_t q_out_stride, void* k_cache, void* v_cache,
+                          const int32_t* block_table, int max_blocks_per_seq, int block_size,
+                          int num_blocks, tv_dtype dt, int32_t* status, tv_stream_t stream) {
+    if (dt != TV_F32 && dt != TV_BF16) return TV_ERR_INVALID_ARG;
+    const int eb = dt == TV_F32 ? 4 : 2;
+    if (T < 0 || B < 0 || Hq < 1 || Hkv < 1 || d < 1 || block_size < 1 || num_blocks < 1 ||
+        max_blocks_per_seq < 1)
+        return TV_ERR_INVALID_ARG;
+    if ((int64_t)Hq * d > 0x7fffffff || (int64_t)Hkv * d > 0x7fffffff) return TV_ERR_UNSUPPORTED;
+    if (rope && (rope->dim < 2 || rope->dim > TV_ROPE_MAX_DIM || rope->dim > d))
+        return TV_ERR_INVALID_ARG;
+    if ((d * eb) % 16 != 0 || (rope && (rope->dim * eb) % 32 != 0)) return TV_ERR_UNSUPPORTED;
+    if (B == 0) return TV_OK;
+    if (!q_start || !prefix_lens || !block_table || !status || !k_cache || !v_cache ||
+        (q == nullptr) != (q_out == nullptr))
+        return TV_ERR_INVALID_ARG;
+    if (T > 0) {
+        if (!k || !v || k_stride < (int64_t)Hkv * d || v_stride < (int64_t)Hkv * d ||
+            (q && (q_stride < (int64_t)Hq * d || q_out_stride < (int64_t)Hq * d)))
+            return TV_ERR_INVALID_ARG;
+        if ((k_stride * eb) % 16 || (v_stride * eb) % 16 ||
+            (q && ((q_stride * eb) % 16 || (q_out_stride * eb) % 16)))
+            return TV_ERR_UNSUPPORTED;
+    }
+    if (misaligned(q) || misaligned(k) || misaligned(v) || misaligned(q_out) ||
+        misaligned(k_cache) || misaligned(v_cache))
+        return TV_ERR_INVALID_ARG;
+    ChunkAppendArgs a;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.positions = positions;
+    a.T = T;
+    a.q_start = q_start;
+    a.prefix_lens = prefix_lens;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.d = d;
+    a.rope = rope;
+    a.q_out = q_out;
+    a.q_out_stride = q_out_stride;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks_per_seq;
+    a.bs = block_size;
+    a.num_blocks = num_blocks;
+    a.elem = eb;
+    a.status = status;
+    a.stream = (cudaStream_t)stream;
+    return launch_chunk_append(a);
+}
+
+static bool chunk_attn_shape_ok(int Hq, int Hkv, int d, tv_dtype dt) {
+    if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return false;
+    if (dt == TV_BF16) return d == 64 || d == 128;
+    return dt == TV_F32 && d >= 32 && d <= 256 && d % 32 == 0;
+}
+
+size_t chunk_attention_workspace(int T, int B, int Hq, int Hkv, int d, tv_dtype dt) {
+    if (T < 1 || B < 1 || !chunk_attn_shape_ok(Hq, Hkv, d, dt)) return 0;
+    return chunk_attn_f32_workspace(T, B, Hq, Hkv, d);
+}
+
+tv_status chunk_attention(const void* q, int64_t q_stride, const void* k_cache,
+                          const void* v_cache, const int32_t* block_table,
+                          int max_blocks_per_seq, const int32_t* q_start,
+                          const int32_t* prefix_lens, int T, int B, int Hq, int Hkv, int d,
+                          int block_size, int num_blocks, tv_dtype dt, float scale, float softcap,
+                          int window, void* out, int64_t out_stride, int32_t* status,
+                          void* workspace, size_t workspace_bytes, tv_stream_t stream) {
+    if (dt != TV_F32 && dt != TV_BF16) return TV_ERR_INVALID_ARG;
+    if (T < 0 || B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_blocks_per_seq < 1 ||
+        block_size < 1 || num_blocks < 1 || !(softcap == softcap) || isinf(softcap))
+        return TV_ERR_INVALID_ARG;
+    if (!chunk_attn_shape_ok(Hq, Hkv, d, dt) || (dt == TV_BF16 && block_size % 16 != 0))
+        return TV_ERR_UNSUPPORTED;
+    if (B == 0) return TV_OK;
+    if (!q_start || !prefix_lens || !block_table || !status) return TV_ERR_INVALID_ARG;
+    const int eb = dt == TV_F32 ? 4 : 2;
+    if (T > 0) {
+        if (!q || !out || !k_cache || !v_cache || q_stride < (int64_t)Hq * d ||
+            out_stride < (int64_t)Hq * d)
+            return TV_ERR_INVALID_ARG;
+        if ((q_stride * eb) % 16 || (out_stride * eb) % 16) return TV_ERR_UNSUPPORTED;
+    }
+    if (misaligned(q) || misaligned(out) || misaligned(k_cache) || misaligned(v_cache))
+        return TV_ERR_INVALID_ARG;
+    const size_t need = chunk_attention_workspace(T, B, Hq, Hkv, d, dt);
+    if (need > 0 && (!workspace || misaligned(workspace) || workspace_bytes < need))
+        return TV_ERR_WORKSPACE;
+    ChunkAttnArgs a;
+    a.q = q;
+    a.q_stride = q_stride;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks_per_seq;
+    a.q_start = q_start;
+    a.prefix_lens = prefix_lens;
+    a.T = T;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.d = d;
+    a.bs = block_size;
+    a.num_blocks = num_blocks;
+    a.dt = dt;
+    a.scale = (scale > 0.f && isfinite(scale)) ? scale : 1.0f / sqrtf((float)d);
+    a.softcap = softcap > 0.f ? softcap : 0.f;
+    a.window = window > 0 ? window : 0;
+    a.out = out;
+    a.out_stride = out_stride;
+    a.status = status;
+    a.ws = workspace;
+    a.stream = (cudaStream_t)stream;
+    return launch_chunk_attn_f32(a);
+}
+
+tv_status token_counts_update(int32_t* counts, const int32_t* tokens, const int32_t* starts,
+                              int total, int B, int V, int clear, int prompt, int32_t* status,
+                              tv_stream_t stream) {
+    if (B < 0 || V < 1 || V > (1 << 24) || total < 0) return TV_ERR_INVALID_ARG;
+    if (B == 0) return TV_OK;
+    if (!counts || !status || (total > 0 && !tokens) || (!starts && total % B != 0))
+        return TV_ERR_INVALID_ARG;
+    return launch_token_counts(counts, tokens, starts, total, B, V, clear != 0, prompt != 0, status,
+                               (cudaStream_t)stream);
+}
+
+tv_status tree_logits_process(const void* logits, tv_dtype dt, int B, int N, int V,
+                              const int32_t* node_counts, const uint64_t* mask,
+                              const int32_t* draft_tokens, const int32_t* counts,
+                              const float* bias, const uint32_t* grammar,
+                              const float* repetition, const float* frequency,
+                              const float* presence, const float* temperature, int probs,
+                              float* out, int32_t* status, tv_stream_t stream) {
+    if (dt != TV_F32 && dt != TV_BF16) return TV_ERR_INVALID_ARG;
+    if (B < 0 || N < 1 || N > 64 || V < 1 || V > (1 << 24)) return TV_ERR_INVALID_ARG;
+    if (B == 0) return TV_OK;
+    if (!logits || !out || !status || (mask == nullptr) != (draft_tokens == nullptr))
+        return TV_ERR_INVALID_ARG;
+    if (!counts && (repetition || frequency || presence)) return TV_ERR_INVALID_ARG;
+    LogitsArgs a;
+    a.logits = logits;
+    a.dt = dt;
+    a.B = B;
+    a.N = N;
+    a.V = V;
+    a.node_counts = node_counts;
+    a.mask = mask;
+    a.tokens = draft_tokens;
+    a.counts = counts;
+    a.bias = bias;
+    a.grammar = grammar;
+    a.rep = repetition;
+    a.freq = frequency;
+    a.pres = presence;
+    a.temp = temperature;
+    a.probs = probs != 0;
+    a.out = out;
+    a.status = status;
+    a.stream = (cudaStream_t)stream;
+    return launch_tree_logits(a);
+}
+
 }  // extern "C"

@@ -1,0 +1,384 @@
+// chunk_attention on the CUDA cores: float32 (and bfloat16 when a kv head has
+// more query heads than a tensor-core row tile holds).
+//
+// The online softmax over key tiles, everything in float32: a CTA owns 64 rows
+// of one (sequence, kv head) (row r is token r / G, head r % G of the kv head's G
+// = Hq / Hkv query heads, so a K/V row is read once for all of them) and walks
+// 64-key tiles: S = Q K^T, running maximum and sum, O = O 2^(m - m') + P V.
+// Bound by float32 multiply-adds: 4 d per (row, key).  128 threads, each an 8 x 4
+// patch of S and an 8 x d/16 patch of O in registers, so that a step of the
+// inner loops is 12 shared-memory loads of 16 bytes for 128 multiply-adds.
+// When the rows are too few to fill the GPU the keys are cut into up to 16
+// parts; each part leaves its unnormalised O, maximum and sum in the workspace
+// and a second kernel joins them in order.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "tv_chunk.cuh"
+#include "tv_internal.h"
+
+namespace tv {
+
+namespace {
+
+constexpr int CF_THREADS = 128;
+constexpr int CF_M = 64, CF_N = 64;  // rows, keys per tile
+constexpr float CF_LOG2E = 1.4426950408889634f;
+
+struct CfParams {
+    ChunkView c;
+    const void *q, *k, *v;
+    void* out;
+    int64_t q_stride, o_stride;   // elements
+    int32_t* status;
+    float* part;                  // [tiles][Hkv][splits] x (64 x d, 64 maxima, 64 sums)
+    int Hq, Hkv, G, d, window, splits, tiles;
+    float scale, softcap;
+};
+
+template <typename E>
+__device__ __forceinline__ float4 cf_load4(const E* p);
+template <>
+__device__ __forceinline__ float4 cf_load4<float>(const float* p) {
+    return *reinterpret_cast<const float4*>(p);
+}
+template <>
+__device__ __forceinline__ float4 cf_load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void cf_store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void cf_store4(__nv_bfloat16* p, float4 v) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
+__device__ __forceinline__ int64_t cf_tiles(const CfParams& p, int b) {
+    return ((int64_t)(p.c.q_start[b + 1] - p.c.q_start[b]) * p.G + CF_M - 1) / CF_M;
+}
+
+// The row tile of this CTA.
+struct CfTile {
+    int b, s, n, P, tile;   // sequence, first row, rows, prefix, tile within the sequence
+    bool ok;                // the sequence passed its check
+};
+
+// false: no such tile.  Called by every thread (contains barriers).
+__device__ __forceinline__ bool cf_find(const CfParams& p, int tile, CfTile& t) {
+    const ChunkPlace at = chunk_locate<CF_THREADS>(p.c.B, tile, [&](int b) { return cf_tiles(p, b); });
+    if (at.b >= p.c.B) return false;
+    t.b = at.b;
+    t.s = p.c.q_start[at.b];
+    t.n = p.c.q_start[at.b + 1] - t.s;
+    t.P = p.c.prefix[at.b];
+    t.tile = tile - (int)at.base;
+    bool ok = chunk_shape_ok(p.c, t.P, t.n);
+    if (ok) ok = chunk_blocks_ok(p.c, t.b, chunk_first_key(t.P, p.window), (int64_t)t.P + t.n, threadIdx.x, CF_THREADS);
+    t.ok = __syncthreads_and(ok ? 1 : 0) != 0;
+    return true;
+}
+
+// NC: groups of 64 head columns (columns from d on are zero).
+template <typename E, int NC>
+__global__ void __launch_bounds__(CF_THREADS) chunk_attn_kernel(CfParams p) {
+    constexpr int DP = NC * 64, LD = DP + 4;
+    extern __shared__ __align__(16) float sm[];
+    float* sq = sm;                    // [64][LD]
+    float* sk = sq + CF_M * LD;        // [64][LD]
+    float* sv = sk + CF_N * LD;        // [64][DP]
+    float* sp = sk;                    // P [64][64 + 4] takes K's place once S is done
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int tile_id = (int)(blockIdx.x / p.splits), split = (int)(blockIdx.x % p.splits);
+    const int g = blockIdx.y;
+    const bool valid = chunk_starts_ok(p.c);
+    if (blockIdx.x == 0 && g == 0)
+        for (int b = tid; b < p.c.B; b += CF_THREADS)
+            if (!valid || p.c.q_start[b] == p.c.q_start[b + 1])
+                p.status[b] = (valid && chunk_shape_ok(p.c, p.c.prefix[b], 0)) ? TV_OK
+                                                                               : TV_ERR_OUT_OF_RANGE;
+    if (!valid) return;
+    CfTile t;
+    if (!cf_find(p, tile_id, t)) return;
+    if (t.tile == 0 && g == 0 && split == 0 && tid == 0)
+        p.status[t.b] = t.ok ? TV_OK : TV_ERR_OUT_OF_RANGE;
+    const int r0 = t.tile * CF_M, rows = min(CF_M, t.n * p.G - r0);
+    const int i_lo = r0 / p.G, i_hi = (r0 + rows - 1) / p.G;   // first and last token
+    // keys of the tile's rows, from the first row's window to the last row itself
+    const int k_lo = t.ok ? chunk_first_key(t.P + i_lo, p.window) : 0;
+    const int k_hi = t.ok ? t.P + i_hi + 1 : 0;
+    const int nt = (k_hi - k_lo + CF_N - 1) / CF_N;
+    const int j0 = (int)((int64_t)nt * split / p.splits), j1 = (int)((int64_t)nt * (split + 1) / p.splits);
+    const E* q = static_cast<const E*>(p.q);
+    const E* kc = static_cast<const E*>(p.k);
+    const E* vc = static_cast<const E*>(p.v);
+    const int d4 = p.d / 4;
+    for (int e = tid; e < CF_M * (DP / 4); e += CF_THREADS) {
+        const int r = e / (DP / 4), c = e % (DP / 4);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows && c < d4)
+            x = cf_load4<E>(q + (int64_t)(t.s + (r0 + r) / p.G) * p.q_stride +
+                            (int64_t)(g * p.G + (r0 + r) % p.G) * p.d + 4 * c);
+        *reinterpret_cast<float4*>(sq + r * LD + 4 * c) = x;
+    }
+    float o[8][NC][4], m[8], l[8];
+    int last[8];                       // the row's own position
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+        last[i] = t.P + (r0 + min(ty * 8 + i, rows - 1)) / p.G;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][c][e] = 0.f;
+    }
+    for (int j = j0; j < j1; ++j) {
+        const int t0 = k_lo + j * CF_N;
+        __syncthreads();               // the previous tile's P and V are done with
+        for (int e = tid; e < CF_N * (DP / 4); e += CF_THREADS) {
+            const int r = e / (DP / 4), c = e % (DP / 4);
+            const int key = t0 + r;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+            if (key < k_hi && c < d4) {
+                const int64_t blk = p.c.table[(int64_t)t.b * p.c.max_blocks + key / p.c.bs];
+                const int64_t at = ((blk * p.Hkv + g) * p.c.bs + key % p.c.bs) * p.d + 4 * c;
+                x = cf_load4<E>(kc + at);
+                y = cf_load4<E>(vc + at);
+            }
+            *reinterpret_cast<float4*>(sk + r * LD + 4 * c) = x;
+            *reinterpret_cast<float4*>(sv + r * DP + 4 * c) = y;
+        }
+        __syncthreads();
+        // S: rows ty * 8 + i, keys tx + 16 u
+        float s[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) s[i][u] = 0.f;
+        for (int c = 0; c < p.d; c += 4) {
+            float4 b4[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) b4[u] = *reinterpret_cast<const float4*>(sk + (tx + 16 * u) * LD + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float4 a4 = *reinterpret_cast<const float4*>(sq + (ty * 8 + i) * LD + c);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    s[i][u] = fmaf(a4.x, b4[u].x, s[i][u]);
+                    s[i][u] = fmaf(a4.y, b4[u].y, s[i][u]);
+                    s[i][u] = fmaf(a4.z, b4[u].z, s[i][u]);
+                    s[i][u] = fmaf(a4.w, b4[u].w, s[i][u]);
+                }
+            }
+        }
+        __syncthreads();               // every thread is done with K
+        // whether every key of the tile is visible to every row
+        const bool full = t0 + CF_N - 1 <= t.P + i_lo &&
+                          (p.window <= 0 || t0 > t.P + i_hi - p.window);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int key = t0 + tx + 16 * u;
+                float z = s[i][u] * p.scale;
+                if (p.softcap > 0.f) z = p.softcap * tanhf(z / p.softcap);
+                const bool seen = full || (key <= last[i] && (p.window <= 0 || key > last[i] - p.window));
+                s[i][u] = seen ? z * CF_LOG2E : -INFINITY;
+                mx = fmaxf(mx, s[i][u]);
+            }
+#pragma unroll
+            for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+            const float mn = fmaxf(m[i], mx), base = mn == -INFINITY ? 0.f : mn;
+            const float f = exp2f(m[i] - base);
+            m[i] = mn;
+            float sum = 0.f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                s[i][u] = exp2f(s[i][u] - base);
+                sum += s[i][u];
+                sp[(ty * 8 + i) * (CF_N + 4) + tx + 16 * u] = s[i][u];
+            }
+#pragma unroll
+            for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+            l[i] = l[i] * f + sum;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][c][e] *= f;
+        }
+        __syncwarp();                  // a row's P is written and read by one half warp
+        // O: columns 64 c + 4 tx + e
+        for (int k = 0; k < CF_N; k += 4) {
+            float4 a4[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                a4[i] = *reinterpret_cast<const float4*>(sp + (ty * 8 + i) * (CF_N + 4) + k);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const float4 v4 = *reinterpret_cast<const float4*>(sv + (k + kk) * DP + 64 * c + 4 * tx);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float w = kk == 0 ? a4[i].x : kk == 1 ? a4[i].y : kk == 2 ? a4[i].z : a4[i].w;
+                        // a masked key's value must not reach the row even if it is not finite
+                        if (full || w != 0.f) {
+                            o[i][c][0] = fmaf(w, v4.x, o[i][c][0]);
+                            o[i][c][1] = fmaf(w, v4.y, o[i][c][1]);
+                            o[i][c][2] = fmaf(w, v4.z, o[i][c][2]);
+                            o[i][c][3] = fmaf(w, v4.w, o[i][c][3]);
+                        }
+                    }
+                }
+            }
+        }
+    }
+    if (p.splits > 1) {
+        float* slot = p.part + (((int64_t)tile_id * p.Hkv + g) * p.splits + split) * (CF_M * (p.d + 2));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = ty * 8 + i;
+            if (r >= rows) continue;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                if (64 * c + 4 * tx < p.d)
+                    *reinterpret_cast<float4*>(slot + r * p.d + 64 * c + 4 * tx) =
+                        make_float4(o[i][c][0], o[i][c][1], o[i][c][2], o[i][c][3]);
+            if (tx == 0) {
+                slot[CF_M * p.d + r] = m[i];
+                slot[CF_M * (p.d + 1) + r] = l[i];
+            }
+        }
+        return;
+    }
+    E* out = static_cast<E*>(p.out);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = ty * 8 + i;
+        if (r >= rows) continue;
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+        E* row = out + (int64_t)(t.s + (r0 + r) / p.G) * p.o_stride + (int64_t)(g * p.G + (r0 + r) % p.G) * p.d;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            if (64 * c + 4 * tx < p.d)
+                cf_store4(row + 64 * c + 4 * tx, make_float4(o[i][c][0] * inv, o[i][c][1] * inv,
+                                                             o[i][c][2] * inv, o[i][c][3] * inv));
+    }
+}
+
+// Joins the parts of a row tile: weights 2^(m_k - max) on the unnormalised rows.
+template <typename E>
+__global__ void __launch_bounds__(CF_THREADS) chunk_join_kernel(CfParams p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int g = blockIdx.y, tid = threadIdx.x;
+    if (!chunk_starts_ok(p.c)) return;
+    const ChunkPlace at = chunk_locate<CF_THREADS>(p.c.B, blockIdx.x, [&](int b) { return cf_tiles(p, b); });
+    if (at.b >= p.c.B) return;
+    const int s = p.c.q_start[at.b], n = p.c.q_start[at.b + 1] - s;
+    const int r0 = ((int)blockIdx.x - (int)at.base) * CF_M, rows = min(CF_M, n * p.G - r0);
+    const int64_t step = CF_M * (p.d + 2);
+    const float* slot = p.part + ((int64_t)blockIdx.x * p.Hkv + g) * p.splits * step;
+    const int d4 = p.d / 4;
+    E* out = static_cast<E*>(p.out);
+    for (int e = tid; e < rows * d4; e += CF_THREADS) {
+        const int r = e / d4, c = e % d4;
+        float mx = -INFINITY;
+        for (int k = 0; k < p.splits; ++k) mx = fmaxf(mx, slot[k * step + CF_M * p.d + r]);
+        const float base = mx == -INFINITY ? 0.f : mx;
+        float den = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < p.splits; ++k) {
+            const float* pk = slot + k * step;
+            const float mk = pk[CF_M * p.d + r];
+            if (mk == -INFINITY && pk[CF_M * (p.d + 1) + r] == 0.f) continue;   // no key in this part
+            const float w = exp2f(mk - base);
+            const float4 x = *reinterpret_cast<const float4*>(pk + r * p.d + 4 * c);
+            den = fmaf(w, pk[CF_M * (p.d + 1) + r], den);
+            acc.x = fmaf(w, x.x, acc.x);
+            acc.y = fmaf(w, x.y, acc.y);
+            acc.z = fmaf(w, x.z, acc.z);
+            acc.w = fmaf(w, x.w, acc.w);
+        }
+        const float inv = den == 0.f ? 0.f : 1.f / den;
+        cf_store4(out + (int64_t)(s + (r0 + r) / p.G) * p.o_stride + (int64_t)(g * p.G + (r0 + r) % p.G) * p.d + 4 * c,
+                  make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    }
+}
+
+template <typename E, int NC>
+tv_status launch_nc(const CfParams& p, cudaStream_t stream) {
+    constexpr int DP = NC * 64;
+    const size_t smem = (size_t)(2 * CF_M * (DP + 4) + CF_N * DP) * 4;
+    static bool set[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TV_ERR_CUDA;
+    if (!set[dev]) {
+        if (cudaFuncSetAttribute(chunk_attn_kernel<E, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)smem) != cudaSuccess) {
+            cudaGetLastError();
+            return TV_ERR_CUDA;
+        }
+        set[dev] = true;
+    }
+    LaunchCfg lc(dim3((unsigned)(p.tiles * p.splits), (unsigned)p.Hkv), dim3(CF_THREADS), smem, stream);
+    if (cudaLaunchKernelEx(&lc.cfg, chunk_attn_kernel<E, NC>, p) != cudaSuccess) return TV_ERR_CUDA;
+    if (p.splits == 1) return TV_OK;
+    LaunchCfg lj(dim3((unsigned)p.tiles, (unsigned)p.Hkv), dim3(CF_THREADS), 0, stream);
+    return cudaLaunchKernelEx(&lj.cfg, chunk_join_kernel<E>, p) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+}
+
+// Upper bound of the row tiles per kv head, whatever q_start says, and the parts
+// that the keys are cut into.
+int64_t cf_tile_bound(int T, int B, int G) { return (int64_t)T * G / CF_M + std::min(T, B); }
+int cf_splits(int T, int B, int Hkv, int G) {
+    const int64_t ctas = std::max<int64_t>(1, cf_tile_bound(T, B, G) * Hkv);
+    return (int)std::clamp<int64_t>(4 * device_sm_count() / ctas, 1, 16);
+}
+
+}  // namespace
+
+size_t chunk_attn_f32_workspace(int T, int B, int Hq, int Hkv, int d) {
+    const int G = Hq / Hkv, s = cf_splits(T, B, Hkv, G);
+    return s == 1 ? 0 : (size_t)(cf_tile_bound(T, B, G) * Hkv) * s * CF_M * (d + 2) * sizeof(float);
+}
+
+tv_status launch_chunk_attn_f32(const ChunkAttnArgs& a) {
+    CfParams p{};
+    p.c = ChunkView{a.q_start, a.prefix_lens, a.block_table, a.T, a.B, a.max_blocks, a.bs, a.num_blocks};
+    p.q = a.q;
+    p.k = a.k_cache;
+    p.v = a.v_cache;
+    p.out = a.out;
+    p.q_stride = a.q_stride;
+    p.o_stride = a.out_stride;
+    p.status = a.status;
+    p.part = static_cast<float*>(a.ws);
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.G = a.Hq / a.Hkv;
+    p.d = a.d;
+    p.window = a.window;
+    p.scale = a.scale;
+    p.softcap = a.softcap;
+    const int64_t tiles = std::max<int64_t>(1, cf_tile_bound(a.T, a.B, p.G));
+    p.splits = cf_splits(a.T, a.B, a.Hkv, p.G);
+    if (tiles * p.splits > 0x7fffffff || a.Hkv > 65535) return TV_ERR_UNSUPPORTED;
+    p.tiles = (int)tiles;
+    const int nc = (a.d + 63) / 64;
+    if (a.dt == TV_BF16)
+        return nc == 1 ? launch_nc<__nv_bfloat16, 1>(p, a.stream) : launch_nc<__nv_bfloat16, 2>(p, a.stream);
+    switch (nc) {
+        case 1: return launch_nc<float, 1>(p, a.stream);
+        case 2: return launch_nc<float, 2>(p, a.stream);
+        case 3: return launch_nc<float, 3>(p, a.stream);
+        default: return launch_nc<float, 4>(p, a.stream);
+    }
+}
+
+}  // namespace tv

@@ -1,0 +1,113 @@
+// Device helpers for ragged chunks: the batch's row ranges (q_start), the keys
+// a sequence needs, and finding the sequence that holds a given unit of work.
+#pragma once
+
+#include "tv_device.cuh"
+
+namespace tv {
+
+struct ChunkView {
+    const int32_t* q_start;   // [B + 1]
+    const int32_t* prefix;    // [B]
+    const int32_t* table;     // [B][max_blocks]
+    int T, B, max_blocks, bs, num_blocks;
+};
+
+// Whether q_start is non-decreasing within [0, T].  Called by every thread of
+// the CTA; contains a barrier.
+__device__ __forceinline__ bool chunk_starts_ok(const ChunkView& c) {
+    bool ok = true;
+    for (int b = threadIdx.x; b < c.B; b += blockDim.x) {
+        const int s = c.q_start[b], e = c.q_start[b + 1];
+        ok = ok && s >= 0 && s <= e && e <= c.T;
+    }
+    return __syncthreads_and(ok ? 1 : 0) != 0;
+}
+
+// Positions stay below this, so that a tile past the last key still has an int32 position.
+constexpr int64_t CHUNK_POS_MAX = 0x7fffffffll - 1023;
+
+// Length part of a sequence's check: its P + n positions fit the block table.
+__device__ __forceinline__ bool chunk_shape_ok(const ChunkView& c, int P, int n) {
+    return P >= 0 && (int64_t)P + n <= min((int64_t)c.max_blocks * c.bs, CHUNK_POS_MAX);
+}
+
+// First key that some row of a sequence attends to (window <= 0: no window).
+__device__ __forceinline__ int chunk_first_key(int P, int window) {
+    return (window > 0 && P >= window) ? P - window + 1 : 0;
+}
+
+// This thread's share of the check of the blocks that hold positions lo .. hi-1
+// of sequence b (threads `id` of `count`); lo and hi inside the block table.
+__device__ __forceinline__ bool chunk_blocks_ok(const ChunkView& c, int b, int64_t lo, int64_t hi,
+                                                int id, int count) {
+    const int32_t* row = c.table + (int64_t)b * c.max_blocks;
+    const int j1 = (int)((hi + c.bs - 1) / c.bs);
+    bool ok = true;
+    // independent loads, four in flight
+    for (int j = (int)(lo / c.bs) + id; j < j1; j += 4 * count) {
+        int blk[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) blk[u] = (j + u * count < j1) ? row[j + u * count] : 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) ok = ok && blk[u] >= 0 && blk[u] < c.num_blocks;
+    }
+    return ok;
+}
+
+// Finds the sequence that holds unit x when sequence b has cost(b) units and the
+// sequences are laid end to end.  Called by every thread of the CTA (THREADS of
+// them); each thread sums a contiguous run of sequences, then the block scans.
+struct ChunkPlace {
+    int64_t total;  // units of all sequences
+    int64_t base;   // first unit of sequence b
+    int b;          // B when x >= total
+};
+
+template <int THREADS, class Cost>
+__device__ __forceinline__ ChunkPlace chunk_locate(int B, int64_t x, Cost cost) {
+    __shared__ int64_t warp_sum[THREADS / 32];
+    __shared__ int64_t found_base;
+    __shared__ int found_b;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (B + THREADS - 1) / THREADS;
+    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    int64_t s = 0;
+    for (int b = b0; b < b1; ++b) s += cost(b);
+    int64_t incl = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    __syncthreads();  // the previous use of the shared words is over
+    if (lane == 31) warp_sum[warp] = incl;
+    if (tid == 0) found_b = B;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        total += warp_sum[w];
+    }
+    int64_t at = before + incl - s;
+    if (x >= at && x < at + s) {
+        for (int b = b0; b < b1; ++b) {
+            const int64_t c = cost(b);
+            if (x < at + c) {
+                found_b = b;
+                found_base = at;
+                break;
+            }
+            at += c;
+        }
+    }
+    __syncthreads();
+    ChunkPlace r;
+    r.total = total;
+    r.b = found_b;
+    r.base = r.b < B ? found_base : total;
+    return r;
+}
+
+}  // namespace tv

@@ -175,4 +175,69 @@ size_t draft_tree_ws_bytes(int B, int k, int layers);
 void draft_tree_chunks(int rows, int V, bool vec, int* c, int* per);
 tv_status launch_draft_expand(const DraftArgs& a);
 
+struct ChunkAppendArgs {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements
+    const int32_t* positions;
+    int T;
+    const int32_t* q_start;
+    const int32_t* prefix_lens;
+    int B, Hq, Hkv, d;
+    const tv_rope_table* rope;  // nullable, host
+    void* q_out;
+    int64_t q_out_stride;
+    void *k_cache, *v_cache;
+    const int32_t* block_table;
+    int max_blocks, bs, num_blocks, elem;
+    int32_t* status;
+    cudaStream_t stream;
+};
+tv_status launch_chunk_append(const ChunkAppendArgs& a);
+tv_status make_rope_table(tv_rope_table* t, int dim, int interleaved, double theta,
+                          tv_rope_scaling scaling, double factor, double original_len, double low,
+                          double high, double amplitude);
+
+struct ChunkAttnArgs {
+    const void* q;
+    int64_t q_stride;  // elements
+    const void *k_cache, *v_cache;
+    const int32_t* block_table;
+    int max_blocks;
+    const int32_t* q_start;
+    const int32_t* prefix_lens;
+    int T, B, Hq, Hkv, d, bs, num_blocks;
+    tv_dtype dt;
+    float scale, softcap;
+    int window;
+    void* out;
+    int64_t out_stride;
+    int32_t* status;
+    void* ws;
+    cudaStream_t stream;
+};
+size_t chunk_attn_f32_workspace(int T, int B, int Hq, int Hkv, int d);
+tv_status launch_chunk_attn_f32(const ChunkAttnArgs& a);
+
+tv_status launch_token_counts(int32_t* counts, const int32_t* tokens, const int32_t* starts,
+                              int total, int B, int V, bool clear, bool prompt, int32_t* status,
+                              cudaStream_t stream);
+
+struct LogitsArgs {
+    const void* logits;
+    tv_dtype dt;
+    int B, N, V;
+    const int32_t* node_counts;
+    const uint64_t* mask;
+    const int32_t* tokens;
+    const int32_t* counts;
+    const float* bias;
+    const uint32_t* grammar;
+    const float *rep, *freq, *pres, *temp;
+    bool probs;
+    float* out;
+    int32_t* status;
+    cudaStream_t stream;
+};
+tv_status launch_tree_logits(const LogitsArgs& a);
+
 }  // namespace tv

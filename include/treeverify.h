@@ -384,6 +384,198 @@ tv_status tree_verify_attention_noalloc(const void* q, const void* k_cache, cons
                                         int num_blocks, tv_dtype dt, float scale, void* out,
                                         int32_t* status, tv_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Chunks of new tokens.  chunk_kv_append and chunk_attention take a ragged
+ * batch: T rows (tokens) laid end to end, sequence b owning rows q_start[b] ..
+ * q_start[b+1] - 1 (q_start: device int32 [B + 1], non-decreasing, within
+ * [0, T]; n_b = q_start[b+1] - q_start[b] may be 0).  Row q_start[b] + i is the
+ * token at logical position P_b + i, P_b = prefix_lens[b].  Rows before
+ * q_start[0] or from q_start[B] on belong to no sequence: they are neither read
+ * into a result nor written.  If q_start breaks these rules every sequence gets
+ * TV_ERR_OUT_OF_RANGE and nothing else is written.  P_b + n_b is at most 2^31 - 1024.  A prompt is one chunk or
+ * several, plain decoding is n_b = 1, and both may share a batch.
+ * ------------------------------------------------------------------------ */
+
+/* Rotary positions.  A table holds, for each of dim / 2 pairs of columns, the
+ * pair's turns per position as a 64-bit fraction of a turn: position times that
+ * integer, modulo 2^64, is the angle modulo one turn without rounding, however
+ * far the position.  It is plain host data (no pointers) that
+ * rope_table_init fills; calls copy it, so it may be freed or changed after
+ * they return.
+ *
+ *   f_j = theta^(-2 j / dim) radians per position, j < dim / 2, then by scaling
+ *   TV_ROPE_NONE    f_j
+ *   TV_ROPE_LINEAR  f_j / factor
+ *   TV_ROPE_BANDS   with n_j = original_len f_j / (2 pi) turns over the original
+ *                   context and k = clamp((n_j - low) / (high - low), 0, 1):
+ *                   f_j (k + (1 - k) / factor)            (low 1, high 4)
+ *   TV_ROPE_RAMP    with e(n) = dim ln(original_len / (2 pi n)) / (2 ln theta),
+ *                   a = max(0, floor(e(high))), z = min(dim - 1, ceil(e(low))),
+ *                   s = clamp((j - a) / max(z - a, 0.001), 0, 1):
+ *                   f_j (1 - s) + f_j / factor s          (low 1, high 32)
+ * low, high <= 0 select the values in parentheses.  amplitude multiplies cos
+ * and sin; <= 0 selects 0.1 ln(factor) + 1 for TV_ROPE_RAMP and 1 otherwise.
+ * interleaved: pairs are columns (2j, 2j + 1); otherwise (j, j + dim / 2).
+ * Columns from dim on are not rotated. */
+typedef enum {
+    TV_ROPE_NONE = 0,
+    TV_ROPE_LINEAR = 1,
+    TV_ROPE_BANDS = 2,
+    TV_ROPE_RAMP = 3
+} tv_rope_scaling;
+
+#define TV_ROPE_MAX_DIM 256
+
+typedef struct {
+    int32_t dim;          /* rotated columns, even, <= TV_ROPE_MAX_DIM */
+    int32_t interleaved;  /* 0 or 1 */
+    float amplitude;
+    int32_t reserved;
+    uint64_t turn[TV_ROPE_MAX_DIM / 2];
+} tv_rope_table;
+
+/* Host only.  TV_ERR_INVALID_ARG: NULL table, dim odd or outside [2,
+ * TV_ROPE_MAX_DIM], theta not finite or <= 1, an unknown scaling, and with a
+ * scaling factor not finite or < 1, or (bands, ramp) original_len not finite or
+ * < 1, or high <= low. */
+tv_status rope_table_init(tv_rope_table* table, int dim, int interleaved, double theta,
+                          tv_rope_scaling scaling, double factor, double original_len, double low,
+                          double high, double amplitude);
+
+/* ------------------------------------------------------------------------
+ * chunk_kv_append — "EAGLE code principles", KV缓存优化: KVCache.cat, for a
+ * chunk of tokens of any length.  The step before chunk_attention (or, with
+ * positions P_b + depth, before tree_verify_attention: the call that rotates a
+ * tree's queries).
+ *
+ * q [T][Hq][d], k and v [T][Hkv][d] (dt elements; heads contiguous, rows
+ * q_stride / k_stride / v_stride elements apart, so all three may be views of
+ * one fused projection).  For every row of a sequence: the value row, and the
+ * rotated key row, go to the slot of logical position P_b + i; the rotated
+ * query row goes to q_out (rows q_out_stride apart; q_out may be q with the
+ * same stride: each element is read by the thread that writes it).  q and
+ * q_out NULL: keys and values only.  rope NULL: nothing is rotated.
+ * The rotary position of a row is P_b + i, or positions[row] (device int32 [T])
+ * if positions is not NULL.  A pair (x, y) with angle a becomes
+ * (x cos a - y sin a, y cos a + x sin a) times amplitude: the angle's fraction
+ * of a turn exact to 64 bits, cos, sin, products and sums in float32, one
+ * rounding to dt.
+ * status int32 [B]: TV_ERR_OUT_OF_RANGE for P_b < 0, a position P_b .. P_b + n_b
+ * - 1 without a valid block, or a negative position; that sequence's cache
+ * slots and q_out rows are left unchanged.  Two sequences must not append to
+ * the same slot.
+ * Host errors: TV_ERR_INVALID_ARG for sizes, NULL or (16 bytes) misaligned
+ * pointers, strides smaller than a row, rope->dim above d; TV_ERR_UNSUPPORTED for d
+ * or a stride that is no multiple of 16 bytes, or rope->dim no multiple of 32
+ * bytes.
+ * ------------------------------------------------------------------------ */
+tv_status chunk_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                          const void* v, int64_t v_stride, const int32_t* positions, int T,
+                          const int32_t* q_start, const int32_t* prefix_lens, int B, int Hq,
+                          int Hkv, int d, const tv_rope_table* rope, void* q_out,
+                          int64_t q_out_stride, void* k_cache, void* v_cache,
+                          const int32_t* block_table, int max_blocks_per_seq, int block_size,
+                          int num_blocks, tv_dtype dt, int32_t* status, tv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * chunk_attention — the target model's attention for what tree_verify_attention
+ * does not cover: prompts in chunks, and plain decoding (n_b = 1), over the
+ * same paged cache ("vLLM-TreeEagle", 核心组件: PagedAttention underneath).
+ *
+ * For row q_start[b] + i (position p = P_b + i) and query head h (kv head g = h
+ * / (Hq / Hkv)):
+ *   keys  K = { t : max(0, p - window + 1) <= t <= p }   (window <= 0: 0 <= t <= p)
+ *   s_t = scale * q . k_t, and with softcap > 0  s_t = softcap * tanh(s_t / softcap)
+ *   out[row][h] = sum_{t in K} softmax_t(s) v_t
+ * The chunk's own keys and values are in the cache already (chunk_kv_append).
+ * q [T][Hq][d] and out [T][Hq][d], dt elements, heads contiguous, rows
+ * q_stride / out_stride elements apart.  out must not overlap q.
+ * dt = TV_BF16: float32 accumulation and softmax; d in {64, 128}, block_size a
+ * multiple of 16.  dt = TV_F32: float32 throughout; d <= 256, d % 32 == 0.
+ * scale <= 0 selects 1/sqrt(d).
+ * status int32 [B]: TV_ERR_OUT_OF_RANGE (and zero rows of out) for P_b < 0, P_b +
+ * n_b > max_blocks_per_seq * block_size, or a block id outside [0, num_blocks)
+ * among the blocks that hold a key of K for some row of the sequence (blocks
+ * wholly before the first row's window may have been given back: their table
+ * entries are not read).
+ * Cache rows that no row of the sequence attends to are never read into a
+ * result.  Where a key is outside K for one row and inside for another, its
+ * contents reach only the rows that attend to it, infinities and NaN included.
+ * workspace: chunk_attention_workspace() bytes, 16-byte aligned, any contents;
+ * partial results of rows whose keys are split over several SMs.  Missing or
+ * smaller: TV_ERR_WORKSPACE.
+ * ------------------------------------------------------------------------ */
+size_t chunk_attention_workspace(int T, int B, int Hq, int Hkv, int d, tv_dtype dt);
+
+tv_status chunk_attention(const void* q, int64_t q_stride, const void* k_cache,
+                          const void* v_cache, const int32_t* block_table,
+                          int max_blocks_per_seq, const int32_t* q_start,
+                          const int32_t* prefix_lens, int T, int B, int Hq, int Hkv, int d,
+                          int block_size, int num_blocks, tv_dtype dt, float scale, float softcap,
+                          int window, void* out, int64_t out_stride, int32_t* status,
+                          void* workspace, size_t workspace_bytes, tv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * token_counts_update — the history that tree_logits_process reads: counts
+ * int32 [B][V], bit 31 of a word set when the token occurs in the prompt, the
+ * low 31 bits the number of times it was emitted.
+ *
+ * tokens: with starts (device int32 [B + 1], non-decreasing, within [0, total])
+ * sequence b's tokens are tokens[starts[b]] .. tokens[starts[b+1] - 1]; with
+ * starts NULL they are row b of [B][total / B] (as tree_accept's out_tokens).
+ * Entries of -1 are skipped.  clear: the row is zeroed first.  prompt: the
+ * tokens set bit 31, otherwise each adds 1 (integer atomics: the order does not
+ * matter).
+ * status int32 [B]: TV_ERR_OUT_OF_RANGE for a token outside [-1, V) or a bad
+ * starts array; that sequence's row is left unchanged.
+ * Host errors: B < 0, V outside [1, 2^24], total < 0, starts NULL and total no
+ * multiple of B, NULL pointers (tokens may be NULL when total is 0).
+ * ------------------------------------------------------------------------ */
+tv_status token_counts_update(int32_t* counts, const int32_t* tokens, const int32_t* starts,
+                              int total, int B, int V, int clear, int prompt, int32_t* status,
+                              tv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * tree_logits_process — the step between the target model and tree_accept: the
+ * model's row for every node of a tree becomes the logits (greedy acceptance) or
+ * the probabilities (stochastic acceptance) that tree_accept reads.
+ *
+ * logits: [B][N][V], float32 or bfloat16 (dt); out float32 [B][N][V] (may be
+ * logits itself when dt is TV_F32).  For row i of sequence b and token x:
+ *   z = logits[b][i][x] + bias[b][x]
+ *   n = occurrences of x among the emitted tokens: the low 31 bits of
+ *       counts[b][x], plus the nodes c >= 1 with bit c of mask[b][i] set and
+ *       draft_tokens[b][c] == x (the node's own path; the root is the last token
+ *       that counts already holds)
+ *   if n > 0 or bit 31 of counts[b][x]:  z = z > 0 ? z / repetition[b] : z * repetition[b]
+ *   z = z - frequency[b] * n - (n > 0 ? presence[b] : 0)
+ *   z = z / temperature[b]
+ *   bit (x % 32) of grammar[b][i][x / 32] clear:  z = -infinity
+ *   probs == 0: out = z;  else out = softmax over x of z (0 for a masked token;
+ *   a row without an allowed token above -infinity is all zeros; a NaN or +infinity
+ *   among the allowed z makes the row NaN).
+ * Every product and sum in float32.  bias [B][V] float32, counts int32 [B][V],
+ * grammar uint32 [B][N][ceil(V / 32)], repetition / frequency / presence /
+ * temperature float32 [B], mask uint64 [B][N] with draft_tokens int32 [B][N]: each
+ * may be NULL (no bias; no history; every token allowed; 1, 0, 0, 1; no path).
+ * The penalties need counts.  node_counts as above: rows of absent nodes are not
+ * written.
+ * status int32 [B]: TV_ERR_OUT_OF_RANGE for a node count outside [1, N] or (with
+ * mask) a token of nodes 1 .. n_b - 1 outside [0, V); TV_ERR_BAD_VALUES for a
+ * repetition or temperature not finite or <= 0, a frequency or presence not
+ * finite.  That sequence's rows (all N when the count is bad) are -infinity
+ * (probs == 0) or zero.
+ * Host errors: N outside [1, 64], V outside [1, 2^24], NULL logits, out or
+ * status, mask without draft_tokens or the reverse, a penalty without counts.
+ * ------------------------------------------------------------------------ */
+tv_status tree_logits_process(const void* logits, tv_dtype dt, int B, int N, int V,
+                              const int32_t* node_counts, const uint64_t* mask,
+                              const int32_t* draft_tokens, const int32_t* counts,
+                              const float* bias, const uint32_t* grammar,
+                              const float* repetition, const float* frequency,
+                              const float* presence, const float* temperature, int probs,
+                              float* out, int32_t* status, tv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
