@@ -370,7 +370,8 @@ static bool chunk_attn_shape_ok(int Hq, int Hkv, int d, tv_dtype dt) {
 
 size_t chunk_attention_workspace(int T, int B, int Hq, int Hkv, int d, tv_dtype dt) {
     if (T < 1 || B < 1 || !chunk_attn_shape_ok(Hq, Hkv, d, dt)) return 0;
-    return chunk_attn_f32_workspace(T, B, Hq, Hkv, d);
+    return chunk_attn_tc_applicable(Hq, Hkv, d, dt) ? chunk_attn_tc_workspace(T, B, Hq, Hkv, d)
+                                                    : chunk_attn_f32_workspace(T, B, Hq, Hkv, d);
 }
 
 tv_status chunk_attention(const void* q, int64_t q_stride, const void* k_cache,
@@ -425,7 +426,9 @@ tv_status chunk_attention(const void* q, int64_t q_stride, const void* k_cache,
     a.status = status;
     a.ws = workspace;
     a.stream = (cudaStream_t)stream;
-    return launch_chunk_attn_f32(a);
+    // without rows there are only statuses to write
+    return T > 0 && chunk_attn_tc_applicable(Hq, Hkv, d, dt) ? launch_chunk_attn_tc(a)
+                                                             : launch_chunk_attn_f32(a);
 }
 
 tv_status token_counts_update(int32_t* counts, const int32_t* tokens, const int32_t* starts,

@@ -67,7 +67,9 @@ struct CfTile {
 
 // false: no such tile.  Called by every thread (contains barriers).
 __device__ __forceinline__ bool cf_find(const CfParams& p, int tile, CfTile& t) {
-    const ChunkPlace at = chunk_locate<CF_THREADS>(p.c.B, tile, [&](int b) { return cf_tiles(p, b); });
+    __shared__ ChunkLocateTmp<CF_THREADS> tmp;
+    const ChunkPlace at = chunk_locate<CF_THREADS>(&tmp, p.c.B, [&](int64_t) { return (int64_t)tile; },
+                                                   [&](int b) { return cf_tiles(p, b); });
     if (at.b >= p.c.B) return false;
     t.b = at.b;
     t.s = p.c.q_start[at.b];
@@ -278,7 +280,9 @@ __global__ void __launch_bounds__(CF_THREADS) chunk_join_kernel(CfParams p) {
     pdl_wait();
     const int g = blockIdx.y, tid = threadIdx.x;
     if (!chunk_starts_ok(p.c)) return;
-    const ChunkPlace at = chunk_locate<CF_THREADS>(p.c.B, blockIdx.x, [&](int b) { return cf_tiles(p, b); });
+    __shared__ ChunkLocateTmp<CF_THREADS> tmp;
+    const ChunkPlace at = chunk_locate<CF_THREADS>(&tmp, p.c.B, [&](int64_t) { return (int64_t)blockIdx.x; },
+                                                   [&](int b) { return cf_tiles(p, b); });
     if (at.b >= p.c.B) return;
     const int s = p.c.q_start[at.b], n = p.c.q_start[at.b + 1] - s;
     const int r0 = ((int)blockIdx.x - (int)at.base) * CF_M, rows = min(CF_M, n * p.G - r0);

@@ -1,0 +1,1097 @@
+// chunk_attention, bfloat16 path on the 5th-generation tensor cores.
+//
+// The online softmax over 128-key tiles: S = Q K^T, m = running row maximum, P =
+// 2^(S c - m), O += P V, O / sum(P) at the end.  Bound by the tensor core for
+// long chunks (4 d operations per row and key) and by the K/V stream for a few
+// rows per sequence (plain decoding).
+//
+// Rows are packed: token-major, then the G = Hq / Hkv query heads of a kv head,
+// so every K/V byte is read once for all of them.  A row tile holds npt =
+// floor(128 / G) whole tokens; an item is (sequence, kv head, up to two
+// consecutive row tiles) with its range of keys.  One CTA per SM keeps two
+// streams of products going, so that the tensor core works on one while the
+// softmax of the other runs:
+//   two row tiles  stream i is row tile i, both over the same key tiles (each
+//                  K/V tile in shared memory serves 256 rows);
+//   one row tile   (at most npt tokens left) stream i takes the key tiles t with
+//                  t % 2 == i, and the two results are joined at the end.
+//
+// Balance: an item costs its keys plus a fixed C0 (in keys).  The items of all
+// sequences, laid end to end, are cut into one run of equal cost per CTA, so
+// every CTA has the same work whatever the lengths; the run's borders follow
+// from closed forms, so nothing is precomputed and the schedule is made on the
+// device from the lengths (a captured graph serves any of them).  An item cut by
+// a border leaves one partial result (unnormalised O, maximum, sum, float32)
+// per run in the workspace, and a second kernel joins them in order.
+//
+// CTA roles (384 threads)
+//   warps 0-3, 4-7  softmax of stream 0 and 1: thread r owns row r (tensor-memory
+//            lane r).  P (bfloat16 pairs) takes the place of S in tensor memory.
+//            The running maximum is raised (and O rescaled) only when a row grows
+//            by more than 2^8.
+//   warp 8   issues every product, alternating the streams: PV(i, t - 1), then
+//            S(i, t).  The tensor core works in issue order, so S(i, t) may
+//            overwrite P(i, t - 1), and S(i, t)'s completion implies that O holds
+//            every earlier product (a rescale waits for nothing else).
+//   warp 9   K/V producer: 16-key pages by TMA into a ring of slots, in the order
+//            in which warp 8 consumes them.
+//   warp 10  loads the items' Q tiles, and clears what must not reach O (zero weight
+//            times NaN is NaN) in the V tiles that not every row sees whole: rows that
+//            no row of the item attends to (past its last key, or before its first
+//            in the same page), and rows with NaN or infinity that some attend to; these
+//            are noted, and the rows that do attend to them add them in their
+//            epilogue.  Such tiles land on a barrier of their own (vraw), and warp 10
+//            passes them on to warp 8.
+//   warp 11  scheduler: walks the run, checks each new sequence's blocks, and
+//            publishes the items a few ahead.
+// Every wait is bounded; one that runs out sets the abort flag, and the roles
+// leave after their copies and products in flight are done.
+#include <algorithm>
+
+#include "tv_chunk.cuh"
+#include "tv_internal.h"
+#include "tv_tc.cuh"
+
+namespace tv {
+
+namespace {
+
+constexpr int KT = 128;            // keys per tile
+constexpr int MT = 128;            // rows per row tile
+constexpr int THREADS = 384;
+constexpr int MMA_WARP = 8, LOAD_WARP = 9, FIX_WARP = 10, SCHED_WARP = 11;
+constexpr int GQ = 4;              // items published ahead
+constexpr int FIX_TILES = 6;       // key tiles of an item that only some of its rows see
+constexpr int FIX_BUFS = 4;        // items whose V notes may be live (see warp 10)
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float RESCALE_LOG2 = 8.0f;
+// fixed cost of an item, in keys: Q load, pipeline fill and drain, epilogue
+constexpr int64_t C0 = 256;
+// least cost of a run, in keys: shorter ones cost more to join than they save
+constexpr int64_t RUN_MIN = 512;
+
+struct Item {
+    int b, g, P, i0;        // sequence, kv head, prefix, first token
+    int ntok, row0, kbase, hi;  // tokens; row of the first; first key (multiple of 16), key end
+    int t_lo, t_hi, fa, fb; // key tiles of this piece; tiles < fa or >= fb need masks
+    int flags, slot, n, pad;  // slot: partial result, or -1; n: tiles to do (0: bad sequence)
+};
+constexpr int ITEM_END = 1, ITEM_TWO = 2, ITEM_BAD = 4, ITEM_STATUS = 8;
+static_assert(sizeof(Item) == 64, "four 16-byte words");
+
+template <int D>
+struct Lay {
+    static constexpr int HALVES = D / 64;
+    static constexpr int PAGE_BYTES = 16 * D * 2;
+    static constexpr int SLOT_BYTES = KT * D * 2;
+    static constexpr int SLOTS = D == 128 ? 5 : 10;
+    static constexpr int Q_BYTES = MT * D * 2;             // one row tile
+    static constexpr int OFF_RING = 0;
+    static constexpr int OFF_Q = SLOTS * SLOT_BYTES;       // two row tiles
+    static constexpr int OFF_X = OFF_Q + Q_BYTES;          // join of the streams: the second Q tile
+    static constexpr int OFF_ITEMS = OFF_Q + 2 * Q_BYTES;  // [GQ]
+    static constexpr int OFF_BAD = OFF_ITEMS + GQ * 64;    // [FIX_BUFS][FIX_TILES][4]
+    static constexpr int OFF_BARS = OFF_BAD + FIX_BUFS * FIX_TILES * 16;
+    static constexpr int NBARS = 3 * SLOTS + 8 + 4 + 2 * GQ;
+    static constexpr int OFF_TMP = OFF_BARS + NBARS * 8;   // ChunkLocateTmp, then words
+    static constexpr int OFF_MISC = OFF_TMP + (int)sizeof(ChunkLocateTmp<THREADS>);
+    static constexpr int BYTES = OFF_MISC + 32 + 1024;     // + alignment slack
+};
+static_assert(Lay<128>::BYTES <= 232448 && Lay<64>::BYTES <= 232448, "shared memory of one SM");
+
+struct Params {
+    ChunkView c;
+    __nv_bfloat16* out;
+    int64_t o_stride;
+    const __nv_bfloat16* q;      // for the rows that see a V row with NaN or infinity
+    int64_t q_stride;
+    const __nv_bfloat16* k;
+    const __nv_bfloat16* v;
+    int32_t* status;
+    float* part;                 // partial results, two slots per CTA
+    int Hq, Hkv, G, npt, window;
+    int prows;                   // rows of a partial result: 128 or 256
+    float scale_log2;            // scale * log2(e); with a cap: 2 log2(e) scale / cap
+    float cap_log2;              // cap * log2(e)
+};
+
+// ------------------------------------------------------------ the run space
+// Sequence of n rows after P keys: items of m = 2 npt tokens, item k costing C0 +
+// min(P + (k + 1) m, window + m) keys, the last one C0 + min(P + n, window + m).
+struct Seq {
+    int P, n;
+    int64_t m, w;                // tokens per item; window + m, or no limit
+    int items;
+    bool shape;                  // P and n fit the block table
+};
+
+__device__ __forceinline__ Seq seq_of(const Params& p, int b) {
+    Seq s;
+    s.P = p.c.prefix[b];
+    s.n = p.c.q_start[b + 1] - p.c.q_start[b];
+    s.shape = chunk_shape_ok(p.c, s.P, s.n);
+    s.m = 2 * p.npt;
+    s.w = p.window > 0 ? p.window + s.m : (1ll << 40);
+    s.items = (int)((s.n + s.m - 1) / s.m);
+    return s;
+}
+// Cost of the first k items.
+__device__ __forceinline__ int64_t seq_cost(const Seq& s, int64_t k) {
+    if (!s.shape) return k * C0;
+    const int64_t full = min(k, (int64_t)s.items - 1);           // items of m tokens
+    int64_t lin = full;                                          // of them below the window's limit
+    if (s.w < (1ll << 40)) lin = min(full, max((int64_t)0, (s.w - s.P + s.m - 1) / s.m - 1));
+    int64_t c = lin * s.P + s.m * (lin * (lin + 1) / 2) + (full - lin) * s.w + full * C0;
+    if (k == s.items && k > 0) c += C0 + min((int64_t)s.P + s.n, s.w);
+    return c;
+}
+__device__ __forceinline__ int64_t seq_units(const Params& p, int b) {
+    const Seq s = seq_of(p, b);
+    return s.items == 0 ? 0 : seq_cost(s, s.items) * p.Hkv;
+}
+// Keys of item k: from kbase (multiple of 16) to hi, in tiles of KT.
+__device__ __forceinline__ void item_keys(const Params& p, const Seq& s, int k, int& i0, int& i1,
+                                          int& kbase, int& hi, int& tiles) {
+    i0 = (int)(k * s.m);
+    i1 = (int)min((int64_t)s.n, i0 + s.m);
+    if (!s.shape) {
+        kbase = hi = tiles = 0;
+        return;
+    }
+    hi = s.P + i1;
+    kbase = chunk_first_key(s.P + i0, p.window) & ~15;
+    tiles = (hi - kbase + KT - 1) / KT;
+}
+// Tile at which a border y units into an item of the given cost cuts it.
+__device__ __forceinline__ int cut_tile(int64_t y, int64_t cost, int tiles) {
+    if (y <= C0) return 0;
+    if (y >= cost) return tiles;
+    return (int)min((int64_t)tiles, ((y - C0) * tiles + (cost - C0) - 1) / (cost - C0));
+}
+// Item at unit y of a sequence (Hkv equal stretches): kv head, item, its first unit.
+__device__ __forceinline__ void item_at(const Params& p, const Seq& s, int64_t y, int& g, int& k,
+                                        int64_t& start) {
+    const int64_t per = seq_cost(s, s.items);
+    g = (int)(y / per);
+    const int64_t r = y - g * per;
+    int lo = 0, hi = s.items;                                    // cost(lo) <= r < cost(hi)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (seq_cost(s, mid) <= r) lo = mid;
+        else hi = mid;
+    }
+    k = lo;
+    start = g * per + seq_cost(s, lo);
+}
+// Runs: as many as there are CTAs, fewer when they would be short.
+__device__ __forceinline__ int64_t run_count(int64_t units, int64_t ctas) {
+    return max((int64_t)1, min(ctas, units / RUN_MIN));
+}
+
+// Tiles of an item that warp 10 goes through: t < fa (some rows' windows start
+// later) and t >= fb (some rows end earlier, or the tile reaches past hi).
+__device__ __forceinline__ void item_edges(const Params& p, Item& it) {
+    it.fb = (it.P + it.i0 + 1 - it.kbase) / KT;
+    const int first_all = p.window > 0 ? it.P + it.i0 + it.ntok - p.window : 0;  // seen by every row
+    it.fa = first_all > it.kbase ? (first_all - it.kbase + KT - 1) / KT : 0;
+}
+__device__ __forceinline__ int fix_index(const Item& it, int t) {  // 0 .. FIX_TILES - 1
+    return t < it.fa ? t : max(it.fa, 0) + (t - max(it.fa, it.fb));
+}
+
+// Weight 2^(s - m) of one key for one row, from global memory (rare: V rows with
+// NaN or infinity).
+template <int D, bool CAP>
+__device__ __noinline__ float key_weight(const Params& p, const __nv_bfloat16* q, int64_t krow, float m) {
+    float s = 0.f;
+    for (int c = 0; c < D; ++c) s = fmaf(__bfloat162float(q[c]), __bfloat162float(p.k[krow * D + c]), s);
+    s *= p.scale_log2;
+    if (CAP) s = p.cap_log2 * (1.f - 2.f / (1.f + exp2f(s)));
+    return exp2f(s - m);
+}
+
+template <int D, bool CAP>
+__global__ void __launch_bounds__(THREADS, 1)
+chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Params p) {
+    using L = Lay<D>;
+    constexpr uint32_t TMEM_O = 256;                       // S at 0 and 128, O at 256 and 256 + D
+    constexpr uint32_t IDESC_QK = idesc_bf16(MT, KT, false), IDESC_PV = idesc_bf16(MT, D, true);
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    Item* items = reinterpret_cast<Item*>(smem + L::OFF_ITEMS);
+    uint32_t* bad = reinterpret_cast<uint32_t*>(smem + L::OFF_BAD);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BARS);
+    uint64_t* empty = full + L::SLOTS;
+    uint64_t* sfull = empty + L::SLOTS;   // [2] S(i, t) done (and all products before it)
+    uint64_t* pfull = sfull + 2;          // [2] P(i, t) written
+    uint64_t* ofull = pfull + 2;          // [2] the item's last PV(i) done
+    uint64_t* ofree = ofull + 2;          // [2] O(i) read by the epilogue
+    uint64_t* qfull = ofree + 2;
+    uint64_t* qempty = qfull + 1;
+    uint64_t* xdone = qempty + 1;         // the join's use of the second Q tile is over
+    uint64_t* drain = xdone + 1;
+    uint64_t* gq_full = drain + 1;        // [GQ]
+    uint64_t* gq_empty = gq_full + GQ;    // [GQ]
+    uint64_t* vraw = gq_empty + GQ;       // [SLOTS] a V tile that warp 10 goes through has landed
+    auto* tmp = reinterpret_cast<ChunkLocateTmp<THREADS>*>(smem + L::OFF_TMP);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+    int* seq_ok = reinterpret_cast<int*>(smem + L::OFF_MISC + 8);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sbase = smem_u32(smem);
+    pdl_launch_dependents();
+    if (tid == 0) {
+        for (int s = 0; s < L::SLOTS; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+            mbar_init(&vraw[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pfull[i], 4);
+            mbar_init(&ofull[i], 1);
+            mbar_init(&ofree[i], 4);
+        }
+        mbar_init(qfull, 1);
+        mbar_init(qempty, 1);
+        mbar_init(xdone, 4);
+        mbar_init(drain, 1);
+        for (int s = 0; s < GQ; ++s) {
+            mbar_init(&gq_full[s], 1);
+            mbar_init(&gq_empty[s], 11);  // 8 softmax warps, MMA, producer, warp 10
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == MMA_WARP) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    {
+        // rows of a Q tile past npt * G are never loaded: zero, so that their scores are finite
+        const int used = p.npt * p.G;
+        for (int e = tid; e < 2 * L::HALVES * (MT - used) * 8; e += THREADS) {
+            const int t = e / ((MT - used) * 8), r = e % ((MT - used) * 8);
+            *reinterpret_cast<uint4*>(smem + L::OFF_Q + t * (MT * 128) + used * 128 + r * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+    pdl_wait();  // everything above touched only shared memory and tensor memory
+
+    // ---- this CTA's run
+    const bool valid = chunk_starts_ok(p.c);
+    if (blockIdx.x == 0)
+        for (int b = tid; b < p.c.B; b += THREADS)
+            if (!valid || p.c.q_start[b] == p.c.q_start[b + 1])
+                p.status[b] = (valid && chunk_shape_ok(p.c, p.c.prefix[b], 0)) ? TV_OK : TV_ERR_OUT_OF_RANGE;
+    ChunkPlace at;
+    at.b = p.c.B;
+    int64_t x_lo = 0, x_hi = 0;
+    if (valid) {
+        int64_t units = 0;
+        at = chunk_locate<THREADS>(tmp, p.c.B, [&](int64_t total) {
+            units = total;
+            const int64_t runs = run_count(total, gridDim.x), r = blockIdx.x;
+            x_lo = r < runs ? r * total / runs : total;
+            x_hi = r < runs ? (r + 1) * total / runs : total;
+            return x_lo;
+        }, [&](int b) { return seq_units(p, b); });
+        if (at.b < p.c.B) {
+            // the first sequence's blocks, by every thread at once
+            const Seq s = seq_of(p, at.b);
+            const bool ok = s.shape && chunk_blocks_ok(p.c, at.b, chunk_first_key(s.P, p.window),
+                                                       (int64_t)s.P + s.n, tid, THREADS);
+            const int all = __syncthreads_and(ok ? 1 : 0);
+            if (tid == 0) *seq_ok = all;
+        }
+    }
+    __syncthreads();
+
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+    };
+    // Work item k, from the queue; false at the end (or after a timeout).
+    auto take = [&](uint32_t k, Item& it) -> bool {
+        const int s = k % GQ;
+        const bool got = wait_all(&gq_full[s], (k / GQ) & 1u);
+        const int4* src = reinterpret_cast<const int4*>(&items[s]);
+        int4* dst = reinterpret_cast<int4*>(&it);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) dst[u] = lds_v4_volatile(src + u);
+        __syncwarp();
+        // "slot read": no release needed, and a release would wait for the epilogue's stores
+        if (lane == 0) remote_arrive_relaxed_after(&gq_empty[s], 0, it.b | it.row0 | it.t_lo | it.n);
+        return got && !(it.flags & ITEM_END);
+    };
+
+    if (warp == SCHED_WARP) {
+        // ============================== scheduler ==============================
+        int b = at.b;
+        int64_t x = x_lo, base = at.base;
+        bool ok = b < p.c.B && *seq_ok != 0;
+        uint32_t k = 0;
+        auto publish = [&](const Item& it) -> bool {
+            const int s = k % GQ;
+            if (!wait_all(&gq_empty[s], ((k / GQ) & 1u) ^ 1u)) return false;
+            if (lane < 4)
+                reinterpret_cast<int4*>(&items[s])[lane] =
+                    lane == 0 ? make_int4(it.b, it.g, it.P, it.i0)
+                    : lane == 1 ? make_int4(it.ntok, it.row0, it.kbase, it.hi)
+                    : lane == 2 ? make_int4(it.t_lo, it.t_hi, it.fa, it.fb)
+                                : make_int4(it.flags, it.slot, it.n, 0);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&gq_full[s]);
+            ++k;
+            return true;
+        };
+        Seq s{};
+        int64_t units = 0;
+        bool fresh = true, alive = true;
+        while (alive && x < x_hi && b < p.c.B) {
+            if (fresh) {
+                s = seq_of(p, b);
+                units = s.items == 0 ? 0 : seq_cost(s, s.items) * p.Hkv;
+                if (b != at.b && units > 0) {
+                    ok = s.shape && chunk_blocks_ok(p.c, b, chunk_first_key(s.P, p.window),
+                                                    (int64_t)s.P + s.n, lane, 32);
+                    ok = __all_sync(0xffffffffu, ok);
+                }
+                fresh = false;
+            }
+            if (x >= base + units) {
+                base += units;
+                ++b;
+                fresh = true;
+                continue;
+            }
+            Item it;
+            int qk, i1, tiles;
+            int64_t start;
+            item_at(p, s, x - base, it.g, qk, start);
+            start += base;
+            const int64_t cost = seq_cost(s, qk + 1) - seq_cost(s, qk);
+            const int64_t y0 = x - start, y1 = min(x_hi - start, cost);
+            item_keys(p, s, qk, it.i0, i1, it.kbase, it.hi, tiles);
+            x = start + y1;
+            it.t_lo = cut_tile(y0, cost, tiles);
+            it.t_hi = cut_tile(y1, cost, tiles);
+            // a sequence that does not fit has items without tiles: the run with the first unit
+            // writes them
+            if (tiles == 0 ? y0 != 0 : it.t_lo == it.t_hi) continue;
+            const bool whole = it.t_lo == 0 && it.t_hi == tiles;
+            it.b = b;
+            it.P = s.P;
+            it.ntok = i1 - it.i0;
+            it.row0 = p.c.q_start[b] + it.i0;
+            it.slot = whole ? -1 : 2 * (int)blockIdx.x + (it.t_lo == 0 ? 1 : 0);
+            it.n = ok ? it.t_hi - it.t_lo : 0;
+            it.flags = (it.ntok > p.npt ? ITEM_TWO : 0) | (ok ? 0 : ITEM_BAD) |
+                       (it.g == 0 && it.i0 == 0 && it.t_lo == 0 ? ITEM_STATUS : 0);
+            item_edges(p, it);
+            alive = publish(it);
+        }
+        if (alive) {
+            Item it{};
+            it.flags = ITEM_END;
+            publish(it);
+        } else if (lane == 0) {
+            *abort_flag = 1;
+        }
+    } else if (warp == LOAD_WARP) {
+        // ============================ K/V producer ============================
+        if (lane == 0) {
+            tma_prefetch_desc(&kmap);
+            tma_prefetch_desc(&vmap);
+        }
+        uint32_t ld = 0;                   // slots filled so far
+        uint32_t raw = 0, raw_ph = 0;      // per slot: last filled through vraw, and vraw's next parity
+        bool alive = true;
+        Item it;
+        for (uint32_t k = 0; alive && take(k, it); ++k) {
+            if (it.n == 0) continue;
+            const bool two = (it.flags & ITEM_TWO) != 0;
+            // K/V of one token's rows are read once; longer chunks come back to them
+            const uint64_t policy = it.ntok == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+            // cache rows of the pages, 32 (four tiles) per window: lane l holds page l.  K runs
+            // at most two tiles ahead of V, so two windows are enough; the block ids of the
+            // window after are loaded early.
+            constexpr int WT = 32 / (KT / 16);
+            const int32_t* table = p.c.table + (int64_t)it.b * p.c.max_blocks;
+            int nxt_blk = 0, nxt_off = 0;
+            auto fetch = [&](int w) {
+                const int key = it.kbase + (it.t_lo + w * WT) * KT + lane * 16;
+                nxt_blk = key < it.hi ? __ldg(table + key / p.c.bs) : 0;
+                nxt_off = key % p.c.bs;
+            };
+            auto rows = [&]() -> int { return (nxt_blk * p.Hkv + it.g) * p.c.bs + nxt_off; };
+            fetch(0);
+            int cur = rows(), prev = 0, wk = 0;
+            if (it.n > WT) fetch(1);
+            auto load = [&](bool is_v, int j) -> bool {    // tile j of the piece
+                const int s = ld % L::SLOTS;
+                bool ok = *abort_flag == 0;
+                if (ok) ok = wait_all(&empty[s], ((ld / L::SLOTS) & 1u) ^ 1u);
+                if (!ok) return false;
+                const int w = j / WT;
+                if (!is_v && w > wk) {
+                    prev = cur;
+                    cur = rows();
+                    wk = w;
+                    if (it.n > (w + 1) * WT) fetch(w + 1);
+                }
+                const int k0 = it.kbase + (it.t_lo + j) * KT;
+                const int pages = min(KT / 16, (it.hi - k0 + 15) >> 4);
+                const int y = __shfl_sync(0xffffffffu, w == wk ? cur : prev, (j % WT) * (KT / 16) + (lane & 7));
+                uint8_t* dst = smem + L::OFF_RING + s * L::SLOT_BYTES + (lane & 7) * L::PAGE_BYTES;
+                // a V tile at the edges goes through warp 10, which passes it on
+                const bool edge = is_v && (it.t_lo + j < it.fa || it.t_lo + j >= it.fb);
+                raw = (raw & ~(1u << s)) | ((edge ? 1u : 0u) << s);
+                raw_ph ^= (edge ? 1u : 0u) << s;
+                uint64_t* bar = edge ? &vraw[s] : &full[s];
+                mbar_arrive_expect_tx_relaxed_elect(bar, (uint32_t)pages * L::PAGE_BYTES);
+                if (lane < pages) {
+                    if constexpr (D == 128) {
+                        if (is_v) tma_load_3d_hint(dst, &vmap, bar, 0, y, 0, policy);
+                        else tma_load_4d_hint(dst, &kmap, bar, 0, 0, 0, y >> 3, policy);
+                    } else {
+                        tma_load_2d(dst, is_v ? &vmap : &kmap, bar, 0, y, policy);
+                    }
+                }
+                __syncwarp();
+                ++ld;
+                return true;
+            };
+            // the order in which the products take them
+            const int lag = two ? 1 : 2;
+            for (int j = 0; alive && j < it.n + lag; ++j) {
+                if (j >= lag && j - lag < it.n) alive = load(true, j - lag);
+                if (alive && j < it.n) alive = load(false, j);
+            }
+        }
+        if (!alive && lane == 0) *abort_flag = 1;
+        // copies in flight end before the CTA does
+        for (uint32_t u = ld > (uint32_t)L::SLOTS ? ld - L::SLOTS : 0; u < ld; ++u) {
+            const uint32_t s = u % L::SLOTS;
+            if ((raw >> s) & 1u) wait_all(&vraw[s], ((raw_ph >> s) & 1u) ^ 1u);
+            else wait_all(&full[s], (u / L::SLOTS) & 1u);
+        }
+    } else if (warp == MMA_WARP) {
+        // ============================== products ==============================
+        uint32_t ld = 0, qi = 0, pc[2] = {0, 0}, oc[2] = {0, 0};
+        bool alive = true;
+        Item it;
+        auto issue_s = [&](int i, int qt, uint32_t slot) {
+            const uint32_t qa = sbase + L::OFF_Q + qt * L::Q_BYTES;
+            const uint32_t ka = sbase + L::OFF_RING + slot * L::SLOT_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t ad = smem_desc_sw128(qa + (kk >> 2) * (MT * 128) + (kk & 3) * 32, 16, 1024);
+                // d = 128: K is [page][row group][half][8 rows][128 bytes], 8-key groups 2 KB apart
+                const uint64_t bd = smem_desc_sw128(ka + (kk >> 2) * 1024 + (kk & 3) * 32, 16,
+                                                    D == 128 ? 2048 : 1024);
+                tc_mma_bf16_elect(tmem + i * KT, ad, bd, IDESC_QK, kk > 0 ? 1u : 0u);
+            }
+            tc_commit_elect(&sfull[i]);
+        };
+        auto issue_pv = [&](int i, uint32_t slot, bool first) {
+            const uint32_t va = sbase + L::OFF_RING + slot * L::SLOT_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < KT / 16; ++kk) {
+                // V is [page][half][16 rows][128 bytes]
+                const uint64_t bd = smem_desc_sw128(va + kk * L::PAGE_BYTES, 2048, 1024);
+                tc_mma_bf16_ts_elect(tmem + TMEM_O + i * D, tmem + i * KT + kk * 8, bd, IDESC_PV,
+                                     (first && kk == 0) ? 0u : 1u);
+            }
+        };
+        auto wait_full = [&](uint32_t u) -> bool {
+            return wait_all(&full[u % L::SLOTS], (u / L::SLOTS) & 1u);
+        };
+        // P of stream i is there, and (first product of an item) O(i) has been read
+        auto wait_p = [&](int i, bool first) -> bool {
+            if (!wait_all(&pfull[i], pc[i] & 1u)) return false;
+            ++pc[i];
+            if (first) {
+                if (oc[i] > 0 && !wait_all(&ofree[i], (oc[i] - 1) & 1u)) return false;
+                ++oc[i];
+            }
+            return true;
+        };
+        for (uint32_t k = 0; alive && take(k, it); ++k) {
+            if (it.n == 0) continue;
+            const int n = it.n;
+            if (!wait_all(qfull, qi & 1u)) {
+                alive = false;
+                break;
+            }
+            ++qi;
+            if (it.flags & ITEM_TWO) {
+                for (int j = 0; alive && j <= n; ++j) {
+                    const uint32_t uv = ld + 2 * j - 1, uk = ld + 2 * j;   // V(j - 1), K(j)
+                    if (j > 0) alive = wait_full(uv);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (!alive) break;
+                        if (j > 0) {
+                            alive = wait_p(i, j == 1);
+                            if (!alive) break;
+                            tc_fence_after();
+                            issue_pv(i, uv % L::SLOTS, j == 1);
+                            if (i == 1) tc_commit_elect(&empty[uv % L::SLOTS]);
+                            if (j == n) tc_commit_elect(&ofull[i]);
+                        }
+                        if (j < n) {
+                            if (i == 0) {
+                                alive = wait_full(uk);
+                                if (!alive) break;
+                                tc_fence_after();
+                            }
+                            issue_s(i, i, uk % L::SLOTS);
+                            if (i == 1) {
+                                tc_commit_elect(&empty[uk % L::SLOTS]);
+                                if (j == n - 1) tc_commit_elect(qempty);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+            } else {
+                uint32_t u = ld;
+                for (int j = 0; alive && j < n + 2; ++j) {
+                    const int i = j & 1;
+                    if (j >= 2 && j - 2 < n) {
+                        alive = wait_full(u);
+                        if (alive) alive = wait_p(i, j < 4);
+                        if (!alive) break;
+                        tc_fence_after();
+                        issue_pv(i, u % L::SLOTS, j < 4);
+                        tc_commit_elect(&empty[u % L::SLOTS]);
+                        if (j >= n) tc_commit_elect(&ofull[i]);
+                        ++u;
+                    }
+                    if (j < n) {
+                        alive = wait_full(u);
+                        if (!alive) break;
+                        tc_fence_after();
+                        issue_s(i, 0, u % L::SLOTS);
+                        tc_commit_elect(&empty[u % L::SLOTS]);
+                        if (j == n - 1) tc_commit_elect(qempty);
+                        ++u;
+                    }
+                    __syncwarp();
+                }
+            }
+            ld += 2 * n;
+        }
+        if (!alive && lane == 0) *abort_flag = 1;
+        // products in flight end before the tensor memory is freed
+        tc_commit_elect(drain);
+        wait_all(drain, 0);
+    } else if (warp == FIX_WARP) {
+        // ==================== Q tiles, V rows that must not reach O ====================
+        if (lane == 0) tma_prefetch_desc(&qmap);
+        const uint64_t qpol = l2_policy_evict_first();
+        uint32_t ld = 0, qi = 0, xi = 0, ph = 0;             // ph: vraw's parity per slot
+        bool alive = true;
+        Item it;
+        for (uint32_t k = 0; alive && take(k, it); ++k) {
+            if (it.n == 0) continue;
+            const int n = it.n;
+            const bool two = (it.flags & ITEM_TWO) != 0;
+            alive = wait_all(qempty, (qi & 1u) ^ 1u);
+            // the second Q tile also serves the joins of the items before
+            if (alive && two && xi > 0) alive = wait_all(xdone, (xi - 1) & 1u);
+            if (!alive) break;
+            ++qi;
+            const int nq = two ? 2 : 1;
+            mbar_arrive_expect_tx_relaxed_elect(qfull, (uint32_t)(nq * L::HALVES * 128 * p.G * p.npt));
+            for (int t = 0; t < nq; ++t)
+                for (int hf = 0; hf < L::HALVES; ++hf)
+                    tma_load_3d_elect(smem + L::OFF_Q + t * L::Q_BYTES + hf * (MT * 128), &qmap, qfull, hf * 64,
+                                      it.g * p.G, it.row0 + t * p.npt, qpol);
+            if (!two && n > 1) {
+                // one join outstanding at most, or the barrier's phases could not be told apart
+                if (xi > 0) alive = wait_all(xdone, (xi - 1) & 1u);
+                if (!alive) break;
+                ++xi;
+            }
+            // ring position of V(j): two row tiles K0 V0 K1 V1 ..., one K0 K1 V0 K2 V1 ... V(n-1)
+            auto v_at = [&](int j) -> uint32_t { return ld + (two || j == n - 1 ? 2 * j + 1 : 2 * j + 2); };
+            // notes of live item qi - 1: its Q buffer is free, so every S of the item before is done,
+            // and with it the epilogue of the item three before
+            uint32_t* notes = bad + ((qi - 1) % FIX_BUFS) * FIX_TILES * 4;
+            for (int e = lane; e < FIX_TILES * 4; e += 32) notes[e] = 0u;
+            __syncwarp();
+            for (int j = 0; alive && j < n; ++j) {
+                const int t = it.t_lo + j;
+                if (t >= it.fa && t < it.fb) {
+                    j = min(n, it.fb - it.t_lo) - 1;       // on to the tiles at the far end
+                    continue;
+                }
+                // (a slot is filled through vraw again only after its tile was passed on and used)
+                const uint32_t slot = v_at(j) % L::SLOTS;
+                alive = wait_all(&vraw[slot], (ph >> slot) & 1u);
+                if (!alive) break;
+                ph ^= 1u << slot;
+                uint8_t* vt = smem + L::OFF_RING + slot * L::SLOT_BYTES;
+                const int nv = it.hi - (it.kbase + t * KT);          // keys the item has in this tile
+                // rows before the first token's window, in the first page
+                const int lead = chunk_first_key(it.P + it.i0, p.window) - (it.kbase + t * KT);
+                // one token: no key is seen by some of its rows only
+                const int scan = it.ntok > 1 ? min(nv, KT) : 0;
+#pragma unroll
+                for (int q = 0; q < KT / 32; ++q) {
+                    const int r = q * 32 + lane;
+                    uint8_t* row = vt + (r >> 4) * L::PAGE_BYTES + (r & 15) * 128;
+                    bool clear = r >= nv || r < lead, odd = false;
+                    if (r < scan && !clear) {
+                        // bfloat16 with all exponent bits set, two per word
+                        uint32_t acc = 0;
+#pragma unroll
+                        for (int hf = 0; hf < L::HALVES; ++hf)
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const uint4 x = *reinterpret_cast<const uint4*>(row + hf * 2048 + ((c ^ (lane & 7)) << 4));
+                                acc |= ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+                                       ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
+                            }
+                        odd = (acc & 0x80008000u) != 0;
+                        clear = odd;
+                    }
+                    const uint32_t m = __ballot_sync(0xffffffffu, odd);
+                    if (m != 0 && lane == 0) notes[fix_index(it, t) * 4 + q] = m;
+                    if (clear)
+#pragma unroll
+                        for (int hf = 0; hf < L::HALVES; ++hf)
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                *reinterpret_cast<uint4*>(row + hf * 2048 + ((c ^ (lane & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();  // the tensor core reads V through the async proxy
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[slot]);
+            }
+            ld += 2 * n;
+        }
+        if (!alive && lane == 0) *abort_flag = 1;
+        if (qi > 0) wait_all(qfull, (qi - 1) & 1u);          // its own copies in flight
+    } else {
+        // ============================== softmax ==============================
+        const int i = warp >> 2;                              // stream
+        const int row = tid & 127;                            // tensor-memory lane
+        const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t tS = tmem + lane_off + i * KT, tO = tmem + lane_off + TMEM_O + i * D;
+        const int tok_l = row / p.G, head = row - tok_l * p.G;
+        float* xo = reinterpret_cast<float*>(smem + L::OFF_X);  // [columns][128 rows]
+        uint32_t sc = 0, oc = 0, live = 0;
+        bool alive = true;
+        Item it;
+        for (uint32_t k = 0; alive && take(k, it); ++k) {
+            const bool two = (it.flags & ITEM_TWO) != 0;
+            if ((it.flags & ITEM_STATUS) && tid == 0)
+                p.status[it.b] = (it.flags & ITEM_BAD) ? TV_ERR_OUT_OF_RANGE : TV_OK;
+            const int tok = tok_l + (two ? i * p.npt : 0);    // token within the item
+            const bool mine = tok_l < p.npt && tok < it.ntok;
+            // keys of the row, from the first key of the piece's tiles on
+            const int self = it.P + it.i0 + min(tok, it.ntok - 1);
+            const int first = p.window > 0 ? max(0, self - p.window + 1) : 0;
+            const int step = two ? 1 : 2, j0 = two ? 0 : i;
+            const int mine_n = it.n > j0 ? (it.n - j0 + step - 1) / step : 0;
+            float m_used = -INFINITY, l = 0.f;
+            for (int j = j0; j < it.n; j += step) {
+                if (!wait_all(&sfull[i], sc & 1u)) {
+                    alive = false;
+                    break;
+                }
+                ++sc;
+                tc_fence_after();
+                float sv[KT];
+                {
+                    uint32_t r[KT / 32][32];
+#pragma unroll
+                    for (int c = 0; c < KT / 32; ++c) tmem_ld32(tS + c * 32, r[c]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < KT; ++c) sv[c] = __uint_as_float(r[c / 32][c % 32]);
+                }
+                const int t = it.t_lo + j;
+                if constexpr (CAP) {
+                    // cap tanh(x) = cap (1 - 2 / (1 + e^(2x))), in units of log 2
+#pragma unroll
+                    for (int c = 0; c < KT; ++c) {
+                        const float e = ex2_approx(sv[c] * p.scale_log2);
+                        sv[c] = fmaf(-2.f * p.cap_log2, rcp_approx(1.f + e), p.cap_log2);
+                    }
+                }
+                if (t < it.fa || t >= it.fb) {
+                    const int k0 = it.kbase + t * KT;
+                    int a = max(first - k0, 0);
+                    int span = self - k0 - a;
+                    if (span < 0) {
+                        a = KT;
+                        span = 0;
+                    }
+#pragma unroll
+                    for (int c = 0; c < KT; ++c)
+                        sv[c] = (uint32_t)(c - a) <= (uint32_t)span ? sv[c] : -INFINITY;
+                }
+                const float csc = CAP ? 1.f : p.scale_log2;
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < KT; c += 8)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) mx[u] = fmax3(mx[u], sv[c + u], sv[c + 4 + u]);
+                const float tmax = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * csc;
+                const bool need = (m_used == -INFINITY) ? (tmax > -INFINITY) : (tmax > m_used + RESCALE_LOG2);
+                if (__any_sync(0xffffffffu, need)) {
+                    const float f = (need && m_used > -INFINITY) ? exp2f(m_used - tmax) : 1.f;
+                    if (j > j0) {
+                        // O holds every product before this S: rescale it
+#pragma unroll
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t r[16];
+                            tmem_ld16(tO + c, r);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+                            tmem_st16(tO + c, r);
+                        }
+                        // (the wait below covers these stores too)
+                    }
+                    l *= f;
+                    if (need) m_used = tmax;
+                }
+                const float nbase = (m_used == -INFINITY) ? 0.f : -m_used;
+                const uint64_t sc2 = f2_pack(csc, csc), nb2 = f2_pack(nbase, nbase);
+                uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+                for (int h = 0; h < KT; h += 64) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int c = 0; c < 64; c += 2) {
+                        float xa, xb;
+                        f2_unpack(f2_fma(f2_pack(sv[h + c], sv[h + c + 1]), sc2, nb2), xa, xb);
+                        const float a = ex2_approx(xa), b2 = ex2_approx(xb);
+                        acc[(c >> 1) & 3] = f2_add(acc[(c >> 1) & 3], f2_pack(a, b2));
+                        // weights to bfloat16, the products' input type: at most 2^-8 of each
+                        pk[c / 2] = pack_bf16x2(a, b2);
+                    }
+                    tmem_st32(tS + h / 2, pk);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_relaxed(&pfull[i]);
+                float lo, hi;
+                f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), lo, hi);
+                l += lo + hi;
+            }
+            if (!alive) break;
+            // ---- epilogue
+            const bool have = mine_n > 0;                     // O(i) holds this item
+            if (have) {
+                if (!wait_all(&ofull[i], oc & 1u)) {
+                    alive = false;
+                    break;
+                }
+                ++oc;
+                tc_fence_after();
+            }
+            // V rows that warp 10 took out although some rows attend to them
+            const uint32_t* notes = bad + (live % FIX_BUFS) * FIX_TILES * 4;
+            if (it.n > 0) ++live;
+            bool noted = false;
+            if (have && it.ntok > 1 && (it.fa > it.t_lo || it.fb < it.t_hi))
+                noted = __any_sync(0xffffffffu, lane < FIX_TILES * 4 && notes[lane] != 0u);
+            const bool wrows = (warp & 3) * 32 < p.G * min(it.ntok, p.npt);   // rows of the item in this warp
+            const float m_own = m_used;                       // the maximum that O(i) is relative to
+            // 32 columns of O from column c on
+            auto load_o = [&](int c, uint32_t (&r)[32]) {
+                if (!have || !wrows) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) r[e] = 0u;
+                    return;
+                }
+                tmem_ld32(tO + c, r);
+                tmem_wait_ld();
+                if (!noted || !mine) return;
+                const __nv_bfloat16* qrow = p.q + (int64_t)(it.row0 + tok) * p.q_stride + (int64_t)(it.g * p.G + head) * D;
+                for (int t = it.t_lo + j0; t < it.t_hi; t += step) {
+                    if (t >= it.fa && t < it.fb) continue;
+                    for (int e = 0; e < KT; ++e) {
+                        if (!((notes[fix_index(it, t) * 4 + (e >> 5)] >> (e & 31)) & 1u)) continue;
+                        const int key = it.kbase + t * KT + e;
+                        if (key < first || key > self) continue;
+                        const int64_t blk = p.c.table[(int64_t)it.b * p.c.max_blocks + key / p.c.bs];
+                        const int64_t krow = (blk * p.Hkv + it.g) * p.c.bs + key % p.c.bs;
+                        const float w = key_weight<D, CAP>(p, qrow, krow, m_own);
+                        const __nv_bfloat16* vrow = p.v + krow * D + c;
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            r[x] = __float_as_uint(fmaf(w, __bfloat162float(vrow[x]), __uint_as_float(r[x])));
+                    }
+                }
+            };
+            __nv_bfloat16* orow = p.out + (int64_t)(it.row0 + tok) * p.o_stride + (int64_t)(it.g * p.G + head) * D;
+            // partial result: [D / 4][rows] x 4 columns, then the maxima and the sums
+            float* pslot = it.slot >= 0 ? p.part + (int64_t)it.slot * p.prows * (D + 2) : nullptr;
+            const int prow = (two ? i * MT : 0) + row;
+            auto store_o = [&](int c, const uint32_t (&r)[32], float inv) {
+                if (!mine) return;
+                if (pslot) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        reinterpret_cast<float4*>(pslot)[(c + e) / 4 * p.prows + prow] =
+                            make_float4(__uint_as_float(r[e]), __uint_as_float(r[e + 1]),
+                                        __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint4 v;
+                        v.x = pack_bf16x2(__uint_as_float(r[e]) * inv, __uint_as_float(r[e + 1]) * inv);
+                        v.y = pack_bf16x2(__uint_as_float(r[e + 2]) * inv, __uint_as_float(r[e + 3]) * inv);
+                        v.z = pack_bf16x2(__uint_as_float(r[e + 4]) * inv, __uint_as_float(r[e + 5]) * inv);
+                        v.w = pack_bf16x2(__uint_as_float(r[e + 6]) * inv, __uint_as_float(r[e + 7]) * inv);
+                        *reinterpret_cast<uint4*>(orow + c + e) = v;
+                    }
+                }
+            };
+            auto store_ml = [&]() {
+                if (!mine || !pslot) return;
+                pslot[p.prows * D + prow] = m_used;
+                pslot[p.prows * (D + 1) + prow] = l;
+            };
+            if (!two && it.n > 1) {
+                // ---- two streams of one row tile: stream 1 hands its result over, half of the
+                // columns at a time (xo: [column][row], conflict-free)
+                constexpr int XC = D / 2;
+                float w0 = 1.f, w1 = 0.f;
+                if (i == 1 && wrows) {
+                    xo[row] = m_used;
+                    xo[128 + row] = l;
+                }
+                named_bar_sync(1, 256);
+                if (i == 0 && wrows) {
+                    const float m1 = xo[row], l1 = xo[128 + row];
+                    const float mm = fmaxf(m_used, m1), bz = mm == -INFINITY ? 0.f : mm;
+                    w0 = exp2f(m_used - bz);
+                    w1 = exp2f(m1 - bz);
+                    l = w0 * l + w1 * l1;
+                    m_used = mm;
+                }
+                named_bar_sync(2, 256);
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                for (int h = 0; h < D; h += XC) {
+                    if (i == 1) {
+#pragma unroll
+                        for (int c = 0; c < XC; c += 32) {
+                            uint32_t r[32];
+                            load_o(h + c, r);
+                            if (wrows)
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) xo[(c + e) * 128 + row] = __uint_as_float(r[e]);
+                        }
+                    }
+                    named_bar_sync(1, 256);
+                    if (i == 0 && wrows) {
+#pragma unroll
+                        for (int c = 0; c < XC; c += 32) {
+                            uint32_t r[32];
+                            load_o(h + c, r);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                r[e] = __float_as_uint(fmaf(w1, xo[(c + e) * 128 + row], w0 * __uint_as_float(r[e])));
+                            store_o(h + c, r, inv);
+                        }
+                    }
+                    named_bar_sync(2, 256);
+                }
+                if (i == 0) {
+                    store_ml();
+                    fence_proxy_async_smem();  // the next Q tile may land where xo was
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_relaxed(xdone);
+                }
+            } else if (two || i == 0) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t r[32];
+                    load_o(c, r);
+                    store_o(c, r, inv);
+                }
+                store_ml();
+            }
+            if (have) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_relaxed(&ofree[i]);  // O may be overwritten by the next item
+            }
+        }
+        if (!alive && lane == 0) *abort_flag = 1;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == MMA_WARP) tmem_dealloc(tmem, 512);
+}
+
+// Joins the pieces of the items that a run border cuts: one CTA per (border, 32
+// columns), which works when its border is the first to cut its item.  Weights
+// 2^(m_k - max) on the unnormalised rows, in run order.
+constexpr int JOIN_THREADS = 256;
+
+template <int D>
+__global__ void __launch_bounds__(JOIN_THREADS)
+chunk_tc_join_kernel(const __grid_constant__ Params p, int ctas) {
+    __shared__ ChunkLocateTmp<JOIN_THREADS> tmp;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (!chunk_starts_ok(p.c)) return;
+    const int64_t border = blockIdx.x + 1;
+    int64_t total = 0, runs = 0, x = 0;
+    const ChunkPlace at = chunk_locate<JOIN_THREADS>(&tmp, p.c.B, [&](int64_t t) {
+        total = t;
+        runs = run_count(t, ctas);
+        x = border < runs ? border * t / runs : t;
+        return x;
+    }, [&](int b) { return seq_units(p, b); });
+    if (at.b >= p.c.B) return;
+    const Seq s = seq_of(p, at.b);
+    int g, k, i0, i1, kbase, hi, tiles;
+    int64_t start;
+    item_at(p, s, x - at.base, g, k, start);
+    start += at.base;
+    const int64_t cost = seq_cost(s, k + 1) - seq_cost(s, k);
+    item_keys(p, s, k, i0, i1, kbase, hi, tiles);
+    const int cut = cut_tile(x - start, cost, tiles);
+    if (cut == 0 || cut == tiles) return;
+    const int64_t before = (border - 1) * total / runs;
+    if (before > start && cut_tile(before - start, cost, tiles) > 0) return;
+    // pieces: run border - 1 has the first, then every run up to the item's end
+    auto cut_of = [&](int64_t r) -> int {
+        const int64_t e = r < runs ? r * total / runs : total;
+        return cut_tile(min(e - start, cost), cost, tiles);
+    };
+    int64_t r_end = border;
+    while (cut_of(r_end + 1) < tiles) ++r_end;
+    const int ntok = i1 - i0, row = threadIdx.x;
+    const int t = row / MT, tok_l = (row % MT) / p.G, head = (row % MT) % p.G, tok = tok_l + t * p.npt;
+    if (tok_l >= p.npt || tok >= ntok || row >= p.prows) return;
+    const int64_t step = (int64_t)p.prows * (D + 2);
+    auto slot_of = [&](int64_t r) -> const float* { return p.part + (2 * r + (r == border - 1 ? 1 : 0)) * step; };
+    auto has = [&](int64_t r) -> bool { return r == border - 1 || cut_of(r) < cut_of(r + 1); };
+    float mx = -INFINITY;
+    for (int64_t r = border - 1; r <= r_end; ++r)
+        if (has(r)) mx = fmaxf(mx, slot_of(r)[p.prows * D + row]);
+    const float bz = mx == -INFINITY ? 0.f : mx;
+    float den = 0.f, acc[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+    const int c0 = blockIdx.y * 32;
+    for (int64_t r = border - 1; r <= r_end; ++r) {
+        if (!has(r)) continue;
+        const float* sl = slot_of(r);
+        const float w = exp2f(sl[p.prows * D + row] - bz);
+        den = fmaf(w, sl[p.prows * (D + 1) + row], den);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float4 v = reinterpret_cast<const float4*>(sl)[(c0 / 4 + e) * p.prows + row];
+            acc[4 * e] = fmaf(w, v.x, acc[4 * e]);
+            acc[4 * e + 1] = fmaf(w, v.y, acc[4 * e + 1]);
+            acc[4 * e + 2] = fmaf(w, v.z, acc[4 * e + 2]);
+            acc[4 * e + 3] = fmaf(w, v.w, acc[4 * e + 3]);
+        }
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    __nv_bfloat16* dst = p.out + (int64_t)(p.c.q_start[at.b] + i0 + tok) * p.o_stride + (int64_t)(g * p.G + head) * D + c0;
+#pragma unroll
+    for (int e = 0; e < 32; e += 8) {
+        uint4 v;
+        v.x = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+        v.y = pack_bf16x2(acc[e + 2] * inv, acc[e + 3] * inv);
+        v.z = pack_bf16x2(acc[e + 4] * inv, acc[e + 5] * inv);
+        v.w = pack_bf16x2(acc[e + 6] * inv, acc[e + 7] * inv);
+        *reinterpret_cast<uint4*>(dst + e) = v;
+    }
+}
+
+// ---------------------------------------------------------------- host side
+int partial_rows(int T, int G) { return T <= MT / G ? MT : 2 * MT; }
+
+template <int D, bool CAP>
+tv_status launch(const ChunkAttnArgs& a, const Params& p, const CUtensorMap& qm, const CUtensorMap& km,
+                 const CUtensorMap& vm, int ctas) {
+    static bool set[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TV_ERR_CUDA;
+    if (!set[dev]) {
+        if (cudaFuncSetAttribute(chunk_tc_kernel<D, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Lay<D>::BYTES) != cudaSuccess) {
+            cudaGetLastError();
+            return TV_ERR_CUDA;
+        }
+        set[dev] = true;
+    }
+    LaunchCfg lc(dim3((unsigned)ctas), dim3(THREADS), Lay<D>::BYTES, a.stream);
+    if (cudaLaunchKernelEx(&lc.cfg, chunk_tc_kernel<D, CAP>, qm, km, vm, p) != cudaSuccess) return TV_ERR_CUDA;
+    if (ctas == 1) return TV_OK;                               // nothing is cut
+    LaunchCfg lj(dim3((unsigned)(ctas - 1), D / 32), dim3(JOIN_THREADS), 0, a.stream);
+    return cudaLaunchKernelEx(&lj.cfg, chunk_tc_join_kernel<D>, p, ctas) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+}
+
+}  // namespace
+
+bool chunk_attn_tc_applicable(int Hq, int Hkv, int d, tv_dtype dt) {
+    return dt == TV_BF16 && (d == 64 || d == 128) && Hq / Hkv <= MT;
+}
+
+size_t chunk_attn_tc_workspace(int T, int B, int Hq, int Hkv, int d) {
+    (void)B;
+    return (size_t)2 * device_sm_count() * partial_rows(T, Hq / Hkv) * (d + 2) * sizeof(float);
+}
+
+tv_status launch_chunk_attn_tc(const ChunkAttnArgs& a) {
+    const int G = a.Hq / a.Hkv, npt = MT / G;
+    const int64_t rows = (int64_t)a.num_blocks * a.Hkv * a.bs;
+    if (rows >= (1ll << 31)) return TV_ERR_UNSUPPORTED;
+    CUtensorMap qm, km, vm;
+    if (!make_q_rows_map(&qm, a.q, a.d, a.Hq, a.T, a.q_stride, G, npt)) return TV_ERR_CUDA;
+    const bool maps = a.d == 128 ? make_kpage_map(&km, a.k_cache, rows) && make_page_map(&vm, a.v_cache, rows)
+                                 : make_cache_map(&km, a.k_cache, 64, rows) && make_cache_map(&vm, a.v_cache, 64, rows);
+    if (!maps) return TV_ERR_CUDA;
+    Params p{};
+    p.c = ChunkView{a.q_start, a.prefix_lens, a.block_table, a.T, a.B, a.max_blocks, a.bs, a.num_blocks};
+    p.out = static_cast<__nv_bfloat16*>(a.out);
+    p.o_stride = a.out_stride;
+    p.q = static_cast<const __nv_bfloat16*>(a.q);
+    p.q_stride = a.q_stride;
+    p.k = static_cast<const __nv_bfloat16*>(a.k_cache);
+    p.v = static_cast<const __nv_bfloat16*>(a.v_cache);
+    p.status = a.status;
+    p.part = static_cast<float*>(a.ws);
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.G = G;
+    p.npt = npt;
+    p.window = a.window;
+    p.prows = partial_rows(a.T, G);
+    p.scale_log2 = a.softcap > 0.f ? 2.f * LOG2E * a.scale / a.softcap : a.scale * LOG2E;
+    p.cap_log2 = a.softcap * LOG2E;
+    // one CTA per SM; fewer when even the longest sequences that fit give fewer runs
+    const int64_t items = (int64_t)a.Hkv * (a.T / (2 * npt) + std::min(a.T, a.B));
+    const int64_t units = items * std::min<int64_t>((int64_t)a.max_blocks * a.bs + C0, 1ll << 31);
+    const int ctas = (int)std::clamp<int64_t>(units / RUN_MIN, 1, device_sm_count());
+    if (a.d == 128)
+        return a.softcap > 0.f ? launch<128, true>(a, p, qm, km, vm, ctas) : launch<128, false>(a, p, qm, km, vm, ctas);
+    return a.softcap > 0.f ? launch<64, true>(a, p, qm, km, vm, ctas) : launch<64, false>(a, p, qm, km, vm, ctas);
+}
+
+}  // namespace tv

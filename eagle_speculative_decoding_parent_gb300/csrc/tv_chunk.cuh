@@ -55,20 +55,26 @@ __device__ __forceinline__ bool chunk_blocks_ok(const ChunkView& c, int b, int64
     return ok;
 }
 
-// Finds the sequence that holds unit x when sequence b has cost(b) units and the
-// sequences are laid end to end.  Called by every thread of the CTA (THREADS of
-// them); each thread sums a contiguous run of sequences, then the block scans.
+// Finds the sequence that holds unit x = where(total) when sequence b has cost(b)
+// units and the sequences are laid end to end.  Called by every thread of the CTA
+// (THREADS of them); each thread sums a contiguous run of sequences, then the
+// block scans.  tmp: shared memory of its own for the call.
 struct ChunkPlace {
     int64_t total;  // units of all sequences
     int64_t base;   // first unit of sequence b
     int b;          // B when x >= total
 };
 
-template <int THREADS, class Cost>
-__device__ __forceinline__ ChunkPlace chunk_locate(int B, int64_t x, Cost cost) {
-    __shared__ int64_t warp_sum[THREADS / 32];
-    __shared__ int64_t found_base;
-    __shared__ int found_b;
+template <int THREADS>
+struct ChunkLocateTmp {
+    int64_t warp_sum[THREADS / 32];
+    int64_t found_base;
+    int found_b;
+};
+
+template <int THREADS, class Where, class Cost>
+__device__ __forceinline__ ChunkPlace chunk_locate(ChunkLocateTmp<THREADS>* tmp, int B, Where where,
+                                                   Cost cost) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (B + THREADS - 1) / THREADS;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
@@ -81,22 +87,23 @@ __device__ __forceinline__ ChunkPlace chunk_locate(int B, int64_t x, Cost cost) 
         if (lane >= o) incl += y;
     }
     __syncthreads();  // the previous use of the shared words is over
-    if (lane == 31) warp_sum[warp] = incl;
-    if (tid == 0) found_b = B;
+    if (lane == 31) tmp->warp_sum[warp] = incl;
+    if (tid == 0) tmp->found_b = B;
     __syncthreads();
     int64_t before = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) before += warp_sum[w];
-        total += warp_sum[w];
+        if (w < warp) before += tmp->warp_sum[w];
+        total += tmp->warp_sum[w];
     }
+    const int64_t x = where(total);
     int64_t at = before + incl - s;
     if (x >= at && x < at + s) {
         for (int b = b0; b < b1; ++b) {
             const int64_t c = cost(b);
             if (x < at + c) {
-                found_b = b;
-                found_base = at;
+                tmp->found_b = b;
+                tmp->found_base = at;
                 break;
             }
             at += c;
@@ -105,8 +112,8 @@ __device__ __forceinline__ ChunkPlace chunk_locate(int B, int64_t x, Cost cost) 
     __syncthreads();
     ChunkPlace r;
     r.total = total;
-    r.b = found_b;
-    r.base = r.b < B ? found_base : total;
+    r.b = tmp->found_b;
+    r.base = r.b < B ? tmp->found_base : total;
     return r;
 }
 

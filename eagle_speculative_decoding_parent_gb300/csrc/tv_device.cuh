@@ -303,6 +303,12 @@ __device__ __forceinline__ float ex2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 1 / x with the hardware approximation (relative error about 2^-23).
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // Pairs of fp32 values in one 64-bit register, for the packed two-lane fp32
 // FMA / add of sm_100-class GPUs (one instruction for both lanes).
 __device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {

@@ -85,6 +85,9 @@ bool make_kpage_map(CUtensorMap* map, const void* base, int64_t rows);
 // Q [B*N][Hq][d] bf16: box 64 columns x G heads x npt nodes, 128-byte swizzle.
 bool make_q_map(CUtensorMap* map, const void* base, int d, int Hq, int64_t nodes, int G,
                 int npt);
+// Q [rows][Hq][d] bf16 with rows row_stride elements apart: the same box.
+bool make_q_rows_map(CUtensorMap* map, const void* base, int d, int Hq, int64_t rows,
+                     int64_t row_stride, int G, int npt);
 
 tv_status launch_tree_mask(const int32_t* parents, int B, int N, const int32_t* counts,
                            uint64_t* mask, int32_t* depth, int32_t* status, cudaStream_t stream);
@@ -217,6 +220,10 @@ struct ChunkAttnArgs {
 };
 size_t chunk_attn_f32_workspace(int T, int B, int Hq, int Hkv, int d);
 tv_status launch_chunk_attn_f32(const ChunkAttnArgs& a);
+// tensor-core kernel: bfloat16, up to 128 query heads per kv head
+bool chunk_attn_tc_applicable(int Hq, int Hkv, int d, tv_dtype dt);
+size_t chunk_attn_tc_workspace(int T, int B, int Hq, int Hkv, int d);
+tv_status launch_chunk_attn_tc(const ChunkAttnArgs& a);
 
 tv_status launch_token_counts(int32_t* counts, const int32_t* tokens, const int32_t* starts,
                               int total, int B, int V, bool clear, bool prompt, int32_t* status,
