@@ -55,8 +55,8 @@ __device__ __forceinline__ void cf_store4(__nv_bfloat16* p, float4 v) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
-__device__ __forceinline__ int64_t cf_tiles(const CfParams& p, int b) {
-    return ((int64_t)(p.c.q_start[b + 1] - p.c.q_start[b]) * p.G + CF_M - 1) / CF_M;
+__device__ __forceinline__ int64_t cf_tiles(const CfParams& p, int n) {
+    return ((int64_t)n * p.G + CF_M - 1) / CF_M;
 }
 
 // The row tile of this CTA.
@@ -68,8 +68,8 @@ struct CfTile {
 // false: no such tile.  Called by every thread (contains barriers).
 __device__ __forceinline__ bool cf_find(const CfParams& p, int tile, CfTile& t) {
     __shared__ ChunkLocateTmp<CF_THREADS> tmp;
-    const ChunkPlace at = chunk_locate<CF_THREADS>(&tmp, p.c.B, [&](int64_t) { return (int64_t)tile; },
-                                                   [&](int b) { return cf_tiles(p, b); });
+    const ChunkPlace at = chunk_locate<CF_THREADS>(&tmp, p.c, [&](int64_t) { return (int64_t)tile; },
+                                                   [&](int, int n) { return cf_tiles(p, n); });
     if (at.b >= p.c.B) return false;
     t.b = at.b;
     t.s = p.c.q_start[at.b];
@@ -281,8 +281,8 @@ __global__ void __launch_bounds__(CF_THREADS) chunk_join_kernel(CfParams p) {
     const int g = blockIdx.y, tid = threadIdx.x;
     if (!chunk_starts_ok(p.c)) return;
     __shared__ ChunkLocateTmp<CF_THREADS> tmp;
-    const ChunkPlace at = chunk_locate<CF_THREADS>(&tmp, p.c.B, [&](int64_t) { return (int64_t)blockIdx.x; },
-                                                   [&](int b) { return cf_tiles(p, b); });
+    const ChunkPlace at = chunk_locate<CF_THREADS>(&tmp, p.c, [&](int64_t) { return (int64_t)blockIdx.x; },
+                                                   [&](int, int n) { return cf_tiles(p, n); });
     if (at.b >= p.c.B) return;
     const int s = p.c.q_start[at.b], n = p.c.q_start[at.b + 1] - s;
     const int r0 = ((int)blockIdx.x - (int)at.base) * CF_M, rows = min(CF_M, n * p.G - r0);

@@ -93,9 +93,9 @@ struct Lay {
     static constexpr int OFF_BAD = OFF_ITEMS + GQ * 64;    // [FIX_BUFS][FIX_TILES][4]
     static constexpr int OFF_BARS = OFF_BAD + FIX_BUFS * FIX_TILES * 16;
     static constexpr int NBARS = 3 * SLOTS + 8 + 4 + 2 * GQ;
-    static constexpr int OFF_TMP = OFF_BARS + NBARS * 8;   // ChunkLocateTmp, then words
-    static constexpr int OFF_MISC = OFF_TMP + (int)sizeof(ChunkLocateTmp<THREADS>);
-    static constexpr int BYTES = OFF_MISC + 32 + 1024;     // + alignment slack
+    static constexpr int OFF_ML = OFF_BARS + NBARS * 8;    // join: maximum, sum per row
+    static constexpr int OFF_MISC = OFF_ML + 2 * MT * 4;
+    static constexpr int BYTES = OFF_MISC + 16 + 1024;     // + alignment slack
 };
 static_assert(Lay<128>::BYTES <= 232448 && Lay<64>::BYTES <= 232448, "shared memory of one SM");
 
@@ -119,41 +119,45 @@ struct Params {
 // Sequence of n rows after P keys: items of m = 2 npt tokens, item k costing C0 +
 // min(P + (k + 1) m, window + m) keys, the last one C0 + min(P + n, window + m).
 struct Seq {
-    int P, n;
-    int64_t m, w;                // tokens per item; window + m, or no limit
-    int items;
+    int P, n, m, items;          // m: tokens per item
+    int64_t w;                   // window + m, or no limit
     bool shape;                  // P and n fit the block table
 };
+constexpr int64_t NO_WINDOW = 1ll << 40;
 
-__device__ __forceinline__ Seq seq_of(const Params& p, int b) {
+__device__ __forceinline__ Seq seq_of(const Params& p, int P, int n) {
     Seq s;
-    s.P = p.c.prefix[b];
-    s.n = p.c.q_start[b + 1] - p.c.q_start[b];
-    s.shape = chunk_shape_ok(p.c, s.P, s.n);
+    s.P = P;
+    s.n = n;
+    s.shape = chunk_shape_ok(p.c, P, n);
     s.m = 2 * p.npt;
-    s.w = p.window > 0 ? p.window + s.m : (1ll << 40);
-    s.items = (int)((s.n + s.m - 1) / s.m);
+    s.w = p.window > 0 ? (int64_t)p.window + s.m : NO_WINDOW;
+    s.items = (int)(((unsigned)n + (unsigned)s.m - 1) / (unsigned)s.m);
     return s;
 }
-// Cost of the first k items.
-__device__ __forceinline__ int64_t seq_cost(const Seq& s, int64_t k) {
-    if (!s.shape) return k * C0;
-    const int64_t full = min(k, (int64_t)s.items - 1);           // items of m tokens
-    int64_t lin = full;                                          // of them below the window's limit
-    if (s.w < (1ll << 40)) lin = min(full, max((int64_t)0, (s.w - s.P + s.m - 1) / s.m - 1));
-    int64_t c = lin * s.P + s.m * (lin * (lin + 1) / 2) + (full - lin) * s.w + full * C0;
-    if (k == s.items && k > 0) c += C0 + min((int64_t)s.P + s.n, s.w);
-    return c;
+// Cost of item k, and of the first k items.
+__device__ __forceinline__ int64_t item_cost(const Seq& s, int k) {
+    if (!s.shape) return C0;
+    return C0 + min((int64_t)s.P + min((int64_t)s.n, (int64_t)(k + 1) * s.m), s.w);
 }
-__device__ __forceinline__ int64_t seq_units(const Params& p, int b) {
-    const Seq s = seq_of(p, b);
+__device__ __forceinline__ int64_t seq_cost(const Seq& s, int k) {
+    if (!s.shape || k == 0) return k * C0;
+    const int64_t full = min(k, s.items - 1);                    // items of m tokens
+    int64_t lin = full;                                          // of them below the window's limit
+    if (s.w != NO_WINDOW) lin = s.w > s.P ? min(full, (int64_t)((unsigned)(s.w - s.P) / (unsigned)s.m)) : 0;
+    int64_t c = lin * s.P + s.m * (lin * (lin + 1) / 2) + full * C0;
+    if (lin < full) c += (full - lin) * s.w;
+    return k == s.items ? c + item_cost(s, k - 1) : c;
+}
+__device__ __forceinline__ int64_t seq_units(const Params& p, int P, int n) {
+    const Seq s = seq_of(p, P, n);
     return s.items == 0 ? 0 : seq_cost(s, s.items) * p.Hkv;
 }
 // Keys of item k: from kbase (multiple of 16) to hi, in tiles of KT.
 __device__ __forceinline__ void item_keys(const Params& p, const Seq& s, int k, int& i0, int& i1,
                                           int& kbase, int& hi, int& tiles) {
-    i0 = (int)(k * s.m);
-    i1 = (int)min((int64_t)s.n, i0 + s.m);
+    i0 = k * s.m;
+    i1 = min(s.n, i0 + s.m);
     if (!s.shape) {
         kbase = hi = tiles = 0;
         return;
@@ -162,19 +166,24 @@ __device__ __forceinline__ void item_keys(const Params& p, const Seq& s, int k, 
     kbase = chunk_first_key(s.P + i0, p.window) & ~15;
     tiles = (hi - kbase + KT - 1) / KT;
 }
-// Tile at which a border y units into an item of the given cost cuts it.
+// Tile at which a border y units into an item of the given cost cuts it (the same
+// float arithmetic everywhere, and non-decreasing in y).
 __device__ __forceinline__ int cut_tile(int64_t y, int64_t cost, int tiles) {
     if (y <= C0) return 0;
     if (y >= cost) return tiles;
-    return (int)min((int64_t)tiles, ((y - C0) * tiles + (cost - C0) - 1) / (cost - C0));
+    const float per = __fdiv_rn((float)tiles, (float)(cost - C0));
+    return min(tiles, (int)ceilf(__fmul_rn((float)(y - C0), per)));
 }
 // Item at unit y of a sequence (Hkv equal stretches): kv head, item, its first unit.
 __device__ __forceinline__ void item_at(const Params& p, const Seq& s, int64_t y, int& g, int& k,
                                         int64_t& start) {
     const int64_t per = seq_cost(s, s.items);
-    g = (int)(y / per);
+    g = min(p.Hkv - 1, (int)__fdiv_rn((float)y, (float)per));
+    while (g * per > y) --g;                                     // the quotient, made exact
+    while ((g + 1) * per <= y) ++g;
     const int64_t r = y - g * per;
     int lo = 0, hi = s.items;                                    // cost(lo) <= r < cost(hi)
+#pragma unroll 1
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (seq_cost(s, mid) <= r) lo = mid;
@@ -183,9 +192,21 @@ __device__ __forceinline__ void item_at(const Params& p, const Seq& s, int64_t y
     k = lo;
     start = g * per + seq_cost(s, lo);
 }
-// Runs: as many as there are CTAs, fewer when they would be short.
-__device__ __forceinline__ int64_t run_count(int64_t units, int64_t ctas) {
-    return max((int64_t)1, min(ctas, units / RUN_MIN));
+// Runs of equal length over the units: as many as there are CTAs, fewer when they
+// would be short; the length is rounded up, so the last run may be shorter.
+struct Runs {
+    int64_t total, len;
+    int count;
+};
+__device__ __forceinline__ Runs runs_of(int64_t total, int ctas) {
+    Runs r;
+    r.total = total;
+    r.count = (int)max((int64_t)1, min((int64_t)ctas, total / RUN_MIN));
+    r.len = __float2ll_ru(__fdiv_ru(__ll2float_ru(total), (float)r.count));
+    return r;
+}
+__device__ __forceinline__ int64_t run_start(const Runs& r, int i) {
+    return i < r.count ? min(i * r.len, r.total) : r.total;
 }
 
 // Tiles of an item that warp 10 goes through: t < fa (some rows' windows start
@@ -199,15 +220,49 @@ __device__ __forceinline__ int fix_index(const Item& it, int t) {  // 0 .. FIX_T
     return t < it.fa ? t : max(it.fa, 0) + (t - max(it.fa, it.fb));
 }
 
-// Weight 2^(s - m) of one key for one row, from global memory (rare: V rows with
-// NaN or infinity).
+// Adds to O (tensor memory, this warp's lanes) the V rows that warp 10 took out
+// although some rows attend to them: weight 2^(s - m), the score from global
+// memory.  Rare (V rows with NaN or infinity), so out of line.  t0, step: the
+// stream's tiles; first .. self: the lane's keys (none: self < first).
 template <int D, bool CAP>
-__device__ __noinline__ float key_weight(const Params& p, const __nv_bfloat16* q, int64_t krow, float m) {
-    float s = 0.f;
-    for (int c = 0; c < D; ++c) s = fmaf(__bfloat162float(q[c]), __bfloat162float(p.k[krow * D + c]), s);
-    s *= p.scale_log2;
-    if (CAP) s = p.cap_log2 * (1.f - 2.f / (1.f + exp2f(s)));
-    return exp2f(s - m);
+__device__ __noinline__ void add_noted(const Params& p, const Item& it, const uint32_t* notes, int t0,
+                                       int step, uint32_t tO, int first, int self,
+                                       const __nv_bfloat16* q, float m) {
+#pragma unroll 1
+    for (int t = t0; t < it.t_hi; t += step) {
+        if (t >= it.fa && t < it.fb) continue;
+#pragma unroll 1
+        for (int e = 0; e < KT; ++e) {
+            if (!((notes[fix_index(it, t) * 4 + (e >> 5)] >> (e & 31)) & 1u)) continue;
+            const int key = it.kbase + t * KT + e;
+            const int64_t blk = p.c.table[(int64_t)it.b * p.c.max_blocks + key / p.c.bs];
+            const int64_t krow = ((blk * p.Hkv + it.g) * p.c.bs + key % p.c.bs) * D;
+            const bool seen = key >= first && key <= self;
+            float w = 0.f;
+            if (seen) {
+                float s = 0.f;
+#pragma unroll 1
+                for (int c = 0; c < D; ++c) s = fmaf(__bfloat162float(q[c]), __bfloat162float(p.k[krow + c]), s);
+                s *= p.scale_log2;
+                if (CAP) s = p.cap_log2 * (1.f - 2.f / (1.f + exp2f(s)));
+                w = exp2f(s - m);
+            }
+            __syncwarp();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+                uint32_t r[16];
+                tmem_ld16(tO + c, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const float o = __uint_as_float(r[x]);
+                    r[x] = __float_as_uint(seen ? fmaf(w, __bfloat162float(p.v[krow + c + x]), o) : o);
+                }
+                tmem_st16(tO + c, r);
+                tmem_wait_st();
+            }
+        }
+    }
 }
 
 template <int D, bool CAP>
@@ -235,14 +290,13 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     uint64_t* gq_full = drain + 1;        // [GQ]
     uint64_t* gq_empty = gq_full + GQ;    // [GQ]
     uint64_t* vraw = gq_empty + GQ;       // [SLOTS] a V tile that warp 10 goes through has landed
-    auto* tmp = reinterpret_cast<ChunkLocateTmp<THREADS>*>(smem + L::OFF_TMP);
+    auto* tmp = reinterpret_cast<ChunkLocateTmp<THREADS>*>(smem + L::OFF_RING);  // before the first copy
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
     int* seq_ok = reinterpret_cast<int*>(smem + L::OFF_MISC + 8);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = smem_u32(smem);
-    pdl_launch_dependents();
     if (tid == 0) {
         for (int s = 0; s < L::SLOTS; ++s) {
             mbar_init(&full[s], 1);
@@ -284,34 +338,32 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
     pdl_wait();  // everything above touched only shared memory and tensor memory
+    // after the wait: the join kernel may read the inputs before its own wait
+    pdl_launch_dependents();
 
     // ---- this CTA's run
-    const bool valid = chunk_starts_ok(p.c);
+    Runs runs;
+    int64_t x_lo = 0, x_hi = 0;
+    const ChunkPlace at = chunk_locate<THREADS>(tmp, p.c, [&](int64_t total) {
+        runs = runs_of(total, gridDim.x);
+        x_lo = run_start(runs, blockIdx.x);
+        x_hi = run_start(runs, blockIdx.x + 1);
+        return x_lo < x_hi ? x_lo : total;
+    }, [&](int P, int n) { return seq_units(p, P, n); });
     if (blockIdx.x == 0)
         for (int b = tid; b < p.c.B; b += THREADS)
-            if (!valid || p.c.q_start[b] == p.c.q_start[b + 1])
-                p.status[b] = (valid && chunk_shape_ok(p.c, p.c.prefix[b], 0)) ? TV_OK : TV_ERR_OUT_OF_RANGE;
-    ChunkPlace at;
-    at.b = p.c.B;
-    int64_t x_lo = 0, x_hi = 0;
-    if (valid) {
-        int64_t units = 0;
-        at = chunk_locate<THREADS>(tmp, p.c.B, [&](int64_t total) {
-            units = total;
-            const int64_t runs = run_count(total, gridDim.x), r = blockIdx.x;
-            x_lo = r < runs ? r * total / runs : total;
-            x_hi = r < runs ? (r + 1) * total / runs : total;
-            return x_lo;
-        }, [&](int b) { return seq_units(p, b); });
-        if (at.b < p.c.B) {
-            // the first sequence's blocks, by every thread at once
-            const Seq s = seq_of(p, at.b);
-            const bool ok = s.shape && chunk_blocks_ok(p.c, at.b, chunk_first_key(s.P, p.window),
-                                                       (int64_t)s.P + s.n, tid, THREADS);
-            const int all = __syncthreads_and(ok ? 1 : 0);
-            if (tid == 0) *seq_ok = all;
-        }
+            if (!at.valid || p.c.q_start[b] == p.c.q_start[b + 1])
+                p.status[b] = (at.valid && chunk_shape_ok(p.c, p.c.prefix[b], 0)) ? TV_OK : TV_ERR_OUT_OF_RANGE;
+    Seq s0{};
+    if (at.b < p.c.B) {
+        // the first sequence's blocks, by every thread at once
+        s0 = seq_of(p, p.c.prefix[at.b], p.c.q_start[at.b + 1] - p.c.q_start[at.b]);
+        const bool ok = s0.shape && chunk_blocks_ok(p.c, at.b, chunk_first_key(s0.P, p.window),
+                                                    (int64_t)s0.P + s0.n, tid, THREADS);
+        const int all = __syncthreads_and(ok ? 1 : 0);
+        if (tid == 0) *seq_ok = all;
     }
+    fence_proxy_async_smem();  // the ring's first bytes held the search's scratch
     __syncthreads();
 
     auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -333,69 +385,71 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
 
     if (warp == SCHED_WARP) {
         // ============================== scheduler ==============================
-        int b = at.b;
-        int64_t x = x_lo, base = at.base;
-        bool ok = b < p.c.B && *seq_ok != 0;
         uint32_t k = 0;
         auto publish = [&](const Item& it) -> bool {
             const int s = k % GQ;
             if (!wait_all(&gq_empty[s], ((k / GQ) & 1u) ^ 1u)) return false;
-            if (lane < 4)
-                reinterpret_cast<int4*>(&items[s])[lane] =
-                    lane == 0 ? make_int4(it.b, it.g, it.P, it.i0)
-                    : lane == 1 ? make_int4(it.ntok, it.row0, it.kbase, it.hi)
-                    : lane == 2 ? make_int4(it.t_lo, it.t_hi, it.fa, it.fb)
-                                : make_int4(it.flags, it.slot, it.n, 0);
+            if (lane == 0) {
+                const int4* src = reinterpret_cast<const int4*>(&it);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) reinterpret_cast<int4*>(&items[s])[u] = src[u];
+                mbar_arrive(&gq_full[s]);
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&gq_full[s]);
             ++k;
             return true;
         };
-        Seq s{};
-        int64_t units = 0;
-        bool fresh = true, alive = true;
-        while (alive && x < x_hi && b < p.c.B) {
-            if (fresh) {
-                s = seq_of(p, b);
-                units = s.items == 0 ? 0 : seq_cost(s, s.items) * p.Hkv;
-                if (b != at.b && units > 0) {
-                    ok = s.shape && chunk_blocks_ok(p.c, b, chunk_first_key(s.P, p.window),
-                                                    (int64_t)s.P + s.n, lane, 32);
-                    ok = __all_sync(0xffffffffu, ok);
+        bool alive = true;
+        if (at.b < p.c.B) {
+            int b = at.b, g, qk;
+            Seq s = s0;
+            bool ok = *seq_ok != 0;
+            int64_t start, x = x_lo;
+            item_at(p, s, x_lo - at.base, g, qk, start);
+            start += at.base;
+#pragma unroll 1
+            while (true) {
+                Item it;
+                int i1, tiles;
+                const int64_t cost = item_cost(s, qk);
+                item_keys(p, s, qk, it.i0, i1, it.kbase, it.hi, tiles);
+                it.t_lo = cut_tile(x - start, cost, tiles);
+                it.t_hi = cut_tile(min(x_hi - start, cost), cost, tiles);
+                // a sequence that does not fit has items without tiles: the run with the first
+                // unit writes them
+                if (tiles == 0 ? x == start : it.t_lo < it.t_hi) {
+                    const bool whole = it.t_lo == 0 && it.t_hi == tiles;
+                    it.b = b;
+                    it.g = g;
+                    it.P = s.P;
+                    it.ntok = i1 - it.i0;
+                    it.row0 = p.c.q_start[b] + it.i0;
+                    it.slot = whole ? -1 : 2 * (int)blockIdx.x + (it.t_lo == 0 ? 1 : 0);
+                    it.n = ok ? it.t_hi - it.t_lo : 0;
+                    it.flags = (it.ntok > p.npt ? ITEM_TWO : 0) | (ok ? 0 : ITEM_BAD) |
+                               (g == 0 && it.i0 == 0 && it.t_lo == 0 ? ITEM_STATUS : 0);
+                    it.pad = 0;
+                    item_edges(p, it);
+                    alive = publish(it);
                 }
-                fresh = false;
+                start += cost;
+                x = start;
+                if (!alive || x >= x_hi) break;
+                if (++qk < s.items) continue;
+                qk = 0;
+                if (++g < p.Hkv) continue;
+                g = 0;
+                // the next sequence with rows: there is one, since x < x_hi
+                int n = 0;
+                do {
+                    ++b;
+                    n = p.c.q_start[b + 1] - p.c.q_start[b];
+                } while (n == 0 && b + 1 < p.c.B);
+                s = seq_of(p, p.c.prefix[b], n);
+                ok = s.shape && chunk_blocks_ok(p.c, b, chunk_first_key(s.P, p.window),
+                                                (int64_t)s.P + s.n, lane, 32);
+                ok = __all_sync(0xffffffffu, ok);
             }
-            if (x >= base + units) {
-                base += units;
-                ++b;
-                fresh = true;
-                continue;
-            }
-            Item it;
-            int qk, i1, tiles;
-            int64_t start;
-            item_at(p, s, x - base, it.g, qk, start);
-            start += base;
-            const int64_t cost = seq_cost(s, qk + 1) - seq_cost(s, qk);
-            const int64_t y0 = x - start, y1 = min(x_hi - start, cost);
-            item_keys(p, s, qk, it.i0, i1, it.kbase, it.hi, tiles);
-            x = start + y1;
-            it.t_lo = cut_tile(y0, cost, tiles);
-            it.t_hi = cut_tile(y1, cost, tiles);
-            // a sequence that does not fit has items without tiles: the run with the first unit
-            // writes them
-            if (tiles == 0 ? y0 != 0 : it.t_lo == it.t_hi) continue;
-            const bool whole = it.t_lo == 0 && it.t_hi == tiles;
-            it.b = b;
-            it.P = s.P;
-            it.ntok = i1 - it.i0;
-            it.row0 = p.c.q_start[b] + it.i0;
-            it.slot = whole ? -1 : 2 * (int)blockIdx.x + (it.t_lo == 0 ? 1 : 0);
-            it.n = ok ? it.t_hi - it.t_lo : 0;
-            it.flags = (it.ntok > p.npt ? ITEM_TWO : 0) | (ok ? 0 : ITEM_BAD) |
-                       (it.g == 0 && it.i0 == 0 && it.t_lo == 0 ? ITEM_STATUS : 0);
-            item_edges(p, it);
-            alive = publish(it);
         }
         if (alive) {
             Item it{};
@@ -688,7 +742,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + lane_off + i * KT, tO = tmem + lane_off + TMEM_O + i * D;
         const int tok_l = row / p.G, head = row - tok_l * p.G;
-        float* xo = reinterpret_cast<float*>(smem + L::OFF_X);  // [columns][128 rows]
+        float* xo = reinterpret_cast<float*>(smem + L::OFF_X);  // [columns][rows]
+        float* ml = reinterpret_cast<float*>(smem + L::OFF_ML);
         uint32_t sc = 0, oc = 0, live = 0;
         bool alive = true;
         Item it;
@@ -730,16 +785,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     }
                 }
                 if (t < it.fa || t >= it.fb) {
+                    // visible keys of the tile: bits a .. z, a word for 32 columns
                     const int k0 = it.kbase + t * KT;
-                    int a = max(first - k0, 0);
-                    int span = self - k0 - a;
-                    if (span < 0) {
-                        a = KT;
-                        span = 0;
-                    }
+                    const int a = first - k0, z = self - k0;
 #pragma unroll
-                    for (int c = 0; c < KT; ++c)
-                        sv[c] = (uint32_t)(c - a) <= (uint32_t)span ? sv[c] : -INFINITY;
+                    for (int h = 0; h < KT; h += 32) {
+                        const int lo = min(max(a - h, 0), 32), hi = min(max(z - h + 1, 0), 32);
+                        const uint32_t vis = hi > lo ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) sv[h + c] = ((vis >> c) & 1u) ? sv[h + c] : -INFINITY;
+                    }
                 }
                 const float csc = CAP ? 1.f : p.scale_log2;
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -753,7 +808,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     const float f = (need && m_used > -INFINITY) ? exp2f(m_used - tmax) : 1.f;
                     if (j > j0) {
                         // O holds every product before this S: rescale it
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             uint32_t r[16];
                             tmem_ld16(tO + c, r);
@@ -806,128 +861,101 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             // V rows that warp 10 took out although some rows attend to them
             const uint32_t* notes = bad + (live % FIX_BUFS) * FIX_TILES * 4;
             if (it.n > 0) ++live;
-            bool noted = false;
-            if (have && it.ntok > 1 && (it.fa > it.t_lo || it.fb < it.t_hi))
-                noted = __any_sync(0xffffffffu, lane < FIX_TILES * 4 && notes[lane] != 0u);
-            const bool wrows = (warp & 3) * 32 < p.G * min(it.ntok, p.npt);   // rows of the item in this warp
-            const float m_own = m_used;                       // the maximum that O(i) is relative to
-            // 32 columns of O from column c on
-            auto load_o = [&](int c, uint32_t (&r)[32]) {
-                if (!have || !wrows) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) r[e] = 0u;
-                    return;
-                }
-                tmem_ld32(tO + c, r);
-                tmem_wait_ld();
-                if (!noted || !mine) return;
-                const __nv_bfloat16* qrow = p.q + (int64_t)(it.row0 + tok) * p.q_stride + (int64_t)(it.g * p.G + head) * D;
-                for (int t = it.t_lo + j0; t < it.t_hi; t += step) {
-                    if (t >= it.fa && t < it.fb) continue;
-                    for (int e = 0; e < KT; ++e) {
-                        if (!((notes[fix_index(it, t) * 4 + (e >> 5)] >> (e & 31)) & 1u)) continue;
-                        const int key = it.kbase + t * KT + e;
-                        if (key < first || key > self) continue;
-                        const int64_t blk = p.c.table[(int64_t)it.b * p.c.max_blocks + key / p.c.bs];
-                        const int64_t krow = (blk * p.Hkv + it.g) * p.c.bs + key % p.c.bs;
-                        const float w = key_weight<D, CAP>(p, qrow, krow, m_own);
-                        const __nv_bfloat16* vrow = p.v + krow * D + c;
-#pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            r[x] = __float_as_uint(fmaf(w, __bfloat162float(vrow[x]), __uint_as_float(r[x])));
-                    }
-                }
-            };
-            __nv_bfloat16* orow = p.out + (int64_t)(it.row0 + tok) * p.o_stride + (int64_t)(it.g * p.G + head) * D;
+            if (have && it.ntok > 1 && (it.fa > it.t_lo || it.fb < it.t_hi) &&
+                __any_sync(0xffffffffu, lane < FIX_TILES * 4 && notes[lane] != 0u))
+                add_noted<D, CAP>(p, it, notes, it.t_lo + j0, step, tO, first, mine ? self : -1,
+                                  p.q + (int64_t)(it.row0 + tok) * p.q_stride + (int64_t)(it.g * p.G + head) * D,
+                                  m_used);
+            // Two streams of one row tile: stream 1 hands its result over through shared
+            // memory, XC columns at a time (all of them when the rows are few).
+            const bool join = !two && it.n > 1;
+            const int rows = p.G * min(it.ntok, p.npt);       // rows of the item in a row tile
+            const bool wrows = (warp & 3) * 32 < rows;        // some of them in this warp
+            const int pitch = rows <= MT / 2 ? MT / 2 : MT;
+            const int XC = join ? (rows <= MT / 2 ? D : D / 2) : D;
+            float w0 = 1.f, w1 = 0.f;
             // partial result: [D / 4][rows] x 4 columns, then the maxima and the sums
             float* pslot = it.slot >= 0 ? p.part + (int64_t)it.slot * p.prows * (D + 2) : nullptr;
             const int prow = (two ? i * MT : 0) + row;
-            auto store_o = [&](int c, const uint32_t (&r)[32], float inv) {
-                if (!mine) return;
-                if (pslot) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        reinterpret_cast<float4*>(pslot)[(c + e) / 4 * p.prows + prow] =
-                            make_float4(__uint_as_float(r[e]), __uint_as_float(r[e + 1]),
-                                        __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint4 v;
-                        v.x = pack_bf16x2(__uint_as_float(r[e]) * inv, __uint_as_float(r[e + 1]) * inv);
-                        v.y = pack_bf16x2(__uint_as_float(r[e + 2]) * inv, __uint_as_float(r[e + 3]) * inv);
-                        v.z = pack_bf16x2(__uint_as_float(r[e + 4]) * inv, __uint_as_float(r[e + 5]) * inv);
-                        v.w = pack_bf16x2(__uint_as_float(r[e + 6]) * inv, __uint_as_float(r[e + 7]) * inv);
-                        *reinterpret_cast<uint4*>(orow + c + e) = v;
-                    }
-                }
-            };
-            auto store_ml = [&]() {
-                if (!mine || !pslot) return;
-                pslot[p.prows * D + prow] = m_used;
-                pslot[p.prows * (D + 1) + prow] = l;
-            };
-            if (!two && it.n > 1) {
-                // ---- two streams of one row tile: stream 1 hands its result over, half of the
-                // columns at a time (xo: [column][row], conflict-free)
-                constexpr int XC = D / 2;
-                float w0 = 1.f, w1 = 0.f;
-                if (i == 1 && wrows) {
-                    xo[row] = m_used;
-                    xo[128 + row] = l;
-                }
-                named_bar_sync(1, 256);
-                if (i == 0 && wrows) {
-                    const float m1 = xo[row], l1 = xo[128 + row];
-                    const float mm = fmaxf(m_used, m1), bz = mm == -INFINITY ? 0.f : mm;
-                    w0 = exp2f(m_used - bz);
-                    w1 = exp2f(m1 - bz);
-                    l = w0 * l + w1 * l1;
-                    m_used = mm;
-                }
-                named_bar_sync(2, 256);
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-                for (int h = 0; h < D; h += XC) {
-                    if (i == 1) {
-#pragma unroll
+            __nv_bfloat16* orow = p.out + (int64_t)(it.row0 + tok) * p.o_stride + (int64_t)(it.g * p.G + head) * D;
+            float inv = 0.f;
+#pragma unroll 1
+            for (int h = 0; h < D; h += XC) {
+                if (join) {
+                    if (i == 1 && wrows) {
+                        if (h == 0) {
+                            ml[row] = m_used;
+                            ml[MT + row] = l;
+                        }
+#pragma unroll 1
                         for (int c = 0; c < XC; c += 32) {
                             uint32_t r[32];
-                            load_o(h + c, r);
-                            if (wrows)
+                            tmem_ld32(tO + h + c, r);
+                            tmem_wait_ld();
+                            if (row < pitch)
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) xo[(c + e) * 128 + row] = __uint_as_float(r[e]);
+                                for (int e = 0; e < 32; ++e) xo[(c + e) * pitch + row] = __uint_as_float(r[e]);
                         }
                     }
                     named_bar_sync(1, 256);
-                    if (i == 0 && wrows) {
-#pragma unroll
-                        for (int c = 0; c < XC; c += 32) {
-                            uint32_t r[32];
-                            load_o(h + c, r);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                r[e] = __float_as_uint(fmaf(w1, xo[(c + e) * 128 + row], w0 * __uint_as_float(r[e])));
-                            store_o(h + c, r, inv);
+                }
+                if ((two || i == 0) && wrows) {
+                    if (h == 0) {
+                        if (join) {
+                            const float m1 = ml[row], l1 = ml[MT + row];
+                            const float mm = fmaxf(m_used, m1), bz = mm == -INFINITY ? 0.f : mm;
+                            w0 = exp2f(m_used - bz);
+                            w1 = exp2f(m1 - bz);
+                            l = w0 * l + w1 * l1;
+                            m_used = mm;
+                        }
+                        inv = pslot ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+                        if (mine && pslot) {
+                            pslot[p.prows * D + prow] = m_used;
+                            pslot[p.prows * (D + 1) + prow] = l;
                         }
                     }
-                    named_bar_sync(2, 256);
-                }
-                if (i == 0) {
-                    store_ml();
-                    fence_proxy_async_smem();  // the next Q tile may land where xo was
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_relaxed(xdone);
-                }
-            } else if (two || i == 0) {
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+                    for (int c = h; c < h + XC; c += 32) {
+                        uint32_t r[32];
+                        if (have) {
+                            tmem_ld32(tO + c, r);
+                            tmem_wait_ld();
+                        } else {
 #pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t r[32];
-                    load_o(c, r);
-                    store_o(c, r, inv);
+                            for (int e = 0; e < 32; ++e) r[e] = 0u;
+                        }
+                        if (!mine) continue;
+                        float f[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(r[e]);
+                        if (join)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) f[e] = fmaf(w1, xo[(c - h + e) * pitch + row], w0 * f[e]);
+                        if (pslot) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                reinterpret_cast<float4*>(pslot)[(c + e) / 4 * p.prows + prow] =
+                                    make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8) {
+                                uint4 v;
+                                v.x = pack_bf16x2(f[e] * inv, f[e + 1] * inv);
+                                v.y = pack_bf16x2(f[e + 2] * inv, f[e + 3] * inv);
+                                v.z = pack_bf16x2(f[e + 4] * inv, f[e + 5] * inv);
+                                v.w = pack_bf16x2(f[e + 6] * inv, f[e + 7] * inv);
+                                *reinterpret_cast<uint4*>(orow + c + e) = v;
+                            }
+                        }
+                    }
                 }
-                store_ml();
+                if (join) named_bar_sync(2, 256);
+            }
+            if (join && i == 0) {
+                fence_proxy_async_smem();  // the next Q tile may land where xo was
+                __syncwarp();
+                if (lane == 0) mbar_arrive_relaxed(xdone);
             }
             if (have) {
                 tc_fence_before();
@@ -952,51 +980,51 @@ template <int D>
 __global__ void __launch_bounds__(JOIN_THREADS)
 chunk_tc_join_kernel(const __grid_constant__ Params p, int ctas) {
     __shared__ ChunkLocateTmp<JOIN_THREADS> tmp;
-    pdl_launch_dependents();
-    pdl_wait();
-    if (!chunk_starts_ok(p.c)) return;
-    const int64_t border = blockIdx.x + 1;
-    int64_t total = 0, runs = 0, x = 0;
-    const ChunkPlace at = chunk_locate<JOIN_THREADS>(&tmp, p.c.B, [&](int64_t t) {
-        total = t;
-        runs = run_count(t, ctas);
-        x = border < runs ? border * t / runs : t;
+    // the inputs were complete when the attention kernel let this one start
+    const int border = blockIdx.x + 1;
+    Runs runs;
+    int64_t x = 0;
+    const ChunkPlace at = chunk_locate<JOIN_THREADS>(&tmp, p.c, [&](int64_t t) {
+        runs = runs_of(t, ctas);
+        x = run_start(runs, border);
         return x;
-    }, [&](int b) { return seq_units(p, b); });
-    if (at.b >= p.c.B) return;
-    const Seq s = seq_of(p, at.b);
-    int g, k, i0, i1, kbase, hi, tiles;
-    int64_t start;
-    item_at(p, s, x - at.base, g, k, start);
-    start += at.base;
-    const int64_t cost = seq_cost(s, k + 1) - seq_cost(s, k);
-    item_keys(p, s, k, i0, i1, kbase, hi, tiles);
-    const int cut = cut_tile(x - start, cost, tiles);
-    if (cut == 0 || cut == tiles) return;
-    const int64_t before = (border - 1) * total / runs;
-    if (before > start && cut_tile(before - start, cost, tiles) > 0) return;
-    // pieces: run border - 1 has the first, then every run up to the item's end
-    auto cut_of = [&](int64_t r) -> int {
-        const int64_t e = r < runs ? r * total / runs : total;
-        return cut_tile(min(e - start, cost), cost, tiles);
-    };
-    int64_t r_end = border;
-    while (cut_of(r_end + 1) < tiles) ++r_end;
+    }, [&](int P, int n) { return seq_units(p, P, n); });
+    int g = 0, k, i0 = 0, i1 = 0, kbase, hi, tiles;
+    int64_t start = 0, cost = 0;
+    bool work = at.b < p.c.B;
+    int r_end = border;
+    auto cut_of = [&](int r) -> int { return cut_tile(min(run_start(runs, r) - start, cost), cost, tiles); };
+    if (work) {
+        const Seq s = seq_of(p, p.c.prefix[at.b], p.c.q_start[at.b + 1] - p.c.q_start[at.b]);
+        item_at(p, s, x - at.base, g, k, start);
+        start += at.base;
+        cost = item_cost(s, k);
+        item_keys(p, s, k, i0, i1, kbase, hi, tiles);
+        const int cut = cut_of(border);
+        const int64_t before = run_start(runs, border - 1);
+        work = cut > 0 && cut < tiles && !(before > start && cut_of(border - 1) > 0);
+        // pieces: run border - 1 has the first, then every run up to the item's end
+        if (work)
+            while (cut_of(r_end + 1) < tiles) ++r_end;
+    }
+    pdl_wait();  // on every path: the next kernel in the stream waits for this one only
+    pdl_launch_dependents();
+    if (!work) return;
     const int ntok = i1 - i0, row = threadIdx.x;
     const int t = row / MT, tok_l = (row % MT) / p.G, head = (row % MT) % p.G, tok = tok_l + t * p.npt;
     if (tok_l >= p.npt || tok >= ntok || row >= p.prows) return;
     const int64_t step = (int64_t)p.prows * (D + 2);
-    auto slot_of = [&](int64_t r) -> const float* { return p.part + (2 * r + (r == border - 1 ? 1 : 0)) * step; };
-    auto has = [&](int64_t r) -> bool { return r == border - 1 || cut_of(r) < cut_of(r + 1); };
+    auto slot_of = [&](int r) -> const float* { return p.part + (2 * r + (r == border - 1 ? 1 : 0)) * step; };
+    auto has = [&](int r) -> bool { return r == border - 1 || cut_of(r) < cut_of(r + 1); };
     float mx = -INFINITY;
-    for (int64_t r = border - 1; r <= r_end; ++r)
+    for (int r = border - 1; r <= r_end; ++r)
         if (has(r)) mx = fmaxf(mx, slot_of(r)[p.prows * D + row]);
     const float bz = mx == -INFINITY ? 0.f : mx;
     float den = 0.f, acc[32];
 #pragma unroll
     for (int e = 0; e < 32; ++e) acc[e] = 0.f;
     const int c0 = blockIdx.y * 32;
-    for (int64_t r = border - 1; r <= r_end; ++r) {
+    for (int r = border - 1; r <= r_end; ++r) {
         if (!has(r)) continue;
         const float* sl = slot_of(r);
         const float w = exp2f(sl[p.prows * D + row] - bz);

@@ -55,14 +55,16 @@ __device__ __forceinline__ bool chunk_blocks_ok(const ChunkView& c, int b, int64
     return ok;
 }
 
-// Finds the sequence that holds unit x = where(total) when sequence b has cost(b)
-// units and the sequences are laid end to end.  Called by every thread of the CTA
-// (THREADS of them); each thread sums a contiguous run of sequences, then the
-// block scans.  tmp: shared memory of its own for the call.
+// Finds the sequence that holds unit x = where(total) when a sequence with prefix
+// P and n rows has cost(P, n) units and the sequences are laid end to end; and
+// checks q_start.  Called by every thread of the CTA (THREADS of them); each
+// thread sums a contiguous run of sequences, then the block scans.  tmp: shared
+// memory of its own for the call.
 struct ChunkPlace {
     int64_t total;  // units of all sequences
     int64_t base;   // first unit of sequence b
-    int b;          // B when x >= total
+    int b;          // B when x >= total, or when q_start is not valid
+    bool valid;     // q_start is non-decreasing within [0, T]
 };
 
 template <int THREADS>
@@ -73,47 +75,53 @@ struct ChunkLocateTmp {
 };
 
 template <int THREADS, class Where, class Cost>
-__device__ __forceinline__ ChunkPlace chunk_locate(ChunkLocateTmp<THREADS>* tmp, int B, Where where,
-                                                   Cost cost) {
+__device__ __forceinline__ ChunkPlace chunk_locate(ChunkLocateTmp<THREADS>* tmp, const ChunkView& c,
+                                                   Where where, Cost cost) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (B + THREADS - 1) / THREADS;
-    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    const int per = (c.B + THREADS - 1) / THREADS;
+    const int b0 = min(c.B, tid * per), b1 = min(c.B, b0 + per);
     int64_t s = 0;
-    for (int b = b0; b < b1; ++b) s += cost(b);
+    bool ok = true;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+        const int lo = c.q_start[b], hi = c.q_start[b + 1], P = c.prefix[b];
+        ok = ok && lo >= 0 && lo <= hi && hi <= c.T;
+        s += cost(P, hi - lo);
+    }
     int64_t incl = s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
     }
-    __syncthreads();  // the previous use of the shared words is over
     if (lane == 31) tmp->warp_sum[warp] = incl;
-    if (tid == 0) tmp->found_b = B;
-    __syncthreads();
-    int64_t before = 0, total = 0;
+    if (tid == 0) tmp->found_b = c.B;
+    ChunkPlace r;
+    r.valid = __syncthreads_and(ok ? 1 : 0) != 0;
+    int64_t before = 0;
+    r.total = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
         if (w < warp) before += tmp->warp_sum[w];
-        total += tmp->warp_sum[w];
+        r.total += tmp->warp_sum[w];
     }
-    const int64_t x = where(total);
+    const int64_t x = where(r.total);
     int64_t at = before + incl - s;
-    if (x >= at && x < at + s) {
+    if (r.valid && x >= at && x < at + s) {
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
-            const int64_t c = cost(b);
-            if (x < at + c) {
+            const int64_t u = cost(c.prefix[b], c.q_start[b + 1] - c.q_start[b]);
+            if (x < at + u) {
                 tmp->found_b = b;
                 tmp->found_base = at;
                 break;
             }
-            at += c;
+            at += u;
         }
     }
     __syncthreads();
-    ChunkPlace r;
-    r.total = total;
     r.b = tmp->found_b;
-    r.base = r.b < B ? tmp->found_base : total;
+    r.base = r.b < c.B ? tmp->found_base : r.total;
     return r;
 }
 
