@@ -63,12 +63,17 @@ constexpr int MMA_WARP = 8, LOAD_WARP = 9, FIX_WARP = 10, SCHED_WARP = 11;
 constexpr int GQ = 4;              // items published ahead
 constexpr int FIX_TILES = 6;       // key tiles of an item that only some of its rows see
 constexpr int FIX_BUFS = 4;        // items whose V notes may be live (see warp 10)
+// Rows up to which the epilogue of a single row tile goes through shared memory row by
+// row (both streams' rows of D + 4 floats fit the second Q tile): one warp would write
+// them out alone otherwise.
+constexpr int FEW = 30;
+static_assert(2 * FEW * (128 + 4) * 4 <= MT * 128 * 2 && 2 * FEW * (64 + 4) * 4 <= MT * 64 * 2, "xo");
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_LOG2 = 8.0f;
 // fixed cost of an item, in keys: Q load, pipeline fill and drain, epilogue
-constexpr int64_t C0 = 256;
-// least cost of a run, in keys: shorter ones cost more to join than they save
-constexpr int64_t RUN_MIN = 512;
+constexpr int64_t C0 = 512;
+// cost of a run, in keys, below which cutting further costs more to join than it saves
+constexpr int64_t RUN_MIN = 768;
 
 struct Item {
     int b, g, P, i0;        // sequence, kv head, prefix, first token
@@ -88,11 +93,11 @@ struct Lay {
     static constexpr int Q_BYTES = MT * D * 2;             // one row tile
     static constexpr int OFF_RING = 0;
     static constexpr int OFF_Q = SLOTS * SLOT_BYTES;       // two row tiles
-    static constexpr int OFF_X = OFF_Q + Q_BYTES;          // join of the streams: the second Q tile
+    static constexpr int OFF_X = OFF_Q + Q_BYTES;          // epilogue of one row tile: the second Q tile
     static constexpr int OFF_ITEMS = OFF_Q + 2 * Q_BYTES;  // [GQ]
     static constexpr int OFF_BAD = OFF_ITEMS + GQ * 64;    // [FIX_BUFS][FIX_TILES][4]
     static constexpr int OFF_BARS = OFF_BAD + FIX_BUFS * FIX_TILES * 16;
-    static constexpr int NBARS = 3 * SLOTS + 8 + 4 + 2 * GQ;
+    static constexpr int NBARS = 3 * SLOTS + 8 + 4 + 2 * GQ + 2;
     static constexpr int OFF_ML = OFF_BARS + NBARS * 8;    // join: maximum, sum per row
     static constexpr int OFF_MISC = OFF_ML + 2 * MT * 4;
     static constexpr int BYTES = OFF_MISC + 16 + 1024;     // + alignment slack
@@ -140,7 +145,7 @@ __device__ __forceinline__ int64_t item_cost(const Seq& s, int k) {
     if (!s.shape) return C0;
     return C0 + min((int64_t)s.P + min((int64_t)s.n, (int64_t)(k + 1) * s.m), s.w);
 }
-__device__ __forceinline__ int64_t seq_cost(const Seq& s, int k) {
+__device__ __noinline__ int64_t seq_cost(Seq s, int k) {
     if (!s.shape || k == 0) return k * C0;
     const int64_t full = min(k, s.items - 1);                    // items of m tokens
     int64_t lin = full;                                          // of them below the window's limit
@@ -168,7 +173,7 @@ __device__ __forceinline__ void item_keys(const Params& p, const Seq& s, int k, 
 }
 // Tile at which a border y units into an item of the given cost cuts it (the same
 // float arithmetic everywhere, and non-decreasing in y).
-__device__ __forceinline__ int cut_tile(int64_t y, int64_t cost, int tiles) {
+__device__ __noinline__ int cut_tile(int64_t y, int64_t cost, int tiles) {
     if (y <= C0) return 0;
     if (y >= cost) return tiles;
     const float per = __fdiv_rn((float)tiles, (float)(cost - C0));
@@ -192,21 +197,126 @@ __device__ __forceinline__ void item_at(const Params& p, const Seq& s, int64_t y
     k = lo;
     start = g * per + seq_cost(s, lo);
 }
-// Runs of equal length over the units: as many as there are CTAs, fewer when they
-// would be short; the length is rounded up, so the last run may be shorter.
+// Runs of equal length over the units: as many as there are CTAs; fewer when they
+// would be short and every (sequence, kv head) has one.  The length is rounded up, so
+// the last run may be shorter.
 struct Runs {
     int64_t total, len;
     int count;
 };
-__device__ __forceinline__ Runs runs_of(int64_t total, int ctas) {
+__device__ __forceinline__ Runs runs_of(const Params& p, int64_t total, int ctas) {
     Runs r;
     r.total = total;
-    r.count = (int)max((int64_t)1, min((int64_t)ctas, total / RUN_MIN));
+    r.count = (int)min((int64_t)ctas, max(total / RUN_MIN, (int64_t)p.c.B * p.Hkv));
     r.len = __float2ll_ru(__fdiv_ru(__ll2float_ru(total), (float)r.count));
     return r;
 }
 __device__ __forceinline__ int64_t run_start(const Runs& r, int i) {
     return i < r.count ? min(i * r.len, r.total) : r.total;
+}
+
+// The bounded wait of tv_device.cuh with its slow path out of line (this kernel has
+// some forty waits, and its instructions have to stay in the cache beside each
+// other).  TRIES polls, each of which may suspend the warp, come before it: the
+// waits of the products and of the softmax are on the critical path, and reading
+// the clock costs more than a poll.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > TV_WAIT_NS) return false;
+    return true;
+}
+template <int TRIES = 1>
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) {
+    bool ok = mbar_try_wait(bar, parity);
+#pragma unroll 1
+    for (int k = 1; k < TRIES && !ok; ++k) ok = mbar_try_wait(bar, parity);
+    if (!ok) ok = wait_slow(bar, parity);
+    return __all_sync(0xffffffffu, ok);
+}
+
+// The same for warp 8, which has nothing to spare: it polls, and leaves the loop only
+// to look at the clock.
+__device__ __forceinline__ bool wait_mma(uint64_t* bar, uint32_t parity) {
+    bool ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+#pragma unroll 1
+    for (int k = 0; k < 256 && !ok; ++k) ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+    return ok || wait_all(bar, parity);
+}
+
+// S = Q K^T of one tile (M = N = 128), then a commit to `bar`: one elected lane of the
+// converged warp issues all of it (an elect per instruction costs more than the
+// instruction).  Descriptors advance 32 bytes per K = 16 step; the second half of the
+// head is 16 KB on in Q and 1 KB on in K.
+template <int D>
+__device__ __forceinline__ void mma_s(uint32_t d, uint64_t a, uint64_t b, uint64_t* bar) {
+    constexpr uint32_t IDESC = idesc_bf16(MT, KT, false);
+    if constexpr (D == 128) {
+        asm volatile(
+            "{\n\t.reg .pred e, f, t;\n\t.reg .b64 a, b;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+            "add.u64 a, %1, 2;\n\tadd.u64 b, %2, 2;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.u64 a, %1, 4;\n\tadd.u64 b, %2, 4;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.u64 a, %1, 6;\n\tadd.u64 b, %2, 6;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.u64 a, %1, 1024;\n\tadd.u64 b, %2, 64;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.u64 a, %1, 1026;\n\tadd.u64 b, %2, 66;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.u64 a, %1, 1028;\n\tadd.u64 b, %2, 68;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.u64 a, %1, 1030;\n\tadd.u64 b, %2, 70;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(IDESC), "r"(smem_u32(bar))
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred e, f, t;\n\t.reg .b64 a, b;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+            "add.u64 a, %1, 2;\n\tadd.u64 b, %2, 2;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.u64 a, %1, 4;\n\tadd.u64 b, %2, 4;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.u64 a, %1, 6;\n\tadd.u64 b, %2, 6;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(IDESC), "r"(smem_u32(bar))
+            : "memory");
+    }
+}
+// O (+)= P V of one tile: P in tensor memory (8 columns per K = 16 step), V a page per step.
+template <int D>
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate) {
+    constexpr uint32_t IDESC = idesc_bf16(MT, D, true);
+    asm volatile(
+        "{\n\t.reg .pred e, f, t;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
+        "add.u32 a, %1, 8;\n\tadd.u64 b, %2, %5;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+        "add.u32 a, a, 8;\n\tadd.u64 b, b, %5;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+        "add.u32 a, a, 8;\n\tadd.u64 b, b, %5;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+        "add.u32 a, a, 8;\n\tadd.u64 b, b, %5;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+        "add.u32 a, a, 8;\n\tadd.u64 b, b, %5;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+        "add.u32 a, a, 8;\n\tadd.u64 b, b, %5;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+        "add.u32 a, a, 8;\n\tadd.u64 b, b, %5;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(IDESC), "r"(accumulate), "n"(16 * D * 2 / 16)
+        : "memory");
 }
 
 // Tiles of an item that warp 10 goes through: t < fa (some rows' windows start
@@ -271,7 +381,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Params p) {
     using L = Lay<D>;
     constexpr uint32_t TMEM_O = 256;                       // S at 0 and 128, O at 256 and 256 + D
-    constexpr uint32_t IDESC_QK = idesc_bf16(MT, KT, false), IDESC_PV = idesc_bf16(MT, D, true);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -285,11 +394,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     uint64_t* ofree = ofull + 2;          // [2] O(i) read by the epilogue
     uint64_t* qfull = ofree + 2;
     uint64_t* qempty = qfull + 1;
-    uint64_t* xdone = qempty + 1;         // the join's use of the second Q tile is over
+    uint64_t* xdone = qempty + 1;         // an epilogue's use of the second Q tile is over
     uint64_t* drain = xdone + 1;
     uint64_t* gq_full = drain + 1;        // [GQ]
     uint64_t* gq_empty = gq_full + GQ;    // [GQ]
     uint64_t* vraw = gq_empty + GQ;       // [SLOTS] a V tile that warp 10 goes through has landed
+    uint64_t* xall = vraw + L::SLOTS;     // [2] every softmax warp has written xo, has read xo
     auto* tmp = reinterpret_cast<ChunkLocateTmp<THREADS>*>(smem + L::OFF_RING);  // before the first copy
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
@@ -311,8 +421,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         }
         mbar_init(qfull, 1);
         mbar_init(qempty, 1);
-        mbar_init(xdone, 4);
+        mbar_init(xdone, 1);
         mbar_init(drain, 1);
+        mbar_init(&xall[0], 8);
+        mbar_init(&xall[1], 8);
         for (int s = 0; s < GQ; ++s) {
             mbar_init(&gq_full[s], 1);
             mbar_init(&gq_empty[s], 11);  // 8 softmax warps, MMA, producer, warp 10
@@ -345,7 +457,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     Runs runs;
     int64_t x_lo = 0, x_hi = 0;
     const ChunkPlace at = chunk_locate<THREADS>(tmp, p.c, [&](int64_t total) {
-        runs = runs_of(total, gridDim.x);
+        runs = runs_of(p, total, gridDim.x);
         x_lo = run_start(runs, blockIdx.x);
         x_hi = run_start(runs, blockIdx.x + 1);
         return x_lo < x_hi ? x_lo : total;
@@ -366,9 +478,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     fence_proxy_async_smem();  // the ring's first bytes held the search's scratch
     __syncthreads();
 
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity));
-    };
     // Work item k, from the queue; false at the end (or after a timeout).
     auto take = [&](uint32_t k, Item& it) -> bool {
         const int s = k % GQ;
@@ -464,7 +573,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             tma_prefetch_desc(&kmap);
             tma_prefetch_desc(&vmap);
         }
-        uint32_t ld = 0;                   // slots filled so far
+        uint32_t ld = 0, slot = 0, ph = 0; // slots filled so far; the next one, its round's parity
         uint32_t raw = 0, raw_ph = 0;      // per slot: last filled through vraw, and vraw's next parity
         bool alive = true;
         Item it;
@@ -488,11 +597,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             fetch(0);
             int cur = rows(), prev = 0, wk = 0;
             if (it.n > WT) fetch(1);
-            auto load = [&](bool is_v, int j) -> bool {    // tile j of the piece
-                const int s = ld % L::SLOTS;
-                bool ok = *abort_flag == 0;
-                if (ok) ok = wait_all(&empty[s], ((ld / L::SLOTS) & 1u) ^ 1u);
-                if (!ok) return false;
+            // the order in which the products take them: V(x / 2 - lag), K(x / 2)
+            const int lag = two ? 1 : 2;
+#pragma unroll 1
+            for (int x = 0; x < 2 * (it.n + lag); ++x) {
+                const bool is_v = (x & 1) == 0;
+                const int j = (x >> 1) - (is_v ? lag : 0);        // tile of the piece
+                if (j < 0 || j >= it.n) continue;
+                // everything but the copies comes before the wait for the slot
                 const int w = j / WT;
                 if (!is_v && w > wk) {
                     prev = cur;
@@ -500,15 +612,17 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     wk = w;
                     if (it.n > (w + 1) * WT) fetch(w + 1);
                 }
-                const int k0 = it.kbase + (it.t_lo + j) * KT;
-                const int pages = min(KT / 16, (it.hi - k0 + 15) >> 4);
+                const int t = it.t_lo + j;
+                const int pages = min(KT / 16, (it.hi - it.kbase - t * KT + 15) >> 4);
                 const int y = __shfl_sync(0xffffffffu, w == wk ? cur : prev, (j % WT) * (KT / 16) + (lane & 7));
-                uint8_t* dst = smem + L::OFF_RING + s * L::SLOT_BYTES + (lane & 7) * L::PAGE_BYTES;
+                uint8_t* dst = smem + L::OFF_RING + slot * L::SLOT_BYTES + (lane & 7) * L::PAGE_BYTES;
                 // a V tile at the edges goes through warp 10, which passes it on
-                const bool edge = is_v && (it.t_lo + j < it.fa || it.t_lo + j >= it.fb);
-                raw = (raw & ~(1u << s)) | ((edge ? 1u : 0u) << s);
-                raw_ph ^= (edge ? 1u : 0u) << s;
-                uint64_t* bar = edge ? &vraw[s] : &full[s];
+                const uint32_t edge = is_v && (t < it.fa || t >= it.fb) ? 1u : 0u;
+                raw = (raw & ~(1u << slot)) | (edge << slot);
+                raw_ph ^= edge << slot;
+                uint64_t* bar = edge ? &vraw[slot] : &full[slot];
+                alive = wait_all<64>(&empty[slot], ph ^ 1u);
+                if (!alive) break;
                 mbar_arrive_expect_tx_relaxed_elect(bar, (uint32_t)pages * L::PAGE_BYTES);
                 if (lane < pages) {
                     if constexpr (D == 128) {
@@ -520,13 +634,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 }
                 __syncwarp();
                 ++ld;
-                return true;
-            };
-            // the order in which the products take them
-            const int lag = two ? 1 : 2;
-            for (int j = 0; alive && j < it.n + lag; ++j) {
-                if (j >= lag && j - lag < it.n) alive = load(true, j - lag);
-                if (alive && j < it.n) alive = load(false, j);
+                if (++slot == L::SLOTS) {
+                    slot = 0;
+                    ph ^= 1u;
+                }
             }
         }
         if (!alive && lane == 0) *abort_flag = 1;
@@ -538,110 +649,105 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         }
     } else if (warp == MMA_WARP) {
         // ============================== products ==============================
-        uint32_t ld = 0, qi = 0, pc[2] = {0, 0}, oc[2] = {0, 0};
+        uint32_t slot = 0, par = 0;                    // next ring position: slot, parity of its round
+        uint32_t qi = 0, ppar = 0, opar = 3;           // ppar, opar: parity bit per stream
         bool alive = true;
         Item it;
-        auto issue_s = [&](int i, int qt, uint32_t slot) {
-            const uint32_t qa = sbase + L::OFF_Q + qt * L::Q_BYTES;
-            const uint32_t ka = sbase + L::OFF_RING + slot * L::SLOT_BYTES;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t ad = smem_desc_sw128(qa + (kk >> 2) * (MT * 128) + (kk & 3) * 32, 16, 1024);
-                // d = 128: K is [page][row group][half][8 rows][128 bytes], 8-key groups 2 KB apart
-                const uint64_t bd = smem_desc_sw128(ka + (kk >> 2) * 1024 + (kk & 3) * 32, 16,
-                                                    D == 128 ? 2048 : 1024);
-                tc_mma_bf16_elect(tmem + i * KT, ad, bd, IDESC_QK, kk > 0 ? 1u : 0u);
-            }
-            tc_commit_elect(&sfull[i]);
-        };
-        auto issue_pv = [&](int i, uint32_t slot, bool first) {
-            const uint32_t va = sbase + L::OFF_RING + slot * L::SLOT_BYTES;
-#pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk) {
-                // V is [page][half][16 rows][128 bytes]
-                const uint64_t bd = smem_desc_sw128(va + kk * L::PAGE_BYTES, 2048, 1024);
-                tc_mma_bf16_ts_elect(tmem + TMEM_O + i * D, tmem + i * KT + kk * 8, bd, IDESC_PV,
-                                     (first && kk == 0) ? 0u : 1u);
+        const uint32_t ring = sbase + L::OFF_RING;
+        const uint64_t qd = smem_desc_sw128(sbase + L::OFF_Q, 16, 1024);
+        // d = 128: K is [page][row group][half][8 rows][128 bytes], 8-key groups 2 KB apart;
+        // V is [page][half][16 rows][128 bytes]
+        const uint64_t kd = smem_desc_sw128(ring, 16, D == 128 ? 2048 : 1024), vd = smem_desc_sw128(ring, 2048, 1024);
+        auto next = [&](uint32_t& s, uint32_t& ph) {
+            if (++s == L::SLOTS) {
+                s = 0;
+                ph ^= 1u;
             }
         };
-        auto wait_full = [&](uint32_t u) -> bool {
-            return wait_all(&full[u % L::SLOTS], (u / L::SLOTS) & 1u);
+        auto issue_s = [&](int i, int qt, uint32_t s) {
+            mma_s<D>(tmem + i * KT, qd + qt * (L::Q_BYTES / 16), kd + s * (L::SLOT_BYTES / 16), &sfull[i]);
+        };
+        auto issue_pv = [&](int i, uint32_t s, bool first) {
+            mma_pv<D>(tmem + TMEM_O + i * D, tmem + i * KT, vd + s * (L::SLOT_BYTES / 16), first ? 0u : 1u);
         };
         // P of stream i is there, and (first product of an item) O(i) has been read
         auto wait_p = [&](int i, bool first) -> bool {
-            if (!wait_all(&pfull[i], pc[i] & 1u)) return false;
-            ++pc[i];
+            bool ok = wait_mma(&pfull[i], (ppar >> i) & 1u);
             if (first) {
-                if (oc[i] > 0 && !wait_all(&ofree[i], (oc[i] - 1) & 1u)) return false;
-                ++oc[i];
+                ok = ok && wait_mma(&ofree[i], (opar >> i) & 1u);
+                opar ^= 1u << i;
             }
-            return true;
+            ppar ^= 1u << i;
+            tc_fence_after();
+            return ok;
         };
+#pragma unroll 1
         for (uint32_t k = 0; alive && take(k, it); ++k) {
             if (it.n == 0) continue;
             const int n = it.n;
-            if (!wait_all(qfull, qi & 1u)) {
-                alive = false;
-                break;
-            }
+            alive = wait_mma(qfull, qi & 1u);
             ++qi;
             if (it.flags & ITEM_TWO) {
-                for (int j = 0; alive && j <= n; ++j) {
-                    const uint32_t uv = ld + 2 * j - 1, uk = ld + 2 * j;   // V(j - 1), K(j)
-                    if (j > 0) alive = wait_full(uv);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (!alive) break;
-                        if (j > 0) {
-                            alive = wait_p(i, j == 1);
-                            if (!alive) break;
-                            tc_fence_after();
-                            issue_pv(i, uv % L::SLOTS, j == 1);
-                            if (i == 1) tc_commit_elect(&empty[uv % L::SLOTS]);
-                            if (j == n) tc_commit_elect(&ofull[i]);
-                        }
-                        if (j < n) {
-                            if (i == 0) {
-                                alive = wait_full(uk);
-                                if (!alive) break;
-                                tc_fence_after();
-                            }
-                            issue_s(i, i, uk % L::SLOTS);
-                            if (i == 1) {
-                                tc_commit_elect(&empty[uk % L::SLOTS]);
-                                if (j == n - 1) tc_commit_elect(qempty);
-                            }
-                        }
-                        __syncwarp();
+                // ring order K(0) V(0) K(1) V(1) ...; both streams read every tile
+                alive = alive && wait_mma(&full[slot], par);
+                if (!alive) break;
+                tc_fence_after();
+                issue_s(0, 0, slot);
+                issue_s(1, 1, slot);
+                tc_commit_elect(&empty[slot]);
+                if (n == 1) tc_commit_elect(qempty);
+#pragma unroll 1
+                for (int j = 1; j <= n; ++j) {
+                    next(slot, par);
+                    const uint32_t vs = slot;
+                    alive = wait_mma(&full[vs], par);              // V(j - 1)
+                    if (j < n) {
+                        next(slot, par);
+                        alive = alive && wait_mma(&full[slot], par);   // K(j)
+                    }
+                    alive = alive && wait_p(0, j == 1);
+                    if (!alive) break;
+                    issue_pv(0, vs, j == 1);
+                    if (j < n) issue_s(0, 0, slot);
+                    else tc_commit_elect(&ofull[0]);
+                    alive = wait_p(1, j == 1);
+                    if (!alive) break;
+                    issue_pv(1, vs, j == 1);
+                    if (j < n) {
+                        issue_s(1, 1, slot);
+                        tc_commit_elect(&empty[vs]);
+                        tc_commit_elect(&empty[slot]);
+                        if (j == n - 1) tc_commit_elect(qempty);
+                    } else {
+                        tc_commit_elect(&ofull[1]);
+                        tc_commit_elect(&empty[vs]);
                     }
                 }
+                next(slot, par);
             } else {
-                uint32_t u = ld;
-                for (int j = 0; alive && j < n + 2; ++j) {
+                // ring order K(0) K(1) V(0) K(2) V(1) ... V(n - 1); stream j % 2 reads tile j
+#pragma unroll 1
+                for (int j = 0; j < n + 2; ++j) {
                     const int i = j & 1;
                     if (j >= 2 && j - 2 < n) {
-                        alive = wait_full(u);
-                        if (alive) alive = wait_p(i, j < 4);
+                        alive = wait_mma(&full[slot], par) && wait_p(i, j < 4);
                         if (!alive) break;
-                        tc_fence_after();
-                        issue_pv(i, u % L::SLOTS, j < 4);
-                        tc_commit_elect(&empty[u % L::SLOTS]);
+                        issue_pv(i, slot, j < 4);
+                        tc_commit_elect(&empty[slot]);
                         if (j >= n) tc_commit_elect(&ofull[i]);
-                        ++u;
+                        next(slot, par);
                     }
                     if (j < n) {
-                        alive = wait_full(u);
+                        alive = wait_mma(&full[slot], par);
                         if (!alive) break;
                         tc_fence_after();
-                        issue_s(i, 0, u % L::SLOTS);
-                        tc_commit_elect(&empty[u % L::SLOTS]);
+                        issue_s(i, 0, slot);
+                        tc_commit_elect(&empty[slot]);
                         if (j == n - 1) tc_commit_elect(qempty);
-                        ++u;
+                        next(slot, par);
                     }
-                    __syncwarp();
                 }
             }
-            ld += 2 * n;
         }
         if (!alive && lane == 0) *abort_flag = 1;
         // products in flight end before the tensor memory is freed
@@ -659,7 +765,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             const int n = it.n;
             const bool two = (it.flags & ITEM_TWO) != 0;
             alive = wait_all(qempty, (qi & 1u) ^ 1u);
-            // the second Q tile also serves the joins of the items before
+            // the second Q tile also serves the epilogues of single row tiles before
             if (alive && two && xi > 0) alive = wait_all(xdone, (xi - 1) & 1u);
             if (!alive) break;
             ++qi;
@@ -669,8 +775,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 for (int hf = 0; hf < L::HALVES; ++hf)
                     tma_load_3d_elect(smem + L::OFF_Q + t * L::Q_BYTES + hf * (MT * 128), &qmap, qfull, hf * 64,
                                       it.g * p.G, it.row0 + t * p.npt, qpol);
-            if (!two && n > 1) {
-                // one join outstanding at most, or the barrier's phases could not be told apart
+            if (!two) {
+                // one use outstanding at most, or the barrier's phases could not be told apart
                 if (xi > 0) alive = wait_all(xdone, (xi - 1) & 1u);
                 if (!alive) break;
                 ++xi;
@@ -699,7 +805,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 const int lead = chunk_first_key(it.P + it.i0, p.window) - (it.kbase + t * KT);
                 // one token: no key is seen by some of its rows only
                 const int scan = it.ntok > 1 ? min(nv, KT) : 0;
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < KT / 32; ++q) {
                     const int r = q * 32 + lane;
                     uint8_t* row = vt + (r >> 4) * L::PAGE_BYTES + (r & 15) * 128;
@@ -744,9 +850,20 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         const int tok_l = row / p.G, head = row - tok_l * p.G;
         float* xo = reinterpret_cast<float*>(smem + L::OFF_X);  // [columns][rows]
         float* ml = reinterpret_cast<float*>(smem + L::OFF_ML);
-        uint32_t sc = 0, oc = 0, live = 0;
+        uint32_t sc = 0, oc = 0, live = 0, xc = 0;
         bool alive = true;
         Item it;
+        // every softmax warp has written xo (0), has read it (1): with a bounded wait, unlike
+        // bar.sync
+        auto all_x = [&](int which) {
+            __syncwarp();
+            if (lane == 0) {
+                if (which == 0) mbar_arrive(&xall[0]);
+                else mbar_arrive_relaxed(&xall[1]);   // reads only: nothing to release
+            }
+            alive = alive && wait_all(&xall[which], xc & 1u);
+            xc += which;
+        };
         for (uint32_t k = 0; alive && take(k, it); ++k) {
             const bool two = (it.flags & ITEM_TWO) != 0;
             if ((it.flags & ITEM_STATUS) && tid == 0)
@@ -757,15 +874,23 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             const int self = it.P + it.i0 + min(tok, it.ntok - 1);
             const int first = p.window > 0 ? max(0, self - p.window + 1) : 0;
             const int step = two ? 1 : 2, j0 = two ? 0 : i;
-            const int mine_n = it.n > j0 ? (it.n - j0 + step - 1) / step : 0;
+            const bool have = it.n > j0;                      // O(i) will hold this item
+            const int rows = p.G * min(it.ntok, p.npt);       // rows of the item in a row tile
+            const bool wrows = (warp & 3) * 32 < rows;        // some of them in this warp
             float m_used = -INFINITY, l = 0.f;
             for (int j = j0; j < it.n; j += step) {
-                if (!wait_all(&sfull[i], sc & 1u)) {
+                if (!wait_all<64>(&sfull[i], sc & 1u)) {
                     alive = false;
                     break;
                 }
                 ++sc;
                 tc_fence_after();
+                if (!wrows) {
+                    // nothing of the item in this warp: its rows of P may hold anything (a row of
+                    // the product reads its own row of P only)
+                    if (lane == 0) mbar_arrive_relaxed(&pfull[i]);
+                    continue;
+                }
                 float sv[KT];
                 {
                     uint32_t r[KT / 32][32];
@@ -848,76 +973,138 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 l += lo + hi;
             }
             if (!alive) break;
-            // ---- epilogue
-            const bool have = mine_n > 0;                     // O(i) holds this item
+            // ---- epilogue.  Two streams of one row tile are joined: weights 2^(m_i - max).
+            const bool join = !two && it.n > 1;
+            // partial result: [D / 4][rows] x 4 columns, then the maxima and the sums
+            float* pslot = it.slot >= 0 ? p.part + (int64_t)it.slot * p.prows * (D + 2) : nullptr;
+            const uint32_t* notes = bad + (live % FIX_BUFS) * FIX_TILES * 4;
+            if (it.n > 0) ++live;
             if (have) {
-                if (!wait_all(&ofull[i], oc & 1u)) {
+                if (!wait_all(&ofull[i], (oc++) & 1u)) {
                     alive = false;
                     break;
                 }
-                ++oc;
                 tc_fence_after();
+                // V rows that warp 10 took out although some rows attend to them
+                if (it.ntok > 1 && (it.fa > it.t_lo || it.fb < it.t_hi) &&
+                    __any_sync(0xffffffffu, lane < FIX_TILES * 4 && notes[lane] != 0u))
+                    add_noted<D, CAP>(p, it, notes, it.t_lo + j0, step, tO, first, mine ? self : -1,
+                                      p.q + (int64_t)(it.row0 + tok) * p.q_stride + (int64_t)(it.g * p.G + head) * D,
+                                      m_used);
             }
-            // V rows that warp 10 took out although some rows attend to them
-            const uint32_t* notes = bad + (live % FIX_BUFS) * FIX_TILES * 4;
-            if (it.n > 0) ++live;
-            if (have && it.ntok > 1 && (it.fa > it.t_lo || it.fb < it.t_hi) &&
-                __any_sync(0xffffffffu, lane < FIX_TILES * 4 && notes[lane] != 0u))
-                add_noted<D, CAP>(p, it, notes, it.t_lo + j0, step, tO, first, mine ? self : -1,
-                                  p.q + (int64_t)(it.row0 + tok) * p.q_stride + (int64_t)(it.g * p.G + head) * D,
-                                  m_used);
-            // Two streams of one row tile: stream 1 hands its result over through shared
-            // memory, XC columns at a time (all of them when the rows are few).
-            const bool join = !two && it.n > 1;
-            const int rows = p.G * min(it.ntok, p.npt);       // rows of the item in a row tile
-            const bool wrows = (warp & 3) * 32 < rows;        // some of them in this warp
-            const int pitch = rows <= MT / 2 ? MT / 2 : MT;
-            const int XC = join ? (rows <= MT / 2 ? D : D / 2) : D;
-            float w0 = 1.f, w1 = 0.f;
-            // partial result: [D / 4][rows] x 4 columns, then the maxima and the sums
-            float* pslot = it.slot >= 0 ? p.part + (int64_t)it.slot * p.prows * (D + 2) : nullptr;
-            const int prow = (two ? i * MT : 0) + row;
-            __nv_bfloat16* orow = p.out + (int64_t)(it.row0 + tok) * p.o_stride + (int64_t)(it.g * p.G + head) * D;
-            float inv = 0.f;
+            auto o_read = [&]() {                             // O may be overwritten by the next item
+                if (!have) return;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_relaxed(&ofree[i]);
+            };
+            if (!two && rows <= FEW) {
+                // few rows: both streams leave theirs in shared memory, then all 256 threads join
+                // and write 8 columns each
+                constexpr int PITCH = D + 4;
+                if (wrows && have) {
+                    float* xr = xo + (i * FEW + row) * PITCH;
 #pragma unroll 1
-            for (int h = 0; h < D; h += XC) {
-                if (join) {
-                    if (i == 1 && wrows) {
-                        if (h == 0) {
-                            ml[row] = m_used;
-                            ml[MT + row] = l;
-                        }
-#pragma unroll 1
-                        for (int c = 0; c < XC; c += 32) {
-                            uint32_t r[32];
-                            tmem_ld32(tO + h + c, r);
-                            tmem_wait_ld();
-                            if (row < pitch)
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t r[16];
+                        tmem_ld16(tO + c, r);
+                        tmem_wait_ld();
+                        if (row < rows)
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) xo[(c + e) * pitch + row] = __uint_as_float(r[e]);
-                        }
+                            for (int e = 0; e < 16; e += 4)
+                                *reinterpret_cast<uint4*>(xr + c + e) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
                     }
-                    named_bar_sync(1, 256);
                 }
-                if ((two || i == 0) && wrows) {
-                    if (h == 0) {
-                        if (join) {
-                            const float m1 = ml[row], l1 = ml[MT + row];
-                            const float mm = fmaxf(m_used, m1), bz = mm == -INFINITY ? 0.f : mm;
-                            w0 = exp2f(m_used - bz);
-                            w1 = exp2f(m1 - bz);
-                            l = w0 * l + w1 * l1;
-                            m_used = mm;
-                        }
-                        inv = pslot ? 1.f : (l == 0.f ? 0.f : 1.f / l);
-                        if (mine && pslot) {
-                            pslot[p.prows * D + prow] = m_used;
-                            pslot[p.prows * (D + 1) + prow] = l;
-                        }
-                    }
+                o_read();
+                if (wrows) {
+                    ml[i * 64 + row] = m_used;
+                    ml[i * 64 + 32 + row] = l;
+                }
+                all_x(0);
 #pragma unroll 1
-                    for (int c = h; c < h + XC; c += 32) {
-                        uint32_t r[32];
+                for (int e = tid; e < rows * (D / 8); e += 256) {
+                    const int r = e / (D / 8), c = e % (D / 8) * 8;
+                    float m = ml[r], sum = ml[32 + r], w0 = 1.f, w1 = 0.f;
+                    float f[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) f[x] = it.n > 0 ? xo[r * PITCH + c + x] : 0.f;
+                    if (join) {
+                        const float m1 = ml[64 + r], mm = fmaxf(m, m1), bz = mm == -INFINITY ? 0.f : mm;
+                        w0 = exp2f(m - bz);
+                        w1 = exp2f(m1 - bz);
+                        sum = w0 * sum + w1 * ml[96 + r];
+                        m = mm;
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) f[x] = fmaf(w1, xo[(FEW + r) * PITCH + c + x], w0 * f[x]);
+                    }
+                    if (pslot) {
+                        float4* dst = reinterpret_cast<float4*>(pslot) + c / 4 * p.prows + r;
+                        dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+                        dst[p.prows] = make_float4(f[4], f[5], f[6], f[7]);
+                        if (c == 0) {
+                            pslot[p.prows * D + r] = m;
+                            pslot[p.prows * (D + 1) + r] = sum;
+                        }
+                    } else {
+                        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                        const int t = r / p.G;
+                        uint4 v;
+                        v.x = pack_bf16x2(f[0] * inv, f[1] * inv);
+                        v.y = pack_bf16x2(f[2] * inv, f[3] * inv);
+                        v.z = pack_bf16x2(f[4] * inv, f[5] * inv);
+                        v.w = pack_bf16x2(f[6] * inv, f[7] * inv);
+                        *reinterpret_cast<uint4*>(p.out + (int64_t)(it.row0 + t) * p.o_stride +
+                                                  (int64_t)(it.g * p.G + r - t * p.G) * D + c) = v;
+                    }
+                }
+                fence_proxy_async_smem();  // the next Q tile may land where xo was
+                all_x(1);
+            } else {
+                // a thread per row; stream 1 of a single row tile hands its rows over, 32 columns at
+                // a time (xo: [column][row])
+                const int prow = (two ? i * MT : 0) + row;
+                const bool writes = (two || i == 0) && wrows;
+                // Four lanes exchange their rows' 16-byte pieces, so that they write 64 bytes of one
+                // row together: a store of 16 bytes of 32 rows takes 32 cycles, of 64 bytes of 8 rows 8.
+                const uint64_t orow = reinterpret_cast<uint64_t>(p.out + (int64_t)(it.row0 + tok) * p.o_stride +
+                                                                 (int64_t)(it.g * p.G + head) * D + (lane & 3) * 8);
+                uint64_t prow4[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) prow4[x] = __shfl_sync(0xffffffffu, orow, (lane & ~3) + x) + 16 * ((lane & 3) - x);
+                const uint32_t valid = __ballot_sync(0xffffffffu, mine) >> (lane & ~3);
+                float w0 = 1.f, w1 = 0.f, inv = 0.f;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t r[32];
+                    if (join) {
+                        if (i == 1 && wrows) {
+                            if (c == 0) {
+                                ml[row] = m_used;
+                                ml[MT + row] = l;
+                            }
+                            tmem_ld32(tO + c, r);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) xo[e * MT + row] = __uint_as_float(r[e]);
+                        }
+                        all_x(0);
+                    }
+                    if (writes) {
+                        if (c == 0) {
+                            if (join) {
+                                const float m1 = ml[row], l1 = ml[MT + row];
+                                const float mm = fmaxf(m_used, m1), bz = mm == -INFINITY ? 0.f : mm;
+                                w0 = exp2f(m_used - bz);
+                                w1 = exp2f(m1 - bz);
+                                l = w0 * l + w1 * l1;
+                                m_used = mm;
+                            }
+                            inv = l == 0.f ? 0.f : 1.f / l;
+                            if (mine && pslot) {
+                                pslot[p.prows * D + prow] = m_used;
+                                pslot[p.prows * (D + 1) + prow] = l;
+                            }
+                        }
                         if (have) {
                             tmem_ld32(tO + c, r);
                             tmem_wait_ld();
@@ -925,43 +1112,50 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
 #pragma unroll
                             for (int e = 0; e < 32; ++e) r[e] = 0u;
                         }
-                        if (!mine) continue;
-                        float f[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(r[e]);
                         if (join)
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) f[e] = fmaf(w1, xo[(c - h + e) * pitch + row], w0 * f[e]);
+                            for (int e = 0; e < 32; ++e)
+                                r[e] = __float_as_uint(fmaf(w1, xo[e * MT + row], w0 * __uint_as_float(r[e])));
                         if (pslot) {
+                            if (mine)
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                reinterpret_cast<float4*>(pslot)[(c + e) / 4 * p.prows + prow] =
-                                    make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+                                for (int e = 0; e < 32; e += 4)
+                                    reinterpret_cast<uint4*>(pslot)[(c + e) / 4 * p.prows + prow] =
+                                        make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
                         } else {
+                            uint32_t u[16];
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8) {
-                                uint4 v;
-                                v.x = pack_bf16x2(f[e] * inv, f[e + 1] * inv);
-                                v.y = pack_bf16x2(f[e + 2] * inv, f[e + 3] * inv);
-                                v.z = pack_bf16x2(f[e + 4] * inv, f[e + 5] * inv);
-                                v.w = pack_bf16x2(f[e + 6] * inv, f[e + 7] * inv);
-                                *reinterpret_cast<uint4*>(orow + c + e) = v;
+                            for (int e = 0; e < 16; ++e)
+                                u[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * inv, __uint_as_float(r[2 * e + 1]) * inv);
+                            // 4 x 4 transpose of 16-byte pieces over four lanes
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if ((e & 4) == 0) {
+                                    const uint32_t y = __shfl_xor_sync(0xffffffffu, (lane & 1) ? u[e] : u[e + 4], 1);
+                                    if (lane & 1) u[e] = y;
+                                    else u[e + 4] = y;
+                                }
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const uint32_t y = __shfl_xor_sync(0xffffffffu, (lane & 2) ? u[e] : u[e + 8], 2);
+                                if (lane & 2) u[e] = y;
+                                else u[e + 8] = y;
                             }
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                if ((valid >> x) & 1u)
+                                    *reinterpret_cast<uint4*>(prow4[x] + 2 * c) =
+                                        make_uint4(u[4 * x], u[4 * x + 1], u[4 * x + 2], u[4 * x + 3]);
                         }
                     }
+                    if (join) {
+                        fence_proxy_async_smem();
+                        all_x(1);
+                    }
                 }
-                if (join) named_bar_sync(2, 256);
+                o_read();
             }
-            if (join && i == 0) {
-                fence_proxy_async_smem();  // the next Q tile may land where xo was
-                __syncwarp();
-                if (lane == 0) mbar_arrive_relaxed(xdone);
-            }
-            if (have) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_relaxed(&ofree[i]);  // O may be overwritten by the next item
-            }
+            if (!two && it.n > 0 && tid == 0) mbar_arrive(xdone);
         }
         if (!alive && lane == 0) *abort_flag = 1;
     }
@@ -985,7 +1179,7 @@ chunk_tc_join_kernel(const __grid_constant__ Params p, int ctas) {
     Runs runs;
     int64_t x = 0;
     const ChunkPlace at = chunk_locate<JOIN_THREADS>(&tmp, p.c, [&](int64_t t) {
-        runs = runs_of(t, ctas);
+        runs = runs_of(p, t, ctas);
         x = run_start(runs, border);
         return x;
     }, [&](int P, int n) { return seq_units(p, P, n); });
@@ -1116,7 +1310,7 @@ tv_status launch_chunk_attn_tc(const ChunkAttnArgs& a) {
     // one CTA per SM; fewer when even the longest sequences that fit give fewer runs
     const int64_t items = (int64_t)a.Hkv * (a.T / (2 * npt) + std::min(a.T, a.B));
     const int64_t units = items * std::min<int64_t>((int64_t)a.max_blocks * a.bs + C0, 1ll << 31);
-    const int ctas = (int)std::clamp<int64_t>(units / RUN_MIN, 1, device_sm_count());
+    const int ctas = (int)std::clamp<int64_t>(std::max(units / RUN_MIN, (int64_t)a.B * a.Hkv), 1, device_sm_count());
     if (a.d == 128)
         return a.softcap > 0.f ? launch<128, true>(a, p, qm, km, vm, ctas) : launch<128, false>(a, p, qm, km, vm, ctas);
     return a.softcap > 0.f ? launch<64, true>(a, p, qm, km, vm, ctas) : launch<64, false>(a, p, qm, km, vm, ctas);
