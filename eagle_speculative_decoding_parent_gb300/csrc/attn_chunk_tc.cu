@@ -68,6 +68,9 @@ constexpr int FIX_BUFS = 4;        // items whose V notes may be live (see warp 
 // them out alone otherwise.
 constexpr int FEW = 30;
 static_assert(2 * FEW * (128 + 4) * 4 <= MT * 128 * 2 && 2 * FEW * (64 + 4) * 4 <= MT * 64 * 2, "xo");
+// a border this close to an item's end (in tiles) moves there: a cut costs more than the
+// imbalance
+constexpr int SNAP = 2;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float RESCALE_LOG2 = 8.0f;
 // fixed cost of an item, in keys: Q load, pipeline fill and drain, epilogue
@@ -81,6 +84,8 @@ struct Item {
     int t_lo, t_hi, fa, fb; // key tiles of this piece; tiles < fa or >= fb need masks
     int flags, slot, n, pad;  // slot: partial result, or -1; n: tiles to do (0: bad sequence)
 };
+// A slot's record: it holds a piece, and the piece is the item's last one.
+constexpr int PIECE = 1, PIECE_LAST = 2;
 constexpr int ITEM_END = 1, ITEM_TWO = 2, ITEM_BAD = 4, ITEM_STATUS = 8;
 static_assert(sizeof(Item) == 64, "four 16-byte words");
 
@@ -113,6 +118,7 @@ struct Params {
     const __nv_bfloat16* k;
     const __nv_bfloat16* v;
     int32_t* status;
+    int4* rec;                   // what the slots hold: (first row, tokens, kv head, PIECE_*)
     float* part;                 // partial results, two slots per CTA
     int Hq, Hkv, G, npt, window;
     int prows;                   // rows of a partial result: 128 or 256
@@ -171,13 +177,14 @@ __device__ __forceinline__ void item_keys(const Params& p, const Seq& s, int k, 
     kbase = chunk_first_key(s.P + i0, p.window) & ~15;
     tiles = (hi - kbase + KT - 1) / KT;
 }
-// Tile at which a border y units into an item of the given cost cuts it (the same
-// float arithmetic everywhere, and non-decreasing in y).
+// Tile at which a border y units into an item of the given cost cuts it (both runs
+// beside the border compute it; non-decreasing in y).
 __device__ __noinline__ int cut_tile(int64_t y, int64_t cost, int tiles) {
     if (y <= C0) return 0;
     if (y >= cost) return tiles;
     const float per = __fdiv_rn((float)tiles, (float)(cost - C0));
-    return min(tiles, (int)ceilf(__fmul_rn((float)(y - C0), per)));
+    const int t = (int)ceilf(__fmul_rn((float)(y - C0), per));
+    return t <= SNAP ? 0 : (t >= tiles - SNAP ? tiles : t);
 }
 // Item at unit y of a sequence (Hkv equal stretches): kv head, item, its first unit.
 __device__ __forceinline__ void item_at(const Params& p, const Seq& s, int64_t y, int& g, int& k,
@@ -450,7 +457,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
     pdl_wait();  // everything above touched only shared memory and tensor memory
-    // after the wait: the join kernel may read the inputs before its own wait
     pdl_launch_dependents();
 
     // ---- this CTA's run
@@ -495,6 +501,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     if (warp == SCHED_WARP) {
         // ============================== scheduler ==============================
         uint32_t k = 0;
+        // the slots' records: empty until a piece is published
+        int4 rec0 = make_int4(0, 0, 0, 0), rec1 = rec0;
         auto publish = [&](const Item& it) -> bool {
             const int s = k % GQ;
             if (!wait_all(&gq_empty[s], ((k / GQ) & 1u) ^ 1u)) return false;
@@ -539,6 +547,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                                (g == 0 && it.i0 == 0 && it.t_lo == 0 ? ITEM_STATUS : 0);
                     it.pad = 0;
                     item_edges(p, it);
+                    if (!whole) {
+                        const int4 rec = make_int4(it.row0, it.ntok, g, PIECE | (it.t_hi == tiles ? PIECE_LAST : 0));
+                        if (it.t_lo == 0) rec1 = rec;
+                        else rec0 = rec;
+                    }
                     alive = publish(it);
                 }
                 start += cost;
@@ -559,6 +572,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                                                 (int64_t)s.P + s.n, lane, 32);
                 ok = __all_sync(0xffffffffu, ok);
             }
+        }
+        if (lane == 0) {
+            p.rec[2 * blockIdx.x] = rec0;
+            p.rec[2 * blockIdx.x + 1] = rec1;
         }
         if (alive) {
             Item it{};
@@ -1165,75 +1182,56 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     if (warp == MMA_WARP) tmem_dealloc(tmem, 512);
 }
 
-// Joins the pieces of the items that a run border cuts: one CTA per (border, 32
-// columns), which works when its border is the first to cut its item.  Weights
-// 2^(m_k - max) on the unnormalised rows, in run order.
+// Joins the pieces of the items that run borders cut: the CTA of slot 2 r + 1 (an item
+// that starts in run r and goes on) and 32 columns.  The pieces that follow are in the
+// slots 2 (r + 1), 2 (r + 2), ... up to the last one; weights 2^(m_k - max) on the
+// unnormalised rows, in run order.
 constexpr int JOIN_THREADS = 256;
 
 template <int D>
 __global__ void __launch_bounds__(JOIN_THREADS)
 chunk_tc_join_kernel(const __grid_constant__ Params p, int ctas) {
-    __shared__ ChunkLocateTmp<JOIN_THREADS> tmp;
-    // the inputs were complete when the attention kernel let this one start
-    const int border = blockIdx.x + 1;
-    Runs runs;
-    int64_t x = 0;
-    const ChunkPlace at = chunk_locate<JOIN_THREADS>(&tmp, p.c, [&](int64_t t) {
-        runs = runs_of(p, t, ctas);
-        x = run_start(runs, border);
-        return x;
-    }, [&](int P, int n) { return seq_units(p, P, n); });
-    int g = 0, k, i0 = 0, i1 = 0, kbase, hi, tiles;
-    int64_t start = 0, cost = 0;
-    bool work = at.b < p.c.B;
-    int r_end = border;
-    auto cut_of = [&](int r) -> int { return cut_tile(min(run_start(runs, r) - start, cost), cost, tiles); };
-    if (work) {
-        const Seq s = seq_of(p, p.c.prefix[at.b], p.c.q_start[at.b + 1] - p.c.q_start[at.b]);
-        item_at(p, s, x - at.base, g, k, start);
-        start += at.base;
-        cost = item_cost(s, k);
-        item_keys(p, s, k, i0, i1, kbase, hi, tiles);
-        const int cut = cut_of(border);
-        const int64_t before = run_start(runs, border - 1);
-        work = cut > 0 && cut < tiles && !(before > start && cut_of(border - 1) > 0);
-        // pieces: run border - 1 has the first, then every run up to the item's end
-        if (work)
-            while (cut_of(r_end + 1) < tiles) ++r_end;
-    }
-    pdl_wait();  // on every path: the next kernel in the stream waits for this one only
+    const int row = threadIdx.x, t = row / MT, tok_l = (row % MT) / p.G, head = (row % MT) % p.G;
+    const int tok = tok_l + t * p.npt, c0 = blockIdx.y * 32;
+    pdl_wait();
     pdl_launch_dependents();
-    if (!work) return;
-    const int ntok = i1 - i0, row = threadIdx.x;
-    const int t = row / MT, tok_l = (row % MT) / p.G, head = (row % MT) % p.G, tok = tok_l + t * p.npt;
-    if (tok_l >= p.npt || tok >= ntok || row >= p.prows) return;
-    const int64_t step = (int64_t)p.prows * (D + 2);
-    auto slot_of = [&](int r) -> const float* { return p.part + (2 * r + (r == border - 1 ? 1 : 0)) * step; };
-    auto has = [&](int r) -> bool { return r == border - 1 || cut_of(r) < cut_of(r + 1); };
-    float mx = -INFINITY;
-    for (int r = border - 1; r <= r_end; ++r)
-        if (has(r)) mx = fmaxf(mx, slot_of(r)[p.prows * D + row]);
-    const float bz = mx == -INFINITY ? 0.f : mx;
-    float den = 0.f, acc[32];
+    int slot = 2 * blockIdx.x + 1;
+    int4 rec = __ldcg(&p.rec[slot]);
+    if (!(rec.w & PIECE) || tok_l >= p.npt || tok >= rec.y || row >= p.prows) return;
+    const int row0 = rec.x, g = rec.z;
+    float mx = -INFINITY, den = 0.f, acc[32];
 #pragma unroll
     for (int e = 0; e < 32; ++e) acc[e] = 0.f;
-    const int c0 = blockIdx.y * 32;
-    for (int r = border - 1; r <= r_end; ++r) {
-        if (!has(r)) continue;
-        const float* sl = slot_of(r);
-        const float w = exp2f(sl[p.prows * D + row] - bz);
-        den = fmaf(w, sl[p.prows * (D + 1) + row], den);
+#pragma unroll 1
+    while (true) {
+        const float* sl = p.part + (int64_t)slot * p.prows * (D + 2);
+        // the next slot's record, early
+        const int ahead = slot + (slot & 1 ? 1 : 2);
+        const bool more = !(rec.w & PIECE_LAST) && ahead < 2 * ctas;
+        const int4 nrec = more ? __ldcg(&p.rec[ahead]) : rec;
+        if (rec.w & PIECE) {
+            const float mk = __ldcg(sl + p.prows * D + row), lk = __ldcg(sl + p.prows * (D + 1) + row);
+            float4 v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float4 v = reinterpret_cast<const float4*>(sl)[(c0 / 4 + e) * p.prows + row];
-            acc[4 * e] = fmaf(w, v.x, acc[4 * e]);
-            acc[4 * e + 1] = fmaf(w, v.y, acc[4 * e + 1]);
-            acc[4 * e + 2] = fmaf(w, v.z, acc[4 * e + 2]);
-            acc[4 * e + 3] = fmaf(w, v.w, acc[4 * e + 3]);
+            for (int e = 0; e < 8; ++e) v[e] = __ldcg(reinterpret_cast<const float4*>(sl) + (c0 / 4 + e) * p.prows + row);
+            const float mm = fmaxf(mx, mk), bz = mm == -INFINITY ? 0.f : mm;
+            const float f = exp2f(mx - bz), w = exp2f(mk - bz);
+            mx = mm;
+            den = fmaf(w, lk, den * f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                acc[4 * e] = fmaf(w, v[e].x, acc[4 * e] * f);
+                acc[4 * e + 1] = fmaf(w, v[e].y, acc[4 * e + 1] * f);
+                acc[4 * e + 2] = fmaf(w, v[e].z, acc[4 * e + 2] * f);
+                acc[4 * e + 3] = fmaf(w, v[e].w, acc[4 * e + 3] * f);
+            }
         }
+        if (!more) break;
+        slot = ahead;
+        rec = nrec;
     }
     const float inv = den == 0.f ? 0.f : 1.f / den;
-    __nv_bfloat16* dst = p.out + (int64_t)(p.c.q_start[at.b] + i0 + tok) * p.o_stride + (int64_t)(g * p.G + head) * D + c0;
+    __nv_bfloat16* dst = p.out + (int64_t)(row0 + tok) * p.o_stride + (int64_t)(g * p.G + head) * D + c0;
 #pragma unroll
     for (int e = 0; e < 32; e += 8) {
         uint4 v;
@@ -1277,7 +1275,7 @@ bool chunk_attn_tc_applicable(int Hq, int Hkv, int d, tv_dtype dt) {
 
 size_t chunk_attn_tc_workspace(int T, int B, int Hq, int Hkv, int d) {
     (void)B;
-    return (size_t)2 * device_sm_count() * partial_rows(T, Hq / Hkv) * (d + 2) * sizeof(float);
+    return (size_t)2 * device_sm_count() * (partial_rows(T, Hq / Hkv) * (d + 2) * sizeof(float) + sizeof(int4));
 }
 
 tv_status launch_chunk_attn_tc(const ChunkAttnArgs& a) {
@@ -1298,7 +1296,8 @@ tv_status launch_chunk_attn_tc(const ChunkAttnArgs& a) {
     p.k = static_cast<const __nv_bfloat16*>(a.k_cache);
     p.v = static_cast<const __nv_bfloat16*>(a.v_cache);
     p.status = a.status;
-    p.part = static_cast<float*>(a.ws);
+    p.rec = static_cast<int4*>(a.ws);
+    p.part = reinterpret_cast<float*>(p.rec + 2 * device_sm_count());
     p.Hq = a.Hq;
     p.Hkv = a.Hkv;
     p.G = G;
