@@ -6,27 +6,38 @@
 // n + presence * [n > 0]; a token that the grammar forbids becomes -infinity.
 // Then z / temperature, or its softmax.
 //
-// Bound by memory: the row is read once and written once; counts and bias are
-// shared by a tree's N rows and come from L2 after the first.  For the softmax
-// a cluster of CTAs holds the row's processed logits in shared memory (a row of
-// 128,256 tokens is 501 KB), so that the maximum and the sum need no second
-// read of the row: each CTA reduces its slice, and the (maximum, then sum) of
-// the slices are exchanged through distributed shared memory.
-//
-// The path's tokens: at most 63 per row.  Those that fall into the CTA's slice
-// are marked in a bitmap in shared memory; an entry whose bit is set (a rare
-// one) counts its occurrences in the list.
+// Bound by memory: a row is read once and written once.  A row is cut into slices, one
+// CTA each; for the softmax the slices of a row form a cluster, and the maximum and the
+// sum of the slices are exchanged through distributed shared memory.  The grid is as
+// large as the GPU holds at once (two CTAs per SM: one loads or stores while the other
+// waits for its cluster), and each group of CTAs takes a contiguous range of rows.
+// A slice comes into shared memory by a bulk copy, the next row's while the present
+// one is reduced and stored.
+// A tree's rows share their sequence's counts and biases, and few tokens have any: when
+// the sequence changes the slice's are gathered into a list, and per row only the list's
+// entries are changed, in shared memory, one per thread or so; then the path's (at most
+// 63).  After that an entry costs a read into a register, the grammar's bit, the
+// maximum, one exponential and the store.
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include "tv_device.cuh"
 #include "tv_internal.h"
+#include "tv_tc.cuh"
 
 namespace tv {
 
 namespace {
 
 constexpr int LG_THREADS = 512;
+constexpr int LG_NV_MAX = 8;                                // 4-entry vectors per thread
+constexpr int LG_SLICE_MAX = LG_THREADS * 4 * LG_NV_MAX - 32;
+constexpr int LG_CLUSTER_MAX = 16;
+constexpr int LG_PLAIN_SLICE = LG_THREADS * 4 * 4 - 32;     // without a softmax: no cluster
+constexpr int LG_SMEM = 112 * 1024;                         // two CTAs per SM
 constexpr float LG_LOG2E = 1.4426950408889634f;
 
 struct LgParams {
@@ -41,318 +52,438 @@ struct LgParams {
     float* out;
     int32_t* status;
     int N, V, words;
+    int64_t rows;
+    int groups;     // of CTAs, each with a range of rows
     int slices;     // CTAs per row (the cluster, for the softmax)
     int slice;      // entries per CTA, a multiple of 32
-    int staged;     // of them, how many are kept in shared memory (softmax)
+    int list_max;   // entries that the list of counts and biases holds
 };
 
-// What one row needs besides its logits.
 struct LgRow {
-    float rep, freq, pres, temp;
-    const int32_t* counts;     // nullable
-    const float* bias;         // nullable
-    const uint32_t* grammar;   // nullable
-    const uint32_t* marks;     // bitmap of the slice's path tokens, null without any
-    const int* path;
-    int n_path;
-    int x0;                    // the slice's first token
+    float rep, inv_rep, freq, pres, inv_temp;
 };
 
-// The processed entry x (before the temperature).
-__device__ __forceinline__ float lg_entry(const LgRow& r, float z, int x, int word, float bias) {
-    z += bias;
-    int n = word & 0x7fffffff;
-    if (r.marks && ((r.marks[(x - r.x0) >> 5] >> ((x - r.x0) & 31)) & 1u))
-        for (int i = 0; i < r.n_path; ++i) n += r.path[i] == x;
-    if (word < 0 || n > 0) z = z > 0.f ? z / r.rep : z * r.rep;
-    z -= r.freq * (float)n;
-    return n > 0 ? z - r.pres : z;
+// The repetition penalty of a token that the history or the path holds, less frequency *
+// n + presence [n > 0].
+__device__ __forceinline__ float lg_penalty(const LgRow& r, float z, int n) {
+    z = z > 0.f ? z * r.inv_rep : z * r.rep;
+    return n > 0 ? z - fmaf(r.freq, (float)n, r.pres) : z;
 }
-
-template <typename E>
-__device__ __forceinline__ float lg_load(const E* p, int64_t i);
-template <>
-__device__ __forceinline__ float lg_load<float>(const float* p, int64_t i) { return __ldcs(p + i); }
-template <>
-__device__ __forceinline__ float lg_load<__nv_bfloat16>(const __nv_bfloat16* p, int64_t i) {
-    return __bfloat162float(__ldcs(p + i));
+// A list entry's word: the entry, and above it 0 (not in the history), 1 (in the prompt
+// only), n + 1, or LG_LONG (the count does not fit: read it again).
+constexpr uint32_t LG_LONG = 0xffffu;
+__device__ __forceinline__ uint32_t lg_word(int x, int c) {
+    const uint32_t n = (uint32_t)c & 0x7fffffffu;
+    return (uint32_t)x | (c == 0 ? 0u : (n + 1u < LG_LONG ? n + 1u : LG_LONG)) << 16;
 }
-__device__ __forceinline__ float4 lg_load4(const float* p) {
-    return __ldcs(reinterpret_cast<const float4*>(p));
-}
-__device__ __forceinline__ float4 lg_load4(const __nv_bfloat16* p) {
-    const uint2 u = __ldcs(reinterpret_cast<const uint2*>(p));
-    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-
-// Row state of (b, i), shared by both kernels.  Returns 0 when the row is to be
-// processed, 1 when it is absent, 2 when its sequence has an error.  Called by
-// every thread of the CTA (contains barriers).
-__device__ __forceinline__ int lg_row_setup(const LgParams& p, int b, int i, int x0, int n,
-                                            uint32_t* marks, int* path, int* misc, LgRow& r,
-                                            bool report) {
-    const int tid = threadIdx.x;
-    const int cnt = p.node_counts ? p.node_counts[b] : p.N;
-    r.rep = p.rep ? p.rep[b] : 1.f;
-    r.freq = p.freq ? p.freq[b] : 0.f;
-    r.pres = p.pres ? p.pres[b] : 0.f;
-    r.temp = p.temp ? p.temp[b] : 1.f;
-    int err = (cnt >= 1 && cnt <= p.N) ? TV_OK : TV_ERR_OUT_OF_RANGE;
-    const bool absent = err == TV_OK && i >= cnt;
-    if (err == TV_OK && !(isfinite(r.rep) && r.rep > 0.f && isfinite(r.temp) && r.temp > 0.f &&
-                          isfinite(r.freq) && isfinite(r.pres)))
-        err = TV_ERR_BAD_VALUES;
-    if (tid == 0) misc[0] = 0;
-    // the tokens of nodes 1 .. cnt-1, one per thread
-    bool tok_ok = true;
-    int tok = -1;
-    if (p.mask && err != TV_ERR_OUT_OF_RANGE && tid >= 1 && tid < cnt) {
-        tok = p.tokens[(int64_t)b * p.N + tid];
-        tok_ok = tok >= 0 && tok < p.V;
-    }
-    if (__syncthreads_and(tok_ok ? 1 : 0) == 0) err = TV_ERR_OUT_OF_RANGE;
-    if (report && tid == 0) p.status[b] = err;
-    if (absent) return 1;
-    if (err != TV_OK) return 2;
-    r.counts = p.counts ? p.counts + (int64_t)b * p.V : nullptr;
-    r.bias = p.bias ? p.bias + (int64_t)b * p.V : nullptr;
-    r.grammar = p.grammar ? p.grammar + ((int64_t)b * p.N + i) * p.words : nullptr;
-    r.marks = nullptr;
-    r.path = path;
-    r.x0 = x0;
-    r.n_path = 0;
-    if (p.mask && p.counts) {
-        const uint64_t m = p.mask[(int64_t)b * p.N + i];
-        const bool mine = tid >= 1 && tid < cnt && ((m >> (tid & 63)) & 1ull) && tok >= x0 && tok < x0 + n;
-        if (mine) path[atomicAdd(&misc[0], 1)] = tok;
-        __syncthreads();
-        r.n_path = misc[0];
-        if (r.n_path > 0) {
-            for (int w = tid; w < (n + 31) / 32; w += blockDim.x) marks[w] = 0u;
-            __syncthreads();
-            if (tid < r.n_path) atomicOr(&marks[(path[tid] - x0) >> 5], 1u << ((path[tid] - x0) & 31));
-            __syncthreads();
-            r.marks = marks;
-        }
-    }
-    return 0;
-}
-
-// Processes entries x .. x + 3 (VEC) or entry x.
-template <typename E, bool VEC>
-__device__ __forceinline__ void lg_process(const LgRow& r, const E* in, int x, float (&z)[VEC ? 4 : 1]) {
-    if constexpr (VEC) {
-        const float4 v = lg_load4(in + x);
-        int4 c = make_int4(0, 0, 0, 0);
-        float4 bs = make_float4(0.f, 0.f, 0.f, 0.f);
-        uint32_t ok = 0xfu;
-        if (r.counts) c = *reinterpret_cast<const int4*>(r.counts + x);
-        if (r.bias) bs = *reinterpret_cast<const float4*>(r.bias + x);
-        if (r.grammar) ok = __ldcs(r.grammar + (x >> 5)) >> (x & 31);
-        z[0] = (ok & 1u) ? lg_entry(r, v.x, x, c.x, bs.x) : -INFINITY;
-        z[1] = (ok & 2u) ? lg_entry(r, v.y, x + 1, c.y, bs.y) : -INFINITY;
-        z[2] = (ok & 4u) ? lg_entry(r, v.z, x + 2, c.z, bs.z) : -INFINITY;
-        z[3] = (ok & 8u) ? lg_entry(r, v.w, x + 3, c.w, bs.w) : -INFINITY;
-    } else {
-        const float v = lg_load<E>(in, x);
-        const int c = r.counts ? r.counts[x] : 0;
-        const float bs = r.bias ? r.bias[x] : 0.f;
-        const bool ok = !r.grammar || ((r.grammar[x >> 5] >> (x & 31)) & 1u);
-        z[0] = ok ? lg_entry(r, v, x, c, bs) : -INFINITY;
-    }
-}
-
-template <int W>
-__device__ __forceinline__ void lg_store(float* p, const float (&z)[W]) {
-    if constexpr (W == 4) __stcs(reinterpret_cast<float4*>(p), make_float4(z[0], z[1], z[2], z[3]));
-    else __stcs(p, z[0]);
-}
-
-template <int W>
-__device__ __forceinline__ void lg_stage(float* p, const float (&z)[W]) {
-    if constexpr (W == 4) *reinterpret_cast<float4*>(p) = make_float4(z[0], z[1], z[2], z[3]);
-    else *p = z[0];
-}
-template <int W>
-__device__ __forceinline__ void lg_unstage(const float* p, float (&z)[W]) {
-    if constexpr (W == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        z[0] = v.x;
-        z[1] = v.y;
-        z[2] = v.z;
-        z[3] = v.w;
-    } else {
-        z[0] = *p;
-    }
-}
-
-// Logits out: one CTA per (slice, row).
-template <typename E, bool VEC>
-__global__ void __launch_bounds__(LG_THREADS) logits_kernel(LgParams p) {
-    extern __shared__ uint32_t marks[];
-    __shared__ int path[64];
-    __shared__ int misc[1];
-    const int64_t row = blockIdx.x / p.slices;
-    const int part = (int)(blockIdx.x % p.slices);
-    const int b = (int)(row / p.N), i = (int)(row % p.N);
-    const int x0 = part * p.slice, n = min(p.slice, p.V - x0);
-    constexpr int W = VEC ? 4 : 1;
-    pdl_launch_dependents();
-    pdl_wait();
-    LgRow r;
-    const int what = lg_row_setup(p, b, i, x0, n, marks, path, misc, r, i == 0 && part == 0);
-    if (what == 1) return;
-    const E* in = static_cast<const E*>(p.logits) + row * p.V;
-    float* out = p.out + row * p.V;
-    for (int x = x0 + threadIdx.x * W; x < x0 + n; x += LG_THREADS * W) {
-        float z[W];
-        if (what == 2) {
-#pragma unroll
-            for (int e = 0; e < W; ++e) z[e] = -INFINITY;
-        } else {
-            lg_process<E, VEC>(r, in, x, z);
-#pragma unroll
-            for (int e = 0; e < W; ++e) z[e] = z[e] / r.temp;
-        }
-        lg_store(out + x, z);
-    }
-}
-
 __device__ __forceinline__ float lg_max(float a, float b) {  // NaN wins
-    return (a > b || a != a) ? a : b;
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
 }
+__device__ __forceinline__ float lg_float(float x) { return x; }
+__device__ __forceinline__ float lg_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// Probabilities out: one cluster per row, CTA c of it the slice c.
-template <typename E, bool VEC>
-__global__ void __launch_bounds__(LG_THREADS) probs_kernel(LgParams p) {
-    extern __shared__ __align__(16) float stage[];      // [staged], then the bitmap
-    __shared__ int path[64];
-    __shared__ int misc[1];
-    __shared__ float red[LG_THREADS / 32];
-    __shared__ __align__(16) float part[2][4];          // this CTA's maximum, its sum
-    const int64_t row = blockIdx.x / p.slices;
-    const int b = (int)(row / p.N), i = (int)(row % p.N);
+template <typename E, bool PROBS, int NV>
+__global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgParams p) {
+    constexpr bool F32 = sizeof(E) == 4;
+    constexpr int CAP = LG_THREADS * 4 * NV;             // positions of the slice buffer
+    extern __shared__ __align__(128) uint8_t lg_smem[];
+    float* zs = reinterpret_cast<float*>(lg_smem);       // [CAP] the slice, entry x at zs[x + sh]
+    E* raw = reinterpret_cast<E*>(F32 ? lg_smem : lg_smem + CAP * 4);   // [CAP + 8] as it comes
+    uint32_t* s_gram = reinterpret_cast<uint32_t*>(lg_smem + CAP * 4 + (F32 ? 0 : CAP * 2 + 16));  // [CAP / 32 + 2]
+    uint2* list = reinterpret_cast<uint2*>(s_gram + CAP / 32 + 2);      // (word, bias)
+    __shared__ int tok[64];
+    __shared__ int list_n;
+    __shared__ float red[2][LG_THREADS / 32];
+    __shared__ float peer[2][LG_CLUSTER_MAX];            // maximum, sum of the row's slices
+    __shared__ __align__(8) uint64_t peer_bar[2];
+    __shared__ __align__(8) uint64_t full;               // the slice has landed
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int cs = p.slices, me = (int)(blockIdx.x % p.slices);
+    const int group = (int)(blockIdx.x / p.slices), me = (int)(blockIdx.x % p.slices);
+    const int64_t row_lo = p.rows * group / p.groups, row_hi = p.rows * (group + 1) / p.groups;
     const int x0 = me * p.slice, n = max(0, min(p.slice, p.V - x0));
-    constexpr int W = VEC ? 4 : 1;
-    uint32_t* marks = reinterpret_cast<uint32_t*>(stage + p.staged);
+    if (tid == 0) {
+        mbar_init(&peer_bar[0], 1);
+        mbar_init(&peer_bar[1], 1);
+        mbar_init(&full, 1);
+        fence_mbar_init();
+        s_gram[0] = 0u;
+    }
+    if (PROBS && p.slices > 1) cluster_barrier_all();    // every slice's barriers are there
+    else __syncthreads();
     pdl_launch_dependents();
     pdl_wait();
-    LgRow r;
-    const int what = lg_row_setup(p, b, i, x0, n, marks, path, misc, r, i == 0 && me == 0);
-    if (what == 1) return;                               // the whole cluster returns
-    const E* in = static_cast<const E*>(p.logits) + row * p.V;
-    float* out = p.out + row * p.V;
-    if (what == 2) {
-        const float zero[W] = {};
-        for (int x = x0 + tid * W; x < x0 + n; x += LG_THREADS * W) lg_store(out + x, zero);
-        return;
-    }
-    // maximum over the cluster
-    float mx = -INFINITY;
-    for (int e = tid * W; e < n; e += LG_THREADS * W) {
-        float z[W];
-        lg_process<E, VEC>(r, in, x0 + e, z);
+    // A slice of a row: the 16-byte pieces that lie inside by a bulk copy (issued by thread 0),
+    // up to 7 entries at each end and its grammar word by each thread, a row ahead.
+    const uint64_t policy = l2_policy_evict_first();
+    E edge{};
+    uint32_t gram = 0xffffffffu;
+    auto fetch = [&](int64_t row) {
+        const E* lo = static_cast<const E*>(p.logits) + row * p.V + x0;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(lo), al = (a + 15) & ~(uintptr_t)15;
+        const uintptr_t ah = max(al, (a + (size_t)n * sizeof(E)) & ~(uintptr_t)15);
+        const int head = (int)((al - a) / sizeof(E)), end = (int)((ah - a) / sizeof(E));   // entries [head, end) by the copy
+        if (tid == 0) {
+            const uint32_t bytes = (uint32_t)(ah - al);
+            mbar_arrive_expect_tx_relaxed_one(&full, bytes);
+            if (bytes > 0) bulk_load(raw + (a / sizeof(E)) % (16 / sizeof(E)) + head, reinterpret_cast<const void*>(al), bytes, &full, policy);
+        }
+        const int x = tid < head ? tid : end + tid - head;
+        if (x < n && tid < 16) edge = lo[x];
+        if (p.grammar && tid * 32 < n) gram = __ldcs(p.grammar + row * p.words + x0 / 32 + tid);
+    };
+    LgRow r{};
+    int cur = -1, cnt = 0, err = TV_OK;
+    uint32_t phase = 0, got = 0;
+    bool alive = true;
+    uint64_t same = 0ull;                                // thread c: the nodes with node c's token
+    int my_x = -1, my_c = 0;                             // its entry in the slice, count and bias
+    float my_bias = 0.f;
+    if (row_lo < row_hi) fetch(row_lo);
+#pragma unroll 1
+    for (int64_t row = row_lo; row < row_hi; ++row) {
+        const int b = (int)(row / p.N), i = (int)(row % p.N);
+        float* out = p.out + row * p.V + x0;
+        const int64_t at = (int64_t)b * p.V + x0;        // the slice in counts and bias
+        const uint64_t m = p.mask ? p.mask[row] & ~1ull : 0ull;
+        if (b != cur) {
+            // ---- the sequence: parameters, checks, the list of its counts and biases
+            cur = b;
+            cnt = p.node_counts ? p.node_counts[b] : p.N;
+            r.rep = p.rep ? p.rep[b] : 1.f;
+            r.freq = p.freq ? p.freq[b] : 0.f;
+            r.pres = p.pres ? p.pres[b] : 0.f;
+            const float temp = p.temp ? p.temp[b] : 1.f;
+            err = (cnt >= 1 && cnt <= p.N) ? TV_OK : TV_ERR_OUT_OF_RANGE;
+            const bool tokens = p.mask && err == TV_OK;
+            if (err == TV_OK && !(isfinite(r.rep) && r.rep > 0.f && isfinite(temp) && temp > 0.f &&
+                                  isfinite(r.freq) && isfinite(r.pres)))
+                err = TV_ERR_BAD_VALUES;
+            r.inv_rep = 1.f / r.rep;
+            r.inv_temp = 1.f / temp;
+            __syncthreads();                              // the sequence before is done with
+            if (tid == 0) list_n = 0;
+            bool tok_ok = true;
+            if (tokens && tid < cnt) {
+                tok[tid] = p.tokens[(int64_t)b * p.N + tid];
+                tok_ok = tid == 0 || (tok[tid] >= 0 && tok[tid] < p.V);
+            }
+            if (__syncthreads_and(tok_ok ? 1 : 0) == 0) err = TV_ERR_OUT_OF_RANGE;
+            if (p.counts || p.bias) {
+                constexpr int U = 8;
+                for (int base = 0; base < n; base += LG_THREADS * U) {
+                    int c[U];
+                    float bs[U];
 #pragma unroll
-        for (int k = 0; k < W; ++k) mx = lg_max(z[k], mx);
-        if (e < p.staged) lg_stage(stage + e, z);
+                    for (int u = 0; u < U; ++u) {
+                        const int x = base + u * LG_THREADS + tid;
+                        c[u] = p.counts && x < n ? p.counts[at + x] : 0;
+                        bs[u] = p.bias && x < n ? p.bias[at + x] : 0.f;
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const bool has = c[u] != 0 || bs[u] != 0.f;
+                        const uint32_t votes = __ballot_sync(0xffffffffu, has);
+                        if (votes == 0u) continue;
+                        int first = 0;
+                        if (lane == 0) first = atomicAdd(&list_n, __popc(votes));
+                        const int j = __shfl_sync(0xffffffffu, first, 0) + __popc(votes & ((1u << lane) - 1u));
+                        if (has && j < p.list_max)
+                            list[j] = make_uint2(lg_word(base + u * LG_THREADS + tid, c[u]), __float_as_uint(bs[u]));
+                    }
+                }
+            }
+            same = 0ull;
+            my_x = -1;
+            if (tokens && err == TV_OK && p.counts && tid >= 1 && tid < cnt) {
+                const int x = tok[tid] - x0;
+                if (x >= 0 && x < n) {
+                    my_x = x;
+                    my_c = p.counts[at + x] & 0x7fffffff;
+                    my_bias = p.bias ? p.bias[at + x] : 0.f;
+                    for (int c = 1; c < cnt; ++c) same |= (uint64_t)(tok[c] == tok[tid]) << c;
+                }
+            }
+            __syncthreads();
+        }
+        if (i == 0 && me == 0 && tid == 0) p.status[b] = err;
+        // ---- the slice has landed; its ends and its grammar words
+        alive = alive && mbar_wait(&full, got & 1u);
+        ++got;
+        const int sh = (int)((reinterpret_cast<uintptr_t>(out) >> 2) & 3);
+        const int rsh = (int)((reinterpret_cast<uintptr_t>(static_cast<const E*>(p.logits) + row * p.V + x0) / sizeof(E)) %
+                              (16 / sizeof(E)));
+        {
+            const int head = min(n, (int)(16 / sizeof(E) - rsh) % (int)(16 / sizeof(E)));
+            const int end = max(head, ((rsh + n) & ~(int)(16 / sizeof(E) - 1)) - rsh);
+            const int x = tid < head ? tid : end + tid - head;
+            if (x < n && tid < 16) raw[x + rsh] = edge;
+            if (tid * 32 < n) s_gram[1 + tid] = gram;
+            if (tid * 32 < n + 32) s_gram[1 + (n + 31) / 32] = 0u;
+        }
+        const bool skip = (cnt >= 1 && cnt <= p.N && i >= cnt) || err != TV_OK;
+        const bool path = m != 0 && p.counts && !skip;
+        if constexpr (!F32) {
+            // bfloat16: widen into the float buffer
+            __syncthreads();
+            for (int x = tid; x < n; x += LG_THREADS) zs[x + sh] = lg_float(raw[x + rsh]);
+        }
+        // (float32: in and out rows may be aligned differently; then the entries move first)
+        float* zr = F32 ? reinterpret_cast<float*>(raw) : zs;
+        const int zsh = F32 ? rsh : sh;
+        // ---- the path's tokens (each once) are computed before the list changes them
+        float my_z = 0.f;
+        const bool mine = path && my_x >= 0 && ((m >> (tid & 63)) & 1ull) && (same & m & ((1ull << (tid & 63)) - 1ull)) == 0ull;
+        if (path || !F32) __syncthreads();
+        if (mine) my_z = lg_penalty(r, zr[my_x + zsh] + my_bias, my_c + __popcll(same & m));
+        __syncthreads();
+        if (!skip && (p.counts || p.bias)) {
+            auto change = [&](int x, int c, float bs) {
+                float z = zr[x + zsh] + bs;
+                if (c != 0) z = lg_penalty(r, z, c & 0x7fffffff);
+                zr[x + zsh] = z;
+            };
+            if (list_n <= p.list_max) {
+                for (int j = tid; j < list_n; j += LG_THREADS) {
+                    const uint2 w = list[j];
+                    const int x = (int)(w.x & 0xffffu);
+                    const uint32_t k = w.x >> 16;
+                    const int c = k == 0u ? 0 : k == LG_LONG ? p.counts[at + x] : (int)(k - 1u) | INT32_MIN;
+                    change(x, c, __uint_as_float(w.y));
+                }
+            } else {
+                // more counts and biases than the list holds: all of them, from L2
+                for (int x = tid; x < n; x += LG_THREADS) {
+                    const int c = p.counts ? p.counts[at + x] : 0;
+                    const float bs = p.bias ? p.bias[at + x] : 0.f;
+                    if (c != 0 || bs != 0.f) change(x, c, bs);
+                }
+            }
+            __syncthreads();
+            if (mine) zr[my_x + zsh] = my_z;
+            if (path) __syncthreads();
+        }
+        // ---- into registers: positions 4 (k LG_THREADS + tid) of the buffer
+        float z[NV][4];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int q = (k * LG_THREADS + tid) * 4, x = q - zsh;
+            const float4 v = *reinterpret_cast<const float4*>(zr + q);
+            z[k][0] = v.x;
+            z[k][1] = v.y;
+            z[k][2] = v.z;
+            z[k][3] = v.w;
+            uint32_t ok = 0xfu;
+            if (p.grammar && x < n) {
+                const int w = (x + 32) >> 5;             // (s_gram[0] stands before the slice)
+                ok = __funnelshift_r(s_gram[w], s_gram[w + 1], (x + 32) & 31);
+            }
+            if (x < 0) ok &= 0xfu << -x;
+            if (x + 4 > n) ok = x >= n ? 0u : ok & (0xfu >> (x + 4 - n));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (!((ok >> e) & 1u)) z[k][e] = -INFINITY;
+            if constexpr (PROBS) mx = lg_max(mx, lg_max(lg_max(z[k][0], z[k][1]), lg_max(z[k][2], z[k][3])));
+        }
+        fence_proxy_async_smem();                        // the next copy lands where this row was
+        __syncthreads();
+        if (row + 1 < row_hi) fetch(row + 1);
+        if (skip && err == TV_OK) continue;              // an absent node: nothing is written
+        auto store = [&](float scale) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int x = (k * LG_THREADS + tid) * 4 - zsh;
+                if (x >= 0 && x + 4 <= n && zsh == sh) {
+                    __stcs(reinterpret_cast<float4*>(out + x),
+                           make_float4(z[k][0] * scale, z[k][1] * scale, z[k][2] * scale, z[k][3] * scale));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (x + e >= 0 && x + e < n) out[x + e] = z[k][e] * scale;
+                }
+            }
+        };
+        if (err != TV_OK) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[k][e] = PROBS ? 0.f : -INFINITY;
+            store(1.f);
+            continue;
+        }
+        if constexpr (!PROBS) {
+            store(r.inv_temp);
+        } else {
+            // ---- softmax: over the CTA, then over the cluster (every CTA combines the slices'
+            // values in the same order)
+            auto reduce = [&](float v, bool sum, int where) -> float {
+                const float none = sum ? 0.f : -INFINITY;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const float y = __shfl_xor_sync(0xffffffffu, v, o);
+                    v = sum ? v + y : lg_max(v, y);
+                }
+                if (lane == 0) red[where][warp] = v;
+                __syncthreads();
+                v = lane < LG_THREADS / 32 ? red[where][lane] : none;
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) {
+                    const float y = __shfl_xor_sync(0xffffffffu, v, o);
+                    v = sum ? v + y : lg_max(v, y);
+                }
+                v = __shfl_sync(0xffffffffu, v, 0);
+                if (p.slices == 1) return v;
+                // Every slice writes its value into all of them and counts the bytes on their
+                // barrier: a cluster barrier would first wait for the row before to be stored.
+                // (A slice sends its next maximum only after it has every sum, and so on: a slot
+                // is read before it is written again, and a CTA ends only with every value here.)
+                if (warp == 0) {
+                    mbar_arrive_expect_tx_relaxed_elect(&peer_bar[where], (uint32_t)p.slices * 4);
+                    __syncwarp();
+                    if (lane < p.slices) remote_st_async(&peer[where][me], &peer_bar[where], (uint32_t)lane, v);
+                }
+                alive = alive && mbar_wait(&peer_bar[where], phase);
+                v = lane < p.slices ? *reinterpret_cast<volatile float*>(&peer[where][lane]) : none;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const float y = __shfl_xor_sync(0xffffffffu, v, o);
+                    v = sum ? v + y : lg_max(v, y);
+                }
+                return v;
+            };
+            mx = reduce(mx, false, 0);
+            // e^((z - max) / temperature); the shift's rounding is the same for every entry and
+            // cancels in the quotient
+            const float scale = LG_LOG2E * r.inv_temp;
+            const float base = mx == -INFINITY ? 0.f : -mx * scale;
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[k][e] = ex2_approx(fmaf(z[k][e], scale, base));
+                sum += (z[k][0] + z[k][1]) + (z[k][2] + z[k][3]);
+            }
+            sum = reduce(sum, true, 1);
+            phase ^= 1u;
+            store(sum == 0.f ? 0.f : 1.f / sum);         // NaN stays NaN
+        }
+        if (__syncthreads_and(alive ? 1 : 0) == 0) {     // a copy or a slice's value never came
+            if (tid == 0) p.status[b] = TV_ERR_TIMEOUT;
+            if (row + 1 < row_hi) mbar_wait(&full, got & 1u);   // its own copy in flight
+            break;
+        }
     }
+}
+
+template <typename E, bool PROBS, int NV>
+tv_status launch_nv(LgParams p, cudaStream_t stream) {
+    auto fn = tree_logits_kernel<E, PROBS, NV>;
+    constexpr int CAP = LG_THREADS * 4 * NV;
+    const size_t fixed = CAP * 4 + (sizeof(E) == 4 ? 0 : CAP * 2 + 16) + (CAP / 32 + 2) * 4;
+    p.list_max = (p.counts || p.bias) ? std::min<int>(p.slice, (int)((LG_SMEM - fixed) / 8)) : 0;
+    const size_t smem = fixed + (size_t)p.list_max * 8;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TV_ERR_CUDA;
+    static bool set[64] = {};
+    if (!set[dev]) {
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, LG_SMEM) != cudaSuccess ||
+            (PROBS && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)) {
+            cudaGetLastError();
+            return TV_ERR_CUDA;
+        }
+        set[dev] = true;
+    }
+    // as many groups as the GPU holds at once
+    LaunchCfg lc(dim3((unsigned)p.slices), dim3(LG_THREADS), smem, stream, PROBS ? (unsigned)p.slices : 0u);
+    // (the last answer is kept: slices, shared memory, what fits)
+    static std::atomic<uint64_t> last[64];
+    const uint64_t key = ((uint64_t)p.slices << 48) | ((uint64_t)smem << 16);
+    const uint64_t known = last[dev].load();
+    int fit = (int)(known & 0xffff);
+    if ((known & ~0xffffull) != key || fit == 0) {
+        const cudaError_t e = PROBS ? cudaOccupancyMaxActiveClusters(&fit, fn, &lc.cfg)
+                                    : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, fn, LG_THREADS, smem);
+        if (e != cudaSuccess || fit < 1) {
+            cudaGetLastError();
+            return TV_ERR_CUDA;
+        }
+        fit = std::min(fit, 0xffff);
+        last[dev].store(key | (uint64_t)fit);
+    }
+    if (!PROBS) fit = std::max(1, fit * device_sm_count() / p.slices);
+    p.groups = (int)std::min<int64_t>(p.rows, fit);
+    lc.cfg.gridDim = dim3((unsigned)(p.groups * p.slices));
+    return cudaLaunchKernelEx(&lc.cfg, fn, p) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+}
+
+template <typename E, bool PROBS>
+tv_status launch_slices(const LgParams& p, cudaStream_t stream) {
+    const int per = (p.slice + 3 + LG_THREADS * 4 - 1) / (LG_THREADS * 4);
+    if constexpr (!PROBS) {
+        return launch_nv<E, PROBS, 4>(p, stream);
+    } else {
+        if (per <= 2) return launch_nv<E, PROBS, 2>(p, stream);
+        if (per <= 5) return launch_nv<E, PROBS, 5>(p, stream);
+        return launch_nv<E, PROBS, LG_NV_MAX>(p, stream);
+    }
+}
+
+// Rows that no cluster holds: the logits are written first, and this softmax, one CTA
+// per row, reads them again.
+__global__ void __launch_bounds__(LG_THREADS) row_softmax_kernel(const LgParams p) {
+    __shared__ float red[2][LG_THREADS / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t row = blockIdx.x;
+    const int b = (int)(row / p.N), i = (int)(row % p.N);
+    pdl_launch_dependents();
+    pdl_wait();
+    const int cnt = p.node_counts ? p.node_counts[b] : p.N;
+    if (cnt >= 1 && cnt <= p.N && i >= cnt) return;      // an absent node's row
+    float* z = p.out + row * p.V;
     auto reduce = [&](float v, bool sum, int where) -> float {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             const float y = __shfl_xor_sync(0xffffffffu, v, o);
             v = sum ? v + y : lg_max(v, y);
         }
-        if (lane == 0) red[warp] = v;
+        if (lane == 0) red[where][warp] = v;
         __syncthreads();
-        v = lane < LG_THREADS / 32 ? red[lane] : (sum ? 0.f : -INFINITY);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float y = __shfl_xor_sync(0xffffffffu, v, o);
-            v = sum ? v + y : lg_max(v, y);
-        }
-        if (tid == 0) part[where][0] = v;
-        cluster_barrier_all();
-        // every CTA adds the parts in rank order, so all hold the same value
-        float all = sum ? 0.f : -INFINITY;
-        for (int c = 0; c < cs; ++c) {
-            const float u = remote_ld_f4(part[where], (uint32_t)c).x;
-            all = sum ? all + u : lg_max(all, u);
-        }
-        return all;
+        v = sum ? 0.f : -INFINITY;
+        for (int w = 0; w < LG_THREADS / 32; ++w) v = sum ? v + red[where][w] : lg_max(v, red[where][w]);
+        return v;
     };
+    float mx = -INFINITY, sum = 0.f;
+    for (int x = tid; x < p.V; x += LG_THREADS) mx = lg_max(mx, z[x]);
     mx = reduce(mx, false, 0);
-    // exp((z - max) / temperature): the difference first, so the temperature's
-    // rounding does not grow with the logits
-    const float scale = LG_LOG2E / r.temp;
     const float base = mx == -INFINITY ? 0.f : mx;
-    float sum = 0.f;
-    for (int e = tid * W; e < n; e += LG_THREADS * W) {
-        float z[W];
-        if (e < p.staged) lg_unstage(stage + e, z);
-        else lg_process<E, VEC>(r, in, x0 + e, z);
-#pragma unroll
-        for (int k = 0; k < W; ++k) {
-            z[k] = ex2_approx((z[k] - base) * scale);
-            sum += z[k];
-        }
-        if (e < p.staged) lg_stage(stage + e, z);
-    }
+    for (int x = tid; x < p.V; x += LG_THREADS) sum += ex2_approx((z[x] - base) * LG_LOG2E);
     sum = reduce(sum, true, 1);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;      // NaN stays NaN
-    for (int e = tid * W; e < n; e += LG_THREADS * W) {
-        float z[W];
-        if (e < p.staged) {
-            lg_unstage(stage + e, z);
-        } else {
-            lg_process<E, VEC>(r, in, x0 + e, z);
-#pragma unroll
-            for (int k = 0; k < W; ++k) z[k] = ex2_approx((z[k] - base) * scale);
-        }
-#pragma unroll
-        for (int k = 0; k < W; ++k) z[k] *= inv;
-        lg_store(out + x0 + e, z);
-    }
-    cluster_barrier_all();  // no CTA leaves while others read its part
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    for (int x = tid; x < p.V; x += LG_THREADS) z[x] = ex2_approx((z[x] - base) * LG_LOG2E) * inv;
 }
 
 template <typename E>
-tv_status launch_logits(const LogitsArgs& a, const LgParams& p0, bool vec) {
-    LgParams p = p0;
-    const int64_t rows = (int64_t)a.B * a.N;
-    if (!a.probs) {
-        p.slice = 4096;
-        p.slices = (a.V + p.slice - 1) / p.slice;
-        if (rows * p.slices > 0x7fffffff) return TV_ERR_UNSUPPORTED;
-        LaunchCfg lc(dim3((unsigned)(rows * p.slices)), dim3(LG_THREADS), (size_t)p.slice / 8, a.stream);
-        const cudaError_t e = vec ? cudaLaunchKernelEx(&lc.cfg, logits_kernel<E, true>, p)
-                                  : cudaLaunchKernelEx(&lc.cfg, logits_kernel<E, false>, p);
-        return e == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+tv_status launch_logits(const LogitsArgs& a, LgParams p) {
+    const bool cluster = a.probs && a.V <= LG_CLUSTER_MAX * LG_SLICE_MAX;
+    p.rows = (int64_t)a.B * a.N;
+    if (cluster) {
+        // the fewest CTAs that hold the row; up to 8 when that leaves SMs without work
+        int cs = 1;
+        while (cs < LG_CLUSTER_MAX && (int64_t)cs * LG_SLICE_MAX < a.V) cs *= 2;
+        while (cs < 8 && p.rows * cs < device_sm_count() && a.V > cs * 4096) cs *= 2;
+        p.slices = cs;
+    } else {
+        p.slices = (a.V + LG_PLAIN_SLICE - 1) / LG_PLAIN_SLICE;
     }
-    // cluster size: the fewest CTAs (up to 8) whose slice is at most 64 KB; rows longer
-    // than eight such slices take larger ones, and what does not fit into shared
-    // memory is read again
-    int cs = 1;
-    while (cs < 8 && (int64_t)cs * 16384 < a.V) cs *= 2;
-    if (rows * cs > 0x7fffffff) return TV_ERR_UNSUPPORTED;
-    p.slices = cs;
-    p.slice = ((a.V + cs - 1) / cs + 31) & ~31;
-    const int room = ((device_smem_optin() - 4096) / 4) & ~31;   // words
-    p.staged = p.slice;
-    if (p.slice + p.slice / 32 > room) p.staged = max(0, (room - p.slice / 32) & ~31);
-    const size_t smem = (size_t)(p.staged + p.slice / 32) * 4;
-    if (smem > (size_t)room * 4) return TV_ERR_UNSUPPORTED;
-    auto fn = vec ? probs_kernel<E, true> : probs_kernel<E, false>;
-    if (smem > 48 * 1024 - 1024 &&
-        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-        cudaGetLastError();
-        return TV_ERR_CUDA;
-    }
-    LaunchCfg lc(dim3((unsigned)(rows * cs)), dim3(LG_THREADS), smem, a.stream, (unsigned)cs);
-    return cudaLaunchKernelEx(&lc.cfg, fn, p) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+    p.slice = ((a.V + p.slices - 1) / p.slices + 31) & ~31;
+    if (cluster) return launch_slices<E, true>(p, a.stream);
+    const tv_status rc = launch_slices<E, false>(p, a.stream);
+    if (rc != TV_OK || !a.probs) return rc;
+    if (p.rows > 0x7fffffff) return TV_ERR_UNSUPPORTED;
+    LaunchCfg lc(dim3((unsigned)p.rows), dim3(LG_THREADS), 0, a.stream);
+    return cudaLaunchKernelEx(&lc.cfg, row_softmax_kernel, p) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
 
 }  // namespace
@@ -375,11 +506,7 @@ tv_status launch_tree_logits(const LogitsArgs& a) {
     p.N = a.N;
     p.V = a.V;
     p.words = (a.V + 31) / 32;
-    const uintptr_t all = reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.counts) |
-                          reinterpret_cast<uintptr_t>(a.bias) |
-                          (reinterpret_cast<uintptr_t>(a.logits) << (a.dt == TV_BF16 ? 1 : 0));
-    const bool vec = a.V % 4 == 0 && (all & 15) == 0;
-    return a.dt == TV_F32 ? launch_logits<float>(a, p, vec) : launch_logits<__nv_bfloat16>(a, p, vec);
+    return a.dt == TV_F32 ? launch_logits<float>(a, p) : launch_logits<__nv_bfloat16>(a, p);
 }
 
 }  // namespace tv

@@ -227,6 +227,12 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_relaxed_elect(uint64_t* ba
         "r"(bytes)
         : "memory");
 }
+// The same from one thread.
+__device__ __forceinline__ void mbar_arrive_expect_tx_relaxed_one(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)),
+                 "r"(bytes)
+                 : "memory");
+}
 __device__ __forceinline__ void tma_load_2d_elect(void* dst, const CUtensorMap* map, uint64_t* bar,
                                                   int32_t x, int32_t y, uint64_t policy) {
     asm volatile(
@@ -403,6 +409,14 @@ __device__ __forceinline__ int4 lds_v4_volatile(const int4* p) {
 }
 __device__ __forceinline__ void remote_st_u32(int* p, uint32_t rank, int v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(p, rank)), "r"(v) : "memory");
+}
+// Asynchronous 4-byte store into cluster rank `rank`, its bytes counted on that rank's
+// mbarrier `bar` (no release: earlier stores of the thread are not waited for).
+__device__ __forceinline__ void remote_st_async(float* p, uint64_t* bar, uint32_t rank, float v) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                     map_rank(p, rank)),
+                 "r"(__float_as_uint(v)), "r"(map_rank(bar, rank))
+                 : "memory");
 }
 __device__ __forceinline__ float4 remote_ld_f4(const float* p, uint32_t rank) {
     float4 v;
