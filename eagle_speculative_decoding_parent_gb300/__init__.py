@@ -402,13 +402,24 @@ def _row_stride(t, dtype, name, heads, d, T):
     return s[0] if T > 1 else heads * d
 
 
-def _on_one_device(*tensors):
-    """The tensors' common device, which must be the current one (the library launches
-    there, and the caller's stream belongs to it)."""
-    dev = torch.cuda.current_device()
+def _raw_stream(stream, *tensors):
+    """The stream to launch on, after a check that the tensors live on the current device
+    (the library launches there).  The raw-stream query instead of torch's Stream object: that
+    costs more than the rest of a small call's marshalling."""
+    dev = torch._C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError("tensors passed to libtreeverify must live on the current CUDA device")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _dense(t, name):
+    """Address of a tensor whose type and shape are checked, None for None."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors passed to libtreeverify must be contiguous")
+    return t.data_ptr()
 
 
 def _paged(k_cache, v_cache, block_table, q_start, prefix_lens, status, dtype, Hkv, d):
@@ -455,14 +466,16 @@ def chunk_kv_append(q, k, v, k_cache, v_cache, block_table, q_start, prefix_lens
         _want(positions, torch.int32, "positions", (T,))
     if rope is not None and not isinstance(rope, RopeTable):
         raise TypeError("rope: expected a RopeTable")
-    _on_one_device(q, k, v, q_out, k_cache, v_cache, block_table, q_start, prefix_lens, status,
-                   positions)
+    s = _raw_stream(stream, q, k, v, q_out, k_cache, v_cache, block_table, q_start, prefix_lens,
+                    status, positions)
     _check(_chunk_append(None if q is None else q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(),
-                         vs, _ptr(positions), T, _ptr(q_start), _ptr(prefix_lens), B, Hq, Hkv, d,
+                         vs, _dense(positions, "positions"), T, _dense(q_start, "q_start"),
+                         _dense(prefix_lens, "prefix_lens"), B, Hq, Hkv, d,
                          None if rope is None else ctypes.addressof(rope),
-                         None if q is None else q_out.data_ptr(), qos, _ptr(k_cache),
-                         _ptr(v_cache), _ptr(block_table), block_table.shape[1], bs, blocks, dt,
-                         _ptr(status), _stream(stream)), "chunk_kv_append")
+                         None if q is None else q_out.data_ptr(), qos, _dense(k_cache, "k_cache"),
+                         _dense(v_cache, "v_cache"), _dense(block_table, "block_table"),
+                         block_table.shape[1], bs, blocks, dt, _dense(status, "status"), s),
+           "chunk_kv_append")
 
 
 def chunk_attention_workspace(T, B, Hq, Hkv, d, dtype=torch.bfloat16) -> int:
@@ -486,12 +499,14 @@ def chunk_attention(q, k_cache, v_cache, block_table, q_start, prefix_lens, out,
     os_ = _row_stride(out, q.dtype, "out", Hq, d, T)
     B, bs, blocks = _paged(k_cache, v_cache, block_table, q_start, prefix_lens, status, q.dtype,
                            Hkv, d)
-    _on_one_device(q, k_cache, v_cache, block_table, q_start, prefix_lens, out, status, workspace)
+    s = _raw_stream(stream, q, k_cache, v_cache, block_table, q_start, prefix_lens, out, status,
+                    workspace)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_chunk_attn(q.data_ptr(), qs, _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
-                       block_table.shape[1], _ptr(q_start), _ptr(prefix_lens), T, B, Hq, Hkv, d,
-                       bs, blocks, dt, float(scale), float(softcap), int(window), out.data_ptr(),
-                       os_, _ptr(status), _ptr(workspace), ws_bytes, _stream(stream)),
+    _check(_chunk_attn(q.data_ptr(), qs, _dense(k_cache, "k_cache"), _dense(v_cache, "v_cache"),
+                       _dense(block_table, "block_table"), block_table.shape[1],
+                       _dense(q_start, "q_start"), _dense(prefix_lens, "prefix_lens"), T, B, Hq,
+                       Hkv, d, bs, blocks, dt, scale, softcap, window, out.data_ptr(), os_,
+                       _dense(status, "status"), _dense(workspace, "workspace"), ws_bytes, s),
            "chunk_attention")
 
 
@@ -513,10 +528,10 @@ def token_counts_update(counts, tokens, status, *, starts=None, clear: bool = Fa
         if tokens.dim() != 1:
             raise ValueError("tokens is int32 [total] with starts")
     _want(status, torch.int32, "status", (B,))
-    _on_one_device(counts, tokens, starts, status)
-    _check(_token_counts(_ptr(counts), _ptr(tokens), _ptr(starts), tokens.numel(), B, V,
-                         int(bool(clear)), int(bool(prompt)), _ptr(status), _stream(stream)),
-           "token_counts_update")
+    s = _raw_stream(stream, counts, tokens, starts, status)
+    _check(_token_counts(_dense(counts, "counts"), _dense(tokens, "tokens"),
+                         _dense(starts, "starts"), tokens.numel(), B, V, int(bool(clear)),
+                         int(bool(prompt)), _dense(status, "status"), s), "token_counts_update")
 
 
 def tree_logits_process(logits, out, status, *, probs: bool, mask=None, draft_tokens=None,
@@ -544,10 +559,12 @@ def tree_logits_process(logits, out, status, *, probs: bool, mask=None, draft_to
                                (temperature, "temperature", torch.float32, (B,))):
         if t is not None:
             _want(t, dtype, n, shape)
-    _on_one_device(logits, out, status, mask, draft_tokens, counts, bias, grammar, repetition,
-                   frequency, presence, temperature, node_counts)
-    _check(_tree_logits(_ptr(logits), dt, B, N, V, _counts(node_counts, B), _ptr(mask),
-                        _ptr(draft_tokens), _ptr(counts), _ptr(bias), _ptr(grammar),
-                        _ptr(repetition), _ptr(frequency), _ptr(presence), _ptr(temperature),
-                        int(bool(probs)), _ptr(out), _ptr(status), _stream(stream)),
+    s = _raw_stream(stream, logits, out, status, mask, draft_tokens, counts, bias, grammar,
+                    repetition, frequency, presence, temperature, node_counts)
+    _check(_tree_logits(_dense(logits, "logits"), dt, B, N, V, _counts(node_counts, B),
+                        _dense(mask, "mask"), _dense(draft_tokens, "draft_tokens"),
+                        _dense(counts, "counts"), _dense(bias, "bias"), _dense(grammar, "grammar"),
+                        _dense(repetition, "repetition"), _dense(frequency, "frequency"),
+                        _dense(presence, "presence"), _dense(temperature, "temperature"),
+                        int(bool(probs)), _dense(out, "out"), _dense(status, "status"), s),
            "tree_logits_process")

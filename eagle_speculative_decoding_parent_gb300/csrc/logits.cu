@@ -96,16 +96,15 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
     __shared__ int tok[64];
     __shared__ int list_n;
     __shared__ float red[2][LG_THREADS / 32];
-    __shared__ float peer[2][LG_CLUSTER_MAX];            // maximum, sum of the row's slices
-    __shared__ __align__(8) uint64_t peer_bar[2];
+    __shared__ float peer[2][2][LG_CLUSTER_MAX];         // [row parity][maximum, sum] of the slices
+    __shared__ __align__(8) uint64_t peer_bar;
     __shared__ __align__(8) uint64_t full;               // the slice has landed
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int group = (int)(blockIdx.x / p.slices), me = (int)(blockIdx.x % p.slices);
     const int64_t row_lo = p.rows * group / p.groups, row_hi = p.rows * (group + 1) / p.groups;
     const int x0 = me * p.slice, n = max(0, min(p.slice, p.V - x0));
     if (tid == 0) {
-        mbar_init(&peer_bar[0], 1);
-        mbar_init(&peer_bar[1], 1);
+        mbar_init(&peer_bar, 1);
         mbar_init(&full, 1);
         fence_mbar_init();
         s_gram[0] = 0u;
@@ -119,7 +118,20 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
     const uint64_t policy = l2_policy_evict_first();
     E edge{};
     uint32_t gram = 0xffffffffu;
-    auto fetch = [&](int64_t row) {
+    uint64_t mask_next = 0ull;
+    auto ahead = [&](const void* lo, size_t bytes) {     // to L2: the 16-byte pieces inside
+        const uintptr_t a = (reinterpret_cast<uintptr_t>(lo) + 15) & ~(uintptr_t)15;
+        const uintptr_t z = (reinterpret_cast<uintptr_t>(lo) + bytes) & ~(uintptr_t)15;
+        if (a < z) bulk_prefetch_l2(reinterpret_cast<const void*>(a), (uint32_t)(z - a));
+    };
+    // (of sequence b, or with same_b false of the one after it, whose counts and biases follow)
+    auto fetch = [&](int64_t row, int b, bool same_b) {
+        if (tid == 0 && !same_b) {
+            const int64_t at = (int64_t)(b + 1) * p.V + x0;
+            if (p.counts) ahead(p.counts + at, (size_t)n * 4);
+            if (p.bias) ahead(p.bias + at, (size_t)n * 4);
+        }
+        if (p.mask) mask_next = p.mask[row] & ~1ull;
         const E* lo = static_cast<const E*>(p.logits) + row * p.V + x0;
         const uintptr_t a = reinterpret_cast<uintptr_t>(lo), al = (a + 15) & ~(uintptr_t)15;
         const uintptr_t ah = max(al, (a + (size_t)n * sizeof(E)) & ~(uintptr_t)15);
@@ -140,13 +152,17 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
     uint64_t same = 0ull;                                // thread c: the nodes with node c's token
     int my_x = -1, my_c = 0;                             // its entry in the slice, count and bias
     float my_bias = 0.f;
-    if (row_lo < row_hi) fetch(row_lo);
+    int b = (int)(row_lo / p.N), i = (int)(row_lo % p.N) - 1;
+    if (row_lo < row_hi) fetch(row_lo, b, true);
 #pragma unroll 1
     for (int64_t row = row_lo; row < row_hi; ++row) {
-        const int b = (int)(row / p.N), i = (int)(row % p.N);
+        if (++i == p.N) {
+            i = 0;
+            ++b;
+        }
         float* out = p.out + row * p.V + x0;
         const int64_t at = (int64_t)b * p.V + x0;        // the slice in counts and bias
-        const uint64_t m = p.mask ? p.mask[row] & ~1ull : 0ull;
+        const uint64_t m = mask_next;
         if (b != cur) {
             // ---- the sequence: parameters, checks, the list of its counts and biases
             cur = b;
@@ -162,16 +178,22 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
                 err = TV_ERR_BAD_VALUES;
             r.inv_rep = 1.f / r.rep;
             r.inv_temp = 1.f / temp;
+            int t = 0;                                    // node tid's token, its count and bias
+            if (tokens && tid < cnt) t = p.tokens[(int64_t)b * p.N + tid];
+            const bool tok_ok = !tokens || tid == 0 || tid >= cnt || (t >= 0 && t < p.V);
+            my_x = -1;
+            if (tokens && tok_ok && p.counts && tid >= 1 && tid < cnt && t >= x0 && t < x0 + n) {
+                my_x = t - x0;
+                my_c = p.counts[at + my_x] & 0x7fffffff;
+                my_bias = p.bias ? p.bias[at + my_x] : 0.f;
+            }
             __syncthreads();                              // the sequence before is done with
             if (tid == 0) list_n = 0;
-            bool tok_ok = true;
-            if (tokens && tid < cnt) {
-                tok[tid] = p.tokens[(int64_t)b * p.N + tid];
-                tok_ok = tid == 0 || (tok[tid] >= 0 && tok[tid] < p.V);
-            }
+            if (tid < 64) tok[tid] = t;
             if (__syncthreads_and(tok_ok ? 1 : 0) == 0) err = TV_ERR_OUT_OF_RANGE;
             if (p.counts || p.bias) {
                 constexpr int U = 8;
+#pragma unroll 1
                 for (int base = 0; base < n; base += LG_THREADS * U) {
                     int c[U];
                     float bs[U];
@@ -181,35 +203,36 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
                         c[u] = p.counts && x < n ? p.counts[at + x] : 0;
                         bs[u] = p.bias && x < n ? p.bias[at + x] : 0.f;
                     }
+                    // the warp's entries in order, their places by one atomic
+                    uint32_t votes[U];
+                    int total = 0;
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        const bool has = c[u] != 0 || bs[u] != 0.f;
-                        const uint32_t votes = __ballot_sync(0xffffffffu, has);
-                        if (votes == 0u) continue;
-                        int first = 0;
-                        if (lane == 0) first = atomicAdd(&list_n, __popc(votes));
-                        const int j = __shfl_sync(0xffffffffu, first, 0) + __popc(votes & ((1u << lane) - 1u));
-                        if (has && j < p.list_max)
-                            list[j] = make_uint2(lg_word(base + u * LG_THREADS + tid, c[u]), __float_as_uint(bs[u]));
+                        votes[u] = __ballot_sync(0xffffffffu, c[u] != 0 || bs[u] != 0.f);
+                        total += __popc(votes[u]);
+                    }
+                    if (total == 0) continue;
+                    int j = 0;
+                    if (lane == 0) j = atomicAdd(&list_n, total);
+                    j = __shfl_sync(0xffffffffu, j, 0);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int k = j + __popc(votes[u] & ((1u << lane) - 1u));
+                        if (((votes[u] >> lane) & 1u) && k < p.list_max)
+                            list[k] = make_uint2(lg_word(base + u * LG_THREADS + tid, c[u]), __float_as_uint(bs[u]));
+                        j += __popc(votes[u]);
                     }
                 }
             }
             same = 0ull;
-            my_x = -1;
-            if (tokens && err == TV_OK && p.counts && tid >= 1 && tid < cnt) {
-                const int x = tok[tid] - x0;
-                if (x >= 0 && x < n) {
-                    my_x = x;
-                    my_c = p.counts[at + x] & 0x7fffffff;
-                    my_bias = p.bias ? p.bias[at + x] : 0.f;
-                    for (int c = 1; c < cnt; ++c) same |= (uint64_t)(tok[c] == tok[tid]) << c;
-                }
-            }
+            if (my_x >= 0)
+                for (int c = 1; c < cnt; ++c) same |= (uint64_t)(tok[c] == t) << c;
             __syncthreads();
         }
         if (i == 0 && me == 0 && tid == 0) p.status[b] = err;
         // ---- the slice has landed; its ends and its grammar words
-        alive = alive && mbar_wait(&full, got & 1u);
+        // (one warp polls; the others see it through the barrier below)
+        if (warp == 0) alive = alive && mbar_wait_sleep(&full, got & 1u);
         ++got;
         const int sh = (int)((reinterpret_cast<uintptr_t>(out) >> 2) & 3);
         const int rsh = (int)((reinterpret_cast<uintptr_t>(static_cast<const E*>(p.logits) + row * p.V + x0) / sizeof(E)) %
@@ -220,13 +243,17 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
             const int x = tid < head ? tid : end + tid - head;
             if (x < n && tid < 16) raw[x + rsh] = edge;
             if (tid * 32 < n) s_gram[1 + tid] = gram;
-            if (tid * 32 < n + 32) s_gram[1 + (n + 31) / 32] = 0u;
+            if (tid == 0) s_gram[1 + (n + 31) / 32] = 0u;
+            // positions beside the slice weigh nothing
+            const int zsh = F32 ? rsh : sh;
+            if (tid < zsh) zs[tid] = -INFINITY;
+            for (int q = zsh + n + tid; q < CAP; q += LG_THREADS) zs[q] = -INFINITY;
         }
         const bool skip = (cnt >= 1 && cnt <= p.N && i >= cnt) || err != TV_OK;
         const bool path = m != 0 && p.counts && !skip;
+        __syncthreads();
         if constexpr (!F32) {
             // bfloat16: widen into the float buffer
-            __syncthreads();
             for (int x = tid; x < n; x += LG_THREADS) zs[x + sh] = lg_float(raw[x + rsh]);
         }
         // (float32: in and out rows may be aligned differently; then the entries move first)
@@ -235,9 +262,9 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
         // ---- the path's tokens (each once) are computed before the list changes them
         float my_z = 0.f;
         const bool mine = path && my_x >= 0 && ((m >> (tid & 63)) & 1ull) && (same & m & ((1ull << (tid & 63)) - 1ull)) == 0ull;
-        if (path || !F32) __syncthreads();
+        if constexpr (!F32) __syncthreads();
         if (mine) my_z = lg_penalty(r, zr[my_x + zsh] + my_bias, my_c + __popcll(same & m));
-        __syncthreads();
+        if (path) __syncthreads();
         if (!skip && (p.counts || p.bias)) {
             auto change = [&](int x, int c, float bs) {
                 float z = zr[x + zsh] + bs;
@@ -275,21 +302,22 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
             z[k][1] = v.y;
             z[k][2] = v.z;
             z[k][3] = v.w;
-            uint32_t ok = 0xfu;
             if (p.grammar && x < n) {
                 const int w = (x + 32) >> 5;             // (s_gram[0] stands before the slice)
-                ok = __funnelshift_r(s_gram[w], s_gram[w + 1], (x + 32) & 31);
-            }
-            if (x < 0) ok &= 0xfu << -x;
-            if (x + 4 > n) ok = x >= n ? 0u : ok & (0xfu >> (x + 4 - n));
+                const uint32_t lo = s_gram[w], hi = zsh != 0 ? s_gram[w + 1] : 0u;
+                const uint32_t ok = __funnelshift_r(lo, hi, (x + 32) & 31);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (!((ok >> e) & 1u)) z[k][e] = -INFINITY;
+                for (int e = 0; e < 4; ++e)
+                    if (!((ok >> e) & 1u)) z[k][e] = -INFINITY;
+            }
             if constexpr (PROBS) mx = lg_max(mx, lg_max(lg_max(z[k][0], z[k][1]), lg_max(z[k][2], z[k][3])));
         }
         fence_proxy_async_smem();                        // the next copy lands where this row was
-        __syncthreads();
-        if (row + 1 < row_hi) fetch(row + 1);
+        if (__syncthreads_and(alive ? 1 : 0) == 0) {     // a wait ran out, in this row or the last
+            if (tid == 0) p.status[b] = TV_ERR_TIMEOUT;
+            return;
+        }
+        if (row + 1 < row_hi) fetch(row + 1, b, i + 1 < p.N);
         if (skip && err == TV_OK) continue;              // an absent node: nothing is written
         auto store = [&](float scale) {
 #pragma unroll
@@ -316,44 +344,26 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
         if constexpr (!PROBS) {
             store(r.inv_temp);
         } else {
-            // ---- softmax: over the CTA, then over the cluster (every CTA combines the slices'
-            // values in the same order)
-            auto reduce = [&](float v, bool sum, int where) -> float {
+            // ---- softmax: maximum m and sum s relative to it over the CTA's slice, then the
+            // slices' pairs are combined (by every CTA in the same order): weights 2^(m - max)
+            auto reduce = [&](float v, bool sum) -> float {
                 const float none = sum ? 0.f : -INFINITY;
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) {
                     const float y = __shfl_xor_sync(0xffffffffu, v, o);
                     v = sum ? v + y : lg_max(v, y);
                 }
-                if (lane == 0) red[where][warp] = v;
+                if (lane == 0) red[sum][warp] = v;
                 __syncthreads();
-                v = lane < LG_THREADS / 32 ? red[where][lane] : none;
+                v = lane < LG_THREADS / 32 ? red[sum][lane] : none;
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) {
                     const float y = __shfl_xor_sync(0xffffffffu, v, o);
                     v = sum ? v + y : lg_max(v, y);
                 }
-                v = __shfl_sync(0xffffffffu, v, 0);
-                if (p.slices == 1) return v;
-                // Every slice writes its value into all of them and counts the bytes on their
-                // barrier: a cluster barrier would first wait for the row before to be stored.
-                // (A slice sends its next maximum only after it has every sum, and so on: a slot
-                // is read before it is written again, and a CTA ends only with every value here.)
-                if (warp == 0) {
-                    mbar_arrive_expect_tx_relaxed_elect(&peer_bar[where], (uint32_t)p.slices * 4);
-                    __syncwarp();
-                    if (lane < p.slices) remote_st_async(&peer[where][me], &peer_bar[where], (uint32_t)lane, v);
-                }
-                alive = alive && mbar_wait(&peer_bar[where], phase);
-                v = lane < p.slices ? *reinterpret_cast<volatile float*>(&peer[where][lane]) : none;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    const float y = __shfl_xor_sync(0xffffffffu, v, o);
-                    v = sum ? v + y : lg_max(v, y);
-                }
-                return v;
+                return __shfl_sync(0xffffffffu, v, 0);
             };
-            mx = reduce(mx, false, 0);
+            mx = reduce(mx, false);
             // e^((z - max) / temperature); the shift's rounding is the same for every entry and
             // cancels in the quotient
             const float scale = LG_LOG2E * r.inv_temp;
@@ -365,16 +375,45 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
                 for (int e = 0; e < 4; ++e) z[k][e] = ex2_approx(fmaf(z[k][e], scale, base));
                 sum += (z[k][0] + z[k][1]) + (z[k][2] + z[k][3]);
             }
-            sum = reduce(sum, true, 1);
-            phase ^= 1u;
-            store(sum == 0.f ? 0.f : 1.f / sum);         // NaN stays NaN
-        }
-        if (__syncthreads_and(alive ? 1 : 0) == 0) {     // a copy or a slice's value never came
-            if (tid == 0) p.status[b] = TV_ERR_TIMEOUT;
-            if (row + 1 < row_hi) mbar_wait(&full, got & 1u);   // its own copy in flight
-            break;
+            sum = reduce(sum, true);
+            float w = 1.f;
+            if (p.slices > 1) {
+                // Every slice writes its pair into all of them and counts the bytes on their
+                // barrier: a cluster barrier would first wait for the row before to be stored.
+                // (A slice is at most one row ahead of another, as it needs the other's pair: two
+                // places are enough, and a CTA ends only with every pair here.)  One warp polls.
+                if (warp == 0) {
+                    const uint32_t par = phase & 1u;
+                    // (relaxed: a release would wait for the row before to be stored, too)
+                    mbar_arrive_expect_tx_relaxed_elect(&peer_bar, (uint32_t)p.slices * 8);
+                    __syncwarp();
+                    if (lane < p.slices) {
+                        remote_st_async(&peer[par][0][me], &peer_bar, (uint32_t)lane, mx);
+                        remote_st_async(&peer[par][1][me], &peer_bar, (uint32_t)lane, sum);
+                    }
+                    alive = alive && mbar_wait_sleep(&peer_bar, par);
+                    const float pm = lane < p.slices ? *reinterpret_cast<volatile float*>(&peer[par][0][lane]) : -INFINITY;
+                    const float ps = lane < p.slices ? *reinterpret_cast<volatile float*>(&peer[par][1][lane]) : 0.f;
+                    float top = pm;
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) top = lg_max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const float tb = top == -INFINITY ? 0.f : -top * scale;
+                    sum = ps * exp2f(fmaf(pm, scale, tb));
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (lane == 0) red[0][0] = sum == 0.f ? 0.f : exp2f(fmaf(mx, scale, tb)) / sum;
+                }
+                ++phase;
+                __syncthreads();
+                w = red[0][0];
+            } else {
+                w = sum == 0.f ? 0.f : 1.f / sum;
+            }
+            store(w);                                    // (NaN stays NaN)
         }
     }
+    // (the last row's pairs)
+    if (__syncthreads_and(alive ? 1 : 0) == 0 && tid == 0 && cur >= 0) p.status[cur] = TV_ERR_TIMEOUT;
 }
 
 template <typename E, bool PROBS, int NV>
