@@ -24,6 +24,7 @@ namespace {
 
 constexpr int CF_THREADS = 128;
 constexpr int CF_M = 64, CF_N = 64;  // rows, keys per tile
+constexpr int CF_SPLITS = 16;        // most parts that the keys are cut into
 constexpr float CF_LOG2E = 1.4426950408889634f;
 
 struct CfParams {
@@ -66,10 +67,11 @@ struct CfTile {
 };
 
 // false: no such tile.  Called by every thread (contains barriers).
-__device__ __forceinline__ bool cf_find(const CfParams& p, int tile, CfTile& t) {
+__device__ __forceinline__ bool cf_find(const CfParams& p, int tile, CfTile& t, bool& valid) {
     __shared__ ChunkLocateTmp<CF_THREADS> tmp;
     const ChunkPlace at = chunk_locate<CF_THREADS>(&tmp, p.c, [&](int64_t) { return (int64_t)tile; },
                                                    [&](int, int n) { return cf_tiles(p, n); });
+    valid = at.valid;
     if (at.b >= p.c.B) return false;
     t.b = at.b;
     t.s = p.c.q_start[at.b];
@@ -96,15 +98,15 @@ __global__ void __launch_bounds__(CF_THREADS) chunk_attn_kernel(CfParams p) {
     pdl_wait();
     const int tile_id = (int)(blockIdx.x / p.splits), split = (int)(blockIdx.x % p.splits);
     const int g = blockIdx.y;
-    const bool valid = chunk_starts_ok(p.c);
+    CfTile t;
+    bool valid;
+    const bool found = cf_find(p, tile_id, t, valid);
     if (blockIdx.x == 0 && g == 0)
         for (int b = tid; b < p.c.B; b += CF_THREADS)
             if (!valid || p.c.q_start[b] == p.c.q_start[b + 1])
                 p.status[b] = (valid && chunk_shape_ok(p.c, p.c.prefix[b], 0)) ? TV_OK
                                                                                : TV_ERR_OUT_OF_RANGE;
-    if (!valid) return;
-    CfTile t;
-    if (!cf_find(p, tile_id, t)) return;
+    if (!found) return;
     if (t.tile == 0 && g == 0 && split == 0 && tid == 0)
         p.status[t.b] = t.ok ? TV_OK : TV_ERR_OUT_OF_RANGE;
     const int r0 = t.tile * CF_M, rows = min(CF_M, t.n * p.G - r0);
@@ -273,14 +275,15 @@ __global__ void __launch_bounds__(CF_THREADS) chunk_attn_kernel(CfParams p) {
     }
 }
 
-// Joins the parts of a row tile: weights 2^(m_k - max) on the unnormalised rows.
+// Joins the parts of a row tile: weights 2^(m_k - max) on the unnormalised rows.  A
+// thread per (row, four columns); the parts' maxima and sums are loaded together, then
+// the rows, so that a part does not wait for the one before.
 template <typename E>
 __global__ void __launch_bounds__(CF_THREADS) chunk_join_kernel(CfParams p) {
-    pdl_launch_dependents();
-    pdl_wait();
-    const int g = blockIdx.y, tid = threadIdx.x;
-    if (!chunk_starts_ok(p.c)) return;
     __shared__ ChunkLocateTmp<CF_THREADS> tmp;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int g = blockIdx.y;
     const ChunkPlace at = chunk_locate<CF_THREADS>(&tmp, p.c, [&](int64_t) { return (int64_t)blockIdx.x; },
                                                    [&](int, int n) { return cf_tiles(p, n); });
     if (at.b >= p.c.B) return;
@@ -288,31 +291,40 @@ __global__ void __launch_bounds__(CF_THREADS) chunk_join_kernel(CfParams p) {
     const int r0 = ((int)blockIdx.x - (int)at.base) * CF_M, rows = min(CF_M, n * p.G - r0);
     const int64_t step = CF_M * (p.d + 2);
     const float* slot = p.part + ((int64_t)blockIdx.x * p.Hkv + g) * p.splits * step;
-    const int d4 = p.d / 4;
-    E* out = static_cast<E*>(p.out);
-    for (int e = tid; e < rows * d4; e += CF_THREADS) {
-        const int r = e / d4, c = e % d4;
-        float mx = -INFINITY;
-        for (int k = 0; k < p.splits; ++k) mx = fmaxf(mx, slot[k * step + CF_M * p.d + r]);
-        const float base = mx == -INFINITY ? 0.f : mx;
-        float den = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < p.splits; ++k) {
-            const float* pk = slot + k * step;
-            const float mk = pk[CF_M * p.d + r];
-            if (mk == -INFINITY && pk[CF_M * (p.d + 1) + r] == 0.f) continue;   // no key in this part
-            const float w = exp2f(mk - base);
-            const float4 x = *reinterpret_cast<const float4*>(pk + r * p.d + 4 * c);
-            den = fmaf(w, pk[CF_M * (p.d + 1) + r], den);
-            acc.x = fmaf(w, x.x, acc.x);
-            acc.y = fmaf(w, x.y, acc.y);
-            acc.z = fmaf(w, x.z, acc.z);
-            acc.w = fmaf(w, x.w, acc.w);
-        }
-        const float inv = den == 0.f ? 0.f : 1.f / den;
-        cf_store4(out + (int64_t)(s + (r0 + r) / p.G) * p.o_stride + (int64_t)(g * p.G + (r0 + r) % p.G) * p.d + 4 * c,
-                  make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    const int d4 = p.d / 4, e = blockIdx.z * CF_THREADS + threadIdx.x;
+    if (e >= rows * d4) return;
+    const int r = e / d4, c = e % d4;
+    float m[CF_SPLITS], w[CF_SPLITS], mx = -INFINITY, den = 0.f;
+#pragma unroll
+    for (int k = 0; k < CF_SPLITS; ++k) {
+        m[k] = k < p.splits ? slot[k * step + CF_M * p.d + r] : -INFINITY;
+        w[k] = k < p.splits ? slot[k * step + CF_M * (p.d + 1) + r] : 0.f;
     }
+#pragma unroll
+    for (int k = 0; k < CF_SPLITS; ++k) mx = fmaxf(mx, m[k]);
+    const float base = mx == -INFINITY ? 0.f : mx;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k0 = 0; k0 < CF_SPLITS; k0 += 8) {
+        float4 x[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            x[u] = k0 + u < p.splits ? *reinterpret_cast<const float4*>(slot + (k0 + u) * step + r * p.d + 4 * c)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const float f = exp2f(m[k0 + u] - base);   // (a part without a key: 0, and zero rows)
+            den = fmaf(f, w[k0 + u], den);
+            acc.x = fmaf(f, x[u].x, acc.x);
+            acc.y = fmaf(f, x[u].y, acc.y);
+            acc.z = fmaf(f, x[u].z, acc.z);
+            acc.w = fmaf(f, x[u].w, acc.w);
+        }
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    E* out = static_cast<E*>(p.out);
+    cf_store4(out + (int64_t)(s + (r0 + r) / p.G) * p.o_stride + (int64_t)(g * p.G + (r0 + r) % p.G) * p.d + 4 * c,
+              make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
 }
 
 template <typename E, int NC>
@@ -333,7 +345,8 @@ tv_status launch_nc(const CfParams& p, cudaStream_t stream) {
     LaunchCfg lc(dim3((unsigned)(p.tiles * p.splits), (unsigned)p.Hkv), dim3(CF_THREADS), smem, stream);
     if (cudaLaunchKernelEx(&lc.cfg, chunk_attn_kernel<E, NC>, p) != cudaSuccess) return TV_ERR_CUDA;
     if (p.splits == 1) return TV_OK;
-    LaunchCfg lj(dim3((unsigned)p.tiles, (unsigned)p.Hkv), dim3(CF_THREADS), 0, stream);
+    LaunchCfg lj(dim3((unsigned)p.tiles, (unsigned)p.Hkv, (unsigned)(CF_M * (p.d / 4) / CF_THREADS)),
+                 dim3(CF_THREADS), 0, stream);
     return cudaLaunchKernelEx(&lj.cfg, chunk_join_kernel<E>, p) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
 
@@ -342,7 +355,7 @@ tv_status launch_nc(const CfParams& p, cudaStream_t stream) {
 int64_t cf_tile_bound(int T, int B, int G) { return (int64_t)T * G / CF_M + std::min(T, B); }
 int cf_splits(int T, int B, int Hkv, int G) {
     const int64_t ctas = std::max<int64_t>(1, cf_tile_bound(T, B, G) * Hkv);
-    return (int)std::clamp<int64_t>(4 * device_sm_count() / ctas, 1, 16);
+    return (int)std::clamp<int64_t>(4 * device_sm_count() / ctas, 1, CF_SPLITS);
 }
 
 }  // namespace
