@@ -9,12 +9,16 @@
 // reduction, and everything behind it is float32 with one rounding to the
 // output type.
 //
-// Bound by memory: every row is read once and written once.  A CTA takes TT
-// consecutive rows; the (cos, sin) of its TT x dim/2 pairs are computed once in
-// shared memory and shared by all heads, and a thread's unit is 16 bytes of a
-// row (half layout: the two 16-byte vectors that hold a pair's columns).
+// Bound by memory: every row is read once and written once.  A CTA takes up to 16
+// consecutive rows, a warp finding and checking each; the (cos, sin) of its rows' pairs
+// are computed once in shared memory and shared by all heads.  A thread's unit is 16
+// bytes of a row (half layout: the two 16-byte vectors that hold a pair's columns), and
+// it takes the same unit of several rows, so that finding it is paid once and the rows'
+// loads are in flight together.
 #include <cuda_bf16.h>
 #include <math.h>
+
+#include <algorithm>
 
 #include "tv_chunk.cuh"
 #include "tv_internal.h"
@@ -24,7 +28,8 @@ namespace tv {
 namespace {
 
 constexpr int CA_THREADS = 256;
-constexpr int CA_TT_MAX = 8;  // rows per CTA
+constexpr int CA_TT_MAX = 16;  // rows per CTA
+constexpr int CA_PER_SM = 4;   // CTAs that an SM holds
 
 struct CaParams {
     ChunkView c;
@@ -102,17 +107,28 @@ __device__ __forceinline__ uint4 pack(const Vec<__nv_bfloat16>& x) {
 }
 
 template <typename E>
-__global__ void __launch_bounds__(CA_THREADS)
+__global__ void __launch_bounds__(CA_THREADS, CA_PER_SM)
 chunk_append_kernel(const CaParams p, const __grid_constant__ tv_rope_table rope) {
     constexpr int VE = Vec<E>::VE;
-    extern __shared__ float2 cs[];                    // [TT][dim / 2] (cos, sin)
+    extern __shared__ __align__(16) float2 cs[];      // (cos, sin), see cs_at
     __shared__ int64_t slot[CA_TT_MAX];               // first row of the slot's head 0, or -1
     __shared__ int32_t pos[CA_TT_MAX];
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_launch_dependents();
     pdl_wait();
     const int t0 = blockIdx.x * p.TT, tn = min(p.TT, p.c.T - t0);
-    const bool valid = chunk_starts_ok(p.c);
+    // q_start is checked as a whole; whoever reads a sequence that holds rows of this CTA
+    // leaves it with them
+    __shared__ int4 owner[CA_TT_MAX];                 // sequence, its first row, rows, prefix
+    if (tid < CA_TT_MAX) owner[tid] = make_int4(-1, 0, 0, 0);
+    __syncthreads();
+    bool valid = true;
+    for (int b = tid; b < p.c.B; b += CA_THREADS) {
+        const int s = p.c.q_start[b], e = p.c.q_start[b + 1], P = p.c.prefix[b];
+        valid = valid && s >= 0 && s <= e && e <= p.c.T;
+        for (int t = max(s, t0); t < min(e, t0 + tn); ++t) owner[t - t0] = make_int4(b, s, e - s, P);
+    }
+    valid = __syncthreads_and(valid ? 1 : 0) != 0;
     if (!p.checked && blockIdx.x == 0) {
         // sequences without rows (and a bad q_start) have no CTA of their own
         for (int b = tid; b < p.c.B; b += CA_THREADS)
@@ -121,46 +137,50 @@ chunk_append_kernel(const CaParams p, const __grid_constant__ tv_rope_table rope
                                                                                : TV_ERR_OUT_OF_RANGE;
     }
     if (!valid) return;
-    // the rows' sequences, one after the other (one for all rows of a long chunk)
-    int seq = -1, s_lo = 0, s_hi = 0, P = 0;
-    bool ok = false;
-    for (int r = 0; r < tn; ++r) {
-        const int t = t0 + r;
-        if (seq < 0 || t >= s_hi) {
-            if (t < p.c.q_start[0] || t >= p.c.q_start[p.c.B]) {
-                if (tid == 0) slot[r] = -1;
-                continue;
-            }
-            int lo = 0, hi = p.c.B;  // q_start[lo] <= t < q_start[hi]
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (p.c.q_start[mid] <= t) lo = mid;
-                else hi = mid;
-            }
-            seq = lo;
-            s_lo = p.c.q_start[lo];
-            s_hi = p.c.q_start[lo + 1];
-            P = p.c.prefix[lo];
+    // sequences that change within the CTA's rows
+    int changes = 0;
+    for (int r = 1; r < tn; ++r) changes += owner[r].x != owner[r - 1].x;
+    // one sequence, or two: its blocks are checked by every thread at once
+    bool whole = false, ok_first = true, ok_last = true;
+    if (!p.checked && changes <= 1) {
+        whole = true;
+        const int4 a = owner[0], z = owner[tn - 1];
+        if (a.x >= 0) ok_first = ca_seq_ok(p, a.x, a.w, a.y, a.z, tid, CA_THREADS);
+        if (z.x >= 0 && z.x != a.x) ok_last = ca_seq_ok(p, z.x, z.w, z.y, z.z, tid, CA_THREADS);
+        ok_first = __syncthreads_and(ok_first ? 1 : 0) != 0;
+        ok_last = changes == 0 ? ok_first : __syncthreads_and(ok_last ? 1 : 0) != 0;
+    }
+    for (int r = warp; r < tn; r += CA_THREADS / 32) {
+        // a warp per row: its sequence's check, its slot
+        const int t = t0 + r, b = owner[r].x, s = owner[r].y, n = owner[r].z, P = owner[r].w;
+        int64_t at = -1;
+        if (b >= 0) {
+            bool ok;
             if (p.checked) {
-                ok = p.status[lo] == TV_OK;
+                ok = p.status[b] == TV_OK;
             } else {
-                ok = __syncthreads_and(ca_seq_ok(p, lo, P, s_lo, s_hi - s_lo, tid, CA_THREADS) ? 1 : 0) != 0;
-                if (tid == 0 && t == s_lo) p.status[lo] = ok ? TV_OK : TV_ERR_OUT_OF_RANGE;
+                ok = whole ? (b == owner[0].x ? ok_first : ok_last)
+                           : __all_sync(0xffffffffu, ca_seq_ok(p, b, P, s, n, lane, 32));
+                if (lane == 0 && t == s) p.status[b] = ok ? TV_OK : TV_ERR_OUT_OF_RANGE;
             }
-        }
-        if (tid == 0) {
-            int64_t at = -1;
             if (ok) {
-                const int64_t l = (int64_t)P + (t - s_lo);
-                const int64_t blk = p.c.table[(int64_t)seq * p.c.max_blocks + l / p.c.bs];
+                const int64_t l = (int64_t)P + (t - s);
+                const int64_t blk = p.c.table[(int64_t)b * p.c.max_blocks + l / p.c.bs];
                 at = blk * p.Hkv * p.c.bs + l % p.c.bs;
-                pos[r] = p.positions ? p.positions[t] : (int)l;
+                if (lane == 0) pos[r] = p.positions ? p.positions[t] : (int)l;
             }
-            slot[r] = at;
         }
+        if (lane == 0) slot[r] = at;
     }
     __syncthreads();
     const int half = rope.dim / 2;
+    const int vec = p.d / VE;                                   // vectors per head row
+    const int rv = rope.dim / VE;                               // rotated vectors
+    const int ru = rope.interleaved ? rv : rv / 2;              // rotated units
+    const int per = rope.interleaved ? VE / 2 : VE;             // pairs of a unit
+    // Pair x of unit c of row r: the 16 bytes of two pairs lie beside the next unit's, so
+    // that lanes with consecutive units read consecutive banks.
+    auto cs_at = [&](int r, int c, int x) -> int { return ((r * (per / 2) + x / 2) * ru + c) * 2 + (x & 1); };
     for (int e = tid; e < tn * half; e += CA_THREADS) {
         const int r = e / half, j = e - r * half;
         if (slot[r] < 0) continue;
@@ -168,76 +188,91 @@ chunk_append_kernel(const CaParams p, const __grid_constant__ tv_rope_table rope
         const int64_t a = (int64_t)((uint64_t)(uint32_t)pos[r] * rope.turn[j]);
         float sn, co;
         sincospif(__ll2float_rn(a) * 1.0842021724855044e-19f, &sn, &co);  // 2^-63: half turns
-        cs[e] = make_float2(co * rope.amplitude, sn * rope.amplitude);
+        cs[cs_at(r, j / per, j % per)] = make_float2(co * rope.amplitude, sn * rope.amplitude);
     }
     __syncthreads();
     // units of a row: for each query and key head its rotated vectors (half layout:
     // pairs of them) and its copied ones, then the value vectors
-    const int vec = p.d / VE;                                   // vectors per head row
-    const int rv = rope.dim / VE;                               // rotated vectors
-    const int ru = rope.interleaved ? rv : rv / 2;              // rotated units
     const int hu = ru + vec - rv;                               // units per rotated head
     const int uq = (p.q ? p.Hq : 0) * hu, uk = uq + p.Hkv * hu, ut = uk + p.Hkv * vec;
-    for (int e = tid; e < tn * ut; e += CA_THREADS) {
-        const int r = e / ut;
-        int u = e - r * ut;
-        const int64_t at = slot[r];
-        if (at < 0) continue;
-        const int64_t t = t0 + r;
-        if (u >= uk) {
-            u -= uk;
-            const int g = u / vec, c = u - g * vec;
-            const uint4 x = *reinterpret_cast<const uint4*>(p.v + t * p.v_stride + (int64_t)u * 16);
-            *reinterpret_cast<uint4*>(p.v_cache + ((at + (int64_t)g * p.c.bs) * vec + c) * 16) = x;
-            continue;
-        }
-        const uint8_t* src;
-        uint8_t* dst;
-        int c;
-        if (u < uq) {
-            const int h = u / hu;
-            c = u - h * hu;
-            src = p.q + t * p.q_stride + (int64_t)h * vec * 16;
-            dst = p.q_out + t * p.qo_stride + (int64_t)h * vec * 16;
+    // few units: the threads also share out the rows
+    const int share = max(1, min(p.TT, CA_THREADS / ut)), mine = tid / ut;
+    const int r_first = share > 1 ? mine : 0;
+    if (share > 1 && mine >= share) return;
+    for (int e = share > 1 ? tid - mine * ut : tid; e < ut; e += share > 1 ? ut : CA_THREADS) {
+        // the unit's first vector in its head, and where the head is: in the source row, and in
+        // the output row or (so many cache rows on) in the slot
+        int h, c;
+        bool copy = true, cache = true;
+        const uint8_t* src = p.v;
+        uint8_t* dst = p.v_cache;
+        int64_t src_step = p.v_stride, dst_step = 0;
+        if (e >= uk) {
+            h = (e - uk) / vec;
+            c = e - uk - h * vec;
         } else {
-            u -= uq;
-            const int g = u / hu;
-            c = u - g * hu;
-            src = p.k + t * p.k_stride + (int64_t)g * vec * 16;
-            dst = p.k_cache + (at + (int64_t)g * p.c.bs) * vec * 16;
+            cache = e >= uq;
+            h = (cache ? e - uq : e) / hu;
+            c = (cache ? e - uq : e) - h * hu;
+            copy = c >= ru;
+            src = cache ? p.k : p.q;
+            dst = cache ? p.k_cache : p.q_out;
+            src_step = cache ? p.k_stride : p.q_stride;
+            dst_step = p.qo_stride;
+            if (copy) c += rv - ru;
         }
-        if (c >= ru) {
-            c += rv - ru;
-            *reinterpret_cast<uint4*>(dst + c * 16) = *reinterpret_cast<const uint4*>(src + c * 16);
-            continue;
-        }
-        const float2* row = cs + r * half;
-        if (rope.interleaved) {
-            Vec<E> x;
-            unpack(*reinterpret_cast<const uint4*>(src + c * 16), x);
+        src += (int64_t)t0 * src_step + ((int64_t)h * vec + c) * 16;
+        dst += cache ? ((int64_t)h * p.c.bs * vec + c) * 16 : (int64_t)t0 * dst_step + ((int64_t)h * vec + c) * 16;
+        const bool two = !copy && !rope.interleaved;            // two vectors
+        // the unit of up to ROWS rows at a time, their loads in flight together
+        constexpr int ROWS = 2;
+        for (int rb = r_first; rb < tn; rb += ROWS * share) {
+            uint4 x[ROWS], y[ROWS];
+            int64_t at[ROWS];
 #pragma unroll
-            for (int i = 0; i < VE; i += 2) {
-                const float2 w = row[(c * VE + i) / 2];
-                const float a = x.f[i], b = x.f[i + 1];
-                x.f[i] = a * w.x - b * w.y;
-                x.f[i + 1] = b * w.x + a * w.y;
+            for (int k = 0; k < ROWS; ++k) {
+                const int r = rb + k * share;
+                at[k] = r < tn ? slot[r] : -1;
+                if (at[k] < 0) continue;
+                x[k] = __ldcs(reinterpret_cast<const uint4*>(src + r * src_step));
+                if (two) y[k] = __ldcs(reinterpret_cast<const uint4*>(src + r * src_step + ru * 16));
             }
-            *reinterpret_cast<uint4*>(dst + c * 16) = pack(x);
-        } else {
-            Vec<E> x, y;
-            const uint4 ux = *reinterpret_cast<const uint4*>(src + c * 16);
-            const uint4 uy = *reinterpret_cast<const uint4*>(src + (c + ru) * 16);
-            unpack(ux, x);
-            unpack(uy, y);
 #pragma unroll
-            for (int i = 0; i < VE; ++i) {
-                const float2 w = row[c * VE + i];
-                const float a = x.f[i], b = y.f[i];
-                x.f[i] = a * w.x - b * w.y;
-                y.f[i] = b * w.x + a * w.y;
+            for (int k = 0; k < ROWS; ++k) {
+                if (at[k] < 0) continue;
+                const int r = rb + k * share;
+                uint8_t* to = dst + (cache ? at[k] * vec * 16 : r * dst_step);
+                if (!copy) {
+                    Vec<E> a;
+                    unpack(x[k], a);
+                    if (two) {
+                        Vec<E> b;
+                        unpack(y[k], b);
+#pragma unroll
+                        for (int i = 0; i < VE; i += 2) {
+                            const float4 w = *reinterpret_cast<const float4*>(cs + cs_at(r, c, i));
+                            const float a0 = a.f[i], b0 = b.f[i], a1 = a.f[i + 1], b1 = b.f[i + 1];
+                            a.f[i] = a0 * w.x - b0 * w.y;
+                            b.f[i] = b0 * w.x + a0 * w.y;
+                            a.f[i + 1] = a1 * w.z - b1 * w.w;
+                            b.f[i + 1] = b1 * w.z + a1 * w.w;
+                        }
+                        *reinterpret_cast<uint4*>(to + ru * 16) = pack(b);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < VE; i += 4) {
+                            const float4 w = *reinterpret_cast<const float4*>(cs + cs_at(r, c, i / 2));
+                            const float a0 = a.f[i], b0 = a.f[i + 1], a1 = a.f[i + 2], b1 = a.f[i + 3];
+                            a.f[i] = a0 * w.x - b0 * w.y;
+                            a.f[i + 1] = b0 * w.x + a0 * w.y;
+                            a.f[i + 2] = a1 * w.z - b1 * w.w;
+                            a.f[i + 3] = b1 * w.z + a1 * w.w;
+                        }
+                    }
+                    x[k] = pack(a);
+                }
+                *reinterpret_cast<uint4*>(to) = x[k];
             }
-            *reinterpret_cast<uint4*>(dst + c * 16) = pack(x);
-            *reinterpret_cast<uint4*>(dst + (c + ru) * 16) = pack(y);
         }
     }
 }
@@ -262,16 +297,17 @@ tv_status launch_chunk_append(const ChunkAppendArgs& a) {
     p.Hq = a.Hq;
     p.Hkv = a.Hkv;
     p.d = a.d;
-    // rows per CTA: as many as still give every SM four CTAs
-    p.TT = 1;
-    while (p.TT < CA_TT_MAX && (int64_t)a.T >= (int64_t)8 * p.TT * device_sm_count()) p.TT *= 2;
+    // rows per CTA: one wave of CTAs while they are at most CA_TT_MAX (their start, two round
+    // trips to memory, is not repeated then)
+    const int wave = CA_PER_SM * device_sm_count();
+    p.TT = std::min(CA_TT_MAX, std::max(1, (a.T + wave - 1) / wave));
     const unsigned grid = (unsigned)((a.T + p.TT - 1) / p.TT);
     // Every CTA of a sequence checks all of the sequence's blocks, so that a bad one
     // is left untouched; for long inputs that would be read too often, and a
     // kernel of one CTA per sequence does it first.
-    p.checked = a.T > 2048 || grid == 0;
+    p.checked = a.T > 32768 || grid == 0;
     if (p.checked) {
-        LaunchCfg lc(dim3((unsigned)min(a.B, 65535)), dim3(CA_THREADS), 0, a.stream);
+        LaunchCfg lc(dim3((unsigned)std::min(a.B, 65535)), dim3(CA_THREADS), 0, a.stream);
         if (cudaLaunchKernelEx(&lc.cfg, chunk_check_kernel, p) != cudaSuccess) return TV_ERR_CUDA;
         if (grid == 0) return TV_OK;
     }

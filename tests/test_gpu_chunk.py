@@ -361,9 +361,9 @@ def test_append(tv, dtype, rope, shape):
     assert torch.equal(kc[keep], c["k_cache"][keep])
 
 
-@pytest.mark.parametrize("T", [700, 5000])
+@pytest.mark.parametrize("T", [700, 5000, 33000])
 def test_append_long_and_positions(tv, T):
-    """More rows than a CTA, and (5000) than the limit from which a kernel checks first;
+    """More rows than a CTA, and (33000) than the limit from which a kernel checks first;
     positions of their own."""
     n, P = [T - 300, 300], [11, 4000]
     rope = dict(dim=64, theta=500000.0)
@@ -378,7 +378,7 @@ def test_append_long_and_positions(tv, T):
     assert ((kc.double() - k).abs() <= rope_tolerance(k, 64, torch.bfloat16, 1 << 30)).all()
 
 
-@pytest.mark.parametrize("T", [60, 4000])
+@pytest.mark.parametrize("T", [60, 4000, 33000])
 def test_append_bad_sequences_stay_untouched(tv, T):
     n, P = [20, T - 45, 0, 5, 10, 10], [3, 40, 1, 7, 12, 500]
     c = append_case(n, P, Hq=2, Hkv=1, d=64, bs=16, dtype=torch.bfloat16, seed=T)
