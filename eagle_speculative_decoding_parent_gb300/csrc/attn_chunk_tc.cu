@@ -410,7 +410,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     auto* tmp = reinterpret_cast<ChunkLocateTmp<THREADS>*>(smem + L::OFF_RING);  // before the first copy
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
-    int* seq_ok = reinterpret_cast<int*>(smem + L::OFF_MISC + 8);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = smem_u32(smem);
@@ -462,27 +461,28 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     // ---- this CTA's run
     Runs runs;
     int64_t x_lo = 0, x_hi = 0;
-    const ChunkPlace at = chunk_locate<THREADS>(tmp, p.c, [&](int64_t total) {
+    auto where = [&](int64_t total) {
         runs = runs_of(p, total, gridDim.x);
         x_lo = run_start(runs, blockIdx.x);
         x_hi = run_start(runs, blockIdx.x + 1);
         return x_lo < x_hi ? x_lo : total;
-    }, [&](int P, int n) { return seq_units(p, P, n); });
+    };
+    auto units = [&](int P, int n) { return seq_units(p, P, n); };
+    const ChunkPlace at = p.c.B <= 32 ? chunk_locate_warp(p.c, where, units)
+                                      : chunk_locate<THREADS>(tmp, p.c, where, units);
     if (blockIdx.x == 0)
         for (int b = tid; b < p.c.B; b += THREADS)
             if (!at.valid || p.c.q_start[b] == p.c.q_start[b + 1])
                 p.status[b] = (at.valid && chunk_shape_ok(p.c, p.c.prefix[b], 0)) ? TV_OK : TV_ERR_OUT_OF_RANGE;
     Seq s0{};
+    bool ok0 = false;
     if (at.b < p.c.B) {
         // the first sequence's blocks, by every thread at once
-        s0 = seq_of(p, p.c.prefix[at.b], p.c.q_start[at.b + 1] - p.c.q_start[at.b]);
-        const bool ok = s0.shape && chunk_blocks_ok(p.c, at.b, chunk_first_key(s0.P, p.window),
-                                                    (int64_t)s0.P + s0.n, tid, THREADS);
-        const int all = __syncthreads_and(ok ? 1 : 0);
-        if (tid == 0) *seq_ok = all;
+        s0 = seq_of(p, at.P, at.n);
+        ok0 = s0.shape && chunk_blocks_ok(p.c, at.b, chunk_first_key(s0.P, p.window), (int64_t)s0.P + s0.n, tid, THREADS);
     }
     fence_proxy_async_smem();  // the ring's first bytes held the search's scratch
-    __syncthreads();
+    ok0 = __syncthreads_and(ok0 ? 1 : 0) != 0;
 
     // Work item k, from the queue; false at the end (or after a timeout).
     auto take = [&](uint32_t k, Item& it) -> bool {
@@ -520,7 +520,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         if (at.b < p.c.B) {
             int b = at.b, g, qk;
             Seq s = s0;
-            bool ok = *seq_ok != 0;
+            bool ok = ok0;
+            int row = at.row;
             int64_t start, x = x_lo;
             item_at(p, s, x_lo - at.base, g, qk, start);
             start += at.base;
@@ -540,7 +541,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     it.g = g;
                     it.P = s.P;
                     it.ntok = i1 - it.i0;
-                    it.row0 = p.c.q_start[b] + it.i0;
+                    it.row0 = row + it.i0;
                     it.slot = whole ? -1 : 2 * (int)blockIdx.x + (it.t_lo == 0 ? 1 : 0);
                     it.n = ok ? it.t_hi - it.t_lo : 0;
                     it.flags = (it.ntok > p.npt ? ITEM_TWO : 0) | (ok ? 0 : ITEM_BAD) |
@@ -565,7 +566,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 int n = 0;
                 do {
                     ++b;
-                    n = p.c.q_start[b + 1] - p.c.q_start[b];
+                    row = p.c.q_start[b];
+                    n = p.c.q_start[b + 1] - row;
                 } while (n == 0 && b + 1 < p.c.B);
                 s = seq_of(p, p.c.prefix[b], n);
                 ok = s.shape && chunk_blocks_ok(p.c, b, chunk_first_key(s.P, p.window),

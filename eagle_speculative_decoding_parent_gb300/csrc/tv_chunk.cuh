@@ -65,6 +65,7 @@ struct ChunkPlace {
     int64_t base;   // first unit of sequence b
     int b;          // B when x >= total, or when q_start is not valid
     bool valid;     // q_start is non-decreasing within [0, T]
+    int row, n, P;  // sequence b's first row, rows, prefix
 };
 
 template <int THREADS>
@@ -122,6 +123,47 @@ __device__ __forceinline__ ChunkPlace chunk_locate(ChunkLocateTmp<THREADS>* tmp,
     __syncthreads();
     r.b = tmp->found_b;
     r.base = r.b < c.B ? tmp->found_base : r.total;
+    r.row = r.n = r.P = 0;
+    if (r.b < c.B) {
+        r.row = c.q_start[r.b];
+        r.n = c.q_start[r.b + 1] - r.row;
+        r.P = c.prefix[r.b];
+    }
+    return r;
+}
+
+// The same for at most 32 sequences, by each warp for itself: one round trip to memory
+// and no barrier, for calls whose start is most of their time.
+template <class Where, class Cost>
+__device__ __forceinline__ ChunkPlace chunk_locate_warp(const ChunkView& c, Where where, Cost cost) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = 0, P = 0;
+    bool ok = true;
+    if (lane < c.B) {
+        const int hi = c.q_start[lane + 1];
+        lo = c.q_start[lane];
+        P = c.prefix[lane];
+        n = hi - lo;
+        ok = lo >= 0 && lo <= hi && hi <= c.T;
+    }
+    ChunkPlace r;
+    r.valid = __all_sync(0xffffffffu, ok);
+    const int64_t s = lane < c.B && ok ? cost(P, n) : 0;
+    int64_t incl = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    r.total = __shfl_sync(0xffffffffu, incl, 31);
+    const int64_t x = where(r.total), at = incl - s;
+    const uint32_t here = __ballot_sync(0xffffffffu, r.valid && x >= at && x < incl);
+    const int b = here ? __ffs(here) - 1 : 0;
+    r.b = here ? b : c.B;
+    r.base = __shfl_sync(0xffffffffu, at, b);
+    r.row = __shfl_sync(0xffffffffu, lo, b);
+    r.n = __shfl_sync(0xffffffffu, n, b);
+    r.P = __shfl_sync(0xffffffffu, P, b);
     return r;
 }
 
