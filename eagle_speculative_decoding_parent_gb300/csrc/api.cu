@@ -419,7 +419,8 @@ tv_status chunk_attention(const void* q, int64_t q_stride, const void* k_cache,
     a.num_blocks = num_blocks;
     a.dt = dt;
     a.scale = (scale > 0.f && isfinite(scale)) ? scale : 1.0f / sqrtf((float)d);
-    a.softcap = softcap > 0.f ? softcap : 0.f;
+    // (a cap of 1e30 changes no score by as much as its rounding)
+    a.softcap = softcap > 0.f && softcap < 1e30f ? softcap : 0.f;
     a.window = window > 0 ? window : 0;
     a.out = out;
     a.out_stride = out_stride;

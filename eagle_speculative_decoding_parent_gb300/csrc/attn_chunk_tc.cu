@@ -47,6 +47,7 @@
 // Every wait is bounded; one that runs out sets the abort flag, and the roles
 // leave after their copies and products in flight are done.
 #include <algorithm>
+#include <cmath>
 
 #include "tv_chunk.cuh"
 #include "tv_internal.h"
@@ -124,7 +125,16 @@ struct Params {
     int prows;                   // rows of a partial result: 128 or 256
     float scale_log2;            // scale * log2(e); with a cap: 2 log2(e) scale / cap
     float cap_log2;              // cap * log2(e)
+    float cap_x, cap_small;      // scale / cap; products with s^2 < cap_small take the polynomial
+    float cap_c[3];              // its coefficients in s^2: scale * log2(e) * (scale / cap)^(2e) * TANH_C[e]
 };
+
+// tanh(x) / x as a polynomial in x^2 for |x| <= 0.35: interpolated at the Chebyshev nodes of
+// [0, 0.35^2] (its nearest pole is at x^2 = -pi^2 / 4), off by at most 2.9e-6 of itself, below
+// a float32 dot product's bound and a thousandth of a weight's rounding for scores up to 100.
+// One term more costs 2.6 us of 41 (2,100 tokens of 16 heads of 64, window 1024).
+constexpr double TANH_SMALL = 0.35;
+constexpr double TANH_C[3] = {0.9999971183259196, -0.3329087359461761, 0.12394375936950675};
 
 // ------------------------------------------------------------ the run space
 // Sequence of n rows after P keys: items of m = 2 npt tokens, item k costing C0 +
@@ -360,8 +370,7 @@ __device__ __noinline__ void add_noted(const Params& p, const Item& it, const ui
                 float s = 0.f;
 #pragma unroll 1
                 for (int c = 0; c < D; ++c) s = fmaf(__bfloat162float(q[c]), __bfloat162float(p.k[krow + c]), s);
-                s *= p.scale_log2;
-                if (CAP) s = p.cap_log2 * (1.f - 2.f / (1.f + exp2f(s)));
+                s = CAP ? p.cap_log2 * tanhf(s * p.cap_x) : s * p.scale_log2;
                 w = exp2f(s - m);
             }
             __syncwarp();
@@ -911,21 +920,53 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     continue;
                 }
                 float sv[KT];
-                {
+                auto load_s = [&]() {
                     uint32_t r[KT / 32][32];
 #pragma unroll
                     for (int c = 0; c < KT / 32; ++c) tmem_ld32(tS + c * 32, r[c]);
                     tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < KT; ++c) sv[c] = __uint_as_float(r[c / 32][c % 32]);
-                }
+                };
+                load_s();
                 const int t = it.t_lo + j;
                 if constexpr (CAP) {
-                    // cap tanh(x) = cap (1 - 2 / (1 + e^(2x))), in units of log 2
+                    // cap tanh(scale s / cap), in units of log 2.  An exponential and a reciprocal
+                    // more per score would bind on the special function unit, so arguments up to
+                    // 0.35 take a polynomial, two scores per instruction; S is read again where it
+                    // turns out that one of the warp's is larger.
+                    float big[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int c = 0; c < KT; ++c) {
-                        const float e = ex2_approx(sv[c] * p.scale_log2);
-                        sv[c] = fmaf(-2.f * p.cap_log2, rcp_approx(1.f + e), p.cap_log2);
+                    for (int c = 0; c < KT; c += 2) {
+                        const uint64_t x = f2_pack(sv[c], sv[c + 1]), u = f2_mul(x, x);
+                        uint64_t y = f2_pack(p.cap_c[2], p.cap_c[2]);
+#pragma unroll
+                        for (int e = 1; e >= 0; --e) y = f2_fma(y, u, f2_pack(p.cap_c[e], p.cap_c[e]));
+                        f2_unpack(f2_mul(x, y), sv[c], sv[c + 1]);
+                        float ua, ub;
+                        f2_unpack(u, ua, ub);
+                        big[(c >> 1) & 3] = fmax3(big[(c >> 1) & 3], ua, ub);
+                    }
+                    if (__any_sync(0xffffffffu, mine && !(fmaxf(fmax3(big[0], big[1], big[2]), big[3]) < p.cap_small))) {
+                        // cap (1 - 2 / (1 + e^(2x))) for those that are, in place and rolled: the
+                        // instruction cache is for the other path
+#pragma unroll 1
+                        for (int c = 0; c < KT; c += 16) {
+                            uint32_t r[16];
+                            tmem_ld16(tS + c, r);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const float x = __uint_as_float(r[e]), u = x * x;
+                                const float w = ex2_approx(x * p.scale_log2);
+                                const float y = fmaf(-2.f * p.cap_log2, rcp_approx(1.f + w), p.cap_log2);
+                                r[e] = __float_as_uint(
+                                    u < p.cap_small ? x * fmaf(fmaf(p.cap_c[2], u, p.cap_c[1]), u, p.cap_c[0]) : y);
+                            }
+                            tmem_st16(tS + c, r);
+                        }
+                        tmem_wait_st();
+                        load_s();
                     }
                 }
                 if (t < it.fa || t >= it.fb) {
@@ -1308,6 +1349,14 @@ tv_status launch_chunk_attn_tc(const ChunkAttnArgs& a) {
     p.prows = partial_rows(a.T, G);
     p.scale_log2 = a.softcap > 0.f ? 2.f * LOG2E * a.scale / a.softcap : a.scale * LOG2E;
     p.cap_log2 = a.softcap * LOG2E;
+    if (a.softcap > 0.f) {
+        const double k = (double)a.scale / a.softcap;
+        p.cap_x = (float)k;
+        for (int e = 0; e < 3; ++e) p.cap_c[e] = (float)(TANH_C[e] * a.scale * 1.4426950408889634 * pow(k, 2 * e));
+        // (scale / cap)^6 has to be a normal number, or x small enough not to need it; s^2 finite
+        const double small = k > 1e5 ? 0.0 : std::min((k < 1e-6 ? 1e-3 : TANH_SMALL) / k, 1e18);
+        p.cap_small = (float)(small * small);
+    }
     // one CTA per SM; fewer when even the longest sequences that fit give fewer runs
     const int64_t items = (int64_t)a.Hkv * (a.T / (2 * npt) + std::min(a.T, a.B));
     const int64_t units = items * std::min<int64_t>((int64_t)a.max_blocks * a.bs + C0, 1ll << 31);

@@ -73,6 +73,16 @@ def test_attention_window_and_cap(tv, dtype, window, cap):
         check(tv, c, window=window, softcap=cap)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cap", [1e-30, 0.01, 3.0, 1000.0, 1e6, 1e20, 1e31])
+def test_attention_caps_of_any_size(tv, dtype, cap):
+    """Scores far below, around and far above the cap, in the same tile."""
+    for heads, d in (((4, 2), 64), ((4, 1), 128)):
+        c = R.cache_case([150, 1], [100, 300], Hq=heads[0], Hkv=heads[1], d=d, bs=16, dtype=dtype, seed=5)
+        c["q"] *= torch.tensor([0.1, 1.0, 4.0])[torch.arange(151) % 3][:, None, None].to(dtype)
+        check(tv, c, softcap=cap)
+
+
 @pytest.mark.parametrize("d", [32, 96, 160, 224, 256])
 def test_attention_f32_head_sizes(tv, d):
     check(tv, R.cache_case([70, 1], [33, 400], Hq=4, Hkv=2, d=d, bs=8, dtype=torch.float32, seed=d))
