@@ -388,54 +388,70 @@ def rope_table(dim, *, theta: float = 10000.0, interleaved: bool = False, scalin
     return t
 
 
-def _row_stride(t, dtype, name, heads, d, T):
-    """[T, heads, d] with contiguous heads and any row stride: the stride, in elements."""
+def _fault(t, dtype, name, shape, dev):
+    """Raises what is wrong with a tensor that failed a check of _arg or _rows."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != (T, heads, d):
-        raise ValueError(f"{name}: expected shape {(T, heads, d)}, got {tuple(t.shape)}")
-    s = t.stride()
-    if (d > 1 and s[2] != 1) or (heads > 1 and s[1] != d):
-        raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return s[0] if T > 1 else heads * d
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: tensors passed to libtreeverify must live on the current CUDA device")
+    raise ValueError(f"{name}: tensors passed to libtreeverify must be contiguous")
 
 
-def _raw_stream(stream, *tensors):
-    """The stream to launch on, after a check that the tensors live on the current device
-    (the library launches there).  The raw-stream query instead of torch's Stream object: that
-    costs more than the rest of a small call's marshalling."""
-    dev = torch._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors passed to libtreeverify must live on the current CUDA device")
+def _arg(t, dtype, name, shape, dev):
+    """Address of a contiguous tensor of this type and shape on device dev; None for None.
+    (One call per tensor: the marshalling of a small call costs as much as its kernel.)"""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _fault(t, dtype, name, shape, dev)
+
+
+def _rows(t, dtype, name, shape, dev):
+    """Address and row stride, in elements, of [T, heads, d] with contiguous heads and rows any
+    stride apart."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+            if t.is_contiguous():
+                return t.data_ptr(), shape[1] * shape[2]
+            s = t.stride()
+            if (s[2] == 1 or shape[2] == 1) and (s[1] == shape[2] or shape[1] == 1):
+                return t.data_ptr(), (s[0] if shape[0] > 1 else shape[1] * shape[2])
+            raise ValueError(f"{name}: the heads of a row must be contiguous")
+    except AttributeError:
+        pass
+    _fault(t, dtype, name, shape, dev)
+
+
+def _stream_of(stream, dev):
+    """The raw-stream query instead of torch's Stream object: that costs more than the rest of a
+    small call's marshalling."""
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _dense(t, name):
-    """Address of a tensor whose type and shape are checked, None for None."""
-    if t is None:
-        return None
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: tensors passed to libtreeverify must be contiguous")
-    return t.data_ptr()
-
-
-def _paged(k_cache, v_cache, block_table, q_start, prefix_lens, status, dtype, Hkv, d):
-    """Checks shared by the chunk calls; returns (B, block size, blocks)."""
-    if k_cache.dim() != 4 or k_cache.shape[1] != Hkv or k_cache.shape[3] != d:
+def _paged(k_cache, v_cache, block_table, q_start, prefix_lens, status, dtype, Hkv, d, dev):
+    """Checks shared by the chunk calls; returns (B, block size, blocks) and the addresses in
+    the order of the arguments."""
+    ks, ts = k_cache.shape, block_table.shape
+    if len(ks) != 4 or ks[1] != Hkv or ks[3] != d:
         raise ValueError("the caches are [num_blocks, Hkv, block_size, d]")
-    _want(k_cache, dtype, "k_cache")
-    _want(v_cache, dtype, "v_cache", k_cache.shape)
-    _want(status, torch.int32, "status")
     B = status.shape[0] if status.dim() == 1 else -1
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    if len(ts) != 2 or ts[0] != B:
         raise ValueError("block_table is int32 [B, max_blocks_per_seq], status int32 [B]")
-    _want(block_table, torch.int32, "block_table")
-    _want(q_start, torch.int32, "q_start", (B + 1,))
-    _want(prefix_lens, torch.int32, "prefix_lens", (B,))
-    return B, k_cache.shape[2], k_cache.shape[0]
+    i32 = torch.int32
+    return (B, ks[2], ks[0], _arg(k_cache, dtype, "k_cache", ks, dev),
+            _arg(v_cache, dtype, "v_cache", ks, dev),
+            _arg(block_table, i32, "block_table", ts, dev),
+            _arg(q_start, i32, "q_start", (B + 1,), dev),
+            _arg(prefix_lens, i32, "prefix_lens", (B,), dev),
+            _arg(status, i32, "status", (B,), dev))
 
 
 def chunk_kv_append(q, k, v, k_cache, v_cache, block_table, q_start, prefix_lens, status, *,
@@ -444,38 +460,34 @@ def chunk_kv_append(q, k, v, k_cache, v_cache, block_table, q_start, prefix_lens
     [T,Hq,d], rows any stride apart; queries and keys rotated by ``rope`` (a RopeTable, or
     None); q_out [T,Hq,d] (default: q in place); positions int32 [T] or None (prefix + row);
     q_start int32 [B+1]; caches [num_blocks,Hkv,bs,d]; prefix_lens, status int32 [B]."""
-    if k.dim() != 3:
+    shape = k.shape
+    if len(shape) != 3:
         raise ValueError("k is [T, Hkv, d]")
-    T, Hkv, d = k.shape
+    T, Hkv, d = shape
+    dtype = k.dtype
     dt = _dtype_code(k)
-    ks = _row_stride(k, k.dtype, "k", Hkv, d, T)
-    vs = _row_stride(v, k.dtype, "v", Hkv, d, T)
-    Hq, qs, qos = 1, 0, 0
+    dev = torch._C._cuda_getDevice()
+    k_at, ks = _rows(k, dtype, "k", shape, dev)
+    v_at, vs = _rows(v, dtype, "v", shape, dev)
+    Hq, q_at, qs, q_out_at, qos = 1, None, 0, None, 0
     if q is not None:
-        if q.dim() != 3:
+        q_shape = q.shape
+        if len(q_shape) != 3 or q_shape[0] != T or q_shape[2] != d:
             raise ValueError("q is [T, Hq, d]")
-        Hq = q.shape[1]
-        q_out = q if q_out is None else q_out
-        qs = _row_stride(q, k.dtype, "q", Hq, d, T)
-        qos = _row_stride(q_out, k.dtype, "q_out", Hq, d, T)
+        Hq = q_shape[1]
+        q_at, qs = _rows(q, dtype, "q", q_shape, dev)
+        q_out_at, qos = (q_at, qs) if q_out is None else _rows(q_out, dtype, "q_out", q_shape, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    B, bs, blocks = _paged(k_cache, v_cache, block_table, q_start, prefix_lens, status, k.dtype,
-                           Hkv, d)
-    if positions is not None:
-        _want(positions, torch.int32, "positions", (T,))
+    B, bs, blocks, kc, vc, table, start, prefix, st = _paged(
+        k_cache, v_cache, block_table, q_start, prefix_lens, status, dtype, Hkv, d, dev)
     if rope is not None and not isinstance(rope, RopeTable):
         raise TypeError("rope: expected a RopeTable")
-    s = _raw_stream(stream, q, k, v, q_out, k_cache, v_cache, block_table, q_start, prefix_lens,
-                    status, positions)
-    _check(_chunk_append(None if q is None else q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(),
-                         vs, _dense(positions, "positions"), T, _dense(q_start, "q_start"),
-                         _dense(prefix_lens, "prefix_lens"), B, Hq, Hkv, d,
-                         None if rope is None else ctypes.addressof(rope),
-                         None if q is None else q_out.data_ptr(), qos, _dense(k_cache, "k_cache"),
-                         _dense(v_cache, "v_cache"), _dense(block_table, "block_table"),
-                         block_table.shape[1], bs, blocks, dt, _dense(status, "status"), s),
-           "chunk_kv_append")
+    _check(_chunk_append(q_at, qs, k_at, ks, v_at, vs,
+                         _arg(positions, torch.int32, "positions", (T,), dev), T, start, prefix, B,
+                         Hq, Hkv, d, None if rope is None else ctypes.addressof(rope), q_out_at,
+                         qos, kc, vc, table, block_table.shape[1], bs, blocks, dt, st,
+                         _stream_of(stream, dev)), "chunk_kv_append")
 
 
 def chunk_attention_workspace(T, B, Hq, Hkv, d, dtype=torch.bfloat16) -> int:
@@ -490,24 +502,25 @@ def chunk_attention(q, k_cache, v_cache, block_table, q_start, prefix_lens, out,
     q_start int32 [B+1]; prefix_lens, status int32 [B]; softcap > 0 caps the scores, window > 0
     limits the keys of a token to itself and the window - 1 before it; workspace uint8 of
     chunk_attention_workspace() bytes."""
-    if q.dim() != 3 or k_cache.dim() != 4:
+    shape = q.shape
+    if len(shape) != 3 or k_cache.dim() != 4:
         raise ValueError("q is [T, Hq, d] and the caches [num_blocks, Hkv, block_size, d]")
-    T, Hq, d = q.shape
+    T, Hq, d = shape
     Hkv = k_cache.shape[1]
+    dtype = q.dtype
     dt = _dtype_code(q)
-    qs = _row_stride(q, q.dtype, "q", Hq, d, T)
-    os_ = _row_stride(out, q.dtype, "out", Hq, d, T)
-    B, bs, blocks = _paged(k_cache, v_cache, block_table, q_start, prefix_lens, status, q.dtype,
-                           Hkv, d)
-    s = _raw_stream(stream, q, k_cache, v_cache, block_table, q_start, prefix_lens, out, status,
-                    workspace)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_chunk_attn(q.data_ptr(), qs, _dense(k_cache, "k_cache"), _dense(v_cache, "v_cache"),
-                       _dense(block_table, "block_table"), block_table.shape[1],
-                       _dense(q_start, "q_start"), _dense(prefix_lens, "prefix_lens"), T, B, Hq,
-                       Hkv, d, bs, blocks, dt, scale, softcap, window, out.data_ptr(), os_,
-                       _dense(status, "status"), _dense(workspace, "workspace"), ws_bytes, s),
-           "chunk_attention")
+    dev = torch._C._cuda_getDevice()
+    q_at, qs = _rows(q, dtype, "q", shape, dev)
+    out_at, os_ = _rows(out, dtype, "out", shape, dev)
+    B, bs, blocks, kc, vc, table, start, prefix, st = _paged(
+        k_cache, v_cache, block_table, q_start, prefix_lens, status, dtype, Hkv, d, dev)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws_bytes = workspace.nbytes
+        ws = _arg(workspace, workspace.dtype, "workspace", workspace.shape, dev)
+    _check(_chunk_attn(q_at, qs, kc, vc, table, block_table.shape[1], start, prefix, T, B, Hq, Hkv,
+                       d, bs, blocks, dt, scale, softcap, window, out_at, os_, st, ws, ws_bytes,
+                       _stream_of(stream, dev)), "chunk_attention")
 
 
 def token_counts_update(counts, tokens, status, *, starts=None, clear: bool = False,
@@ -515,23 +528,23 @@ def token_counts_update(counts, tokens, status, *, starts=None, clear: bool = Fa
     """Token histories counts int32 [B,V] (bit 31: in the prompt; below: times emitted):
     tokens int32, [total] with starts int32 [B+1], or [B,W] without (-1 entries are skipped);
     clear zeroes the rows first; prompt marks instead of counting; status int32 [B]."""
-    _want(counts, torch.int32, "counts")
-    if counts.dim() != 2:
+    shape = counts.shape
+    if len(shape) != 2:
         raise ValueError("counts is int32 [B, V]")
-    B, V = counts.shape
-    _want(tokens, torch.int32, "tokens")
+    B, V = shape
+    i32 = torch.int32
+    dev = torch._C._cuda_getDevice()
+    words = tokens.shape
     if starts is None:
-        if tokens.dim() != 2 or tokens.shape[0] != B:
+        if len(words) != 2 or words[0] != B:
             raise ValueError("tokens is int32 [B, W], or [total] with starts")
-    else:
-        _want(starts, torch.int32, "starts", (B + 1,))
-        if tokens.dim() != 1:
-            raise ValueError("tokens is int32 [total] with starts")
-    _want(status, torch.int32, "status", (B,))
-    s = _raw_stream(stream, counts, tokens, starts, status)
-    _check(_token_counts(_dense(counts, "counts"), _dense(tokens, "tokens"),
-                         _dense(starts, "starts"), tokens.numel(), B, V, int(bool(clear)),
-                         int(bool(prompt)), _dense(status, "status"), s), "token_counts_update")
+    elif len(words) != 1:
+        raise ValueError("tokens is int32 [total] with starts")
+    _check(_token_counts(_arg(counts, i32, "counts", shape, dev), _arg(tokens, i32, "tokens", words, dev),
+                         _arg(starts, i32, "starts", (B + 1,), dev), tokens.numel(), B, V,
+                         1 if clear else 0, 1 if prompt else 0,
+                         _arg(status, i32, "status", (B,), dev), _stream_of(stream, dev)),
+           "token_counts_update")
 
 
 def tree_logits_process(logits, out, status, *, probs: bool, mask=None, draft_tokens=None,
@@ -542,29 +555,23 @@ def tree_logits_process(logits, out, status, *, probs: bool, mask=None, draft_to
     [B,V], the penalties float32 [B] for tokens of the history (counts int32 [B,V]) and of
     each node's path (mask int64 [B,N], draft_tokens int32 [B,N]), the temperature float32 [B]
     and the grammar bits int32 [B,N,ceil(V/32)]; all of them optional; status int32 [B]."""
-    if logits.dim() != 3:
+    shape = logits.shape
+    if len(shape) != 3:
         raise ValueError("logits is [B, N, V]")
-    B, N, V = logits.shape
+    B, N, V = shape
     dt = _dtype_code(logits)
-    _want(out, torch.float32, "out", (B, N, V))
-    _want(status, torch.int32, "status", (B,))
-    for t, n, dtype, shape in ((mask, "mask", torch.int64, (B, N)),
-                               (draft_tokens, "draft_tokens", torch.int32, (B, N)),
-                               (counts, "counts", torch.int32, (B, V)),
-                               (bias, "bias", torch.float32, (B, V)),
-                               (grammar, "grammar", torch.int32, (B, N, (V + 31) // 32)),
-                               (repetition, "repetition", torch.float32, (B,)),
-                               (frequency, "frequency", torch.float32, (B,)),
-                               (presence, "presence", torch.float32, (B,)),
-                               (temperature, "temperature", torch.float32, (B,))):
-        if t is not None:
-            _want(t, dtype, n, shape)
-    s = _raw_stream(stream, logits, out, status, mask, draft_tokens, counts, bias, grammar,
-                    repetition, frequency, presence, temperature, node_counts)
-    _check(_tree_logits(_dense(logits, "logits"), dt, B, N, V, _counts(node_counts, B),
-                        _dense(mask, "mask"), _dense(draft_tokens, "draft_tokens"),
-                        _dense(counts, "counts"), _dense(bias, "bias"), _dense(grammar, "grammar"),
-                        _dense(repetition, "repetition"), _dense(frequency, "frequency"),
-                        _dense(presence, "presence"), _dense(temperature, "temperature"),
-                        int(bool(probs)), _dense(out, "out"), _dense(status, "status"), s),
-           "tree_logits_process")
+    f32, i32 = torch.float32, torch.int32
+    dev = torch._C._cuda_getDevice()
+    _check(_tree_logits(_arg(logits, logits.dtype, "logits", shape, dev), dt, B, N, V,
+                        _arg(node_counts, i32, "node_counts", (B,), dev),
+                        _arg(mask, torch.int64, "mask", (B, N), dev),
+                        _arg(draft_tokens, i32, "draft_tokens", (B, N), dev),
+                        _arg(counts, i32, "counts", (B, V), dev),
+                        _arg(bias, f32, "bias", (B, V), dev),
+                        _arg(grammar, i32, "grammar", (B, N, (V + 31) // 32), dev),
+                        _arg(repetition, f32, "repetition", (B,), dev),
+                        _arg(frequency, f32, "frequency", (B,), dev),
+                        _arg(presence, f32, "presence", (B,), dev),
+                        _arg(temperature, f32, "temperature", (B,), dev), 1 if probs else 0,
+                        _arg(out, f32, "out", shape, dev), _arg(status, i32, "status", (B,), dev),
+                        _stream_of(stream, dev)), "tree_logits_process")
