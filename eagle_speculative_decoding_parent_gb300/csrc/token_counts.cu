@@ -4,8 +4,11 @@
 // it zeroes the slice in shared memory, goes through all tokens of the
 // sequence (they stay in L2) applying those that fall into the slice, and
 // writes the slice out once: the row's bytes are the bound.  Without it only a
-// few words change: one CTA per sequence checks the tokens, then applies them
-// with integer atomics on the row.
+// few words change: the CTAs of a sequence all check its tokens, and each applies
+// its share with integer atomics on the row.  A scan is bound by the latency of
+// its loads, so each thread has UNROLL of them in flight.
+#include <algorithm>
+
 #include "tv_device.cuh"
 #include "tv_internal.h"
 
@@ -14,6 +17,8 @@ namespace tv {
 namespace {
 
 constexpr int TC_THREADS = 256;
+constexpr int UNROLL = 8;
+constexpr int TC_SHARE = 4096;  // tokens per CTA without `clear`, on average over the sequences
 constexpr int TC_SLICE = 8192;  // entries per CTA: 32 KB of shared memory, six CTAs per SM
 
 struct TcParams {
@@ -21,7 +26,7 @@ struct TcParams {
     const int32_t* tokens;
     const int32_t* starts;  // nullable
     int32_t* status;
-    int total, B, V, slices;  // slices of a row
+    int total, B, V, slices;  // CTAs per sequence
     bool prompt;
 };
 
@@ -33,36 +38,49 @@ __device__ __forceinline__ bool tc_range(const TcParams& p, int b, int& lo, int&
         hi = lo + w;
         return true;
     }
+    lo = p.starts[b];       // beside the loads of the check, whose barrier is in between
+    hi = p.starts[b + 1];
     bool ok = true;
     for (int i = threadIdx.x; i < p.B; i += TC_THREADS) {
         const int s = p.starts[i], e = p.starts[i + 1];
         ok = ok && s >= 0 && s <= e && e <= p.total;
     }
-    lo = p.starts[b];
-    hi = p.starts[b + 1];
     return __syncthreads_and(ok ? 1 : 0) != 0;
 }
 
 __device__ __forceinline__ bool tc_token_ok(const TcParams& p, int x) { return x >= -1 && x < p.V; }
 
+// each(token) for the tokens lo .. hi, every `step`-th from lo + first on.
+template <class Each>
+__device__ __forceinline__ void tc_tokens(const TcParams& p, int lo, int hi, int first, int step, Each each) {
+    for (int64_t i = (int64_t)lo + first; i < hi; i += (int64_t)UNROLL * step) {
+        int x[UNROLL];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const int64_t at = i + (int64_t)u * step;
+            x[u] = at < hi ? p.tokens[at] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) each(x[u]);
+    }
+}
+
 __global__ void __launch_bounds__(TC_THREADS) counts_add_kernel(TcParams p) {
-    const int b = blockIdx.x;
+    const int b = blockIdx.x / p.slices, share = blockIdx.x % p.slices;
     pdl_launch_dependents();
     pdl_wait();
     int lo, hi;
     bool ok = tc_range(p, b, lo, hi);
-    if (ok)
-        for (int i = lo + threadIdx.x; i < hi; i += TC_THREADS) ok = ok && tc_token_ok(p, p.tokens[i]);
+    if (ok) tc_tokens(p, lo, hi, threadIdx.x, TC_THREADS, [&](int x) { ok = ok && tc_token_ok(p, x); });
     ok = __syncthreads_and(ok ? 1 : 0) != 0;
-    if (threadIdx.x == 0) p.status[b] = ok ? TV_OK : TV_ERR_OUT_OF_RANGE;
+    if (threadIdx.x == 0 && share == 0) p.status[b] = ok ? TV_OK : TV_ERR_OUT_OF_RANGE;
     if (!ok) return;
     int32_t* row = p.counts + (int64_t)b * p.V;
-    for (int i = lo + threadIdx.x; i < hi; i += TC_THREADS) {
-        const int x = p.tokens[i];
-        if (x < 0) continue;
+    tc_tokens(p, lo, hi, share * TC_THREADS + threadIdx.x, p.slices * TC_THREADS, [&](int x) {
+        if (x < 0) return;
         if (p.prompt) atomicOr(row + x, INT32_MIN);
         else atomicAdd(row + x, 1);
-    }
+    });
 }
 
 __global__ void __launch_bounds__(TC_THREADS) counts_clear_kernel(TcParams p) {
@@ -76,15 +94,13 @@ __global__ void __launch_bounds__(TC_THREADS) counts_clear_kernel(TcParams p) {
     int lo, hi;
     bool ok = tc_range(p, b, lo, hi);
     __syncthreads();
-    if (ok) {
-        for (int i = lo + threadIdx.x; i < hi; i += TC_THREADS) {
-            const int x = p.tokens[i], at = x - x0;
+    if (ok)
+        tc_tokens(p, lo, hi, threadIdx.x, TC_THREADS, [&](int x) {
             ok = ok && tc_token_ok(p, x);
-            if (x < 0 || at < 0 || at >= n) continue;
-            if (p.prompt) part[at] = INT32_MIN;   // every writer writes the same word
-            else atomicAdd(&part[at], 1);
-        }
-    }
+            if (x < x0 || x >= x0 + n) return;
+            if (p.prompt) part[x - x0] = INT32_MIN;   // every writer writes the same word
+            else atomicAdd(&part[x - x0], 1);
+        });
     ok = __syncthreads_and(ok ? 1 : 0) != 0;
     if (threadIdx.x == 0 && x0 == 0) p.status[b] = ok ? TV_OK : TV_ERR_OUT_OF_RANGE;
     if (!ok) return;
@@ -109,7 +125,8 @@ tv_status launch_token_counts(int32_t* counts, const int32_t* tokens, const int3
         LaunchCfg lc(dim3((unsigned)(B * p.slices)), dim3(TC_THREADS), 0, stream);
         return cudaLaunchKernelEx(&lc.cfg, counts_clear_kernel, p) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
     }
-    LaunchCfg lc(dim3((unsigned)B), dim3(TC_THREADS), 0, stream);
+    p.slices = std::max(1, (int)std::min<int64_t>(total / ((int64_t)B * TC_SHARE), 0x7fffffff / B));
+    LaunchCfg lc(dim3((unsigned)(B * p.slices)), dim3(TC_THREADS), 0, stream);
     return cudaLaunchKernelEx(&lc.cfg, counts_add_kernel, p) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
 
