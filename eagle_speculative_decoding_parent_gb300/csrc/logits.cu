@@ -7,17 +7,21 @@
 // Then z / temperature, or its softmax.
 //
 // Bound by memory: a row is read once and written once.  A row is cut into slices, one
-// CTA each; for the softmax the slices of a row form a cluster, and the maximum and the
-// sum of the slices are exchanged through distributed shared memory.  The grid is as
+// CTA each; for the softmax the slices of a row form a cluster, and the maxima and sums
+// of their warps are exchanged through distributed shared memory.  The grid is as
 // large as the GPU holds at once (two CTAs per SM: one loads or stores while the other
 // waits for its cluster), and each group of CTAs takes a contiguous range of rows.
 // A slice comes into shared memory by a bulk copy, the next row's while the present
 // one is reduced and stored.
 // A tree's rows share their sequence's counts and biases, and few tokens have any: when
 // the sequence changes the slice's are gathered into a list, and per row only the list's
-// entries are changed, in shared memory, one per thread or so; then the path's (at most
-// 63).  After that an entry costs a read into a register, the grammar's bit, the
-// maximum, one exponential and the store.
+// entries are changed, in shared memory, one per thread or so, except the tree's own
+// tokens (at most 63), whose threads add the path's.  After that an entry costs a read
+// into a register, the grammar's bit, the maximum, one exponential and the store.
+// The shared memory leaves some 20 KB of L1: a few spilled registers of 1,024 threads do
+// not fit and come back from L2 in every row, so the row loop keeps its state in shared
+// memory and spills nothing (832 rows of 128,256 float32 probabilities 256 -> 190 us,
+// 4.7 TB/s; 24 rows of 152,064 bfloat16 logits 17 us).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -37,7 +41,8 @@ constexpr int LG_NV_MAX = 8;                                // 4-entry vectors p
 constexpr int LG_SLICE_MAX = LG_THREADS * 4 * LG_NV_MAX - 32;
 constexpr int LG_CLUSTER_MAX = 16;
 constexpr int LG_PLAIN_SLICE = LG_THREADS * 4 * 4 - 32;     // without a softmax: no cluster
-constexpr int LG_SMEM = 112 * 1024;                         // two CTAs per SM
+constexpr int LG_SMEM = 103 * 1024;                         // two CTAs per SM
+constexpr int LG_WARPS = LG_THREADS / 32;
 constexpr float LG_LOG2E = 1.4426950408889634f;
 
 struct LgParams {
@@ -61,6 +66,7 @@ struct LgParams {
 
 struct LgRow {
     float rep, inv_rep, freq, pres, inv_temp;
+    int cnt, err;                               // nodes, status
 };
 
 // The repetition penalty of a token that the history or the path holds, less frequency *
@@ -72,6 +78,7 @@ __device__ __forceinline__ float lg_penalty(const LgRow& r, float z, int n) {
 // A list entry's word: the entry, and above it 0 (not in the history), 1 (in the prompt
 // only), n + 1, or LG_LONG (the count does not fit: read it again).
 constexpr uint32_t LG_LONG = 0xffffu;
+constexpr uint32_t LG_NODE = 0xffffu;   // the whole word (a slice has fewer entries): skip it
 __device__ __forceinline__ uint32_t lg_word(int x, int c) {
     const uint32_t n = (uint32_t)c & 0x7fffffffu;
     return (uint32_t)x | (c == 0 ? 0u : (n + 1u < LG_LONG ? n + 1u : LG_LONG)) << 16;
@@ -79,6 +86,11 @@ __device__ __forceinline__ uint32_t lg_word(int x, int c) {
 __device__ __forceinline__ float lg_max(float a, float b) {  // NaN wins
     float d;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float lg_max3(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 __device__ __forceinline__ float lg_float(float x) { return x; }
@@ -94,17 +106,25 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
     uint32_t* s_gram = reinterpret_cast<uint32_t*>(lg_smem + CAP * 4 + (F32 ? 0 : CAP * 2 + 16));  // [CAP / 32 + 2]
     uint2* list = reinterpret_cast<uint2*>(s_gram + CAP / 32 + 2);      // (word, bias)
     __shared__ int tok[64];
+    // The sequence's state: in shared memory, since registers that hold it would be spilled, and
+    // spilled ones do not stay in the little that is left of L1.
+    __shared__ uint64_t masks[64], node_same[64];        // node c's path; the nodes with its token
+    __shared__ int node_x[64], node_c[64];               // its entry in the slice (or -1), history,
+    __shared__ float node_bias[64];                      // bias
+    __shared__ LgRow r;
     __shared__ int list_n;
-    __shared__ float red[2][LG_THREADS / 32];
-    __shared__ float peer[2][2][LG_CLUSTER_MAX];         // [row parity][maximum, sum] of the slices
-    __shared__ __align__(8) uint64_t peer_bar;
+    __shared__ uint32_t nodes[CAP / 32];                 // entries that nodes' threads change
+    // [row parity] (maximum, sum) of every warp of the cluster, and their barriers
+    __shared__ __align__(16) float2 peer[2][PROBS ? LG_CLUSTER_MAX * LG_WARPS : 1];
+    __shared__ __align__(8) uint64_t peer_bar[2];
     __shared__ __align__(8) uint64_t full;               // the slice has landed
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int group = (int)(blockIdx.x / p.slices), me = (int)(blockIdx.x % p.slices);
     const int64_t row_lo = p.rows * group / p.groups, row_hi = p.rows * (group + 1) / p.groups;
     const int x0 = me * p.slice, n = max(0, min(p.slice, p.V - x0));
     if (tid == 0) {
-        mbar_init(&peer_bar, 1);
+        mbar_init(&peer_bar[0], 1);
+        mbar_init(&peer_bar[1], 1);
         mbar_init(&full, 1);
         fence_mbar_init();
         s_gram[0] = 0u;
@@ -114,11 +134,8 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
     pdl_launch_dependents();
     pdl_wait();
     // A slice of a row: the 16-byte pieces that lie inside by a bulk copy (issued by thread 0),
-    // up to 7 entries at each end and its grammar word by each thread, a row ahead.
-    const uint64_t policy = l2_policy_evict_first();
+    // up to 7 entries at each end and a grammar word by each thread, a row ahead.
     E edge{};
-    uint32_t gram = 0xffffffffu;
-    uint64_t mask_next = 0ull;
     auto ahead = [&](const void* lo, size_t bytes) {     // to L2: the 16-byte pieces inside
         const uintptr_t a = (reinterpret_cast<uintptr_t>(lo) + 15) & ~(uintptr_t)15;
         const uintptr_t z = (reinterpret_cast<uintptr_t>(lo) + bytes) & ~(uintptr_t)15;
@@ -131,7 +148,6 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
             if (p.counts) ahead(p.counts + at, (size_t)n * 4);
             if (p.bias) ahead(p.bias + at, (size_t)n * 4);
         }
-        if (p.mask) mask_next = p.mask[row] & ~1ull;
         const E* lo = static_cast<const E*>(p.logits) + row * p.V + x0;
         const uintptr_t a = reinterpret_cast<uintptr_t>(lo), al = (a + 15) & ~(uintptr_t)15;
         const uintptr_t ah = max(al, (a + (size_t)n * sizeof(E)) & ~(uintptr_t)15);
@@ -139,19 +155,17 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
         if (tid == 0) {
             const uint32_t bytes = (uint32_t)(ah - al);
             mbar_arrive_expect_tx_relaxed_one(&full, bytes);
-            if (bytes > 0) bulk_load(raw + (a / sizeof(E)) % (16 / sizeof(E)) + head, reinterpret_cast<const void*>(al), bytes, &full, policy);
+            if (bytes > 0) bulk_load(raw + (a / sizeof(E)) % (16 / sizeof(E)) + head, reinterpret_cast<const void*>(al), bytes, &full, l2_policy_evict_first());
         }
         const int x = tid < head ? tid : end + tid - head;
-        if (x < n && tid < 16) edge = lo[x];
-        if (p.grammar && tid * 32 < n) gram = __ldcs(p.grammar + row * p.words + x0 / 32 + tid);
+        if (x < n && tid < 16) {
+            if constexpr (F32) cp_async_4(raw + a / sizeof(E) % (16 / sizeof(E)) + x, lo + x);
+            else edge = lo[x];
+        }
+        if (p.grammar && tid * 32 < n) cp_async_4(s_gram + 1 + tid, p.grammar + row * p.words + x0 / 32 + tid);
     };
-    LgRow r{};
-    int cur = -1, cnt = 0, err = TV_OK;
     uint32_t phase = 0, got = 0;
     bool alive = true;
-    uint64_t same = 0ull;                                // thread c: the nodes with node c's token
-    int my_x = -1, my_c = 0;                             // its entry in the slice, count and bias
-    float my_bias = 0.f;
     int b = (int)(row_lo / p.N), i = (int)(row_lo % p.N) - 1;
     if (row_lo < row_hi) fetch(row_lo, b, true);
 #pragma unroll 1
@@ -162,37 +176,37 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
         }
         float* out = p.out + row * p.V + x0;
         const int64_t at = (int64_t)b * p.V + x0;        // the slice in counts and bias
-        const uint64_t m = mask_next;
-        if (b != cur) {
+        if (i == 0 || row == row_lo) {
             // ---- the sequence: parameters, checks, the list of its counts and biases
-            cur = b;
-            cnt = p.node_counts ? p.node_counts[b] : p.N;
-            r.rep = p.rep ? p.rep[b] : 1.f;
-            r.freq = p.freq ? p.freq[b] : 0.f;
-            r.pres = p.pres ? p.pres[b] : 0.f;
-            const float temp = p.temp ? p.temp[b] : 1.f;
-            err = (cnt >= 1 && cnt <= p.N) ? TV_OK : TV_ERR_OUT_OF_RANGE;
+            const int cnt = p.node_counts ? p.node_counts[b] : p.N;
+            const float rep = p.rep ? p.rep[b] : 1.f, freq = p.freq ? p.freq[b] : 0.f;
+            const float pres = p.pres ? p.pres[b] : 0.f, temp = p.temp ? p.temp[b] : 1.f;
+            int err = (cnt >= 1 && cnt <= p.N) ? TV_OK : TV_ERR_OUT_OF_RANGE;
             const bool tokens = p.mask && err == TV_OK;
-            if (err == TV_OK && !(isfinite(r.rep) && r.rep > 0.f && isfinite(temp) && temp > 0.f &&
-                                  isfinite(r.freq) && isfinite(r.pres)))
+            if (err == TV_OK && !(isfinite(rep) && rep > 0.f && isfinite(temp) && temp > 0.f &&
+                                  isfinite(freq) && isfinite(pres)))
                 err = TV_ERR_BAD_VALUES;
-            r.inv_rep = 1.f / r.rep;
-            r.inv_temp = 1.f / temp;
             int t = 0;                                    // node tid's token, its count and bias
             if (tokens && tid < cnt) t = p.tokens[(int64_t)b * p.N + tid];
             const bool tok_ok = !tokens || tid == 0 || tid >= cnt || (t >= 0 && t < p.V);
-            my_x = -1;
+            int my_x = -1, my_c = 0;
+            float my_bias = 0.f;
             if (tokens && tok_ok && p.counts && tid >= 1 && tid < cnt && t >= x0 && t < x0 + n) {
                 my_x = t - x0;
-                my_c = p.counts[at + my_x] & 0x7fffffff;
+                my_c = p.counts[at + my_x];
                 my_bias = p.bias ? p.bias[at + my_x] : 0.f;
             }
             __syncthreads();                              // the sequence before is done with
             if (tid == 0) list_n = 0;
             if (tid < 64) tok[tid] = t;
+            if (tid < p.N) masks[tid] = p.mask ? p.mask[(int64_t)b * p.N + tid] & ~1ull : 0ull;
+            if (tid < CAP / 32) nodes[tid] = 0u;
             if (__syncthreads_and(tok_ok ? 1 : 0) == 0) err = TV_ERR_OUT_OF_RANGE;
+            if (tid == 0) r = LgRow{rep, 1.f / rep, freq, pres, 1.f / temp, cnt, err};
+            if (my_x >= 0) atomicOr(&nodes[my_x >> 5], 1u << (my_x & 31));
+            __syncthreads();
             if (p.counts || p.bias) {
-                constexpr int U = 8;
+                constexpr int U = 4;
 #pragma unroll 1
                 for (int base = 0; base < n; base += LG_THREADS * U) {
                     int c[U];
@@ -218,18 +232,26 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         const int k = j + __popc(votes[u] & ((1u << lane) - 1u));
-                        if (((votes[u] >> lane) & 1u) && k < p.list_max)
-                            list[k] = make_uint2(lg_word(base + u * LG_THREADS + tid, c[u]), __float_as_uint(bs[u]));
+                        if (((votes[u] >> lane) & 1u) && k < p.list_max) {
+                            const int x = base + u * LG_THREADS + tid;
+                            list[k] = make_uint2((nodes[x >> 5] >> (x & 31)) & 1u ? LG_NODE : lg_word(x, c[u]), __float_as_uint(bs[u]));
+                        }
                         j += __popc(votes[u]);
                     }
                 }
             }
-            same = 0ull;
-            if (my_x >= 0)
-                for (int c = 1; c < cnt; ++c) same |= (uint64_t)(tok[c] == t) << c;
+            if (tid < 64) {
+                uint64_t same = 0ull;
+                if (my_x >= 0)
+                    for (int c = 1; c < cnt; ++c) same |= (uint64_t)(tok[c] == t) << c;
+                node_same[tid] = same;
+                node_x[tid] = (same & ((1ull << tid) - 1ull)) == 0ull ? my_x : -1;   // once per token
+                node_c[tid] = my_c;
+                node_bias[tid] = my_bias;
+            }
             __syncthreads();
         }
-        if (i == 0 && me == 0 && tid == 0) p.status[b] = err;
+        if (i == 0 && me == 0 && tid == 0) p.status[b] = r.err;
         // ---- the slice has landed; its ends and its grammar words
         // (one warp polls; the others see it through the barrier below)
         if (warp == 0) alive = alive && mbar_wait_sleep(&full, got & 1u);
@@ -238,19 +260,21 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
         const int rsh = (int)((reinterpret_cast<uintptr_t>(static_cast<const E*>(p.logits) + row * p.V + x0) / sizeof(E)) %
                               (16 / sizeof(E)));
         {
-            const int head = min(n, (int)(16 / sizeof(E) - rsh) % (int)(16 / sizeof(E)));
-            const int end = max(head, ((rsh + n) & ~(int)(16 / sizeof(E) - 1)) - rsh);
-            const int x = tid < head ? tid : end + tid - head;
-            if (x < n && tid < 16) raw[x + rsh] = edge;
-            if (tid * 32 < n) s_gram[1 + tid] = gram;
+            if constexpr (!F32) {
+                const int head = min(n, (8 - rsh) % 8), end = max(head, ((rsh + n) & ~7) - rsh);
+                const int x = tid < head ? tid : end + tid - head;
+                if (x < n && tid < 16) raw[x + rsh] = edge;
+            }
+            cp_async_wait_all();
             if (tid == 0) s_gram[1 + (n + 31) / 32] = 0u;
             // positions beside the slice weigh nothing
             const int zsh = F32 ? rsh : sh;
             if (tid < zsh) zs[tid] = -INFINITY;
             for (int q = zsh + n + tid; q < CAP; q += LG_THREADS) zs[q] = -INFINITY;
         }
-        const bool skip = (cnt >= 1 && cnt <= p.N && i >= cnt) || err != TV_OK;
-        const bool path = m != 0 && p.counts && !skip;
+        const uint64_t m = masks[i];
+        auto absent = [&]() -> bool { return r.cnt >= 1 && r.cnt <= p.N && i >= r.cnt; };
+        const bool skip = absent() || r.err != TV_OK;
         __syncthreads();
         if constexpr (!F32) {
             // bfloat16: widen into the float buffer
@@ -259,21 +283,28 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
         // (float32: in and out rows may be aligned differently; then the entries move first)
         float* zr = F32 ? reinterpret_cast<float*>(raw) : zs;
         const int zsh = F32 ? rsh : sh;
-        // ---- the path's tokens (each once) are computed before the list changes them
-        float my_z = 0.f;
-        const bool mine = path && my_x >= 0 && ((m >> (tid & 63)) & 1ull) && (same & m & ((1ull << (tid & 63)) - 1ull)) == 0ull;
+        // ---- the history and the biases: the list's entries, and (each token once) the nodes'
+        const int my_x = tid < 64 ? node_x[tid] : -1;
+        const bool mine = my_x >= 0 && !skip;
         if constexpr (!F32) __syncthreads();
-        if (mine) my_z = lg_penalty(r, zr[my_x + zsh] + my_bias, my_c + __popcll(same & m));
-        if (path) __syncthreads();
         if (!skip && (p.counts || p.bias)) {
+            const bool all = list_n > p.list_max;        // (of the whole CTA)
+            float my_z = 0.f;
+            if (mine) {
+                const int on_path = __popcll(node_same[tid] & m), my_c = node_c[tid];
+                my_z = zr[my_x + zsh] + node_bias[tid];
+                if (my_c != 0 || on_path > 0) my_z = lg_penalty(r, my_z, (my_c & 0x7fffffff) + on_path);
+                if (!all) zr[my_x + zsh] = my_z;
+            }
             auto change = [&](int x, int c, float bs) {
                 float z = zr[x + zsh] + bs;
                 if (c != 0) z = lg_penalty(r, z, c & 0x7fffffff);
                 zr[x + zsh] = z;
             };
-            if (list_n <= p.list_max) {
+            if (!all) {
                 for (int j = tid; j < list_n; j += LG_THREADS) {
                     const uint2 w = list[j];
+                    if (w.x == LG_NODE) continue;
                     const int x = (int)(w.x & 0xffffu);
                     const uint32_t k = w.x >> 16;
                     const int c = k == 0u ? 0 : k == LG_LONG ? p.counts[at + x] : (int)(k - 1u) | INT32_MIN;
@@ -281,15 +312,16 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
                 }
             } else {
                 // more counts and biases than the list holds: all of them, from L2
+                __syncthreads();
                 for (int x = tid; x < n; x += LG_THREADS) {
                     const int c = p.counts ? p.counts[at + x] : 0;
                     const float bs = p.bias ? p.bias[at + x] : 0.f;
                     if (c != 0 || bs != 0.f) change(x, c, bs);
                 }
+                __syncthreads();
+                if (mine) zr[my_x + zsh] = my_z;
             }
             __syncthreads();
-            if (mine) zr[my_x + zsh] = my_z;
-            if (path) __syncthreads();
         }
         // ---- into registers: positions 4 (k LG_THREADS + tid) of the buffer
         float z[NV][4];
@@ -302,7 +334,7 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
             z[k][1] = v.y;
             z[k][2] = v.z;
             z[k][3] = v.w;
-            if (p.grammar && x < n) {
+            if (p.grammar) {                             // (beyond the slice: whatever is there, on -infinity)
                 const int w = (x + 32) >> 5;             // (s_gram[0] stands before the slice)
                 const uint32_t lo = s_gram[w], hi = zsh != 0 ? s_gram[w + 1] : 0u;
                 const uint32_t ok = __funnelshift_r(lo, hi, (x + 32) & 31);
@@ -310,16 +342,24 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
                 for (int e = 0; e < 4; ++e)
                     if (!((ok >> e) & 1u)) z[k][e] = -INFINITY;
             }
-            if constexpr (PROBS) mx = lg_max(mx, lg_max(lg_max(z[k][0], z[k][1]), lg_max(z[k][2], z[k][3])));
+            if constexpr (PROBS) mx = lg_max3(lg_max3(mx, z[k][0], z[k][1]), z[k][2], z[k][3]);
         }
         fence_proxy_async_smem();                        // the next copy lands where this row was
         if (__syncthreads_and(alive ? 1 : 0) == 0) {     // a wait ran out, in this row or the last
             if (tid == 0) p.status[b] = TV_ERR_TIMEOUT;
-            return;
+            break;
         }
         if (row + 1 < row_hi) fetch(row + 1, b, i + 1 < p.N);
-        if (skip && err == TV_OK) continue;              // an absent node: nothing is written
+        const int err = r.err;
+        if (absent() && err == TV_OK) continue;          // an absent node: nothing is written
         auto store = [&](float scale) {
+            // (computed again, rather than kept in registers that there are too few of)
+            int64_t at_row = row;
+            asm volatile("" : "+l"(at_row));
+            float* out = p.out + at_row * p.V + x0;
+            const int sh = (int)((reinterpret_cast<uintptr_t>(out) >> 2) & 3);
+            const int zsh = F32 ? (int)((reinterpret_cast<uintptr_t>(static_cast<const E*>(p.logits) + at_row * p.V + x0) / sizeof(E)) %
+                                        (16 / sizeof(E))) : sh;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int x = (k * LG_THREADS + tid) * 4 - zsh;
@@ -344,30 +384,16 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
         if constexpr (!PROBS) {
             store(r.inv_temp);
         } else {
-            // ---- softmax: maximum m and sum s relative to it over the CTA's slice, then the
-            // slices' pairs are combined (by every CTA in the same order): weights 2^(m - max)
-            auto reduce = [&](float v, bool sum) -> float {
-                const float none = sum ? 0.f : -INFINITY;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    const float y = __shfl_xor_sync(0xffffffffu, v, o);
-                    v = sum ? v + y : lg_max(v, y);
-                }
-                if (lane == 0) red[sum][warp] = v;
-                __syncthreads();
-                v = lane < LG_THREADS / 32 ? red[sum][lane] : none;
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) {
-                    const float y = __shfl_xor_sync(0xffffffffu, v, o);
-                    v = sum ? v + y : lg_max(v, y);
-                }
-                return __shfl_sync(0xffffffffu, v, 0);
-            };
-            mx = reduce(mx, false);
-            // e^((z - max) / temperature); the shift's rounding is the same for every entry and
-            // cancels in the quotient
+            // ---- softmax: every warp's maximum and its sum relative to that go to all CTAs of the
+            // row, and each warp combines them all, in the same order: weights 2^(m - max).  No
+            // barrier of the CTA is needed, nor one of the cluster (which would first wait for the
+            // row before to be stored).  m is the rounded product with the scale that the exponents
+            // are relative to, so its rounding cancels in the quotient.
             const float scale = LG_LOG2E * r.inv_temp;
-            const float base = mx == -INFINITY ? 0.f : -mx * scale;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = lg_max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            mx *= scale;
+            const float base = mx == -INFINITY ? 0.f : -mx;
             float sum = 0.f;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
@@ -375,45 +401,36 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
                 for (int e = 0; e < 4; ++e) z[k][e] = ex2_approx(fmaf(z[k][e], scale, base));
                 sum += (z[k][0] + z[k][1]) + (z[k][2] + z[k][3]);
             }
-            sum = reduce(sum, true);
-            float w = 1.f;
-            if (p.slices > 1) {
-                // Every slice writes its pair into all of them and counts the bytes on their
-                // barrier: a cluster barrier would first wait for the row before to be stored.
-                // (A slice is at most one row ahead of another, as it needs the other's pair: two
-                // places are enough, and a CTA ends only with every pair here.)  One warp polls.
-                if (warp == 0) {
-                    const uint32_t par = phase & 1u;
-                    // (relaxed: a release would wait for the row before to be stored, too)
-                    mbar_arrive_expect_tx_relaxed_elect(&peer_bar, (uint32_t)p.slices * 8);
-                    __syncwarp();
-                    if (lane < p.slices) {
-                        remote_st_async(&peer[par][0][me], &peer_bar, (uint32_t)lane, mx);
-                        remote_st_async(&peer[par][1][me], &peer_bar, (uint32_t)lane, sum);
-                    }
-                    alive = alive && mbar_wait_sleep(&peer_bar, par);
-                    const float pm = lane < p.slices ? *reinterpret_cast<volatile float*>(&peer[par][0][lane]) : -INFINITY;
-                    const float ps = lane < p.slices ? *reinterpret_cast<volatile float*>(&peer[par][1][lane]) : 0.f;
-                    float top = pm;
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) top = lg_max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const float tb = top == -INFINITY ? 0.f : -top * scale;
-                    sum = ps * exp2f(fmaf(pm, scale, tb));
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            // Two barriers in turn: a CTA may be one row ahead of another (for the row after that
+            // it needs a pair that the other sends when it has all of this row's).  A CTA ends only
+            // with every pair here.
+            const uint32_t par = phase & 1u;
+            uint64_t* bar = &peer_bar[par];
+            if (warp == 0) mbar_arrive_expect_tx_relaxed_elect(bar, (uint32_t)(p.slices * LG_WARPS * 8));
+            __syncwarp();
+            if (lane < p.slices) remote_st_async(&peer[par][me * LG_WARPS + warp], bar, (uint32_t)lane, mx, sum);
+            alive = alive && mbar_wait_sleep(bar, (phase >> 1) & 1u);
+            ++phase;
+            const volatile float* pairs = reinterpret_cast<const volatile float*>(peer[par]);
+            float top = -INFINITY, total = 0.f;
+            for (int k = lane; k < p.slices * LG_WARPS; k += 32) top = lg_max(top, pairs[2 * k]);
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    if (lane == 0) red[0][0] = sum == 0.f ? 0.f : exp2f(fmaf(mx, scale, tb)) / sum;
-                }
-                ++phase;
-                __syncthreads();
-                w = red[0][0];
-            } else {
-                w = sum == 0.f ? 0.f : 1.f / sum;
-            }
+            for (int o = 16; o > 0; o >>= 1) top = lg_max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (top == -INFINITY) top = 0.f;
+            for (int k = lane; k < p.slices * LG_WARPS; k += 32) total = fmaf(pairs[2 * k + 1], exp2f(pairs[2 * k] - top), total);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+            const float w = total == 0.f ? 0.f : exp2f(mx - top) / total;
             store(w);                                    // (NaN stays NaN)
         }
     }
     // (the last row's pairs)
-    if (__syncthreads_and(alive ? 1 : 0) == 0 && tid == 0 && cur >= 0) p.status[cur] = TV_ERR_TIMEOUT;
+    if (__syncthreads_and(alive ? 1 : 0) == 0 && tid == 0 && row_lo < row_hi) p.status[b] = TV_ERR_TIMEOUT;
+    // after a wait that ran out, pairs may still be on their way to this CTA; every CTA gets here,
+    // as every wait is bounded
+    if (PROBS && p.slices > 1) cluster_barrier_relaxed();
 }
 
 template <typename E, bool PROBS, int NV>

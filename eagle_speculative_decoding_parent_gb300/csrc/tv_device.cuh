@@ -162,6 +162,12 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity) 
     return true;
 }
 
+// Asynchronous 4-byte copy global -> shared, and the wait for all of the thread's.
+__device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
@@ -410,12 +416,12 @@ __device__ __forceinline__ int4 lds_v4_volatile(const int4* p) {
 __device__ __forceinline__ void remote_st_u32(int* p, uint32_t rank, int v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(p, rank)), "r"(v) : "memory");
 }
-// Asynchronous 4-byte store into cluster rank `rank`, its bytes counted on that rank's
+// Asynchronous 8-byte store into cluster rank `rank`, its bytes counted on that rank's
 // mbarrier `bar` (no release: earlier stores of the thread are not waited for).
-__device__ __forceinline__ void remote_st_async(float* p, uint64_t* bar, uint32_t rank, float v) {
-    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+__device__ __forceinline__ void remote_st_async(float2* p, uint64_t* bar, uint32_t rank, float x, float y) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(
                      map_rank(p, rank)),
-                 "r"(__float_as_uint(v)), "r"(map_rank(bar, rank))
+                 "l"(f2_pack(x, y)), "r"(map_rank(bar, rank))
                  : "memory");
 }
 __device__ __forceinline__ float4 remote_ld_f4(const float* p, uint32_t rank) {
@@ -457,6 +463,11 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
 __device__ __forceinline__ void cluster_barrier_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The same without ordering memory: nothing is waited for but the other CTAs.
+__device__ __forceinline__ void cluster_barrier_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\t"
+                 "barrier.cluster.wait.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint4 remote_ld_u4(const void* p, uint32_t rank) {
     uint4 v;
