@@ -875,12 +875,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         const int row = tid & 127;                            // tensor-memory lane
         const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + lane_off + i * KT, tO = tmem + lane_off + TMEM_O + i * D;
-        const int tok_l = row / p.G, head = row - tok_l * p.G;
         float* xo = reinterpret_cast<float*>(smem + L::OFF_X);  // [columns][rows]
         float* ml = reinterpret_cast<float*>(smem + L::OFF_ML);
         uint32_t sc = 0, oc = 0, live = 0, xc = 0;
         bool alive = true;
-        Item it;
         // every softmax warp has written xo (0), has read it (1): with a bounded wait, unlike
         // bar.sync
         auto all_x = [&](int which) {
@@ -892,21 +890,29 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             alive = alive && wait_all(&xall[which], xc & 1u);
             xc += which;
         };
-        for (uint32_t k = 0; alive && take(k, it); ++k) {
+        for (uint32_t k = 0; alive; ++k) {
+            // the item stays in its slot, which is given back at its end: its fields in registers
+            // would be spilled beside the scores, and L1 is too small to hold what is spilled
+            const Item& it = items[k % GQ];
+            if (!wait_all(&gq_full[k % GQ], (k / GQ) & 1u) || (it.flags & ITEM_END)) break;
             const bool two = (it.flags & ITEM_TWO) != 0;
+            const int n = it.n, ja = it.fa - it.t_lo, jb = it.fb - it.t_lo;
             if ((it.flags & ITEM_STATUS) && tid == 0)
                 p.status[it.b] = (it.flags & ITEM_BAD) ? TV_ERR_OUT_OF_RANGE : TV_OK;
+            int row_ = row;
+            asm volatile("" : "+r"(row_));                  // (per item, not kept over the tiles)
+            const int tok_l = row_ / p.G, head = row_ - tok_l * p.G;
             const int tok = tok_l + (two ? i * p.npt : 0);    // token within the item
             const bool mine = tok_l < p.npt && tok < it.ntok;
             // keys of the row, from the first key of the piece's tiles on
             const int self = it.P + it.i0 + min(tok, it.ntok - 1);
             const int first = p.window > 0 ? max(0, self - p.window + 1) : 0;
             const int step = two ? 1 : 2, j0 = two ? 0 : i;
-            const bool have = it.n > j0;                      // O(i) will hold this item
+            const bool have = n > j0;                      // O(i) will hold this item
             const int rows = p.G * min(it.ntok, p.npt);       // rows of the item in a row tile
             const bool wrows = (warp & 3) * 32 < rows;        // some of them in this warp
             float m_used = -INFINITY, l = 0.f;
-            for (int j = j0; j < it.n; j += step) {
+            for (int j = j0; j < n; j += step) {
                 if (!wait_all<64>(&sfull[i], sc & 1u)) {
                     alive = false;
                     break;
@@ -929,7 +935,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     for (int c = 0; c < KT; ++c) sv[c] = __uint_as_float(r[c / 32][c % 32]);
                 };
                 load_s();
-                const int t = it.t_lo + j;
                 if constexpr (CAP) {
                     // cap tanh(scale s / cap), in units of log 2.  An exponential and a reciprocal
                     // more per score would bind on the special function unit, so arguments up to
@@ -969,9 +974,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                         load_s();
                     }
                 }
-                if (t < it.fa || t >= it.fb) {
+                if (j < ja || j >= jb) {
                     // visible keys of the tile: bits a .. z, a word for 32 columns
-                    const int k0 = it.kbase + t * KT;
+                    const int k0 = it.kbase + (it.t_lo + j) * KT;
                     const int a = first - k0, z = self - k0;
 #pragma unroll
                     for (int h = 0; h < KT; h += 32) {
@@ -1216,6 +1221,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 o_read();
             }
             if (!two && it.n > 0 && tid == 0) mbar_arrive(xdone);
+            __syncwarp();
+            if (lane == 0) remote_arrive_relaxed_after(&gq_empty[k % GQ], 0, it.b);
         }
         if (!alive && lane == 0) *abort_flag = 1;
     }
