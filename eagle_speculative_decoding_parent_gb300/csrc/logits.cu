@@ -23,6 +23,7 @@
 // memory and spills nothing (832 rows of 128,256 float32 probabilities 256 -> 190 us,
 // 4.7 TB/s; 24 rows of 152,064 bfloat16 logits 17 us).
 #include <cuda_bf16.h>
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -183,7 +184,8 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
             const float pres = p.pres ? p.pres[b] : 0.f, temp = p.temp ? p.temp[b] : 1.f;
             int err = (cnt >= 1 && cnt <= p.N) ? TV_OK : TV_ERR_OUT_OF_RANGE;
             const bool tokens = p.mask && err == TV_OK;
-            if (err == TV_OK && !(isfinite(rep) && rep > 0.f && isfinite(temp) && temp > 0.f &&
+            // (1 / x overflows for the smallest positive x)
+            if (err == TV_OK && !(isfinite(rep) && rep >= FLT_MIN && isfinite(temp) && temp >= FLT_MIN &&
                                   isfinite(freq) && isfinite(pres)))
                 err = TV_ERR_BAD_VALUES;
             int t = 0;                                    // node tid's token, its count and bias
@@ -387,18 +389,23 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
             // ---- softmax: every warp's maximum and its sum relative to that go to all CTAs of the
             // row, and each warp combines them all, in the same order: weights 2^(m - max).  No
             // barrier of the CTA is needed, nor one of the cluster (which would first wait for the
-            // row before to be stored).  m is the rounded product with the scale that the exponents
-            // are relative to, so its rounding cancels in the quotient.
+            // row before to be stored).  Exponents are differences of logits times the scale, not of
+            // products: those may be too large for their difference to mean anything.
             const float scale = LG_LOG2E * r.inv_temp;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mx = lg_max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            mx *= scale;
             const float base = mx == -INFINITY ? 0.f : -mx;
+            const uint64_t base2 = f2_pack(base, base), scale2 = f2_pack(scale, scale);
             float sum = 0.f;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) z[k][e] = ex2_approx(fmaf(z[k][e], scale, base));
+                for (int e = 0; e < 4; e += 2) {
+                    float a, c;
+                    f2_unpack(f2_mul(f2_add(f2_pack(z[k][e], z[k][e + 1]), base2), scale2), a, c);
+                    z[k][e] = ex2_approx(a);
+                    z[k][e + 1] = ex2_approx(c);
+                }
                 sum += (z[k][0] + z[k][1]) + (z[k][2] + z[k][3]);
             }
 #pragma unroll
@@ -419,10 +426,10 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) top = lg_max(top, __shfl_xor_sync(0xffffffffu, top, o));
             if (top == -INFINITY) top = 0.f;
-            for (int k = lane; k < p.slices * LG_WARPS; k += 32) total = fmaf(pairs[2 * k + 1], exp2f(pairs[2 * k] - top), total);
+            for (int k = lane; k < p.slices * LG_WARPS; k += 32) total = fmaf(pairs[2 * k + 1], exp2f((pairs[2 * k] - top) * scale), total);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-            const float w = total == 0.f ? 0.f : exp2f(mx - top) / total;
+            const float w = total == 0.f ? 0.f : exp2f((mx - top) * scale) / total;
             store(w);                                    // (NaN stays NaN)
         }
     }

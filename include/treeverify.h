@@ -17,6 +17,11 @@
  *   tree_accept            greedy argmax or rejection-sampling acceptance
  *   kv_compact             gather-then-scatter of the accepted K/V rows
  *
+ * Beside them: growing the tree (draft_tree_expand), writing its K/V rows
+ * (tree_kv_append), the prompts and plainly decoded tokens of the same cache
+ * (chunk_kv_append, chunk_attention), and what the model's rows go through before
+ * acceptance reads them (tree_logits_process, token_counts_update).
+ *
  * Conventions shared by all calls
  * -------------------------------
  * - Tree: N nodes (1 <= N <= 64).  Node 0 is the root: the last token the
@@ -392,8 +397,9 @@ tv_status tree_verify_attention_noalloc(const void* q, const void* k_cache, cons
  * token at logical position P_b + i, P_b = prefix_lens[b].  Rows before
  * q_start[0] or from q_start[B] on belong to no sequence: they are neither read
  * into a result nor written.  If q_start breaks these rules every sequence gets
- * TV_ERR_OUT_OF_RANGE and nothing else is written.  P_b + n_b is at most 2^31 - 1024.  A prompt is one chunk or
- * several, plain decoding is n_b = 1, and both may share a batch.
+ * TV_ERR_OUT_OF_RANGE and nothing else is written.  P_b + n_b is at most
+ * 2^31 - 1024.  A prompt is one chunk or several, plain decoding is n_b = 1, and
+ * both may share a batch.
  * ------------------------------------------------------------------------ */
 
 /* Rotary positions.  A table holds, for each of dim / 2 pairs of columns, the
@@ -562,8 +568,8 @@ tv_status token_counts_update(int32_t* counts, const int32_t* tokens, const int3
  * written.
  * status int32 [B]: TV_ERR_OUT_OF_RANGE for a node count outside [1, N] or (with
  * mask) a token of nodes 1 .. n_b - 1 outside [0, V); TV_ERR_BAD_VALUES for a
- * repetition or temperature not finite or <= 0, a frequency or presence not
- * finite.  That sequence's rows (all N when the count is bad) are -infinity
+ * repetition or temperature not finite, <= 0 or below 2^-126, a frequency or
+ * presence not finite.  That sequence's rows (all N when the count is bad) are -infinity
  * (probs == 0) or zero.
  * Host errors: N outside [1, 64], V outside [1, 2^24], NULL logits, out or
  * status, mask without draft_tokens or the reverse, a penalty without counts.

@@ -262,6 +262,39 @@ def test_attention_many_sequences(tv):
     check(tv, R.cache_case(n, P, Hq=2, Hkv=1, d=64, bs=16, dtype=torch.bfloat16, seed=10))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_blocks_past_32_bits(tv, dtype):
+    """Blocks at both ends of caches of more than 2^31 elements: appended and attended."""
+    Hq, Hkv, d, bs = 8, 4, 128, 32
+    c = append_case([70, 1], [40, 200], Hq=Hq, Hkv=Hkv, d=d, bs=bs, dtype=dtype, seed=12)
+    used = c["k_cache"].shape[0]
+    blocks = 2 ** 31 // (Hkv * bs * d) + 100
+    far = [b if b % 2 else blocks - 1 - b for b in range(used)]
+    idx = torch.tensor(far, device="cuda")
+    big = [torch.empty((blocks, Hkv, bs, d), dtype=dtype, device="cuda") for _ in range(2)]
+    assert big[0].numel() > 2 ** 31
+    for t, n in zip(big, ("k_cache", "v_cache")):
+        t[idx] = c[n].cuda()
+    small = {k: v.cuda() for k, v in c.items() if isinstance(v, torch.Tensor)}
+    table = small["table"]
+    moved = torch.where(table >= 0, idx.to(torch.int32)[table.clamp(min=0).long()], table)
+    rope, outs = tv.rope_table(128), []
+    for k_cache, v_cache, tab in ((small["k_cache"], small["v_cache"], table), (*big, moved)):
+        qkv = small["qkv"].clone()
+        q, out = qkv[:, :Hq], torch.zeros((71, Hq, d), dtype=dtype, device="cuda")
+        st = torch.full((2, 2), -9, dtype=torch.int32, device="cuda")
+        ws = torch.zeros(max(16, tv.chunk_attention_workspace(71, 2, Hq, Hkv, d, dtype)), dtype=torch.uint8, device="cuda")
+        tv.chunk_kv_append(q, qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], k_cache, v_cache, tab,
+                           small["q_start"], small["prefix"], st[0], rope=rope)
+        tv.chunk_attention(q, k_cache, v_cache, tab, small["q_start"], small["prefix"], out, st[1], ws)
+        torch.cuda.synchronize()
+        assert st.eq(0).all()
+        outs.append(out)
+    assert torch.equal(outs[0], outs[1])
+    for t, n in zip(big, ("k_cache", "v_cache")):
+        assert torch.equal(t[idx], small[n])
+
+
 def test_attention_refusals(tv):
     c = R.cache_case([5], [10], Hq=4, Hkv=2, d=64, bs=16, dtype=torch.bfloat16)
     g = {k: v.cuda() for k, v in c.items() if isinstance(v, torch.Tensor)}

@@ -198,6 +198,26 @@ def test_node_counts_and_bad_sequences(tv, probs):
     assert out[3:].eq(bad).all()
 
 
+@pytest.mark.parametrize("probs", [False, True])
+def test_smallest_temperatures(tv, probs):
+    """Down to the smallest normal number, whose reciprocal is finite; below it the sequence is
+    refused.  Logits of at most 2^-20 keep z / temperature finite."""
+    c = case(5, 2, 300, seed=4, penalties=False, grammar=False, bias=False)
+    c["z"] = (c["z"] * 2.0 ** -24).float()
+    c["kw"]["temp"] = torch.tensor([1e-3, 2.0 ** -100, 2.0 ** -126, 2.0 ** -127, 1e-45], dtype=torch.float32)
+    out, status = process(tv, c, probs)
+    assert status.tolist() == [0, 0, 0, 7, 7]
+    ref = R.logits(c["z"], probs=probs, temp=c["kw"]["temp"])[:3]
+    # one float32 rounding of the reciprocal and one of the product; a probability moves by that
+    # times the largest |z| / temperature in the exponent, at most all of itself
+    z = (c["z"].double().abs().amax((1, 2)) / c["kw"]["temp"].double())[:3, None, None]
+    rel = 4 * 2.0 ** -24
+    tol = ref.abs() * rel if not probs else \
+        torch.minimum(ref * (2 * rel * z + (300 / 512 + 24) * 2.0 ** -24 + 2.0 ** -20), torch.tensor(1.0).double()) + 2.0 ** -126
+    assert ((out[:3].double() - ref).abs() <= tol).all()
+    assert out[3:].eq(0.0 if probs else -math.inf).all()
+
+
 def test_logits_refusals(tv):
     z = torch.zeros(1, 2, 64, device="cuda")
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
