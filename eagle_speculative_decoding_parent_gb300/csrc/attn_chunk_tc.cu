@@ -44,6 +44,12 @@
 //            passes them on to warp 8.
 //   warp 11  scheduler: walks the run, checks each new sequence's blocks, and
 //            publishes the items a few ahead.
+// Measured: 4,096 rows after 12,281 keys (28/4 heads of 128) 541 us = 1,556 TFLOP/s; one row
+// of each of 64 sequences of 512-8,192 keys 124 us = 5.6 TB/s; chunks of 1-1,500 rows 98 us
+// (four to five us per item beside its tiles); one row after 300 keys 15.5 us.  A pair of
+// tiles of two full row tiles takes 1.65 us, of which the softmax is the longer half; an
+// exponential by polynomial for a part of the scores is slower (573-680 us), as are four
+// softmax warpgroups.
 // Every wait is bounded; one that runs out sets the abort flag, and the roles
 // leave after their copies and products in flight are done.
 #include <algorithm>

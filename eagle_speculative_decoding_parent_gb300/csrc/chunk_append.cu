@@ -15,6 +15,10 @@
 // bytes of a row (half layout: the two 16-byte vectors that hold a pair's columns), and
 // it takes the same unit of several rows, so that finding it is paid once and the rows'
 // loads are in flight together.
+// Measured (bfloat16): 9,190 rows of 28 + 2 x 4 heads of 128, 169 MB, 43.6 us, where a
+// plain copy of those bytes takes 33 (prefetching the rows to L2 first 45.9, four rows in
+// flight per thread 55); 832 rows of 32 + 2 x 8 heads 10.6 us, most of it the three round
+// trips to a row's slot.
 #include <cuda_bf16.h>
 #include <math.h>
 
