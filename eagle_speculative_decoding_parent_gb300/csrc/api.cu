@@ -316,7 +316,7 @@ tv_status chunk_kv_append(const void* q, int64_t q_stride, const void* k, int64_
     if ((int64_t)Hq * d > 0x7fffffff || (int64_t)Hkv * d > 0x7fffffff) return TV_ERR_UNSUPPORTED;
     if (rope && (rope->dim < 2 || rope->dim > TV_ROPE_MAX_DIM || rope->dim > d))
         return TV_ERR_INVALID_ARG;
-    if ((d * eb) % 16 != 0 || (rope && (rope->dim * eb) % 32 != 0)) return TV_ERR_UNSUPPORTED;
+    if (((int64_t)d * eb) % 16 != 0 || (rope && (rope->dim * eb) % 32 != 0)) return TV_ERR_UNSUPPORTED;
     if (B == 0) return TV_OK;
     if (!q_start || !prefix_lens || !block_table || !status || !k_cache || !v_cache ||
         (q == nullptr) != (q_out == nullptr))
@@ -419,8 +419,8 @@ tv_status chunk_attention(const void* q, int64_t q_stride, const void* k_cache,
     a.num_blocks = num_blocks;
     a.dt = dt;
     a.scale = (scale > 0.f && isfinite(scale)) ? scale : 1.0f / sqrtf((float)d);
-    // (a cap of 1e30 changes no score by as much as its rounding)
-    a.softcap = softcap > 0.f && softcap < 1e30f ? softcap : 0.f;
+    // (a cap of 1e30 changes no score by as much as its rounding, one of 1e-30 leaves nothing of it)
+    a.softcap = softcap > 0.f && softcap < 1e30f ? fmaxf(softcap, 1e-30f) : 0.f;
     a.window = window > 0 ? window : 0;
     a.out = out;
     a.out_stride = out_stride;

@@ -74,7 +74,7 @@ def test_attention_window_and_cap(tv, dtype, window, cap):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("cap", [1e-30, 0.01, 3.0, 1000.0, 1e6, 1e20, 1e31])
+@pytest.mark.parametrize("cap", [1e-42, 1e-30, 0.01, 3.0, 1000.0, 1e6, 1e20, 1e31])
 def test_attention_caps_of_any_size(tv, dtype, cap):
     """Scores far below, around and far above the cap, in the same tile."""
     for heads, d in (((4, 2), 64), ((4, 1), 128)):

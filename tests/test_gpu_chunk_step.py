@@ -2,6 +2,8 @@
 serving loop runs them: prompts in, a tree verified on sampled rows, the accepted rows moved,
 one more token decoded.  Each step's output is compared with a plain computation in 64 bits
 from what the GPU held before that step."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -260,3 +262,37 @@ def test_sampling_needs_its_buffers(tv):
                         dtype=torch.bfloat16, max_path=N, V=V)
     with pytest.raises(ValueError):
         s.step.run(**s.verify_args())
+
+
+def test_two_host_threads(tv):
+    """Two threads, each with its own loop on its own stream, give what one alone gives."""
+    def run(s, stream):
+        with torch.cuda.stream(stream):
+            for _ in range(3):
+                s.fill.run(**s.prefill_args())
+                tv.token_counts_update(s.counts, s.prompt, s.st, starts=s.starts, clear=True, prompt=True)
+                s.prefix, s.ones = i32(PROMPTS), i32(list(range(B + 1)))
+                s.append_tree()
+                s.step.run(**s.verify_args())
+                s.one.run(**s.decode_args())
+        stream.synchronize()
+
+    def state(s):
+        return [t.cpu() for t in (s.fill.out, s.step.out, s.step.target, s.step.out_tokens, s.one.out, s.counts)]
+
+    want = []
+    for mode in (0, 1):
+        s = Loop(tv, mode, torch.bfloat16)
+        torch.cuda.synchronize()
+        run(s, torch.cuda.Stream())
+        want.append(state(s))
+    loops = [Loop(tv, mode, torch.bfloat16) for mode in (0, 1)]
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=run, args=(s, torch.cuda.Stream())) for s in loops]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for s, w in zip(loops, want):
+        for x, y in zip(state(s), w):
+            assert torch.equal(x, y)
