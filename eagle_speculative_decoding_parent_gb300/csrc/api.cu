@@ -371,7 +371,7 @@ static bool chunk_attn_shape_ok(int Hq, int Hkv, int d, tv_dtype dt) {
 size_t chunk_attention_workspace(int T, int B, int Hq, int Hkv, int d, tv_dtype dt) {
     if (T < 1 || B < 1 || !chunk_attn_shape_ok(Hq, Hkv, d, dt)) return 0;
     return chunk_attn_tc_applicable(Hq, Hkv, d, dt) ? chunk_attn_tc_workspace(T, B, Hq, Hkv, d)
-                                                    : chunk_attn_f32_workspace(T, B, Hq, Hkv, d);
+                                                    : chunk_attn_f32_workspace(T, B, Hq, Hkv, d, dt);
 }
 
 tv_status chunk_attention(const void* q, int64_t q_stride, const void* k_cache,

@@ -360,14 +360,300 @@ int cf_splits(int T, int B, int Hkv, int G) {
     return (int)std::clamp<int64_t>(4 * device_sm_count() / ctas, 1, CF_SPLITS);
 }
 
+// ------------------------------------------------------------------ few rows
+// Batches with about one token per sequence (plain decoding): a token's G <= 8 rows against
+// its keys, bound by the K/V stream.  A CTA takes one (token, kv head, part of the keys);
+// 16 lanes hold a key's columns, float2 by float2, and go through four keys at a time whose
+// K and V rows are in flight together.  The 4 R partial dot products of a group of lanes are
+// added up by halving exchanges, which leave lane i with the score of (row i / 4, key i % 4):
+// 15 exchanges instead of 64 for R = 4.  Every group keeps its own running maximum, sum and
+// O; they are joined at the end, then the parts of the keys by a second kernel.
+constexpr int CR_THREADS = 128;
+constexpr int CR_GROUPS = CR_THREADS / 16;
+constexpr int CR_KEYS = 4;             // per group and step
+constexpr int CR_PART = 256;           // keys below which a part is not cut further
+
+struct CrParams {
+    ChunkView c;
+    const float *q, *k, *v;
+    float* out;
+    int64_t q_stride, o_stride;
+    int32_t* status;
+    int32_t* parts;               // [T][Hkv] parts that the join finds (0: none)
+    float* part;                  // [T][Hkv][splits] x (G x d, G maxima, G sums)
+    int Hkv, G, d, window, splits;
+    float scale, softcap;
+};
+
+template <int NJ, int R>
+__global__ void __launch_bounds__(CR_THREADS) chunk_rows_kernel(CrParams p) {
+    __shared__ ChunkLocateTmp<CR_THREADS> tmp;
+    __shared__ float so[CR_THREADS / 32][R][NJ * 32];
+    __shared__ float sm_m[CR_THREADS / 32][R], sm_l[CR_THREADS / 32][R];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l16 = lane & 15;
+    const int t = blockIdx.x / p.splits, split = blockIdx.x % p.splits, g = blockIdx.y;
+    pdl_launch_dependents();
+    pdl_wait();
+    const ChunkPlace at = chunk_locate<CR_THREADS>(
+        &tmp, p.c, [&](int64_t) { return (int64_t)t - p.c.q_start[0]; }, [&](int, int n) { return (int64_t)n; });
+    if (blockIdx.x == 0 && g == 0)
+        for (int b = tid; b < p.c.B; b += CR_THREADS)
+            if (!at.valid || p.c.q_start[b] == p.c.q_start[b + 1])
+                p.status[b] = (at.valid && chunk_shape_ok(p.c, p.c.prefix[b], 0)) ? TV_OK : TV_ERR_OUT_OF_RANGE;
+    int32_t* n_parts = p.parts + (int64_t)t * p.Hkv + g;
+    if (at.b >= p.c.B) {                                  // a row of no sequence
+        if (split == 0 && tid == 0) *n_parts = 0;
+        return;
+    }
+    bool ok = chunk_shape_ok(p.c, at.P, at.n);
+    if (ok) ok = chunk_blocks_ok(p.c, at.b, chunk_first_key(at.P, p.window), (int64_t)at.P + at.n, tid, CR_THREADS);
+    ok = __syncthreads_and(ok ? 1 : 0) != 0;
+    if (t == at.row && g == 0 && split == 0 && tid == 0) p.status[at.b] = ok ? TV_OK : TV_ERR_OUT_OF_RANGE;
+    float* out = p.out + (int64_t)t * p.o_stride + (int64_t)g * p.G * p.d;
+    if (!ok) {
+        if (split == 0) {
+            for (int e = tid; e < p.G * p.d; e += CR_THREADS) out[e] = 0.f;
+            if (tid == 0) *n_parts = 0;
+        }
+        return;
+    }
+    const int pos = at.P + (t - at.row), first = chunk_first_key(pos, p.window), keys = pos - first + 1;
+    const int active = min(p.splits, (keys + CR_PART - 1) / CR_PART);
+    if (split == 0 && tid == 0) *n_parts = active > 1 ? active : 0;
+    if (split >= active) return;
+    const int k_lo = first + (int)((int64_t)keys * split / active), k_hi = first + (int)((int64_t)keys * (split + 1) / active);
+    float2 q[R][NJ], o[R][NJ];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const bool in = r < p.G && j * 32 < p.d;
+            q[r][j] = in ? *reinterpret_cast<const float2*>(p.q + (int64_t)t * p.q_stride + (int64_t)(g * p.G + r) * p.d + j * 32 + 2 * l16)
+                         : make_float2(0.f, 0.f);
+            o[r][j] = make_float2(0.f, 0.f);
+        }
+    // lane i of a group: the running statistics of rows i / 4 (and i / 4 + 4)
+    constexpr int H = R / 4;
+    float m[H], l[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        m[h] = -INFINITY;
+        l[h] = 0.f;
+    }
+    const int32_t* table = p.c.table + (int64_t)at.b * p.c.max_blocks;
+    // the cache rows of the step's keys: lane u of a group holds key u's, a step ahead
+    auto key_at = [&](int base) -> int { return base + (tid >> 4) * CR_KEYS + (l16 & (CR_KEYS - 1)); };
+    auto block = [&](int base) -> int {
+        const int key = key_at(base);
+        return key < k_hi ? table[key / p.c.bs] : 0;
+    };
+    int blk = block(k_lo);
+    for (int base = k_lo; base < k_hi; base += CR_GROUPS * CR_KEYS) {
+        const int my_key = key_at(base);
+        const int64_t my_row = (((int64_t)blk * p.Hkv + g) * p.c.bs + my_key % p.c.bs) * p.d;
+        float2 kx[CR_KEYS][NJ], vx[CR_KEYS][NJ];
+#pragma unroll
+        for (int u = 0; u < CR_KEYS; ++u) {
+            const int64_t row = __shfl_sync(0xffffffffu, my_row, u, 16);
+            const bool in = base + (tid >> 4) * CR_KEYS + u < k_hi;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                kx[u][j] = vx[u][j] = make_float2(0.f, 0.f);
+                if (in && j * 32 < p.d) {
+                    kx[u][j] = __ldcs(reinterpret_cast<const float2*>(p.k + row + j * 32 + 2 * l16));
+                    vx[u][j] = __ldcs(reinterpret_cast<const float2*>(p.v + row + j * 32 + 2 * l16));
+                }
+            }
+        }
+        blk = block(base + CR_GROUPS * CR_KEYS);
+        float f[H], w[H];
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            float s[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int r = h * 4 + i / 4, u = i % 4;
+                float a = 0.f;
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) a = fmaf(q[r][j].x, kx[u][j].x, fmaf(q[r][j].y, kx[u][j].y, a));
+                s[i] = a;
+            }
+#pragma unroll
+            for (int step = 8; step > 0; step >>= 1)
+#pragma unroll
+                for (int i = 0; i < step; ++i) {
+                    const bool up = (l16 & step) != 0;
+                    const float y = __shfl_xor_sync(0xffffffffu, up ? s[i] : s[i + step], step);
+                    s[i] = (up ? s[i + step] : s[i]) + y;
+                }
+            float z = s[0] * p.scale;
+            if (p.softcap > 0.f) z = p.softcap * tanhf(z / p.softcap);
+            z = my_key < k_hi ? z * CF_LOG2E : -INFINITY;
+            float mx = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float mn = fmaxf(m[h], mx), bz = mn == -INFINITY ? 0.f : mn;
+            f[h] = exp2f(m[h] - bz);
+            w[h] = exp2f(z - bz);
+            l[h] = fmaf(l[h], f[h], w[h]);
+            m[h] = mn;
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float fr = __shfl_sync(0xffffffffu, f[r / 4], r % 4 * 4, 16);
+            float wr[CR_KEYS];
+#pragma unroll
+            for (int u = 0; u < CR_KEYS; ++u) wr[u] = __shfl_sync(0xffffffffu, w[r / 4], r % 4 * 4 + u, 16);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                float x = o[r][j].x * fr, y = o[r][j].y * fr;
+#pragma unroll
+                for (int u = 0; u < CR_KEYS; ++u) {
+                    x = fmaf(wr[u], vx[u][j].x, x);
+                    y = fmaf(wr[u], vx[u][j].y, y);
+                }
+                o[r][j] = make_float2(x, y);
+            }
+        }
+    }
+    // ---- join: the two groups of a warp by exchanges, the warps through shared memory
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        const float mo = __shfl_xor_sync(0xffffffffu, m[h], 16), lo = __shfl_xor_sync(0xffffffffu, l[h], 16);
+        const float mm = fmaxf(m[h], mo), bz = mm == -INFINITY ? 0.f : mm;
+        const float f = exp2f(m[h] - bz);
+        l[h] = l[h] * f + lo * exp2f(mo - bz);
+        m[h] = mm;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = h * 4 + i;
+            const float fr = __shfl_sync(0xffffffffu, f, i * 4, 16);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const float x = o[r][j].x * fr, y = o[r][j].y * fr;
+                const float xs = x + __shfl_xor_sync(0xffffffffu, x, 16), ys = y + __shfl_xor_sync(0xffffffffu, y, 16);
+                if (lane < 16) *reinterpret_cast<float2*>(&so[warp][r][j * 32 + 2 * l16]) = make_float2(xs, ys);
+            }
+        }
+        if (lane < 16 && (l16 & 3) == 0) {
+            sm_m[warp][h * 4 + l16 / 4] = m[h];
+            sm_l[warp][h * 4 + l16 / 4] = l[h];
+        }
+    }
+    __syncthreads();
+    float* slot = p.part + (((int64_t)t * p.Hkv + g) * p.splits + split) * ((int64_t)p.G * (p.d + 2));
+    for (int e = tid; e < p.G * p.d; e += CR_THREADS) {
+        const int r = e / p.d, c = e - r * p.d;
+        float mm = -INFINITY, sum = 0.f, acc = 0.f;
+#pragma unroll
+        for (int x = 0; x < CR_THREADS / 32; ++x) mm = fmaxf(mm, sm_m[x][r]);
+        const float bz = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+        for (int x = 0; x < CR_THREADS / 32; ++x) {
+            const float f = exp2f(sm_m[x][r] - bz);
+            sum = fmaf(f, sm_l[x][r], sum);
+            acc = fmaf(f, so[x][r][c], acc);
+        }
+        if (active == 1) {
+            out[e] = acc / sum;
+        } else {
+            slot[e] = acc;
+            if (c == 0) {
+                slot[p.G * p.d + r] = mm;
+                slot[p.G * (p.d + 1) + r] = sum;
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(CR_THREADS) chunk_rows_join_kernel(CrParams p) {
+    const int t = blockIdx.x, g = blockIdx.y;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int n = p.parts[(int64_t)t * p.Hkv + g];
+    if (n == 0) return;
+    const int64_t step = (int64_t)p.G * (p.d + 2);
+    const float* slot = p.part + ((int64_t)t * p.Hkv + g) * p.splits * step;
+    float* out = p.out + (int64_t)t * p.o_stride + (int64_t)g * p.G * p.d;
+    for (int e = threadIdx.x; e < p.G * p.d; e += CR_THREADS) {
+        const int r = e / p.d;
+        float m[CF_SPLITS], sums[CF_SPLITS], x[CF_SPLITS], mx = -INFINITY, den = 0.f, acc = 0.f;
+#pragma unroll
+        for (int k = 0; k < CF_SPLITS; ++k) {
+            m[k] = k < n ? slot[k * step + p.G * p.d + r] : -INFINITY;
+            sums[k] = k < n ? slot[k * step + p.G * (p.d + 1) + r] : 0.f;
+            x[k] = k < n ? slot[k * step + e] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < CF_SPLITS; ++k) mx = fmaxf(mx, m[k]);
+        const float bz = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+        for (int k = 0; k < CF_SPLITS; ++k) {
+            const float f = exp2f(m[k] - bz);
+            den = fmaf(f, sums[k], den);
+            acc = fmaf(f, x[k], acc);
+        }
+        out[e] = acc / den;
+    }
+}
+
+// Each token reads its keys for itself, so at most about one token per sequence; a thread
+// holds 3 to 4 x G x d / 16 registers of rows and keys.
+bool cr_applies(int T, int B, int Hkv, int G, int d, tv_dtype dt) {
+    return dt == TV_F32 && T <= 2 * (int64_t)B && G <= (d <= 128 ? 8 : 4) && Hkv <= 65535;
+}
+int cr_splits(int T, int Hkv) {
+    return (int)std::clamp<int64_t>(32 * (int64_t)device_sm_count() / ((int64_t)T * Hkv), 1, CF_SPLITS);
+}
+size_t cr_counts_bytes(int T, int Hkv) { return ((size_t)T * Hkv * 4 + 15) & ~(size_t)15; }
+
+template <int NJ>
+cudaError_t cr_launch(const CrParams& p, const LaunchCfg& lc) {
+    if constexpr (NJ < 8)
+        if (p.G > 4) return cudaLaunchKernelEx(&lc.cfg, chunk_rows_kernel<NJ, 8>, p);
+    return cudaLaunchKernelEx(&lc.cfg, chunk_rows_kernel<NJ, 4>, p);
+}
+
+tv_status launch_rows(const ChunkAttnArgs& a) {
+    CrParams p{};
+    p.c = ChunkView{a.q_start, a.prefix_lens, a.block_table, a.T, a.B, a.max_blocks, a.bs, a.num_blocks};
+    p.q = static_cast<const float*>(a.q);
+    p.k = static_cast<const float*>(a.k_cache);
+    p.v = static_cast<const float*>(a.v_cache);
+    p.out = static_cast<float*>(a.out);
+    p.q_stride = a.q_stride;
+    p.o_stride = a.out_stride;
+    p.status = a.status;
+    p.parts = static_cast<int32_t*>(a.ws);
+    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + cr_counts_bytes(a.T, a.Hkv));
+    p.Hkv = a.Hkv;
+    p.G = a.Hq / a.Hkv;
+    p.d = a.d;
+    p.window = a.window;
+    p.splits = cr_splits(a.T, a.Hkv);
+    p.scale = a.scale;
+    p.softcap = a.softcap;
+    if ((int64_t)a.T * p.splits > 0x7fffffff) return TV_ERR_UNSUPPORTED;
+    LaunchCfg lc(dim3((unsigned)(a.T * p.splits), (unsigned)a.Hkv), dim3(CR_THREADS), 0, a.stream);
+    const cudaError_t e = a.d <= 64 ? cr_launch<2>(p, lc) : a.d <= 128 ? cr_launch<4>(p, lc) : cr_launch<8>(p, lc);
+    if (e != cudaSuccess) return TV_ERR_CUDA;
+    if (p.splits == 1) return TV_OK;
+    LaunchCfg lj(dim3((unsigned)a.T, (unsigned)a.Hkv), dim3(CR_THREADS), 0, a.stream);
+    return cudaLaunchKernelEx(&lj.cfg, chunk_rows_join_kernel, p) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+}
+
 }  // namespace
 
-size_t chunk_attn_f32_workspace(int T, int B, int Hq, int Hkv, int d) {
+size_t chunk_attn_f32_workspace(int T, int B, int Hq, int Hkv, int d, tv_dtype dt) {
     const int G = Hq / Hkv, s = cf_splits(T, B, Hkv, G);
+    if (T > 0 && cr_applies(T, B, Hkv, G, d, dt))
+        return cr_counts_bytes(T, Hkv) + (size_t)T * Hkv * cr_splits(T, Hkv) * G * (d + 2) * sizeof(float);
     return s == 1 ? 0 : (size_t)(cf_tile_bound(T, B, G) * Hkv) * s * CF_M * (d + 2) * sizeof(float);
 }
 
 tv_status launch_chunk_attn_f32(const ChunkAttnArgs& a) {
+    if (a.T > 0 && cr_applies(a.T, a.B, a.Hkv, a.Hq / a.Hkv, a.d, a.dt)) return launch_rows(a);
     CfParams p{};
     p.c = ChunkView{a.q_start, a.prefix_lens, a.block_table, a.T, a.B, a.max_blocks, a.bs, a.num_blocks};
     p.q = a.q;

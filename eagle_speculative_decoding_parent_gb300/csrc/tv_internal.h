@@ -218,7 +218,7 @@ struct ChunkAttnArgs {
     void* ws;
     cudaStream_t stream;
 };
-size_t chunk_attn_f32_workspace(int T, int B, int Hq, int Hkv, int d);
+size_t chunk_attn_f32_workspace(int T, int B, int Hq, int Hkv, int d, tv_dtype dt);
 tv_status launch_chunk_attn_f32(const ChunkAttnArgs& a);
 // tensor-core kernel: bfloat16, up to 128 query heads per kv head
 bool chunk_attn_tc_applicable(int Hq, int Hkv, int d, tv_dtype dt);

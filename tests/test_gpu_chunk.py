@@ -262,6 +262,47 @@ def test_attention_many_sequences(tv):
     check(tv, R.cache_case(n, P, Hq=2, Hkv=1, d=64, bs=16, dtype=torch.bfloat16, seed=10))
 
 
+@pytest.mark.parametrize("heads,d", [((2, 2), 32), ((4, 1), 64), ((6, 2), 96), ((8, 1), 128), ((5, 5), 128),
+                                     ((4, 2), 160), ((4, 1), 256), ((8, 1), 256), ((9, 1), 64)])
+@pytest.mark.parametrize("window,cap", [(0, 0.0), (1, 0.0), (100, 5.0)])
+def test_decoding_f32(tv, heads, d, window, cap):
+    """About one token per sequence: none, one and several; keys from one on, in one part or many."""
+    n = [1, 0, 1, 1, 3, 1, 1, 0, 2, 1]
+    P = [0, 5, 1, 15, 16, 255, 256, 0, 1000, 5000]
+    check(tv, R.cache_case(n, P, Hq=heads[0], Hkv=heads[1], d=d, bs=16, dtype=torch.float32, seed=d),
+          window=window, softcap=cap)
+
+
+@pytest.mark.parametrize("B", [1, 2, 40, 300])
+def test_decoding_f32_batches(tv, B):
+    rng = np.random.default_rng(B)
+    P = [int(x) for x in rng.integers(0, 3000 if B < 300 else 200, B)]
+    check(tv, R.cache_case([1] * B, P, Hq=8, Hkv=2, d=64, bs=8, dtype=torch.float32, seed=B))
+
+
+def test_decoding_f32_bad_sequences(tv):
+    """A bad block, a prefix past the table, rows of no sequence; keys with NaN beyond the last."""
+    c = R.cache_case([1, 1, 1, 1], [40, 600, 3, 70], Hq=4, Hkv=2, d=64, bs=16, dtype=torch.float32, seed=1)
+    ref, A, S = R.attention(c)
+    tol = R.attention_tolerance(c, ref, A, S, 64)
+    for b in range(4):
+        blk, row = int(c["table"][b][(c["P"][b] + 1) // 16]), (c["P"][b] + 1) % 16
+        if row:
+            c["k_cache"][blk, :, row:], c["v_cache"][blk, :, row:] = float("nan"), float("inf")
+    c["table"][1, 20] = c["k_cache"].shape[0]
+    c["prefix"][3] = 16 * c["table"].shape[1]
+    c["q"] = torch.cat([c["q"][:1], c["q"], c["q"][:2]])
+    c["q_start"] = c["q_start"] + 1
+    out, status = attend(tv, c)
+    assert status.tolist() == [0, 3, 0, 3]
+    for b in (0, 2):
+        assert ((out[b + 1].double() - ref[b]).abs() <= tol[b]).all()
+    assert out[[2, 4]].eq(0).all() and out[[0, 5, 6]].eq(7.0).all()
+    c["q_start"] = torch.tensor([0, 2, 1, 3, 4], dtype=torch.int32)
+    out, status = attend(tv, c)
+    assert status.eq(3).all() and out.eq(7.0).all()
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_blocks_past_32_bits(tv, dtype):
     """Blocks at both ends of caches of more than 2^31 elements: appended and attended."""
