@@ -11,7 +11,8 @@
 // When the rows are too few to fill the GPU the keys are cut into up to 16
 // parts; each part leaves its unnormalised O, maximum and sum in the workspace
 // and a second kernel joins them in order.
-// Measured: 316 rows of 2 heads of 64 after up to 900 keys 25 us, of which two launches
+// Batches of about one token per sequence take a second form, further down.
+// Measured: 1,000 rows of 32/8 heads of 128 after 3,000 keys 2.69 ms (21 TFLOP/s); 316 rows of 2 heads of 64 after up to 900 keys 25 us, of which two launches
 // and one item's way through the tiles are nearly all.
 #include <cuda_bf16.h>
 
@@ -363,14 +364,19 @@ int cf_splits(int T, int B, int Hkv, int G) {
 // ------------------------------------------------------------------ few rows
 // Batches with about one token per sequence (plain decoding): a token's G <= 8 rows against
 // its keys, bound by the K/V stream.  A CTA takes one (token, kv head, part of the keys);
-// 16 lanes hold a key's columns, float2 by float2, and go through four keys at a time whose
-// K and V rows are in flight together.  The 4 R partial dot products of a group of lanes are
+// 16 lanes hold a key's columns, float2 by float2, and go through four keys at a time.  The
+// rows come by bulk copies into two stages of eight keys per warp, one filling while the other
+// is read.  The 4 R partial dot products of a group of lanes are
 // added up by halving exchanges, which leave lane i with the score of (row i / 4, key i % 4):
 // 15 exchanges instead of 64 for R = 4.  Every group keeps its own running maximum, sum and
 // O; they are joined at the end, then the parts of the keys by a second kernel.
+// Measured: 64 sequences of 512-8,192 keys, 32/8 heads of 128: 252 us = 5.8 TB/s (rows straight
+// into registers 509, three stages 301; by row tiles 3,866).
 constexpr int CR_THREADS = 128;
 constexpr int CR_GROUPS = CR_THREADS / 16;
 constexpr int CR_KEYS = 4;             // per group and step
+constexpr int CR_STAGES = 2;
+constexpr int CR_WARP_KEYS = 2 * CR_KEYS;
 constexpr int CR_PART = 256;           // keys below which a part is not cut further
 
 struct CrParams {
@@ -390,8 +396,13 @@ __global__ void __launch_bounds__(CR_THREADS) chunk_rows_kernel(CrParams p) {
     __shared__ ChunkLocateTmp<CR_THREADS> tmp;
     __shared__ float so[CR_THREADS / 32][R][NJ * 32];
     __shared__ float sm_m[CR_THREADS / 32][R], sm_l[CR_THREADS / 32][R];
+    __shared__ __align__(8) uint64_t bars[CR_THREADS / 32][CR_STAGES];
+    extern __shared__ __align__(128) float ring[];        // [warp][stage][K, V][key][d]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l16 = lane & 15;
     const int t = blockIdx.x / p.splits, split = blockIdx.x % p.splits, g = blockIdx.y;
+    if (lane < CR_STAGES) mbar_init(&bars[warp][lane], 1);
+    fence_mbar_init();
+    __syncwarp();
     pdl_launch_dependents();
     pdl_wait();
     const ChunkPlace at = chunk_locate<CR_THREADS>(
@@ -441,31 +452,43 @@ __global__ void __launch_bounds__(CR_THREADS) chunk_rows_kernel(CrParams p) {
         l[h] = 0.f;
     }
     const int32_t* table = p.c.table + (int64_t)at.b * p.c.max_blocks;
-    // the cache rows of the step's keys: lane u of a group holds key u's, a step ahead
-    auto key_at = [&](int base) -> int { return base + (tid >> 4) * CR_KEYS + (l16 & (CR_KEYS - 1)); };
-    auto block = [&](int base) -> int {
-        const int key = key_at(base);
-        return key < k_hi ? table[key / p.c.bs] : 0;
+    const uint64_t policy = l2_policy_evict_first();
+    // Lanes 0 - 7 copy the K rows of the warp's keys of a step, 8 - 15 their V rows (past the
+    // last key that one's again, at weight 0); the block is looked up a step ahead.
+    constexpr int STEP = CR_THREADS / 32 * CR_WARP_KEYS;
+    const int steps = (k_hi - k_lo + STEP - 1) / STEP;
+    const int copy_key = k_lo + warp * CR_WARP_KEYS + (lane & (CR_WARP_KEYS - 1));
+    auto block = [&](int i) -> int {
+        return i < steps && lane < 2 * CR_WARP_KEYS ? table[min(copy_key + i * STEP, k_hi - 1) / p.c.bs] : 0;
     };
-    int blk = block(k_lo);
-    for (int base = k_lo; base < k_hi; base += CR_GROUPS * CR_KEYS) {
-        const int my_key = key_at(base);
-        const int64_t my_row = (((int64_t)blk * p.Hkv + g) * p.c.bs + my_key % p.c.bs) * p.d;
-        float2 kx[CR_KEYS][NJ], vx[CR_KEYS][NJ];
-#pragma unroll
-        for (int u = 0; u < CR_KEYS; ++u) {
-            const int64_t row = __shfl_sync(0xffffffffu, my_row, u, 16);
-            const bool in = base + (tid >> 4) * CR_KEYS + u < k_hi;
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                kx[u][j] = vx[u][j] = make_float2(0.f, 0.f);
-                if (in && j * 32 < p.d) {
-                    kx[u][j] = __ldcs(reinterpret_cast<const float2*>(p.k + row + j * 32 + 2 * l16));
-                    vx[u][j] = __ldcs(reinterpret_cast<const float2*>(p.v + row + j * 32 + 2 * l16));
-                }
-            }
+    const int stage_floats = 2 * CR_WARP_KEYS * p.d;
+    float* mine = ring + (size_t)warp * CR_STAGES * stage_floats;
+    auto fill = [&](int i, int blk) {
+        if (i >= steps) return;
+        uint64_t* bar = &bars[warp][i % CR_STAGES];
+        if (lane == 0) mbar_arrive_expect_tx_relaxed_one(bar, (uint32_t)stage_floats * 4);
+        __syncwarp();
+        if (lane < 2 * CR_WARP_KEYS) {
+            const int key = min(copy_key + i * STEP, k_hi - 1);
+            const float* src = (lane < CR_WARP_KEYS ? p.k : p.v) + (((int64_t)blk * p.Hkv + g) * p.c.bs + key % p.c.bs) * p.d;
+            bulk_load(mine + (i % CR_STAGES) * stage_floats + lane * p.d, src, (uint32_t)p.d * 4, bar, policy);
         }
-        blk = block(base + CR_GROUPS * CR_KEYS);
+    };
+#pragma unroll
+    for (int i = 0; i < CR_STAGES; ++i) fill(i, block(i));
+    int blk = block(CR_STAGES);
+    bool alive = true;
+    for (int i = 0; i < steps; ++i) {
+        alive = __all_sync(0xffffffffu, mbar_wait(&bars[warp][i % CR_STAGES], (i / CR_STAGES) & 1));
+        if (!alive) break;
+        const float* stage = mine + (i % CR_STAGES) * stage_floats + (lane >> 4) * CR_KEYS * p.d + 2 * l16;
+        const int my_key = k_lo + i * STEP + (tid >> 4) * CR_KEYS + (l16 & (CR_KEYS - 1));
+        float2 kx[CR_KEYS][NJ];
+#pragma unroll
+        for (int u = 0; u < CR_KEYS; ++u)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                kx[u][j] = j * 32 < p.d ? *reinterpret_cast<const float2*>(stage + u * p.d + j * 32) : make_float2(0.f, 0.f);
         float f[H], w[H];
 #pragma unroll
         for (int h = 0; h < H; ++h) {
@@ -497,6 +520,12 @@ __global__ void __launch_bounds__(CR_THREADS) chunk_rows_kernel(CrParams p) {
             l[h] = fmaf(l[h], f[h], w[h]);
             m[h] = mn;
         }
+        float2 vx[CR_KEYS][NJ];
+#pragma unroll
+        for (int u = 0; u < CR_KEYS; ++u)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                vx[u][j] = j * 32 < p.d ? *reinterpret_cast<const float2*>(stage + (CR_WARP_KEYS + u) * p.d + j * 32) : make_float2(0.f, 0.f);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const float fr = __shfl_sync(0xffffffffu, f[r / 4], r % 4 * 4, 16);
@@ -514,6 +543,15 @@ __global__ void __launch_bounds__(CR_THREADS) chunk_rows_kernel(CrParams p) {
                 o[r][j] = make_float2(x, y);
             }
         }
+        __syncwarp();                                     // the stage is read
+        fill(i + CR_STAGES, blk);
+        blk = block(i + CR_STAGES + 1);
+    }
+    if (!alive) {
+        // a copy that did not come: the ones behind it are waited for, too
+        for (int x = 0; x < CR_STAGES; ++x)
+            for (int y = 0; y < 2; ++y) mbar_wait(&bars[warp][x], y);
+        if (lane == 0) p.status[at.b] = TV_ERR_TIMEOUT;
     }
     // ---- join: the two groups of a warp by exchanges, the warps through shared memory
 #pragma unroll
@@ -608,11 +646,30 @@ int cr_splits(int T, int Hkv) {
 }
 size_t cr_counts_bytes(int T, int Hkv) { return ((size_t)T * Hkv * 4 + 15) & ~(size_t)15; }
 
+template <int NJ, int R>
+cudaError_t cr_launch_r(const CrParams& p, cudaStream_t stream) {
+    const size_t smem = (size_t)CR_THREADS / 32 * CR_STAGES * 2 * CR_WARP_KEYS * p.d * sizeof(float);
+    static bool set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!set[dev]) {
+        const size_t most = (size_t)CR_THREADS / 32 * CR_STAGES * 2 * CR_WARP_KEYS * NJ * 32 * sizeof(float);
+        e = cudaFuncSetAttribute(chunk_rows_kernel<NJ, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return e;
+        }
+        set[dev] = true;
+    }
+    LaunchCfg lc(dim3((unsigned)(p.c.T * p.splits), (unsigned)p.Hkv), dim3(CR_THREADS), smem, stream);
+    return cudaLaunchKernelEx(&lc.cfg, chunk_rows_kernel<NJ, R>, p);
+}
 template <int NJ>
-cudaError_t cr_launch(const CrParams& p, const LaunchCfg& lc) {
+cudaError_t cr_launch(const CrParams& p, cudaStream_t stream) {
     if constexpr (NJ < 8)
-        if (p.G > 4) return cudaLaunchKernelEx(&lc.cfg, chunk_rows_kernel<NJ, 8>, p);
-    return cudaLaunchKernelEx(&lc.cfg, chunk_rows_kernel<NJ, 4>, p);
+        if (p.G > 4) return cr_launch_r<NJ, 8>(p, stream);
+    return cr_launch_r<NJ, 4>(p, stream);
 }
 
 tv_status launch_rows(const ChunkAttnArgs& a) {
@@ -635,8 +692,7 @@ tv_status launch_rows(const ChunkAttnArgs& a) {
     p.scale = a.scale;
     p.softcap = a.softcap;
     if ((int64_t)a.T * p.splits > 0x7fffffff) return TV_ERR_UNSUPPORTED;
-    LaunchCfg lc(dim3((unsigned)(a.T * p.splits), (unsigned)a.Hkv), dim3(CR_THREADS), 0, a.stream);
-    const cudaError_t e = a.d <= 64 ? cr_launch<2>(p, lc) : a.d <= 128 ? cr_launch<4>(p, lc) : cr_launch<8>(p, lc);
+    const cudaError_t e = a.d <= 64 ? cr_launch<2>(p, a.stream) : a.d <= 128 ? cr_launch<4>(p, a.stream) : cr_launch<8>(p, a.stream);
     if (e != cudaSuccess) return TV_ERR_CUDA;
     if (p.splits == 1) return TV_OK;
     LaunchCfg lj(dim3((unsigned)a.T, (unsigned)a.Hkv), dim3(CR_THREADS), 0, a.stream);
