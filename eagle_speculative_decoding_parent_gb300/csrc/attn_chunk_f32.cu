@@ -20,6 +20,7 @@
 
 #include "tv_chunk.cuh"
 #include "tv_internal.h"
+#include "tv_tc.cuh"
 
 namespace tv {
 
@@ -96,7 +97,12 @@ __global__ void __launch_bounds__(CF_THREADS) chunk_attn_kernel(CfParams p) {
     float* sk = sq + CF_M * LD;        // [64][LD]
     float* sv = sk + CF_N * LD;        // [64][DP]
     float* sp = sk;                    // P [64][64 + 4] takes K's place once S is done
+    __shared__ __align__(8) uint64_t landed;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    if (tid == 0) {
+        mbar_init(&landed, 1);
+        fence_mbar_init();
+    }
     pdl_launch_dependents();
     pdl_wait();
     const int tile_id = (int)(blockIdx.x / p.splits), split = (int)(blockIdx.x % p.splits);
@@ -143,8 +149,29 @@ __global__ void __launch_bounds__(CF_THREADS) chunk_attn_kernel(CfParams p) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][c][e] = 0.f;
     }
+    const uint64_t policy = l2_policy_evict_normal();
     for (int j = j0; j < j1; ++j) {
         const int t0 = k_lo + j * CF_N;
+        if constexpr (sizeof(E) == 4) {
+            // a row per thread by bulk copies.  (Rows past the last key keep what they held: their
+            // scores are masked, and their values are not multiplied.)
+            fence_proxy_async_smem();  // P was written where K lands
+            __syncthreads();           // the previous tile's P and V are done with
+            const int r = tid & (CF_N - 1), nk = min(CF_N, k_hi - t0);
+            if (tid == 0) mbar_arrive_expect_tx_relaxed_one(&landed, (uint32_t)(2 * nk * p.d) * 4);
+            if (r < nk) {
+                const int key = t0 + r;
+                const int64_t blk = p.c.table[(int64_t)t.b * p.c.max_blocks + key / p.c.bs];
+                const int64_t at = ((blk * p.Hkv + g) * p.c.bs + key % p.c.bs) * p.d;
+                if (tid < CF_N) bulk_load(sk + r * LD, kc + at, (uint32_t)p.d * 4, &landed, policy);
+                else bulk_load(sv + r * DP, vc + at, (uint32_t)p.d * 4, &landed, policy);
+            }
+            const bool here = mbar_wait(&landed, (uint32_t)(j - j0) & 1u);
+            if (__syncthreads_and(here ? 1 : 0) == 0) {
+                if (tid == 0) p.status[t.b] = TV_ERR_TIMEOUT;
+                break;
+            }
+        } else {
         __syncthreads();               // the previous tile's P and V are done with
         for (int e = tid; e < CF_N * (DP / 4); e += CF_THREADS) {
             const int r = e / (DP / 4), c = e % (DP / 4);
@@ -160,6 +187,7 @@ __global__ void __launch_bounds__(CF_THREADS) chunk_attn_kernel(CfParams p) {
             *reinterpret_cast<float4*>(sv + r * DP + 4 * c) = y;
         }
         __syncthreads();
+        }
         // S: rows ty * 8 + i, keys tx + 16 u
         float s[8][4];
 #pragma unroll
