@@ -7,16 +7,19 @@
 // 64-key tiles: S = Q K^T, running maximum and sum, O = O 2^(m - m') + P V.
 // Bound by float32 multiply-adds: 4 d per (row, key).  128 threads, each an 8 x 4
 // patch of S and an 8 x d/16 patch of O in registers, so that a step of the
-// inner loops is 12 shared-memory loads of 16 bytes for 128 multiply-adds.
+// inner loops is 12 shared-memory loads of 16 bytes for 128 multiply-adds, which go two by
+// two (packed; sums over even and odd columns apart).  K and V come by one bulk copy per row.
 // When the rows are too few to fill the GPU the keys are cut into up to 16
 // parts; each part leaves its unnormalised O, maximum and sum in the workspace
 // and a second kernel joins them in order.
 // Batches of about one token per sequence take a second form, further down.
-// Measured: 1,000 rows of 32/8 heads of 128 after 3,000 keys 2.69 ms (21 TFLOP/s); 316 rows of 2 heads of 64 after up to 900 keys 25 us, of which two launches
+// Measured: 1,000 rows of 32/8 heads of 128 after 3,000 keys 1.64 ms (35 TFLOP/s; 2.02 with
+// single multiply-adds, 2.69 with rows through registers); 316 rows of 2 heads of 64 after up to 900 keys 25 us, of which two launches
 // and one item's way through the tiles are nearly all.
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "tv_chunk.cuh"
 #include "tv_internal.h"
@@ -190,10 +193,11 @@ __global__ void __launch_bounds__(CF_THREADS) chunk_attn_kernel(CfParams p) {
         }
         // S: rows ty * 8 + i, keys tx + 16 u
         float s[8][4];
+        uint64_t s2[8][4];             // sums over even and odd columns
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) s[i][u] = 0.f;
+            for (int u = 0; u < 4; ++u) s2[i][u] = 0ull;
         for (int c = 0; c < p.d; c += 4) {
             float4 b4[4];
 #pragma unroll
@@ -203,13 +207,19 @@ __global__ void __launch_bounds__(CF_THREADS) chunk_attn_kernel(CfParams p) {
                 const float4 a4 = *reinterpret_cast<const float4*>(sq + (ty * 8 + i) * LD + c);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    s[i][u] = fmaf(a4.x, b4[u].x, s[i][u]);
-                    s[i][u] = fmaf(a4.y, b4[u].y, s[i][u]);
-                    s[i][u] = fmaf(a4.z, b4[u].z, s[i][u]);
-                    s[i][u] = fmaf(a4.w, b4[u].w, s[i][u]);
+                    s2[i][u] = f2_fma(f2_pack(a4.x, a4.y), f2_pack(b4[u].x, b4[u].y), s2[i][u]);
+                    s2[i][u] = f2_fma(f2_pack(a4.z, a4.w), f2_pack(b4[u].z, b4[u].w), s2[i][u]);
                 }
             }
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float lo, hi;
+                f2_unpack(s2[i][u], lo, hi);
+                s[i][u] = lo + hi;
+            }
         __syncthreads();               // every thread is done with K
         // whether every key of the tile is visible to every row
         const bool full = t0 + CF_N - 1 <= t.P + i_lo &&
@@ -248,6 +258,7 @@ __global__ void __launch_bounds__(CF_THREADS) chunk_attn_kernel(CfParams p) {
         }
         __syncwarp();                  // a row's P is written and read by one half warp
         // O: columns 64 c + 4 tx + e
+        auto add = [&](auto all) {
         for (int k = 0; k < CF_N; k += 4) {
             float4 a4[8];
 #pragma unroll
@@ -262,16 +273,17 @@ __global__ void __launch_bounds__(CF_THREADS) chunk_attn_kernel(CfParams p) {
                     for (int i = 0; i < 8; ++i) {
                         const float w = kk == 0 ? a4[i].x : kk == 1 ? a4[i].y : kk == 2 ? a4[i].z : a4[i].w;
                         // a masked key's value must not reach the row even if it is not finite
-                        if (full || w != 0.f) {
-                            o[i][c][0] = fmaf(w, v4.x, o[i][c][0]);
-                            o[i][c][1] = fmaf(w, v4.y, o[i][c][1]);
-                            o[i][c][2] = fmaf(w, v4.z, o[i][c][2]);
-                            o[i][c][3] = fmaf(w, v4.w, o[i][c][3]);
+                        if (decltype(all)::value || w != 0.f) {
+                            f2_unpack(f2_fma(f2_pack(w, w), f2_pack(v4.x, v4.y), f2_pack(o[i][c][0], o[i][c][1])), o[i][c][0], o[i][c][1]);
+                            f2_unpack(f2_fma(f2_pack(w, w), f2_pack(v4.z, v4.w), f2_pack(o[i][c][2], o[i][c][3])), o[i][c][2], o[i][c][3]);
                         }
                     }
                 }
             }
         }
+        };
+        if (full) add(std::true_type{});
+        else add(std::false_type{});
     }
     if (p.splits > 1) {
         float* slot = p.part + (((int64_t)tile_id * p.Hkv + g) * p.splits + split) * (CF_M * (p.d + 2));
