@@ -136,7 +136,6 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
     pdl_wait();
     // A slice of a row: the 16-byte pieces that lie inside by a bulk copy (issued by thread 0),
     // up to 7 entries at each end and a grammar word by each thread, a row ahead.
-    E edge{};
     auto ahead = [&](const void* lo, size_t bytes) {     // to L2: the 16-byte pieces inside
         const uintptr_t a = (reinterpret_cast<uintptr_t>(lo) + 15) & ~(uintptr_t)15;
         const uintptr_t z = (reinterpret_cast<uintptr_t>(lo) + bytes) & ~(uintptr_t)15;
@@ -160,8 +159,9 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
         }
         const int x = tid < head ? tid : end + tid - head;
         if (x < n && tid < 16) {
-            if constexpr (F32) cp_async_4(raw + a / sizeof(E) % (16 / sizeof(E)) + x, lo + x);
-            else edge = lo[x];
+            E* to = raw + a / sizeof(E) % (16 / sizeof(E)) + x;
+            if constexpr (F32) cp_async_4(to, lo + x);
+            else *to = lo[x];
         }
         if (p.grammar && tid * 32 < n) cp_async_4(s_gram + 1 + tid, p.grammar + row * p.words + x0 / 32 + tid);
     };
@@ -262,11 +262,6 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
         const int rsh = (int)((reinterpret_cast<uintptr_t>(static_cast<const E*>(p.logits) + row * p.V + x0) / sizeof(E)) %
                               (16 / sizeof(E)));
         {
-            if constexpr (!F32) {
-                const int head = min(n, (8 - rsh) % 8), end = max(head, ((rsh + n) & ~7) - rsh);
-                const int x = tid < head ? tid : end + tid - head;
-                if (x < n && tid < 16) raw[x + rsh] = edge;
-            }
             cp_async_wait_all();
             if (tid == 0) s_gram[1 + (n + 31) / 32] = 0u;
             // positions beside the slice weigh nothing
