@@ -528,9 +528,8 @@ tv_status launch_logits(const LogitsArgs& a, LgParams p) {
     p.rows = (int64_t)a.B * a.N;
     if (cluster) {
         // the fewest CTAs that hold the row; up to 8 when that leaves SMs without work
-        int cs = 1;
-        while (cs < LG_CLUSTER_MAX && (int64_t)cs * LG_SLICE_MAX < a.V) cs *= 2;
-        while (cs < 8 && p.rows * cs < device_sm_count() && a.V > cs * 4096) cs *= 2;
+        int cs = (a.V + LG_SLICE_MAX - 1) / LG_SLICE_MAX;
+        while (cs <= 4 && p.rows * cs < device_sm_count() && a.V > cs * 4096) cs *= 2;
         p.slices = cs;
     } else {
         p.slices = (a.V + LG_PLAIN_SLICE - 1) / LG_PLAIN_SLICE;

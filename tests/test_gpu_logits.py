@@ -198,6 +198,17 @@ def test_node_counts_and_bad_sequences(tv, probs):
     assert out[3:].eq(bad).all()
 
 
+@pytest.mark.parametrize("k", range(1, 17))
+def test_probs_of_every_cluster_size(tv, k):
+    """Rows that k CTAs just hold, of odd lengths."""
+    V = 16352 * k - 7
+    c = case(1, 3, V, seed=k)
+    out, status = process(tv, c, True)
+    assert status.eq(0).all()
+    ref = R.logits(c["z"], probs=True, **c["kw"])
+    assert ((out.double() - ref).abs() <= tolerance(None, ref, c, True)).all()
+
+
 @pytest.mark.parametrize("probs", [False, True])
 def test_smallest_temperatures(tv, probs):
     """Down to the smallest normal number, whose reciprocal is finite; below it the sequence is
