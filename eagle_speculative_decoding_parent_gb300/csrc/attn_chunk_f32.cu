@@ -41,7 +41,7 @@ struct CfParams {
     int64_t q_stride, o_stride;   // elements
     int32_t* status;
     float* part;                  // [tiles][Hkv][splits] x (64 x d, 64 maxima, 64 sums)
-    int Hq, Hkv, G, d, window, splits, tiles;
+    int Hkv, G, d, window, splits, tiles;
     float scale, softcap;
 };
 
@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(CF_THREADS) chunk_attn_kernel(CfParams p) {
             }
             const bool here = mbar_wait(&landed, (uint32_t)(j - j0) & 1u);
             if (__syncthreads_and(here ? 1 : 0) == 0) {
+                mbar_wait(&landed, (uint32_t)(j - j0) & 1u);   // (copies still in flight)
                 if (tid == 0) p.status[t.b] = TV_ERR_TIMEOUT;
                 break;
             }
@@ -760,7 +761,6 @@ tv_status launch_chunk_attn_f32(const ChunkAttnArgs& a) {
     p.o_stride = a.out_stride;
     p.status = a.status;
     p.part = static_cast<float*>(a.ws);
-    p.Hq = a.Hq;
     p.Hkv = a.Hkv;
     p.G = a.Hq / a.Hkv;
     p.d = a.d;

@@ -127,7 +127,7 @@ struct Params {
     int32_t* status;
     int4* rec;                   // what the slots hold: (first row, tokens, kv head, PIECE_*)
     float* part;                 // partial results, two slots per CTA
-    int Hq, Hkv, G, npt, window;
+    int Hkv, G, npt, window;
     int prows;                   // rows of a partial result: 128 or 256
     float scale_log2;            // scale * log2(e); with a cap: 2 log2(e) scale / cap
     float cap_log2;              // cap * log2(e)
@@ -1354,7 +1354,6 @@ tv_status launch_chunk_attn_tc(const ChunkAttnArgs& a) {
     p.status = a.status;
     p.rec = static_cast<int4*>(a.ws);
     p.part = reinterpret_cast<float*>(p.rec + 2 * device_sm_count());
-    p.Hq = a.Hq;
     p.Hkv = a.Hkv;
     p.G = G;
     p.npt = npt;

@@ -375,6 +375,7 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
         fence_proxy_async_smem();                        // the next copy lands where this row was
         if (__syncthreads_and(alive ? 1 : 0) == 0) {     // a wait ran out, in this row or the last
             if (tid == 0) p.status[b] = TV_ERR_TIMEOUT;
+            mbar_wait_sleep(&full, (got - 1u) & 1u);     // (a copy still in flight)
             break;
         }
         if (row + 1 < row_hi) fetch(row + 1, b, i + 1 < p.N);

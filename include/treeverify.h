@@ -510,6 +510,10 @@ tv_status chunk_kv_append(const void* q, int64_t q_stride, const void* k, int64_
  * workspace: chunk_attention_workspace() bytes, 16-byte aligned, any contents;
  * partial results of rows whose keys are split over several SMs.  Missing or
  * smaller: TV_ERR_WORKSPACE.
+ * Other host errors: TV_ERR_INVALID_ARG for sizes, NULL or (16 bytes) misaligned
+ * pointers, strides smaller than a row, a softcap that is NaN or infinite;
+ * TV_ERR_UNSUPPORTED for other head or block sizes, a stride that is no multiple
+ * of 16 bytes, or a bfloat16 cache of 2^31 rows (blocks x heads x block size).
  * ------------------------------------------------------------------------ */
 size_t chunk_attention_workspace(int T, int B, int Hq, int Hkv, int d, tv_dtype dt);
 
