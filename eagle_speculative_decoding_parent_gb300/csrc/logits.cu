@@ -305,8 +305,26 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
         const bool skip = absent() || r.err != TV_OK;
         __syncthreads();
         if constexpr (!F32) {
-            // bfloat16: widen into the float buffer
-            for (int x = tid; x < n; x += LG_THREADS) zs[x + sh] = lg_float(raw[x + rsh]);
+            // bfloat16: widen into the float buffer, four at a time where both are aligned alike
+            if (((rsh ^ sh) & 3) == 0) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    const int q = (k * LG_THREADS + tid) * 4, x = q - sh;
+                    const uint2 u = *reinterpret_cast<const uint2*>(raw + q + (rsh - sh));
+                    float4 v = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                                           __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+                    if (x >= 0 && x + 4 <= n) {
+                        *reinterpret_cast<float4*>(zs + q) = v;
+                    } else {
+                        const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (x + e >= 0 && x + e < n) zs[q + e] = f[e];
+                    }
+                }
+            } else {
+                for (int x = tid; x < n; x += LG_THREADS) zs[x + sh] = lg_float(raw[x + rsh]);
+            }
         }
         // (float32: in and out rows may be aligned differently; then the entries move first)
         float* zr = F32 ? reinterpret_cast<float*>(raw) : zs;
