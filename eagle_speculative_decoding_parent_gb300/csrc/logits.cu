@@ -21,7 +21,9 @@
 // The shared memory leaves some 20 KB of L1: a few spilled registers of 1,024 threads do
 // not fit and come back from L2 in every row, so the row loop keeps its state in shared
 // memory and spills nothing (832 rows of 128,256 float32 probabilities 256 -> 182 us,
-// 4.9 TB/s, without history, biases and grammar 137; 24 rows of 152,064 bfloat16 logits 17).
+// 4.9 TB/s, without history, biases and grammar 137; from bfloat16 195; 24 rows of 152,064
+// bfloat16 logits 15).  Histories and biases with more entries than the list holds (some
+// 4,500 per slice) are gone through in every row.
 #include <cuda_bf16.h>
 #include <float.h>
 #include <math.h>
@@ -94,17 +96,17 @@ __device__ __forceinline__ float lg_max3(float a, float b, float c) {
     asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-__device__ __forceinline__ float lg_float(float x) { return x; }
-__device__ __forceinline__ float lg_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 template <typename E, bool PROBS, int NV>
 __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgParams p) {
     constexpr bool F32 = sizeof(E) == 4;
     constexpr int CAP = LG_THREADS * 4 * NV;             // positions of the slice buffer
     extern __shared__ __align__(128) uint8_t lg_smem[];
-    float* zs = reinterpret_cast<float*>(lg_smem);       // [CAP] the slice, entry x at zs[x + sh]
-    E* raw = reinterpret_cast<E*>(F32 ? lg_smem : lg_smem + CAP * 4);   // [CAP + 8] as it comes
-    uint32_t* s_gram = reinterpret_cast<uint32_t*>(lg_smem + CAP * 4 + (F32 ? 0 : CAP * 2 + 16));  // [CAP / 32 + 2]
+    float* zs = reinterpret_cast<float*>(lg_smem);       // [CAP] the slice, entry x at zs[x + shift]
+    // the slice as it comes; bfloat16: the buffer's second half and 8 entries more, widened in
+    // place through registers
+    E* raw = reinterpret_cast<E*>(F32 ? lg_smem : lg_smem + CAP * 2);
+    uint32_t* s_gram = reinterpret_cast<uint32_t*>(lg_smem + CAP * 4 + (F32 ? 0 : 16));  // [CAP / 32 + 2]
     uint2* list = reinterpret_cast<uint2*>(s_gram + CAP / 32 + 2);      // (word, bias)
     __shared__ int tok[64];
     // The sequence's state: in shared memory, since registers that hold it would be spilled, and
@@ -296,34 +298,43 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
             cp_async_wait_all();
             if (tid == 0) s_gram[1 + (n + 31) / 32] = 0u;
             // positions beside the slice weigh nothing
-            const int zsh = F32 ? rsh : sh;
-            if (tid < zsh) zs[tid] = -INFINITY;
-            for (int q = zsh + n + tid; q < CAP; q += LG_THREADS) zs[q] = -INFINITY;
+            if constexpr (F32) {
+                if (tid < rsh) zs[tid] = -INFINITY;
+                for (int q = rsh + n + tid; q < CAP; q += LG_THREADS) zs[q] = -INFINITY;
+            }
         }
         const uint64_t m = masks[i];
         auto absent = [&]() -> bool { return r.cnt >= 1 && r.cnt <= p.N && i >= r.cnt; };
         const bool skip = absent() || r.err != TV_OK;
         __syncthreads();
         if constexpr (!F32) {
-            // bfloat16: widen into the float buffer, four at a time where both are aligned alike
-            if (((rsh ^ sh) & 3) == 0) {
+            // bfloat16: widened, four at a time where both are aligned alike
+            uint2 u[NV];
 #pragma unroll
-                for (int k = 0; k < NV; ++k) {
-                    const int q = (k * LG_THREADS + tid) * 4, x = q - sh;
-                    const uint2 u = *reinterpret_cast<const uint2*>(raw + q + (rsh - sh));
-                    float4 v = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                                           __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-                    if (x >= 0 && x + 4 <= n) {
-                        *reinterpret_cast<float4*>(zs + q) = v;
-                    } else {
-                        const float f[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (x + e >= 0 && x + e < n) zs[q + e] = f[e];
-                    }
+            for (int k = 0; k < NV; ++k) {
+                const int q = (k * LG_THREADS + tid) * 4, x = q - sh;
+                if (((rsh ^ sh) & 3) == 0) {
+                    u[k] = *reinterpret_cast<const uint2*>(raw + q + (rsh - sh));
+                } else {
+                    const uint16_t* h = reinterpret_cast<const uint16_t*>(raw) + rsh;
+                    auto one = [&](int e) -> uint32_t { return x + e >= 0 && x + e < n ? h[x + e] : 0u; };
+                    u[k] = make_uint2(one(0) | one(1) << 16, one(2) | one(3) << 16);
                 }
-            } else {
-                for (int x = tid; x < n; x += LG_THREADS) zs[x + sh] = lg_float(raw[x + rsh]);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int q = (k * LG_THREADS + tid) * 4, x = q - sh;
+                float4 v = make_float4(__uint_as_float(u[k].x << 16), __uint_as_float(u[k].x & 0xffff0000u),
+                                       __uint_as_float(u[k].y << 16), __uint_as_float(u[k].y & 0xffff0000u));
+                if (x < 0 || x + 4 > n) {
+                    // positions beside the slice weigh nothing
+                    if (x < 0 || x >= n) v.x = -INFINITY;
+                    if (x + 1 < 0 || x + 1 >= n) v.y = -INFINITY;
+                    if (x + 2 < 0 || x + 2 >= n) v.z = -INFINITY;
+                    if (x + 3 < 0 || x + 3 >= n) v.w = -INFINITY;
+                }
+                *reinterpret_cast<float4*>(zs + q) = v;
             }
         }
         // (float32: in and out rows may be aligned differently; then the entries move first)
@@ -489,7 +500,7 @@ template <typename E, bool PROBS, int NV>
 tv_status launch_nv(LgParams p, cudaStream_t stream) {
     auto fn = tree_logits_kernel<E, PROBS, NV>;
     constexpr int CAP = LG_THREADS * 4 * NV;
-    const size_t fixed = CAP * 4 + (sizeof(E) == 4 ? 0 : CAP * 2 + 16) + (CAP / 32 + 2) * 4;
+    const size_t fixed = CAP * 4 + (sizeof(E) == 4 ? 0 : 16) + (CAP / 32 + 2) * 4;
     p.list_max = (p.counts || p.bias) ? std::min<int>(p.slice, (int)((LG_SMEM - fixed) / 8)) : 0;
     const size_t smem = fixed + (size_t)p.list_max * 8;
     int dev = 0;
