@@ -23,7 +23,7 @@
 // memory and spills nothing (832 rows of 128,256 float32 probabilities 256 -> 182 us,
 // 4.9 TB/s, without history, biases and grammar 137; from bfloat16 195; 24 rows of 152,064
 // bfloat16 logits 15).  Histories and biases with more entries than the list holds (some
-// 4,500 per slice) are gone through in every row.
+// 4,500 per slice) are gone through in every row (both dense: 271 us for the 832 rows).
 #include <cuda_bf16.h>
 #include <float.h>
 #include <math.h>
@@ -370,7 +370,21 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
             } else {
                 // more counts and biases than the list holds: all of them, from L2
                 __syncthreads();
-                for (int x = tid; x < n; x += LG_THREADS) {
+                const bool wide = ((reinterpret_cast<uintptr_t>(p.counts) | reinterpret_cast<uintptr_t>(p.bias) |
+                                    (uintptr_t)at * 4) & 15) == 0;
+                const int four = wide ? n & ~3 : 0;
+#pragma unroll 1
+                for (int x = tid * 4; x < four; x += LG_THREADS * 4) {
+                    int4 c = make_int4(0, 0, 0, 0);
+                    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (p.counts) c = *reinterpret_cast<const int4*>(p.counts + at + x);
+                    if (p.bias) f = *reinterpret_cast<const float4*>(p.bias + at + x);
+                    change(x, c.x, f.x);
+                    change(x + 1, c.y, f.y);
+                    change(x + 2, c.z, f.z);
+                    change(x + 3, c.w, f.w);
+                }
+                for (int x = four + tid; x < n; x += LG_THREADS) {
                     const int c = p.counts ? p.counts[at + x] : 0;
                     const float bs = p.bias ? p.bias[at + x] : 0.f;
                     if (c != 0 || bs != 0.f) change(x, c, bs);
