@@ -29,6 +29,16 @@ int device_smem_optin() {
     return cached_attr(cudaDevAttrMaxSharedMemoryPerBlockOptin, cache);
 }
 
+LateWait test_late_wait() {
+    LateWait l;
+    if (const char* e = getenv("TV_TEST_WAITS_RUN_OUT")) {
+        char* end = nullptr;
+        l.warp = (int)strtol(e, &end, 10);
+        if (*end == '@') l.cta = (int)strtol(end + 1, nullptr, 10);
+    }
+    return l;
+}
+
 }  // namespace tv
 
 using namespace tv;

@@ -50,8 +50,10 @@
 // tiles of two full row tiles takes 1.65 us, of which the softmax is the longer half; an
 // exponential by polynomial for a part of the scores is slower (573-680 us), as are four
 // softmax warpgroups.
-// Every wait is bounded; one that runs out sets the abort flag, and the roles
-// leave after their copies and products in flight are done.
+// Every wait is bounded; one that runs out sets the abort flag, which ends the other
+// roles' waits, and the roles leave after their copies and products in flight are done.
+// The CTA's records then name the sequences of its run, and the second kernel, behind
+// every TV_OK, gives them TV_ERR_TIMEOUT.
 #include <algorithm>
 #include <cmath>
 
@@ -91,8 +93,9 @@ struct Item {
     int t_lo, t_hi, fa, fb; // key tiles of this piece; tiles < fa or >= fb need masks
     int flags, slot, n, pad;  // slot: partial result, or -1; n: tiles to do (0: bad sequence)
 };
-// A slot's record: it holds a piece, and the piece is the item's last one.
-constexpr int PIECE = 1, PIECE_LAST = 2;
+// A slot's record: it holds a piece, and the piece is the item's last one; or a wait of the CTA
+// ran out (then the record is: first and last sequence of its run).
+constexpr int PIECE = 1, PIECE_LAST = 2, PIECE_LATE = 4;
 constexpr int ITEM_END = 1, ITEM_TWO = 2, ITEM_BAD = 4, ITEM_STATUS = 8;
 static_assert(sizeof(Item) == 64, "four 16-byte words");
 
@@ -107,12 +110,13 @@ struct Lay {
     static constexpr int OFF_Q = SLOTS * SLOT_BYTES;       // two row tiles
     static constexpr int OFF_X = OFF_Q + Q_BYTES;          // epilogue of one row tile: the second Q tile
     static constexpr int OFF_ITEMS = OFF_Q + 2 * Q_BYTES;  // [GQ]
-    static constexpr int OFF_BAD = OFF_ITEMS + GQ * 64;    // [FIX_BUFS][FIX_TILES][4]
-    static constexpr int OFF_BARS = OFF_BAD + FIX_BUFS * FIX_TILES * 16;
+    static constexpr int OFF_MISC = OFF_ITEMS + GQ * 64;   // tensor memory's address, abort flag
+    static constexpr int OFF_BARS = OFF_MISC + 16;
     static constexpr int NBARS = 3 * SLOTS + 8 + 4 + 2 * GQ + 2;
-    static constexpr int OFF_ML = OFF_BARS + NBARS * 8;    // join: maximum, sum per row
-    static constexpr int OFF_MISC = OFF_ML + 2 * MT * 4;
-    static constexpr int BYTES = OFF_MISC + 16 + 1024;     // + alignment slack
+    static constexpr int OFF_BAD = OFF_BARS + (NBARS * 8 + 15) / 16 * 16;  // [FIX_BUFS][FIX_TILES][4]
+    static constexpr int OFF_ML = OFF_BAD + FIX_BUFS * FIX_TILES * 16;  // join: maximum, sum per row
+    static constexpr int BYTES = OFF_ML + 2 * MT * 4 + 1024;   // + alignment slack
+    static_assert(OFF_ITEMS % 1024 == 0 && OFF_BAD - OFF_ITEMS <= 1024, "the barriers beside the abort flag");
 };
 static_assert(Lay<128>::BYTES <= 232448 && Lay<64>::BYTES <= 232448, "shared memory of one SM");
 
@@ -133,6 +137,7 @@ struct Params {
     float cap_log2;              // cap * log2(e)
     float cap_x, cap_small;      // scale / cap; products with s^2 < cap_small take the polynomial
     float cap_c[3];              // its coefficients in s^2: scale * log2(e) * (scale / cap)^(2e) * TANH_C[e]
+    LateWait late;               // test-only
 };
 
 // tanh(x) / x as a polynomial in x^2 for |x| <= 0.35: interpolated at the Chebyshev nodes of
@@ -243,21 +248,28 @@ __device__ __forceinline__ int64_t run_start(const Runs& r, int i) {
 // other).  TRIES polls, each of which may suspend the warp, come before it: the
 // waits of the products and of the softmax are on the critical path, and reading
 // the clock costs more than a poll.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity) {
+// The abort flag ends a wait early, but not one for the role's own copies or products (`own`).
+// It lies in the 1,024 bytes that hold the barriers, so that its address needs no register.
+constexpr uint32_t ABORT_AT = GQ * 64 + 4;
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, bool own) {
     const uint64_t t0 = globaltimer_ns();
 #pragma unroll 1
-    while (!mbar_try_wait(bar, parity))
-        if (globaltimer_ns() - t0 > TV_WAIT_NS) return false;
+    while (!mbar_try_wait(bar, parity)) {
+        uint32_t late;
+        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(late) : "r"((smem_u32(bar) & ~1023u) + ABORT_AT));
+        if ((late != 0 && !own) || globaltimer_ns() - t0 > TV_WAIT_NS) return false;
+    }
     return true;
 }
 template <int TRIES = 1>
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, bool own = false) {
     bool ok = mbar_try_wait(bar, parity);
 #pragma unroll 1
     for (int k = 1; k < TRIES && !ok; ++k) ok = mbar_try_wait(bar, parity);
-    if (!ok) ok = wait_slow(bar, parity);
+    if (!ok) ok = wait_slow(bar, parity, own);
     return __all_sync(0xffffffffu, ok);
 }
+__device__ __forceinline__ void wait_own(uint64_t* bar, uint32_t parity) { wait_all(bar, parity, true); }
 
 // The same for warp 8, which has nothing to spare: it polls, and leaves the loop only
 // to look at the clock.
@@ -266,6 +278,33 @@ __device__ __forceinline__ bool wait_mma(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
     for (int k = 0; k < 256 && !ok; ++k) ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
     return ok || wait_all(bar, parity);
+}
+
+// After a wait ran out, by one thread: the sequences with units in this CTA's run get
+// TV_ERR_TIMEOUT, and the CTA's records their range, for the second kernel to repeat it (the
+// first CTA of a sequence may write its TV_OK later).  The run is found again, so that nothing
+// about it is kept in registers for this.
+__device__ __noinline__ void report_late(const Params& p) {
+    int64_t total = 0;
+    for (int b = 0; b < p.c.B; ++b) {
+        const int lo = p.c.q_start[b], hi = p.c.q_start[b + 1];
+        if (lo < 0 || lo > hi || hi > p.c.T) return;       // (every sequence has its status)
+        total += seq_units(p, p.c.prefix[b], hi - lo);
+    }
+    const Runs runs = runs_of(p, total, gridDim.x);
+    const int64_t x_lo = run_start(runs, blockIdx.x), x_hi = run_start(runs, blockIdx.x + 1);
+    int first = 0, last = -1;
+    int64_t at = 0;
+    for (int b = 0; b < p.c.B && at < x_hi; ++b) {
+        const int64_t end = at + seq_units(p, p.c.prefix[b], p.c.q_start[b + 1] - p.c.q_start[b]);
+        if (end > at && end > x_lo) {
+            if (last < 0) first = b;
+            last = b;
+            p.status[b] = TV_ERR_TIMEOUT;
+        }
+        at = end;
+    }
+    p.rec[2 * blockIdx.x] = p.rec[2 * blockIdx.x + 1] = make_int4(first, last, 0, PIECE_LATE);
 }
 
 // S = Q K^T of one tile (M = N = 128), then a commit to `bar`: one elected lane of the
@@ -424,7 +463,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     uint64_t* xall = vraw + L::SLOTS;     // [2] every softmax warp has written xo, has read xo
     auto* tmp = reinterpret_cast<ChunkLocateTmp<THREADS>*>(smem + L::OFF_RING);  // before the first copy
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_ITEMS + ABORT_AT);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = smem_u32(smem);
@@ -499,10 +538,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     fence_proxy_async_smem();  // the ring's first bytes held the search's scratch
     ok0 = __syncthreads_and(ok0 ? 1 : 0) != 0;
 
-    // Work item k, from the queue; false at the end (or after a timeout).
+    // (test-only: this warp's first wait for work counts as run out)
+    bool alive = !(p.late.warp == warp && (p.late.cta < 0 || p.late.cta == (int)blockIdx.x));
+    // Work item k, from the queue; false at the end, or (alive false) after a timeout.
     auto take = [&](uint32_t k, Item& it) -> bool {
         const int s = k % GQ;
-        const bool got = wait_all(&gq_full[s], (k / GQ) & 1u);
+        alive = wait_all(&gq_full[s], (k / GQ) & 1u);
         const int4* src = reinterpret_cast<const int4*>(&items[s]);
         int4* dst = reinterpret_cast<int4*>(&it);
 #pragma unroll
@@ -510,7 +551,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         __syncwarp();
         // "slot read": no release needed, and a release would wait for the epilogue's stores
         if (lane == 0) remote_arrive_relaxed_after(&gq_empty[s], 0, it.b | it.row0 | it.t_lo | it.n);
-        return got && !(it.flags & ITEM_END);
+        return alive && !(it.flags & ITEM_END);
     };
 
     if (warp == SCHED_WARP) {
@@ -531,8 +572,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             ++k;
             return true;
         };
-        bool alive = true;
-        if (at.b < p.c.B) {
+        if (alive && at.b < p.c.B) {
             int b = at.b, g, qk;
             Seq s = s0;
             bool ok = ok0;
@@ -597,10 +637,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         if (alive) {
             Item it{};
             it.flags = ITEM_END;
-            publish(it);
-        } else if (lane == 0) {
-            *abort_flag = 1;
+            alive = publish(it);
         }
+        if (!alive && lane == 0) *abort_flag = 1;
     } else if (warp == LOAD_WARP) {
         // ============================ K/V producer ============================
         if (lane == 0) {
@@ -609,7 +648,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         }
         uint32_t ld = 0, slot = 0, ph = 0; // slots filled so far; the next one, its round's parity
         uint32_t raw = 0, raw_ph = 0;      // per slot: last filled through vraw, and vraw's next parity
-        bool alive = true;
         Item it;
         for (uint32_t k = 0; alive && take(k, it); ++k) {
             if (it.n == 0) continue;
@@ -652,11 +690,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 uint8_t* dst = smem + L::OFF_RING + slot * L::SLOT_BYTES + (lane & 7) * L::PAGE_BYTES;
                 // a V tile at the edges goes through warp 10, which passes it on
                 const uint32_t edge = is_v && (t < it.fa || t >= it.fb) ? 1u : 0u;
-                raw = (raw & ~(1u << slot)) | (edge << slot);
-                raw_ph ^= edge << slot;
                 uint64_t* bar = edge ? &vraw[slot] : &full[slot];
                 alive = wait_all<64>(&empty[slot], ph ^ 1u);
                 if (!alive) break;
+                raw = (raw & ~(1u << slot)) | (edge << slot);
+                raw_ph ^= edge << slot;
                 mbar_arrive_expect_tx_relaxed_elect(bar, (uint32_t)pages * L::PAGE_BYTES);
                 if (lane < pages) {
                     if constexpr (D == 128) {
@@ -678,14 +716,13 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         // copies in flight end before the CTA does
         for (uint32_t u = ld > (uint32_t)L::SLOTS ? ld - L::SLOTS : 0; u < ld; ++u) {
             const uint32_t s = u % L::SLOTS;
-            if ((raw >> s) & 1u) wait_all(&vraw[s], ((raw_ph >> s) & 1u) ^ 1u);
-            else wait_all(&full[s], (u / L::SLOTS) & 1u);
+            if ((raw >> s) & 1u) wait_own(&vraw[s], ((raw_ph >> s) & 1u) ^ 1u);
+            else wait_own(&full[s], (u / L::SLOTS) & 1u);
         }
     } else if (warp == MMA_WARP) {
         // ============================== products ==============================
         uint32_t slot = 0, par = 0;                    // next ring position: slot, parity of its round
         uint32_t qi = 0, ppar = 0, opar = 3;           // ppar, opar: parity bit per stream
-        bool alive = true;
         Item it;
         const uint32_t ring = sbase + L::OFF_RING;
         const uint64_t qd = smem_desc_sw128(sbase + L::OFF_Q, 16, 1024);
@@ -786,13 +823,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         if (!alive && lane == 0) *abort_flag = 1;
         // products in flight end before the tensor memory is freed
         tc_commit_elect(drain);
-        wait_all(drain, 0);
+        wait_own(drain, 0);
     } else if (warp == FIX_WARP) {
         // ==================== Q tiles, V rows that must not reach O ====================
         if (lane == 0) tma_prefetch_desc(&qmap);
         const uint64_t qpol = l2_policy_evict_first();
         uint32_t ld = 0, qi = 0, xi = 0, ph = 0;             // ph: vraw's parity per slot
-        bool alive = true;
         Item it;
         for (uint32_t k = 0; alive && take(k, it); ++k) {
             if (it.n == 0) continue;
@@ -874,7 +910,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             ld += 2 * n;
         }
         if (!alive && lane == 0) *abort_flag = 1;
-        if (qi > 0) wait_all(qfull, (qi - 1) & 1u);          // its own copies in flight
+        if (qi > 0) wait_own(qfull, (qi - 1) & 1u);          // its own copies in flight
     } else {
         // ============================== softmax ==============================
         const int i = warp >> 2;                              // stream
@@ -884,7 +920,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         float* xo = reinterpret_cast<float*>(smem + L::OFF_X);  // [columns][rows]
         float* ml = reinterpret_cast<float*>(smem + L::OFF_ML);
         uint32_t sc = 0, oc = 0, live = 0, xc = 0;
-        bool alive = true;
         // every softmax warp has written xo (0), has read it (1): with a bounded wait, unlike
         // bar.sync
         auto all_x = [&](int which) {
@@ -900,7 +935,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             // the item stays in its slot, which is given back at its end: its fields in registers
             // would be spilled beside the scores, and L1 is too small to hold what is spilled
             const Item& it = items[k % GQ];
-            if (!wait_all(&gq_full[k % GQ], (k / GQ) & 1u) || (it.flags & ITEM_END)) break;
+            alive = wait_all(&gq_full[k % GQ], (k / GQ) & 1u);
+            if (!alive || (it.flags & ITEM_END)) break;
             const bool two = (it.flags & ITEM_TWO) != 0;
             const int n = it.n, ja = it.fa - it.t_lo, jb = it.fb - it.t_lo;
             if ((it.flags & ITEM_STATUS) && tid == 0)
@@ -1236,12 +1272,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     __syncthreads();
     tc_fence_after();
     if (warp == MMA_WARP) tmem_dealloc(tmem, 512);
+    if (tid == 0 && *abort_flag != 0) report_late(p);
 }
 
 // Joins the pieces of the items that run borders cut: the CTA of slot 2 r + 1 (an item
 // that starts in run r and goes on) and 32 columns.  The pieces that follow are in the
 // slots 2 (r + 1), 2 (r + 2), ... up to the last one; weights 2^(m_k - max) on the
-// unnormalised rows, in run order.
+// unnormalised rows, in run order.  A run with a wait that ran out: its sequences' statuses,
+// again; an item that it cut gives zeros.
 constexpr int JOIN_THREADS = 256;
 
 template <int D>
@@ -1253,6 +1291,9 @@ chunk_tc_join_kernel(const __grid_constant__ Params p, int ctas) {
     pdl_launch_dependents();
     int slot = 2 * blockIdx.x + 1;
     int4 rec = __ldcg(&p.rec[slot]);
+    if ((rec.w & PIECE_LATE) && c0 == 0)
+        for (int b = rec.x + (int)threadIdx.x; b <= rec.y; b += JOIN_THREADS)
+            if (p.c.q_start[b] != p.c.q_start[b + 1]) p.status[b] = TV_ERR_TIMEOUT;
     if (!(rec.w & PIECE) || tok_l >= p.npt || tok >= rec.y || row >= p.prows) return;
     const int row0 = rec.x, g = rec.z;
     float mx = -INFINITY, den = 0.f, acc[32];
@@ -1265,6 +1306,12 @@ chunk_tc_join_kernel(const __grid_constant__ Params p, int ctas) {
         const int ahead = slot + (slot & 1 ? 1 : 2);
         const bool more = !(rec.w & PIECE_LAST) && ahead < 2 * ctas;
         const int4 nrec = more ? __ldcg(&p.rec[ahead]) : rec;
+        if (rec.w & PIECE_LATE) {
+            den = 0.f;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+            break;
+        }
         if (rec.w & PIECE) {
             const float mk = __ldcg(sl + p.prows * D + row), lk = __ldcg(sl + p.prows * (D + 1) + row);
             float4 v[8];
@@ -1319,7 +1366,7 @@ tv_status launch(const ChunkAttnArgs& a, const Params& p, const CUtensorMap& qm,
     LaunchCfg lc(dim3((unsigned)ctas), dim3(THREADS), Lay<D>::BYTES, a.stream);
     if (cudaLaunchKernelEx(&lc.cfg, chunk_tc_kernel<D, CAP>, qm, km, vm, p) != cudaSuccess) return TV_ERR_CUDA;
     if (ctas == 1) return TV_OK;                               // nothing is cut
-    LaunchCfg lj(dim3((unsigned)(ctas - 1), D / 32), dim3(JOIN_THREADS), 0, a.stream);
+    LaunchCfg lj(dim3((unsigned)ctas, D / 32), dim3(JOIN_THREADS), 0, a.stream);
     return cudaLaunchKernelEx(&lj.cfg, chunk_tc_join_kernel<D>, p, ctas) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
 
@@ -1358,6 +1405,7 @@ tv_status launch_chunk_attn_tc(const ChunkAttnArgs& a) {
     p.G = G;
     p.npt = npt;
     p.window = a.window;
+    p.late = test_late_wait();
     p.prows = partial_rows(a.T, G);
     p.scale_log2 = a.softcap > 0.f ? 2.f * LOG2E * a.scale / a.softcap : a.scale * LOG2E;
     p.cap_log2 = a.softcap * LOG2E;

@@ -57,6 +57,14 @@ struct LaunchCfg {
 int device_sm_count();
 int device_smem_optin();
 
+// Test-only: TV_TEST_WAITS_RUN_OUT = "w" or "w@c" in the environment makes the first wait for work
+// or data of warp w (kernels without roles: of every warp) of CTA c (without @c: of every CTA)
+// count as run out, so that a test sees what is reported and nothing hangs.
+struct LateWait {
+    int warp = -1, cta = -1;  // -1: none, every CTA
+};
+LateWait test_late_wait();
+
 struct AttnArgs {
     const void* q;
     const void* k_cache;

@@ -503,7 +503,8 @@ tv_status chunk_kv_append(const void* q, int64_t q_stride, const void* k, int64_
  * n_b > max_blocks_per_seq * block_size, or a block id outside [0, num_blocks)
  * among the blocks that hold a key of K for some row of the sequence (blocks
  * wholly before the first row's window may have been given back: their table
- * entries are not read).
+ * entries are not read).  TV_ERR_TIMEOUT: a wait ran out in work on the sequence, or on another
+ * beside it; its rows of out are not all written.
  * Cache rows that no row of the sequence attends to are never read into a
  * result.  Where a key is outside K for one row and inside for another, its
  * contents reach only the rows that attend to it, infinities and NaN included.
