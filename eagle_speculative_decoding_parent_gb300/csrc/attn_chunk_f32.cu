@@ -43,7 +43,13 @@ struct CfParams {
     float* part;                  // [tiles][Hkv][splits] x (64 x d, 64 maxima, 64 sums)
     int Hkv, G, d, window, splits, tiles;
     float scale, softcap;
+    LateWait late;                // test-only
 };
+
+// Test-only: this CTA's waits for data count as run out.
+__device__ __forceinline__ bool cf_forced(const LateWait& l) {
+    return l.warp >= 0 && (l.cta < 0 || l.cta == (int)blockIdx.x);
+}
 
 template <typename E>
 __device__ __forceinline__ float4 cf_load4(const E* p);
@@ -169,7 +175,7 @@ __global__ void __launch_bounds__(CF_THREADS) chunk_attn_kernel(CfParams p) {
                 if (tid < CF_N) bulk_load(sk + r * LD, kc + at, (uint32_t)p.d * 4, &landed, policy);
                 else bulk_load(sv + r * DP, vc + at, (uint32_t)p.d * 4, &landed, policy);
             }
-            const bool here = mbar_wait(&landed, (uint32_t)(j - j0) & 1u);
+            const bool here = mbar_wait(&landed, (uint32_t)(j - j0) & 1u) && !cf_forced(p.late);
             if (__syncthreads_and(here ? 1 : 0) == 0) {
                 mbar_wait(&landed, (uint32_t)(j - j0) & 1u);   // (copies still in flight)
                 if (tid == 0) p.status[t.b] = TV_ERR_TIMEOUT;
@@ -430,6 +436,7 @@ struct CrParams {
     float* part;                  // [T][Hkv][splits] x (G x d, G maxima, G sums)
     int Hkv, G, d, window, splits;
     float scale, softcap;
+    LateWait late;                // test-only
 };
 
 template <int NJ, int R>
@@ -520,7 +527,7 @@ __global__ void __launch_bounds__(CR_THREADS) chunk_rows_kernel(CrParams p) {
     int blk = block(CR_STAGES);
     bool alive = true;
     for (int i = 0; i < steps; ++i) {
-        alive = __all_sync(0xffffffffu, mbar_wait(&bars[warp][i % CR_STAGES], (i / CR_STAGES) & 1));
+        alive = __all_sync(0xffffffffu, mbar_wait(&bars[warp][i % CR_STAGES], (i / CR_STAGES) & 1) && !cf_forced(p.late));
         if (!alive) break;
         const float* stage = mine + (i % CR_STAGES) * stage_floats + (lane >> 4) * CR_KEYS * p.d + 2 * l16;
         const int my_key = k_lo + i * STEP + (tid >> 4) * CR_KEYS + (l16 & (CR_KEYS - 1));
@@ -730,6 +737,7 @@ tv_status launch_rows(const ChunkAttnArgs& a) {
     p.d = a.d;
     p.window = a.window;
     p.splits = cr_splits(a.T, a.Hkv);
+    p.late = test_late_wait();
     p.scale = a.scale;
     p.softcap = a.softcap;
     if ((int64_t)a.T * p.splits > 0x7fffffff) return TV_ERR_UNSUPPORTED;
@@ -765,6 +773,7 @@ tv_status launch_chunk_attn_f32(const ChunkAttnArgs& a) {
     p.G = a.Hq / a.Hkv;
     p.d = a.d;
     p.window = a.window;
+    p.late = test_late_wait();
     p.scale = a.scale;
     p.softcap = a.softcap;
     const int64_t tiles = std::max<int64_t>(1, cf_tile_bound(a.T, a.B, p.G));

@@ -59,3 +59,14 @@ def test_one_cta_of_the_bfloat16_kernel(tv, monkeypatch, warp, cta):
     late = (status == 6).nonzero().view(-1).tolist()
     assert late == list(range(late[0], late[-1] + 1)) and len(late) < 10
     matches(c, out, status, [b for b in range(60) if b not in late])
+
+
+@pytest.mark.parametrize("n,P", [([1, 1, 0, 1], [40, 900, 7, 3000]), ([70, 0, 300, 1], [33, 2, 500, 1200])])
+def test_float32_kernels(tv, monkeypatch, n, P):
+    c = R.cache_case(n, P, Hq=4, Hkv=2, d=64, bs=16, dtype=torch.float32, seed=1)
+    monkeypatch.setenv("TV_TEST_WAITS_RUN_OUT", "0")
+    _, status = attend(tv, c)
+    assert status.tolist() == [6 if k else 0 for k in n]
+    monkeypatch.delenv("TV_TEST_WAITS_RUN_OUT")
+    out, status = attend(tv, c)
+    matches(c, out, status, range(4))
