@@ -22,6 +22,7 @@ from . import _build
 
 __all__ = ["TV_OK", "TV_ERR_BAD_TREE", "TV_ERR_OUT_OF_RANGE", "TV_ERR_UNSUPPORTED",
            "TV_ERR_TIMEOUT", "TV_ERR_BAD_VALUES", "TV_F32", "TV_BF16", "GREEDY", "STOCHASTIC",
+           "GREEDY_MASKED",
            "TreeVerifyError", "library_path", "status_string", "tree_mask_build",
            "tree_verify_attention_workspace", "tree_verify_attention_kernels", "tree_kv_append",
            "tree_verify_attention",
@@ -34,7 +35,7 @@ __all__ = ["TV_OK", "TV_ERR_BAD_TREE", "TV_ERR_OUT_OF_RANGE", "TV_ERR_UNSUPPORTE
 (TV_OK, TV_ERR_INVALID_ARG, TV_ERR_BAD_TREE, TV_ERR_OUT_OF_RANGE, TV_ERR_UNSUPPORTED,
  TV_ERR_CUDA, TV_ERR_TIMEOUT, TV_ERR_BAD_VALUES, TV_ERR_WORKSPACE) = range(9)
 TV_F32, TV_BF16 = 0, 1
-GREEDY, STOCHASTIC = 0, 1
+GREEDY, STOCHASTIC, GREEDY_MASKED = 0, 1, 2
 
 
 class TreeVerifyError(RuntimeError):

@@ -56,6 +56,7 @@ struct AccParams {
     int32_t* status;
     uint64_t data_wait_ns;  // row scan: limit of a wait for streamed data (TV_WAIT_NS)
     const int32_t* counts;  // nullable: nodes per sequence (its tree: the first counts[b] of N)
+    bool masked;            // greedy: -infinity never wins
 };
 
 // Node count of sequence b; nodes n..N-1 are absent (never checked or accepted).
@@ -72,6 +73,11 @@ struct ArgBest {
 // i == NO_INDEX carry no candidate (v is -inf there).
 __device__ __forceinline__ bool beats(float v, int i, float w, int j) {
     return (v > w) || (v == w && i < j);
+}
+
+// A row without an argmax: only NaNs or, where -infinity marks what is not allowed, nothing above it.
+__device__ __forceinline__ bool no_winner(const AccParams& p, const ArgBest& a) {
+    return a.i == NO_INDEX || (p.masked && a.v == -INFINITY);
 }
 
 __device__ __forceinline__ void take(ArgBest& a, float x, int i) {
@@ -469,7 +475,7 @@ accept_rows_kernel(AccParams p, int ch, int2* __restrict__ part, int32_t* __rest
                 x.i = j;
             }
         }
-        if (lane == 0) sam[r] = late ? TIMED_OUT : (x.i == NO_INDEX) ? -1 : x.i;
+        if (lane == 0) sam[r] = late ? TIMED_OUT : no_winner(p, x) ? -1 : x.i;
     }
     __syncthreads();
     if (tid < 32) {
@@ -582,7 +588,7 @@ accept_walk_kernel(AccParams p) {
                         x.i = j;
                     }
                 }
-                if (lane == 0) sam[u] = late ? TIMED_OUT : (x.i == NO_INDEX) ? -1 : x.i;
+                if (lane == 0) sam[u] = late ? TIMED_OUT : no_winner(p, x) ? -1 : x.i;
             }
         }
         __syncthreads();
@@ -1344,7 +1350,7 @@ size_t stoch_ws_sums(int B, int V) { return align256((size_t)B * ((V + PIECE - 1
 
 size_t accept_workspace(tv_accept_mode mode, int B, int N, int V) {
     if (B <= 0) return 0;
-    if (mode == TV_ACCEPT_GREEDY)
+    if (mode != TV_ACCEPT_STOCHASTIC)
         return prefer_rowscan(B, N, V) ? rows_ws(B, N).total : 0;
     return stoch_ws_sums(B, V) + align256((size_t)B * 4);
 }
@@ -1367,6 +1373,7 @@ tv_status launch_accept(const AcceptArgs& a) {
     p.max_path = a.max_path;
     p.status = a.status;
     p.counts = a.counts;
+    p.masked = a.mode == TV_ACCEPT_GREEDY_MASKED;
     // Test-only: TV_TEST_DATA_WAIT_NS shortens the row scan's waits for streamed
     // data (never the waits that drain copies still in flight), so a test can
     // make a legitimate wait run out and check the TV_ERR_TIMEOUT status.
@@ -1383,7 +1390,7 @@ tv_status launch_accept(const AcceptArgs& a) {
     if (need > 0 && (a.ws == nullptr || a.ws_bytes < need)) return TV_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     cudaError_t e;
-    if (a.mode == TV_ACCEPT_GREEDY && need > 0) {
+    if (a.mode != TV_ACCEPT_STOCHASTIC && need > 0) {
         const int64_t R = (int64_t)a.B * a.N;
         static int64_t cap = -1;
         if (cap < 0) cap = resident_ctas(accept_rows_kernel<true>, ROWS_SMEM, sms);
@@ -1395,7 +1402,7 @@ tv_status launch_accept(const AcceptArgs& a) {
         LaunchCfg lc(dim3((unsigned)(R * ch)), dim3(CH_THREADS), vec ? ROWS_SMEM : 0, a.stream);
         e = vec ? cudaLaunchKernelEx(&lc.cfg, accept_rows_kernel<true>, p, ch, part, st)
                 : cudaLaunchKernelEx(&lc.cfg, accept_rows_kernel<false>, p, ch, part, st);
-    } else if (a.mode == TV_ACCEPT_GREEDY) {
+    } else if (a.mode != TV_ACCEPT_STOCHASTIC) {
         const int C = walk_cluster_size(a.B, a.V);
         if (C <= 0) return TV_ERR_CUDA;
         if ((int64_t)a.B * C > 0x7fffffff) return TV_ERR_UNSUPPORTED;

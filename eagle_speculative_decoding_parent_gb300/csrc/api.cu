@@ -154,7 +154,8 @@ tv_status tree_accept(tv_accept_mode mode, const int32_t* parents, const int32_t
                       int32_t* accept_len, int32_t* path,
                       int32_t* out_tokens, int max_path, int32_t* status, void* workspace,
                       size_t workspace_bytes, tv_stream_t stream) {
-    if (mode != TV_ACCEPT_GREEDY && mode != TV_ACCEPT_STOCHASTIC) return TV_ERR_INVALID_ARG;
+    if (mode != TV_ACCEPT_GREEDY && mode != TV_ACCEPT_STOCHASTIC && mode != TV_ACCEPT_GREEDY_MASKED)
+        return TV_ERR_INVALID_ARG;
     if (B < 0 || N < 1 || N > 64 || V < 1 || V > (1 << 24) || max_path < 1)
         return TV_ERR_INVALID_ARG;
     if ((int64_t)B * 16 > 0x7fffffff) return TV_ERR_UNSUPPORTED;

@@ -14,7 +14,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (GREEDY, STOCHASTIC, chunk_attention, chunk_attention_workspace, chunk_kv_append,
+from . import (GREEDY, GREEDY_MASKED, STOCHASTIC, chunk_attention, chunk_attention_workspace, chunk_kv_append,
                kv_compact, token_counts_update, tree_accept, tree_accept_workspace,
                tree_logits_process, tree_mask_build, tree_verify_attention,
                tree_verify_attention_workspace)
@@ -134,7 +134,9 @@ class VerifyStep:
         sampling (or None: target is what tree_accept reads): tree_logits_process's counts,
         bias, grammar, repetition, frequency, presence and temperature, those that are wanted;
         target is then the target model's raw rows, float32 or bfloat16, and the tokens that
-        the step emits are added to counts."""
+        the step emits are added to counts.  A sequence that cannot be processed, or whose
+        grammar leaves nothing where a token is to be chosen, emits none (st_process,
+        st_accept; out_tokens -1): its counts stay, and its cache keeps the root."""
         if sampling is not None and self.target is None:
             raise ValueError("sampling needs a step made with process=True")
         self.mask_build(parents, stream, node_counts)
@@ -142,6 +144,8 @@ class VerifyStep:
         if sampling is not None:
             self.process(mode, target, draft_tokens, sampling, stream, node_counts)
             target = self.target
+            if mode == GREEDY:
+                mode = GREEDY_MASKED
         self.accept(mode, parents, draft_tokens, target, draft_probs, seed, offset, stream,
                     node_counts)
         if sampling is not None and sampling.get("counts") is not None:

@@ -77,7 +77,11 @@ typedef enum {
 } tv_status;
 
 typedef enum { TV_F32 = 0, TV_BF16 = 1 } tv_dtype;
-typedef enum { TV_ACCEPT_GREEDY = 0, TV_ACCEPT_STOCHASTIC = 1 } tv_accept_mode;
+typedef enum {
+    TV_ACCEPT_GREEDY = 0,
+    TV_ACCEPT_STOCHASTIC = 1,
+    TV_ACCEPT_GREEDY_MASKED = 2
+} tv_accept_mode;
 
 /* Static description of a status code.  Never NULL. */
 const char* tv_status_string(int status);
@@ -184,6 +188,10 @@ tv_status tree_verify_attention(const void* q, const void* k_cache, const void* 
  *   are those whose whole root path matches; the chosen node is the deepest
  *   accepted node (ties: smallest id).  The bonus token is the argmax of the
  *   chosen node's row.  draft_probs is ignored (may be NULL).
+ * TV_ACCEPT_GREEDY_MASKED: the same for rows in which -infinity marks tokens that
+ *   are not allowed (tree_logits_process): it never wins either, so a row without
+ *   anything above it is like a row of NaNs.  It has no argmax, no child matches
+ *   it, and chosen it gives TV_ERR_BAD_VALUES.
  * TV_ACCEPT_STOCHASTIC: draft_probs [B][N][V] row k is the draft
  *   distribution node k's token was drawn from.  On a chain (parents[i] =
  *   i - 1):
@@ -548,8 +556,8 @@ tv_status token_counts_update(int32_t* counts, const int32_t* tokens, const int3
 
 /* ------------------------------------------------------------------------
  * tree_logits_process — the step between the target model and tree_accept: the
- * model's row for every node of a tree becomes the logits (greedy acceptance) or
- * the probabilities (stochastic acceptance) that tree_accept reads.
+ * model's row for every node of a tree becomes the logits (TV_ACCEPT_GREEDY_MASKED)
+ * or the probabilities (TV_ACCEPT_STOCHASTIC) that tree_accept reads.
  *
  * logits: [B][N][V], float32 or bfloat16 (dt); out float32 [B][N][V] (may be
  * logits itself when dt is TV_F32).  For row i of sequence b and token x:
@@ -575,7 +583,9 @@ tv_status token_counts_update(int32_t* counts, const int32_t* tokens, const int3
  * mask) a token of nodes 1 .. n_b - 1 outside [0, V); TV_ERR_BAD_VALUES for a
  * repetition or temperature not finite, <= 0 or below 2^-126, a frequency or
  * presence not finite.  That sequence's rows (all N when the count is bad) are -infinity
- * (probs == 0) or zero.
+ * (probs == 0) or zero.  Acceptance takes such rows, and those of a grammar that
+ * allows nothing, for what they are in the modes TV_ACCEPT_GREEDY_MASKED and
+ * TV_ACCEPT_STOCHASTIC: no token is emitted, and its status is TV_ERR_BAD_VALUES.
  * Host errors: N outside [1, 64], V outside [1, 2^24], NULL logits, out or
  * status, mask without draft_tokens or the reverse, a penalty without counts.
  * ------------------------------------------------------------------------ */
