@@ -439,6 +439,9 @@ struct CrParams {
     LateWait late;                // test-only
 };
 
+// What is copied for the values past the last key: weight 0 would not keep out an infinity.
+__device__ __align__(16) float cr_zeros[256];
+
 template <int NJ, int R>
 __global__ void __launch_bounds__(CR_THREADS) chunk_rows_kernel(CrParams p) {
     __shared__ ChunkLocateTmp<CR_THREADS> tmp;
@@ -502,7 +505,7 @@ __global__ void __launch_bounds__(CR_THREADS) chunk_rows_kernel(CrParams p) {
     const int32_t* table = p.c.table + (int64_t)at.b * p.c.max_blocks;
     const uint64_t policy = l2_policy_evict_first();
     // Lanes 0 - 7 copy the K rows of the warp's keys of a step, 8 - 15 their V rows (past the
-    // last key that one's again, at weight 0); the block is looked up a step ahead.
+    // last key that one's K row again, at weight 0, and zeros); the block is looked up a step ahead.
     constexpr int STEP = CR_THREADS / 32 * CR_WARP_KEYS;
     const int steps = (k_hi - k_lo + STEP - 1) / STEP;
     const int copy_key = k_lo + warp * CR_WARP_KEYS + (lane & (CR_WARP_KEYS - 1));
@@ -519,6 +522,7 @@ __global__ void __launch_bounds__(CR_THREADS) chunk_rows_kernel(CrParams p) {
         if (lane < 2 * CR_WARP_KEYS) {
             const int key = min(copy_key + i * STEP, k_hi - 1);
             const float* src = (lane < CR_WARP_KEYS ? p.k : p.v) + (((int64_t)blk * p.Hkv + g) * p.c.bs + key % p.c.bs) * p.d;
+            if (lane >= CR_WARP_KEYS && copy_key + i * STEP >= k_hi) src = cr_zeros;
             bulk_load(mine + (i % CR_STAGES) * stage_floats + lane * p.d, src, (uint32_t)p.d * 4, bar, policy);
         }
     };
