@@ -65,6 +65,7 @@ struct LgParams {
     int slices;     // CTAs per row (the cluster, for the softmax)
     int slice;      // entries per CTA, a multiple of 32
     int list_max;   // entries that the list of counts and biases holds
+    bool unscaled;  // the temperature is left to row_softmax_kernel
 };
 
 struct LgRow {
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
             if (tid < p.N) masks[tid] = p.mask ? p.mask[(int64_t)b * p.N + tid] & ~1ull : 0ull;
             if (tid < CAP / 32) nodes[tid] = 0u;
             if (__syncthreads_and(tok_ok ? 1 : 0) == 0) err = TV_ERR_OUT_OF_RANGE;
-            if (tid == 0) r = LgRow{rep, 1.f / rep, freq, pres, 1.f / temp, cnt, err};
+            if (tid == 0) r = LgRow{rep, 1.f / rep, freq, pres, p.unscaled ? 1.f : 1.f / temp, cnt, err};
             if (my_x >= 0) atomicOr(&nodes[my_x >> 5], 1u << (my_x & 31));
             __syncthreads();
             if (p.counts || p.bias) {
@@ -563,8 +564,9 @@ tv_status launch_slices(const LgParams& p, cudaStream_t stream) {
     }
 }
 
-// Rows that no cluster holds: the logits are written first, and this softmax, one CTA
-// per row, reads them again.
+// Rows that no cluster holds: the logits are written first, not yet divided by the
+// temperature, and this softmax, one CTA per row, reads them again: exponents are
+// differences of logits times the scale here, too.
 __global__ void __launch_bounds__(LG_THREADS) row_softmax_kernel(const LgParams p) {
     __shared__ float red[2][LG_THREADS / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -590,11 +592,15 @@ __global__ void __launch_bounds__(LG_THREADS) row_softmax_kernel(const LgParams 
     float mx = -INFINITY, sum = 0.f;
     for (int x = tid; x < p.V; x += LG_THREADS) mx = lg_max(mx, z[x]);
     mx = reduce(mx, false, 0);
-    const float base = mx == -INFINITY ? 0.f : mx;
-    for (int x = tid; x < p.V; x += LG_THREADS) sum += ex2_approx((z[x] - base) * LG_LOG2E);
+    if (mx == -INFINITY) {                               // nothing allowed, or a refused sequence
+        for (int x = tid; x < p.V; x += LG_THREADS) z[x] = 0.f;
+        return;
+    }
+    const float scale = LG_LOG2E * (p.temp ? 1.f / p.temp[b] : 1.f);
+    for (int x = tid; x < p.V; x += LG_THREADS) sum += ex2_approx((z[x] - mx) * scale);
     sum = reduce(sum, true, 1);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    for (int x = tid; x < p.V; x += LG_THREADS) z[x] = ex2_approx((z[x] - base) * LG_LOG2E) * inv;
+    const float inv = 1.f / sum;                         // (the sum is at least 1, or NaN)
+    for (int x = tid; x < p.V; x += LG_THREADS) z[x] = ex2_approx((z[x] - mx) * scale) * inv;
 }
 
 template <typename E>
@@ -611,6 +617,7 @@ tv_status launch_logits(const LogitsArgs& a, LgParams p) {
     }
     p.slice = ((a.V + p.slices - 1) / p.slices + 31) & ~31;
     if (cluster) return launch_slices<E, true>(p, a.stream);
+    p.unscaled = a.probs;
     const tv_status rc = launch_slices<E, false>(p, a.stream);
     if (rc != TV_OK || !a.probs) return rc;
     if (p.rows > 0x7fffffff) return TV_ERR_UNSUPPORTED;

@@ -1,0 +1,61 @@
+"""tree_logits_process at the edges of its arguments."""
+import math
+
+import pytest
+import torch
+
+import chunk_ref as R
+from test_gpu_logits import case, process
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import eagle_speculative_decoding_parent_gb300 as m
+    return m
+
+
+# ------------------------------------------------------------------ the smallest temperatures
+
+@pytest.mark.parametrize("V", [300, 20001, 151669, 262144, 300007])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_smallest_temperatures_give_the_largest_entry_everything(tv, V, dtype):
+    """Ordinary logits, whose quotients by the temperature float32 cannot hold: the row's mass is
+    on its largest entries, in equal shares, and every other entry is 0."""
+    c = case(4, 2, V, dtype, seed=V, penalties=False, bias=False, grammar=False)
+    c["kw"]["temp"] = torch.tensor([2.0 ** -100, 2.0 ** -126, 1e-30, 2.0 ** -127], dtype=torch.float32)
+    out, status = process(tv, c, True)
+    assert status.tolist() == [0, 0, 0, 7] and out[3].eq(0).all()
+    z = c["z"][:3].float()
+    top = z == z.amax(-1, keepdim=True)
+    want = top / top.sum(-1, keepdim=True)
+    assert torch.equal(out[:3] != 0, top)
+    # a sum of at most V ones (exact) and the division
+    assert ((out[:3] - want).abs() <= want * 2.0 ** -20).all()
+    # the formula in 64 bits says the same
+    ref = R.logits(c["z"][:3], probs=True, temp=c["kw"]["temp"][:3])
+    assert ((ref - want).abs() <= 1e-12).all()
+
+
+@pytest.mark.parametrize("V", [262144, 300007])
+def test_rows_that_no_cluster_holds(tv, V):
+    """Masked rows, rows with NaN or infinity, and each row's own sequence's temperature."""
+    c = case(3, 2, V, seed=5, penalties=False)
+    c["kw"]["temp"] = torch.tensor([0.01, 1.0, 40.0], dtype=torch.float32)
+    c["kw"]["grammar"][0, 1] = 0
+    bits = c["kw"]["grammar"].long()[..., torch.arange(V) // 32] >> (torch.arange(V) % 32) & 1
+    c["z"][2, 0, int(bits[2, 0].nonzero()[5])] = float("nan")
+    c["z"][2, 1, int((bits[2, 1] == 0).nonzero()[5])] = float("nan")
+    out, status = process(tv, c, True)
+    assert status.eq(0).all() and out[0, 1].eq(0).all() and out[2, 0].isnan().all()
+    ref = R.logits(c["z"], probs=True, **c["kw"])
+    # u = 2^-24; three roundings of a logit (bias, reciprocal, product), of at most M / temp; the
+    # sum of V terms in at least 512 partial sums; 2^-20 for the exponential and the division
+    u = 2.0 ** -24
+    M = c["z"].double().nan_to_num().abs().amax((1, 2)) + c["kw"]["bias"].double().abs().amax(1)
+    rel = (6 * u * M / c["kw"]["temp"].double())[:, None, None] + (V / 512 + 24) * u + 2.0 ** -20
+    for b, i in ((0, 0), (1, 0), (1, 1), (2, 1)):
+        assert ((out[b, i].double() - ref[b, i]).abs() <= ref[b, i] * rel[b] + 2.0 ** -126).all(), (b, i)
