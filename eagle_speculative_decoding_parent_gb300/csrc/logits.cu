@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
         }
         if (row + 1 < row_hi) fetch(row + 1, b, i + 1 < p.N);
         const int err = r.err;
-        if (absent() && err == TV_OK) continue;          // an absent node: nothing is written
+        if (absent()) continue;                          // an absent node: nothing is written
         auto store = [&](float scale) {
             // (computed again, rather than kept in registers that there are too few of)
             int64_t at_row = row;

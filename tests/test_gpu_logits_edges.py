@@ -18,6 +18,26 @@ def tv():
     return m
 
 
+# ------------------------------------------------------------------ absent nodes
+
+@pytest.mark.parametrize("probs", [False, True])
+@pytest.mark.parametrize("V", [1000, 40001, 270000])
+def test_absent_rows_of_a_failed_sequence_are_not_written(tv, probs, V):
+    """A bad temperature, or a bad token, with a count that is good: only the present nodes' rows
+    take the error's value."""
+    c = case(4, 5, V, seed=2, grammar=False)
+    counts = torch.tensor([3, 5, 2, 1], dtype=torch.int32)
+    c["kw"]["temp"][0] = 0.0
+    c["kw"]["tokens"][2, 1] = V
+    c["kw"]["rep"][3] = float("inf")
+    out, status = process(tv, c, probs, node_counts=counts)
+    assert status.tolist() == [7, 0, 3, 7]
+    for b, n in enumerate(counts.tolist()):
+        assert out[b, n:].eq(7.0).all(), b
+        if b != 1:
+            assert out[b, :n].eq(0.0 if probs else -math.inf).all(), b
+
+
 # ------------------------------------------------------------------ the smallest temperatures
 
 @pytest.mark.parametrize("V", [300, 20001, 151669, 262144, 300007])
