@@ -66,6 +66,7 @@ struct LgParams {
     int slice;      // entries per CTA, a multiple of 32
     int list_max;   // entries that the list of counts and biases holds
     bool unscaled;  // the temperature is left to row_softmax_kernel
+    LateWait late;  // test-only
 };
 
 struct LgRow {
@@ -98,8 +99,25 @@ __device__ __forceinline__ float lg_max3(float a, float b, float c) {
     return d;
 }
 
+// After a wait ran out, by every thread: the rows from the one that waited to the last of the
+// CTA's range take the value of a refused sequence, and their sequences TV_ERR_TIMEOUT.
+// (Whole rows: no other slice of them is worth anything.)
+__device__ __forceinline__ void lg_fail(const LgParams& p, int64_t row, float value) {
+    const int64_t row_hi = p.rows * (blockIdx.x / p.slices + 1) / p.groups;
+#pragma unroll 1
+    for (; row < row_hi; ++row) {
+        const int b = (int)(row / p.N), i = (int)(row % p.N);
+        const int cnt = p.node_counts ? p.node_counts[b] : p.N;
+        const bool counted = cnt >= 1 && cnt <= p.N;
+        if (threadIdx.x == 0) p.status[b] = counted ? TV_ERR_TIMEOUT : TV_ERR_OUT_OF_RANGE;
+        if (counted && i >= cnt) continue;
+#pragma unroll 1
+        for (int x = threadIdx.x; x < p.V; x += LG_THREADS) p.out[row * p.V + x] = value;
+    }
+}
+
 template <typename E, bool PROBS, int NV>
-__global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgParams p) {
+__global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const __grid_constant__ LgParams p) {
     constexpr bool F32 = sizeof(E) == 4;
     constexpr int CAP = LG_THREADS * 4 * NV;             // positions of the slice buffer
     extern __shared__ __align__(128) uint8_t lg_smem[];
@@ -122,6 +140,7 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
     __shared__ __align__(16) float2 peer[2][PROBS ? LG_CLUSTER_MAX * LG_WARPS : 1];
     __shared__ __align__(8) uint64_t peer_bar[2];
     __shared__ __align__(8) uint64_t full;               // the slice has landed
+    __shared__ int64_t late_row;                         // first row that a wait may have left wrong
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int group = (int)(blockIdx.x / p.slices), me = (int)(blockIdx.x % p.slices);
     const int64_t row_lo = p.rows * group / p.groups, row_hi = p.rows * (group + 1) / p.groups;
@@ -132,6 +151,7 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
         mbar_init(&full, 1);
         fence_mbar_init();
         s_gram[0] = 0u;
+        late_row = row_hi - 1;                           // (found out behind the last row)
     }
     if (PROBS && p.slices > 1) cluster_barrier_all();    // every slice's barriers are there
     else __syncthreads();
@@ -169,7 +189,7 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
         if (p.grammar && tid * 32 < n) cp_async_4(s_gram + 1 + tid, p.grammar + row * p.words + x0 / 32 + tid);
     };
     uint32_t phase = 0, got = 0;
-    bool alive = true;
+    bool alive = !(p.late.warp >= 0 && (p.late.cta < 0 || p.late.cta == (int)blockIdx.x));   // (test-only)
     int b = (int)(row_lo / p.N), i = (int)(row_lo % p.N) - 1;
     if (row_lo < row_hi) fetch(row_lo, b, true);
 #pragma unroll 1
@@ -418,7 +438,7 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
         }
         fence_proxy_async_smem();                        // the next copy lands where this row was
         if (__syncthreads_and(alive ? 1 : 0) == 0) {     // a wait ran out, in this row or the last
-            if (tid == 0) p.status[b] = TV_ERR_TIMEOUT;
+            if (tid == 0) late_row = max(row_lo, row - 1);
             mbar_wait_sleep(&full, (got - 1u) & 1u);     // (a copy still in flight)
             break;
         }
@@ -504,11 +524,11 @@ __global__ void __launch_bounds__(LG_THREADS, 2) tree_logits_kernel(const LgPara
             store(w);                                    // (NaN stays NaN)
         }
     }
-    // (the last row's pairs)
-    if (__syncthreads_and(alive ? 1 : 0) == 0 && tid == 0 && row_lo < row_hi) p.status[b] = TV_ERR_TIMEOUT;
+    const bool late = __syncthreads_and(alive ? 1 : 0) == 0;   // (the last row's pairs, too)
     // after a wait that ran out, pairs may still be on their way to this CTA; every CTA gets here,
     // as every wait is bounded
     if (PROBS && p.slices > 1) cluster_barrier_relaxed();
+    if (late) lg_fail(p, late_row, PROBS ? 0.f : -INFINITY);
 }
 
 template <typename E, bool PROBS, int NV>
@@ -645,6 +665,7 @@ tv_status launch_tree_logits(const LogitsArgs& a) {
     p.N = a.N;
     p.V = a.V;
     p.words = (a.V + 31) / 32;
+    p.late = test_late_wait();
     return a.dt == TV_F32 ? launch_logits<float>(a, p) : launch_logits<__nv_bfloat16>(a, p);
 }
 

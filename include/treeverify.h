@@ -583,7 +583,8 @@ tv_status token_counts_update(int32_t* counts, const int32_t* tokens, const int3
  * mask) a token of nodes 1 .. n_b - 1 outside [0, V); TV_ERR_BAD_VALUES for a
  * repetition or temperature not finite, <= 0 or below 2^-126, a frequency or
  * presence not finite.  That sequence's rows (all N when the count is bad) are -infinity
- * (probs == 0) or zero.  Acceptance takes such rows, and those of a grammar that
+ * (probs == 0) or zero; so are those not finished when a wait runs out
+ * (TV_ERR_TIMEOUT).  Acceptance takes such rows, and those of a grammar that
  * allows nothing, for what they are in the modes TV_ACCEPT_GREEDY_MASKED and
  * TV_ACCEPT_STOCHASTIC: no token is emitted, and its status is TV_ERR_BAD_VALUES.
  * Host errors: N outside [1, 64], V outside [1, 2^24], NULL logits, out or

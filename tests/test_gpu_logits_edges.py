@@ -79,3 +79,55 @@ def test_rows_that_no_cluster_holds(tv, V):
     rel = (6 * u * M / c["kw"]["temp"].double())[:, None, None] + (V / 512 + 24) * u + 2.0 ** -20
     for b, i in ((0, 0), (1, 0), (1, 1), (2, 1)):
         assert ((out[b, i].double() - ref[b, i]).abs() <= ref[b, i] * rel[b] + 2.0 ** -126).all(), (b, i)
+
+
+# ------------------------------------------------------------------ waits that run out
+
+def plain(c, out, probs, keep):
+    """Rows of the sequences `keep` of a case with temperatures only."""
+    z = c["z"].double()[keep] / c["kw"]["temp"].double()[keep][:, None, None]
+    # float32: the reciprocal and the product, 2 u of at most |z| each, and the softmax as above; a
+    # probability below float32's smallest normal number, 2^-126, becomes 0 (here |z| reaches 60
+    # and more, and e^-88 is below it)
+    u, top, V = 2.0 ** -24, float(z.abs().max()), z.shape[-1]
+    ref = torch.softmax(z, -1) if probs else z
+    tol = ref * (6 * u * top + (V / 512 + 24) * u + 2.0 ** -20) + 2.0 ** -126 if probs else 3 * u * z.abs()
+    assert ((out[keep].double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("probs", [False, True])
+@pytest.mark.parametrize("B,N,V", [(5, 9, 40000), (1500, 1, 500), (300, 5, 2000), (2, 3, 270000)])
+def test_waits_that_run_out(tv, monkeypatch, probs, B, N, V):
+    """Every sequence with a row behind the wait says so, those included that the group of CTAs
+    had not come to, and no row of theirs looks right.  (The test-only variable makes the first
+    wait for a row count as run out.)"""
+    c = case(B, N, V, seed=1, penalties=False, bias=False, grammar=False)
+    counts = torch.full((B,), N, dtype=torch.int32)
+    counts[B // 2] = N - 1 if N > 1 else 7
+    monkeypatch.setenv("TV_TEST_WAITS_RUN_OUT", "0")
+    out, status = process(tv, c, probs, node_counts=counts)
+    want = torch.where(counts <= N, 6, 3)
+    assert torch.equal(status, want.int())
+    bad = torch.full_like(out, 0.0 if probs else -math.inf)
+    if N > 1:
+        bad[B // 2, N - 1] = 7.0
+    assert torch.equal(out, bad)
+    monkeypatch.delenv("TV_TEST_WAITS_RUN_OUT")
+    out, status = process(tv, c, probs)
+    assert status.eq(0).all()
+    plain(c, out, probs, slice(None))
+
+
+@pytest.mark.parametrize("probs", [False, True])
+@pytest.mark.parametrize("cta", [0, 3, 40])
+def test_a_wait_that_runs_out_in_one_cta(tv, monkeypatch, probs, cta):
+    """The other CTAs' sequences are right."""
+    c = case(1500, 1, 500, seed=1, penalties=False, bias=False, grammar=False)
+    monkeypatch.setenv("TV_TEST_WAITS_RUN_OUT", f"0@{cta}")
+    out, status = process(tv, c, probs)
+    late = (status == 6).nonzero().view(-1).tolist()
+    assert late == list(range(late[0], late[-1] + 1)) and 1 < len(late) < 20
+    assert out[late].eq(0.0 if probs else -math.inf).all()
+    good = status == 0
+    assert int(good.sum()) == 1500 - len(late)
+    plain(c, out, probs, good)
