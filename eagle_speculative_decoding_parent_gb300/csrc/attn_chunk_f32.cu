@@ -150,8 +150,9 @@ __global__ void __launch_bounds__(CF_THREADS) chunk_attn_kernel(CfParams p) {
     int last[8];                       // the row's own position
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        m[i] = -INFINITY;
-        l[i] = 0.f;
+        // (a bad sequence has no tiles: 0 / 1.  A row whose every score is -infinity ends as 0 / 0.)
+        m[i] = t.ok ? -INFINITY : 0.f;
+        l[i] = t.ok ? 0.f : 1.f;
         last[i] = t.P + (r0 + min(ty * 8 + i, rows - 1)) / p.G;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(CF_THREADS) chunk_attn_kernel(CfParams p) {
     for (int i = 0; i < 8; ++i) {
         const int r = ty * 8 + i;
         if (r >= rows) continue;
-        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+        const float inv = 1.f / l[i];
         E* row = out + (int64_t)(t.s + (r0 + r) / p.G) * p.o_stride + (int64_t)(g * p.G + (r0 + r) % p.G) * p.d;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(CF_THREADS) chunk_join_kernel(CfParams p) {
             acc.w = fmaf(f, x[u].w, acc.w);
         }
     }
-    const float inv = den == 0.f ? 0.f : 1.f / den;
+    const float inv = 1.f / den;
     E* out = static_cast<E*>(p.out);
     cf_store4(out + (int64_t)(s + (r0 + r) / p.G) * p.o_stride + (int64_t)(g * p.G + (r0 + r) % p.G) * p.d + 4 * c,
               make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));

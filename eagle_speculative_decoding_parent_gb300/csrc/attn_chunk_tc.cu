@@ -953,7 +953,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             const bool have = n > j0;                      // O(i) will hold this item
             const int rows = p.G * min(it.ntok, p.npt);       // rows of the item in a row tile
             const bool wrows = (warp & 3) * 32 < rows;        // some of them in this warp
-            float m_used = -INFINITY, l = 0.f;
+            // (a bad sequence has no tiles: 0 / 1.  A row whose every score is -infinity ends as 0 / 0.)
+            float m_used = n > 0 ? -INFINITY : 0.f, l = n > 0 ? 0.f : 1.f;
             for (int j = j0; j < n; j += step) {
                 if (!wait_all<64>(&sfull[i], sc & 1u)) {
                     alive = false;
@@ -1153,7 +1154,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                             pslot[p.prows * (D + 1) + r] = sum;
                         }
                     } else {
-                        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                        const float inv = 1.f / sum;
                         const int t = r / p.G;
                         uint4 v;
                         v.x = pack_bf16x2(f[0] * inv, f[1] * inv);
@@ -1206,7 +1207,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                                 l = w0 * l + w1 * l1;
                                 m_used = mm;
                             }
-                            inv = l == 0.f ? 0.f : 1.f / l;
+                            inv = 1.f / l;
                             if (mine && pslot) {
                                 pslot[p.prows * D + prow] = m_used;
                                 pslot[p.prows * (D + 1) + prow] = l;
@@ -1307,7 +1308,7 @@ chunk_tc_join_kernel(const __grid_constant__ Params p, int ctas) {
         const bool more = !(rec.w & PIECE_LAST) && ahead < 2 * ctas;
         const int4 nrec = more ? __ldcg(&p.rec[ahead]) : rec;
         if (rec.w & PIECE_LATE) {
-            den = 0.f;
+            den = 1.f;
 #pragma unroll
             for (int e = 0; e < 32; ++e) acc[e] = 0.f;
             break;
@@ -1333,7 +1334,7 @@ chunk_tc_join_kernel(const __grid_constant__ Params p, int ctas) {
         slot = ahead;
         rec = nrec;
     }
-    const float inv = den == 0.f ? 0.f : 1.f / den;
+    const float inv = 1.f / den;
     __nv_bfloat16* dst = p.out + (int64_t)(row0 + tok) * p.o_stride + (int64_t)(g * p.G + head) * D + c0;
 #pragma unroll
     for (int e = 0; e < 32; e += 8) {

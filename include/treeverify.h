@@ -501,6 +501,7 @@ tv_status chunk_kv_append(const void* q, int64_t q_stride, const void* k, int64_
  *   keys  K = { t : max(0, p - window + 1) <= t <= p }   (window <= 0: 0 <= t <= p)
  *   s_t = scale * q . k_t, and with softcap > 0  s_t = softcap * tanh(s_t / softcap)
  *   out[row][h] = sum_{t in K} softmax_t(s) v_t
+ * (NaN for a row whose every score is -infinity).
  * The chunk's own keys and values are in the cache already (chunk_kv_append).
  * q [T][Hq][d] and out [T][Hq][d], dt elements, heads contiguous, rows
  * q_stride / out_stride elements apart.  out must not overlap q.

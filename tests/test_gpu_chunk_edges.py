@@ -41,3 +41,29 @@ def test_decoding_f32_infinite_values(tv, heads, d, window):
     ref, A, S = R.attention(c, window=window)
     tol = R.attention_tolerance(c, ref, A, S, d)
     assert ((out.double() - ref).abs() <= tol)[:, :, 32:].all()
+
+
+# ------------------------------------------------------------------ scores of -infinity
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,P,window", [([1], [0], 0), ([1], [2500], 0), ([1, 90, 1, 300], [40, 0, 0, 700], 1),
+                                        ([200], [1000], 0), ([3, 70], [0, 300], 0)])
+def test_rows_whose_every_score_is_minus_infinity(tv, dtype, n, P, window):
+    """The softmax of such a row has no value: NaN, in every form of the kernels; rows that see
+    some other key are as if the keys at -infinity were not there."""
+    c = R.cache_case(n, P, Hq=4, Hkv=1, d=64, bs=16, dtype=dtype, seed=len(n) + n[0])
+    c["q"][..., 0] = c["q"][..., 0].abs() + 0.1
+    for b in range(len(n)):
+        # every key up to that of the sequence's middle row
+        for t in range(P[b] + n[b] // 2 + 1):
+            put(c, "k_cache", b, t, 0, float("-inf"))
+    out, status = attend(tv, c, window=window)
+    assert status.eq(0).all()
+    ref, A, _ = R.attention(c, window=window)
+    assert torch.equal(out.isnan(), ref.isnan())
+    seen = ~ref.isnan()
+    assert seen.any() == any(a > 1 for a in n) and ref.isnan().any()
+    k = dict(c, k_cache=torch.where(c["k_cache"].isinf(), torch.zeros((), dtype=dtype), c["k_cache"]))
+    _, _, S = R.attention(k, window=window)     # (the keys at -infinity have weight 0, not a rounding)
+    tol = R.attention_tolerance(c, ref, A, S, 64)
+    assert ((out.double() - ref).abs() <= tol)[seen].all()
