@@ -141,8 +141,9 @@ struct Params {
 };
 
 // tanh(x) / x as a polynomial in x^2 for |x| <= 0.35: interpolated at the Chebyshev nodes of
-// [0, 0.35^2] (its nearest pole is at x^2 = -pi^2 / 4), off by at most 2.9e-6 of itself, below
-// a float32 dot product's bound and a thousandth of a weight's rounding for scores up to 100.
+// [0, 0.35^2] (its nearest pole is at x^2 = -pi^2 / 4), off by at most 2.9e-6 of itself: of a
+// score of 100 that is a fourteenth of a weight's rounding (2^-8).  The error changes slowly with
+// the score, and what the scores near a row's maximum share cancels in the softmax.
 // One term more costs 2.6 us of 41 (2,100 tokens of 16 heads of 64, window 1024).
 constexpr double TANH_SMALL = 0.35;
 constexpr double TANH_C[3] = {0.9999971183259196, -0.3329087359461761, 0.12394375936950675};
@@ -1408,14 +1409,18 @@ tv_status launch_chunk_attn_tc(const ChunkAttnArgs& a) {
     p.window = a.window;
     p.late = test_late_wait();
     p.prows = partial_rows(a.T, G);
-    p.scale_log2 = a.softcap > 0.f ? 2.f * LOG2E * a.scale / a.softcap : a.scale * LOG2E;
+    // (finite: a score of 0 stays 0)
+    p.scale_log2 = a.softcap > 0.f ? fminf(2.f * LOG2E * a.scale / a.softcap, 3e38f) : a.scale * LOG2E;
     p.cap_log2 = a.softcap * LOG2E;
     if (a.softcap > 0.f) {
         const double k = (double)a.scale / a.softcap;
-        p.cap_x = (float)k;
+        p.cap_x = (float)std::min(k, 3e38);
         for (int e = 0; e < 3; ++e) p.cap_c[e] = (float)(TANH_C[e] * a.scale * 1.4426950408889634 * pow(k, 2 * e));
-        // (scale / cap)^6 has to be a normal number, or x small enough not to need it; s^2 finite
-        const double small = k > 1e5 ? 0.0 : std::min((k < 1e-6 ? 1e-3 : TANH_SMALL) / k, 1e18);
+        // Beyond the polynomial's range a score is a difference of numbers of the cap's size, off by
+        // 2^-23 of the cap: so the range is left only at 0.35 caps, whatever the cap, until the last
+        // coefficient is no float32 any more (k^4 below 2^-149) and x has to be small enough not to
+        // need it.  s^2 has to be finite.
+        const double small = k > 1e5 ? 0.0 : std::min((k < 1e-10 ? 0.05 : TANH_SMALL) / k, 1e18);
         p.cap_small = (float)(small * small);
     }
     // one CTA per SM; fewer when even the longest sequences that fit give fewer runs

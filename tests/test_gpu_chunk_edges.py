@@ -1,9 +1,10 @@
-"""chunk_attention where its arithmetic meets infinities."""
+"""chunk_attention where its arithmetic meets infinities: values, scores, and caps far above the
+scores."""
 import pytest
 import torch
 
 import chunk_ref as R
-from test_gpu_chunk import attend
+from test_gpu_chunk import attend, check
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +68,33 @@ def test_rows_whose_every_score_is_minus_infinity(tv, dtype, n, P, window):
     _, _, S = R.attention(k, window=window)     # (the keys at -infinity have weight 0, not a rounding)
     tol = R.attention_tolerance(c, ref, A, S, 64)
     assert ((out.double() - ref).abs() <= tol)[seen].all()
+
+
+# ------------------------------------------------------------------ caps far above the scores
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cap", [30.0, 1e4, 2e6, 1e7, 1e8, 1e9])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_of_thousands_below_a_far_cap(tv, dtype, cap, d):
+    """Scores of 2,400 to 2,404 and a cap of thousands of times that: a score keeps float32's
+    precision, which a difference of numbers as large as the cap would not.  Few keys per row, so
+    that errors do not average out.  The products are exact: one column gives 2,400, one the
+    sixteenths behind it, the rest zero."""
+    c = R.cache_case([1, 6, 9], [5, 0, 3], Hq=4, Hkv=2, d=d, bs=16, dtype=dtype, seed=d)
+    g = torch.Generator().manual_seed(int(cap) % 1000)
+    c["q"].zero_()
+    c["q"][..., 0], c["q"][..., 9] = 32.0, 1.0
+    c["k_cache"].zero_()
+    c["k_cache"][..., 0] = 75.0
+    c["k_cache"][..., 9] = (torch.randint(0, 64, c["k_cache"].shape[:3], generator=g) / 16).to(dtype)
+    check(tv, c, scale=1.0, softcap=cap)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_scores_of_zero_with_the_largest_scale_over_cap(tv, dtype):
+    """scale / cap past float32's range: a score of 0 stays 0."""
+    c = R.cache_case([40], [30], Hq=4, Hkv=2, d=64, bs=16, dtype=dtype, seed=1)
+    c["q"][1::2] = 0.0
+    c["q"][::2] = 1.0
+    c["k_cache"][:] = 1.0
+    check(tv, c, scale=1e12, softcap=1e-30)
