@@ -19,6 +19,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "tv_chunk.cuh"
@@ -382,7 +383,7 @@ template <typename E, int NC>
 tv_status launch_nc(const CfParams& p, cudaStream_t stream) {
     constexpr int DP = NC * 64;
     const size_t smem = (size_t)(2 * CF_M * (DP + 4) + CF_N * DP) * 4;
-    static bool set[64] = {};
+    static std::atomic<bool> set[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TV_ERR_CUDA;
     if (!set[dev]) {
@@ -702,7 +703,7 @@ size_t cr_counts_bytes(int T, int Hkv) { return ((size_t)T * Hkv * 4 + 15) & ~(s
 template <int NJ, int R>
 cudaError_t cr_launch_r(const CrParams& p, cudaStream_t stream) {
     const size_t smem = (size_t)CR_THREADS / 32 * CR_STAGES * 2 * CR_WARP_KEYS * p.d * sizeof(float);
-    static bool set[64] = {};
+    static std::atomic<bool> set[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;

@@ -55,6 +55,7 @@
 // The CTA's records then name the sequences of its run, and the second kernel, behind
 // every TV_OK, gives them TV_ERR_TIMEOUT.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "tv_chunk.cuh"
@@ -1354,7 +1355,7 @@ int partial_rows(int T, int G) { return T <= MT / G ? MT : 2 * MT; }
 template <int D, bool CAP>
 tv_status launch(const ChunkAttnArgs& a, const Params& p, const CUtensorMap& qm, const CUtensorMap& km,
                  const CUtensorMap& vm, int ctas) {
-    static bool set[64] = {};
+    static std::atomic<bool> set[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TV_ERR_CUDA;
     if (!set[dev]) {

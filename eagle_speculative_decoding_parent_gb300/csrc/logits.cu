@@ -540,7 +540,7 @@ tv_status launch_nv(LgParams p, cudaStream_t stream) {
     const size_t smem = fixed + (size_t)p.list_max * 8;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TV_ERR_CUDA;
-    static bool set[64] = {};
+    static std::atomic<bool> set[64];
     if (!set[dev]) {
         if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, LG_SMEM) != cudaSuccess ||
             (PROBS && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)) {
