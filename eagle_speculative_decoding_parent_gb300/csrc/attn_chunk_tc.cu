@@ -88,7 +88,7 @@ constexpr int64_t C0 = 512;
 // cost of a run, in keys, below which cutting further costs more to join than it saves
 constexpr int64_t RUN_MIN = 768;
 
-struct Item {
+struct alignas(16) Item {      // moved as four 16-byte words
     int b, g, P, i0;        // sequence, kv head, prefix, first token
     int ntok, row0, kbase, hi;  // tokens; row of the first; first key (multiple of 16), key end
     int t_lo, t_hi, fa, fb; // key tiles of this piece; tiles < fa or >= fb need masks
@@ -98,7 +98,7 @@ struct Item {
 // ran out (then the record is: first and last sequence of its run).
 constexpr int PIECE = 1, PIECE_LAST = 2, PIECE_LATE = 4;
 constexpr int ITEM_END = 1, ITEM_TWO = 2, ITEM_BAD = 4, ITEM_STATUS = 8;
-static_assert(sizeof(Item) == 64, "four 16-byte words");
+static_assert(sizeof(Item) == 64 && alignof(Item) == 16, "four 16-byte words");
 
 template <int D>
 struct Lay {
