@@ -519,6 +519,8 @@ def chunk_attention(q, k_cache, v_cache, block_table, q_start, prefix_lens, out,
     if workspace is not None:
         ws_bytes = workspace.nbytes
         ws = _arg(workspace, workspace.dtype, "workspace", workspace.shape, dev)
+    if not 0 < window < 1 << 31:                # (the C argument has 32 bits)
+        window = 0
     _check(_chunk_attn(q_at, qs, kc, vc, table, block_table.shape[1], start, prefix, T, B, Hq, Hkv,
                        d, bs, blocks, dt, scale, softcap, window, out_at, os_, st, ws, ws_bytes,
                        _stream_of(stream, dev)), "chunk_attention")

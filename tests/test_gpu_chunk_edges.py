@@ -1,5 +1,5 @@
-"""chunk_attention where its arithmetic meets infinities: values, scores, and caps far above the
-scores."""
+"""chunk_attention at the edges: infinite values and scores, caps far above the scores, windows past
+32 bits."""
 import pytest
 import torch
 
@@ -98,3 +98,13 @@ def test_scores_of_zero_with_the_largest_scale_over_cap(tv, dtype):
     c["q"][::2] = 1.0
     c["k_cache"][:] = 1.0
     check(tv, c, scale=1e12, softcap=1e-30)
+
+
+# ------------------------------------------------------------------ windows past 32 bits
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, -2 ** 32 + 5])
+def test_windows_past_32_bits_are_none(tv, window):
+    c = R.cache_case([40, 1], [30, 200], Hq=4, Hkv=2, d=64, bs=16, dtype=torch.bfloat16, seed=1)
+    out, status = attend(tv, c, window=window)
+    assert status.eq(0).all()
+    assert torch.equal(out, attend(tv, c)[0])
