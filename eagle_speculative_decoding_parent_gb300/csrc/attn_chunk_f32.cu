@@ -13,9 +13,9 @@
 // parts; each part leaves its unnormalised O, maximum and sum in the workspace
 // and a second kernel joins them in order.
 // Batches of about one token per sequence take a second form, further down.
-// Measured: 1,000 rows of 32/8 heads of 128 after 3,000 keys 1.64 ms (35 TFLOP/s; 2.02 with
-// single multiply-adds, 2.69 with rows through registers); 316 rows of 2 heads of 64 after up to 900 keys 25 us, of which two launches
-// and one item's way through the tiles are nearly all.
+// Measured: 1,000 rows of 32/8 heads of 128 after 3,000 keys 1.65 ms (35 TFLOP/s; 2.02 with
+// single multiply-adds, 2.69 with rows through registers); 316 rows of 2 heads of 64 after up to
+// 900 keys 22 us, of which two launches and one item's way through the tiles are nearly all.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -419,8 +419,8 @@ int cf_splits(int T, int B, int Hkv, int G) {
 // added up by halving exchanges, which leave lane i with the score of (row i / 4, key i % 4):
 // 15 exchanges instead of 64 for R = 4.  Every group keeps its own running maximum, sum and
 // O; they are joined at the end, then the parts of the keys by a second kernel.
-// Measured: 64 sequences of 512-8,192 keys, 32/8 heads of 128: 252 us = 5.8 TB/s (rows straight
-// into registers 509, three stages 301; by row tiles 3,866).
+// Measured: 64 sequences of 512-8,192 keys, 1.4 GB with 32/8 heads of 128: 246 us = 5.7 TB/s
+// (rows straight into registers twice that, three stages a fifth more).
 constexpr int CR_THREADS = 128;
 constexpr int CR_GROUPS = CR_THREADS / 16;
 constexpr int CR_KEYS = 4;             // per group and step
@@ -691,7 +691,11 @@ __global__ void __launch_bounds__(CR_THREADS) chunk_rows_join_kernel(CrParams p)
 }
 
 // Each token reads its keys for itself, so at most about one token per sequence; a thread
-// holds 3 to 4 x G x d / 16 registers of rows and keys.
+// holds 3 to 4 x G x d / 16 registers of rows and keys.  Only T and B are known here, not the
+// lengths.  Measured against the row tiles (32/8 heads of 128): 64 sequences of 512-8,192 keys with
+// one token each 246 us against 1,954, with two 442 against 1,960; 8 of 300-3,000 keys 30 and 48
+// against 123 and 129; one of 2,000 keys 19 and 21 against 29.  Where all 2 B rows belong to one
+// sequence of 3,000 keys and share them: 128 rows 439 against 710, 16 rows 78 against 102.
 bool cr_applies(int T, int B, int Hkv, int G, int d, tv_dtype dt) {
     return dt == TV_F32 && T <= 2 * (int64_t)B && G <= (d <= 128 ? 8 : 4) && Hkv <= 65535;
 }

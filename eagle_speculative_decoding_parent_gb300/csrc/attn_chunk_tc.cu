@@ -44,9 +44,10 @@
 //            passes them on to warp 8.
 //   warp 11  scheduler: walks the run, checks each new sequence's blocks, and
 //            publishes the items a few ahead.
-// Measured: 4,096 rows after 12,281 keys (28/4 heads of 128) 541 us = 1,556 TFLOP/s; one row
-// of each of 64 sequences of 512-8,192 keys 124 us = 5.6 TB/s; chunks of 1-1,500 rows 98 us
-// (four to five us per item beside its tiles); one row after 300 keys 15.5 us.  A pair of
+// Measured: 4,096 rows after 12,281 keys (28/4 heads of 128) 547 us = 1,539 TFLOP/s by
+// themselves, 574-584 us called for seconds under the power cap; one row of each of 64
+// sequences of 512-8,192 keys 121 us = 5.8 TB/s; chunks of 1-1,500 rows 89 us (four to five us
+// per item beside its tiles); one row after 300 keys 14 us (captured 12).  A pair of
 // tiles of two full row tiles takes 1.65 us, of which the softmax is the longer half; an
 // exponential by polynomial for a part of the scores is slower (573-680 us), as are four
 // softmax warpgroups.

@@ -15,10 +15,13 @@
 // bytes of a row (half layout: the two 16-byte vectors that hold a pair's columns), and
 // it takes the same unit of several rows, so that finding it is paid once and the rows'
 // loads are in flight together.
-// Measured (bfloat16): 9,190 rows of 28 + 2 x 4 heads of 128, 169 MB, 43.6 us, where a
-// plain copy of those bytes takes 33 (prefetching the rows to L2 first 45.9, four rows in
-// flight per thread 55); 832 rows of 32 + 2 x 8 heads 10.6 us, most of it the three round
-// trips to a row's slot.
+// Measured (bfloat16): 9,164 rows of 28 + 2 x 4 heads of 128, 169 MB, 40.6 us, where a
+// plain copy of those bytes takes 33 (prefetching the rows to L2 first 5 % more, four rows in
+// flight per thread 25 %); 832 rows of 32 + 2 x 8 heads 7.8 us captured, most of it the three
+// round trips to a row's slot, and 12.7 from the host, which takes that long.  Float32, 6,677
+// rows of 32 + 2 x 8 heads, 328 MB: 62 us.  With positions of their own every CTA of a sequence
+// reads all of the sequence's: 8,000 rows of 32 + 2 x 8 heads in one, 197 MB, 54 us; 40,000 rows
+// of 8 + 2 x 2, 246 MB, the check in a kernel before, 113 us.
 #include <cuda_bf16.h>
 #include <math.h>
 

@@ -20,9 +20,9 @@
 // into a register, the grammar's bit, the maximum, one exponential and the store.
 // The shared memory leaves some 20 KB of L1: a few spilled registers of 1,024 threads do
 // not fit and come back from L2 in every row, so the row loop keeps its state in shared
-// memory and spills nothing (832 rows of 128,256 float32 probabilities 256 -> 182 us,
-// 4.9 TB/s, without history, biases and grammar 137; from bfloat16 195; 24 rows of 152,064
-// bfloat16 logits 15).  Histories and biases with more entries than the list holds (some
+// memory and spills nothing (832 rows of 128,256 float32 probabilities 256 -> 181 us,
+// 5.0 TB/s, without history, biases and grammar 137; from bfloat16 199; logits instead of
+// probabilities 165; 24 rows of 152,064 bfloat16 logits 12).  Histories and biases with more entries than the list holds (some
 // 4,500 per slice) are gone through in every row (both dense: 271 us for the 832 rows).
 #include <cuda_bf16.h>
 #include <float.h>
@@ -586,7 +586,8 @@ tv_status launch_slices(const LgParams& p, cudaStream_t stream) {
 
 // Rows that no cluster holds: the logits are written first, not yet divided by the
 // temperature, and this softmax, one CTA per row, reads them again: exponents are
-// differences of logits times the scale here, too.
+// differences of logits times the scale here, too (208 rows of 262,144: 388 us, where one
+// reading and writing of them would be 68 at the copy rate).
 __global__ void __launch_bounds__(LG_THREADS) row_softmax_kernel(const LgParams p) {
     __shared__ float red[2][LG_THREADS / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

@@ -7,8 +7,9 @@
 // few words change: the CTAs of a sequence all check its tokens, and each applies
 // its share with integer atomics on the row.  A scan is bound by the latency of
 // its loads, so each thread has UNROLL of them in flight.
-// Measured: 32 rows of 128,256 with up to 8,192 tokens each 8.5 us (1.9 TB/s; a launch alone
-// is 4.4; 512 or 1,024 threads and slices of 4,096 no faster), 128 rows with 1-6 tokens 4.4.
+// Measured: 32 rows of 128,256 with up to 8,192 tokens each 6.4 us (2.6 TB/s; 512 or 1,024
+// threads and slices of 4,096 no faster), 128 rows with 1-6 tokens 1.7 us captured, 5.5 from the
+// host, which takes that long.
 #include <algorithm>
 
 #include "tv_device.cuh"

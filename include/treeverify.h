@@ -574,7 +574,8 @@ tv_status token_counts_update(int32_t* counts, const int32_t* tokens, const int3
  *   probs == 0: out = z;  else out = softmax over x of z (0 for a masked token;
  *   a row without an allowed token above -infinity is all zeros; a NaN or +infinity
  *   among the allowed z makes the row NaN).
- * Every product and sum in float32.  bias [B][V] float32, counts int32 [B][V],
+ * Every product and sum in float32; the divisions by repetition and temperature are
+ * products with their float32 reciprocals.  bias [B][V] float32, counts int32 [B][V],
  * grammar uint32 [B][N][ceil(V / 32)], repetition / frequency / presence /
  * temperature float32 [B], mask uint64 [B][N] with draft_tokens int32 [B][N]: each
  * may be NULL (no bias; no history; every token allowed; 1, 0, 0, 1; no path).
