@@ -14,9 +14,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (GREEDY, GREEDY_MASKED, STOCHASTIC, chunk_attention, chunk_attention_workspace, chunk_kv_append,
-               kv_compact, token_counts_update, tree_accept, tree_accept_workspace,
-               tree_logits_process, tree_mask_build, tree_verify_attention,
+from . import (GREEDY, GREEDY_MASKED, STOCHASTIC, chunk_attention, chunk_attention_workspace,
+               chunk_kv_append, kv_compact, token_counts_update, tree_accept,
+               tree_accept_workspace, tree_logits_process, tree_mask_build, tree_verify_attention,
                tree_verify_attention_workspace)
 
 
@@ -38,7 +38,8 @@ def _capture(run, step_args) -> "torch.cuda.CUDAGraph":
 class ChunkStep:
     """Chunks of prompts, or single decoded tokens, of up to B sequences with T rows in all:
     rotates the queries and keys by ``rope``, appends K/V to the paged cache and attends.  The
-    attention is in ``out``, the rotated queries in ``q``."""
+    attention is in ``out``, the rotated queries in ``q``.  A sequence that st_append refuses has
+    its rows of the step before in ``q``, and nothing of worth in ``out``, whatever st_attn says."""
 
     def __init__(self, *, T, B, Hq, Hkv, d, dtype, rope=None, scale=0.0, softcap=0.0, window=0,
                  device="cuda"):
