@@ -127,7 +127,7 @@ def draw(rng):
     if op == "attend":
         c["tree"] = kind == "tree"
         c["window"] = _log_int(rng, 1, 4000) if kind == "window" else 0
-        c["sinks"] = rng.choice([0, 1, 4, 16, X else 0
+        c["sinks"] = rng.choice([0, 1, 4, 16, _log_int(rng, 1, 64)]) if kind == "window" else 0
         c["cap"] = rng.choice([0.0, 0.0, rng.uniform(5.0, 60.0)])
     else:
         c["layout"] = rng.choice(["half", "interleaved"])
