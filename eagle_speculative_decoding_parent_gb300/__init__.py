@@ -30,7 +30,8 @@ __all__ = ["TV_OK", "TV_ERR_BAD_TREE", "TV_ERR_OUT_OF_RANGE", "TV_ERR_UNSUPPORTE
            "tree_accept_workspace",
            "tree_accept", "kv_compact", "draft_tree_workspace", "draft_tree_expand",
            "RopeTable", "rope_table", "chunk_kv_append", "chunk_attention_workspace",
-           "chunk_attention", "token_counts_update", "tree_logits_process"]
+           "chunk_attention", "chunk_attention_q8_workspace", "chunk_attention_q8",
+           "token_counts_update", "tree_logits_process"]
 
 (TV_OK, TV_ERR_INVALID_ARG, TV_ERR_BAD_TREE, TV_ERR_OUT_OF_RANGE, TV_ERR_UNSUPPORTED,
  TV_ERR_CUDA, TV_ERR_TIMEOUT, TV_ERR_BAD_VALUES, TV_ERR_WORKSPACE) = range(9)
@@ -94,6 +95,10 @@ _chunk_append = _sig("chunk_kv_append", _i, [_p, _i64, _p, _i64, _p, _i64, _p, _
 _chunk_attn_ws = _sig("chunk_attention_workspace", _sz, [_i, _i, _i, _i, _i, _i])
 _chunk_attn = _sig("chunk_attention", _i, [_p, _i64, _p, _p, _p, _i, _p, _p, _i, _i, _i, _i, _i,
                                            _i, _i, _i, _f, _f, _i, _p, _i64, _p, _p, _sz, _p])
+_chunk_attn_q8_ws = _sig("chunk_attention_q8_workspace", _sz, [_i, _i, _i, _i, _i])
+_chunk_attn_q8 = _sig("chunk_attention_q8", _i, [_p, _i64, _p, _p, _p, _p, _p, _i, _p, _p, _p, _i, _i, _i,
+                                                 _i, _i, _i, _i, _f, _f, _i, _i, _p, _i64, _p, _p,
+                                                 _sz, _p])
 _token_counts = _sig("token_counts_update", _i, [_p, _p, _p, _i, _i, _i, _i, _i, _p, _p])
 _tree_logits = _sig("tree_logits_process", _i, [_p, _i, _i, _i, _i] + [_p] * 10 + [_i, _p, _p, _p])
 
@@ -524,6 +529,53 @@ def chunk_attention(q, k_cache, v_cache, block_table, q_start, prefix_lens, out,
     _check(_chunk_attn(q_at, qs, kc, vc, table, block_table.shape[1], start, prefix, T, B, Hq, Hkv,
                        d, bs, blocks, dt, scale, softcap, window, out_at, os_, st, ws, ws_bytes,
                        _stream_of(stream, dev)), "chunk_attention")
+
+
+def _paged_q8(k_cache, v_cache, k_scale, v_scale, block_table, q_start, prefix_lens, status, Hkv,
+              d, dev):
+    """_paged for an 8-bit cache: e4m3 codes and their scales float32 [num_blocks, Hkv]."""
+    paged = _paged(k_cache, v_cache, block_table, q_start, prefix_lens, status, torch.float8_e4m3fn,
+                   Hkv, d, dev)
+    shape = (paged[2], Hkv)
+    return paged + (_arg(k_scale, torch.float32, "k_scale", shape, dev),
+                    _arg(v_scale, torch.float32, "v_scale", shape, dev))
+
+
+def chunk_attention_q8_workspace(T, B, Hq, Hkv, d) -> int:
+    return int(_chunk_attn_q8_ws(T, B, Hq, Hkv, d))
+
+
+def chunk_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, q_start, prefix_lens,
+                       out, status, workspace=None, *, scale: float = 0.0, softcap: float = 0.0,
+                       window: int = 0, sinks: int = 0, mask=None, stream=None) -> None:
+    """chunk_attention over an 8-bit cache: q / out bfloat16 [T,Hq,d]; caches float8_e4m3fn
+    [num_blocks,Hkv,bs,d] with scales float32 [num_blocks,Hkv]; window > 0 limits the keys of a
+    token to itself, the window - 1 before it and the first ``sinks`` (at most 64) of its
+    sequence; mask int64 [T] (rows of tree_mask_build's masks) makes a sequence's rows the nodes
+    of a tree; workspace uint8 of chunk_attention_q8_workspace() bytes."""
+    shape = q.shape
+    if len(shape) != 3 or k_cache.dim() != 4:
+        raise ValueError("q is [T, Hq, d] and the caches [num_blocks, Hkv, block_size, d]")
+    T, Hq, d = shape
+    Hkv = k_cache.shape[1]
+    bf16 = torch.bfloat16
+    dev = torch._C._cuda_getDevice()
+    q_at, qs = _rows(q, bf16, "q", shape, dev)
+    out_at, os_ = _rows(out, bf16, "out", shape, dev)
+    B, bs, blocks, kc, vc, table, start, prefix, st, ksc, vsc = _paged_q8(
+        k_cache, v_cache, k_scale, v_scale, block_table, q_start, prefix_lens, status, Hkv, d, dev)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws_bytes = workspace.nbytes
+        ws = _arg(workspace, workspace.dtype, "workspace", workspace.shape, dev)
+    if not 0 < window < 1 << 31:                # (the C argument has 32 bits)
+        window = 0
+    if not 0 <= sinks <= 64:
+        raise ValueError("sinks is 0 to 64")
+    _check(_chunk_attn_q8(q_at, qs, kc, vc, ksc, vsc, table, block_table.shape[1], start, prefix,
+                          _arg(mask, torch.int64, "mask", (T,), dev), T, B, Hq, Hkv, d, bs, blocks,
+                          scale, softcap, window, sinks, out_at, os_, st, ws, ws_bytes,
+                          _stream_of(stream, dev)), "chunk_attention_q8")
 
 
 def token_counts_update(counts, tokens, status, *, starts=None, clear: bool = False,

@@ -443,6 +443,74 @@ tv_status chunk_attention(const void* q, int64_t q_stride, const void* k_cache,
                                                              : launch_chunk_attn_f32(a);
 }
 
+static bool q8_shape_ok(int Hq, int Hkv, int d) {
+    return Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 && chunk_attn_tc_applicable(Hq, Hkv, d, TV_BF16);
+}
+
+size_t chunk_attention_q8_workspace(int T, int B, int Hq, int Hkv, int d) {
+    return T < 1 || B < 1 || !q8_shape_ok(Hq, Hkv, d) ? 0 : chunk_attn_tc_workspace(T, B, Hq, Hkv, d);
+}
+
+tv_status chunk_attention_q8(const void* q, int64_t q_stride, const void* k_cache,
+                             const void* v_cache, const float* k_scale, const float* v_scale,
+                             const int32_t* block_table, int max_blocks_per_seq,
+                             const int32_t* q_start, const int32_t* prefix_lens,
+                             const uint64_t* mask, int T, int B, int Hq, int Hkv, int d,
+                             int block_size, int num_blocks, float scale, float softcap,
+                             int window, int sinks, void* out, int64_t out_stride,
+                             int32_t* status, void* workspace, size_t workspace_bytes,
+                             tv_stream_t stream) {
+    if (T < 0 || B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_blocks_per_seq < 1 ||
+        block_size < 1 || num_blocks < 1 || !(softcap == softcap) || isinf(softcap) || sinks < 0 ||
+        sinks > TV_MAX_SINKS || (mask && window > 0))
+        return TV_ERR_INVALID_ARG;
+    if (!q8_shape_ok(Hq, Hkv, d) || block_size % 16 != 0) return TV_ERR_UNSUPPORTED;
+    if (B == 0) return TV_OK;
+    if (!q_start || !prefix_lens || !block_table || !status) return TV_ERR_INVALID_ARG;
+    if (T > 0) {
+        if (!q || !out || !k_cache || !v_cache || !k_scale || !v_scale || q_stride < (int64_t)Hq * d ||
+            out_stride < (int64_t)Hq * d)
+            return TV_ERR_INVALID_ARG;
+        if ((q_stride * 2) % 16 || (out_stride * 2) % 16) return TV_ERR_UNSUPPORTED;
+    }
+    if (misaligned(q) || misaligned(out) || misaligned(k_cache) || misaligned(v_cache))
+        return TV_ERR_INVALID_ARG;
+    const size_t need = chunk_attention_q8_workspace(T, B, Hq, Hkv, d);
+    if (need > 0 && (!workspace || misaligned(workspace) || workspace_bytes < need))
+        return TV_ERR_WORKSPACE;
+    ChunkAttnArgs a;
+    a.q = q;
+    a.q_stride = q_stride;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.mask = mask;
+    a.sinks = sinks;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks_per_seq;
+    a.q_start = q_start;
+    a.prefix_lens = prefix_lens;
+    a.T = T;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.d = d;
+    a.bs = block_size;
+    a.num_blocks = num_blocks;
+    a.dt = TV_BF16;
+    a.scale = (scale > 0.f && isfinite(scale)) ? scale : 1.0f / sqrtf((float)d);
+    a.softcap = softcap > 0.f && softcap < 1e30f ? fmaxf(softcap, 1e-30f) : 0.f;
+    a.window = window > 0 ? window : 0;
+    a.out = out;
+    a.out_stride = out_stride;
+    a.status = status;
+    a.ws = workspace;
+    a.stream = (cudaStream_t)stream;
+    // without rows there are only statuses to write
+    return T > 0 ? launch_chunk_attn_q8(a) : launch_chunk_attn_f32(a);
+}
+
 tv_status token_counts_update(int32_t* counts, const int32_t* tokens, const int32_t* starts,
                               int total, int B, int V, int clear, int prompt, int32_t* status,
                               tv_stream_t stream) {

@@ -225,6 +225,10 @@ struct ChunkAttnArgs {
     int32_t* status;
     void* ws;
     cudaStream_t stream;
+    // 8-bit caches
+    const float *k_scale = nullptr, *v_scale = nullptr;
+    const uint64_t* mask = nullptr;
+    int sinks = 0;
 };
 size_t chunk_attn_f32_workspace(int T, int B, int Hq, int Hkv, int d, tv_dtype dt);
 tv_status launch_chunk_attn_f32(const ChunkAttnArgs& a);
@@ -232,6 +236,7 @@ tv_status launch_chunk_attn_f32(const ChunkAttnArgs& a);
 bool chunk_attn_tc_applicable(int Hq, int Hkv, int d, tv_dtype dt);
 size_t chunk_attn_tc_workspace(int T, int B, int Hq, int Hkv, int d);
 tv_status launch_chunk_attn_tc(const ChunkAttnArgs& a);
+tv_status launch_chunk_attn_q8(const ChunkAttnArgs& a);  // the same, 8-bit caches
 
 tv_status launch_token_counts(int32_t* counts, const int32_t* tokens, const int32_t* starts,
                               int total, int B, int V, bool clear, bool prompt, int32_t* status,

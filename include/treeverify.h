@@ -536,6 +536,61 @@ tv_status chunk_attention(const void* q, int64_t q_stride, const void* k_cache,
                           void* workspace, size_t workspace_bytes, tv_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * 8-bit caches.  k_cache and v_cache hold e4m3 codes (sign, four bits of exponent with
+ * bias 7, three of mantissa; subnormals; no infinities, 0x7f and 0xff are NaN), laid
+ * out like the other caches: [num_blocks][Hkv][block_size][d] bytes.  Each block of
+ * each kv head has a scale, k_scale and v_scale float32 [num_blocks][Hkv], and a code
+ * stands for code * scale.  Scales are powers of two (of any other number the
+ * exponent alone counts; zero is zero), so that what a code stands for is a bfloat16
+ * number exactly, and a code moves to a larger scale without rounding until it falls
+ * below the smallest normal code (2^-6).  block_size is a multiple of 16; d is 64 or
+ * 128; queries, new keys and values and outputs are bfloat16.  Half the bytes of the
+ * stream that bounds decoding and verification, for a relative error of 2^-4 an
+ * element.
+ *
+ * A block's codes mean nothing until chunk_kv_append_q8 has written to it; beyond a
+ * sequence's last position they may hold anything, and so may a block's scales until
+ * its first position has been appended.
+ * ------------------------------------------------------------------------ */
+
+/* ------------------------------------------------------------------------
+ * chunk_attention_q8 — chunk_attention over an 8-bit cache, for every kind of new
+ * token: prompts in chunks, single tokens and chains of drafts (the rows of a
+ * sequence are causal), and trees (mask).
+ *
+ * For row q_start[b] + i (position p = P_b + i) and query head h:
+ *   keys  K = { t : t <= p and (window <= 0 or t > p - window or t < sinks) }
+ *   with mask: K = { t : t < P_b } U { P_b + a : bit a of mask[row], a <= i }
+ *   s_t and out as in chunk_attention, k_t and v_t what the codes stand for.
+ * sinks: the first tokens that stay visible behind a window, 0 .. 64; without a
+ * window they are visible anyway.  mask: uint64 [T] (row i of a sequence is node i
+ * of its tree, as tree_mask_build writes them for trees of n_b nodes) or NULL; with
+ * it n_b is at most 64, and there is no window.
+ * A row without a key is zero; one whose every score is -infinity is NaN.
+ * Float32 accumulation and softmax; the weights are rounded to bfloat16.
+ * status int32 [B]: as chunk_attention (with sinks, the blocks of the first sinks
+ * positions are needed too), and TV_ERR_OUT_OF_RANGE for more than 64 rows with a
+ * mask.  Cache contents outside K reach no row, NaN included.
+ * workspace: chunk_attention_q8_workspace() bytes, 16-byte aligned, any contents.
+ * Host errors: as chunk_attention; TV_ERR_INVALID_ARG for sinks outside [0, 64], mask
+ * with a window, NULL scales; TV_ERR_UNSUPPORTED for d other than 64 and 128, a block
+ * size that is no multiple of 16, more than 128 query heads per kv head.
+ * ------------------------------------------------------------------------ */
+#define TV_MAX_SINKS 64
+
+size_t chunk_attention_q8_workspace(int T, int B, int Hq, int Hkv, int d);
+
+tv_status chunk_attention_q8(const void* q, int64_t q_stride, const void* k_cache,
+                             const void* v_cache, const float* k_scale, const float* v_scale,
+                             const int32_t* block_table, int max_blocks_per_seq,
+                             const int32_t* q_start, const int32_t* prefix_lens,
+                             const uint64_t* mask, int T, int B, int Hq, int Hkv, int d,
+                             int block_size, int num_blocks, float scale, float softcap,
+                             int window, int sinks, void* out, int64_t out_stride,
+                             int32_t* status, void* workspace, size_t workspace_bytes,
+                             tv_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * token_counts_update — the history that tree_logits_process reads: counts
  * int32 [B][V], bit 31 of a word set when the token occurs in the prompt, the
  * low 31 bits the number of times it was emitted.
