@@ -30,7 +30,8 @@ __all__ = ["TV_OK", "TV_ERR_BAD_TREE", "TV_ERR_OUT_OF_RANGE", "TV_ERR_UNSUPPORTE
            "tree_accept_workspace",
            "tree_accept", "kv_compact", "draft_tree_workspace", "draft_tree_expand",
            "RopeTable", "rope_table", "chunk_kv_append", "chunk_attention_workspace",
-           "chunk_attention", "chunk_attention_q8_workspace", "chunk_attention_q8",
+           "chunk_attention", "chunk_kv_append_q8", "chunk_attention_q8_workspace",
+           "chunk_attention_q8", "kv_compact_q8", "logits_sample",
            "token_counts_update", "tree_logits_process"]
 
 (TV_OK, TV_ERR_INVALID_ARG, TV_ERR_BAD_TREE, TV_ERR_OUT_OF_RANGE, TV_ERR_UNSUPPORTED,
@@ -99,6 +100,12 @@ _chunk_attn_q8_ws = _sig("chunk_attention_q8_workspace", _sz, [_i, _i, _i, _i, _
 _chunk_attn_q8 = _sig("chunk_attention_q8", _i, [_p, _i64, _p, _p, _p, _p, _p, _i, _p, _p, _p, _i, _i, _i,
                                                  _i, _i, _i, _i, _f, _f, _i, _i, _p, _i64, _p, _p,
                                                  _sz, _p])
+_chunk_append_q8 = _sig("chunk_kv_append_q8", _i, [_p, _i64, _p, _i64, _p, _i64, _p, _i, _p, _p, _i, _i,
+                                                   _i, _i, _p, _p, _i64, _p, _p, _p, _p, _p, _i, _i,
+                                                   _i, _p, _p])
+_compact_q8 = _sig("kv_compact_q8", _i, [_p, _p, _p, _p, _i, _i64, _i64, _p, _i, _p, _p, _p, _i, _i, _i, _i,
+                                         _i, _i, _p, _p, _p, _p, _p])
+_sample = _sig("logits_sample", _i, [_p, _i, _i, _i, _i] + [_p] * 10)
 _token_counts = _sig("token_counts_update", _i, [_p, _p, _p, _i, _i, _i, _i, _i, _p, _p])
 _tree_logits = _sig("tree_logits_process", _i, [_p, _i, _i, _i, _i] + [_p] * 10 + [_i, _p, _p, _p])
 
@@ -541,6 +548,41 @@ def _paged_q8(k_cache, v_cache, k_scale, v_scale, block_table, q_start, prefix_l
                     _arg(v_scale, torch.float32, "v_scale", shape, dev))
 
 
+def chunk_kv_append_q8(q, k, v, k_cache, v_cache, k_scale, v_scale, block_table, q_start,
+                       prefix_lens, status, *, q_out=None, rope=None, positions=None,
+                       stream=None) -> None:
+    """chunk_kv_append into an 8-bit cache: q, k, v, q_out bfloat16; caches float8_e4m3fn
+    [num_blocks,Hkv,bs,d] with scales float32 [num_blocks,Hkv], powers of two that grow with
+    what is appended to a block."""
+    shape = k.shape
+    if len(shape) != 3:
+        raise ValueError("k is [T, Hkv, d]")
+    T, Hkv, d = shape
+    bf16 = torch.bfloat16
+    dev = torch._C._cuda_getDevice()
+    k_at, ks = _rows(k, bf16, "k", shape, dev)
+    v_at, vs = _rows(v, bf16, "v", shape, dev)
+    Hq, q_at, qs, q_out_at, qos = 1, None, 0, None, 0
+    if q is not None:
+        q_shape = q.shape
+        if len(q_shape) != 3 or q_shape[0] != T or q_shape[2] != d:
+            raise ValueError("q is [T, Hq, d]")
+        Hq = q_shape[1]
+        q_at, qs = _rows(q, bf16, "q", q_shape, dev)
+        q_out_at, qos = (q_at, qs) if q_out is None else _rows(q_out, bf16, "q_out", q_shape, dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    B, bs, blocks, kc, vc, table, start, prefix, st, ksc, vsc = _paged_q8(
+        k_cache, v_cache, k_scale, v_scale, block_table, q_start, prefix_lens, status, Hkv, d, dev)
+    if rope is not None and not isinstance(rope, RopeTable):
+        raise TypeError("rope: expected a RopeTable")
+    _check(_chunk_append_q8(q_at, qs, k_at, ks, v_at, vs,
+                            _arg(positions, torch.int32, "positions", (T,), dev), T, start, prefix,
+                            B, Hq, Hkv, d, None if rope is None else ctypes.addressof(rope),
+                            q_out_at, qos, kc, vc, ksc, vsc, table, block_table.shape[1], bs,
+                            blocks, st, _stream_of(stream, dev)), "chunk_kv_append_q8")
+
+
 def chunk_attention_q8_workspace(T, B, Hq, Hkv, d) -> int:
     return int(_chunk_attn_q8_ws(T, B, Hq, Hkv, d))
 
@@ -576,6 +618,63 @@ def chunk_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, q_sta
                           _arg(mask, torch.int64, "mask", (T,), dev), T, B, Hq, Hkv, d, bs, blocks,
                           scale, softcap, window, sinks, out_at, os_, st, ws, ws_bytes,
                           _stream_of(stream, dev)), "chunk_attention_q8")
+
+
+def kv_compact_q8(k_cache, v_cache, k_scale, v_scale, block_table, prefix_lens, path, accept_len,
+                  new_lens, status, *, src_slots=None, dst_slots=None, stream=None) -> None:
+    """kv_compact on 8-bit caches: float8_e4m3fn [num_blocks,Hkv,bs,d] with scales float32
+    [num_blocks,Hkv], or both with the layers in front; path int32 [B,max_path]; accept_len,
+    new_lens, status int32 [B]; src_slots, dst_slots int64 [B,max_path] or None."""
+    shape, where = k_cache.shape, path.shape
+    if len(shape) not in (4, 5):
+        raise ValueError("the caches are [num_blocks, Hkv, block_size, d], or layers of them")
+    if len(where) != 2:
+        raise ValueError("path is int32 [B, max_path]")
+    layers = shape[0] if len(shape) == 5 else 1
+    num_blocks, Hkv, bs, d = shape[-4:]
+    B, max_path = where
+    ts = block_table.shape
+    if len(ts) != 2 or ts[0] != B:
+        raise ValueError("block_table is int32 [B, max_blocks_per_seq]")
+    i32, i64, f32 = torch.int32, torch.int64, torch.float32
+    dev = torch._C._cuda_getDevice()
+    f8 = torch.float8_e4m3fn
+    _check(_compact_q8(_arg(k_cache, f8, "k_cache", shape, dev), _arg(v_cache, f8, "v_cache", shape, dev),
+                       _arg(k_scale, f32, "k_scale", shape[:-2], dev),
+                       _arg(v_scale, f32, "v_scale", shape[:-2], dev), layers,
+                       num_blocks * Hkv * bs * d, num_blocks * Hkv,
+                       _arg(block_table, i32, "block_table", ts, dev), ts[1],
+                       _arg(prefix_lens, i32, "prefix_lens", (B,), dev),
+                       _arg(path, i32, "path", where, dev),
+                       _arg(accept_len, i32, "accept_len", (B,), dev), max_path, B, Hkv, d, bs,
+                       num_blocks, _arg(new_lens, i32, "new_lens", (B,), dev),
+                       _arg(src_slots, i64, "src_slots", where, dev),
+                       _arg(dst_slots, i64, "dst_slots", where, dev),
+                       _arg(status, i32, "status", (B,), dev), _stream_of(stream, dev)),
+           "kv_compact_q8")
+
+
+def logits_sample(logits, uniform, tokens, status, *, temperature=None, top_k=None, top_p=None,
+                  min_p=None, probs=None, node_counts=None, stream=None) -> None:
+    """Samples rows of logits, float32 or bfloat16 [B,N,V], with the given uniform numbers float32
+    [B,N] into tokens int32 [B,N], and writes the filtered distributions to probs float32
+    [B,N,V] if given; temperature (0: the best entry), top_p, min_p float32 [B] and top_k int32
+    [B], each optional; status int32 [B,N]."""
+    shape = logits.shape
+    if len(shape) != 3:
+        raise ValueError("logits is [B, N, V]")
+    B, N, V = shape
+    dt = _dtype_code(logits)
+    f32, i32 = torch.float32, torch.int32
+    dev = torch._C._cuda_getDevice()
+    _check(_sample(_arg(logits, logits.dtype, "logits", shape, dev), dt, B, N, V,
+                   _arg(node_counts, i32, "node_counts", (B,), dev),
+                   _arg(uniform, f32, "uniform", (B, N), dev),
+                   _arg(temperature, f32, "temperature", (B,), dev),
+                   _arg(top_k, i32, "top_k", (B,), dev), _arg(top_p, f32, "top_p", (B,), dev),
+                   _arg(min_p, f32, "min_p", (B,), dev), _arg(tokens, i32, "tokens", (B, N), dev),
+                   _arg(probs, f32, "probs", shape, dev), _arg(status, i32, "status", (B, N), dev),
+                   _stream_of(stream, dev)), "logits_sample")
 
 
 def token_counts_update(counts, tokens, status, *, starts=None, clear: bool = False,

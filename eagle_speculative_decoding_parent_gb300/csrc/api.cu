@@ -443,6 +443,142 @@ tv_status chunk_attention(const void* q, int64_t q_stride, const void* k_cache,
                                                              : launch_chunk_attn_f32(a);
 }
 
+tv_status chunk_kv_append_q8(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, const int32_t* positions, int T,
+                             const int32_t* q_start, const int32_t* prefix_lens, int B, int Hq,
+                             int Hkv, int d, const tv_rope_table* rope, void* q_out,
+                             int64_t q_out_stride, void* k_cache, void* v_cache, float* k_scale,
+                             float* v_scale, const int32_t* block_table, int max_blocks_per_seq,
+                             int block_size, int num_blocks, int32_t* status,
+                             tv_stream_t stream) {
+    if (T < 0 || B < 0 || Hq < 1 || Hkv < 1 || d < 1 || block_size < 1 || num_blocks < 1 ||
+        max_blocks_per_seq < 1)
+        return TV_ERR_INVALID_ARG;
+    if (rope && (rope->dim < 2 || rope->dim > TV_ROPE_MAX_DIM || rope->dim > d))
+        return TV_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || block_size % 16 != 0 || (rope && rope->dim % 16 != 0) ||
+        (int64_t)Hq * d > 0x7fffffff || (int64_t)Hkv * d > 0x7fffffff)
+        return TV_ERR_UNSUPPORTED;
+    if (B == 0) return TV_OK;
+    if (!q_start || !prefix_lens || !block_table || !status || !k_cache || !v_cache || !k_scale ||
+        !v_scale || (q == nullptr) != (q_out == nullptr))
+        return TV_ERR_INVALID_ARG;
+    if (T > 0) {
+        if (!k || !v || k_stride < (int64_t)Hkv * d || v_stride < (int64_t)Hkv * d ||
+            (q && (q_stride < (int64_t)Hq * d || q_out_stride < (int64_t)Hq * d)))
+            return TV_ERR_INVALID_ARG;
+        if (k_stride % 8 || v_stride % 8 || (q && (q_stride % 8 || q_out_stride % 8)))
+            return TV_ERR_UNSUPPORTED;
+    }
+    if (misaligned(q) || misaligned(k) || misaligned(v) || misaligned(q_out) ||
+        misaligned(k_cache) || misaligned(v_cache))
+        return TV_ERR_INVALID_ARG;
+    ChunkAppendArgs a;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.positions = positions;
+    a.T = T;
+    a.q_start = q_start;
+    a.prefix_lens = prefix_lens;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.d = d;
+    a.rope = rope;
+    a.q_out = q_out;
+    a.q_out_stride = q_out_stride;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks_per_seq;
+    a.bs = block_size;
+    a.num_blocks = num_blocks;
+    a.elem = 1;
+    a.status = status;
+    a.stream = (cudaStream_t)stream;
+    return launch_chunk_append_q8(a);
+}
+
+tv_status kv_compact_q8(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                        int num_layers, int64_t layer_stride, int64_t scale_layer_stride,
+                        const int32_t* block_table, int max_blocks_per_seq,
+                        const int32_t* prefix_lens, const int32_t* path,
+                        const int32_t* accept_len, int max_path, int B, int Hkv, int d,
+                        int block_size, int num_blocks, int32_t* new_lens, int64_t* src_slots,
+                        int64_t* dst_slots, int32_t* status, tv_stream_t stream) {
+    if (B < 0 || Hkv < 1 || d < 1 || block_size < 1 || num_blocks < 1 || max_blocks_per_seq < 1 ||
+        max_path < 1 || num_layers < 0 || layer_stride < 0 || scale_layer_stride < 0)
+        return TV_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || block_size % 16 != 0) return TV_ERR_UNSUPPORTED;
+    if (num_layers > 1 && (layer_stride < (int64_t)num_blocks * Hkv * block_size * d ||
+                           scale_layer_stride < (int64_t)num_blocks * Hkv))
+        return TV_ERR_INVALID_ARG;
+    if (B == 0 || num_layers == 0) return TV_OK;
+    if (!k_cache || !v_cache || !k_scale || !v_scale || !block_table || !prefix_lens || !path ||
+        !accept_len || !new_lens || !status)
+        return TV_ERR_INVALID_ARG;
+    if (misaligned(k_cache) || misaligned(v_cache) || (layer_stride & 15)) return TV_ERR_INVALID_ARG;
+    CompactQ8Args a;
+    a.k_cache = static_cast<uint8_t*>(k_cache);
+    a.v_cache = static_cast<uint8_t*>(v_cache);
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.num_layers = num_layers;
+    a.layer_stride = layer_stride;
+    a.scale_layer_stride = scale_layer_stride;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks_per_seq;
+    a.prefix_lens = prefix_lens;
+    a.path = path;
+    a.accept_len = accept_len;
+    a.max_path = max_path;
+    a.B = B;
+    a.Hkv = Hkv;
+    a.d = d;
+    a.bs = block_size;
+    a.num_blocks = num_blocks;
+    a.new_lens = new_lens;
+    a.src_slots = src_slots;
+    a.dst_slots = dst_slots;
+    a.status = status;
+    a.stream = (cudaStream_t)stream;
+    return launch_compact_q8(a);
+}
+
+tv_status logits_sample(const void* logits, tv_dtype dt, int B, int N, int V,
+                        const int32_t* node_counts, const float* uniform,
+                        const float* temperature, const int32_t* top_k, const float* top_p,
+                        const float* min_p, int32_t* tokens, float* probs, int32_t* status,
+                        tv_stream_t stream) {
+    if (dt != TV_F32 && dt != TV_BF16) return TV_ERR_INVALID_ARG;
+    if (B < 0 || N < 1 || N > 64 || V < 1 || V > (1 << 24)) return TV_ERR_INVALID_ARG;
+    if (B == 0) return TV_OK;
+    if (!logits || !uniform || !tokens || !status || (const void*)probs == logits) return TV_ERR_INVALID_ARG;
+    SampleArgs a;
+    a.logits = logits;
+    a.dt = dt;
+    a.B = B;
+    a.N = N;
+    a.V = V;
+    a.node_counts = node_counts;
+    a.uniform = uniform;
+    a.temp = temperature;
+    a.top_k = top_k;
+    a.top_p = top_p;
+    a.min_p = min_p;
+    a.tokens = tokens;
+    a.probs = probs;
+    a.status = status;
+    a.stream = (cudaStream_t)stream;
+    return launch_logits_sample(a);
+}
+
 static bool q8_shape_ok(int Hq, int Hkv, int d) {
     return Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 && chunk_attn_tc_applicable(Hq, Hkv, d, TV_BF16);
 }

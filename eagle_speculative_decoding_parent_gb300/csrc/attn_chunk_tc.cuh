@@ -62,6 +62,7 @@
 #include <cmath>
 
 #include "tv_chunk.cuh"
+#include "tv_fp8.cuh"
 #include "tv_internal.h"
 #include "tv_tc.cuh"
 
@@ -436,14 +437,6 @@ __device__ __forceinline__ int fix_index(const Item& it, int t) {  // 0 .. FIX_T
 }
 
 // ------------------------------------------------------- 8-bit caches
-// A block's scale is a power of two; of any other number the exponent counts.
-__device__ __forceinline__ uint32_t exponent_byte(float scale) { return (__float_as_uint(scale) >> 23) & 0xffu; }
-__device__ __forceinline__ float scale_of(uint32_t e) { return __uint_as_float(e << 23); }
-// An e4m3 code: sign, four bits of exponent (bias 7), three of mantissa; 0x7f is NaN.
-__device__ __forceinline__ float e4m3_float(uint32_t c) {
-    const float x = __uint_as_float(((c & 0x80u) << 24) | ((c & 0x7fu) << 20)) * 1.329227995784916e36f;  // 2^120
-    return (c & 0x7fu) == 0x7fu ? __uint_as_float(0x7fc00000u) : x;
-}
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));

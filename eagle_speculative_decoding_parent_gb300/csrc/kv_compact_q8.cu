@@ -1,0 +1,161 @@
+// kv_compact_q8: gather-then-scatter of the accepted rows of an 8-bit cache.
+// A warp takes the rows of one kv head, one layer, K or V.  A row's codes mean what the scale of the
+// block that they lie in says, so the scale of a destination block becomes the largest of
+// those that its rows bring with them, and of its own where it keeps positions before the root;
+// codes whose scale grows are rounded again (by a power of two: exactly, above the
+// subnormal codes).  Everything is read into shared memory before anything is written, so a
+// destination may be another row's source.  Rows that stay where they are in a block that
+// keeps its scale are not touched.  Bound by latency: a chain of four round trips (lengths and
+// path, blocks, scales, rows).
+#include "tv_device.cuh"
+#include "tv_fp8.cuh"
+#include "tv_internal.h"
+
+namespace tv {
+
+namespace {
+
+constexpr int CQ_WARPS = 4;
+constexpr int CQ_MAX_ROWS = 64;
+
+struct CqParams {
+    uint8_t *k, *v;
+    float *k_scale, *v_scale;
+    int64_t layer_stride, scale_layer_stride;
+    const int32_t* table;
+    const int32_t* prefix_lens;
+    const int32_t* path;
+    const int32_t* accept_len;
+    int max_blocks, max_path, Hkv, bs, num_blocks, rows;   // rows: of a warp's buffer
+    int32_t* new_lens;
+    int64_t* src_slots;
+    int64_t* dst_slots;
+    int32_t* status;
+};
+
+__device__ __forceinline__ int64_t cq_slot(const CqParams& p, int b, int64_t t) {
+    if (t < 0) return -1;
+    const int64_t lb = t / p.bs;
+    if (lb >= p.max_blocks) return -1;
+    const int blk = p.table[(int64_t)b * p.max_blocks + lb];
+    if (blk < 0 || blk >= p.num_blocks) return -1;
+    return (int64_t)blk * p.bs + t % p.bs;
+}
+
+template <int D>
+__global__ void __launch_bounds__(CQ_WARPS * 32) kv_compact_q8_kernel(const __grid_constant__ CqParams p) {
+    constexpr int VEC = D / 16;                     // 16-byte pieces of a row
+    extern __shared__ uint4 cq_rows[];              // [CQ_WARPS][rows][VEC]
+    __shared__ int64_t ssrc[CQ_MAX_ROWS], sdst[CQ_MAX_ROWS];
+    __shared__ float sscale[CQ_WARPS][CQ_MAX_ROWS], dscale[CQ_WARPS][CQ_MAX_ROWS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.y, unit = blockIdx.x * CQ_WARPS + warp;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int P = p.prefix_lens[b], A = p.accept_len[b];
+    bool ok = P >= 0 && A >= 0 && A < p.max_path && A < CQ_MAX_ROWS;
+    if (ok && tid <= A) {
+        const int from = p.path[(int64_t)b * p.max_path + tid];
+        const int64_t s = from < 0 ? -1 : cq_slot(p, b, (int64_t)P + from), d = cq_slot(p, b, (int64_t)P + tid);
+        ssrc[tid] = s;
+        sdst[tid] = d;
+        ok = s >= 0 && d >= 0;
+    }
+    ok = __syncthreads_and(ok ? 1 : 0) != 0;
+    if (blockIdx.x == 0 && blockIdx.z == 0) {
+        for (int j = tid; j < p.max_path; j += CQ_WARPS * 32) {
+            const bool in = ok && j <= A;
+            if (p.src_slots) p.src_slots[(int64_t)b * p.max_path + j] = in ? ssrc[j] : -1;
+            if (p.dst_slots) p.dst_slots[(int64_t)b * p.max_path + j] = in ? sdst[j] : -1;
+        }
+        if (tid == 0) {
+            p.status[b] = ok ? TV_OK : TV_ERR_OUT_OF_RANGE;
+            p.new_lens[b] = ok ? P + A + 1 : P;
+        }
+    }
+    if (!ok || unit >= 2 * p.Hkv) return;
+    const int g = unit >> 1;
+    uint8_t* codes = (unit & 1 ? p.v : p.k) + blockIdx.z * p.layer_stride;
+    float* scale = (unit & 1 ? p.v_scale : p.k_scale) + blockIdx.z * p.scale_layer_stride;
+    uint4* rows = cq_rows + warp * p.rows * VEC;
+    auto block_scale = [&](int64_t slot) -> float* { return scale + slot / p.bs * p.Hkv + g; };
+    auto row_at = [&](int64_t slot) -> uint4* {
+        return reinterpret_cast<uint4*>(codes + ((slot / p.bs * p.Hkv + g) * p.bs + slot % p.bs) * D);
+    };
+    // ---- scales: what each row brings with it, and what its destination had
+    for (int j = lane; j <= A; j += 32) {
+        sscale[warp][j] = scale_of(exponent_byte(*block_scale(ssrc[j])));
+        dscale[warp][j] = scale_of(exponent_byte(*block_scale(sdst[j])));
+    }
+    __syncwarp();
+    // rows P + j with the same (P + j) / bs share a block: rows j0(j) .. j1(j)
+    const int off = P % p.bs;
+    auto fresh = [&](int j) -> float {
+        const int lb = (off + j) / p.bs, j0 = max(0, lb * p.bs - off), j1 = min(A, (lb + 1) * p.bs - 1 - off);
+        float s = lb == 0 && off > 0 ? dscale[warp][0] : 0.f;
+        for (int i = j0; i <= j1; ++i) s = fmaxf(s, sscale[warp][i]);
+        return s;
+    };
+    // ---- rows that move, or whose scale grows
+    for (int e = lane; e < (A + 1) * VEC; e += 32) {
+        const int j = e / VEC;
+        rows[e] = row_at(ssrc[j])[e % VEC];
+    }
+    __syncwarp();
+    auto scaled = [&](uint4 w, float by) -> uint4 {
+        return make_uint4(e4m3_scaled(w.x, by), e4m3_scaled(w.y, by), e4m3_scaled(w.z, by), e4m3_scaled(w.w, by));
+    };
+    for (int e = lane; e < (A + 1) * VEC; e += 32) {
+        const int j = e / VEC;
+        const float s = fresh(j), was = sscale[warp][j];
+        if (ssrc[j] == sdst[j] && was == s) continue;
+        row_at(sdst[j])[e % VEC] = was == s ? rows[e] : scaled(rows[e], was * scale_inverse(s));
+    }
+    if (off > 0) {
+        // positions before the root in its block
+        const float s = fresh(0), was = dscale[warp][0];
+        if (was != s) {
+            uint4* first = row_at(sdst[0] - off);
+            for (int e = lane; e < off * VEC; e += 32) first[e] = scaled(first[e], was * scale_inverse(s));
+        }
+    }
+    // ---- the scales of the destination blocks, each by its first row
+    __syncwarp();
+    for (int j = lane; j <= A; j += 32)
+        if (j == 0 || (off + j) % p.bs == 0) *block_scale(sdst[j]) = fresh(j);
+}
+
+}  // namespace
+
+tv_status launch_compact_q8(const CompactQ8Args& a) {
+    if (a.B == 0 || a.Hkv == 0 || a.num_layers == 0) return TV_OK;
+    CqParams p;
+    p.k = a.k_cache;
+    p.v = a.v_cache;
+    p.k_scale = a.k_scale;
+    p.v_scale = a.v_scale;
+    p.layer_stride = a.layer_stride;
+    p.scale_layer_stride = a.scale_layer_stride;
+    p.table = a.block_table;
+    p.prefix_lens = a.prefix_lens;
+    p.path = a.path;
+    p.accept_len = a.accept_len;
+    p.max_blocks = a.max_blocks;
+    p.max_path = a.max_path;
+    p.Hkv = a.Hkv;
+    p.bs = a.bs;
+    p.num_blocks = a.num_blocks;
+    p.rows = a.max_path < CQ_MAX_ROWS ? a.max_path : CQ_MAX_ROWS;
+    p.new_lens = a.new_lens;
+    p.src_slots = a.src_slots;
+    p.dst_slots = a.dst_slots;
+    p.status = a.status;
+    const dim3 grid((unsigned)((2 * a.Hkv + CQ_WARPS - 1) / CQ_WARPS), (unsigned)a.B, (unsigned)a.num_layers);
+    if (a.B > 65535 || a.num_layers > 65535) return TV_ERR_UNSUPPORTED;
+    LaunchCfg lc(grid, dim3(CQ_WARPS * 32), (size_t)CQ_WARPS * p.rows * a.d, a.stream);
+    const cudaError_t e = a.d == 128 ? cudaLaunchKernelEx(&lc.cfg, kv_compact_q8_kernel<128>, p)
+                                     : cudaLaunchKernelEx(&lc.cfg, kv_compact_q8_kernel<64>, p);
+    return e == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+}
+
+}  // namespace tv

@@ -160,6 +160,25 @@ struct CompactArgs {
 };
 tv_status launch_compact(const CompactArgs& a);
 
+struct CompactQ8Args {
+    uint8_t *k_cache, *v_cache;
+    float *k_scale, *v_scale;
+    int num_layers;
+    int64_t layer_stride, scale_layer_stride;
+    const int32_t* block_table;
+    int max_blocks;
+    const int32_t* prefix_lens;
+    const int32_t* path;
+    const int32_t* accept_len;
+    int max_path, B, Hkv, d, bs, num_blocks;
+    int32_t* new_lens;
+    int64_t* src_slots;
+    int64_t* dst_slots;
+    int32_t* status;
+    cudaStream_t stream;
+};
+tv_status launch_compact_q8(const CompactQ8Args& a);
+
 // Draft-tree construction limits: chunks per vocabulary row, top-k, nodes
 // created per tree (1 + k + (layers - 1) k^2).
 constexpr int DT_CH_MAX = 64;
@@ -202,8 +221,10 @@ struct ChunkAppendArgs {
     int max_blocks, bs, num_blocks, elem;
     int32_t* status;
     cudaStream_t stream;
+    float *k_scale = nullptr, *v_scale = nullptr;  // 8-bit caches
 };
 tv_status launch_chunk_append(const ChunkAppendArgs& a);
+tv_status launch_chunk_append_q8(const ChunkAppendArgs& a);
 tv_status make_rope_table(tv_rope_table* t, int dim, int interleaved, double theta,
                           tv_rope_scaling scaling, double factor, double original_len, double low,
                           double high, double amplitude);
@@ -259,5 +280,21 @@ struct LogitsArgs {
     cudaStream_t stream;
 };
 tv_status launch_tree_logits(const LogitsArgs& a);
+
+struct SampleArgs {
+    const void* logits;
+    tv_dtype dt;
+    int B, N, V;
+    const int32_t* node_counts;
+    const float* uniform;
+    const float* temp;
+    const int32_t* top_k;
+    const float *top_p, *min_p;
+    int32_t* tokens;
+    float* probs;
+    int32_t* status;
+    cudaStream_t stream;
+};
+tv_status launch_logits_sample(const SampleArgs& a);
 
 }  // namespace tv

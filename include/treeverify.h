@@ -554,6 +554,35 @@ tv_status chunk_attention(const void* q, int64_t q_stride, const void* k_cache,
  * ------------------------------------------------------------------------ */
 
 /* ------------------------------------------------------------------------
+ * chunk_kv_append_q8 — chunk_kv_append into an 8-bit cache: new keys and values
+ * rotated, then quantised; queries rotated.  q, k, v, q_out, strides, positions and
+ * rope as there, all of them bfloat16; keys and values are rounded once, from
+ * float32 to codes.
+ *
+ * Per block, kv head and cache that new rows fall into, with m their largest finite
+ * absolute value (of keys after the rotation):
+ *   scale = the smallest power of two, at least 2^-100, with m <= 448 scale; but at
+ *           least the block's present scale if it holds positions before P_b
+ *   new codes      = e4m3(value / scale), to the nearest, ties to even; infinities
+ *                    and NaN become NaN
+ *   earlier codes  (positions before P_b) = e4m3(code * present scale / scale)
+ * So a block that is appended to from its first position on starts anew, and the
+ * scale of one that is filled step by step only grows; rows of rejected drafts that
+ * a later call overwrites leave at most a larger scale behind.
+ * status int32 [B], refused sequences and host errors: as chunk_kv_append, for d 64
+ * or 128 and block sizes that are multiples of 16 (others: TV_ERR_UNSUPPORTED); NULL
+ * scales: TV_ERR_INVALID_ARG.  Two sequences must not append to the same block.
+ * ------------------------------------------------------------------------ */
+tv_status chunk_kv_append_q8(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, const int32_t* positions, int T,
+                             const int32_t* q_start, const int32_t* prefix_lens, int B, int Hq,
+                             int Hkv, int d, const tv_rope_table* rope, void* q_out,
+                             int64_t q_out_stride, void* k_cache, void* v_cache, float* k_scale,
+                             float* v_scale, const int32_t* block_table, int max_blocks_per_seq,
+                             int block_size, int num_blocks, int32_t* status,
+                             tv_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * chunk_attention_q8 — chunk_attention over an 8-bit cache, for every kind of new
  * token: prompts in chunks, single tokens and chains of drafts (the rows of a
  * sequence are causal), and trees (mask).
@@ -589,6 +618,28 @@ tv_status chunk_attention_q8(const void* q, int64_t q_stride, const void* k_cach
                              int window, int sinks, void* out, int64_t out_stride,
                              int32_t* status, void* workspace, size_t workspace_bytes,
                              tv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * kv_compact_q8 — kv_compact on 8-bit caches (the steps around it as there; on a
+ * chain the accepted rows lie where they belong already, and no call is needed).
+ *
+ * For every layer l (caches layer_stride bytes apart, scales scale_layer_stride
+ * numbers apart), kv head and cache: what the rows at positions P_b + path[b][j] stand
+ * for goes to positions P_b + j, gather-then-scatter.  The scale of a block that holds
+ * destinations becomes the largest of the scales of the blocks that its rows come
+ * from (its own among them where a row stays) and, where it holds positions before
+ * P_b, of its own; codes whose scale grows, those before P_b too, are rounded again.
+ * new_lens, src_slots, dst_slots, status and host errors: as kv_compact, for d 64 or 128
+ * (others: TV_ERR_UNSUPPORTED) and block sizes that are multiples of 16; NULL scales:
+ * TV_ERR_INVALID_ARG.  accept_len is below 64.
+ * ------------------------------------------------------------------------ */
+tv_status kv_compact_q8(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                        int num_layers, int64_t layer_stride, int64_t scale_layer_stride,
+                        const int32_t* block_table, int max_blocks_per_seq,
+                        const int32_t* prefix_lens, const int32_t* path,
+                        const int32_t* accept_len, int max_path, int B, int Hkv, int d,
+                        int block_size, int num_blocks, int32_t* new_lens, int64_t* src_slots,
+                        int64_t* dst_slots, int32_t* status, tv_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * token_counts_update — the history that tree_logits_process reads: counts
@@ -654,6 +705,45 @@ tv_status tree_logits_process(const void* logits, tv_dtype dt, int B, int N, int
                               const float* repetition, const float* frequency,
                               const float* presence, const float* temperature, int probs,
                               float* out, int32_t* status, tv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * logits_sample — sampling, for the rows that no draft covers (the first token behind
+ * a prompt, plain decoding), and the filtered distributions of a tree's rows as the
+ * target of tree_accept (TV_ACCEPT_STOCHASTIC; a draft model's rows likewise).
+ *
+ * logits: [B][N][V], float32 or bfloat16 (dt), -infinity for what is not allowed
+ * (tree_logits_process without probs).  Per row, with the parameters of its sequence,
+ * the entries ordered by (logit descending, index ascending):
+ *   temperature 0: the first entry is kept, with probability 1; otherwise
+ *   w_x = exp((logit_x - the largest) / temperature), and kept are
+ *   1. the first top_k entries (all for top_k <= 0 or >= V),
+ *   2. of these the entry e when the w of those before it sum to less than top_p times
+ *      the w of all of these (so the first one always; all for top_p = 1),
+ *   3. of these the entries with w >= min_p (0: all).
+ *   probs[b][i][x] = w_x / (the sum W of the kept ones), 0 for the others
+ *   tokens[b][i] = the smallest x with w_0 + .. + w_x (kept ones) > uniform[b][i] * W
+ * The w of 1 and 2 and the sums are in fixed point, steps of 2^-42, each w off by at
+ * most 2^-38 of itself and half a step: cuts and tokens differ from the exact ones only
+ * where a sum comes that near to its border.  probs are float32, off by at most 2^-20
+ * of themselves and of the exponent's rounding, 2^-23 (logit - largest) / temperature.
+ * temperature, top_p, min_p float32 [B], top_k int32 [B]: each may be NULL (1; 1; 0; all).
+ * uniform float32 [B][N], in [0, 1): the random numbers are the caller's.  probs float32
+ * [B][N][V] or NULL (not logits).  node_counts as above: rows of absent nodes are not
+ * written, nor are their tokens and statuses.
+ * status int32 [B][N], per row: TV_ERR_OUT_OF_RANGE for a node count outside [1, N];
+ * TV_ERR_BAD_VALUES for a temperature that is not finite, negative, or positive below
+ * 2^-126, a top_p outside (0, 1], a min_p outside [0, 1], a uniform outside [0, 1), and
+ * for a row with NaN or +infinity, or with nothing above -infinity.  Such a row has
+ * token -1 and probs 0.
+ * Host errors: TV_ERR_INVALID_ARG for N outside [1, 64], V outside [1, 2^24], B < 0, NULL
+ * logits, uniform, tokens or status; TV_ERR_UNSUPPORTED for V above 786,432 (a row is
+ * held in the shared memory of 16 SMs).
+ * ------------------------------------------------------------------------ */
+tv_status logits_sample(const void* logits, tv_dtype dt, int B, int N, int V,
+                        const int32_t* node_counts, const float* uniform,
+                        const float* temperature, const int32_t* top_k, const float* top_p,
+                        const float* min_p, int32_t* tokens, float* probs, int32_t* status,
+                        tv_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -109,3 +109,71 @@ def attention(c, *, scale=0.0, softcap=0.0, window=0, sinks=0, mask=None):
             if some.numel():
                 S[lo:lo + n, g * G:(g + 1) * G] = torch.where(seen[:, None], m, 0.0).amax(-1)
     return out, A, S
+
+
+def append(c, name, rows):
+    """The cache and scales [codes uint8, scales float64] after rows [T, heads, d] (float64: what is
+    quantised) have been appended to case c; block by block."""
+    code, scale = c[name + "_cache"].view(torch.uint8).clone(), c[name + "_scale"].double().clone()
+    bs = c["bs"]
+    for b, (n, P) in enumerate(zip(c["n"], c["P"])):
+        for lb in range(P // bs, (P + n - 1) // bs + 1) if n else ():
+            at = int(c["table"][b, lb])
+            lo, hi = max(P, lb * bs), min(P + n, (lb + 1) * bs)
+            x = rows[int(c["q_start"][b]) + lo - P:int(c["q_start"][b]) + hi - P].transpose(0, 1)   # [H, new, d]
+            s = need(torch.where(torch.isfinite(x), x.abs(), 0.0).amax((1, 2)))
+            r0, r1 = lo - lb * bs, hi - lb * bs
+            if r0:
+                s = torch.maximum(s, scale[at])
+                was = code[at, :, :r0].view(E4M3).double()
+                code[at, :, :r0] = to_code(was * (scale[at] / s)[:, None, None])
+            code[at, :, r0:r1] = to_code(x / s[:, None, None])
+            scale[at] = s
+    return code, scale
+
+
+def compact(c, name, path, accept):
+    """[codes uint8, scales float64] after the accepted paths have been moved."""
+    code, scale = c[name + "_cache"].view(torch.uint8).clone(), c[name + "_scale"].double().clone()
+    was, had, bs = code.clone(), scale.clone(), c["bs"]
+    for b, P in enumerate(c["P"]):
+        A, block = int(accept[b]), c["table"][b].tolist()
+        for lb in range(P // bs, (P + A) // bs + 1):
+            js = [j for j in range(A + 1) if (P + j) // bs == lb]
+            to, keep = block[lb], max(0, P - lb * bs)
+            s = torch.stack([had[block[(P + int(path[b, j])) // bs]] for j in js]).amax(0)
+            if keep:
+                s = torch.maximum(s, had[to])
+                code[to, :, :keep] = to_code(was[to, :, :keep].view(E4M3).double() * (had[to] / s)[:, None, None])
+            for j in js:
+                src = P + int(path[b, j])
+                x = was[block[src // bs], :, src % bs].view(E4M3).double() * had[block[src // bs]][:, None]
+                code[to, :, (P + j) % bs] = to_code(x / s[:, None])
+            scale[to] = s
+    return code, scale
+
+
+def sample_sets(x, temp, k, top_p, min_p):
+    """(weights, kept, near): exact weights of a row x (1-D), what the filters keep, and the entries
+    whose keeping hangs on a sum within 2^-30 of a border."""
+    x = x.double()
+    V = x.numel()
+    w = torch.zeros(V, dtype=torch.float64)
+    near = torch.zeros(V, dtype=torch.bool)
+    order = torch.argsort(x, descending=True, stable=True)
+    if temp == 0:
+        w[order[0]] = 1.0
+        return w, w > 0, near
+    w = torch.exp((x - x.max()) / temp)
+    kept = torch.zeros(V, dtype=torch.bool)
+    first = order[:k] if 0 < k < V else order
+    ww = w[first]
+    before = torch.cumsum(ww, 0) - ww
+    goal = top_p * float(ww.sum())
+    take = (before < goal) | (top_p >= 1.0)
+    take[0] = True
+    if top_p < 1.0:
+        near[first[(before - goal).abs() <= 2.0 ** -30 * float(ww.sum())]] = True
+    kept[first[take]] = True
+    near |= (w - min_p).abs() <= 2.0 ** -36
+    return w, kept & (w >= min_p), near
