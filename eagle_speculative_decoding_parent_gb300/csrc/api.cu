@@ -584,7 +584,9 @@ static bool q8_shape_ok(int Hq, int Hkv, int d) {
 }
 
 size_t chunk_attention_q8_workspace(int T, int B, int Hq, int Hkv, int d) {
-    return T < 1 || B < 1 || !q8_shape_ok(Hq, Hkv, d) ? 0 : chunk_attn_tc_workspace(T, B, Hq, Hkv, d);
+    if (T < 1 || B < 1 || !q8_shape_ok(Hq, Hkv, d)) return 0;
+    return rows_q8_applicable(T, B, Hq, Hkv) ? rows_q8_workspace(T, B, Hq, Hkv, d)
+                                             : chunk_attn_tc_workspace(T, B, Hq, Hkv, d);
 }
 
 tv_status chunk_attention_q8(const void* q, int64_t q_stride, const void* k_cache,
@@ -644,7 +646,8 @@ tv_status chunk_attention_q8(const void* q, int64_t q_stride, const void* k_cach
     a.ws = workspace;
     a.stream = (cudaStream_t)stream;
     // without rows there are only statuses to write
-    return T > 0 ? launch_chunk_attn_q8(a) : launch_chunk_attn_f32(a);
+    if (T == 0) return launch_chunk_attn_f32(a);
+    return rows_q8_applicable(T, B, Hq, Hkv) ? launch_rows_q8(a) : launch_chunk_attn_q8(a);
 }
 
 tv_status token_counts_update(int32_t* counts, const int32_t* tokens, const int32_t* starts,

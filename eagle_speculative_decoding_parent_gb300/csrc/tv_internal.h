@@ -90,6 +90,8 @@ bool make_cache_map(CUtensorMap* map, const void* base, int d, int64_t rows);
 // 64-column halves, [half][16 rows][64 columns], 128-byte swizzle.
 bool make_page_map(CUtensorMap* map, const void* base, int64_t rows);
 bool make_kpage_map(CUtensorMap* map, const void* base, int64_t rows);
+// An 8-bit cache with d = 128: box 16 rows of 128 codes, 128-byte swizzle.
+bool make_code_map(CUtensorMap* map, const void* base, int64_t rows);
 // Q [B*N][Hq][d] bf16: box 64 columns x G heads x npt nodes, 128-byte swizzle.
 bool make_q_map(CUtensorMap* map, const void* base, int d, int Hq, int64_t nodes, int G,
                 int npt);
@@ -258,6 +260,10 @@ bool chunk_attn_tc_applicable(int Hq, int Hkv, int d, tv_dtype dt);
 size_t chunk_attn_tc_workspace(int T, int B, int Hq, int Hkv, int d);
 tv_status launch_chunk_attn_tc(const ChunkAttnArgs& a);
 tv_status launch_chunk_attn_q8(const ChunkAttnArgs& a);  // the same, 8-bit caches
+// 8-bit caches, a few rows per sequence
+bool rows_q8_applicable(int T, int B, int Hq, int Hkv);
+size_t rows_q8_workspace(int T, int B, int Hq, int Hkv, int d);
+tv_status launch_rows_q8(const ChunkAttnArgs& a);
 
 tv_status launch_token_counts(int32_t* counts, const int32_t* tokens, const int32_t* starts,
                               int total, int B, int V, bool clear, bool prompt, int32_t* status,
