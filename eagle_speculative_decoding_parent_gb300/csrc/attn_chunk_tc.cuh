@@ -85,7 +85,7 @@ constexpr int FIX_BUFS = 4;        // items whose V notes may be live (see warp 
 // row (both streams' rows of D + 4 floats fit the second Q tile): one warp would write
 // them out alone otherwise.
 constexpr int FEW = 30;
-static_assert(2 * FEW * (128 + 4) * 4 <= MT * 128 * 2 && 2 * FEW * (64 + 4) * 4 <= MT * 64 * 2, "xo");
+static_assert(2 * FEW * (128 + 4) * 4 + 2 * MT * 4 <= MT * 128 * 2 && 2 * FEW * (64 + 4) * 4 <= MT * 64 * 2, "xo");
 // a border this close to an item's end (in tiles) moves there: a cut costs more than the
 // imbalance
 constexpr int SNAP = 2;
@@ -117,23 +117,32 @@ struct Lay {
     static constexpr int HALVES = D / 64;
     static constexpr int PAGE_BYTES = 16 * D * 2;
     static constexpr int SLOT_BYTES = KT * D * 2;
-    static constexpr int SLOTS = (E8 ? 3 : 5) * (128 / D);
-    // 8-bit caches: tiles of codes as they come, and their pages' scales (exponent bytes)
+    // 8-bit caches: tiles of codes as they come, and their pages' scales (exponent bytes).  With
+    // d = 128 a key's codes are a row of 128 bytes, which the tensor core takes as it is: only V is
+    // widened (K8).
+    static constexpr bool K8 = E8 && D == 128;
+    static constexpr int SLOTS = K8 ? 2 : (E8 ? 3 : 5) * (128 / D);
     static constexpr int RAW_BYTES = KT * D;
-    static constexpr int RAWS = E8 ? 4 * (128 / D) : 0;
+    static constexpr int RAWS = K8 ? 3 : E8 ? 4 * (128 / D) : 0;
+    static constexpr int KSLOTS = K8 ? 3 : 0;
+    static constexpr int KEXPS = 8;                        // tiles of K whose scales are kept
     static constexpr int Q_BYTES = MT * D * 2;             // one row tile
     static constexpr int OFF_RING = 0;
     static constexpr int OFF_RAW = SLOTS * SLOT_BYTES;
-    static constexpr int OFF_Q = OFF_RAW + RAWS * RAW_BYTES;  // two row tiles
+    static constexpr int OFF_K = OFF_RAW + RAWS * RAW_BYTES;
+    static constexpr int OFF_Q = OFF_K + KSLOTS * RAW_BYTES;  // two row tiles
     static constexpr int OFF_X = OFF_Q + Q_BYTES;          // epilogue of one row tile: the second Q tile
     static constexpr int OFF_ITEMS = OFF_Q + 2 * Q_BYTES;  // [GQ]
     static constexpr int OFF_MISC = OFF_ITEMS + GQ * 64;   // tensor memory's address, abort flag
     static constexpr int OFF_BARS = OFF_MISC + 16;
-    static constexpr int NBARS = (E8 ? 2 * SLOTS + 2 * RAWS : 3 * SLOTS) + 8 + 4 + 2 * GQ + 2;
-    static constexpr int OFF_EXP = OFF_BARS + NBARS * 8;   // [RAWS][8 pages]
-    static constexpr int OFF_BAD = (OFF_EXP + RAWS * 8 + 15) / 16 * 16;  // [FIX_BUFS][FIX_TILES][4]
-    static constexpr int OFF_ML = OFF_BAD + FIX_BUFS * FIX_TILES * 16;  // join: maximum, sum per row
-    static constexpr int BYTES = OFF_ML + 2 * MT * 4 + 1024;   // + alignment slack
+    static constexpr int NBARS = (E8 ? 2 * SLOTS + 2 * RAWS + 2 * KSLOTS + (K8 ? 1 : 0) : 3 * SLOTS) + 8 + 4 + 2 * GQ + 2;
+    static constexpr int OFF_EXP = OFF_BARS + NBARS * 8;   // [RAWS][8 pages], K8: and [KEXPS][8]
+    static constexpr int OFF_BAD = (OFF_EXP + (RAWS + (K8 ? KEXPS : 0)) * 8 + 15) / 16 * 16;  // [FIX_BUFS][FIX_TILES][4]
+    static constexpr int OFF_END = OFF_BAD + FIX_BUFS * FIX_TILES * 16;
+    // join: maximum, sum per row (K8: behind what the epilogue has in the second Q tile)
+    static constexpr int OFF_ML = K8 ? OFF_X + Q_BYTES - 2 * MT * 4 : OFF_END;
+    static constexpr int OFF_QX = OFF_END;                 // K8: exponents of the query rows' scales, of two items
+    static constexpr int BYTES = OFF_END + (K8 ? 2 * 2 * MT : 2 * MT * 4) + 1024;   // + alignment slack
     static_assert(OFF_ITEMS % 1024 == 0 && OFF_BAD - OFF_ITEMS <= 1024, "the barriers beside the abort flag");
 };
 static_assert(Lay<128, false>::BYTES <= 232448 && Lay<64, false>::BYTES <= 232448 && Lay<128, true>::BYTES <= 232448 &&
@@ -396,6 +405,33 @@ __device__ __forceinline__ void mma_s(uint32_t d, uint64_t a, uint64_t b, uint64
             : "memory");
     }
 }
+// The same of queries and keys in e4m3: the query tile's two parts (16 KB apart; their sum is the
+// query) times the keys, 32 columns a product.
+__device__ __forceinline__ void mma_s8(uint32_t d, uint64_t a, uint64_t b, uint64_t* bar) {
+    constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(KT >> 3) << 17) | ((uint32_t)(MT >> 4) << 24);
+    asm volatile(
+        "{\n\t.reg .pred e, f, t;\n\t.reg .b64 a, b;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, f;\n\t"
+        "add.u64 a, %1, 1024;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, %2, %3, t;\n\t"
+        "add.u64 a, %1, 2;\n\tadd.u64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 1026;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 4;\n\tadd.u64 b, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 1028;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 6;\n\tadd.u64 b, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.u64 a, %1, 1030;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(IDESC), "r"(smem_u32(bar))
+        : "memory");
+}
 // O (+)= P V of one tile: P in tensor memory (8 columns per K = 16 step), V a page per step.
 template <int D>
 __device__ __forceinline__ void mma_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate) {
@@ -450,11 +486,13 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return (w & 0x7f7f7f
 // pages' scales follow two tiles later, so that their loads (behind the block ids') hold up no
 // copy: a byte each, and an arrival of their own on the tile's barrier.
 template <class L, int D, class Take>
-__device__ __forceinline__ void load_codes(const Params& p, uint8_t* smem, uint64_t* rfull, uint64_t* rempty,
+__device__ __forceinline__ void load_codes(const Params& p, const CUtensorMap& kmap, uint8_t* smem, uint64_t* rfull,
+                                           uint64_t* rempty, uint64_t* kfull, uint64_t* kempty,
                                            volatile int* abort_flag, Take& take, bool& alive) {
     constexpr int PAGE = 16 * D, WT = 32 / (KT / 16);      // tiles of a window of 32 pages, a lane each
     const int lane = threadIdx.x & 31;
-    uint32_t ld = 0, slot = 0, ph = 0;
+    uint32_t ld = 0, slot = 0, ph = 0;                     // K8: V's
+    uint32_t kld = 0, kslot = 0, kph = 0, ksent = 0;       // K8: K's; scales sent
     Item it;
     for (uint32_t k = 0; alive && take(k, it); ++k) {
         if (it.n == 0) continue;
@@ -492,6 +530,16 @@ __device__ __forceinline__ void load_codes(const Params& p, uint8_t* smem, uint6
             const bool now = j / WT == wk;
             const uint32_t mine = is_v ? exponent_byte(now ? vs : pvs) : exponent_byte(now ? ks : pks);
             const uint32_t e = __shfl_sync(0xffffffffu, mine, (j % WT) * (KT / 16) + (lane & 7));
+            if constexpr (L::K8) {
+                if (!is_v) {
+                    if (lane < 8) smem[L::OFF_EXP + (L::RAWS + ksent % L::KEXPS) * 8 + lane] = (uint8_t)e;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&kfull[ksent % L::KSLOTS]);
+                    __syncwarp();
+                    ++ksent;
+                    return;
+                }
+            }
             if (lane < 8) smem[L::OFF_EXP + sent * 8 + lane] = (uint8_t)e;
             __syncwarp();
             if (lane == 0) mbar_arrive(&rfull[sent]);
@@ -516,6 +564,22 @@ __device__ __forceinline__ void load_codes(const Params& p, uint8_t* smem, uint6
             }
             const int pages = min(KT / 16, (vend - (it.t_lo + j) * KT + 15) >> 4);
             const int y = __shfl_sync(0xffffffffu, w == wk ? row : prow, (j % WT) * (KT / 16) + (lane & 7));
+            if constexpr (L::K8) {
+                if (!is_v) {
+                    alive = wait_all<64>(&kempty[kslot], kph ^ 1u);
+                    if (!alive) break;
+                    mbar_arrive_expect_tx_relaxed_elect(&kfull[kslot], (uint32_t)pages * PAGE);
+                    if (lane < pages)
+                        tma_load_2d(smem + L::OFF_K + kslot * L::RAW_BYTES + lane * PAGE, &kmap, &kfull[kslot], 0, y, policy);
+                    __syncwarp();
+                    ++kld;
+                    if (++kslot == L::KSLOTS) {
+                        kslot = 0;
+                        kph ^= 1u;
+                    }
+                    continue;
+                }
+            }
             alive = wait_all<64>(&rempty[slot], ph ^ 1u);
             if (!alive) break;
             mbar_arrive_expect_tx_relaxed_elect(&rfull[slot], (uint32_t)pages * PAGE);
@@ -536,6 +600,71 @@ __device__ __forceinline__ void load_codes(const Params& p, uint8_t* smem, uint6
     // copies in flight end before the CTA does
     for (uint32_t u = ld > (uint32_t)L::RAWS ? ld - L::RAWS : 0; u < ld; ++u)
         wait_own(&rfull[u % L::RAWS], (u / L::RAWS) & 1u);
+    if constexpr (L::K8)
+        for (uint32_t u = kld > (uint32_t)L::KSLOTS ? kld - L::KSLOTS : 0; u < kld; ++u)
+            wait_own(&kfull[u % L::KSLOTS], (u / L::KSLOTS) & 1u);
+}
+
+// Row r of the item's query tiles (d = 128), bfloat16, into two e4m3 parts in its place: scaled by
+// the power of two that brings its largest element to 2^7 .. 2^8, the nearest code and what is
+// left.  Eight significant bits go into two codes of four exactly, down to 2^-18 of the largest
+// element (the codes' smallest step, 2^-9; elements below lose bits).  Its exponent is noted.
+template <class L>
+__device__ __forceinline__ void split_queries(const Params& p, uint8_t* smem, const Item& it, int r, uint32_t buf) {
+    const int nq = (it.flags & ITEM_TWO) ? 2 : 1;
+#pragma unroll 1
+    for (int t = 0; t < nq; ++t) {
+        const int rows = p.G * min(it.ntok - t * p.npt, p.npt);
+        if ((r & ~31) >= rows) continue;                   // (nothing in this warp: zeros, or rows that no one reads)
+        uint8_t* row = smem + L::OFF_Q + t * L::Q_BYTES + r * 128;
+        auto piece = [&](int c) -> uint4 {                 // columns 8 c .. 8 c + 7
+            return *reinterpret_cast<const uint4*>(row + (c >> 3) * (MT * 128) + (((c & 7) ^ (r & 7)) << 4));
+        };
+        float top = 0.f;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            const uint4 x = piece(c);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const float a = __uint_as_float(w[y] << 16), b = __uint_as_float(w[y] & 0xffff0000u);
+                top = fmaxf(top, fmaxf(fabsf(fmaf(a, 0.f, a)), fabsf(fmaf(b, 0.f, b))));   // finite ones
+            }
+        }
+        const uint32_t ex = min(max(__float_as_uint(top) >> 23, 20u), 253u);
+        const float up = __uint_as_float(min(261u - ex, 254u) << 23);      // 2^(7 - exponent)
+        smem[L::OFF_QX + (buf * 2 + t) * MT + r] = (uint8_t)ex;
+        // sixteen columns at a time; what lies where the second part goes is held
+        uint4 back[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) back[c] = piece(8 + c);
+#pragma unroll
+        for (int c = 0; c < 16; c += 2) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 x = c < 8 ? piece(c + h) : back[(c + h) & 7];
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int y = 0; y < 4; y += 2) {
+                    float f[4];
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        f[2 * z] = __uint_as_float(w[y + z] << 16) * up;
+                        f[2 * z + 1] = __uint_as_float(w[y + z] & 0xffff0000u) * up;
+                    }
+                    // (an infinite element becomes NaN, as the products with it are)
+                    const uint32_t c0 = e4m3_pair(f[0] + f[0] * 0.f, f[1] + f[1] * 0.f), c1 = e4m3_pair(f[2] + f[2] * 0.f, f[3] + f[3] * 0.f);
+                    hi[2 * h + y / 2] = c0 | c1 << 16;
+                    lo[2 * h + y / 2] = e4m3_pair(f[0] - e4m3_float(c0 & 0xffu), f[1] - e4m3_float(c0 >> 8)) |
+                                        e4m3_pair(f[2] - e4m3_float(c1 & 0xffu), f[3] - e4m3_float(c1 >> 8)) << 16;
+                }
+            }
+            const int at = ((c >> 1) ^ (r & 7)) << 4;
+            *reinterpret_cast<uint4*>(row + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(row + MT * 128 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+    }
 }
 
 // Warps 12 - 15 of an 8-bit kernel: a tile's codes to bfloat16, exactly, where the products
@@ -547,8 +676,8 @@ __device__ __forceinline__ void load_codes(const Params& p, uint8_t* smem, uint6
 // (see warp 10 of the other kernels).
 template <class L, int D, class Take>
 __device__ __forceinline__ void widen_codes(const Params& p, uint8_t* smem, uint64_t* full, uint64_t* empty,
-                                            uint64_t* rfull, uint64_t* rempty, uint32_t* bad,
-                                            volatile int* abort_flag, Take& take, bool& alive) {
+                                            uint64_t* rfull, uint64_t* rempty, uint64_t* qfull, uint64_t* qready,
+                                            uint32_t* bad, volatile int* abort_flag, Take& take, bool& alive) {
     constexpr int NCH = D / 16;                            // 16-code pieces of a row
     const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) - CONV_WARP;
     const int r = q * 32 + lane, r16 = r & 15, r8 = r & 7;
@@ -567,12 +696,20 @@ __device__ __forceinline__ void widen_codes(const Params& p, uint8_t* smem, uint
         ++live;
         if (lane < FIX_TILES) notes[lane * 4 + q] = 0u;
         __syncwarp();
+        if constexpr (L::K8) {
+            alive = wait_all<64>(qfull, (live - 1) & 1u);
+            if (!alive) break;
+            split_queries<L>(p, smem, it, r, (live - 1) & 1u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qready);
+        }
         const int lag = two ? 1 : 2;
 #pragma unroll 1
         for (int x = 0; x < 2 * (it.n + lag); ++x) {
             const bool is_v = (x & 1) == 0;
             const int j = (x >> 1) - (is_v ? lag : 0);
-            if (j < 0 || j >= it.n) continue;
+            if (j < 0 || j >= it.n || (L::K8 && !is_v)) continue;
             const int t = it.t_lo + j;
             alive = wait_all<64>(&rfull[rs], rph);
             if (!alive) break;
@@ -737,6 +874,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     uint64_t* vraw = xall + 2;            // [SLOTS] a V tile that warp 10 goes through has landed
     uint64_t* rfull = xall + 2;           // [RAWS] 8-bit caches: a tile of codes has landed,
     uint64_t* rempty = rfull + L::RAWS;   // [RAWS] has been read
+    uint64_t* kfull = rempty + L::RAWS;   // [KSLOTS] K8: a tile of K has landed,
+    uint64_t* kempty = kfull + L::KSLOTS; // [KSLOTS] has been used;
+    uint64_t* qready = kempty + L::KSLOTS; // the queries are in two parts
     auto* tmp = reinterpret_cast<ChunkLocateTmp<THREADS>*>(smem + L::OFF_RING);  // before the first copy
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_ITEMS + ABORT_AT);
@@ -753,6 +893,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             mbar_init(&rfull[s], 2);   // the copies' bytes, the scales
             mbar_init(&rempty[s], CONV_WARPS);
         }
+        for (int s = 0; s < L::KSLOTS; ++s) {
+            mbar_init(&kfull[s], 2);
+            mbar_init(&kempty[s], 1);
+        }
+        if constexpr (L::K8) mbar_init(qready, CONV_WARPS);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
             mbar_init(&pfull[i], 4);
@@ -921,7 +1066,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     } else if (warp == LOAD_WARP) {
         // ============================ K/V producer ============================
         if constexpr (E8) {
-            load_codes<L, D>(p, smem, rfull, rempty, abort_flag, take, alive);
+            if constexpr (L::K8) {
+                if (lane == 0) tma_prefetch_desc(&kmap);
+            }
+            load_codes<L, D>(p, kmap, smem, rfull, rempty, kfull, kempty, abort_flag, take, alive);
         } else {
         if (lane == 0) {
             tma_prefetch_desc(&kmap);
@@ -1002,7 +1150,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         }
         }
     } else if (E8 && warp >= CONV_WARP) {
-        widen_codes<L, D>(p, smem, full, empty, rfull, rempty, bad, abort_flag, take, alive);
+        widen_codes<L, D>(p, smem, full, empty, rfull, rempty, qfull, qready, bad, abort_flag, take, alive);
     } else if (warp == MMA_WARP) {
         // ============================== products ==============================
         uint32_t slot = 0, par = 0;                    // next ring position: slot, parity of its round
@@ -1019,8 +1167,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 ph ^= 1u;
             }
         };
+        const uint64_t kd8 = smem_desc_sw128(sbase + L::OFF_K, 16, 1024);
+        uint32_t kslot = 0, kpar = 0;                  // K8: K's ring
         auto issue_s = [&](int i, int qt, uint32_t s) {
-            mma_s<D>(tmem + i * KT, qd + qt * (L::Q_BYTES / 16), kd + s * (L::SLOT_BYTES / 16), &sfull[i]);
+            if constexpr (L::K8) mma_s8(tmem + i * KT, qd + qt * (L::Q_BYTES / 16), kd8 + s * (L::RAW_BYTES / 16), &sfull[i]);
+            else mma_s<D>(tmem + i * KT, qd + qt * (L::Q_BYTES / 16), kd + s * (L::SLOT_BYTES / 16), &sfull[i]);
         };
         auto issue_pv = [&](int i, uint32_t s, bool first) {
             mma_pv<D>(tmem + TMEM_O + i * D, tmem + i * KT, vd + s * (L::SLOT_BYTES / 16), first ? 0u : 1u);
@@ -1040,9 +1191,70 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         for (uint32_t k = 0; alive && take(k, it); ++k) {
             if (it.n == 0) continue;
             const int n = it.n;
-            alive = wait_mma(qfull, qi & 1u);
+            alive = wait_mma(L::K8 ? qready : qfull, qi & 1u);
             ++qi;
-            if (it.flags & ITEM_TWO) {
+            auto next_k = [&]() {
+                if (++kslot == (uint32_t)L::KSLOTS) {
+                    kslot = 0;
+                    kpar ^= 1u;
+                }
+            };
+            if (L::K8 && (it.flags & ITEM_TWO)) {
+                // K(0) V(0) K(1) V(1) ..., each in its own ring
+                alive = alive && wait_mma(&kfull[kslot], kpar);
+                if (!alive) break;
+                tc_fence_after();
+                issue_s(0, 0, kslot);
+                issue_s(1, 1, kslot);
+                tc_commit_elect(&kempty[kslot]);
+                next_k();
+                if (n == 1) tc_commit_elect(qempty);
+#pragma unroll 1
+                for (int j = 1; j <= n; ++j) {
+                    alive = wait_mma(&full[slot], par);            // V(j - 1)
+                    if (j < n) alive = alive && wait_mma(&kfull[kslot], kpar);   // K(j)
+                    alive = alive && wait_p(0, j == 1);
+                    if (!alive) break;
+                    issue_pv(0, slot, j == 1);
+                    if (j < n) issue_s(0, 0, kslot);
+                    else tc_commit_elect(&ofull[0]);
+                    alive = wait_p(1, j == 1);
+                    if (!alive) break;
+                    issue_pv(1, slot, j == 1);
+                    tc_commit_elect(&empty[slot]);
+                    if (j < n) {
+                        issue_s(1, 1, kslot);
+                        tc_commit_elect(&kempty[kslot]);
+                        if (j == n - 1) tc_commit_elect(qempty);
+                        next_k();
+                    } else {
+                        tc_commit_elect(&ofull[1]);
+                    }
+                    next(slot, par);
+                }
+            } else if (L::K8) {
+#pragma unroll 1
+                for (int j = 0; j < n + 2; ++j) {
+                    const int i = j & 1;
+                    if (j >= 2 && j - 2 < n) {
+                        alive = wait_mma(&full[slot], par) && wait_p(i, j < 4);
+                        if (!alive) break;
+                        issue_pv(i, slot, j < 4);
+                        tc_commit_elect(&empty[slot]);
+                        if (j >= n) tc_commit_elect(&ofull[i]);
+                        next(slot, par);
+                    }
+                    if (j < n) {
+                        alive = wait_mma(&kfull[kslot], kpar);
+                        if (!alive) break;
+                        tc_fence_after();
+                        issue_s(i, 0, kslot);
+                        tc_commit_elect(&kempty[kslot]);
+                        if (j == n - 1) tc_commit_elect(qempty);
+                        next_k();
+                    }
+                }
+            } else if (it.flags & ITEM_TWO) {
                 // ring order K(0) V(0) K(1) V(1) ...; both streams read every tile
                 alive = alive && wait_mma(&full[slot], par);
                 if (!alive) break;
@@ -1204,7 +1416,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         const uint32_t tS = tmem + lane_off + i * KT, tO = tmem + lane_off + TMEM_O + i * D;
         float* xo = reinterpret_cast<float*>(smem + L::OFF_X);  // [columns][rows]
         float* ml = reinterpret_cast<float*>(smem + L::OFF_ML);
-        uint32_t sc = 0, oc = 0, live = 0, xc = 0;
+        uint32_t sc = 0, oc = 0, live = 0, xc = 0, kc = 0;    // kc: tiles of the items before
         // every softmax warp has written xo (0), has read it (1): with a bounded wait, unlike
         // bar.sync
         auto all_x = [&](int which) {
@@ -1260,6 +1472,20 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 // registers each) half by half, the second half's maximum first; it is then read again.
                 constexpr int PART = E8 ? KT / 2 : KT;
                 const bool edge = j < ja || j >= jb;
+                // K8: what the columns of 16 keys are multiplied by (the scale of the keys' block, of the
+                // row, and into units of log 2).  Never zero: times -infinity it has to stay that.
+                uint32_t kx[2] = {0u, 0u};
+                float row_scale = 1.f;
+                if constexpr (L::K8) {
+                    const uint2 e = *reinterpret_cast<const uint2*>(smem + L::OFF_EXP + (L::RAWS + (kc + j) % L::KEXPS) * 8);
+                    kx[0] = e.x;
+                    kx[1] = e.y;
+                    row_scale = scale_inverse(__uint_as_float(min(261u - (uint32_t)smem[L::OFF_QX + ((live & 1u) * 2 + (two ? i : 0)) * MT + row], 254u) << 23)) *
+                                (CAP ? 1.f : p.scale_log2);
+                }
+                auto key_scale = [&](int c) -> float {         // of column c of the tile
+                    return fmaxf(scale_of((kx[c >> 6] >> (((c >> 4) & 3) * 8)) & 0xffu) * row_scale, 1.2e-38f);
+                };
                 float sv[PART];
                 auto load_s = [&](int h0) {
                     uint32_t r[PART / 32][32];
@@ -1269,10 +1495,17 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
 #pragma unroll
                     for (int c = 0; c < PART; ++c) sv[c] = __uint_as_float(r[c / 32][c % 32]);
                 };
-                const float csc = CAP ? 1.f : p.scale_log2;
+                const float csc = CAP || L::K8 ? 1.f : p.scale_log2;
                 // loads a part, caps and masks it; its maximum
                 auto part_max = [&](int h0) -> float {
                     load_s(h0);
+                    if constexpr (CAP && L::K8) {
+#pragma unroll
+                        for (int c = 0; c < PART; c += 2) {
+                            const float f = key_scale(h0 + c);
+                            f2_unpack(f2_mul(f2_pack(sv[c], sv[c + 1]), f2_pack(f, f)), sv[c], sv[c + 1]);
+                        }
+                    }
                     if constexpr (CAP) {
                         // cap tanh(scale s / cap), in units of log 2.  An exponential and a reciprocal
                         // more per score would bind on the special function unit, so arguments up to
@@ -1300,7 +1533,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) {
-                                    const float x = __uint_as_float(r[e]), u = x * x;
+                                    const float x = __uint_as_float(r[e]) * (L::K8 ? key_scale(h0 + c) : 1.f), u = x * x;
                                     const float w = ex2_approx(x * p.scale_log2);
                                     const float y = fmaf(-2.f * p.cap_log2, rcp_approx(1.f + w), p.cap_log2);
                                     r[e] = __float_as_uint(
@@ -1333,6 +1566,19 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
 #pragma unroll
                             for (int c = 0; c < 32; ++c) sv[h + c] = ((vis >> c) & 1u) ? sv[h + c] : -INFINITY;
                         }
+                    }
+                    if constexpr (L::K8 && !CAP) {
+                        float all = -INFINITY;
+#pragma unroll
+                        for (int g = 0; g < PART; g += 16) {
+                            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                            for (int c = 0; c < 16; c += 8)
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) mx[u] = fmax3(mx[u], sv[g + c + u], sv[g + c + 4 + u]);
+                            all = fmaxf(all, fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * key_scale(h0 + g));
+                        }
+                        return all;
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -1387,7 +1633,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
 #pragma unroll
                         for (int c = 0; c < 64; c += 2) {
                             float xa, xb;
-                            f2_unpack(f2_fma(f2_pack(sv[h + c], sv[h + c + 1]), sc2, nb2), xa, xb);
+                            uint64_t by = sc2;
+                            if constexpr (L::K8 && !CAP) {
+                                const float f = key_scale(h0 + h + c);
+                                by = f2_pack(f, f);
+                            }
+                            f2_unpack(f2_fma(f2_pack(sv[h + c], sv[h + c + 1]), by, nb2), xa, xb);
                             const float a = ex2_approx(xa), b2 = ex2_approx(xb);
                             acc[(c >> 1) & 3] = f2_add(acc[(c >> 1) & 3], f2_pack(a, b2));
                             // weights to bfloat16, the products' input type: at most 2^-8 of each
@@ -1413,6 +1664,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             float* pslot = it.slot >= 0 ? p.part + (int64_t)it.slot * p.prows * (D + 2) : nullptr;
             const uint32_t* notes = bad + (live % FIX_BUFS) * FIX_TILES * 4;
             if (it.n > 0) ++live;
+            kc += it.n;
             if (have) {
                 if (!wait_all(&ofull[i], (oc++) & 1u)) {
                     alive = false;
@@ -1705,7 +1957,8 @@ tv_status launch_any(const ChunkAttnArgs& a) {
     CUtensorMap qm, km, vm;
     if (!make_q_rows_map(&qm, a.q, a.d, a.Hq, a.T, a.q_stride, G, npt)) return TV_ERR_CUDA;
     if constexpr (E8) {
-        km = vm = qm;                                          // (codes come without tensor maps)
+        km = vm = qm;                                          // (the others come without tensor maps)
+        if (a.d == 128 && !make_code_map(&km, a.k_cache, rows)) return TV_ERR_CUDA;
     } else {
         const bool maps = a.d == 128 ? make_kpage_map(&km, a.k_cache, rows) && make_page_map(&vm, a.v_cache, rows)
                                      : make_cache_map(&km, a.k_cache, 64, rows) && make_cache_map(&vm, a.v_cache, 64, rows);

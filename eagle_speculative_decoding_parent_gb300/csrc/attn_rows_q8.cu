@@ -64,7 +64,7 @@ constexpr int RQ_PIECE = 1, RQ_LAST = 2, RQ_LATE = 4;
 template <int NT>
 struct RqShape {
     static constexpr int ROWS = 8 * NT;
-    static constexpr int PER_SM = NT == 1 ? 4 : NT == 2 ? 3 : 2;
+    static constexpr int PER_SM = NT == 1 ? 3 : 2;
     static constexpr int STAGES = NT == 3 ? 5 : 3;
 };
 
@@ -150,6 +150,7 @@ rows_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     __shared__ ChunkLocateTmp<RQ_THREADS> tmp;
     __shared__ __align__(8) uint64_t bars[RQ_WARPS][ST];
     __shared__ float sm_m[RQ_WARPS][ROWS], sm_l[RQ_WARPS][ROWS];
+    __shared__ __align__(16) uint4 sq[NT][D / 32][32];     // the queries, as the products take them
     __shared__ int late;
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(rq_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q4 = lane & 3, r8 = lane >> 2;
@@ -211,10 +212,9 @@ rows_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 const bool whole = lo == 0 && up == pages;
                 if (g == 0 && i0 == 0 && lo == 0 && tid == 0) p.status[b] = ok ? TV_OK : TV_ERR_OUT_OF_RANGE;
                 const int steps = max(0, (up - lo - warp + RQ_WARPS - 1) / RQ_WARPS);
-                // ---- queries: row 8 j + r8, its columns q4 D / 4 .. + D / 4
-                uint32_t qf[NT][2 * KS];
+                // ---- queries: row 8 j + r8, its columns q4 D / 4 .. + D / 4 (in shared memory: registers are
+                // for O)
                 float fac[NT][2];
-                int self[NT][2];
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
                     const int rr = 8 * j + r8;
@@ -242,9 +242,11 @@ rows_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 #pragma unroll
                     for (int e = 0; e < D / 32; ++e) {
                         const uint32_t w[4] = {x4[e].x, x4[e].y, x4[e].z, x4[e].w};
+                        uint32_t h[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
-                            qf[j][e * 4 + y] = half2_of(__uint_as_float(w[y] << 16) * up2, __uint_as_float(w[y] & 0xffff0000u) * up2);
+                            h[y] = half2_of(__uint_as_float(w[y] << 16) * up2, __uint_as_float(w[y] & 0xffff0000u) * up2);
+                        if (j % RQ_WARPS == warp) sq[j][e][lane] = make_uint4(h[0], h[1], h[2], h[3]);
                     }
                     const float down = scale_inverse(up2);
                     fac[j][0] = __shfl_sync(0xffffffffu, down, 8 * q4);
@@ -253,9 +255,8 @@ rows_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         fac[j][0] *= p.scale_log2;
                         fac[j][1] *= p.scale_log2;
                     }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) self[j][e] = s.P + i0 + min((8 * j + 2 * q4 + e) / p.G, ntok - 1);
                 }
+                __syncthreads();
                 const int first_all = p.window > 0 ? max(0, s.P + i0 + ntok - p.window) : 0;   // seen by every row
                 // ---- pages: a window of 32 steps, a lane each; the next one's blocks, then scales, ahead
                 const int32_t* table = p.c.table + (int64_t)b * p.c.max_blocks;
@@ -308,12 +309,15 @@ rows_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 };
 #pragma unroll
                 for (int i = 0; i < ST; ++i) fill(i);
-                float o[NT][KS][4], m[NT][2], l[NT][2];
+                // nb: the bias less the running maximum (of s + log2 of V's scale; none yet: 0); lim: what a
+                // score may exceed it by
+                float o[NT][KS][4], nb[NT][2], lim[NT][2], l[NT][2];
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
 #pragma unroll
                     for (int t = 0; t < KS; ++t) o[j][t][0] = o[j][t][1] = o[j][t][2] = o[j][t][3] = 0.f;
-                    m[j][0] = m[j][1] = -INFINITY;
+                    nb[j][0] = nb[j][1] = RQ_BIAS;
+                    lim[j][0] = lim[j][1] = -INFINITY;
                     l[j][0] = l[j][1] = 0.f;
                 }
                 int i = 0;
@@ -349,35 +353,46 @@ rows_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         }
                         const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            uint32_t a0, a1, a2, a3;
-                            e4m3_halves(w0[y], a0, a2);
-                            e4m3_halves(w1[y], a1, a3);
+                        for (int z = 0; z < 2; ++z) {
+                            uint32_t a[2][4];
 #pragma unroll
-                            for (int j = 0; j < NT; ++j) mma_f16(sc[j], a0, a1, a2, a3, qf[j][(hf * 4 + y) * 2], qf[j][(hf * 4 + y) * 2 + 1]);
+                            for (int y = 0; y < 2; ++y) {
+                                e4m3_halves(w0[2 * z + y], a[y][0], a[y][2]);
+                                e4m3_halves(w1[2 * z + y], a[y][1], a[y][3]);
+                            }
+#pragma unroll
+                            for (int j = 0; j < NT; ++j) {
+                                const uint4 b = sq[j][hf * 2 + z][lane];
+                                mma_f16(sc[j], a[0][0], a[0][1], a[0][2], a[0][3], b.x, b.y);
+                                mma_f16(sc[j], a[1][0], a[1][1], a[1][2], a[1][3], b.z, b.w);
+                            }
                         }
                     }
-                    // ---- scores in units of log 2, with V's scale; what a row does not see is -infinity
+                    // ---- scores in units of log 2, with V's scale, less the running maximum; what a row does
+                    // not see is -infinity
                     const int v0 = (lo + warp + i * RQ_WARPS) * 16, key0 = key_of(v0);
                     const bool edge = !(v0 < front ? v0 + 16 <= p.sinks
                                                    : key0 >= first_all && key0 + 15 <= s.P + i0 - (p.mask ? i0 + 1 : 0));
                     bool need = false;
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
+                        const float f0 = ks * fac[j][0], f1 = ks * fac[j][1];
+                        const float b0 = ev + nb[j][0], b1 = ev + nb[j][1];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            float y = sc[j][e] * ks * fac[j][e & 1];
                             if constexpr (CAP) {
-                                const float u = y * y, w = ex2_approx(y * p.scale_log2);
-                                y = u < p.cap_small ? y * fmaf(fmaf(p.cap_c[2], u, p.cap_c[1]), u, p.cap_c[0])
-                                                    : fmaf(-2.f * p.cap_log2, rcp_approx(1.f + w), p.cap_log2);
+                                const float y = sc[j][e] * (e & 1 ? f1 : f0), u = y * y, w = ex2_approx(y * p.scale_log2);
+                                sc[j][e] = (u < p.cap_small ? y * fmaf(fmaf(p.cap_c[2], u, p.cap_c[1]), u, p.cap_c[0])
+                                                            : fmaf(-2.f * p.cap_log2, rcp_approx(1.f + w), p.cap_log2)) + (e & 1 ? b1 : b0);
+                            } else {
+                                sc[j][e] = fmaf(sc[j][e], e & 1 ? f1 : f0, e & 1 ? b1 : b0);
                             }
-                            sc[j][e] = y + ev;
                         }
                         if (edge) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const int key = key0 + r8 + (e >> 1) * 8, me = self[j][e & 1];
+                                const int key = key0 + r8 + (e >> 1) * 8;
+                                const int me = s.P + i0 + min((8 * j + 2 * q4 + (e & 1)) / p.G, ntok - 1);
                                 bool seen = key <= me && (p.window <= 0 || key > me - p.window || key < p.sinks);
                                 if (p.mask && key >= s.P && seen)
                                     seen = (p.mask[row + me - s.P] >> (key - s.P)) & 1ull;
@@ -385,22 +400,26 @@ rows_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                             }
                         }
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float mx = fmaxf(sc[j][e], sc[j][e + 2]);
-                            need = need || (m[j][e] == -INFINITY ? mx > -INFINITY : mx > m[j][e] + RQ_SLACK);
-                        }
+                        for (int e = 0; e < 2; ++e)
+                            need = need || fmaxf(sc[j][e], sc[j][e + 2]) > lim[j][e];
                     }
                     if (__any_sync(0xffffffffu, need)) {
+                        // the maxima, over the warp's eight lanes with the same rows
 #pragma unroll
                         for (int j = 0; j < NT; ++j)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                float mx = fmaxf(m[j][e], fmaxf(sc[j][e], sc[j][e + 2]));
+                                float mx = fmaxf(sc[j][e], sc[j][e + 2]);
                                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                                const float f = m[j][e] == -INFINITY ? 0.f : exp2f(m[j][e] - mx);
-                                m[j][e] = mx;
+                                const bool none = lim[j][e] == -INFINITY;      // no maximum yet, and l and O zero
+                                const float by = none ? (mx == -INFINITY ? 0.f : mx - RQ_BIAS) : fmaxf(mx - RQ_BIAS, 0.f);
+                                const float f = none ? 0.f : exp2f(-by);
+                                if (mx != -INFINITY) lim[j][e] = RQ_BIAS + RQ_SLACK;
+                                nb[j][e] -= by;
+                                sc[j][e] -= by;
+                                sc[j][e + 2] -= by;
                                 l[j][e] *= f;
 #pragma unroll
                                 for (int t = 0; t < KS; ++t) {
@@ -415,10 +434,7 @@ rows_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float bz = m[j][e & 1] == -INFINITY ? 0.f : m[j][e & 1] - RQ_BIAS;
-                            pw[j][e] = ex2_approx(sc[j][e] - bz);
-                        }
+                        for (int e = 0; e < 4; ++e) pw[j][e] = ex2_approx(sc[j][e]);
                         l[j][0] = fmaf(pw[j][0] + pw[j][2], lsc, l[j][0]);
                         l[j][1] = fmaf(pw[j][1] + pw[j][3], lsc, l[j][1]);
                         pb[j][0] = transposed(half2_of(pw[j][0], pw[j][1]));
@@ -513,7 +529,7 @@ rows_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                         if (r8 == 0) {
-                            sm_m[warp][8 * j + 2 * q4 + e] = m[j][e];
+                            sm_m[warp][8 * j + 2 * q4 + e] = lim[j][e] == -INFINITY ? -INFINITY : RQ_BIAS - nb[j][e];
                             sm_l[warp][8 * j + 2 * q4 + e] = sum;
                         }
                     }
