@@ -78,6 +78,7 @@ template <bool E8>
 constexpr int NTHREADS = E8 ? 512 : 384;
 constexpr int MMA_WARP = 8, LOAD_WARP = 9, FIX_WARP = 10, SCHED_WARP = 11, CONV_WARP = 12;
 constexpr int CONV_WARPS = 4;
+constexpr int WIDEN_UNROLL = 2;
 constexpr int GQ = 4;              // items published ahead
 constexpr int FIX_TILES = 6;       // key tiles of an item that only some of its rows see
 constexpr int FIX_BUFS = 4;        // items whose V notes may be live (see warp 10)
@@ -713,69 +714,86 @@ __device__ __forceinline__ void widen_codes(const Params& p, uint8_t* smem, uint
             const int t = it.t_lo + j;
             alive = wait_all<64>(&rfull[rs], rph);
             if (!alive) break;
-            uint4 c[NCH];
             const uint8_t* src = smem + L::OFF_RAW + rs * L::RAW_BYTES + r * D;
-#pragma unroll
-            for (int u = 0; u < NCH; ++u) c[u] = *reinterpret_cast<const uint4*>(src + piece(u) * 16);
             const uint32_t e = smem[L::OFF_EXP + rs * 8 + (r >> 4)];
-            uint32_t acc = 0;
-#pragma unroll
-            for (int u = 0; u < NCH; ++u) acc |= nan_bytes(c[u].x) | nan_bytes(c[u].y) | nan_bytes(c[u].z) | nan_bytes(c[u].w);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&rempty[rs]);
-            if (++rs == L::RAWS) {
-                rs = 0;
-                rph ^= 1u;
-            }
-            bool nan = (acc & 0x80808080u) != 0;
+            auto codes = [&](int u) -> uint4 { return *reinterpret_cast<const uint4*>(src + piece(u) * 16); };
+            auto odd_bytes = [&](const uint4& c) -> uint32_t {
+                return (nan_bytes(c.x) | nan_bytes(c.y) | nan_bytes(c.z) | nan_bytes(c.w)) & 0x80808080u;
+            };
+            bool clear = false;
             if (is_v && (t < it.fa || t >= it.fb)) {
+                uint32_t acc = 0;
+#pragma unroll 1
+                for (int u = 0; u < NCH; ++u) acc |= odd_bytes(codes(u));
                 const int v = t * KT + r, key = item_key(it, v);
-                bool clear = v >= vend || (key < first && key >= p.sinks);
-                const bool odd = !clear && nan && some;
+                clear = v >= vend || (key < first && key >= p.sinks);
+                const bool odd = !clear && acc != 0u && some;
                 const uint32_t m = __ballot_sync(0xffffffffu, odd);
                 if (lane == 0) notes[fix_index(it, t) * 4 + q] = m;
                 clear = clear || odd;
-                if (clear) {
-                    nan = false;
-#pragma unroll
-                    for (int u = 0; u < NCH; ++u) c[u] = make_uint4(0u, 0u, 0u, 0u);
-                }
             }
-            const bool any_nan = __any_sync(0xffffffffu, nan);
-            // 2^120 times the scale, in two factors where it is no bfloat16
-            const uint32_t f = e == 0u ? 0u : min(e + 120u, 254u) << 7, m2 = f | f << 16;
-            const uint32_t f1 = (max(e + 120u, 254u) - 127u) << 7, m3 = f1 | f1 << 16;
-            const bool far = e > 134u;
+            // 2^120 times the scale (zero clears a row: every code is finite then); above 2^127 in two
+            // factors
+            const uint32_t f = e == 0u || clear ? 0u : min(e + 120u, 254u) << 7, m2 = f | f << 16;
             alive = wait_all<64>(&empty[slot], ph ^ 1u);
             if (!alive) break;
             uint8_t* dst = smem + L::OFF_RING + slot * L::SLOT_BYTES + (r >> 4) * L::PAGE_BYTES;
             if constexpr (D == 128) dst += is_v ? r16 * 128 : (r16 >> 3) * 2048 + r8 * 128;
             else dst += r16 * 128;
             const int half = is_v ? 2048 : 1024;
-#pragma unroll
-            for (int u = 0; u < NCH; ++u) {
-                const uint32_t w[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
-                uint32_t o[8];
+            auto widen = [&](const uint4& c, uint32_t (&o)[8]) {
+                const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                     const uint32_t lo = __byte_perm(w[y], 0u, 0x1404), hi = __byte_perm(w[y], 0u, 0x3424);
                     o[2 * y] = mul_bf16x2((lo & 0x80008000u) | ((lo >> 4) & 0x07f007f0u), m2);
                     o[2 * y + 1] = mul_bf16x2((hi & 0x80008000u) | ((hi >> 4) & 0x07f007f0u), m2);
                 }
-                if (far)
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) o[y] = mul_bf16x2(o[y], m3);
-                if (any_nan)
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const uint32_t nb = nan_bytes(w[y]);
-                        o[2 * y] |= ((nb & 0x80u) ? 0x7fc0u : 0u) | ((nb & 0x8000u) ? 0x7fc00000u : 0u);
-                        o[2 * y + 1] |= ((nb & 0x800000u) ? 0x7fc0u : 0u) | ((nb & 0x80000000u) ? 0x7fc00000u : 0u);
-                    }
+            };
+            auto put = [&](int u, const uint32_t (&o)[8]) {
                 const int pc = piece(u), ch = D == 128 ? 2 * (pc & 3) : 2 * pc;
                 uint8_t* to = dst + (D == 128 ? (pc >> 2) * half : 0);
                 *reinterpret_cast<uint4*>(to + ((ch ^ r8) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 *reinterpret_cast<uint4*>(to + (((ch + 1) ^ r8) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            };
+            // (few instructions: the warps' roles share the instruction cache)
+            uint32_t acc = 0;
+#pragma unroll WIDEN_UNROLL
+            for (int u = 0; u < NCH; ++u) {
+                const uint4 c = codes(u);
+                uint32_t o[8];
+                widen(c, o);
+                put(u, o);
+                acc |= nan_bytes(c.x) | nan_bytes(c.y) | nan_bytes(c.z) | nan_bytes(c.w);
+            }
+            const bool nan = !clear && (acc & 0x80808080u) != 0u;
+            if (__any_sync(0xffffffffu, nan || e > 134u)) {
+                // NaN codes, and scales that need two factors: once more
+                const uint32_t f1 = (max(e + 120u, 254u) - 127u) << 7, m3 = f1 | f1 << 16;
+#pragma unroll 1
+                for (int u = 0; u < NCH; ++u) {
+                    const uint4 c = codes(u);
+                    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+                    uint32_t o[8];
+                    widen(c, o);
+#pragma unroll
+                    for (int y = 0; y < 8; ++y)
+                        if (e > 134u) o[y] = mul_bf16x2(o[y], m3);
+                    if (nan)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const uint32_t nb = nan_bytes(w[y]);
+                            o[2 * y] |= ((nb & 0x80u) ? 0x7fc0u : 0u) | ((nb & 0x8000u) ? 0x7fc00000u : 0u);
+                            o[2 * y + 1] |= ((nb & 0x800000u) ? 0x7fc0u : 0u) | ((nb & 0x80000000u) ? 0x7fc00000u : 0u);
+                        }
+                    put(u, o);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&rempty[rs]);
+            if (++rs == L::RAWS) {
+                rs = 0;
+                rph ^= 1u;
             }
             fence_proxy_async_smem();                      // the tensor core reads through the async proxy
             __syncwarp();
@@ -1484,7 +1502,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                                 (CAP ? 1.f : p.scale_log2);
                 }
                 auto key_scale = [&](int c) -> float {         // of column c of the tile
-                    return fmaxf(scale_of((kx[c >> 6] >> (((c >> 4) & 3) * 8)) & 0xffu) * row_scale, 1.2e-38f);
+                    return fmaxf(scale_of(((c < 64 ? kx[0] : kx[1]) >> (((c >> 4) & 3) * 8)) & 0xffu) * row_scale, 1.2e-38f);
                 };
                 float sv[PART];
                 auto load_s = [&](int h0) {
@@ -1587,19 +1605,20 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                         for (int u = 0; u < 4; ++u) mx[u] = fmax3(mx[u], sv[c + u], sv[c + 4 + u]);
                     return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
                 };
-                float tmax = part_max(KT - PART);
-                if constexpr (PART < KT) {
-                    if (CAP || edge) {
+                float tmax = -INFINITY;
+#pragma unroll 1
+                for (int h0 = KT - PART; h0 >= 0; h0 -= PART) {
+                    tmax = fmaxf(tmax, part_max(h0));
+                    if (PART < KT && h0 > 0 && (CAP || edge)) {
 #pragma unroll
                         for (int c = 0; c < PART; c += 32) {
                             uint32_t r[32];
 #pragma unroll
                             for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(sv[c + e]);
-                            tmem_st32(tS + KT - PART + c, r);
+                            tmem_st32(tS + h0 + c, r);
                         }
                         tmem_wait_st();
                     }
-                    tmax = fmaxf(tmax, part_max(0));
                 }
                 tmax *= csc;
                 const bool need = (m_used == -INFINITY) ? (tmax > -INFINITY) : (tmax > m_used + RESCALE_LOG2);
@@ -1624,7 +1643,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 const float nbase = (m_used == -INFINITY) ? 0.f : -m_used;
                 const uint64_t sc2 = f2_pack(csc, csc), nb2 = f2_pack(nbase, nbase);
                 uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
+#pragma unroll 1
                 for (int h0 = 0; h0 < KT; h0 += PART) {
                     if (h0 > 0) load_s(h0);
 #pragma unroll
