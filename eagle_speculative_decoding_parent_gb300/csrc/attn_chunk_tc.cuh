@@ -78,7 +78,8 @@ template <bool E8>
 constexpr int NTHREADS = E8 ? 512 : 384;
 constexpr int MMA_WARP = 8, LOAD_WARP = 9, FIX_WARP = 10, SCHED_WARP = 11, CONV_WARP = 12;
 constexpr int CONV_WARPS = 4;
-constexpr int WIDEN_UNROLL = 2;
+constexpr int WIDEN_UNROLL = 1;
+constexpr int Q8_PART = 64;
 constexpr int GQ = 4;              // items published ahead
 constexpr int FIX_TILES = 6;       // key tiles of an item that only some of its rows see
 constexpr int FIX_BUFS = 4;        // items whose V notes may be live (see warp 10)
@@ -124,8 +125,8 @@ struct Lay {
     static constexpr bool K8 = E8 && D == 128;
     static constexpr int SLOTS = K8 ? 2 : (E8 ? 3 : 5) * (128 / D);
     static constexpr int RAW_BYTES = KT * D;
-    static constexpr int RAWS = K8 ? 3 : E8 ? 4 * (128 / D) : 0;
-    static constexpr int KSLOTS = K8 ? 3 : 0;
+    static constexpr int RAWS = K8 ? 4 : E8 ? 4 * (128 / D) : 0;
+    static constexpr int KSLOTS = K8 ? 2 : 0;
     static constexpr int KEXPS = 8;                        // tiles of K whose scales are kept
     static constexpr int Q_BYTES = MT * D * 2;             // one row tile
     static constexpr int OFF_RING = 0;
@@ -610,6 +611,11 @@ __device__ __forceinline__ void load_codes(const Params& p, const CUtensorMap& k
 // the power of two that brings its largest element to 2^7 .. 2^8, the nearest code and what is
 // left.  Eight significant bits go into two codes of four exactly, down to 2^-18 of the largest
 // element (the codes' smallest step, 2^-9; elements below lose bits).  Its exponent is noted.
+// A row with an infinity or NaN is NaN, as its scores are.
+// Step k takes columns 16 k .. 16 k + 15, the pieces 2 k and 2 k + 1 of the row's sixteen, and writes
+// piece k of the first part, in the first half, and of the second part, in the second.  First the
+// first half upwards, with its four pieces of the second part held; then the second half
+// downwards: what is written has been read.
 template <class L>
 __device__ __forceinline__ void split_queries(const Params& p, uint8_t* smem, const Item& it, int r, uint32_t buf) {
     const int nq = (it.flags & ITEM_TWO) ? 2 : 1;
@@ -618,53 +624,60 @@ __device__ __forceinline__ void split_queries(const Params& p, uint8_t* smem, co
         const int rows = p.G * min(it.ntok - t * p.npt, p.npt);
         if ((r & ~31) >= rows) continue;                   // (nothing in this warp: zeros, or rows that no one reads)
         uint8_t* row = smem + L::OFF_Q + t * L::Q_BYTES + r * 128;
-        auto piece = [&](int c) -> uint4 {                 // columns 8 c .. 8 c + 7
-            return *reinterpret_cast<const uint4*>(row + (c >> 3) * (MT * 128) + (((c & 7) ^ (r & 7)) << 4));
+        auto piece = [&](int c) -> uint4* {
+            return reinterpret_cast<uint4*>(row + (c >> 3) * (MT * 128) + (((c & 7) ^ (r & 7)) << 4));
         };
-        float top = 0.f;
-#pragma unroll
+        uint32_t top = 0u;                                 // the largest absolute value's bits, even and odd columns
+#pragma unroll 2
         for (int c = 0; c < 16; ++c) {
-            const uint4 x = piece(c);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const float a = __uint_as_float(w[y] << 16), b = __uint_as_float(w[y] & 0xffff0000u);
-                top = fmaxf(top, fmaxf(fabsf(fmaf(a, 0.f, a)), fabsf(fmaf(b, 0.f, b))));   // finite ones
-            }
+            const uint4 x = *piece(c);
+            top = max_u16x2(max_u16x2(top, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
+            top = max_u16x2(max_u16x2(top, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
         }
-        const uint32_t ex = min(max(__float_as_uint(top) >> 23, 20u), 253u);
+        const uint32_t e = max(top >> 16, top & 0xffffu) >> 7;
+        const uint32_t ex = min(max(e, 20u), 253u), odd = e == 255u ? 0x7f7f7f7fu : 0u;
         const float up = __uint_as_float(min(261u - ex, 254u) << 23);      // 2^(7 - exponent)
         smem[L::OFF_QX + (buf * 2 + t) * MT + r] = (uint8_t)ex;
-        // sixteen columns at a time; what lies where the second part goes is held
-        uint4 back[8];
+        auto split = [&](int k, uint4& hi, uint4& lo) {
+            uint32_t h[4], l[4];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) back[c] = piece(8 + c);
-#pragma unroll
-        for (int c = 0; c < 16; c += 2) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint4 x = c < 8 ? piece(c + h) : back[(c + h) & 7];
+            for (int v = 0; v < 2; ++v) {
+                const uint4 x = *piece(2 * k + v);
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int y = 0; y < 4; y += 2) {
-                    float f[4];
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        f[2 * z] = __uint_as_float(w[y + z] << 16) * up;
-                        f[2 * z + 1] = __uint_as_float(w[y + z] & 0xffff0000u) * up;
+                for (int y = 0; y < 4; ++y) {
+                    // exact in float16, as is what is left
+                    const uint32_t q = half2_of(__uint_as_float(w[y] << 16) * up, __uint_as_float(w[y] & 0xffff0000u) * up);
+                    const uint32_t c = e4m3_of_half2(q), left = e4m3_of_half2(half2_sub(q, half2_of_e4m3(c)));
+                    if (y & 1) {
+                        h[2 * v + y / 2] |= c << 16 | odd;
+                        l[2 * v + y / 2] |= left << 16;
+                    } else {
+                        h[2 * v + y / 2] = c;
+                        l[2 * v + y / 2] = left;
                     }
-                    // (an infinite element becomes NaN, as the products with it are)
-                    const uint32_t c0 = e4m3_pair(f[0] + f[0] * 0.f, f[1] + f[1] * 0.f), c1 = e4m3_pair(f[2] + f[2] * 0.f, f[3] + f[3] * 0.f);
-                    hi[2 * h + y / 2] = c0 | c1 << 16;
-                    lo[2 * h + y / 2] = e4m3_pair(f[0] - e4m3_float(c0 & 0xffu), f[1] - e4m3_float(c0 >> 8)) |
-                                        e4m3_pair(f[2] - e4m3_float(c1 & 0xffu), f[3] - e4m3_float(c1 >> 8)) << 16;
                 }
             }
-            const int at = ((c >> 1) ^ (r & 7)) << 4;
-            *reinterpret_cast<uint4*>(row + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(row + MT * 128 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            hi = make_uint4(h[0], h[1], h[2], h[3]);
+            lo = make_uint4(l[0], l[1], l[2], l[3]);
+        };
+        uint4 held[4], hi, lo;
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+            split(k, hi, lo);
+            *piece(k) = hi;
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if (k == y) held[y] = lo;
         }
+#pragma unroll 1
+        for (int k = 7; k >= 4; --k) {
+            split(k, hi, lo);
+            *piece(k) = hi;
+            *piece(8 + k) = lo;
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) *piece(8 + y) = held[y];
     }
 }
 
@@ -1487,8 +1500,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     continue;
                 }
                 // The scores in parts of PART columns: all of them at once, or (512 threads have 128
-                // registers each) half by half, the second half's maximum first; it is then read again.
-                constexpr int PART = E8 ? KT / 2 : KT;
+                // registers each) half by half.
+                constexpr int PART = E8 ? Q8_PART : KT;
                 const bool edge = j < ja || j >= jb;
                 // K8: what the columns of 16 keys are multiplied by (the scale of the keys' block, of the
                 // row, and into units of log 2).  Never zero: times -infinity it has to stay that.
@@ -1605,52 +1618,54 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                         for (int u = 0; u < 4; ++u) mx[u] = fmax3(mx[u], sv[c + u], sv[c + 4 + u]);
                     return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
                 };
-                float tmax = -INFINITY;
-#pragma unroll 1
-                for (int h0 = KT - PART; h0 >= 0; h0 -= PART) {
-                    tmax = fmaxf(tmax, part_max(h0));
-                    if (PART < KT && h0 > 0 && (CAP || edge)) {
-#pragma unroll
-                        for (int c = 0; c < PART; c += 32) {
-                            uint32_t r[32];
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(sv[c + e]);
-                            tmem_st32(tS + h0 + c, r);
-                        }
-                        tmem_wait_st();
-                    }
-                }
-                tmax *= csc;
-                const bool need = (m_used == -INFINITY) ? (tmax > -INFINITY) : (tmax > m_used + RESCALE_LOG2);
-                if (__any_sync(0xffffffffu, need)) {
-                    const float f = (need && m_used > -INFINITY) ? exp2f(m_used - tmax) : 1.f;
-                    if (j > j0) {
-                        // O holds every product before this S: rescale it
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
-                            uint32_t r[16];
-                            tmem_ld16(tO + c, r);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-                            tmem_st16(tO + c, r);
-                        }
-                        // (the wait below covers these stores too)
-                    }
-                    l *= f;
-                    if (need) m_used = tmax;
-                }
-                const float nbase = (m_used == -INFINITY) ? 0.f : -m_used;
-                const uint64_t sc2 = f2_pack(csc, csc), nb2 = f2_pack(nbase, nbase);
                 uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll 1
                 for (int h0 = 0; h0 < KT; h0 += PART) {
-                    if (h0 > 0) load_s(h0);
+                    const float tmax = part_max(h0) * csc;
+                    const bool need = (m_used == -INFINITY) ? (tmax > -INFINITY) : (tmax > m_used + RESCALE_LOG2);
+                    if (__any_sync(0xffffffffu, need)) {
+                        // (in parts: a whole number, so that the part before is rescaled exactly)
+                        const float tnew = E8 ? ceilf(tmax) : tmax;
+                        const float f = (need && m_used > -INFINITY) ? exp2f(m_used - tnew) : 1.f;
+                        if (j > j0) {
+                            // O holds every product before this S: rescale it
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t r[16];
+                                tmem_ld16(tO + c, r);
+                                tmem_wait_ld();
 #pragma unroll
-                    for (int h = 0; h < PART; h += 64) {
-                        uint32_t pk[32];
+                                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+                                tmem_st16(tO + c, r);
+                            }
+                            // (the wait below covers these stores too)
+                        }
+                        if constexpr (E8) {
+                            const uint32_t fb = pack_bf16x2(f, f);
+#pragma unroll 1
+                            for (int c = 0; c < h0 / 2; c += 16) {
+                                uint32_t r[16];
+                                tmem_wait_st();
+                                tmem_ld16(tS + c, r);
+                                tmem_wait_ld();
 #pragma unroll
-                        for (int c = 0; c < 64; c += 2) {
+                                for (int e = 0; e < 16; ++e) r[e] = mul_bf16x2(r[e], fb);
+                                tmem_st16(tS + c, r);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[e] = f2_mul(acc[e], f2_pack(f, f));
+                        }
+                        l *= f;
+                        if (need) m_used = tnew;
+                    }
+                    const float nbase = (m_used == -INFINITY) ? 0.f : -m_used;
+                    const uint64_t sc2 = f2_pack(csc, csc), nb2 = f2_pack(nbase, nbase);
+                    constexpr int CH = PART < 64 ? PART : 64;
+#pragma unroll
+                    for (int h = 0; h < PART; h += CH) {
+                        uint32_t pk[CH / 2];
+#pragma unroll
+                        for (int c = 0; c < CH; c += 2) {
                             float xa, xb;
                             uint64_t by = sc2;
                             if constexpr (L::K8 && !CAP) {
@@ -1663,7 +1678,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                             // weights to bfloat16, the products' input type: at most 2^-8 of each
                             pk[c / 2] = pack_bf16x2(a, b2);
                         }
-                        tmem_st32(tS + (h0 + h) / 2, pk);
+                        if constexpr (CH == 64) tmem_st32(tS + (h0 + h) / 2, pk);
+                        else tmem_st16(tS + (h0 + h) / 2, pk);
                     }
                 }
                 tmem_wait_st();

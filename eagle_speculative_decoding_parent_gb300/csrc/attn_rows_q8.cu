@@ -18,8 +18,6 @@
 // joined in shared memory at the item's end.  An item is (sequence, kv head, up to 8 NT / G
 // tokens); the items of all sequences, laid end to end, are cut into equal runs, one per CTA, as in
 // attn_chunk_tc.cuh, and pieces of items that a border cuts are joined by a second kernel.
-#include <cuda_fp16.h>
-
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -121,11 +119,6 @@ __device__ __forceinline__ void rq_runs(const RqParams& p, int64_t total, int ct
 __device__ __forceinline__ void e4m3_halves(uint32_t w, uint32_t& lo, uint32_t& hi) {   // four codes
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
         "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w));
-}
-__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
 }
 __device__ __forceinline__ uint32_t transposed(uint32_t a) {   // an 8 x 8 tile of 16-bit elements
     uint32_t d;

@@ -32,6 +32,32 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
     return d;
 }
+// The same of and to pairs of float16.
+__device__ __forceinline__ uint32_t e4m3_of_half2(uint32_t h) {
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(h));
+    return d;
+}
+__device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t c) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)c));
+    return d;
+}
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ uint32_t half2_sub(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
 // Four codes times a power of two, rounded again.
 __device__ __forceinline__ uint32_t e4m3_scaled(uint32_t w, float by) {
     const uint32_t lo = e4m3_pair(e4m3_float(w & 0xffu) * by, e4m3_float((w >> 8) & 0xffu) * by);
