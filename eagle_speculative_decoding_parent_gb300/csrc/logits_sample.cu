@@ -9,7 +9,9 @@
 //
 // A cluster of CTAs holds a row in shared memory, a slice each:
 //   1  the maximum;
-//   2  entries counted by (max - x) / T in 2,048 bins of 1/64, over the cluster;
+//   2  entries counted by (max - x) / T in bins of 1/64, over the cluster, those within 11 of the
+//      maximum first (weights from 2^-16 on), the others where that is not enough; without
+//      top-k the sum of all weights in the same pass;
 //   3  top-k: the bin that holds the k-th entry, its entries in a list, ranked;
 //   4  top-p: the bin where the mass reaches top_p of what top-k left (estimated from the counts,
 //      then proved by the exact sums on both sides, or corrected), its entries ranked;
@@ -17,6 +19,8 @@
 //   6  the distribution.
 // Bins with more entries than the list holds (long runs of equal logits) are cut by bisection
 // over the logits' bits and a count of equal ones by index.
+// A weight takes some forty instructions and few entries need theirs, scattered over the row: a
+// thread marks them among 32 of its entries, and goes through the marks.
 #include <cuda_bf16.h>
 #include <float.h>
 #include <math.h>
@@ -39,11 +43,15 @@ constexpr int LS_SLICE = 16384;              // entries per CTA, two CTAs per SM
 constexpr int LS_SLICE_MAX = 49152;          // longer rows: one CTA per SM
 constexpr int LS_BINS = 2048;
 constexpr float LS_BIN = 64.f;               // bins per unit of (max - x) / T
+constexpr int LS_NEAR = 704;                 // bins of the first count
+constexpr float LS_SMALL = 19.f;             // weights below 2^-19 enter the sum of all in float32
 constexpr int LS_LIST = 1024;
+constexpr int LS_HEAVY = 4 * LS_THREADS;     // near entries that a CTA's threads hold
+constexpr int LS_TRIES = 4;
 constexpr int LS_FRAC = 42;                  // a weight of 1 is 2^42
 
 // 2^(62 - j / 64)
-__constant__ uint64_t LS_TABLE[64] = {
+__device__ const uint64_t LS_TABLE[64] = {
     0x4000000000000000ull, 0x3f4f83033d21b05dull, 0x3ea0ecb6dc8a80cfull, 0x3df437dcc2b44eeeull,
     0x3d495f454921b30bull, 0x3ca05dcf167fec4eull, 0x3bf92e66f736bd73ull, 0x3b53cc07b6650ae1ull,
     0x3ab031b9f7490e4cull, 0x3a0e5a940f12f71aull, 0x396e41b9df20d22aull, 0x38cfe25cafa29694ull,
@@ -84,6 +92,20 @@ __device__ __forceinline__ uint64_t ls_key(float x, int idx) {
     return (uint64_t)(~ls_bits(x)) << 32 | (uint32_t)idx;
 }
 
+// f times z, f in [0, 1], exactly, rounded down, or (UP) up.
+template <bool UP>
+__device__ __forceinline__ uint64_t ls_part(float f, uint64_t z) {
+    const uint32_t b = __float_as_uint(f), ex = max(b >> 23, 1u);
+    const uint64_t mant = (b & 0x7fffffu) | (b >> 23 ? 0x800000u : 0u);
+    const int shift = 150 - (int)ex;                           // f = mant 2^-shift, 23 <= shift <= 149
+    const uint64_t hi = __umul64hi(z, mant), lo = z * mant;
+    const bool far = shift >= 64;
+    const uint64_t whole = far ? (shift - 64 < 64 ? hi >> (shift - 64) : 0ull) : (hi << (64 - shift) | lo >> shift);
+    const bool rest = far ? (lo != 0ull || (shift - 64 < 64 ? (hi & ((1ull << (shift - 64)) - 1ull)) != 0ull : hi != 0ull))
+                          : (lo & ((1ull << shift) - 1ull)) != 0ull;
+    return UP && rest ? whole + 1ull : whole;
+}
+
 // exp((x - top) / T) in 2^-42, rounded; (ch, cl): log2(e) / T.  The exponent t = n / 64 + r in two
 // floats; 2^-r = 1 - p + p^2 / 2 - p^3 / 6 + p^4 / 24 with p = r ln 2 <= 0.0055 (the next term is
 // 2^-44), p in two floats too, and 2^(-n / 64) from a table and a shift.
@@ -109,6 +131,8 @@ __device__ __forceinline__ uint64_t ls_weight(float x, float top, float ch, floa
     return (v + (1ull << (61 - LS_FRAC + q))) >> (62 - LS_FRAC + q);
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void remote_st_u64(uint64_t* p, uint32_t rank, uint64_t v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(map_rank(p, rank)), "l"(v) : "memory");
 }
@@ -131,10 +155,14 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     __shared__ uint64_t table[64];
     __shared__ uint64_t part[3][LS_WARPS];                 // per warp
     __shared__ uint64_t peer[2][3][LS_CLUSTER_MAX];        // per CTA, two exchanges in turn
-    __shared__ uint64_t result;                            // of the first CTA
-    __shared__ uint32_t list_n[2];
+    __shared__ uint64_t result[3];                         // of the first CTA, of a bisection
+    // the near entries, in index order, where the list comes later (two barriers of the cluster on)
+    float* near_x = reinterpret_cast<float*>(weight);
+    uint16_t* near_i = reinterpret_cast<uint16_t*>(list);
+    static_assert(LS_HEAVY * sizeof(float) <= sizeof(weight) && LS_HEAVY * sizeof(uint16_t) <= sizeof(list), "near entries");
+    __shared__ uint32_t list_n[3 + LS_TRIES];
     __shared__ uint32_t pick[2];                           // a bin, entries before it
-    __shared__ float fpart[LS_WARPS];
+    __shared__ float fpart[LS_WARPS], est;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = p.ctas, me = (int)(blockIdx.x % C);
     const int64_t row = blockIdx.x / C;
@@ -142,8 +170,8 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     const int x0 = me * p.slice, n = max(0, min(p.slice, p.V - x0));
     const int chunk = p.slice / LS_WARPS, w0 = warp * chunk;   // a warp's entries
     if (tid < 64) table[tid] = LS_TABLE[tid];
-    if (tid < 2) list_n[tid] = 0u;
-    if (tid == 0) result = ~0ull;
+    if (tid < 3 + LS_TRIES) list_n[tid] = 0u;
+    if (tid < 3) result[tid] = ~0ull;
     for (int i = tid; i < LS_BINS; i += LS_THREADS) hist[i] = 0u;
     pdl_launch_dependents();
     pdl_wait();
@@ -166,6 +194,8 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         }
     };
     if (err != TV_OK) return refuse();
+    __syncthreads();
+    cluster_arrive();                                          // this CTA has started, its counters are zero
 
     // ---- the slice, and its maximum (a NaN wins)
     float mx = -INFINITY;
@@ -259,6 +289,29 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             f(v.w, w0 + i + 3);
         }
     };
+    // f(entry, its place) where mark(entry) holds: marks of 32 entries of a thread at a time
+    auto marked = [&](auto mark, auto f) {
+#pragma unroll 1
+        for (int g = 0; g < chunk; g += 1024) {
+            uint32_t m = 0u;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (g + e * 128 < chunk) {
+                    const float4 v = *reinterpret_cast<const float4*>(xs + w0 + g + e * 128 + lane * 4);
+                    m |= (mark(v.x) ? 1u : 0u) << (4 * e) | (mark(v.y) ? 2u : 0u) << (4 * e) | (mark(v.z) ? 4u : 0u) << (4 * e) |
+                         (mark(v.w) ? 8u : 0u) << (4 * e);
+                }
+#pragma unroll 1
+            while (__any_sync(0xffffffffu, m != 0u)) {
+                if (m != 0u) {
+                    const int e = __ffs(m) - 1, i = w0 + g + (e >> 2) * 128 + lane * 4 + (e & 3);
+                    m &= m - 1u;
+                    f(xs[i], i);
+                }
+                __syncwarp();
+            }
+        }
+    };
     float top;
     {
 #pragma unroll
@@ -270,7 +323,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         __syncthreads();
         mx = fpart[0];
         for (int w = 1; w < LS_WARPS; ++w) asm("max.NaN.f32 %0, %1, %2;" : "=f"(mx) : "f"(mx), "f"(fpart[w]));
-        cluster_barrier_all();                                 // every CTA has started
+        cluster_wait();
         exchange(__float_as_uint(mx), 0ull, 0ull);
         top = __uint_as_float((uint32_t)peer[turn ^ 1][0][0]);
         for (int r = 1; r < C; ++r) {
@@ -307,13 +360,314 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             for (int i = tid; i < n; i += LS_THREADS) out[i] = place(i) == token ? 1.f : 0.f;
         return;
     }
-    const double c64 = 1.4426950408889634 / (double)T;
-    const float ch = (float)c64, cl = (float)(c64 - (double)ch);
+    // log2(e) / T in two floats (64-bit arithmetic is slow here)
+    constexpr float L2EH = 1.44269502162933349609f, L2EL = 1.92596299112661746887e-8f;
+    const float ch = L2EH / T, cl = (fmaf(-ch, T, L2EH) + L2EL) / T;
     const float bin_scale = fminf(LS_BIN / T, 1e38f);
-    auto bin_of = [&](float x) -> int { return (int)fminf((top - x) * bin_scale, (float)(LS_BINS - 1)); };
+    auto depth = [&](float x) -> float { return fminf((top - x) * bin_scale, (float)(LS_BINS - 1)); };
+    auto bin_of = [&](float x) -> int { return (int)depth(x); };
     auto weigh = [&](float x) -> uint64_t { return ls_weight(x, top, ch, cl, table); };
     const bool use_k = k > 0 && k < p.V, use_p = top_p < 1.f;
     uint64_t cut = ~0ull;                                      // entries up to this key are kept
+    const uint64_t least = (uint64_t)ceilf(min_p * (float)(1ull << LS_FRAC));
+    uint64_t all = 0ull;                                       // the sum of what is kept
+    constexpr int PER = LS_BINS / LS_THREADS;                  // bins per thread
+    uint32_t c[PER], counted_before = 0u;
+    // The row's counts of the bins from .. to - 1 into tot, those below `to` into c; returns their sum.
+    // (Between two barriers: the first after every CTA's hist is complete.)
+    auto sum_bins = [&](int from, int to) {
+        for (int i = me * LS_THREADS + tid; i < LS_BINS; i += C * LS_THREADS)
+            if (i >= from && i < to) {
+                uint32_t sum = 0u;
+                for (int r = 0; r < C; ++r) sum += remote_ld_u32(&hist[i], r);
+                for (int r = 0; r < C; ++r) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(&tot[i], r)), "r"(sum) : "memory");
+            }
+        cluster_barrier_all();
+        uint32_t sum = 0u;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) sum += c[e] = tid * PER + e < to ? tot[tid * PER + e] : 0u;
+        uint32_t incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) part[0][warp] = incl;
+        __syncthreads();
+        counted_before = incl - sum;
+        uint32_t in_all = 0u;
+        for (int w = 0; w < LS_WARPS; ++w) {
+            if (w < warp) counted_before += (uint32_t)part[0][w];
+            in_all += (uint32_t)part[0][w];
+        }
+        if (to == LS_BINS - 1 && tid == LS_THREADS - 1) c[PER - 1] = tot[LS_BINS - 1] = (uint32_t)p.V - in_all;
+        __syncthreads();
+        return in_all;
+    };
+    // The bin that holds the k-th entry, and the entries before it.
+    auto bin_of_rank = [&](uint32_t rank) {
+        uint32_t at = counted_before;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            if (at < rank && rank <= at + c[e]) {
+                pick[0] = tid * PER + e;
+                pick[1] = at;
+            }
+            at += c[e];
+        }
+        __syncthreads();
+    };
+    // The bin in which the mass reaches goal by the counts (up to k_bin, of which k_rank entries count), or
+    // LS_BINS; est: the mass before it, by the counts.  (The best entry weighs 1, not what its bin's
+    // middle does.)
+    auto bin_of_mass = [&](float goal, int k_bin, uint32_t k_rank) -> int {
+        float m[PER], ms = 0.f;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            const int bin = tid * PER + e;
+            const uint32_t in = use_k && bin >= k_bin ? (bin == k_bin ? k_rank : 0u) : c[e];
+            m[e] = (float)in * ex2_approx(-1.44269504f * ((float)bin + 0.5f) / LS_BIN);
+            if (bin == 0) m[e] += 0.5f / LS_BIN;
+            ms += m[e];
+        }
+        float mi = ms;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, mi, o);
+            if (lane >= o) mi += y;
+        }
+        if (lane == 31) fpart[warp] = mi;
+        if (tid == 0) pick[0] = (uint32_t)LS_BINS;
+        __syncthreads();
+        float at = mi - ms;
+        for (int w = 0; w < warp; ++w) at += fpart[w];
+        const float begin = at;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            if (at < goal && goal <= at + m[e]) atomicMin(&pick[0], (uint32_t)(tid * PER + e));
+            at += m[e];
+        }
+        __syncthreads();
+        const int found = (int)pick[0];
+        at = begin;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            if (tid * PER + e == found) est = at;
+            at += m[e];
+        }
+        __syncthreads();
+        return found;
+    };
+    // The next bin to try when the exact mass before this one is not what the counts say.
+    auto next_bin = [&](int bin, float need, float exact_before, bool below, int k_bin, uint32_t k_rank) -> int {
+        const int next = bin_of_mass(need + (est - exact_before), k_bin, k_rank);
+        return below ? min(next, bin - 1) : (next >= LS_BINS ? bin + 1 : max(next, bin + 1));
+    };
+    auto value_of = [](uint64_t key) -> float {
+        const uint32_t bits = ~(uint32_t)(key >> 32);
+        return __uint_as_float((bits & 0x80000000u) ? bits & 0x7fffffffu : ~bits);
+    };
+    auto to_list = [&](int which, uint64_t key) {              // of the first CTA
+        const uint32_t at = remote_add_u32(&list_n[which], 0, 1u);
+        if (at < LS_LIST) remote_st_u64(&list[at], 0, key);
+    };
+    // By the first CTA, for all: the key with rank `rank` in the list, or (mass) of the last one that
+    // begins below need, `base` being what comes before the list.
+    auto rank_list = [&](int which, int into, bool mass, uint64_t rank, uint64_t base, uint64_t need) {
+        const int m = min((int)list_n[which], LS_LIST);
+        if (mass)
+            for (int e = tid; e < m; e += LS_THREADS) weight[e] = weigh(value_of(list[e]));
+        __syncthreads();
+        for (int e = tid; e < m; e += LS_THREADS) {
+            const uint64_t key = list[e];
+            uint64_t before = mass ? base : 0ull;
+#pragma unroll 4
+            for (int f = 0; f < m; ++f) before += list[f] < key ? (mass ? weight[f] : 1ull) : 0ull;
+            // (mass: the last one that begins below; the next one does not, or there is none)
+            if (mass ? before < need && before + weight[e] >= need : before == rank)
+                for (int r = 0; r < C; ++r) remote_st_u64(&result[into], r, key);
+        }
+    };
+
+    // ---- Where all that may be kept weighs 2^-16 or more, and few entries do: those are compacted, in index
+    // order, and a thread holds up to four with their weights.
+    auto near_path = [&]() -> bool {
+        if (!(use_k || use_p || min_p >= 3.1e-5f) || chunk > 1024) return false;
+        uint32_t marks = 0u, small = 0u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e * 128 < chunk) {
+                const float4 q = *reinterpret_cast<const float4*>(xs + w0 + e * 128 + lane * 4);
+                const float y[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const float d = top - y[z];
+                    const bool is_near = d * bin_scale < (float)LS_NEAR;
+                    marks |= is_near ? 1u << (4 * e + z) : 0u;
+                    if (!use_k && !is_near) {
+                        // in 2^-38 of the largest, below 2^23 of them: rounded by adding 2^23
+                        const float t = fmaf(d, cl, d * ch);
+                        small += __float_as_uint(ex2_approx(fmaxf((float)(LS_FRAC - 4) - t, -126.f)) + 8388608.f) - __float_as_uint(8388608.f);
+                    }
+                }
+            }
+        // places in index order: 128 entries after 128, lane after lane
+        const int own = __popc(marks);
+        const uint32_t warp_all = __reduce_add_sync(0xffffffffu, (uint32_t)own);
+        if (lane == 0) part[0][warp] = warp_all;
+        __syncthreads();
+        uint32_t at = 0u, held = 0u;
+        for (int w = 0; w < LS_WARPS; ++w) {
+            if (w < warp) at += (uint32_t)part[0][w];
+            held += (uint32_t)part[0][w];
+        }
+        if (held <= LS_HEAVY) {
+#pragma unroll 1
+            for (int e = 0; e * 128 < chunk; ++e) {
+                const uint32_t nib = (marks >> (4 * e)) & 15u;
+                const uint32_t mine = (uint32_t)__popc(nib);
+                uint32_t incl = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += y;
+                }
+                uint32_t to = at + incl - mine;
+                for (uint32_t left = nib; left != 0u; left &= left - 1u, ++to) {
+                    const int i = w0 + e * 128 + lane * 4 + __ffs(left) - 1;
+                    near_x[to] = xs[i];
+                    near_i[to] = (uint16_t)i;
+                }
+                at += __shfl_sync(0xffffffffu, incl, 31);
+            }
+        }
+        __syncthreads();
+        // this thread's entries: keys, bins, weights
+        const int each = ((int)min(held, (uint32_t)LS_HEAVY) + LS_THREADS - 1) / LS_THREADS;
+        uint64_t wt[4], key[4];
+        int bin[4];
+        uint64_t v[3] = {0ull, 0ull, 0ull};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const int e = tid * each + y;
+            wt[y] = 0ull;
+            key[y] = ~0ull;
+            bin[y] = LS_BINS;
+            if (y < each && e < (int)held && held <= LS_HEAVY) {
+                const float x = near_x[e];
+                key[y] = ls_key(x, place(near_i[e]));
+                bin[y] = bin_of(x);
+                wt[y] = weigh(x);
+                v[0] += wt[y];
+                atomicAdd(&hist[bin[y]], 1u);
+            }
+        }
+        v[0] += (uint64_t)small << 4;
+        block_sum(v, 1);
+        exchange(v[0], held <= LS_HEAVY ? 0ull : 1ull, 0ull);
+        uint64_t mass_all = 0ull, over = 0ull;
+        for (int r = 0; r < C; ++r) {
+            mass_all += peer[turn ^ 1][0][r];
+            over += peer[turn ^ 1][1][r];
+        }
+        if (over != 0ull) return false;
+        int k_bin = LS_BINS - 1;
+        uint32_t k_rank = (uint32_t)p.V;
+        if (use_k || use_p) {
+            const uint32_t counted = sum_bins(0, LS_NEAR);
+            if (use_k) {
+                if (counted < (uint32_t)k) return false;
+                bin_of_rank((uint32_t)k);
+                k_bin = (int)pick[0];
+                k_rank = (uint32_t)k - pick[1];
+                if (tot[k_bin] > LS_LIST) return false;
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    if (bin[y] == k_bin) to_list(2, key[y]);
+                cluster_barrier_all();
+                if (me == 0) rank_list(2, 0, false, k_rank - 1u, 0ull, 0ull);
+                cluster_barrier_all();
+                cut = result[0];
+            }
+        }
+        if (use_p) {
+            if (use_k) {
+                v[0] = 0ull;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) v[0] += key[y] <= cut ? wt[y] : 0ull;
+                cluster_sum(v, 1);
+                mass_all = v[0];
+            }
+            const uint64_t need = ls_part<true>(top_p, mass_all);
+            int guess = bin_of_mass((float)need * 2.2737368e-13f, k_bin, k_rank);
+            if (guess >= LS_NEAR) {
+                if (!use_k) return false;
+                guess = k_bin;
+            }
+            int tries = 0;
+            for (;; ++tries) {
+                if (tries == LS_TRIES || tot[guess] > LS_LIST) return false;
+                v[0] = v[1] = 0ull;
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    if (key[y] <= cut && bin[y] <= guess) {
+                        if (bin[y] == guess) {
+                            v[1] += wt[y];
+                            to_list(3 + tries, key[y]);
+                        } else {
+                            v[0] += wt[y];
+                        }
+                    }
+                cluster_sum(v, 2);
+                if (v[0] < need && need <= v[0] + v[1]) break;
+                __syncthreads();
+                guess = next_bin(guess, (float)need * 2.2737368e-13f, (float)v[0] * 2.2737368e-13f, need <= v[0], k_bin, k_rank);
+                if (guess < 0 || guess > min(k_bin, LS_NEAR - 1)) return false;
+                cluster_barrier_all();                         // (the next entries go where these are)
+            }
+            if (me == 0) rank_list(3 + tries, 1, true, 0ull, v[0], need);
+            cluster_barrier_all();
+            cut = min(cut, result[1]);
+        }
+        // ---- the mass that is left, and where the draw falls
+        uint64_t mine = 0ull;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            if (key[y] > cut || wt[y] < least) wt[y] = 0ull;
+            mine += wt[y];
+        }
+        uint64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) part[0][warp] = incl;
+        __syncthreads();
+        uint64_t before = incl - mine, sum = 0ull;
+        for (int w = 0; w < LS_WARPS; ++w) {
+            if (w < warp) before += part[0][w];
+            sum += part[0][w];
+        }
+        exchange(sum, 0ull, 0ull);
+        for (int r = 0; r < C; ++r) {
+            if (r < me) before += peer[turn ^ 1][0][r];
+            all += peer[turn ^ 1][0][r];
+        }
+        const uint64_t goal = ls_part<false>(u, all);
+        if (goal >= before && goal < before + mine) {
+            uint64_t idx = key[0], to = before + wt[0];
+#pragma unroll
+            for (int z = 1; z < 4; ++z)
+                if (to <= goal) {
+                    to += wt[z];
+                    idx = key[z];
+                }
+            p.tokens[row] = (int)(uint32_t)idx;
+            p.status[row] = TV_OK;
+        }
+        return true;
+    };
     // The cut of a run of entries that no list holds, by bisection over the logits' bits: the
     // first key with which count entries, or a mass above before, are kept (`kept` entries count).
     auto bisect = [&](bool mass, uint64_t need, uint64_t limit) -> uint64_t {
@@ -362,219 +716,230 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
                     const int here = __popc(m);
                     if (want <= before + here) {
                         const int at = __fns(m, 0, (int)(want - before));
-                        if (lane < C) remote_st_u64(&result, lane, ls_key(x, place(w0 + i + at)));
+                        if (lane < C) remote_st_u64(&result[2], lane, ls_key(x, place(w0 + i + at)));
                         break;
                     }
                     before += here;
                 }
         }
         cluster_barrier_all();
-        const uint64_t found = result;
+        const uint64_t found = result[2];
         cluster_barrier_all();                                 // (read before it is written again)
         return found;
     };
-    // The entries of a bin (up to `limit`) in the first CTA's list, ranked there; the key of the
-    // one with rank `rank`, or (mass) of the last one that begins below `need`.
+    // The entries of a bin (up to `limit`) in the first CTA's list, ranked there.
     auto cut_in_bin = [&](int which, int bin, bool mass, uint64_t rank, uint64_t base, uint64_t need, uint64_t limit) -> uint64_t {
-        entries([&](float x, int i) {
-            if (bin_of(x) != bin || place(i) >= p.V) return;
+        const float lo_d = (float)bin, up_d = (float)(bin + 1);
+        marked([&](float x) { const float d = depth(x); return d >= lo_d && d < up_d; }, [&](float x, int i) {
+            if (place(i) >= p.V) return;
             const uint64_t key = ls_key(x, place(i));
-            if (key > limit) return;
-            const uint32_t at = remote_add_u32(&list_n[which], 0, 1u);
-            if (at < LS_LIST) remote_st_u64(&list[at], 0, key);
+            if (key <= limit) to_list(which, key);
         });
         cluster_barrier_all();
-        if (me == 0) {
-            const int m = min((int)list_n[which], LS_LIST);
-            if (mass)
-                for (int e = tid; e < m; e += LS_THREADS) {
-                    const uint32_t bits = ~(uint32_t)(list[e] >> 32);
-                    weight[e] = weigh(__uint_as_float((bits & 0x80000000u) ? bits & 0x7fffffffu : ~bits));
-                }
-            __syncthreads();
-            for (int e = tid; e < m; e += LS_THREADS) {
-                const uint64_t key = list[e];
-                if (mass) {
-                    uint64_t before = base;
-                    for (int f = 0; f < m; ++f) before += list[f] < key ? weight[f] : 0ull;
-                    // the last one that begins below: the next one does not, or there is none
-                    if (before < need && before + weight[e] >= need)
-                        for (int r = 0; r < C; ++r) remote_st_u64(&result, r, key);
-                } else {
-                    uint64_t before = 0ull;
-                    for (int f = 0; f < m; ++f) before += list[f] < key ? 1ull : 0ull;
-                    if (before == rank)
-                        for (int r = 0; r < C; ++r) remote_st_u64(&result, r, key);
-                }
-            }
-        }
+        if (me == 0) rank_list(which, which, mass, rank, base, need);
         cluster_barrier_all();
-        const uint64_t found = result;
-        cluster_barrier_all();
-        return found;
+        return result[which];
     };
+    // ---- Otherwise: over the whole row.
+    auto whole_path = [&]() {
+    __syncthreads();
+    for (int i = tid; i < LS_BINS; i += LS_THREADS) hist[i] = 0u;
+    if (tid < 2) result[tid] = ~0ull;
+    __syncthreads();
+    cut = ~0ull;
     if (use_k || use_p) {
-        // ---- counts per bin, over the cluster: a CTA sums a part of the bins for all
-        entries([&](float x, int) {
-            const int bin = bin_of(x);
-            if (bin < LS_BINS - 1) atomicAdd(&hist[bin], 1u);
-        });
-        cluster_barrier_all();
-        for (int i = me * LS_THREADS + tid; i < LS_BINS; i += C * LS_THREADS) {
-            uint32_t s = 0u;
-            for (int r = 0; r < C; ++r) s += remote_ld_u32(&hist[i], r);
-            for (int r = 0; r < C; ++r) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(&tot[i], r)), "r"(s) : "memory");
+        // adds the bins from .. to - 1 of the slice to the row's counts
+        auto count = [&](int from, int to) {
+            cluster_barrier_all();
+            return sum_bins(from, to);
+        };
+        // the entries that weigh 2^-16 or more; in the same pass, without top-k, the sum of all weights
+        uint64_t v[3] = {0ull, 0ull, 0ull};
+        uint32_t small = 0u;                                   // in 2^-42
+        marked(
+            [&](float x) -> bool {
+                const float d = top - x;
+                if (!use_k) {
+                    const float t = fmaf(d, cl, d * ch);
+                    if (t >= LS_SMALL) {
+                        // below 2^23 steps: rounded by adding 2^23
+                        small += __float_as_uint(ex2_approx(fmaxf((float)LS_FRAC - t, -126.f)) + 8388608.f) - __float_as_uint(8388608.f);
+                        return false;
+                    }
+                    return true;
+                }
+                return d * bin_scale < (float)LS_NEAR;
+            },
+            [&](float x, int) {
+                if (!use_k) v[0] += weigh(x);
+                const int bin = bin_of(x);
+                if (bin < LS_NEAR) atomicAdd(&hist[bin], 1u);
+            });
+        uint64_t mass_all = 0ull;
+        if (!use_k) {
+            v[0] += small;
+            cluster_sum(v, 1);
+            mass_all = v[0];
         }
-        cluster_barrier_all();
-        // four bins per thread; the last one holds what is left
-        constexpr int PER = LS_BINS / LS_THREADS;
-        uint32_t c[PER], s = 0u;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) s += c[e] = tot[tid * PER + e];
-        uint32_t incl = s;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-        }
-        if (lane == 31) part[0][warp] = incl;
-        __syncthreads();
-        uint32_t before = incl - s;
-        for (int w = 0; w < warp; ++w) before += (uint32_t)part[0][w];
-        if (tid == LS_THREADS - 1) c[PER - 1] = tot[LS_BINS - 1] = (uint32_t)p.V - (before + s);
-        __syncthreads();
+        uint32_t counted = count(0, LS_NEAR);
+        auto count_all = [&]() {
+            // the others, where those do not reach
+            entries([&](float x, int) {
+                const int bin = bin_of(x);
+                if (bin >= LS_NEAR && bin < LS_BINS - 1) atomicAdd(&hist[bin], 1u);
+            });
+            counted = count(LS_NEAR, LS_BINS - 1);
+            counted = (uint32_t)p.V;
+        };
         int k_bin = LS_BINS - 1;
         uint32_t k_rank = (uint32_t)p.V;
         if (use_k) {
-            uint32_t at = before;
-#pragma unroll
-            for (int e = 0; e < PER; ++e) {
-                if (at < (uint32_t)k && (uint32_t)k <= at + c[e]) {
-                    pick[0] = tid * PER + e;
-                    pick[1] = at;
-                }
-                at += c[e];
-            }
-            __syncthreads();
+            if (counted < (uint32_t)k) count_all();
+            bin_of_rank((uint32_t)k);
             k_bin = (int)pick[0];
             k_rank = (uint32_t)k - pick[1];                     // entries of that bin that are kept
             cut = tot[k_bin] <= LS_LIST ? cut_in_bin(0, k_bin, false, k_rank - 1u, 0ull, 0ull, ~0ull)
                                         : bisect(false, (uint64_t)k, ~0ull);
         }
         if (use_p) {
-            // ---- the bin where the mass reaches top_p, from the counts at first
-            float m[PER], ms = 0.f;
-#pragma unroll
-            for (int e = 0; e < PER; ++e) {
-                const int bin = tid * PER + e;
-                const uint32_t in = use_k && bin >= k_bin ? (bin == k_bin ? k_rank : 0u) : c[e];
-                m[e] = (float)in * exp2f(-1.44269504f * ((float)bin + 0.5f) / LS_BIN);
-                ms += m[e];
-            }
-            float mi = ms;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float y = __shfl_up_sync(0xffffffffu, mi, o);
-                if (lane >= o) mi += y;
-            }
-            if (lane == 31) fpart[warp] = mi;
-            if (tid == 0) pick[0] = (uint32_t)k_bin;
-            __syncthreads();
-            float at = mi - ms, all = 0.f;
-            for (int w = 0; w < LS_WARPS; ++w) {
-                if (w < warp) at += fpart[w];
-                all += fpart[w];
-            }
-            const float goal = top_p * all;
-#pragma unroll
-            for (int e = 0; e < PER; ++e) {
-                if (at < goal && goal <= at + m[e]) atomicMin(&pick[0], (uint32_t)(tid * PER + e));
-                at += m[e];
-            }
-            __syncthreads();
-            int bin = (int)pick[0], lo = 0, hi = k_bin;
-            uint64_t v[3], need = 0ull;
-            for (int tries = 0;; ++tries) {
-                v[0] = v[1] = v[2] = 0ull;
-                entries([&](float x, int i) {
-                    if (cut != ~0ull && ls_key(x, place(i)) > cut) return;
-                    const int y = bin_of(x);
-                    const uint64_t w = weigh(x);
-                    if (y < bin) v[0] += w;
-                    else if (y == bin) v[1] += w;
-                    else v[2] += w;
+            // ---- the mass that top-k left
+            if (use_k) {
+                const float up_d = (float)(k_bin + 1);
+                v[0] = 0ull;
+                marked([&](float x) { return depth(x) < up_d; }, [&](float x, int i) {
+                    if (ls_key(x, place(i)) <= cut) v[0] += weigh(x);
                 });
-                cluster_sum(v, 3);
-                // kept: what begins below top_p of the sum (an integer begins below it when it does below
-                // the next one)
-                need = (uint64_t)ceil((double)top_p * (double)(v[0] + v[1] + v[2]));
+                cluster_sum(v, 1);
+                mass_all = v[0];
+            }
+            // kept: what begins below top_p of the sum (an integer begins below it when it does below
+            // the next one)
+            const uint64_t need = ls_part<true>(top_p, mass_all);
+            // ---- the bin where the mass reaches that, from the counts at first
+            const float goal = (float)need * 2.2737368e-13f;   // 2^-42
+            int guess = bin_of_mass(goal, k_bin, k_rank);
+            if (guess >= LS_BINS && counted < (uint32_t)p.V && k_bin >= LS_NEAR) {
+                // not reached: among the entries not yet counted
+                count_all();
+                guess = bin_of_mass(goal, k_bin, k_rank);
+            }
+            // (or by the estimate's error in the last one)
+            if (guess >= LS_BINS) guess = min(k_bin, counted < (uint32_t)p.V ? LS_NEAR - 1 : LS_BINS - 1);
+            int bin = guess, lo = 0, hi = k_bin;
+            for (int tries = 0;; ++tries) {
+                if (bin >= LS_NEAR && counted < (uint32_t)p.V) count_all();
+                const float at_d = (float)bin, up_d = (float)(bin + 1);
+                v[0] = v[1] = 0ull;
+                marked([&](float x) { return depth(x) < up_d; }, [&](float x, int i) {
+                    if (ls_key(x, place(i)) > cut) return;
+                    const uint64_t w = weigh(x);
+                    if (depth(x) < at_d) v[0] += w;
+                    else v[1] += w;
+                });
+                cluster_sum(v, 2);
                 if (v[0] < need && need <= v[0] + v[1]) break;
                 if (need <= v[0]) hi = bin - 1;
                 else lo = bin + 1;
                 if (lo >= hi) {
                     bin = min(max(lo, 0), LS_BINS - 1);
                     if (tries > 2 * 11) break;
+                } else if (tries < LS_TRIES) {
+                    __syncthreads();
+                    bin = min(max(next_bin(bin, goal, (float)v[0] * 2.2737368e-13f, need <= v[0], k_bin, k_rank), lo), hi);
                 } else {
-                    bin = tries < 2 ? (need <= v[0] ? hi : lo) : (lo + hi) >> 1;
+                    bin = (lo + hi) >> 1;
                 }
             }
             cut = min(cut, tot[bin] <= LS_LIST ? cut_in_bin(1, bin, true, 0ull, v[0], need, cut) : bisect(true, need, cut));
         }
     }
     // ---- the mass that is left, and where the draw falls
-    const uint64_t least = (uint64_t)ceil((double)min_p * (double)(1ull << LS_FRAC));
     auto kept = [&](float x, int i) -> uint64_t {
-        if (cut != ~0ull && ls_key(x, place(i)) > cut) return 0ull;
+        if (ls_key(x, place(i)) > cut) return 0ull;
         const uint64_t w = weigh(x);
         return w >= least ? w : 0ull;
     };
+    // (the logit of the cut, and the exponent of min_p with room for its rounding: what may be kept)
+    const float cut_x = cut == ~0ull ? -INFINITY : value_of(cut);
+    const float most_t = min_p > 0.f ? fminf((float)(LS_FRAC + 1), 0.001f - log2f(min_p)) : (float)(LS_FRAC + 1);
+    auto maybe = [&](float x) -> bool { return x >= cut_x && (top - x) * ch < most_t; };
     uint64_t v[3] = {0ull, 0ull, 0ull};
-    entries([&](float x, int i) { v[0] += kept(x, i); });
+    marked(maybe, [&](float x, int i) { v[0] += kept(x, i); });
     uint64_t mine = v[0];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     block_sum(v, 1);
     exchange(v[0], 0ull, 0ull);
-    uint64_t before = 0ull, all = 0ull;
+    uint64_t before = 0ull;
     for (int r = 0; r < C; ++r) {
         if (r < me) before += peer[turn ^ 1][0][r];
         all += peer[turn ^ 1][0][r];
     }
-    const uint64_t goal = (uint64_t)((double)u * (double)all);  // the first entry whose sum exceeds it
+    const uint64_t goal = ls_part<false>(u, all);              // the first entry whose sum exceeds it
     if (goal >= before && goal < before + v[0]) {
         if (lane == 0) part[0][warp] = mine;
         __syncthreads();
         for (int w = 0; w < warp; ++w) before += part[0][w];
         if (goal >= before && goal < before + mine)
-            for (int i = 0; i < chunk; i += 32) {
-                uint64_t s = kept(xs[w0 + i + lane], w0 + i + lane);
+#pragma unroll 1
+            for (int i = 0; i < chunk; i += 128) {
+                // four entries of a lane, in order
+                const float4 x = *reinterpret_cast<const float4*>(xs + w0 + i + lane * 4);
+                const bool some = maybe(x.x) || maybe(x.y) || maybe(x.z) || maybe(x.w);
+                if (!__any_sync(0xffffffffu, some)) continue;
+                const float y[4] = {x.x, x.y, x.z, x.w};
+                uint64_t w[4], sum = 0ull;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum += w[e] = maybe(y[e]) ? kept(y[e], w0 + i + lane * 4 + e) : 0ull;
+                uint64_t incl = sum;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const uint64_t y = __shfl_up_sync(0xffffffffu, s, o);
-                    if (lane >= o) s += y;
+                    const uint64_t z = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += z;
                 }
-                const uint32_t over = __ballot_sync(0xffffffffu, before + s > goal);
+                const uint32_t over = __ballot_sync(0xffffffffu, before + incl > goal);
                 if (over != 0u) {
-                    if (lane == 0) {
-                        p.tokens[row] = place(w0 + i + __ffs(over) - 1);
+                    if (lane == __ffs(over) - 1) {
+                        uint64_t at = before + incl - sum;
+                        int e = 0;
+                        while (e < 3 && at + w[e] <= goal) at += w[e++];
+                        p.tokens[row] = place(w0 + i + lane * 4 + e);
                         p.status[row] = TV_OK;
                     }
                     break;
                 }
-                before += __shfl_sync(0xffffffffu, s, 31);
+                before += __shfl_sync(0xffffffffu, incl, 31);
             }
     }
+    };
+    if (!near_path()) whole_path();
     if (out) {
+        const float cut_x = cut == ~0ull ? -INFINITY : value_of(cut);
         // weights again, in float32: 2^-22 of each, with the exponent's rounding
-        const float inv = (float)((double)(1ull << LS_FRAC) / (double)all);
-        for (int i = tid; i < n; i += LS_THREADS) {
-            const float x = xs[i];
-            float y = 0.f;
-            if (cut == ~0ull || ls_key(x, place(i)) <= cut) {
-                y = exp2f((x - top) * ch) * inv;
-                if (min_p > 0.f && weigh(x) < least) y = 0.f;
+        const float inv = 1.f / ((float)all * 2.2737368e-13f); // 2^-42
+        auto prob = [&](float x, int i) -> float {
+            if (!(x >= cut_x)) return 0.f;
+            const float t = (x - top) * ch, w = ex2_approx(t);
+            if (x == cut_x && ls_key(x, place(i)) > cut) return 0.f;
+            // (near min_p the exact weight decides)
+            if (min_p > 0.f && w < min_p * 1.001f && (w < min_p * 0.999f || weigh(x) < least)) return 0.f;
+            return w * inv;
+        };
+        if ((reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+#pragma unroll 2
+            for (int i = tid * 4; i < n; i += LS_THREADS * 4) {
+                const float4 x = *reinterpret_cast<const float4*>(xs + i);
+                const float4 y = make_float4(prob(x.x, i), prob(x.y, i + 1), prob(x.z, i + 2), prob(x.w, i + 3));
+                if (i + 4 <= n) {
+                    __stcs(reinterpret_cast<float4*>(out + i), y);
+                } else {
+                    out[i] = y.x;
+                    if (i + 1 < n) out[i + 1] = y.y;
+                    if (i + 2 < n) out[i + 2] = y.z;
+                }
             }
-            out[i] = y;
+        } else {
+            for (int i = tid; i < n; i += LS_THREADS) out[i] = prob(xs[i], i);
         }
     }
 }
