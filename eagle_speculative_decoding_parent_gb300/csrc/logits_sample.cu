@@ -151,15 +151,17 @@ template <typename E>
 __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __grid_constant__ LsParams p) {
     extern __shared__ __align__(16) float xs[];            // the slice
     __shared__ uint32_t hist[LS_BINS], tot[LS_BINS];       // the slice's counts, the row's
-    __shared__ uint64_t list[LS_LIST], weight[LS_LIST];    // first CTA: entries of one bin
+    __shared__ uint64_t lists[2 * LS_LIST];
+    uint64_t *list = lists, *weight = lists + LS_LIST;     // first CTA: entries of one bin
     __shared__ uint64_t table[64];
-    __shared__ uint64_t part[3][LS_WARPS];                 // per warp
-    __shared__ uint64_t peer[2][3][LS_CLUSTER_MAX];        // per CTA, two exchanges in turn
+    __shared__ uint64_t part[2][LS_WARPS];                 // per warp
+    __shared__ uint64_t peer[2][2][LS_CLUSTER_MAX];        // per CTA, two exchanges in turn
+    __shared__ uint32_t held_n, kept_n;
     __shared__ uint64_t result[3];                         // of the first CTA, of a bisection
-    // the near entries, in index order, where the list comes later (two barriers of the cluster on)
-    float* near_x = reinterpret_cast<float*>(weight);
-    uint16_t* near_i = reinterpret_cast<uint16_t*>(list);
-    static_assert(LS_HEAVY * sizeof(float) <= sizeof(weight) && LS_HEAVY * sizeof(uint16_t) <= sizeof(list), "near entries");
+    // the near entries, where the lists come later (a barrier of the cluster on)
+    float* near_x = reinterpret_cast<float*>(lists);
+    uint16_t* near_i = reinterpret_cast<uint16_t*>(near_x + LS_HEAVY);
+    static_assert(LS_HEAVY * 6 <= sizeof(lists) && LS_HEAVY <= 2 * LS_LIST, "near entries");
     __shared__ uint32_t list_n[3 + LS_TRIES];
     __shared__ uint32_t pick[2];                           // a bin, entries before it
     __shared__ float fpart[LS_WARPS], est;
@@ -172,6 +174,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     if (tid < 64) table[tid] = LS_TABLE[tid];
     if (tid < 3 + LS_TRIES) list_n[tid] = 0u;
     if (tid < 3) result[tid] = ~0ull;
+    if (tid == 0) held_n = kept_n = 0u;
     for (int i = tid; i < LS_BINS; i += LS_THREADS) hist[i] = 0u;
     pdl_launch_dependents();
     pdl_wait();
@@ -249,31 +252,33 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     }
     // ---- exchanges over the cluster: what a CTA's threads pass, reduced
     int turn = 0;
-    auto exchange = [&](uint64_t v0, uint64_t v1, uint64_t v2) {  // per CTA values into every CTA's peer[turn]
+    auto exchange = [&](uint64_t v0, uint64_t v1) {            // per CTA values into every CTA's peer[turn]
         if (tid < C) {
             remote_st_u64(&peer[turn][0][me], tid, v0);
             remote_st_u64(&peer[turn][1][me], tid, v1);
-            remote_st_u64(&peer[turn][2][me], tid, v2);
         }
         cluster_barrier_all();
         turn ^= 1;                                             // (read peer[turn ^ 1])
     };
-    auto block_sum = [&](uint64_t (&v)[3], int count) {
+    // Sums over the CTA: true in the first warp, which has them (and passes them on); part is
+    // free again after the next barrier.
+    auto block_sum = [&](uint64_t (&v)[2], int count) {
         for (int c = 0; c < count; ++c) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) v[c] += __shfl_xor_sync(0xffffffffu, v[c], o);
             if (lane == 0) part[c][warp] = v[c];
         }
         __syncthreads();
-        for (int c = 0; c < count; ++c) {
-            v[c] = 0ull;
-            for (int w = 0; w < LS_WARPS; ++w) v[c] += part[c][w];
-        }
-        __syncthreads();
+        if (warp == 0)
+            for (int c = 0; c < count; ++c) {
+                v[c] = lane < LS_WARPS ? part[c][lane] : 0ull;
+#pragma unroll
+                for (int o = LS_WARPS / 2; o > 0; o >>= 1) v[c] += __shfl_xor_sync(0xffffffffu, v[c], o);
+            }
     };
-    auto cluster_sum = [&](uint64_t (&v)[3], int count) {
+    auto cluster_sum = [&](uint64_t (&v)[2], int count) {
         block_sum(v, count);
-        exchange(v[0], v[1], v[2]);
+        exchange(v[0], v[1]);
         for (int c = 0; c < count; ++c) {
             v[c] = 0ull;
             for (int r = 0; r < C; ++r) v[c] += peer[turn ^ 1][c][r];
@@ -324,7 +329,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         mx = fpart[0];
         for (int w = 1; w < LS_WARPS; ++w) asm("max.NaN.f32 %0, %1, %2;" : "=f"(mx) : "f"(mx), "f"(fpart[w]));
         cluster_wait();
-        exchange(__float_as_uint(mx), 0ull, 0ull);
+        exchange(__float_as_uint(mx), 0ull);
         top = __uint_as_float((uint32_t)peer[turn ^ 1][0][0]);
         for (int r = 1; r < C; ++r) {
             const float y = __uint_as_float((uint32_t)peer[turn ^ 1][0][r]);
@@ -349,7 +354,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         if (lane == 0) part[0][warp] = best;
         __syncthreads();
         for (int w = 0; w < LS_WARPS; ++w) best = min(best, (uint32_t)part[0][w]);
-        exchange(best, 0ull, 0ull);
+        exchange(best, 0ull);
         for (int r = 0; r < C; ++r) best = min(best, (uint32_t)peer[turn ^ 1][0][r]);
         token = (int)best;
         if (me == 0 && tid == 0) {
@@ -378,8 +383,11 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     auto sum_bins = [&](int from, int to) {
         for (int i = me * LS_THREADS + tid; i < LS_BINS; i += C * LS_THREADS)
             if (i >= from && i < to) {
-                uint32_t sum = 0u;
-                for (int r = 0; r < C; ++r) sum += remote_ld_u32(&hist[i], r);
+                uint32_t sum = 0u, got[LS_CLUSTER_MAX];
+#pragma unroll
+                for (int r = 0; r < LS_CLUSTER_MAX; ++r) got[r] = r < C ? remote_ld_u32(&hist[i], r) : 0u;
+#pragma unroll
+                for (int r = 0; r < LS_CLUSTER_MAX; ++r) sum += got[r];
                 for (int r = 0; r < C; ++r) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(&tot[i], r)), "r"(sum) : "memory");
             }
         cluster_barrier_all();
@@ -489,71 +497,63 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         }
     };
 
-    // ---- Where all that may be kept weighs 2^-16 or more, and few entries do: those are compacted, in index
-    // order, and a thread holds up to four with their weights.
+    // ---- Where all that may be kept weighs 2^-16 or more, and few entries do: those are compacted, and a
+    // thread holds up to four with their weights.
     auto near_path = [&]() -> bool {
-        if (!(use_k || use_p || min_p >= 3.1e-5f) || chunk > 1024) return false;
-        uint32_t marks = 0u, small = 0u;
+        if (!(use_k || use_p || min_p >= 3.1e-5f)) return false;
+        uint32_t small = 0u;
+#pragma unroll 1
+        for (int g = 0; g < chunk; g += 1024) {
+            uint32_t marks = 0u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e * 128 < chunk) {
-                const float4 q = *reinterpret_cast<const float4*>(xs + w0 + e * 128 + lane * 4);
-                const float y[4] = {q.x, q.y, q.z, q.w};
+            for (int e = 0; e < 8; ++e)
+                if (g + e * 128 < chunk) {
+                    const float4 q = *reinterpret_cast<const float4*>(xs + w0 + g + e * 128 + lane * 4);
+                    const float y[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const float d = top - y[z];
-                    const bool is_near = d * bin_scale < (float)LS_NEAR;
-                    marks |= is_near ? 1u << (4 * e + z) : 0u;
-                    if (!use_k && !is_near) {
-                        // in 2^-38 of the largest, below 2^23 of them: rounded by adding 2^23
-                        const float t = fmaf(d, cl, d * ch);
-                        small += __float_as_uint(ex2_approx(fmaxf((float)(LS_FRAC - 4) - t, -126.f)) + 8388608.f) - __float_as_uint(8388608.f);
+                    for (int z = 0; z < 4; ++z) {
+                        const float d = top - y[z];
+                        const bool is_near = d * bin_scale < (float)LS_NEAR;
+                        marks |= is_near ? 1u << (4 * e + z) : 0u;
+                        if (!use_k && !is_near) {
+                            // in 2^-38 of the largest, below 2^23 of them: rounded by adding 2^23
+                            const float t = fmaf(d, cl, d * ch);
+                            small += __float_as_uint(ex2_approx(fmaxf((float)(LS_FRAC - 4) - t, -126.f)) + 8388608.f) - __float_as_uint(8388608.f);
+                        }
                     }
                 }
-            }
-        // places in index order: 128 entries after 128, lane after lane
-        const int own = __popc(marks);
-        const uint32_t warp_all = __reduce_add_sync(0xffffffffu, (uint32_t)own);
-        if (lane == 0) part[0][warp] = warp_all;
-        __syncthreads();
-        uint32_t at = 0u, held = 0u;
-        for (int w = 0; w < LS_WARPS; ++w) {
-            if (w < warp) at += (uint32_t)part[0][w];
-            held += (uint32_t)part[0][w];
-        }
-        if (held <= LS_HEAVY) {
-#pragma unroll 1
-            for (int e = 0; e * 128 < chunk; ++e) {
-                const uint32_t nib = (marks >> (4 * e)) & 15u;
-                const uint32_t mine = (uint32_t)__popc(nib);
-                uint32_t incl = mine;
+            // places for the warp's entries by one atomic
+            const uint32_t own = (uint32_t)__popc(marks);
+            uint32_t incl = own;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += y;
-                }
-                uint32_t to = at + incl - mine;
-                for (uint32_t left = nib; left != 0u; left &= left - 1u, ++to) {
-                    const int i = w0 + e * 128 + lane * 4 + __ffs(left) - 1;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            uint32_t to = 0u;
+            if (lane == 31) to = atomicAdd(&held_n, incl);
+            to = __shfl_sync(0xffffffffu, to, 31) + incl - own;
+            for (; marks != 0u; marks &= marks - 1u, ++to) {
+                const int e = __ffs(marks) - 1, i = w0 + g + (e >> 2) * 128 + lane * 4 + (e & 3);
+                if (to < LS_HEAVY) {
                     near_x[to] = xs[i];
                     near_i[to] = (uint16_t)i;
                 }
-                at += __shfl_sync(0xffffffffu, incl, 31);
             }
         }
         __syncthreads();
+        const uint32_t held = held_n;
         // this thread's entries: keys, bins, weights
-        const int each = ((int)min(held, (uint32_t)LS_HEAVY) + LS_THREADS - 1) / LS_THREADS;
         uint64_t wt[4], key[4];
         int bin[4];
-        uint64_t v[3] = {0ull, 0ull, 0ull};
+        uint64_t v[2] = {0ull, 0ull};
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-            const int e = tid * each + y;
+            const int e = tid + y * LS_THREADS;
             wt[y] = 0ull;
             key[y] = ~0ull;
             bin[y] = LS_BINS;
-            if (y < each && e < (int)held && held <= LS_HEAVY) {
+            if (e < (int)held && held <= LS_HEAVY) {
                 const float x = near_x[e];
                 key[y] = ls_key(x, place(near_i[e]));
                 bin[y] = bin_of(x);
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         }
         v[0] += (uint64_t)small << 4;
         block_sum(v, 1);
-        exchange(v[0], held <= LS_HEAVY ? 0ull : 1ull, 0ull);
+        exchange(v[0], held <= LS_HEAVY ? 0ull : 1ull);
         uint64_t mass_all = 0ull, over = 0ull;
         for (int r = 0; r < C; ++r) {
             mass_all += peer[turn ^ 1][0][r];
@@ -630,41 +630,40 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             cut = min(cut, result[1]);
         }
         // ---- the mass that is left, and where the draw falls
-        uint64_t mine = 0ull;
+        v[0] = 0ull;
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
             if (key[y] > cut || wt[y] < least) wt[y] = 0ull;
-            mine += wt[y];
+            v[0] += wt[y];
         }
-        uint64_t incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-        }
-        if (lane == 31) part[0][warp] = incl;
-        __syncthreads();
-        uint64_t before = incl - mine, sum = 0ull;
-        for (int w = 0; w < LS_WARPS; ++w) {
-            if (w < warp) before += part[0][w];
-            sum += part[0][w];
-        }
-        exchange(sum, 0ull, 0ull);
+        block_sum(v, 1);
+        exchange(v[0], 0ull);
+        uint64_t before = 0ull;
         for (int r = 0; r < C; ++r) {
             if (r < me) before += peer[turn ^ 1][0][r];
             all += peer[turn ^ 1][0][r];
         }
         const uint64_t goal = ls_part<false>(u, all);
-        if (goal >= before && goal < before + mine) {
-            uint64_t idx = key[0], to = before + wt[0];
+        if (goal >= before && goal < before + peer[turn ^ 1][0][me]) {
+            // in this CTA: what it keeps in a list, (place in the slice, weight) in a word each
 #pragma unroll
-            for (int z = 1; z < 4; ++z)
-                if (to <= goal) {
-                    to += wt[z];
-                    idx = key[z];
+            for (int y = 0; y < 4; ++y)
+                if (wt[y] != 0ull) lists[atomicAdd(&kept_n, 1u)] = (uint64_t)((uint32_t)key[y] - (uint32_t)x0) << 44 | wt[y];
+            __syncthreads();
+            const int m = (int)kept_n;
+            for (int e = tid; e < m; e += LS_THREADS) {
+                const uint64_t mine = lists[e];
+                uint64_t at = before;
+#pragma unroll 4
+                for (int f = 0; f < m; ++f) {
+                    const uint64_t other = lists[f];
+                    at += (other >> 44) < (mine >> 44) ? other & ((1ull << 44) - 1ull) : 0ull;
                 }
-            p.tokens[row] = (int)(uint32_t)idx;
-            p.status[row] = TV_OK;
+                if (goal >= at && goal < at + (mine & ((1ull << 44) - 1ull))) {
+                    p.tokens[row] = place((int)(mine >> 44));
+                    p.status[row] = TV_OK;
+                }
+            }
         }
         return true;
     };
@@ -672,7 +671,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     // first key with which count entries, or a mass above before, are kept (`kept` entries count).
     auto bisect = [&](bool mass, uint64_t need, uint64_t limit) -> uint64_t {
         uint32_t lo = 0u, hi = 0xffffffffu;                    // largest bits from which on there are `need`
-        uint64_t v[3];
+        uint64_t v[2];
         auto above = [&](uint32_t bits, bool strict) -> uint64_t {
             v[0] = 0ull;
             entries([&](float x, int i) {
@@ -698,14 +697,14 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
         block_sum(v, 1);
-        exchange(v[0], 0ull, 0ull);
+        exchange(v[0], 0ull);
         uint64_t before = 0ull, all = 0ull;
         for (int r = 0; r < C; ++r) {
             if (r < me) before += peer[turn ^ 1][0][r];
             all += peer[turn ^ 1][0][r];
         }
         const uint64_t want = min(ties, all);
-        if (want > before && want <= before + v[0]) {
+        if (want > before && want <= before + peer[turn ^ 1][0][me]) {
             // in this CTA: its warps in order
             if (lane == 0) part[0][warp] = mine;
             __syncthreads();
@@ -754,7 +753,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             return sum_bins(from, to);
         };
         // the entries that weigh 2^-16 or more; in the same pass, without top-k, the sum of all weights
-        uint64_t v[3] = {0ull, 0ull, 0ull};
+        uint64_t v[2] = {0ull, 0ull};
         uint32_t small = 0u;                                   // in 2^-42
         marked(
             [&](float x) -> bool {
@@ -863,20 +862,20 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     const float cut_x = cut == ~0ull ? -INFINITY : value_of(cut);
     const float most_t = min_p > 0.f ? fminf((float)(LS_FRAC + 1), 0.001f - log2f(min_p)) : (float)(LS_FRAC + 1);
     auto maybe = [&](float x) -> bool { return x >= cut_x && (top - x) * ch < most_t; };
-    uint64_t v[3] = {0ull, 0ull, 0ull};
+    uint64_t v[2] = {0ull, 0ull};
     marked(maybe, [&](float x, int i) { v[0] += kept(x, i); });
     uint64_t mine = v[0];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     block_sum(v, 1);
-    exchange(v[0], 0ull, 0ull);
+    exchange(v[0], 0ull);
     uint64_t before = 0ull;
     for (int r = 0; r < C; ++r) {
         if (r < me) before += peer[turn ^ 1][0][r];
         all += peer[turn ^ 1][0][r];
     }
     const uint64_t goal = ls_part<false>(u, all);              // the first entry whose sum exceeds it
-    if (goal >= before && goal < before + v[0]) {
+    if (goal >= before && goal < before + peer[turn ^ 1][0][me]) {
         if (lane == 0) part[0][warp] = mine;
         __syncthreads();
         for (int w = 0; w < warp; ++w) before += part[0][w];
