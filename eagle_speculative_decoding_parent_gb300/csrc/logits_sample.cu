@@ -48,6 +48,12 @@ constexpr float LS_SMALL = 19.f;             // weights below 2^-19 enter the su
 constexpr int LS_LIST = 1024;
 constexpr int LS_HEAVY = 4 * LS_THREADS;     // near entries that a CTA's threads hold
 constexpr int LS_TRIES = 4;
+// Rows left to logits_sample_rows_kernel: at most so many near entries, dumped behind a header of so
+// many words into the slices' part of the distribution; the status that says so.
+constexpr int LS_ROW = 8192;
+constexpr int LS_HEAD = 8;
+constexpr int32_t LS_PENDING = -0x5eed;
+constexpr int LS_BUCKETS = 1024;             // of the vocabulary, for the draw
 constexpr int LS_FRAC = 42;                  // a weight of 1 is 2^42
 
 // 2^(62 - j / 64)
@@ -81,6 +87,8 @@ struct LsParams {
     float* probs;
     int32_t* status;
     int N, V, slice, ctas;   // ctas: of a row
+    int64_t rows, ahead;     // ahead: rows that the GPU holds at once
+    bool defer;              // distributions of many rows: the near entries to the second kernel
 };
 
 // The order of the entries: smaller is better, all different.
@@ -197,6 +205,13 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         }
     };
     if (err != TV_OK) return refuse();
+    if (p.defer && tid == 0) {
+        // to L2: this slice of the row that a cluster of the next wave takes
+        const int64_t next = row + p.ahead;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(static_cast<const E*>(p.logits) + next * p.V + x0);
+        const uintptr_t lo = (a + 15) & ~(uintptr_t)15, hi = (a + (uintptr_t)n * sizeof(E)) & ~(uintptr_t)15;
+        if (next < p.rows && lo < hi) bulk_prefetch_l2(reinterpret_cast<const void*>(lo), (uint32_t)(hi - lo));
+    }
     __syncthreads();
     cluster_arrive();                                          // this CTA has started, its counters are zero
 
@@ -499,6 +514,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
 
     // ---- Where all that may be kept weighs 2^-16 or more, and few entries do: those are compacted, and a
     // thread holds up to four with their weights.
+    bool deferred = false;
     auto near_path = [&]() -> bool {
         if (!(use_k || use_p || min_p >= 3.1e-5f)) return false;
         uint32_t small = 0u;
@@ -546,7 +562,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         // this thread's entries: keys, bins, weights
         uint64_t wt[4], key[4];
         int bin[4];
-        uint64_t v[2] = {0ull, 0ull};
+        uint64_t v[2] = {0ull, small};
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
             const int e = tid + y * LS_THREADS;
@@ -559,18 +575,54 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
                 bin[y] = bin_of(x);
                 wt[y] = weigh(x);
                 v[0] += wt[y];
-                atomicAdd(&hist[bin[y]], 1u);
+                if (!p.defer) atomicAdd(&hist[bin[y]], 1u);
             }
         }
-        v[0] += (uint64_t)small << 4;
-        block_sum(v, 1);
-        exchange(v[0], held <= LS_HEAVY ? 0ull : 1ull);
-        uint64_t mass_all = 0ull, over = 0ull;
+        // the weights' sum; how many, and the sum of the others
+        const bool fits = held <= LS_HEAVY && (!p.defer || LS_HEAD + 2 * (int)held <= n);
+        block_sum(v, 2);
+        exchange(v[0], v[1] << 16 | (fits ? held : 0xffffu));
+        uint64_t mass_near = 0ull, mass_all = 0ull;
+        uint32_t held_all = 0u;
+        bool over = false;
         for (int r = 0; r < C; ++r) {
-            mass_all += peer[turn ^ 1][0][r];
-            over += peer[turn ^ 1][1][r];
+            const uint64_t a = peer[turn ^ 1][1][r];
+            mass_near += peer[turn ^ 1][0][r];
+            mass_all += (a >> 16) << 4;
+            over = over || (a & 0xffffull) == 0xffffull;
+            held_all += (uint32_t)(a & 0xffffull);
         }
-        if (over != 0ull) return false;
+        mass_all += mass_near;
+        if (over) return false;
+        if (p.defer) {
+            // the second kernel takes it from here, if the near entries hold all that may be kept
+            if (held_all > LS_ROW || (use_k ? held_all < (uint32_t)k : use_p && ls_part<true>(top_p, mass_all) > mass_near)) return false;
+            uint32_t* dump = reinterpret_cast<uint32_t*>(out);
+            const uint64_t mine = peer[turn ^ 1][1][me];
+            if (tid == 0) {
+                dump[0] = held;
+                dump[1] = (uint32_t)(mine >> 16);
+                dump[2] = (uint32_t)(mine >> 48);
+                dump[3] = __float_as_uint(top);
+                if (me == 0) p.status[row] = LS_PENDING;
+            }
+            for (int e = tid; e < (int)held; e += LS_THREADS) {
+                dump[LS_HEAD + 2 * e] = __float_as_uint(near_x[e]);
+                dump[LS_HEAD + 2 * e + 1] = (uint32_t)place(near_i[e]);
+            }
+            const int from = LS_HEAD + 2 * (int)held;
+            if ((reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+                const int full = min(n, (from + 3) & ~3);
+                if (from + tid < full) out[from + tid] = 0.f;
+                for (int i = full + tid * 4; i + 4 <= n; i += LS_THREADS * 4) __stcs(reinterpret_cast<float4*>(out + i), make_float4(0.f, 0.f, 0.f, 0.f));
+                const int tail = max(full, n & ~3);
+                if (tail + tid < n) out[tail + tid] = 0.f;
+            } else {
+                for (int i = from + tid; i < n; i += LS_THREADS) out[i] = 0.f;
+            }
+            deferred = true;
+            return true;
+        }
         int k_bin = LS_BINS - 1;
         uint32_t k_rank = (uint32_t)p.V;
         if (use_k || use_p) {
@@ -912,7 +964,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     }
     };
     if (!near_path()) whole_path();
-    if (out) {
+    if (out && !deferred) {
         const float cut_x = cut == ~0ull ? -INFINITY : value_of(cut);
         // weights again, in float32: 2^-22 of each, with the exponent's rounding
         const float inv = 1.f / ((float)all * 2.2737368e-13f); // 2^-42
@@ -943,6 +995,278 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     }
 }
 
+// The rows that the kernel above left: their near entries, by one CTA each.  Counts and exact masses by
+// bins give the bins of the cuts, whose entries are ranked (or, if a bin has more than the list
+// holds, bisected by key); then what is kept goes where it belongs, and the draw is found by
+// buckets of the vocabulary.
+constexpr int LR_THREADS = 512, LR_WARPS = LR_THREADS / 32;
+static_assert(LS_BUCKETS == 2 * LR_THREADS && LS_NEAR <= LS_BUCKETS, "two bins or buckets per thread");
+
+__global__ void __launch_bounds__(LR_THREADS, 2) logits_sample_rows_kernel(const __grid_constant__ LsParams p) {
+    extern __shared__ __align__(16) uint2 held[];           // [LS_ROW] (logit, index)
+    __shared__ uint32_t count[LS_BUCKETS];                  // entries and mass per bin, then mass per bucket
+    __shared__ unsigned long long mass[LS_BUCKETS];
+    __shared__ uint64_t list[LS_LIST], weight[LS_LIST];
+    __shared__ uint64_t table[64];
+    __shared__ uint64_t part[LR_WARPS];
+    __shared__ uint32_t cpart[LR_WARPS];
+    __shared__ uint64_t result, upto, others, before_pick;
+    __shared__ uint32_t first[LS_CLUSTER_MAX + 1], list_n, pick, pick_rank;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t row = blockIdx.x;
+    const int b = (int)(row / p.N), node = (int)(row % p.N);
+    if (tid < 64) table[tid] = LS_TABLE[tid];
+    for (int i = tid; i < LS_BUCKETS; i += LR_THREADS) {
+        count[i] = 0u;
+        mass[i] = 0ull;
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+    const int cnt = p.node_counts ? p.node_counts[b] : p.N;
+    if ((cnt >= 1 && cnt <= p.N && node >= cnt) || p.status[row] != LS_PENDING) return;
+    const float T = p.temp ? p.temp[b] : 1.f, top_p = p.top_p ? p.top_p[b] : 1.f;
+    const float min_p = p.min_p ? p.min_p[b] : 0.f, u = p.uniform[row];
+    const int k = p.top_k ? p.top_k[b] : 0;
+    const bool use_k = k > 0 && k < p.V, use_p = top_p < 1.f;
+    const uint64_t least = (uint64_t)ceilf(min_p * (float)(1ull << LS_FRAC));
+    float* out = p.probs + row * p.V;
+    const uint32_t* dump = reinterpret_cast<const uint32_t*>(out);
+    if (warp == 0) {
+        const uint32_t* head = dump + (int64_t)lane * p.slice;
+        const uint32_t mine = lane < p.ctas ? head[0] : 0u;
+        uint64_t rest = lane < p.ctas ? (uint64_t)head[1] | (uint64_t)head[2] << 32 : 0ull;
+        uint32_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+        if (lane <= LS_CLUSTER_MAX) first[lane] = incl - mine;
+        if (lane == 0) others = rest << 4;
+    }
+    const float top = __uint_as_float(dump[3]);
+    __syncthreads();
+    const int total = (int)first[p.ctas];
+    for (int r = warp; r < p.ctas; r += LR_WARPS) {
+        const uint32_t* src = dump + (int64_t)r * p.slice + LS_HEAD;
+        const int m = (int)(first[r + 1] - first[r]);
+#pragma unroll 4
+        for (int e = lane; e < m; e += 32) held[first[r] + e] = make_uint2(src[2 * e], src[2 * e + 1]);
+    }
+    __syncthreads();
+    // (the dump lies in the distribution)
+    for (int r = warp; r < p.ctas; r += LR_WARPS) {
+        float* to = out + (int64_t)r * p.slice;
+        const int words = LS_HEAD + 2 * (int)(first[r + 1] - first[r]);
+        for (int e = lane; e < words; e += 32) to[e] = 0.f;
+    }
+    constexpr float L2EH = 1.44269502162933349609f, L2EL = 1.92596299112661746887e-8f;
+    const float ch = L2EH / T, cl = (fmaf(-ch, T, L2EH) + L2EL) / T;
+    const float bin_scale = fminf(LS_BIN / T, 1e38f);
+    auto bin_of = [&](float x) -> int { return (int)fminf((top - x) * bin_scale, (float)(LS_BUCKETS - 1)); };
+    auto weigh = [&](float x) -> uint64_t { return ls_weight(x, top, ch, cl, table); };
+    auto each = [&](auto f) {                               // f(logit, index)
+#pragma unroll 1
+        for (int e = tid; e < total; e += LR_THREADS) {
+            const uint2 a = held[e];
+            f(__uint_as_float(a.x), (int)a.y);
+        }
+    };
+    auto sum_of = [&](uint64_t v) -> uint64_t {             // over the CTA, for every thread
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        __syncthreads();
+        if (lane == 0) part[warp] = v;
+        __syncthreads();
+        v = 0ull;
+#pragma unroll
+        for (int w = 0; w < LR_WARPS; ++w) v += part[w];
+        return v;
+    };
+    // Entries and mass before this thread's two bins (or buckets); the mass of all.
+    uint32_t c0 = 0u, c1 = 0u, c_before = 0u;
+    uint64_t m0 = 0ull, m1 = 0ull, m_before = 0ull;
+    auto scan = [&]() -> uint64_t {
+        c0 = count[2 * tid], c1 = count[2 * tid + 1];
+        m0 = mass[2 * tid], m1 = mass[2 * tid + 1];
+        uint32_t ci = c0 + c1;
+        uint64_t mi = m0 + m1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, ci, o);
+            const uint64_t z = __shfl_up_sync(0xffffffffu, mi, o);
+            if (lane >= o) {
+                ci += y;
+                mi += z;
+            }
+        }
+        if (lane == 31) {
+            part[warp] = mi;
+            cpart[warp] = ci;
+        }
+        __syncthreads();
+        c_before = ci - c0 - c1;
+        m_before = mi - m0 - m1;
+        uint64_t all = 0ull;
+#pragma unroll
+        for (int w = 0; w < LR_WARPS; ++w) {
+            if (w < warp) {
+                c_before += cpart[w];
+                m_before += part[w];
+            }
+            all += part[w];
+        }
+        return all;
+    };
+    // The bin in which the mass passes `goal` (before <= goal < up to it): pick, and the mass before it.
+    auto pick_mass = [&](uint64_t goal) {
+        if (m_before <= goal && goal < m_before + m0) {
+            pick = 2 * tid;
+            before_pick = m_before;
+        } else if (m_before + m0 <= goal && goal < m_before + m0 + m1) {
+            pick = 2 * tid + 1;
+            before_pick = m_before + m0;
+        }
+        __syncthreads();
+    };
+    // The key in a bin with rank `rank` there (by_rank), or of the last entry (up to `limit`) that begins
+    // below need when `base` comes before the bin: result; upto: the bin's mass up to it.
+    auto cut_in = [&](int bin, bool by_rank, uint32_t rank, uint64_t base, uint64_t need, uint64_t limit) {
+        if (count[bin] <= LS_LIST) {
+            if (tid == 0) list_n = 0u;
+            __syncthreads();
+            each([&](float x, int i) {
+                if (bin_of(x) != bin || ls_key(x, i) > limit) return;
+                const uint32_t at = atomicAdd(&list_n, 1u);
+                list[at] = ls_key(x, i);
+                weight[at] = weigh(x);
+            });
+            __syncthreads();
+            const int m = (int)list_n;
+            for (int e = tid; e < m; e += LR_THREADS) {
+                const uint64_t key = list[e], w = weight[e];
+                uint32_t n = 0u;
+                uint64_t before = 0ull;
+#pragma unroll 4
+                for (int f = 0; f < m; ++f)
+                    if (list[f] < key) {
+                        ++n;
+                        before += weight[f];
+                    }
+                if (by_rank ? n == rank : base + before < need && base + before + w >= need) {
+                    result = key;
+                    upto = before + w;
+                }
+            }
+            __syncthreads();
+            return;
+        }
+        // many equal entries: the smallest key up to which there are enough
+        uint64_t lo = 0ull, hi = limit, got = 0ull;
+        while (lo < hi) {
+            const uint64_t mid = lo + ((hi - lo) >> 1);
+            uint64_t v = 0ull;
+            each([&](float x, int i) {
+                if (bin_of(x) == bin && ls_key(x, i) <= mid) v += by_rank ? 1ull : weigh(x);
+            });
+            v = sum_of(v);
+            if (by_rank ? v > rank : base + v >= need) hi = mid;
+            else lo = mid + 1ull;
+        }
+        each([&](float x, int i) {
+            if (bin_of(x) == bin && ls_key(x, i) <= hi) got += weigh(x);
+        });
+        got = sum_of(got);
+        if (tid == 0) {
+            result = hi;
+            upto = got;
+        }
+        __syncthreads();
+    };
+    uint64_t cut = ~0ull;
+    if (use_k || use_p) {
+        each([&](float x, int) {
+            const int bin = bin_of(x);
+            atomicAdd(&count[bin], 1u);
+            atomicAdd(&mass[bin], (unsigned long long)weigh(x));
+        });
+        __syncthreads();
+        uint64_t left = scan() + others;                    // the mass that top-k leaves
+        int k_bin = LS_BUCKETS;
+        uint64_t k_before = 0ull;
+        if (use_k) {
+            const uint32_t want = (uint32_t)k;
+            if (c_before < want && want <= c_before + c0) {
+                pick = 2 * tid;
+                pick_rank = want - c_before - 1u;
+                before_pick = m_before;
+            } else if (c_before + c0 < want && want <= c_before + c0 + c1) {
+                pick = 2 * tid + 1;
+                pick_rank = want - c_before - c0 - 1u;
+                before_pick = m_before + m0;
+            }
+            __syncthreads();
+            k_bin = (int)pick;
+            k_before = before_pick;
+            cut_in(k_bin, true, pick_rank, 0ull, 0ull, ~0ull);
+            cut = result;
+            left = k_before + upto;
+            __syncthreads();
+        }
+        if (use_p) {
+            const uint64_t need = ls_part<true>(top_p, left);   // (at least 1: the best entry weighs 2^42)
+            int bin = k_bin;
+            uint64_t base = k_before;
+            if (!use_k || need <= k_before) {
+                pick_mass(need - 1ull);
+                bin = (int)pick;
+                base = before_pick;
+            }
+            cut_in(bin, false, 0u, base, need, cut);
+            cut = min(cut, result);
+        }
+    }
+    // ---- what is kept: its sum, by buckets of the vocabulary
+    __syncthreads();
+    for (int i = tid; i < LS_BUCKETS; i += LR_THREADS) mass[i] = 0ull;
+    __syncthreads();
+    const uint32_t width = (uint32_t)(p.V + LS_BUCKETS - 1) / LS_BUCKETS;
+    each([&](float x, int i) {
+        if (ls_key(x, i) > cut) return;
+        const uint64_t w = weigh(x);
+        if (w >= least) atomicAdd(&mass[(uint32_t)i / width], (unsigned long long)w);
+    });
+    __syncthreads();
+    const uint64_t all = scan(), goal = ls_part<false>(u, all);
+    if (tid == 0) list_n = 0u;
+    pick_mass(goal);
+    const uint32_t bucket = pick;
+    const float inv = 1.f / (float)all;
+    each([&](float x, int i) {
+        if (ls_key(x, i) > cut) return;
+        const uint64_t w = weigh(x);
+        if (w < least) return;
+        out[i] = (float)w * inv;
+        if ((uint32_t)i / width == bucket) {
+            const uint32_t at = atomicAdd(&list_n, 1u);     // (a bucket has at most `width` entries)
+            list[at] = (uint64_t)i;
+            weight[at] = w;
+        }
+    });
+    __syncthreads();
+    const int m = (int)list_n;
+    for (int e = tid; e < m; e += LR_THREADS) {
+        uint64_t at = before_pick;
+        for (int f = 0; f < m; ++f) at += list[f] < list[e] ? weight[f] : 0ull;
+        if (at <= goal && goal < at + weight[e]) {
+            p.tokens[row] = (int)list[e];
+            p.status[row] = TV_OK;
+        }
+    }
+}
+
 template <typename E>
 tv_status launch_sample(const LsParams& q, int64_t rows, cudaStream_t stream) {
     LsParams p = q;
@@ -961,7 +1285,7 @@ tv_status launch_sample(const LsParams& q, int64_t rows, cudaStream_t stream) {
     if (p.slice > LS_SLICE_MAX) return TV_ERR_UNSUPPORTED;
     if (rows * C > 0x7fffffff) return TV_ERR_UNSUPPORTED;
     const size_t smem = (size_t)p.slice * sizeof(float);
-    static std::atomic<bool> set[64];
+    static std::atomic<bool> set[64], set_rows[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TV_ERR_CUDA;
     if (!set[dev]) {
@@ -972,8 +1296,23 @@ tv_status launch_sample(const LsParams& q, int64_t rows, cudaStream_t stream) {
         }
         set[dev] = true;
     }
+    // Several waves of clusters, each of which would go through its cuts' barriers with its row in shared
+    // memory: the cuts are left to a second kernel, behind the dumps in the distributions.
+    p.rows = rows;
+    p.ahead = std::max(1, 2 * device_sm_count() / C);
+    p.defer = p.probs != nullptr && rows * C > 4 * device_sm_count() && p.slice >= LS_STEP && p.V <= LS_LIST * LS_BUCKETS;
+    if (p.defer && !set_rows[dev]) {
+        if (cudaFuncSetAttribute(logits_sample_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, LS_ROW * (int)sizeof(uint2)) != cudaSuccess) {
+            cudaGetLastError();
+            return TV_ERR_CUDA;
+        }
+        set_rows[dev] = true;
+    }
     LaunchCfg lc(dim3((unsigned)(rows * C)), dim3(LS_THREADS), smem, stream, (unsigned)C);
-    return cudaLaunchKernelEx(&lc.cfg, fn, p) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+    if (cudaLaunchKernelEx(&lc.cfg, fn, p) != cudaSuccess) return TV_ERR_CUDA;
+    if (!p.defer) return TV_OK;
+    LaunchCfg lr(dim3((unsigned)rows), dim3(LR_THREADS), LS_ROW * sizeof(uint2), stream);
+    return cudaLaunchKernelEx(&lr.cfg, logits_sample_rows_kernel, p) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
 
 }  // namespace

@@ -85,6 +85,31 @@ def test_many_rows(tv):
     check(tv, x, u, temp=[0.5 + 0.1 * b for b in range(20)], p=[0.5 + 0.02 * b for b in range(20)], k=[0, 7] * 10)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,N,V", [(60, 22, 3001), (20, 13, 40000), (41, 16, 2100)])
+def test_distributions_of_many_rows(tv, dtype, B, N, V):
+    """More rows than the GPU holds at once; each sequence with filters of its own."""
+    x, u = rows(B, N, V, V, dtype)
+    x[1] = 0.25                                                  # rows of equal entries,
+    x[2] = (torch.arange(V) % 3).to(dtype)                       # of few different ones,
+    x[3, :, ::2] = -math.inf                                     # masked ones,
+    x[4] *= 0.01                                                 # nearly flat ones
+    x[5, :, 7] = 100.0
+    some = [0.0, 0.3, 0.7, 1.0, 1.6]
+    check(tv, x, u, temp=[some[b % 5] for b in range(B)], k=[[0, 40, 3, 2000][b % 4] for b in range(B)],
+          p=[[1.0, 0.9, 0.99, 0.2, 0.95, 0.5][b % 6] for b in range(B)], m=[[0.0, 0.0, 0.05][b % 3] for b in range(B)])
+    # rows that cannot be sampled beside the others
+    x[6, 0, 3] = math.nan
+    x[7] = -math.inf
+    u[8, 1] = 2.0
+    tokens, status, probs = sample(tv, x, u, p=[0.9] * B, counts=[N if b != 9 else 3 for b in range(B)])
+    assert status[6, 0] == 7 and status[7].eq(7).all() and status[8, 1] == 7 and status[9, 3:].eq(-9).all()
+    assert bool((probs[6, 0] == 0).all()) and bool((probs[7] == 0).all()) and bool((probs[9, 3:] == 5.0).all())
+    good = torch.ones((B, N), dtype=torch.bool)
+    good[6, 0], good[7], good[8, 1], good[9, 3:] = False, False, False, False
+    assert status[good].eq(0).all() and bool(((probs[good].double().sum(-1) - 1).abs() < 1e-5).all())
+
+
 @pytest.mark.parametrize("V", [5, 3000, 40000])
 def test_equal_logits(tv, V):
     """Rows with long runs of equal entries, which are taken by their index: whole rows of one value, of a
