@@ -39,11 +39,12 @@ constexpr int LS_THREADS = 512;
 constexpr int LS_WARPS = LS_THREADS / 32;
 constexpr int LS_STEP = LS_WARPS * 128;      // a slice is a multiple of this
 constexpr int LS_CLUSTER_MAX = 16;
-constexpr int LS_SLICE = 16384;              // entries per CTA, two CTAs per SM
+constexpr int LS_SLICE_BYTES = 65536;        // of a row per CTA, two CTAs per SM
 constexpr int LS_SLICE_MAX = 49152;          // longer rows: one CTA per SM
 constexpr int LS_BINS = 2048;
 constexpr float LS_BIN = 64.f;               // bins per unit of (max - x) / T
-constexpr int LS_NEAR = 704;                 // bins of the first count
+// Bins of the first count: near entries weigh 2^-16 or more, or 2^-12 where those are too many.
+constexpr int LS_NEAR = 704, LS_NEARER = 544;
 constexpr float LS_SMALL = 19.f;             // weights below 2^-19 enter the sum of all in float32
 constexpr int LS_LIST = 1024;
 constexpr int LS_HEAVY = 4 * LS_THREADS;     // near entries that a CTA's threads hold
@@ -139,8 +140,20 @@ __device__ __forceinline__ uint64_t ls_weight(float x, float top, float ch, floa
     return (v + (1ull << (61 - LS_FRAC + q))) >> (62 - LS_FRAC + q);
 }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// The cluster's barrier in its two halves and whole.  Its aligned form wants the warp's lanes together,
+// and behind stores by some of them, or a loop over a list, nothing else brings them there.
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    cluster_arrive();
+    cluster_wait();
+}
 __device__ __forceinline__ void remote_st_u64(uint64_t* p, uint32_t rank, uint64_t v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(map_rank(p, rank)), "l"(v) : "memory");
 }
@@ -157,7 +170,8 @@ __device__ __forceinline__ uint32_t remote_ld_u32(const uint32_t* p, uint32_t ra
 
 template <typename E>
 __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __grid_constant__ LsParams p) {
-    extern __shared__ __align__(16) float xs[];            // the slice
+    extern __shared__ __align__(16) uint8_t ls_smem[];
+    E* xs = reinterpret_cast<E*>(ls_smem);                 // the slice
     __shared__ uint32_t hist[LS_BINS], tot[LS_BINS];       // the slice's counts, the row's
     __shared__ uint64_t lists[2 * LS_LIST];
     uint64_t *list = lists, *weight = lists + LS_LIST;     // first CTA: entries of one bin
@@ -216,52 +230,64 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     cluster_arrive();                                          // this CTA has started, its counters are zero
 
     // ---- the slice, and its maximum (a NaN wins)
-    float mx = -INFINITY;
-    auto take = [&](float x) -> float {
-        x += 0.f;                                              // -0 is 0
-        asm("max.NaN.f32 %0, %1, %2;" : "=f"(mx) : "f"(mx), "f"(x));
-        return x;
+    // (read as numbers plus 0: -0 is 0)
+    auto at1 = [&](int i) -> float { return (float)xs[i] + 0.f; };
+    auto wide = [](const uint2& h) -> float4 {
+        return make_float4(__uint_as_float(h.x << 16) + 0.f, __uint_as_float(h.x & 0xffff0000u) + 0.f,
+                           __uint_as_float(h.y << 16) + 0.f, __uint_as_float(h.y & 0xffff0000u) + 0.f);
     };
+    auto at4 = [&](int i) -> float4 {                          // i a multiple of 4
+        if constexpr (sizeof(E) == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(xs + i);
+            return make_float4(v.x + 0.f, v.y + 0.f, v.z + 0.f, v.w + 0.f);
+        } else {
+            return wide(*reinterpret_cast<const uint2*>(xs + i));
+        }
+    };
+    float mx = -INFINITY;
+    auto take = [&](float x) { asm("max.NaN.f32 %0, %1, %2;" : "=f"(mx) : "f"(mx), "f"(x)); };
     {
         const E* src = static_cast<const E*>(p.logits) + row * p.V + x0;
-        if ((reinterpret_cast<uintptr_t>(src) & (4 * sizeof(E) - 1)) == 0) {
-            constexpr int U = 4;
-            for (int i = tid * 4; i < p.slice; i += LS_THREADS * 4 * U) {
-                float4 v[U];
+        if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+            // sixteen bytes at a time
+            constexpr int U = 4, VE = 16 / (int)sizeof(E);
+            for (int i = tid * VE; i < p.slice; i += LS_THREADS * VE * U) {
+                uint4 v[U];
 #pragma unroll
                 for (int y = 0; y < U; ++y) {
-                    const int e = i + y * LS_THREADS * 4;
-                    v[y] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-                    if (e + 4 <= n) {
-                        if constexpr (sizeof(E) == 4) {
-                            v[y] = __ldcs(reinterpret_cast<const float4*>(src + e));
-                        } else {
-                            const uint2 h = __ldcs(reinterpret_cast<const uint2*>(src + e));
-                            v[y] = make_float4(__uint_as_float(h.x << 16), __uint_as_float(h.x & 0xffff0000u),
-                                               __uint_as_float(h.y << 16), __uint_as_float(h.y & 0xffff0000u));
-                        }
-                    } else if (e < n) {
-                        v[y].x = (float)src[e];
-                        if (e + 1 < n) v[y].y = (float)src[e + 1];
-                        if (e + 2 < n) v[y].z = (float)src[e + 2];
-                    }
+                    const int e = i + y * LS_THREADS * VE;
+                    const uint32_t low = sizeof(E) == 4 ? 0xff800000u : 0xff80ff80u;     // -infinity
+                    v[y] = make_uint4(low, low, low, low);
+                    if (e + VE <= n) v[y] = __ldcs(reinterpret_cast<const uint4*>(src + e));
+                    else
+                        for (int z = 0; e + z < n; ++z) reinterpret_cast<E*>(&v[y])[z] = src[e + z];
                 }
 #pragma unroll
                 for (int y = 0; y < U; ++y) {
-                    const int e = i + y * LS_THREADS * 4;
-                    if (e < p.slice)
-                        *reinterpret_cast<float4*>(xs + e) = make_float4(take(v[y].x), take(v[y].y), take(v[y].z), take(v[y].w));
+                    const int e = i + y * LS_THREADS * VE;
+                    if (e < p.slice) {
+                        *reinterpret_cast<uint4*>(xs + e) = v[y];
+                        if constexpr (sizeof(E) == 4) {
+                            take(__uint_as_float(v[y].x)), take(__uint_as_float(v[y].y)), take(__uint_as_float(v[y].z)), take(__uint_as_float(v[y].w));
+                        } else {
+                            const float4 a = wide(make_uint2(v[y].x, v[y].y)), b2 = wide(make_uint2(v[y].z, v[y].w));
+                            take(a.x), take(a.y), take(a.z), take(a.w), take(b2.x), take(b2.y), take(b2.z), take(b2.w);
+                        }
+                    }
                 }
             }
         } else {
             constexpr int U = 8;
             for (int i = tid; i < p.slice; i += LS_THREADS * U) {
-                float v[U];
+                E v[U];
 #pragma unroll
-                for (int y = 0; y < U; ++y) v[y] = i + y * LS_THREADS < n ? (float)src[i + y * LS_THREADS] : -INFINITY;
+                for (int y = 0; y < U; ++y) v[y] = i + y * LS_THREADS < n ? src[i + y * LS_THREADS] : (E)(-INFINITY);
 #pragma unroll
                 for (int y = 0; y < U; ++y)
-                    if (i + y * LS_THREADS < p.slice) xs[i + y * LS_THREADS] = take(v[y]);
+                    if (i + y * LS_THREADS < p.slice) {
+                        xs[i + y * LS_THREADS] = v[y];
+                        take((float)v[y]);
+                    }
             }
         }
     }
@@ -272,7 +298,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             remote_st_u64(&peer[turn][0][me], tid, v0);
             remote_st_u64(&peer[turn][1][me], tid, v1);
         }
-        cluster_barrier_all();
+        cluster_sync();
         turn ^= 1;                                             // (read peer[turn ^ 1])
     };
     // Sums over the CTA: true in the first warp, which has them (and passes them on); part is
@@ -302,7 +328,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     // f(entry, its place in the slice) over the warp's entries, four at a time
     auto entries = [&](auto f) {
         for (int i = lane * 4; i < chunk; i += 128) {
-            const float4 v = *reinterpret_cast<const float4*>(xs + w0 + i);
+            const float4 v = at4(w0 + i);
             f(v.x, w0 + i);
             f(v.y, w0 + i + 1);
             f(v.z, w0 + i + 2);
@@ -317,7 +343,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (g + e * 128 < chunk) {
-                    const float4 v = *reinterpret_cast<const float4*>(xs + w0 + g + e * 128 + lane * 4);
+                    const float4 v = at4(w0 + g + e * 128 + lane * 4);
                     m |= (mark(v.x) ? 1u : 0u) << (4 * e) | (mark(v.y) ? 2u : 0u) << (4 * e) | (mark(v.z) ? 4u : 0u) << (4 * e) |
                          (mark(v.w) ? 8u : 0u) << (4 * e);
                 }
@@ -326,7 +352,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
                 if (m != 0u) {
                     const int e = __ffs(m) - 1, i = w0 + g + (e >> 2) * 128 + lane * 4 + (e & 3);
                     m &= m - 1u;
-                    f(xs[i], i);
+                    f(at1(i), i);
                 }
                 __syncwarp();
             }
@@ -351,10 +377,11 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             asm("max.NaN.f32 %0, %1, %2;" : "=f"(top) : "f"(top), "f"(y));
         }
     }
+    top += 0.f;
     if (!(fabsf(top) <= FLT_MAX)) {                            // NaN, infinity, or nothing above -infinity
         err = TV_ERR_BAD_VALUES;
         refuse();
-        cluster_barrier_all();                                 // (no CTA leaves while others write to it)
+        cluster_sync();                                 // (no CTA leaves while others write to it)
         return;
     }
     auto place = [&](int i) -> int { return x0 + i; };
@@ -405,7 +432,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
                 for (int r = 0; r < LS_CLUSTER_MAX; ++r) sum += got[r];
                 for (int r = 0; r < C; ++r) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(&tot[i], r)), "r"(sum) : "memory");
             }
-        cluster_barrier_all();
+        cluster_sync();
         uint32_t sum = 0u;
 #pragma unroll
         for (int e = 0; e < PER; ++e) sum += c[e] = tid * PER + e < to ? tot[tid * PER + e] : 0u;
@@ -441,7 +468,8 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         __syncthreads();
     };
     // The bin in which the mass reaches goal by the counts (up to k_bin, of which k_rank entries count), or
-    // LS_BINS; est: the mass before it, by the counts.  (The best entry weighs 1, not what its bin's
+    // LS_BINS; est: the mass before it, by the counts (of all bins, where it is none; every CTA has to
+    // come to the same bin, or some would leave while others still write to them).  (The best entry weighs 1, not what its bin's
     // middle does.)
     auto bin_of_mass = [&](float goal, int k_bin, uint32_t k_rank) -> int {
         float m[PER], ms = 0.f;
@@ -478,6 +506,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             if (tid * PER + e == found) est = at;
             at += m[e];
         }
+        if (found >= LS_BINS && tid == LS_THREADS - 1) est = at;
         __syncthreads();
         return found;
     };
@@ -517,26 +546,55 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     bool deferred = false;
     auto near_path = [&]() -> bool {
         if (!(use_k || use_p || min_p >= 3.1e-5f)) return false;
-        uint32_t small = 0u;
+        // counts of both reaches; without top-k the weights of the entries between them, and beyond, in 2^-34
+        // and 2^-38 of the largest: below 2^23 of them each, so rounded by adding 2^23
+        uint32_t between = 0u, beyond = 0u, many = 0u;
+#pragma unroll 1
+        for (int g = 0; g < chunk; g += 1024)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (g + e * 128 < chunk) {
+                    const float4 q = at4(w0 + g + e * 128 + lane * 4);
+                    const float y[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const float d = top - y[z], v = d * bin_scale;
+                        const bool is_near = v < (float)LS_NEAR, is_nearer = v < (float)LS_NEARER;
+                        many += (is_near ? 0x10000u : 0u) + (is_nearer ? 1u : 0u);
+                        if (!use_k && !is_nearer) {
+                            const float t = fmaf(d, cl, d * ch), s = is_near ? (float)(LS_FRAC - 8) : (float)(LS_FRAC - 4);
+                            const uint32_t w = __float_as_uint(ex2_approx(fmaxf(s - t, -126.f)) + 8388608.f) - __float_as_uint(8388608.f);
+                            between += is_near ? w : 0u;
+                            beyond += is_near ? 0u : w;
+                        }
+                    }
+                }
+        // (a thread has at most 96 entries, a CTA 49,152)
+        uint64_t v[2] = {(uint64_t)(many >> 16) << 32 | (many & 0xffffu), 0ull};
+        block_sum(v, 1);
+        exchange(v[0], 0ull);
+        uint64_t in_all = 0ull;
+        bool fits = true, fits_nearer = true;
+        for (int r = 0; r < C; ++r) {
+            const uint64_t a = peer[turn ^ 1][0][r];
+            const int room = p.defer ? min(LS_HEAVY, (min(p.slice, p.V - r * p.slice) - LS_HEAD) / 2) : LS_HEAVY;
+            in_all += a;
+            fits = fits && (int)(a >> 32) <= room;
+            fits_nearer = fits_nearer && (int)(a & 0xffffffffull) <= room;
+        }
+        fits = fits && (!p.defer || (uint32_t)(in_all >> 32) <= LS_ROW);
+        fits_nearer = fits_nearer && (!p.defer || (uint32_t)in_all <= LS_ROW);
+        if (!fits && (!fits_nearer || !(use_k || use_p || min_p >= 2.1e-4f))) return false;
+        const int reach = fits ? LS_NEAR : LS_NEARER;
 #pragma unroll 1
         for (int g = 0; g < chunk; g += 1024) {
             uint32_t marks = 0u;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (g + e * 128 < chunk) {
-                    const float4 q = *reinterpret_cast<const float4*>(xs + w0 + g + e * 128 + lane * 4);
-                    const float y[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const float d = top - y[z];
-                        const bool is_near = d * bin_scale < (float)LS_NEAR;
-                        marks |= is_near ? 1u << (4 * e + z) : 0u;
-                        if (!use_k && !is_near) {
-                            // in 2^-38 of the largest, below 2^23 of them: rounded by adding 2^23
-                            const float t = fmaf(d, cl, d * ch);
-                            small += __float_as_uint(ex2_approx(fmaxf((float)(LS_FRAC - 4) - t, -126.f)) + 8388608.f) - __float_as_uint(8388608.f);
-                        }
-                    }
+                    const float4 q = at4(w0 + g + e * 128 + lane * 4);
+                    marks |= ((top - q.x) * bin_scale < (float)reach ? 1u : 0u) << (4 * e) | ((top - q.y) * bin_scale < (float)reach ? 2u : 0u) << (4 * e) |
+                             ((top - q.z) * bin_scale < (float)reach ? 4u : 0u) << (4 * e) | ((top - q.w) * bin_scale < (float)reach ? 8u : 0u) << (4 * e);
                 }
             // places for the warp's entries by one atomic
             const uint32_t own = (uint32_t)__popc(marks);
@@ -551,10 +609,8 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             to = __shfl_sync(0xffffffffu, to, 31) + incl - own;
             for (; marks != 0u; marks &= marks - 1u, ++to) {
                 const int e = __ffs(marks) - 1, i = w0 + g + (e >> 2) * 128 + lane * 4 + (e & 3);
-                if (to < LS_HEAVY) {
-                    near_x[to] = xs[i];
-                    near_i[to] = (uint16_t)i;
-                }
+                near_x[to] = at1(i);
+                near_i[to] = (uint16_t)i;
             }
         }
         __syncthreads();
@@ -562,14 +618,15 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         // this thread's entries: keys, bins, weights
         uint64_t wt[4], key[4];
         int bin[4];
-        uint64_t v[2] = {0ull, small};
+        v[0] = 0ull;
+        v[1] = ((uint64_t)beyond << 4) + (fits ? 0ull : (uint64_t)between << 8);
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
             const int e = tid + y * LS_THREADS;
             wt[y] = 0ull;
             key[y] = ~0ull;
             bin[y] = LS_BINS;
-            if (e < (int)held && held <= LS_HEAVY) {
+            if (e < (int)held) {
                 const float x = near_x[e];
                 key[y] = ls_key(x, place(near_i[e]));
                 bin[y] = bin_of(x);
@@ -578,31 +635,25 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
                 if (!p.defer) atomicAdd(&hist[bin[y]], 1u);
             }
         }
-        // the weights' sum; how many, and the sum of the others
-        const bool fits = held <= LS_HEAVY && (!p.defer || LS_HEAD + 2 * (int)held <= n);
+        // the weights' sums, of these and of the others
         block_sum(v, 2);
-        exchange(v[0], v[1] << 16 | (fits ? held : 0xffffu));
+        exchange(v[0], v[1]);
         uint64_t mass_near = 0ull, mass_all = 0ull;
-        uint32_t held_all = 0u;
-        bool over = false;
         for (int r = 0; r < C; ++r) {
-            const uint64_t a = peer[turn ^ 1][1][r];
             mass_near += peer[turn ^ 1][0][r];
-            mass_all += (a >> 16) << 4;
-            over = over || (a & 0xffffull) == 0xffffull;
-            held_all += (uint32_t)(a & 0xffffull);
+            mass_all += peer[turn ^ 1][1][r];
         }
         mass_all += mass_near;
-        if (over) return false;
+        const uint32_t held_all = fits ? (uint32_t)(in_all >> 32) : (uint32_t)in_all;
         if (p.defer) {
             // the second kernel takes it from here, if the near entries hold all that may be kept
-            if (held_all > LS_ROW || (use_k ? held_all < (uint32_t)k : use_p && ls_part<true>(top_p, mass_all) > mass_near)) return false;
+            if (use_k ? held_all < (uint32_t)k : use_p && ls_part<true>(top_p, mass_all) > mass_near) return false;
             uint32_t* dump = reinterpret_cast<uint32_t*>(out);
             const uint64_t mine = peer[turn ^ 1][1][me];
             if (tid == 0) {
                 dump[0] = held;
-                dump[1] = (uint32_t)(mine >> 16);
-                dump[2] = (uint32_t)(mine >> 48);
+                dump[1] = (uint32_t)mine;
+                dump[2] = (uint32_t)(mine >> 32);
                 dump[3] = __float_as_uint(top);
                 if (me == 0) p.status[row] = LS_PENDING;
             }
@@ -626,7 +677,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         int k_bin = LS_BINS - 1;
         uint32_t k_rank = (uint32_t)p.V;
         if (use_k || use_p) {
-            const uint32_t counted = sum_bins(0, LS_NEAR);
+            const uint32_t counted = sum_bins(0, reach);
             if (use_k) {
                 if (counted < (uint32_t)k) return false;
                 bin_of_rank((uint32_t)k);
@@ -636,9 +687,9 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
 #pragma unroll
                 for (int y = 0; y < 4; ++y)
                     if (bin[y] == k_bin) to_list(2, key[y]);
-                cluster_barrier_all();
+                cluster_sync();
                 if (me == 0) rank_list(2, 0, false, k_rank - 1u, 0ull, 0ull);
-                cluster_barrier_all();
+                cluster_sync();
                 cut = result[0];
             }
         }
@@ -652,7 +703,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             }
             const uint64_t need = ls_part<true>(top_p, mass_all);
             int guess = bin_of_mass((float)need * 2.2737368e-13f, k_bin, k_rank);
-            if (guess >= LS_NEAR) {
+            if (guess >= reach) {
                 if (!use_k) return false;
                 guess = k_bin;
             }
@@ -674,11 +725,11 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
                 if (v[0] < need && need <= v[0] + v[1]) break;
                 __syncthreads();
                 guess = next_bin(guess, (float)need * 2.2737368e-13f, (float)v[0] * 2.2737368e-13f, need <= v[0], k_bin, k_rank);
-                if (guess < 0 || guess > min(k_bin, LS_NEAR - 1)) return false;
-                cluster_barrier_all();                         // (the next entries go where these are)
+                if (guess < 0 || guess > min(k_bin, reach - 1)) return false;
+                cluster_sync();                         // (the next entries go where these are)
             }
             if (me == 0) rank_list(3 + tries, 1, true, 0ull, v[0], need);
-            cluster_barrier_all();
+            cluster_sync();
             cut = min(cut, result[1]);
         }
         // ---- the mass that is left, and where the draw falls
@@ -763,7 +814,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             for (int w2 = 0; w2 < warp; ++w2) before += part[0][w2];
             if (want > before && want <= before + mine)
                 for (int i = 0; i < chunk; i += 32) {
-                    const uint32_t m = __ballot_sync(0xffffffffu, ls_bits(xs[w0 + i + lane]) == lo && place(w0 + i + lane) < p.V);
+                    const uint32_t m = __ballot_sync(0xffffffffu, ls_bits(at1(w0 + i + lane)) == lo && place(w0 + i + lane) < p.V);
                     const int here = __popc(m);
                     if (want <= before + here) {
                         const int at = __fns(m, 0, (int)(want - before));
@@ -773,9 +824,9 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
                     before += here;
                 }
         }
-        cluster_barrier_all();
+        cluster_sync();
         const uint64_t found = result[2];
-        cluster_barrier_all();                                 // (read before it is written again)
+        cluster_sync();                                 // (read before it is written again)
         return found;
     };
     // The entries of a bin (up to `limit`) in the first CTA's list, ranked there.
@@ -786,9 +837,9 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             const uint64_t key = ls_key(x, place(i));
             if (key <= limit) to_list(which, key);
         });
-        cluster_barrier_all();
+        cluster_sync();
         if (me == 0) rank_list(which, which, mass, rank, base, need);
-        cluster_barrier_all();
+        cluster_sync();
         return result[which];
     };
     // ---- Otherwise: over the whole row.
@@ -801,7 +852,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     if (use_k || use_p) {
         // adds the bins from .. to - 1 of the slice to the row's counts
         auto count = [&](int from, int to) {
-            cluster_barrier_all();
+            cluster_sync();
             return sum_bins(from, to);
         };
         // the entries that weigh 2^-16 or more; in the same pass, without top-k, the sum of all weights
@@ -915,7 +966,8 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     const float most_t = min_p > 0.f ? fminf((float)(LS_FRAC + 1), 0.001f - log2f(min_p)) : (float)(LS_FRAC + 1);
     auto maybe = [&](float x) -> bool { return x >= cut_x && (top - x) * ch < most_t; };
     uint64_t v[2] = {0ull, 0ull};
-    marked(maybe, [&](float x, int i) { v[0] += kept(x, i); });
+    if (cut == ~0ull && min_p == 0.f) entries([&](float x, int) { v[0] += weigh(x); });
+    else marked(maybe, [&](float x, int i) { v[0] += kept(x, i); });
     uint64_t mine = v[0];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
@@ -935,7 +987,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
 #pragma unroll 1
             for (int i = 0; i < chunk; i += 128) {
                 // four entries of a lane, in order
-                const float4 x = *reinterpret_cast<const float4*>(xs + w0 + i + lane * 4);
+                const float4 x = at4(w0 + i + lane * 4);
                 const bool some = maybe(x.x) || maybe(x.y) || maybe(x.z) || maybe(x.w);
                 if (!__any_sync(0xffffffffu, some)) continue;
                 const float y[4] = {x.x, x.y, x.z, x.w};
@@ -979,7 +1031,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         if ((reinterpret_cast<uintptr_t>(out) & 15) == 0) {
 #pragma unroll 2
             for (int i = tid * 4; i < n; i += LS_THREADS * 4) {
-                const float4 x = *reinterpret_cast<const float4*>(xs + i);
+                const float4 x = at4(i);
                 const float4 y = make_float4(prob(x.x, i), prob(x.y, i + 1), prob(x.z, i + 2), prob(x.w, i + 3));
                 if (i + 4 <= n) {
                     __stcs(reinterpret_cast<float4*>(out + i), y);
@@ -990,7 +1042,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
                 }
             }
         } else {
-            for (int i = tid; i < n; i += LS_THREADS) out[i] = prob(xs[i], i);
+            for (int i = tid; i < n; i += LS_THREADS) out[i] = prob(at1(i), i);
         }
     }
 }
@@ -1044,7 +1096,7 @@ __global__ void __launch_bounds__(LR_THREADS, 2) logits_sample_rows_kernel(const
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
         if (lane <= LS_CLUSTER_MAX) first[lane] = incl - mine;
-        if (lane == 0) others = rest << 4;
+        if (lane == 0) others = rest;
     }
     const float top = __uint_as_float(dump[3]);
     __syncthreads();
@@ -1271,20 +1323,16 @@ template <typename E>
 tv_status launch_sample(const LsParams& q, int64_t rows, cudaStream_t stream) {
     LsParams p = q;
     auto fn = logits_sample_kernel<E>;
-    const int fewest = (p.V + LS_SLICE - 1) / LS_SLICE;
-    int C;
-    if (fewest > LS_CLUSTER_MAX) {
-        C = LS_CLUSTER_MAX;
-    } else {
-        // few rows: more CTAs per row, while they have a few thousand entries each
-        C = fewest;
-        while (C * 2 <= LS_CLUSTER_MAX && rows * C * 2 <= 2 * device_sm_count() && p.V > C * 2 * LS_STEP) C *= 2;
-    }
+    constexpr int SLICE = LS_SLICE_BYTES / (int)sizeof(E);
+    const int fewest = (p.V + SLICE - 1) / SLICE;
+    // few rows: more CTAs per row, while they have a few thousand entries each
+    int C = std::min(fewest, LS_CLUSTER_MAX);
+    while (C * 2 <= LS_CLUSTER_MAX && rows * C * 2 <= 2 * device_sm_count() && p.V > C * 2 * LS_STEP) C *= 2;
     p.ctas = C;
     p.slice = ((p.V + C - 1) / C + LS_STEP - 1) / LS_STEP * LS_STEP;
     if (p.slice > LS_SLICE_MAX) return TV_ERR_UNSUPPORTED;
     if (rows * C > 0x7fffffff) return TV_ERR_UNSUPPORTED;
-    const size_t smem = (size_t)p.slice * sizeof(float);
+    const size_t smem = (size_t)p.slice * sizeof(E);
     static std::atomic<bool> set[64], set_rows[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TV_ERR_CUDA;
