@@ -44,7 +44,8 @@ constexpr int LS_SLICE_MAX = 49152;          // longer rows: one CTA per SM
 constexpr int LS_BINS = 2048;
 constexpr float LS_BIN = 64.f;               // bins per unit of (max - x) / T
 // Bins of the first count: near entries weigh 2^-16 or more, or 2^-12 where those are too many.
-constexpr int LS_NEAR = 704, LS_NEARER = 544;
+constexpr int LS_NEAR = 680, LS_NEARER = 544;
+static_assert(LS_NEAR % 2 == 0 && LS_NEAR * 12 <= LS_BINS * 4, "counts and masses of the near bins in a histogram's room");
 constexpr float LS_SMALL = 19.f;             // weights below 2^-19 enter the sum of all in float32
 constexpr int LS_LIST = 1024;
 constexpr int LS_HEAVY = 4 * LS_THREADS;     // near entries that a CTA's threads hold
@@ -162,6 +163,11 @@ __device__ __forceinline__ uint32_t remote_add_u32(uint32_t* p, uint32_t rank, u
     asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(r) : "r"(map_rank(p, rank)), "r"(v) : "memory");
     return r;
 }
+__device__ __forceinline__ uint64_t remote_ld_u64(const unsigned long long* p, uint32_t rank) {
+    uint64_t r;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(r) : "r"(map_rank(p, rank)) : "memory");
+    return r;
+}
 __device__ __forceinline__ uint32_t remote_ld_u32(const uint32_t* p, uint32_t rank) {
     uint32_t r;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(r) : "r"(map_rank(p, rank)) : "memory");
@@ -180,11 +186,12 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     __shared__ uint64_t peer[2][2][LS_CLUSTER_MAX];        // per CTA, two exchanges in turn
     __shared__ uint32_t held_n, kept_n;
     __shared__ uint64_t result[3];                         // of the first CTA, of a bisection
+    __shared__ uint64_t plan[2], before_pick, upto;        // bins that the first CTA looks into
     // the near entries, where the lists come later (a barrier of the cluster on)
     float* near_x = reinterpret_cast<float*>(lists);
     uint16_t* near_i = reinterpret_cast<uint16_t*>(near_x + LS_HEAVY);
     static_assert(LS_HEAVY * 6 <= sizeof(lists) && LS_HEAVY <= 2 * LS_LIST, "near entries");
-    __shared__ uint32_t list_n[3 + LS_TRIES];
+    __shared__ uint32_t list_n[4];
     __shared__ uint32_t pick[2];                           // a bin, entries before it
     __shared__ float fpart[LS_WARPS], est;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     const int x0 = me * p.slice, n = max(0, min(p.slice, p.V - x0));
     const int chunk = p.slice / LS_WARPS, w0 = warp * chunk;   // a warp's entries
     if (tid < 64) table[tid] = LS_TABLE[tid];
-    if (tid < 3 + LS_TRIES) list_n[tid] = 0u;
+    if (tid < 4) list_n[tid] = 0u;
     if (tid < 3) result[tid] = ~0ull;
     if (tid == 0) held_n = kept_n = 0u;
     for (int i = tid; i < LS_BINS; i += LS_THREADS) hist[i] = 0u;
@@ -249,24 +256,18 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     {
         const E* src = static_cast<const E*>(p.logits) + row * p.V + x0;
         if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-            // sixteen bytes at a time
+            // sixteen bytes at a time, the end by entries
             constexpr int U = 4, VE = 16 / (int)sizeof(E);
-            for (int i = tid * VE; i < p.slice; i += LS_THREADS * VE * U) {
+            const int full = n & ~(VE - 1);
+            for (int i = tid * VE; i < full; i += LS_THREADS * VE * U) {
                 uint4 v[U];
 #pragma unroll
-                for (int y = 0; y < U; ++y) {
-                    const int e = i + y * LS_THREADS * VE;
-                    const uint32_t low = sizeof(E) == 4 ? 0xff800000u : 0xff80ff80u;     // -infinity
-                    v[y] = make_uint4(low, low, low, low);
-                    if (e + VE <= n) v[y] = __ldcs(reinterpret_cast<const uint4*>(src + e));
-                    else
-                        for (int z = 0; e + z < n; ++z) reinterpret_cast<E*>(&v[y])[z] = src[e + z];
-                }
+                for (int y = 0; y < U; ++y)
+                    if (i + y * LS_THREADS * VE < full) v[y] = __ldcs(reinterpret_cast<const uint4*>(src + i + y * LS_THREADS * VE));
 #pragma unroll
-                for (int y = 0; y < U; ++y) {
-                    const int e = i + y * LS_THREADS * VE;
-                    if (e < p.slice) {
-                        *reinterpret_cast<uint4*>(xs + e) = v[y];
+                for (int y = 0; y < U; ++y)
+                    if (i + y * LS_THREADS * VE < full) {
+                        *reinterpret_cast<uint4*>(xs + i + y * LS_THREADS * VE) = v[y];
                         if constexpr (sizeof(E) == 4) {
                             take(__uint_as_float(v[y].x)), take(__uint_as_float(v[y].y)), take(__uint_as_float(v[y].z)), take(__uint_as_float(v[y].w));
                         } else {
@@ -274,7 +275,11 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
                             take(a.x), take(a.y), take(a.z), take(a.w), take(b2.x), take(b2.y), take(b2.z), take(b2.w);
                         }
                     }
-                }
+            }
+            for (int i = full + tid; i < p.slice; i += LS_THREADS) {
+                const E x = i < n ? src[i] : (E)(-INFINITY);
+                xs[i] = x;
+                take((float)x);
             }
         } else {
             constexpr int U = 8;
@@ -616,6 +621,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         __syncthreads();
         const uint32_t held = held_n;
         // this thread's entries: keys, bins, weights
+        auto masses = [](uint32_t* counts) { return reinterpret_cast<unsigned long long*>(counts + LS_NEAR); };
         uint64_t wt[4], key[4];
         int bin[4];
         v[0] = 0ull;
@@ -632,7 +638,10 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
                 bin[y] = bin_of(x);
                 wt[y] = weigh(x);
                 v[0] += wt[y];
-                if (!p.defer) atomicAdd(&hist[bin[y]], 1u);
+                if (!p.defer && (use_k || use_p)) {
+                    atomicAdd(&hist[bin[y]], 1u);
+                    atomicAdd(&masses(hist)[bin[y]], (unsigned long long)wt[y]);
+                }
             }
         }
         // the weights' sums, of these and of the others
@@ -645,9 +654,10 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         }
         mass_all += mass_near;
         const uint32_t held_all = fits ? (uint32_t)(in_all >> 32) : (uint32_t)in_all;
+        // (not where the near entries do not hold all that may be kept)
+        if (use_k ? held_all < (uint32_t)k : use_p && ls_part<true>(top_p, mass_all) > mass_near) return false;
         if (p.defer) {
-            // the second kernel takes it from here, if the near entries hold all that may be kept
-            if (use_k ? held_all < (uint32_t)k : use_p && ls_part<true>(top_p, mass_all) > mass_near) return false;
+            // the second kernel takes it from here
             uint32_t* dump = reinterpret_cast<uint32_t*>(out);
             const uint64_t mine = peer[turn ^ 1][1][me];
             if (tid == 0) {
@@ -674,63 +684,161 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             deferred = true;
             return true;
         }
-        int k_bin = LS_BINS - 1;
-        uint32_t k_rank = (uint32_t)p.V;
         if (use_k || use_p) {
-            const uint32_t counted = sum_bins(0, reach);
-            if (use_k) {
-                if (counted < (uint32_t)k) return false;
-                bin_of_rank((uint32_t)k);
-                k_bin = (int)pick[0];
-                k_rank = (uint32_t)k - pick[1];
-                if (tot[k_bin] > LS_LIST) return false;
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    if (bin[y] == k_bin) to_list(2, key[y]);
-                cluster_sync();
-                if (me == 0) rank_list(2, 0, false, k_rank - 1u, 0ull, 0ull);
-                cluster_sync();
-                cut = result[0];
-            }
-        }
-        if (use_p) {
-            if (use_k) {
-                v[0] = 0ull;
-#pragma unroll
-                for (int y = 0; y < 4; ++y) v[0] += key[y] <= cut ? wt[y] : 0ull;
-                cluster_sum(v, 1);
-                mass_all = v[0];
-            }
-            const uint64_t need = ls_part<true>(top_p, mass_all);
-            int guess = bin_of_mass((float)need * 2.2737368e-13f, k_bin, k_rank);
-            if (guess >= reach) {
-                if (!use_k) return false;
-                guess = k_bin;
-            }
-            int tries = 0;
-            for (;; ++tries) {
-                if (tries == LS_TRIES || tot[guess] > LS_LIST) return false;
-                v[0] = v[1] = 0ull;
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    if (key[y] <= cut && bin[y] <= guess) {
-                        if (bin[y] == guess) {
-                            v[1] += wt[y];
-                            to_list(3 + tries, key[y]);
-                        } else {
-                            v[0] += wt[y];
-                        }
-                    }
-                cluster_sum(v, 2);
-                if (v[0] < need && need <= v[0] + v[1]) break;
+            // The first CTA sums the counts and masses, says which bin it needs, ranks that bin's entries,
+            // and (top-p below the bin that top-k cuts) another one's.
+            uint32_t c0 = 0u, c1 = 0u, c_before = 0u;
+            uint64_t m0 = 0ull, m1 = 0ull, m_before = 0ull;
+            auto pick_mass = [&](uint64_t goal) {              // before <= goal < up to it
+                if (m_before <= goal && goal < m_before + m0) {
+                    pick[0] = 2 * tid;
+                    before_pick = m_before;
+                } else if (m_before + m0 <= goal && goal < m_before + m0 + m1) {
+                    pick[0] = 2 * tid + 1;
+                    before_pick = m_before + m0;
+                }
                 __syncthreads();
-                guess = next_bin(guess, (float)need * 2.2737368e-13f, (float)v[0] * 2.2737368e-13f, need <= v[0], k_bin, k_rank);
-                if (guess < 0 || guess > min(k_bin, reach - 1)) return false;
-                cluster_sync();                         // (the next entries go where these are)
+            };
+            // the key with rank `rank` among the list's, or (mass) of the last one up to `limit` that begins below
+            // need; upto: the list's mass up to it
+            auto rank_of = [&](int m, bool by_mass, uint32_t rank, uint64_t base, uint64_t need, uint64_t limit) {
+                for (int e = tid; e < m; e += LS_THREADS) {
+                    const uint64_t k0 = list[e], w = weight[e];
+                    uint32_t nb = 0u;
+                    uint64_t before = 0ull;
+#pragma unroll 4
+                    for (int f = 0; f < m; ++f)
+                        if (list[f] < k0) {
+                            ++nb;
+                            before += weight[f];
+                        }
+                    if (by_mass ? k0 <= limit && base + before < need && base + before + w >= need : nb == rank) {
+                        result[2] = k0;
+                        upto = before + w;
+                    }
+                }
+                __syncthreads();
+            };
+            auto weights_of_list = [&](int which) -> int {
+                const int m = (int)list_n[which];
+                for (int e = tid; e < m; e += LS_THREADS) weight[e] = weigh(value_of(list[e]));
+                __syncthreads();
+                return m;
+            };
+            uint32_t k_rank = 0u;
+            uint64_t base = 0ull;
+            if (me == 0) {
+                for (int i = tid; i < reach; i += LS_THREADS) {
+                    uint32_t got[LS_CLUSTER_MAX], sum = 0u;
+                    uint64_t more[LS_CLUSTER_MAX], mass = 0ull;
+#pragma unroll
+                    for (int r = 0; r < LS_CLUSTER_MAX; ++r) {
+                        got[r] = r < C ? remote_ld_u32(&hist[i], r) : 0u;
+                        more[r] = r < C ? remote_ld_u64(&masses(hist)[i], r) : 0ull;
+                    }
+#pragma unroll
+                    for (int r = 0; r < LS_CLUSTER_MAX; ++r) {
+                        sum += got[r];
+                        mass += more[r];
+                    }
+                    tot[i] = sum;
+                    masses(tot)[i] = mass;
+                }
+                __syncthreads();
+                // two bins per thread
+                if (2 * tid < reach) {
+                    c0 = tot[2 * tid], c1 = tot[2 * tid + 1];
+                    m0 = masses(tot)[2 * tid], m1 = masses(tot)[2 * tid + 1];
+                }
+                uint32_t ci = c0 + c1;
+                uint64_t mi = m0 + m1;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t y = __shfl_up_sync(0xffffffffu, ci, o);
+                    const uint64_t z = __shfl_up_sync(0xffffffffu, mi, o);
+                    if (lane >= o) {
+                        ci += y;
+                        mi += z;
+                    }
+                }
+                if (lane == 31) {
+                    part[0][warp] = mi;
+                    part[1][warp] = ci;
+                }
+                __syncthreads();
+                c_before = ci - c0 - c1;
+                m_before = mi - m0 - m1;
+                for (int w = 0; w < warp; ++w) {
+                    m_before += part[0][w];
+                    c_before += (uint32_t)part[1][w];
+                }
+                if (use_k) {
+                    const uint32_t want = (uint32_t)k;
+                    if (c_before < want && want <= c_before + c0) {
+                        pick[0] = 2 * tid;
+                        pick[1] = want - c_before - 1u;
+                        before_pick = m_before;
+                    } else if (c_before + c0 < want && want <= c_before + c0 + c1) {
+                        pick[0] = 2 * tid + 1;
+                        pick[1] = want - c_before - c0 - 1u;
+                        before_pick = m_before + m0;
+                    }
+                    __syncthreads();
+                    k_rank = pick[1];
+                } else {
+                    pick_mass(ls_part<true>(top_p, mass_all) - 1ull);
+                }
+                base = before_pick;
+                if (tid < C) remote_st_u64(&plan[0], tid, tot[pick[0]] > LS_LIST ? ~0ull : (uint64_t)pick[0]);
             }
-            if (me == 0) rank_list(3 + tries, 1, true, 0ull, v[0], need);
             cluster_sync();
-            cut = min(cut, result[1]);
+            if (plan[0] == ~0ull) return false;
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if (bin[y] == (int)plan[0]) to_list(2, key[y]);
+            cluster_sync();
+            if (me == 0) {
+                const int m = weights_of_list(2);
+                uint64_t limit = ~0ull, then = ~0ull - 1ull;
+                if (use_k) {
+                    rank_of(m, false, k_rank, 0ull, 0ull, ~0ull);
+                    limit = result[2];
+                }
+                if (use_p) {
+                    const uint64_t need = ls_part<true>(top_p, use_k ? base + upto : mass_all);
+                    __syncthreads();
+                    if (!use_k || need > base) {
+                        rank_of(m, true, 0u, base, need, limit);
+                        limit = result[2];
+                    } else {
+                        pick_mass(need - 1ull);
+                        then = tot[pick[0]] > LS_LIST ? ~0ull : (uint64_t)pick[0];
+                        upto = need;
+                    }
+                }
+                if (tid < C) {
+                    remote_st_u64(&result[0], tid, limit);
+                    remote_st_u64(&plan[1], tid, then);
+                }
+            }
+            cluster_sync();
+            cut = result[0];
+            if (plan[1] == ~0ull) return false;
+            if (plan[1] != ~0ull - 1ull) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    if (bin[y] == (int)plan[1]) to_list(3, key[y]);
+                cluster_sync();
+                if (me == 0) {
+                    const int m = weights_of_list(3);
+                    const uint64_t need = upto;
+                    __syncthreads();
+                    rank_of(m, true, 0u, before_pick, need, ~0ull);
+                    if (tid < C) remote_st_u64(&result[1], tid, result[2]);
+                }
+                cluster_sync();
+                cut = min(cut, result[1]);
+            }
         }
         // ---- the mass that is left, and where the draw falls
         v[0] = 0ull;
@@ -846,7 +954,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     auto whole_path = [&]() {
     __syncthreads();
     for (int i = tid; i < LS_BINS; i += LS_THREADS) hist[i] = 0u;
-    if (tid < 2) result[tid] = ~0ull;
+    if (tid < 3) result[tid] = ~0ull;
     __syncthreads();
     cut = ~0ull;
     if (use_k || use_p) {
