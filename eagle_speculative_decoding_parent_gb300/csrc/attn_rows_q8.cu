@@ -131,6 +131,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// l 2^d.  A maximum has the logarithm of V's scale in it, a sum has not: it can be as small as 2^-200 of
+// what the maxima say.
+__device__ __forceinline__ float times_exp2(float l, float d) {
+    const float h = exp2f(0.5f * d);
+    return l * h * h;
+}
+
 template <int D, int NT, bool CAP>
 __global__ void __launch_bounds__(RQ_THREADS, RqShape<NT>::PER_SM)
 rows_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -313,12 +320,21 @@ rows_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     lim[j][0] = lim[j][1] = -INFINITY;
                     l[j][0] = l[j][1] = 0.f;
                 }
+                // V's scales of this window lie far below the largest so far, some of them
+                int ev_top = -127;
+                auto far = [&](const Win& w) -> bool {
+                    const bool in = wk * 32 + lane < steps;
+                    ev_top = max(ev_top, __reduce_max_sync(0xffffffffu, in ? (int)w.ev : -127));
+                    return __reduce_min_sync(0xffffffffu, in ? (int)w.ev : 128) < ev_top - 60;
+                };
+                bool mixed = far(cur);
                 int i = 0;
 #pragma unroll 1
                 for (; i < steps; ++i) {
                     if ((i & 31) == 0 && i > 0) {
                         cur = nxt;
                         wk = i >> 5;
+                        mixed = far(cur);
                         if (steps > (wk + 1) * 32) {
                             ids(wk + 1);
                             nxt = win();
@@ -366,7 +382,8 @@ rows_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     const int v0 = (lo + warp + i * RQ_WARPS) * 16, key0 = key_of(v0);
                     const bool edge = !(v0 < front ? v0 + 16 <= p.sinks
                                                    : key0 >= first_all && key0 + 15 <= s.P + i0 - (p.mask ? i0 + 1 : 0));
-                    bool need = false;
+                    bool need = mixed;
+                    float lsc = exp2f(-ev - RQ_BIAS);          // V's scale and the bias out of the sum
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
                         const float f0 = ks * fac[j][0], f1 = ks * fac[j][1];
@@ -413,16 +430,24 @@ rows_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                                 nb[j][e] -= by;
                                 sc[j][e] -= by;
                                 sc[j][e + 2] -= by;
-                                l[j][e] *= f;
+                                l[j][e] = none ? 0.f : times_exp2(l[j][e], -by);
 #pragma unroll
                                 for (int t = 0; t < KS; ++t) {
                                     o[j][t][e] *= f;
                                     o[j][t][e + 2] *= f;
                                 }
                             }
+                        if (mixed && ev < ev_top - 60.f) {
+                            // beside a block of much larger values (one of zeros has the smallest scale) the
+                            // weights vanish with V's scale in them, but not from the sum
+#pragma unroll
+                            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) l[j][e & 1] += ex2_approx(sc[j][e] - (ev + RQ_BIAS));
+                            lsc = 0.f;
+                        }
                     }
                     uint32_t pb[NT][2];
-                    const float lsc = exp2f(-ev - RQ_BIAS);    // V's scale and the bias out of the sum
                     float pw[NT][4];
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
@@ -551,9 +576,9 @@ rows_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int w = 0; w < RQ_WARPS; ++w) {
-                        const float f = exp2f(sm_m[w][rr] - bz);
+                        const float f = exp2f(sm_m[w][rr] - bz), part = times_exp2(sm_l[w][rr], sm_m[w][rr] - bz);
                         const float4 y = *reinterpret_cast<const float4*>(so + (w * ROWS + rr) * D + c);
-                        den = fmaf(f, sm_l[w][rr], den);
+                        den += part;
                         acc.x = fmaf(f, y.x, acc.x);
                         acc.y = fmaf(f, y.y, acc.y);
                         acc.z = fmaf(f, y.z, acc.z);
@@ -655,12 +680,12 @@ __global__ void __launch_bounds__(RQ_JOIN_THREADS) rows_q8_join_kernel(const __g
                 const float4 y = __ldcg(reinterpret_cast<const float4*>(sl + rr * D + c));
                 const float mm = fmaxf(mx, mk), bz = mm == -INFINITY ? 0.f : mm;
                 const float f = exp2f(mx - bz), w = exp2f(mk - bz);
-                mx = mm;
-                den = fmaf(w, lk, den * f);
+                den = times_exp2(lk, mk - bz) + (mx == -INFINITY ? 0.f : times_exp2(den, mx - bz));
                 acc.x = fmaf(w, y.x, acc.x * f);
                 acc.y = fmaf(w, y.y, acc.y * f);
                 acc.z = fmaf(w, y.z, acc.z * f);
                 acc.w = fmaf(w, y.w, acc.w * f);
+                mx = mm;
             }
             if (!more) break;
             slot = ahead;

@@ -20,7 +20,9 @@
  * Beside them: growing the tree (draft_tree_expand), writing its K/V rows
  * (tree_kv_append), the prompts and plainly decoded tokens of the same cache
  * (chunk_kv_append, chunk_attention), and what the model's rows go through before
- * acceptance reads them (tree_logits_process, token_counts_update).
+ * acceptance reads them (tree_logits_process, token_counts_update).  The same cache in
+ * 8 bits, for prompts, decoded tokens and trees alike (chunk_kv_append_q8,
+ * chunk_attention_q8, kv_compact_q8), and the sampling of rows (logits_sample).
  *
  * Conventions shared by all calls
  * -------------------------------
@@ -540,8 +542,9 @@ tv_status chunk_attention(const void* q, int64_t q_stride, const void* k_cache,
  * bias 7, three of mantissa; subnormals; no infinities, 0x7f and 0xff are NaN), laid
  * out like the other caches: [num_blocks][Hkv][block_size][d] bytes.  Each block of
  * each kv head has a scale, k_scale and v_scale float32 [num_blocks][Hkv], and a code
- * stands for code * scale.  Scales are powers of two (of any other number the
- * exponent alone counts; zero is zero), so that what a code stands for is a bfloat16
+ * stands for code * scale.  Scales are powers of two from 2^-100 on, as
+ * chunk_kv_append_q8 writes them (of any other number the exponent alone counts, and
+ * smaller ones may count as 2^-100), so that what a code stands for is a bfloat16
  * number exactly, and a code moves to a larger scale without rounding until it falls
  * below the smallest normal code (2^-6).  block_size is a multiple of 16; d is 64 or
  * 128; queries, new keys and values and outputs are bfloat16.  Half the bytes of the
@@ -596,7 +599,10 @@ tv_status chunk_kv_append_q8(const void* q, int64_t q_stride, const void* k, int
  * of its tree, as tree_mask_build writes them for trees of n_b nodes) or NULL; with
  * it n_b is at most 64, and there is no window.
  * A row without a key is zero; one whose every score is -infinity is NaN.
- * Float32 accumulation and softmax; the weights are rounded to bfloat16.
+ * Float32 accumulation and softmax.  Besides their order, what is rounded: the weights,
+ * to bfloat16 or (few rows per sequence: those below 2^-27 of a row's largest weight x
+ * scale of V by 2^-38 of that) float16; with d = 128, elements of a query row below 2^-10 of
+ * its largest, to steps of 2^-17 of that.
  * status int32 [B]: as chunk_attention (with sinks, the blocks of the first sinks
  * positions are needed too), and TV_ERR_OUT_OF_RANGE for more than 64 rows with a
  * mask.  Cache contents outside K reach no row, NaN included.
@@ -723,8 +729,9 @@ tv_status tree_logits_process(const void* logits, tv_dtype dt, int B, int N, int
  *   probs[b][i][x] = w_x / (the sum W of the kept ones), 0 for the others
  *   tokens[b][i] = the smallest x with w_0 + .. + w_x (kept ones) > uniform[b][i] * W
  * The w of 1 and 2 and the sums are in fixed point, steps of 2^-42, each w off by at
- * most 2^-38 of itself and half a step: cuts and tokens differ from the exact ones only
- * where a sum comes that near to its border.  probs are float32, off by at most 2^-20
+ * most 2^-38 of itself and half a step (one below 2^-19, in the sum over a whole row, by
+ * 2^-18 of itself): cuts and tokens differ from the exact ones only where a sum comes
+ * that near to its border.  probs are float32, off by at most 2^-20
  * of themselves and of the exponent's rounding, 2^-23 (logit - largest) / temperature.
  * temperature, top_p, min_p float32 [B], top_k int32 [B]: each may be NULL (1; 1; 0; all).
  * uniform float32 [B][N], in [0, 1): the random numbers are the caller's.  probs float32
