@@ -125,8 +125,8 @@ struct Lay {
     static constexpr bool K8 = E8 && D == 128;
     static constexpr int SLOTS = K8 ? 2 : (E8 ? 3 : 5) * (128 / D);
     static constexpr int RAW_BYTES = KT * D;
-    static constexpr int RAWS = K8 ? 4 : E8 ? 4 * (128 / D) : 0;
-    static constexpr int KSLOTS = K8 ? 2 : 0;
+    static constexpr int RAWS = K8 ? 2 : E8 ? 4 * (128 / D) : 0;
+    static constexpr int KSLOTS = K8 ? 4 : 0;
     static constexpr int KEXPS = 8;                        // tiles of K whose scales are kept
     static constexpr int Q_BYTES = MT * D * 2;             // one row tile
     static constexpr int OFF_RING = 0;
@@ -483,18 +483,16 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 // Bytes that are NaN codes, as their top bits (no carries: a byte is at most 0x7f + 1).
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
 
-// Warp 9 of an 8-bit kernel: the pages' codes by bulk copies (a page's rows of one head lie
+// Warp 9 of the 8-bit kernel for d = 64: the pages' codes by bulk copies (a page's rows of one head lie
 // beside each other) into a ring, in the order in which the products take the tiles.  The
 // pages' scales follow two tiles later, so that their loads (behind the block ids') hold up no
 // copy: a byte each, and an arrival of their own on the tile's barrier.
 template <class L, int D, class Take>
-__device__ __forceinline__ void load_codes(const Params& p, const CUtensorMap& kmap, uint8_t* smem, uint64_t* rfull,
-                                           uint64_t* rempty, uint64_t* kfull, uint64_t* kempty,
+__device__ __forceinline__ void load_codes(const Params& p, uint8_t* smem, uint64_t* rfull, uint64_t* rempty,
                                            volatile int* abort_flag, Take& take, bool& alive) {
     constexpr int PAGE = 16 * D, WT = 32 / (KT / 16);      // tiles of a window of 32 pages, a lane each
     const int lane = threadIdx.x & 31;
-    uint32_t ld = 0, slot = 0, ph = 0;                     // K8: V's
-    uint32_t kld = 0, kslot = 0, kph = 0, ksent = 0;       // K8: K's; scales sent
+    uint32_t ld = 0, slot = 0, ph = 0;
     Item it;
     for (uint32_t k = 0; alive && take(k, it); ++k) {
         if (it.n == 0) continue;
@@ -532,16 +530,6 @@ __device__ __forceinline__ void load_codes(const Params& p, const CUtensorMap& k
             const bool now = j / WT == wk;
             const uint32_t mine = is_v ? exponent_byte(now ? vs : pvs) : exponent_byte(now ? ks : pks);
             const uint32_t e = __shfl_sync(0xffffffffu, mine, (j % WT) * (KT / 16) + (lane & 7));
-            if constexpr (L::K8) {
-                if (!is_v) {
-                    if (lane < 8) smem[L::OFF_EXP + (L::RAWS + ksent % L::KEXPS) * 8 + lane] = (uint8_t)e;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&kfull[ksent % L::KSLOTS]);
-                    __syncwarp();
-                    ++ksent;
-                    return;
-                }
-            }
             if (lane < 8) smem[L::OFF_EXP + sent * 8 + lane] = (uint8_t)e;
             __syncwarp();
             if (lane == 0) mbar_arrive(&rfull[sent]);
@@ -566,22 +554,6 @@ __device__ __forceinline__ void load_codes(const Params& p, const CUtensorMap& k
             }
             const int pages = min(KT / 16, (vend - (it.t_lo + j) * KT + 15) >> 4);
             const int y = __shfl_sync(0xffffffffu, w == wk ? row : prow, (j % WT) * (KT / 16) + (lane & 7));
-            if constexpr (L::K8) {
-                if (!is_v) {
-                    alive = wait_all<64>(&kempty[kslot], kph ^ 1u);
-                    if (!alive) break;
-                    mbar_arrive_expect_tx_relaxed_elect(&kfull[kslot], (uint32_t)pages * PAGE);
-                    if (lane < pages)
-                        tma_load_2d(smem + L::OFF_K + kslot * L::RAW_BYTES + lane * PAGE, &kmap, &kfull[kslot], 0, y, policy);
-                    __syncwarp();
-                    ++kld;
-                    if (++kslot == L::KSLOTS) {
-                        kslot = 0;
-                        kph ^= 1u;
-                    }
-                    continue;
-                }
-            }
             alive = wait_all<64>(&rempty[slot], ph ^ 1u);
             if (!alive) break;
             mbar_arrive_expect_tx_relaxed_elect(&rfull[slot], (uint32_t)pages * PAGE);
@@ -602,9 +574,85 @@ __device__ __forceinline__ void load_codes(const Params& p, const CUtensorMap& k
     // copies in flight end before the CTA does
     for (uint32_t u = ld > (uint32_t)L::RAWS ? ld - L::RAWS : 0; u < ld; ++u)
         wait_own(&rfull[u % L::RAWS], (u / L::RAWS) & 1u);
-    if constexpr (L::K8)
-        for (uint32_t u = kld > (uint32_t)L::KSLOTS ? kld - L::KSLOTS : 0; u < kld; ++u)
-            wait_own(&kfull[u % L::KSLOTS], (u / L::KSLOTS) & 1u);
+}
+
+// d = 128: K and V have rings of their own, so a warp each: warp 9 loads K, and an item's queries
+// before it; warp 10 loads V.  A tile's scales follow its copies by one tile.  (Four slots of K and two
+// of V's codes, which are widened as they come: 32 trees of 26 nodes 88 us, two and four 91.)
+template <class L, int D, bool V, class Take, class Before, class Last>
+__device__ __forceinline__ void load_stream(const Params& p, const CUtensorMap& kmap, uint8_t* smem, uint64_t* filled,
+                                            uint64_t* freed, volatile int* abort_flag, Take& take, bool& alive, Before before,
+                                            Last last) {
+    constexpr int PAGE = 16 * D, WT = 32 / (KT / 16), RING = V ? L::RAWS : L::KSLOTS, EXPS = V ? L::RAWS : L::KEXPS;
+    constexpr int OFF = V ? L::OFF_RAW : L::OFF_K, EXP = L::OFF_EXP + (V ? 0 : L::RAWS * 8);
+    const int lane = threadIdx.x & 31;
+    const float* scales = V ? p.v_scale : p.k_scale;
+    uint32_t ld = 0, slot = 0, ph = 0, sslot = 0, sexp = 0;
+    Item it;
+    for (uint32_t k = 0; alive && take(k, it); ++k) {
+        if (it.n == 0) continue;
+        const uint64_t policy = it.ntok == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+        const int32_t* table = p.c.table + (int64_t)it.b * p.c.max_blocks;
+        const int vend = it.hi - it.kbase;
+        // a window's block ids (32 pages, a lane each) are loaded two windows ahead, its scales one
+        struct Ids { int blk, off; };
+        auto ids = [&](int w) -> Ids {
+            const int v = (it.t_lo + w * WT) * KT + lane * 16;
+            if (w * WT >= it.n || v >= vend) return Ids{0, 0};
+            const int key = item_key(it, v);
+            return Ids{__ldg(table + key / p.c.bs), key % p.c.bs};
+        };
+        auto scale = [&](const Ids& i) { return __ldg(scales + (int64_t)i.blk * p.Hkv + it.g); };
+        Ids i0 = ids(0), i1 = ids(1), i2 = ids(2);
+        if (!before(it)) break;
+        float sc = scale(i0), nsc = 0.f;
+        if (it.n > WT) nsc = scale(i1);
+        int row = (i0.blk * p.Hkv + it.g) * p.c.bs + i0.off;
+        auto send = [&](int j, float from) {
+            const uint32_t e = __shfl_sync(0xffffffffu, exponent_byte(from), (j % WT) * (KT / 16) + (lane & 7));
+            if (lane < 8) smem[EXP + sexp * 8 + lane] = (uint8_t)e;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&filled[sslot]);
+            __syncwarp();
+            if (++sexp == EXPS) sexp = 0;
+            if (++sslot == RING) sslot = 0;
+        };
+        int j = 0;
+#pragma unroll 1
+        for (; j < it.n; ++j) {
+            if (j > 0) send(j - 1, sc);
+            if (j % WT == 0 && j > 0) {
+                row = (i1.blk * p.Hkv + it.g) * p.c.bs + i1.off;
+                sc = nsc;
+                i1 = i2;
+                if (it.n > j + WT) nsc = scale(i1);
+                i2 = ids(j / WT + 2);
+            }
+            const int pages = min(KT / 16, (vend - (it.t_lo + j) * KT + 15) >> 4);
+            const int y = __shfl_sync(0xffffffffu, row, (j % WT) * (KT / 16) + (lane & 7));
+            alive = wait_all<64>(&freed[slot], ph ^ 1u);
+            if (!alive) break;
+            mbar_arrive_expect_tx_relaxed_elect(&filled[slot], (uint32_t)pages * PAGE);
+            if (lane < pages) {
+                uint8_t* dst = smem + OFF + slot * L::RAW_BYTES + lane * PAGE;
+                if constexpr (V) bulk_load(dst, static_cast<const uint8_t*>(p.v) + (int64_t)y * D, PAGE, &filled[slot], policy);
+                else tma_load_2d(dst, &kmap, &filled[slot], 0, y, policy);
+            }
+            __syncwarp();
+            ++ld;
+            if (++slot == RING) {
+                slot = 0;
+                ph ^= 1u;
+            }
+        }
+        // (after a timeout no tile under way is without its scales)
+        const bool go = !alive || last(it);
+        if (j == it.n) send(it.n - 1, sc);
+        if (!go) break;
+    }
+    if (!alive && lane == 0) *abort_flag = 1;
+    // copies in flight end before the CTA does
+    for (uint32_t u = ld > (uint32_t)RING ? ld - RING : 0; u < ld; ++u) wait_own(&filled[u % RING], (u / RING) & 1u);
 }
 
 // Row r of the item's query tiles (d = 128), bfloat16, into two e4m3 parts in its place: scaled by
@@ -1010,6 +1058,36 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         return alive && !(it.flags & ITEM_END);
     };
 
+    // Warp 10 (K8: warp 9): an item's query tiles.
+    uint32_t qi = 0, xi = 0;
+    auto load_q = [&](const Item& it) -> bool {
+        const bool two = (it.flags & ITEM_TWO) != 0;
+        alive = wait_all(qempty, (qi & 1u) ^ 1u);
+        // the second Q tile also serves the epilogues of single row tiles before
+        if (alive && two && xi > 0) alive = wait_all(xdone, (xi - 1) & 1u);
+        if (!alive) return false;
+        ++qi;
+        const int nq = two ? 2 : 1;
+        const uint64_t qpol = l2_policy_evict_first();
+        mbar_arrive_expect_tx_relaxed_elect(qfull, (uint32_t)(nq * L::HALVES * 128 * p.G * p.npt));
+        for (int t = 0; t < nq; ++t)
+            for (int hf = 0; hf < L::HALVES; ++hf)
+                tma_load_3d_elect(smem + L::OFF_Q + t * L::Q_BYTES + hf * (MT * 128), &qmap, qfull, hf * 64,
+                                  it.g * p.G, it.row0 + t * p.npt, qpol);
+        xi += (L::K8 && !two) ? 1 : 0;
+        return true;
+    };
+    // The second Q tile's use by the epilogue of a single row tile: one outstanding at most, or the
+    // barrier's phases could not be told apart.  (K8: warp 10, before the last tile of V is released,
+    // without which there is no epilogue.)
+    auto single = [&](const Item& it) -> bool {
+        if ((it.flags & ITEM_TWO) != 0) return true;
+        if (xi > 0) alive = wait_all(xdone, (xi - 1) & 1u);
+        if (!alive) return false;
+        ++xi;
+        return true;
+    };
+
     if (warp == SCHED_WARP) {
         // ============================== scheduler ==============================
         uint32_t k = 0;
@@ -1098,9 +1176,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         // ============================ K/V producer ============================
         if constexpr (E8) {
             if constexpr (L::K8) {
-                if (lane == 0) tma_prefetch_desc(&kmap);
+                if (lane == 0) {
+                    tma_prefetch_desc(&kmap);
+                    tma_prefetch_desc(&qmap);
+                }
+                load_stream<L, D, false>(p, kmap, smem, kfull, kempty, abort_flag, take, alive, load_q, [](const Item&) { return true; });
+                if (!alive && lane == 0) *abort_flag = 1;
+                if (qi > 0) wait_own(qfull, (qi - 1) & 1u);
+            } else {
+                load_codes<L, D>(p, smem, rfull, rempty, abort_flag, take, alive);
             }
-            load_codes<L, D>(p, kmap, smem, rfull, rempty, kfull, kempty, abort_flag, take, alive);
         } else {
         if (lane == 0) {
             tma_prefetch_desc(&kmap);
@@ -1353,31 +1438,17 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         wait_own(drain, 0);
     } else if (warp == FIX_WARP) {
         // ==================== Q tiles, V rows that must not reach O ====================
+        if constexpr (L::K8) {
+            load_stream<L, D, true>(p, kmap, smem, rfull, rempty, abort_flag, take, alive, [](const Item&) { return true; }, single);
+        } else {
         if (lane == 0) tma_prefetch_desc(&qmap);
-        const uint64_t qpol = l2_policy_evict_first();
-        uint32_t ld = 0, qi = 0, xi = 0, ph = 0;             // ph: vraw's parity per slot
+        uint32_t ld = 0, ph = 0;                              // ph: vraw's parity per slot
         Item it;
         for (uint32_t k = 0; alive && take(k, it); ++k) {
             if (it.n == 0) continue;
             const int n = it.n;
             const bool two = (it.flags & ITEM_TWO) != 0;
-            alive = wait_all(qempty, (qi & 1u) ^ 1u);
-            // the second Q tile also serves the epilogues of single row tiles before
-            if (alive && two && xi > 0) alive = wait_all(xdone, (xi - 1) & 1u);
-            if (!alive) break;
-            ++qi;
-            const int nq = two ? 2 : 1;
-            mbar_arrive_expect_tx_relaxed_elect(qfull, (uint32_t)(nq * L::HALVES * 128 * p.G * p.npt));
-            for (int t = 0; t < nq; ++t)
-                for (int hf = 0; hf < L::HALVES; ++hf)
-                    tma_load_3d_elect(smem + L::OFF_Q + t * L::Q_BYTES + hf * (MT * 128), &qmap, qfull, hf * 64,
-                                      it.g * p.G, it.row0 + t * p.npt, qpol);
-            if (!two) {
-                // one use outstanding at most, or the barrier's phases could not be told apart
-                if (xi > 0) alive = wait_all(xdone, (xi - 1) & 1u);
-                if (!alive) break;
-                ++xi;
-            }
+            if (!load_q(it) || !single(it)) break;
             if constexpr (E8) continue;                        // (the V rows are looked at where they are widened)
             // ring position of V(j): two row tiles K0 V0 K1 V1 ..., one K0 K1 V0 K2 V1 ... V(n-1)
             auto v_at = [&](int j) -> uint32_t { return ld + (two || j == n - 1 ? 2 * j + 1 : 2 * j + 2); };
@@ -1439,6 +1510,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         }
         if (!alive && lane == 0) *abort_flag = 1;
         if (qi > 0) wait_own(qfull, (qi - 1) & 1u);          // its own copies in flight
+        }
     } else {
         // ============================== softmax ==============================
         const int i = warp >> 2;                              // stream
@@ -1780,11 +1852,92 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 }
                 fence_proxy_async_smem();  // the next Q tile may land where xo was
                 all_x(1);
+            } else if (L::K8 && join) {
+                // A thread per row and half of the columns, 16 at a time: each stream hands over what it
+                // has of the other's half (xo: [stream][row][column], the maxima and sums behind).  Few
+                // instructions: they are fetched for the occasion.
+                constexpr int PITCH = 20;
+                float4* to = reinterpret_cast<float4*>(xo + (i * MT + row) * PITCH);
+                const float4* from = reinterpret_cast<const float4*>(xo + ((i ^ 1) * MT + row) * PITCH);
+                float* stats = xo + 2 * MT * PITCH + row;
+                if (wrows) {
+                    stats[i * 2 * MT] = m_used;
+                    stats[i * 2 * MT + MT] = l;
+                }
+                float w0 = 1.f, w1 = 0.f;
+#pragma unroll 1
+                for (int c = i * (D / 2); c < (i + 1) * (D / 2); c += 16) {
+                    uint32_t r[16];
+                    if (wrows) {
+                        tmem_ld16(tO + (c ^ (D / 2)), r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            reinterpret_cast<uint4*>(to)[e] = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+                    }
+                    all_x(0);
+                    if (wrows) {
+                        if (c == i * (D / 2)) {
+                            const float m1 = stats[(i ^ 1) * 2 * MT], l1 = stats[(i ^ 1) * 2 * MT + MT];
+                            const float mm = fmaxf(m_used, m1), bz = mm == -INFINITY ? 0.f : mm;
+                            w0 = exp2f(m_used - bz);
+                            w1 = exp2f(m1 - bz);
+                            l = w0 * l + w1 * l1;
+                            m_used = mm;
+                            if (!pslot) {
+                                w0 /= l;
+                                w1 /= l;
+                            }
+                        }
+                        tmem_ld16(tO + c, r);
+                        tmem_wait_ld();
+                        const uint64_t a = f2_pack(w0, w0), b2 = f2_pack(w1, w1);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 y = from[e];
+                            float x0, x1, x2, x3;
+                            f2_unpack(f2_fma(b2, f2_pack(y.x, y.y), f2_mul(a, f2_pack(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1])))), x0, x1);
+                            f2_unpack(f2_fma(b2, f2_pack(y.z, y.w), f2_mul(a, f2_pack(__uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3])))), x2, x3);
+                            r[4 * e] = __float_as_uint(x0), r[4 * e + 1] = __float_as_uint(x1);
+                            r[4 * e + 2] = __float_as_uint(x2), r[4 * e + 3] = __float_as_uint(x3);
+                        }
+                        tmem_st16(tO + c, r);
+                        tmem_wait_st();
+                    }
+                    fence_proxy_async_smem();
+                    all_x(1);
+                }
+                // (written behind the exchange: an arrival would wait for the stores before it)
+#pragma unroll 1
+                for (int c = i * (D / 2); wrows && c < (i + 1) * (D / 2); c += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(tO + c, r);
+                    tmem_wait_ld();
+                    if (mine && pslot) {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4)
+                            reinterpret_cast<uint4*>(pslot)[(c + e) / 4 * p.prows + row] = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+                    } else if (mine) {
+                        uint4* dst = reinterpret_cast<uint4*>(p.out + (int64_t)(it.row0 + tok) * p.o_stride + (int64_t)(it.g * p.G + head) * D + c);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 8) {
+                            uint32_t u[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                u[x] = pack_bf16x2(__uint_as_float(r[e + 2 * x]), __uint_as_float(r[e + 2 * x + 1]));
+                            dst[e / 8] = make_uint4(u[0], u[1], u[2], u[3]);
+                        }
+                    }
+                }
+                if (wrows && mine && pslot && i == 0) {
+                    pslot[p.prows * D + row] = m_used;
+                    pslot[p.prows * (D + 1) + row] = l;
+                }
+                o_read();
             } else {
                 // a thread per row; stream 1 of a single row tile hands its rows over, 32 columns at
                 // a time (xo: [column][row])
                 const int prow = (two ? i * MT : 0) + row;
-                const bool writes = (two || i == 0) && wrows;
                 // Four lanes exchange their rows' 16-byte pieces, so that they write 64 bytes of one
                 // row together: a store of 16 bytes of 32 rows takes 32 cycles, of 64 bytes of 8 rows 8.
                 const uint64_t orow = reinterpret_cast<uint64_t>(p.out + (int64_t)(it.row0 + tok) * p.o_stride +
@@ -1794,6 +1947,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 for (int x = 0; x < 4; ++x) prow4[x] = __shfl_sync(0xffffffffu, orow, (lane & ~3) + x) + 16 * ((lane & 3) - x);
                 const uint32_t valid = __ballot_sync(0xffffffffu, mine) >> (lane & ~3);
                 float w0 = 1.f, w1 = 0.f, inv = 0.f;
+                const bool writes = (two || i == 0) && wrows;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t r[32];
