@@ -27,6 +27,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "tv_device.cuh"
 #include "tv_internal.h"
@@ -43,15 +44,20 @@ constexpr int LS_SLICE_BYTES = 65536;        // of a row per CTA, two CTAs per S
 constexpr int LS_SLICE_MAX = 49152;          // longer rows: one CTA per SM
 constexpr int LS_BINS = 2048;
 constexpr float LS_BIN = 64.f;               // bins per unit of (max - x) / T
-// Bins of the first count: near entries weigh 2^-16 or more, or 2^-12 where those are too many.
-constexpr int LS_NEAR = 680, LS_NEARER = 544;
+// Reaches of the near entries, in bins: those within 6, 7.5, 9.25 and 10.6 of the maximum (the last
+// weigh 2^-15.3 of the first or more).
+constexpr int LS_REACHES = 4;
+constexpr int LS_NEARER = 592, LS_NEAR = 680;
+__device__ constexpr int ls_reach(int j) { return j == 0 ? 384 : j == 1 ? 480 : j == 2 ? LS_NEARER : LS_NEAR; }
 static_assert(LS_NEAR % 2 == 0 && LS_NEAR * 12 <= LS_BINS * 4, "counts and masses of the near bins in a histogram's room");
 constexpr float LS_SMALL = 19.f;             // weights below 2^-19 enter the sum of all in float32
 constexpr int LS_LIST = 1024;
-constexpr int LS_HEAVY = 4 * LS_THREADS;     // near entries that a CTA's threads hold
+constexpr int LS_HEAVY = 6144;               // near entries of a CTA (fewer beside the longest slices)
+constexpr int LS_STATIC = 34 * 1024, LS_SHARED = 227 * 1024;   // other shared memory, all that there is
+constexpr int LS_FEW = 4 * LS_THREADS;       // so many that what is kept of them is put into order
 constexpr int LS_TRIES = 4;
-// Rows left to logits_sample_rows_kernel: at most so many near entries, dumped behind a header of so
-// many words into the slices' part of the distribution; the status that says so.
+// Rows left to logits_sample_rows_kernel, which holds at most so many near entries (more of them are
+// read again for each use): dumped behind a header of so many words into the slices' part of the distribution; the status that says so.
 constexpr int LS_ROW = 8192;
 constexpr int LS_HEAD = 8;
 constexpr int32_t LS_PENDING = -0x5eed;
@@ -90,6 +96,7 @@ struct LsParams {
     int32_t* status;
     int N, V, slice, ctas;   // ctas: of a row
     int64_t rows, ahead;     // ahead: rows that the GPU holds at once
+    int heavy;               // near entries of a CTA
     bool defer;              // distributions of many rows: the near entries to the second kernel
 };
 
@@ -187,10 +194,8 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     __shared__ uint32_t held_n, kept_n;
     __shared__ uint64_t result[3];                         // of the first CTA, of a bisection
     __shared__ uint64_t plan[2], before_pick, upto;        // bins that the first CTA looks into
-    // the near entries, where the lists come later (a barrier of the cluster on)
-    float* near_x = reinterpret_cast<float*>(lists);
-    uint16_t* near_i = reinterpret_cast<uint16_t*>(near_x + LS_HEAVY);
-    static_assert(LS_HEAVY * 6 <= sizeof(lists) && LS_HEAVY <= 2 * LS_LIST, "near entries");
+    uint16_t* near_i = reinterpret_cast<uint16_t*>(ls_smem + (size_t)p.slice * sizeof(E));   // places of the near entries
+    static_assert(LS_FEW <= 2 * LS_LIST, "what is kept of few entries in the lists' room");
     __shared__ uint32_t list_n[4];
     __shared__ uint32_t pick[2];                           // a bin, entries before it
     __shared__ float fpart[LS_WARPS], est;
@@ -549,48 +554,71 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
     // ---- Where all that may be kept weighs 2^-16 or more, and few entries do: those are compacted, and a
     // thread holds up to four with their weights.
     bool deferred = false;
-    auto near_path = [&]() -> bool {
-        if (!(use_k || use_p || min_p >= 3.1e-5f)) return false;
-        // counts of both reaches; without top-k the weights of the entries between them, and beyond, in 2^-34
-        // and 2^-38 of the largest: below 2^23 of them each, so rounded by adding 2^23
+    // Says what is left to do: nothing, the draw, or all of it.
+    enum { DONE, DRAW, ALL };
+    auto near_path = [&]() -> int {
+        if (!(use_k || use_p || min_p > 0.f)) return ALL;
+        // The entries within each reach, a byte for each (a thread has at most 96 entries).  For top-p of the
+        // whole row also the weights of the entries between the last two and beyond, in 2^-34 and 2^-38
+        // of the largest: below 2^23 of them each, so rounded by adding 2^23.
+        const bool weights = use_p && !use_k;
         uint32_t between = 0u, beyond = 0u, many = 0u;
+        if (weights) {
 #pragma unroll 1
-        for (int g = 0; g < chunk; g += 1024)
+            for (int g = 0; g < chunk; g += 1024)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (g + e * 128 < chunk) {
-                    const float4 q = at4(w0 + g + e * 128 + lane * 4);
-                    const float y[4] = {q.x, q.y, q.z, q.w};
+                for (int e = 0; e < 8; ++e)
+                    if (g + e * 128 < chunk) {
+                        const float4 q = at4(w0 + g + e * 128 + lane * 4);
+                        const float y[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const float d = top - y[z], v = d * bin_scale;
-                        const bool is_near = v < (float)LS_NEAR, is_nearer = v < (float)LS_NEARER;
-                        many += (is_near ? 0x10000u : 0u) + (is_nearer ? 1u : 0u);
-                        if (!use_k && !is_nearer) {
-                            const float t = fmaf(d, cl, d * ch), s = is_near ? (float)(LS_FRAC - 8) : (float)(LS_FRAC - 4);
-                            const uint32_t w = __float_as_uint(ex2_approx(fmaxf(s - t, -126.f)) + 8388608.f) - __float_as_uint(8388608.f);
-                            between += is_near ? w : 0u;
-                            beyond += is_near ? 0u : w;
+                        for (int z = 0; z < 4; ++z) {
+                            const float d = top - y[z], v = d * bin_scale;
+                            const bool is_near = v < (float)LS_NEAR, is_nearer = v < (float)LS_NEARER;
+                            many += (is_near ? 1u << 24 : 0u) + (is_nearer ? 1u << 16 : 0u);
+                            if (!is_nearer) {
+                                const float t = fmaf(d, cl, d * ch), s = is_near ? (float)(LS_FRAC - 8) : (float)(LS_FRAC - 4);
+                                const uint32_t w = __float_as_uint(ex2_approx(fmaxf(s - t, -126.f)) + 8388608.f) - __float_as_uint(8388608.f);
+                                between += is_near ? w : 0u;
+                                beyond += is_near ? 0u : w;
+                            }
                         }
                     }
-                }
-        // (a thread has at most 96 entries, a CTA 49,152)
-        uint64_t v[2] = {(uint64_t)(many >> 16) << 32 | (many & 0xffffu), 0ull};
+        } else {
+            // (most entries are beyond the last: the others are marked and looked at by themselves)
+            marked([&](float x) { return (top - x) * bin_scale < (float)LS_NEAR; },
+                   [&](float x, int) {
+                       const float t = (top - x) * bin_scale;
+#pragma unroll
+                       for (int j = 0; j < LS_REACHES; ++j) many += t < (float)ls_reach(j) ? 1u << (8 * j) : 0u;
+                   });
+        }
+        // (a CTA has less than 2^16 entries)
+        uint64_t v[2] = {(uint64_t)(many & 0xffu) | (uint64_t)(many & 0xff00u) << 8 | (uint64_t)(many & 0xff0000u) << 16 |
+                             (uint64_t)(many >> 24) << 48, 0ull};
         block_sum(v, 1);
         exchange(v[0], 0ull);
-        uint64_t in_all = 0ull;
-        bool fits = true, fits_nearer = true;
-        for (int r = 0; r < C; ++r) {
-            const uint64_t a = peer[turn ^ 1][0][r];
-            const int room = p.defer ? min(LS_HEAVY, (min(p.slice, p.V - r * p.slice) - LS_HEAD) / 2) : LS_HEAVY;
-            in_all += a;
-            fits = fits && (int)(a >> 32) <= room;
-            fits_nearer = fits_nearer && (int)(a & 0xffffffffull) <= room;
+        // The reach: the smallest with which the near entries hold all that may be kept, if there is room for
+        // them; for top-p of the whole row the largest with room.
+        int reach = 0;
+        bool few = true, enough = false;
+        for (int j = weights ? 2 : 0; j < LS_REACHES; ++j) {
+            uint32_t sum = 0u;
+            bool room = true, small = true;
+            for (int r = 0; r < C; ++r) {
+                const int a = (int)(peer[turn ^ 1][0][r] >> (16 * j)) & 0xffff;
+                room = room && a <= (p.defer ? min(p.heavy, (min(p.slice, p.V - r * p.slice) - LS_HEAD) / 2) : p.heavy);
+                small = small && a <= LS_FEW;
+                sum += (uint32_t)a;
+            }
+            if (!room) break;
+            reach = ls_reach(j);
+            few = small;
+            enough = weights || (use_k ? sum >= (uint32_t)k : min_p >= 1.01f * ex2_approx((float)reach * (-1.4427f / LS_BIN)));
+            if (enough && !weights) break;
         }
-        fits = fits && (!p.defer || (uint32_t)(in_all >> 32) <= LS_ROW);
-        fits_nearer = fits_nearer && (!p.defer || (uint32_t)in_all <= LS_ROW);
-        if (!fits && (!fits_nearer || !(use_k || use_p || min_p >= 2.1e-4f))) return false;
-        const int reach = fits ? LS_NEAR : LS_NEARER;
+        if (!enough) return ALL;
+        const bool fits = reach == LS_NEAR;
 #pragma unroll 1
         for (int g = 0; g < chunk; g += 1024) {
             uint32_t marks = 0u;
@@ -613,37 +641,28 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             if (lane == 31) to = atomicAdd(&held_n, incl);
             to = __shfl_sync(0xffffffffu, to, 31) + incl - own;
             for (; marks != 0u; marks &= marks - 1u, ++to) {
-                const int e = __ffs(marks) - 1, i = w0 + g + (e >> 2) * 128 + lane * 4 + (e & 3);
-                near_x[to] = at1(i);
-                near_i[to] = (uint16_t)i;
+                const int e = __ffs(marks) - 1;
+                near_i[to] = (uint16_t)(w0 + g + (e >> 2) * 128 + lane * 4 + (e & 3));
             }
         }
         __syncthreads();
         const uint32_t held = held_n;
-        // this thread's entries: keys, bins, weights
         auto masses = [](uint32_t* counts) { return reinterpret_cast<unsigned long long*>(counts + LS_NEAR); };
-        uint64_t wt[4], key[4];
-        int bin[4];
+        auto each_near = [&](auto f) {                         // f(entry, its place in the slice)
+#pragma unroll 1
+            for (int e = tid; e < (int)held; e += LS_THREADS) f(at1(near_i[e]), (int)near_i[e]);
+        };
         v[0] = 0ull;
         v[1] = ((uint64_t)beyond << 4) + (fits ? 0ull : (uint64_t)between << 8);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const int e = tid + y * LS_THREADS;
-            wt[y] = 0ull;
-            key[y] = ~0ull;
-            bin[y] = LS_BINS;
-            if (e < (int)held) {
-                const float x = near_x[e];
-                key[y] = ls_key(x, place(near_i[e]));
-                bin[y] = bin_of(x);
-                wt[y] = weigh(x);
-                v[0] += wt[y];
-                if (!p.defer && (use_k || use_p)) {
-                    atomicAdd(&hist[bin[y]], 1u);
-                    atomicAdd(&masses(hist)[bin[y]], (unsigned long long)wt[y]);
-                }
+        each_near([&](float x, int) {
+            const uint64_t w = weigh(x);
+            v[0] += w;
+            if (!p.defer && (use_k || use_p)) {
+                const int bin = bin_of(x);
+                atomicAdd(&hist[bin], 1u);
+                atomicAdd(&masses(hist)[bin], (unsigned long long)w);
             }
-        }
+        });
         // the weights' sums, of these and of the others
         block_sum(v, 2);
         exchange(v[0], v[1]);
@@ -653,9 +672,8 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             mass_all += peer[turn ^ 1][1][r];
         }
         mass_all += mass_near;
-        const uint32_t held_all = fits ? (uint32_t)(in_all >> 32) : (uint32_t)in_all;
         // (not where the near entries do not hold all that may be kept)
-        if (use_k ? held_all < (uint32_t)k : use_p && ls_part<true>(top_p, mass_all) > mass_near) return false;
+        if (weights && ls_part<true>(top_p, mass_all) > mass_near) return ALL;
         if (p.defer) {
             // the second kernel takes it from here
             uint32_t* dump = reinterpret_cast<uint32_t*>(out);
@@ -668,7 +686,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
                 if (me == 0) p.status[row] = LS_PENDING;
             }
             for (int e = tid; e < (int)held; e += LS_THREADS) {
-                dump[LS_HEAD + 2 * e] = __float_as_uint(near_x[e]);
+                dump[LS_HEAD + 2 * e] = __float_as_uint(at1(near_i[e]));
                 dump[LS_HEAD + 2 * e + 1] = (uint32_t)place(near_i[e]);
             }
             const int from = LS_HEAD + 2 * (int)held;
@@ -682,7 +700,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
                 for (int i = from + tid; i < n; i += LS_THREADS) out[i] = 0.f;
             }
             deferred = true;
-            return true;
+            return DONE;
         }
         if (use_k || use_p) {
             // The first CTA sums the counts and masses, says which bin it needs, ranks that bin's entries,
@@ -792,10 +810,10 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
                 if (tid < C) remote_st_u64(&plan[0], tid, tot[pick[0]] > LS_LIST ? ~0ull : (uint64_t)pick[0]);
             }
             cluster_sync();
-            if (plan[0] == ~0ull) return false;
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-                if (bin[y] == (int)plan[0]) to_list(2, key[y]);
+            if (plan[0] == ~0ull) return ALL;
+            each_near([&](float x, int i) {
+                if (bin_of(x) == (int)plan[0]) to_list(2, ls_key(x, place(i)));
+            });
             cluster_sync();
             if (me == 0) {
                 const int m = weights_of_list(2);
@@ -823,11 +841,11 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             }
             cluster_sync();
             cut = result[0];
-            if (plan[1] == ~0ull) return false;
+            if (plan[1] == ~0ull) return ALL;
             if (plan[1] != ~0ull - 1ull) {
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    if (bin[y] == (int)plan[1]) to_list(3, key[y]);
+                each_near([&](float x, int i) {
+                    if (bin_of(x) == (int)plan[1]) to_list(3, ls_key(x, place(i)));
+                });
                 cluster_sync();
                 if (me == 0) {
                     const int m = weights_of_list(3);
@@ -840,13 +858,15 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
                 cut = min(cut, result[1]);
             }
         }
+        if (!few) return DRAW;
         // ---- the mass that is left, and where the draw falls
+        auto kept = [&](float x, int i) -> uint64_t {
+            if (ls_key(x, place(i)) > cut) return 0ull;
+            const uint64_t w = weigh(x);
+            return w >= least ? w : 0ull;
+        };
         v[0] = 0ull;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            if (key[y] > cut || wt[y] < least) wt[y] = 0ull;
-            v[0] += wt[y];
-        }
+        each_near([&](float x, int i) { v[0] += kept(x, i); });
         block_sum(v, 1);
         exchange(v[0], 0ull);
         uint64_t before = 0ull;
@@ -857,9 +877,10 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         const uint64_t goal = ls_part<false>(u, all);
         if (goal >= before && goal < before + peer[turn ^ 1][0][me]) {
             // in this CTA: what it keeps in a list, (place in the slice, weight) in a word each
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-                if (wt[y] != 0ull) lists[atomicAdd(&kept_n, 1u)] = (uint64_t)((uint32_t)key[y] - (uint32_t)x0) << 44 | wt[y];
+            each_near([&](float x, int i) {
+                const uint64_t w = kept(x, i);
+                if (w != 0ull) lists[atomicAdd(&kept_n, 1u)] = (uint64_t)i << 44 | w;
+            });
             __syncthreads();
             const int m = (int)kept_n;
             for (int e = tid; e < m; e += LS_THREADS) {
@@ -876,7 +897,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
                 }
             }
         }
-        return true;
+        return DONE;
     };
     // The cut of a run of entries that no list holds, by bisection over the logits' bits: the
     // first key with which count entries, or a mass above before, are kept (`kept` entries count).
@@ -951,7 +972,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         return result[which];
     };
     // ---- Otherwise: over the whole row.
-    auto whole_path = [&]() {
+    auto whole_cut = [&]() {
     __syncthreads();
     for (int i = tid; i < LS_BINS; i += LS_THREADS) hist[i] = 0u;
     if (tid < 3) result[tid] = ~0ull;
@@ -1063,6 +1084,8 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             cut = min(cut, tot[bin] <= LS_LIST ? cut_in_bin(1, bin, true, 0ull, v[0], need, cut) : bisect(true, need, cut));
         }
     }
+    };
+    auto draw = [&]() {
     // ---- the mass that is left, and where the draw falls
     auto kept = [&](float x, int i) -> uint64_t {
         if (ls_key(x, place(i)) > cut) return 0ull;
@@ -1123,7 +1146,9 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             }
     }
     };
-    if (!near_path()) whole_path();
+    const int left = near_path();
+    if (left == ALL) whole_cut();
+    if (left != DONE) draw();
     if (out && !deferred) {
         const float cut_x = cut == ~0ull ? -INFINITY : value_of(cut);
         // weights again, in float32: 2^-22 of each, with the exponent's rounding
@@ -1160,12 +1185,13 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
 // holds, bisected by key); then what is kept goes where it belongs, and the draw is found by
 // buckets of the vocabulary.
 constexpr int LR_THREADS = 512, LR_WARPS = LR_THREADS / 32;
+static_assert(LS_HEAVY <= LS_ROW, "a CTA's entries at a time");
 static_assert(LS_BUCKETS == 2 * LR_THREADS && LS_NEAR <= LS_BUCKETS, "two bins or buckets per thread");
 
 __global__ void __launch_bounds__(LR_THREADS, 2) logits_sample_rows_kernel(const __grid_constant__ LsParams p) {
     extern __shared__ __align__(16) uint2 held[];           // [LS_ROW] (logit, index)
     __shared__ uint32_t count[LS_BUCKETS];                  // entries and mass per bin, then mass per bucket
-    __shared__ unsigned long long mass[LS_BUCKETS];
+    __shared__ uint32_t mass[3][LS_BUCKETS];                // (64-bit sums in shared memory are loops)
     __shared__ uint64_t list[LS_LIST], weight[LS_LIST];
     __shared__ uint64_t table[64];
     __shared__ uint64_t part[LR_WARPS];
@@ -1178,8 +1204,16 @@ __global__ void __launch_bounds__(LR_THREADS, 2) logits_sample_rows_kernel(const
     if (tid < 64) table[tid] = LS_TABLE[tid];
     for (int i = tid; i < LS_BUCKETS; i += LR_THREADS) {
         count[i] = 0u;
-        mass[i] = 0ull;
+        mass[0][i] = mass[1][i] = mass[2][i] = 0u;
     }
+    // less than 2^17 weights of at most 2^42
+    auto add = [&](int i, uint64_t w) {
+        atomicAdd(&mass[0][i], (uint32_t)w & 0x7fffu);
+        atomicAdd(&mass[1][i], (uint32_t)(w >> 15) & 0x7fffu);
+        if (w >> 30) atomicAdd(&mass[2][i], (uint32_t)(w >> 30));
+    };
+    auto mass_of = [&](int i) -> uint64_t { return mass[0][i] + ((uint64_t)mass[1][i] << 15) + ((uint64_t)mass[2][i] << 30); };
+    static_assert(LS_CLUSTER_MAX * LS_HEAVY < 1 << 17, "sums of the weights' parts in 32 bits");
     pdl_launch_dependents();
     pdl_wait();
     const int cnt = p.node_counts ? p.node_counts[b] : p.N;
@@ -1209,29 +1243,51 @@ __global__ void __launch_bounds__(LR_THREADS, 2) logits_sample_rows_kernel(const
     const float top = __uint_as_float(dump[3]);
     __syncthreads();
     const int total = (int)first[p.ctas];
-    for (int r = warp; r < p.ctas; r += LR_WARPS) {
+    // (wide: more entries than are held here, read again each time)
+    auto body = [&](auto kind) {
+    constexpr bool wide = decltype(kind)::value;
+    auto entry = [&](int r, int e) -> uint2 {
         const uint32_t* src = dump + (int64_t)r * p.slice + LS_HEAD;
-        const int m = (int)(first[r + 1] - first[r]);
-#pragma unroll 4
-        for (int e = lane; e < m; e += 32) held[first[r] + e] = make_uint2(src[2 * e], src[2 * e + 1]);
-    }
-    __syncthreads();
+        return make_uint2(src[2 * e], src[2 * e + 1]);
+    };
     // (the dump lies in the distribution)
-    for (int r = warp; r < p.ctas; r += LR_WARPS) {
+    auto clear = [&](int r, int id, int count) {
         float* to = out + (int64_t)r * p.slice;
         const int words = LS_HEAD + 2 * (int)(first[r + 1] - first[r]);
-        for (int e = lane; e < words; e += 32) to[e] = 0.f;
+        for (int e = id; e < words; e += count) to[e] = 0.f;
+    };
+    if constexpr (!wide) {
+        for (int r = warp; r < p.ctas; r += LR_WARPS) {
+            const int m = (int)(first[r + 1] - first[r]);
+#pragma unroll 4
+            for (int e = lane; e < m; e += 32) held[first[r] + e] = entry(r, e);
+        }
+        __syncthreads();
+        for (int r = warp; r < p.ctas; r += LR_WARPS) clear(r, lane, 32);
     }
     constexpr float L2EH = 1.44269502162933349609f, L2EL = 1.92596299112661746887e-8f;
     const float ch = L2EH / T, cl = (fmaf(-ch, T, L2EH) + L2EL) / T;
     const float bin_scale = fminf(LS_BIN / T, 1e38f);
     auto bin_of = [&](float x) -> int { return (int)fminf((top - x) * bin_scale, (float)(LS_BUCKETS - 1)); };
     auto weigh = [&](float x) -> uint64_t { return ls_weight(x, top, ch, cl, table); };
-    auto each = [&](auto f) {                               // f(logit, index)
+    // f(logit, index), by every thread of the CTA; a wide row's entries by the CTA that left them
+    auto over = [&](int m, auto f) {
 #pragma unroll 1
-        for (int e = tid; e < total; e += LR_THREADS) {
-            const uint2 a = held[e];
-            f(__uint_as_float(a.x), (int)a.y);
+        for (int e = tid; e < m; e += LR_THREADS) f(__uint_as_float(held[e].x), (int)held[e].y);
+    };
+    auto each = [&](auto f) {
+        if constexpr (!wide) {
+            over(total, f);
+        } else {
+#pragma unroll 1
+            for (int r = 0; r < p.ctas; ++r) {
+                const int m = (int)(first[r + 1] - first[r]);
+                __syncthreads();
+#pragma unroll 4
+                for (int e = tid; e < m; e += LR_THREADS) held[e] = entry(r, e);
+                __syncthreads();
+                over(m, f);
+            }
         }
     };
     auto sum_of = [&](uint64_t v) -> uint64_t {             // over the CTA, for every thread
@@ -1250,7 +1306,7 @@ __global__ void __launch_bounds__(LR_THREADS, 2) logits_sample_rows_kernel(const
     uint64_t m0 = 0ull, m1 = 0ull, m_before = 0ull;
     auto scan = [&]() -> uint64_t {
         c0 = count[2 * tid], c1 = count[2 * tid + 1];
-        m0 = mass[2 * tid], m1 = mass[2 * tid + 1];
+        m0 = mass_of(2 * tid), m1 = mass_of(2 * tid + 1);
         uint32_t ci = c0 + c1;
         uint64_t mi = m0 + m1;
 #pragma unroll
@@ -1291,17 +1347,36 @@ __global__ void __launch_bounds__(LR_THREADS, 2) logits_sample_rows_kernel(const
         }
         __syncthreads();
     };
+    // Buckets of the vocabulary, for what is kept, in the bins' room once those have been summed.
+    int shift = 0;
+    while ((p.V - 1) >> shift >= LS_BUCKETS) ++shift;
+    auto to_bucket = [&](int i, uint64_t w) {
+        if (w >= least) add(i >> shift, w);
+    };
+    auto clear_buckets = [&]() {
+        __syncthreads();
+        for (int i = tid; i < LS_BUCKETS; i += LR_THREADS) mass[0][i] = mass[1][i] = mass[2][i] = 0u;
+        __syncthreads();
+    };
+    // (last: what comes before the bin, and what the cut keeps of it, to the buckets)
     // The key in a bin with rank `rank` there (by_rank), or of the last entry (up to `limit`) that begins
     // below need when `base` comes before the bin: result; upto: the bin's mass up to it.
-    auto cut_in = [&](int bin, bool by_rank, uint32_t rank, uint64_t base, uint64_t need, uint64_t limit) {
+    auto cut_in = [&](int bin, bool by_rank, uint32_t rank, uint64_t base, uint64_t need, uint64_t limit, bool last) {
+        if (last) clear_buckets();
         if (count[bin] <= LS_LIST) {
             if (tid == 0) list_n = 0u;
             __syncthreads();
             each([&](float x, int i) {
-                if (bin_of(x) != bin || ls_key(x, i) > limit) return;
-                const uint32_t at = atomicAdd(&list_n, 1u);
-                list[at] = ls_key(x, i);
-                weight[at] = weigh(x);
+                const int its = bin_of(x);
+                if (its > bin || (!last && its != bin) || ls_key(x, i) > limit) return;
+                const uint64_t w = weigh(x);
+                if (its < bin) {
+                    to_bucket(i, w);
+                } else {
+                    const uint32_t at = atomicAdd(&list_n, 1u);
+                    list[at] = ls_key(x, i);
+                    weight[at] = w;
+                }
             });
             __syncthreads();
             const int m = (int)list_n;
@@ -1321,6 +1396,9 @@ __global__ void __launch_bounds__(LR_THREADS, 2) logits_sample_rows_kernel(const
                 }
             }
             __syncthreads();
+            if (last)
+                for (int e = tid; e < m; e += LR_THREADS)
+                    if (list[e] <= result) to_bucket((int)(uint32_t)list[e], weight[e]);
             return;
         }
         // many equal entries: the smallest key up to which there are enough
@@ -1344,13 +1422,17 @@ __global__ void __launch_bounds__(LR_THREADS, 2) logits_sample_rows_kernel(const
             upto = got;
         }
         __syncthreads();
+        if (last)
+            each([&](float x, int i) {
+                if (ls_key(x, i) <= hi) to_bucket(i, weigh(x));
+            });
     };
     uint64_t cut = ~0ull;
     if (use_k || use_p) {
         each([&](float x, int) {
             const int bin = bin_of(x);
             atomicAdd(&count[bin], 1u);
-            atomicAdd(&mass[bin], (unsigned long long)weigh(x));
+            add(bin, weigh(x));
         });
         __syncthreads();
         uint64_t left = scan() + others;                    // the mass that top-k leaves
@@ -1370,7 +1452,7 @@ __global__ void __launch_bounds__(LR_THREADS, 2) logits_sample_rows_kernel(const
             __syncthreads();
             k_bin = (int)pick;
             k_before = before_pick;
-            cut_in(k_bin, true, pick_rank, 0ull, 0ull, ~0ull);
+            cut_in(k_bin, true, pick_rank, 0ull, 0ull, ~0ull, !use_p);
             cut = result;
             left = k_before + upto;
             __syncthreads();
@@ -1384,37 +1466,48 @@ __global__ void __launch_bounds__(LR_THREADS, 2) logits_sample_rows_kernel(const
                 bin = (int)pick;
                 base = before_pick;
             }
-            cut_in(bin, false, 0u, base, need, cut);
+            cut_in(bin, false, 0u, base, need, cut, true);
             cut = min(cut, result);
         }
     }
     // ---- what is kept: its sum, by buckets of the vocabulary
-    __syncthreads();
-    for (int i = tid; i < LS_BUCKETS; i += LR_THREADS) mass[i] = 0ull;
-    __syncthreads();
-    const uint32_t width = (uint32_t)(p.V + LS_BUCKETS - 1) / LS_BUCKETS;
-    each([&](float x, int i) {
-        if (ls_key(x, i) > cut) return;
-        const uint64_t w = weigh(x);
-        if (w >= least) atomicAdd(&mass[(uint32_t)i / width], (unsigned long long)w);
-    });
+    if (!(use_k || use_p)) {
+        clear_buckets();
+        each([&](float x, int i) { to_bucket(i, weigh(x)); });
+    }
     __syncthreads();
     const uint64_t all = scan(), goal = ls_part<false>(u, all);
     if (tid == 0) list_n = 0u;
     pick_mass(goal);
     const uint32_t bucket = pick;
-    const float inv = 1.f / (float)all;
-    each([&](float x, int i) {
+    // weights again, in float32, as in the kernel above
+    const float inv = 1.f / ((float)all * 2.2737368e-13f);  // 2^-42
+    auto give = [&](float x, int i) {
         if (ls_key(x, i) > cut) return;
-        const uint64_t w = weigh(x);
-        if (w < least) return;
-        out[i] = (float)w * inv;
-        if ((uint32_t)i / width == bucket) {
-            const uint32_t at = atomicAdd(&list_n, 1u);     // (a bucket has at most `width` entries)
+        const float w = ex2_approx((x - top) * ch);
+        if (min_p > 0.f && w < min_p * 1.001f && (w < min_p * 0.999f || weigh(x) < least)) return;
+        out[i] = w * inv;
+        if ((uint32_t)i >> shift == bucket) {
+            const uint32_t at = atomicAdd(&list_n, 1u);     // (a bucket is no larger)
             list[at] = (uint64_t)i;
-            weight[at] = w;
+            weight[at] = weigh(x);
         }
-    });
+    };
+    if constexpr (!wide) {
+        each(give);
+    } else {
+        // a CTA's entries, which lie where some of them go, at a time
+        for (int r = 0; r < p.ctas; ++r) {
+            const int n = (int)(first[r + 1] - first[r]);
+            __syncthreads();
+#pragma unroll 4
+            for (int e = tid; e < n; e += LR_THREADS) held[e] = entry(r, e);
+            __syncthreads();
+            clear(r, tid, LR_THREADS);
+            __syncthreads();
+            over(n, give);
+        }
+    }
     __syncthreads();
     const int m = (int)list_n;
     for (int e = tid; e < m; e += LR_THREADS) {
@@ -1425,6 +1518,9 @@ __global__ void __launch_bounds__(LR_THREADS, 2) logits_sample_rows_kernel(const
             p.status[row] = TV_OK;
         }
     }
+    };
+    if (total > LS_ROW) body(std::true_type{});
+    else body(std::false_type{});
 }
 
 template <typename E>
@@ -1440,12 +1536,13 @@ tv_status launch_sample(const LsParams& q, int64_t rows, cudaStream_t stream) {
     p.slice = ((p.V + C - 1) / C + LS_STEP - 1) / LS_STEP * LS_STEP;
     if (p.slice > LS_SLICE_MAX) return TV_ERR_UNSUPPORTED;
     if (rows * C > 0x7fffffff) return TV_ERR_UNSUPPORTED;
-    const size_t smem = (size_t)p.slice * sizeof(E);
+    p.heavy = std::min(LS_HEAVY, (LS_SHARED - LS_STATIC - p.slice * (int)sizeof(E)) / 2);
+    const size_t smem = (size_t)p.slice * sizeof(E) + (size_t)p.heavy * sizeof(uint16_t);
     static std::atomic<bool> set[64], set_rows[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TV_ERR_CUDA;
     if (!set[dev]) {
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, LS_SLICE_MAX * (int)sizeof(float)) != cudaSuccess ||
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, LS_SHARED - LS_STATIC) != cudaSuccess ||
             cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
             cudaGetLastError();
             return TV_ERR_CUDA;

@@ -196,3 +196,35 @@ def test_draws_follow_the_distribution(tv):
     p = torch.where(kept, w, 0.0) / w[kept].sum()
     got = torch.bincount(tokens.view(-1).long(), minlength=V).double()
     assert bool(((got - n * p).abs() <= 6 * (n * p * (1 - p)).sqrt() + 1e-9).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_flat_rows(tv, dtype):
+    """Rows in which thousands of entries carry the mass, few of them and more than the GPU holds at once."""
+    for B, N, V, spread in ((3, 1, 128256, 3.0), (2, 1, 60000, 2.0), (30, 20, 32000, 2.5), (8, 12, 128256, 3.0)):
+        x, u = rows(B, N, V, B + V, dtype, spread)
+        if B * N > 200:                                          # (the reference on the CPU: some sequences)
+            x[3:] = x[0] * 0.5
+        keep = [0, 1, 2, B - 1]
+        p, k, temp = ([v[b % 4] for b in range(B)] for v in ([0.95, 0.9, 0.97, 0.6], [0, 20000, 0, 3000], [1.0, 1.2, 0.9, 1.5]))
+        m = [[0.0, 0.0, 2e-4, 0.0][b % 4] for b in range(B)]
+        tokens, status, probs = sample(tv, x, u, temp=temp, k=k, p=p, m=m)
+        assert status.eq(0).all() and bool(((probs.double().sum(-1) - 1).abs() < 1e-5).all())
+        for b in keep[:B]:
+            some = lambda v: [v[b]]  # noqa: E731
+            check(tv, x[b:b + 1, :2], u[b:b + 1, :2], temp=some(temp), k=some(k), p=some(p), m=some(m))
+            for i in range(min(N, 2)):                           # alone or among many: the same token, the same entries
+                t1, _, p1 = sample(tv, x[b:b + 1, i:i + 1], u[b:b + 1, i:i + 1], temp=some(temp), k=some(k), p=some(p), m=some(m))
+                assert int(t1) == int(tokens[b, i]) and torch.equal(p1[0, 0] > 0, probs[b, i] > 0)
+                assert bool(((p1[0, 0] - probs[b, i]).abs() <= 2.0 ** -18 * p1[0, 0]).all())
+
+
+def test_longest_rows(tv):
+    for dtype in (torch.float32, torch.bfloat16):
+        x, u = rows(2, 1, 786432, 3, dtype)
+        check(tv, x, u, k=[50, 0], p=[0.9, 0.3])
+        x, u = rows(1, 1, 786433, 3, dtype)
+        tokens = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+        if dtype == torch.float32:
+            with pytest.raises(tv.TreeVerifyError):
+                tv.logits_sample(x.cuda(), u.cuda(), tokens, tokens.clone())
