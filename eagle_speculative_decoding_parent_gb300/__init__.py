@@ -382,7 +382,7 @@ ROPE_SCALINGS = {"none": 0, "linear": 1, "bands": 2, "ramp": 3}
 class RopeTable(ctypes.Structure):
     """Rotary frequencies (plain host data, see rope_table); dim columns are rotated."""
     _fields_ = [("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
-                ("amplitude", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("amplitude", ctypes.c_float), ("amplitude_rest", ctypes.c_float),
                 ("turn", ctypes.c_uint64 * 128)]
 
 

@@ -354,8 +354,9 @@ tv_status make_rope_table(tv_rope_table* t, int dim, int interleaved, double the
     memset(t, 0, sizeof(*t));
     t->dim = dim;
     t->interleaved = interleaved ? 1 : 0;
-    t->amplitude = (float)(amplitude > 0.0 ? amplitude
-                                           : (scaling == TV_ROPE_RAMP ? 0.1 * log(factor) + 1.0 : 1.0));
+    const double amp = amplitude > 0.0 ? amplitude : (scaling == TV_ROPE_RAMP ? 0.1 * log(factor) + 1.0 : 1.0);
+    t->amplitude = (float)amp;
+    t->amplitude_rest = isfinite(t->amplitude) ? (float)(amp - t->amplitude) : 0.f;
     for (int j = 0; j < dim / 2; ++j) {
         double f = pow(theta, -2.0 * j / dim);
         if (scaling == TV_ROPE_LINEAR) {

@@ -201,8 +201,9 @@ append_q8_kernel(const __grid_constant__ AqParams p, const __grid_constant__ tv_
                     const float by = __ll2float_rn(rest) * (1.0842021724855044e-19f * 3.14159265f);
                     float sn, co;
                     sincospif(ah * 1.0842021724855044e-19f, &sn, &co);  // 2^-63
-                    cs[cs_at(r - c0, j / per, j % per)] =
-                        make_float2(fmaf(-sn, by, co) * rope.amplitude, fmaf(co, by, sn) * rope.amplitude);
+                    const float rest_c = fmaf(co, rope.amplitude_rest, -sn * by * rope.amplitude);
+                    const float rest_s = fmaf(sn, rope.amplitude_rest, co * by * rope.amplitude);
+                    cs[cs_at(r - c0, j / per, j % per)] = make_float2(fmaf(co, rope.amplitude, rest_c), fmaf(sn, rope.amplitude, rest_s));
                 }
             ok = __syncthreads_and(ok ? 1 : 0) != 0;
             if (fresh && !p.checked && cell == at.base && split == 0 && tid == 0) p.status[at.b] = ok ? TV_OK : TV_ERR_OUT_OF_RANGE;

@@ -446,7 +446,7 @@ typedef struct {
     int32_t dim;          /* rotated columns, even, <= TV_ROPE_MAX_DIM */
     int32_t interleaved;  /* 0 or 1 */
     float amplitude;
-    int32_t reserved;
+    float amplitude_rest; /* what the rounding of amplitude leaves (or 0) */
     uint64_t turn[TV_ROPE_MAX_DIM / 2];
 } tv_rope_table;
 
