@@ -1,5 +1,5 @@
-// chunk_attention_q8: the kernel of attn_chunk_tc.cuh on tiles of e4m3 codes that four of its warps
-// widen to bfloat16.
+// chunk_attention_q8 for more than a few rows per sequence: the kernel of attn_chunk_tc.cuh on tiles
+// of e4m3 codes (fewer rows: attn_rows_q8.cu).
 #include "attn_chunk_tc.cuh"
 
 namespace tv {

@@ -6,7 +6,7 @@
 // subnormal codes).  Everything is read into shared memory before anything is written, so a
 // destination may be another row's source.  Rows that stay where they are in a block that
 // keeps its scale are not touched.  Bound by latency: a chain of four round trips (lengths and
-// path, blocks, scales, rows).
+// path, blocks, scales, rows): 32 paths in 4 layers 6.7 us captured, one path in 32 layers 5.2.
 #include "tv_device.cuh"
 #include "tv_fp8.cuh"
 #include "tv_internal.h"
