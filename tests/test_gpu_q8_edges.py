@@ -357,3 +357,35 @@ def test_same_bits_every_time(tv):
         first = attend(tv, c)[0]
         for _ in range(5):
             assert torch.equal(first, attend(tv, c)[0])
+
+
+# ------------------------------------------------------------------ shapes between the two kernels
+
+@pytest.mark.parametrize("heads", [(128, 1), (24, 1), (28, 4), (5, 5), (65, 1)])
+def test_query_heads_per_kv_head_of_128(tv, heads):
+    for n, P in (([5, 1, 40], [30, 260, 0]), ([1, 1], [300, 17]), ([130, 3], [5, 600])):
+        c = Q.cache_case(n, P, Hq=heads[0], Hkv=heads[1], d=128, bs=16, seed=heads[0])
+        check(tv, c)
+        if max(n) <= 64:
+            check(tv, c, mask=Q.trees(n, 4))
+
+
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("G,each", [(1, 8), (1, 9), (1, 16), (1, 17), (1, 24), (1, 25), (4, 2), (4, 3), (4, 4), (4, 5), (4, 6),
+                                    (4, 7), (8, 1), (7, 3), (3, 5), (24, 1)])
+def test_rows_per_sequence(tv, d, G, each):
+    """Around the numbers of rows at which another form is taken; lengths around the average."""
+    n = [max(0, each + e) for e in (0, 1, -1, 0, 2, -2)]
+    c = Q.cache_case(n, [40, 200, 7, 1000, 0, 128], Hq=2 * G, Hkv=2, d=d, bs=16, seed=each)
+    check(tv, c)
+    check(tv, c, window=30, sinks=6, softcap=15.0)
+    check(tv, c, mask=Q.trees(n, each))
+
+
+@pytest.mark.parametrize("d", [128, 64])
+def test_prompt_among_decoding_sequences(tv, d):
+    """Few rows on average, but a long chunk among them."""
+    n, P = [300] + [1] * 150, [700] + [(b * 53) % 900 for b in range(150)]
+    c = Q.cache_case(n, P, Hq=8, Hkv=2, d=d, bs=16, seed=1)
+    check(tv, c)
+    check(tv, c, window=100, sinks=4)

@@ -228,3 +228,53 @@ def test_longest_rows(tv):
         if dtype == torch.float32:
             with pytest.raises(tv.TreeVerifyError):
                 tv.logits_sample(x.cuda(), u.cuda(), tokens, tokens.clone())
+
+
+def test_streams_and_graphs(tv):
+    """Two calls at once on streams of their own; a captured call replayed on other rows and filters."""
+    f = lambda v, dt=torch.float32: torch.tensor(v, dtype=dt, device="cuda")  # noqa: E731
+    for B, N, V in ((4, 1, 20000), (80, 10, 5000)):
+        data = [rows(B, N, V, s) for s in (1, 2)]
+        p = [[0.9, 0.5, 1.0, 0.97][b % 4] for b in range(B)]
+        k = [[0, 40, 7][b % 3] for b in range(B)]
+        want = [sample(tv, x, u, p=p, k=k) for x, u in data]
+        bufs = [dict(x=x.cuda(), u=u.cuda(), tok=torch.zeros((B, N), dtype=torch.int32, device="cuda"),
+                     st=torch.full((B, N), -9, dtype=torch.int32, device="cuda"), pr=torch.full((B, N, V), 5.0, device="cuda"))
+                for x, u in data]
+        P, K = f(p), f(k, torch.int32)
+        streams = [torch.cuda.Stream() for _ in bufs]
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for g, s in zip(bufs, streams):
+                tv.logits_sample(g["x"], g["u"], g["tok"], g["st"], top_p=P, top_k=K, probs=g["pr"], stream=s)
+        torch.cuda.synchronize()
+        for g, (tokens, _, probs) in zip(bufs, want):
+            assert g["st"].eq(0).all() and torch.equal(g["tok"].cpu(), tokens) and torch.equal(g["pr"].cpu(), probs)
+        g = bufs[0]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            tv.logits_sample(g["x"], g["u"], g["tok"], g["st"], top_p=P, top_k=K, probs=g["pr"])
+        for i in (1, 0, 1):
+            g["x"].copy_(data[i][0])
+            g["u"].copy_(data[i][1])
+            g["pr"].fill_(3.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(g["tok"].cpu(), want[i][0]) and torch.equal(g["pr"].cpu(), want[i][2])
+        P.fill_(0.4)
+        graph.replay()
+        torch.cuda.synchronize()
+        again = sample(tv, data[1][0], data[1][1], p=[0.4] * B, k=k)
+        assert torch.equal(g["tok"].cpu(), again[0]) and torch.equal(g["pr"].cpu(), again[2])
+
+
+def test_the_same_bits_alone_or_with_distributions(tv):
+    """Tokens do not depend on whether the distributions are asked for, nor on the rows around them."""
+    x, u = rows(100, 10, 6000, 7)
+    p, k = [[0.9, 1.0, 0.6][b % 3] for b in range(100)], [[0, 30][b % 2] for b in range(100)]
+    tokens, _, probs = sample(tv, x, u, p=p, k=k)
+    bare, _, _ = sample(tv, x, u, p=p, k=k, probs=False)
+    assert torch.equal(tokens, bare)
+    for b in (0, 17, 99):
+        one, _, _ = sample(tv, x[b:b + 1], u[b:b + 1], p=p[b:b + 1], k=k[b:b + 1])
+        assert torch.equal(one[0], tokens[b])
