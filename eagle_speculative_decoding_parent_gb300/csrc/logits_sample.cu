@@ -562,8 +562,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         }
     };
 
-    // ---- Where all that may be kept weighs 2^-16 or more, and few entries do: those are compacted, and a
-    // thread holds up to four with their weights.
+    // ---- The near entries, where they hold all that may be kept: their places in the slice in a list.
     bool deferred = false;
     // Says what is left to do: nothing, the draw, or all of it.
     enum { DONE, DRAW, ALL };
