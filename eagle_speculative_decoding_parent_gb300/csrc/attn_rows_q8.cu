@@ -18,10 +18,10 @@
 // joined in shared memory at the item's end.  An item is (sequence, kv head, up to 8 NT / G
 // tokens); the items of all sequences, laid end to end, are cut into equal runs, one per CTA, as in
 // attn_chunk_tc.cuh, and pieces of items that a border cuts are joined by a second kernel.
-// Measured (32/8 heads of 128): one row of each of 64 sequences of 512-8,192 keys 68 us = 5.1 TB/s,
-// the stream and 41 % of the issue slots; 6 rows of each of 128 sequences of 1,024-4,096 keys 204 us,
-// bound by the products (three row tiles of 8: 135 of the some 140 TFLOP/s that this GPU gives
-// products by warp); one row after 300 keys 11 us, two launches and their start.
+// Measured (32/8 heads of 128): one row of each of 64 sequences of 512-8,192 keys 63 us = 5.6 TB/s,
+// the stream and 41 % of the issue slots; 6 rows of each of 128 sequences of 1,024-4,096 keys 189 us,
+// bound by the products (three row tiles of 8: 146 TFLOP/s, about what this GPU gives products by
+// warp); one row after 300 keys 11 us, two launches and their start.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -41,10 +41,13 @@ constexpr float RQ_LOG2E = 1.4426950408889634f;
 // The largest weight is 2^(RQ_BIAS + RQ_SLACK): float16's range is used downwards.  The running
 // maximum is raised when a score exceeds it by RQ_SLACK.
 constexpr float RQ_BIAS = 13.f, RQ_SLACK = 2.f;
-// fixed cost of an item, in pages, and a border that is this close to an item's end moves there
-constexpr int64_t RQ_C0 = 8;
+// fixed cost of an item, in pages, and a border that is this close to an item's end moves there (the
+// cases below, us, with 8: 68 and 204; 16: 63 and 195; 24: 63 and 189; 32: 67 and 187)
+constexpr int64_t RQ_C0 = 24;
 constexpr int RQ_SNAP = 4;
-constexpr int RQ_RUN_MIN = 12;   // cost of a run, in pages, below which cutting further saves nothing
+// cost of a run, in pages, below which cutting further saves nothing: one that begins an item has
+// pages of it behind the fixed cost
+constexpr int RQ_RUN_MIN = RQ_C0 + RQ_SNAP + 1;
 
 struct RqParams {
     ChunkView c;
