@@ -142,8 +142,10 @@ __device__ __forceinline__ uint64_t ls_weight(float x, float top, float ch, floa
     const float t = d * ch;
     if (!(t < (float)(LS_FRAC + 1))) return 0ull;
     const float tl = fmaf(d, cl, fmaf(dl, ch, fmaf(d, ch, -t)));
-    const float nf = rintf(t * 64.f), r = fmaf(nf, -0.015625f, t);
-    const int n = (int)nf;
+    // (rounded by adding 1.5 * 2^23: the conversions' unit is slow)
+    constexpr float WHOLE = 12582912.f;
+    const float near = fmaf(t, 64.f, WHOLE), r = fmaf(near - WHOLE, -0.015625f, t);
+    const int n = __float_as_int(near) - __float_as_int(WHOLE);
     constexpr float LN2H = 0.69314718246459960938f, LN2L = -1.90465429995776804525e-9f;
     const float p = LN2H * r;
     const float e = fmaf(LN2H, tl, fmaf(LN2L, r, fmaf(LN2H, r, -p)));
@@ -1171,22 +1173,26 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             if (min_p > 0.f && w < min_p * 1.001f && (w < min_p * 0.999f || weigh(x) < least)) return 0.f;
             return w * inv;
         };
-        if ((reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+        auto write = [&](auto f) {
+            if ((reinterpret_cast<uintptr_t>(out) & 15) == 0) {
 #pragma unroll 2
-            for (int i = tid * 4; i < n; i += LS_THREADS * 4) {
-                const float4 x = at4(i);
-                const float4 y = make_float4(prob(x.x, i), prob(x.y, i + 1), prob(x.z, i + 2), prob(x.w, i + 3));
-                if (i + 4 <= n) {
-                    __stcs(reinterpret_cast<float4*>(out + i), y);
-                } else {
-                    out[i] = y.x;
-                    if (i + 1 < n) out[i + 1] = y.y;
-                    if (i + 2 < n) out[i + 2] = y.z;
+                for (int i = tid * 4; i < n; i += LS_THREADS * 4) {
+                    const float4 x = at4(i);
+                    const float4 y = make_float4(f(x.x, i), f(x.y, i + 1), f(x.z, i + 2), f(x.w, i + 3));
+                    if (i + 4 <= n) {
+                        __stcs(reinterpret_cast<float4*>(out + i), y);
+                    } else {
+                        out[i] = y.x;
+                        if (i + 1 < n) out[i + 1] = y.y;
+                        if (i + 2 < n) out[i + 2] = y.z;
+                    }
                 }
+            } else {
+                for (int i = tid; i < n; i += LS_THREADS) out[i] = f(at1(i), i);
             }
-        } else {
-            for (int i = tid; i < n; i += LS_THREADS) out[i] = prob(at1(i), i);
-        }
+        };
+        if (cut == ~0ull && min_p == 0.f) write([&](float x, int) -> float { return ex2_approx((x - top) * ch) * inv; });
+        else write(prob);
     }
 }
 
