@@ -30,8 +30,9 @@
 // thread marks them among 32 of its entries, and goes through the marks.
 // Measured, rows of 128,256: one row of bfloat16 15-21 us, 64 rows with top-k, top-p and min-p 29
 // (latency: launch, the slices, some eight barriers of a cluster; the best entries alone 8); 832
-// rows of float32 with distributions: 214 the best entries, 349 min-p, 473 top-p, 522 no filter,
-// 856 top-p of flat rows; the bytes take 126.  59 % of the issue slots in the first kernel.
+// rows of float32 with distributions: 214 the best entries, 349 min-p, 474 top-p, 470 no filter (of
+// that 185 the exact weights of every entry), 856 top-p of flat rows; the bytes take 126.  59 % of the
+// issue slots in the first kernel.
 #include <cuda_bf16.h>
 #include <float.h>
 #include <math.h>
