@@ -620,7 +620,8 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             bool room = true, small = true;
             for (int r = 0; r < C; ++r) {
                 const int a = (int)(peer[turn ^ 1][0][r] >> (16 * j)) & 0xffff;
-                room = room && a <= (p.defer ? min(p.heavy, (min(p.slice, p.V - r * p.slice) - LS_HEAD) / 2) : p.heavy);
+                // (a dump's header and pairs lie in the slice's own part of the distribution)
+                room = room && a <= p.heavy && (!p.defer || LS_HEAD + 2 * a <= min(p.slice, p.V - r * p.slice));
                 small = small && a <= LS_FEW;
                 sum += (uint32_t)a;
             }
