@@ -70,6 +70,7 @@ constexpr int LS_FEW = 4 * LS_THREADS;       // so many that what is kept of the
 constexpr int LS_TRIES = 4;
 // Rows left to logits_sample_rows_kernel, which holds at most so many near entries (more of them are
 // read again for each use): dumped behind a header of so many words into the slices' part of the distribution; the status that says so.
+// A last slice that is empty or shorter than the header has none, and no near entry.
 constexpr int LS_ROW = 8192;
 constexpr int LS_HEAD = 8;
 constexpr int32_t LS_PENDING = -0x5eed;
@@ -110,6 +111,8 @@ struct LsParams {
     int64_t rows, ahead;     // ahead: rows that the GPU holds at once
     int heavy;               // near entries of a CTA
     bool defer;              // distributions of many rows: the near entries to the second kernel
+    __device__ __forceinline__ int cells(int r) const { return min(slice, V - r * slice); }   // of CTA r's slice (0 or less: none)
+    __device__ __forceinline__ bool headed(int r) const { return cells(r) >= LS_HEAD; }
 };
 
 // The order of the entries: smaller is better, all different.
@@ -621,7 +624,7 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
             for (int r = 0; r < C; ++r) {
                 const int a = (int)(peer[turn ^ 1][0][r] >> (16 * j)) & 0xffff;
                 // (a dump's header and pairs lie in the slice's own part of the distribution)
-                room = room && a <= p.heavy && (!p.defer || LS_HEAD + 2 * a <= min(p.slice, p.V - r * p.slice));
+                room = room && a <= p.heavy && (!p.defer || a == 0 || LS_HEAD + 2 * a <= p.cells(r));
                 small = small && a <= LS_FEW;
                 sum += (uint32_t)a;
             }
@@ -689,21 +692,24 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         // (not where the near entries do not hold all that may be kept)
         if (weights && ls_part<true>(top_p, mass_all) > mass_near) return ALL;
         if (p.defer) {
-            // the second kernel takes it from here
+            // the second kernel takes it from here (the first slice has a header: in rows shorter than one there is
+            // no room for the largest entry)
             uint32_t* dump = reinterpret_cast<uint32_t*>(out);
-            const uint64_t mine = peer[turn ^ 1][1][me];
-            if (tid == 0) {
+            const uint64_t others = mass_all - mass_near;
+            if (tid == 0 && p.headed(me)) {
                 dump[0] = held;
-                dump[1] = (uint32_t)mine;
-                dump[2] = (uint32_t)(mine >> 32);
-                dump[3] = __float_as_uint(top);
-                if (me == 0) p.status[row] = LS_PENDING;
+                if (me == 0) {
+                    dump[1] = (uint32_t)others;
+                    dump[2] = (uint32_t)(others >> 32);
+                    dump[3] = __float_as_uint(top);
+                    p.status[row] = LS_PENDING;
+                }
             }
             for (int e = tid; e < (int)held; e += LS_THREADS) {
                 dump[LS_HEAD + 2 * e] = __float_as_uint(at1(near_i[e]));
                 dump[LS_HEAD + 2 * e + 1] = (uint32_t)place(near_i[e]);
             }
-            const int from = LS_HEAD + 2 * (int)held;
+            const int from = p.headed(me) ? LS_HEAD + 2 * (int)held : 0;
             if ((reinterpret_cast<uintptr_t>(out) & 15) == 0) {
                 const int full = min(n, (from + 3) & ~3);
                 if (from + tid < full) out[from + tid] = 0.f;
@@ -1244,19 +1250,15 @@ __global__ void __launch_bounds__(LR_THREADS, 2) logits_sample_rows_kernel(const
     float* out = p.probs + row * p.V;
     const uint32_t* dump = reinterpret_cast<const uint32_t*>(out);
     if (warp == 0) {
-        const uint32_t* head = dump + (int64_t)lane * p.slice;
-        const uint32_t mine = lane < p.ctas ? head[0] : 0u;
-        uint64_t rest = lane < p.ctas ? (uint64_t)head[1] | (uint64_t)head[2] << 32 : 0ull;
+        const uint32_t mine = lane < p.ctas && p.headed(lane) ? dump[(int64_t)lane * p.slice] : 0u;
         uint32_t incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += y;
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
         if (lane <= LS_CLUSTER_MAX) first[lane] = incl - mine;
-        if (lane == 0) others = rest;
+        if (lane == 0) others = (uint64_t)dump[1] | (uint64_t)dump[2] << 32;
     }
     const float top = __uint_as_float(dump[3]);
     __syncthreads();
@@ -1271,7 +1273,7 @@ __global__ void __launch_bounds__(LR_THREADS, 2) logits_sample_rows_kernel(const
     // (the dump lies in the distribution)
     auto clear = [&](int r, int id, int count) {
         float* to = out + (int64_t)r * p.slice;
-        const int words = LS_HEAD + 2 * (int)(first[r + 1] - first[r]);
+        const int words = p.headed(r) ? LS_HEAD + 2 * (int)(first[r + 1] - first[r]) : 0;
         for (int e = id; e < words; e += count) to[e] = 0.f;
     };
     if constexpr (!wide) {

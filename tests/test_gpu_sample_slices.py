@@ -72,3 +72,16 @@ def test_last_slice_of_seven_entries(tv, V, offset):
 
 def test_last_slice_of_seven_entries_half_precision(tv):
     around(tv, 491527, torch.bfloat16, 14, 3, 0)
+
+
+@pytest.mark.parametrize("V", [114689, 114690, 114696, 114698, 131075, 262208, 300000])
+def test_last_slice_empty_or_short(tv, V):
+    """One entry, two, as many as the header, one pair more; an empty slice (262,208 entries: sixteen slices of
+    18,432)."""
+    around(tv, V, torch.float32, 28, 3, V % 2)
+
+
+@pytest.mark.parametrize("V", [5, 7, 8, 9, 2047, 2049, 2055, 2056])
+def test_many_short_rows(tv, V):
+    """Rows shorter than a slice, or than a dump's header."""
+    around(tv, V, torch.float32, 35, 64, 0)
