@@ -61,7 +61,7 @@ constexpr float LS_BIN = 64.f;               // bins per unit of (max - x) / T
 constexpr int LS_REACHES = 4;
 constexpr int LS_NEARER = 592, LS_NEAR = 680;
 __device__ constexpr int ls_reach(int j) { return j == 0 ? 384 : j == 1 ? 480 : j == 2 ? LS_NEARER : LS_NEAR; }
-static_assert(LS_NEAR % 2 == 0 && LS_NEAR * 12 <= LS_BINS * 4, "counts and masses of the near bins in a histogram's room");
+static_assert(LS_NEAR % 2 == 0 && LS_NEAR * 12 <= LS_BINS * 4, "counts and masses (of 8 bytes, aligned) of the near bins in a histogram's room");
 constexpr float LS_SMALL = 19.f;             // weights below 2^-19 enter the sum of all in float32
 constexpr int LS_LIST = 1024;
 constexpr int LS_HEAVY = 6144;               // near entries of a CTA (fewer beside the longest slices)
@@ -202,7 +202,8 @@ template <typename E>
 __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __grid_constant__ LsParams p) {
     extern __shared__ __align__(16) uint8_t ls_smem[];
     E* xs = reinterpret_cast<E*>(ls_smem);                 // the slice
-    __shared__ uint32_t hist[LS_BINS], tot[LS_BINS];       // the slice's counts, the row's
+    __shared__ __align__(16) uint32_t hist[LS_BINS];       // the slice's counts (see masses: words of 8 bytes too),
+    __shared__ __align__(16) uint32_t tot[LS_BINS];        // the row's
     __shared__ uint64_t lists[2 * LS_LIST];
     uint64_t *list = lists, *weight = lists + LS_LIST;     // first CTA: entries of one bin
     __shared__ uint64_t table[64];
