@@ -5,7 +5,9 @@
 // a row's filters come down to one cut in that order.  Weights are exp((x - max) / T) in fixed
 // point, 2^-42 steps, off by some 2^-39 of themselves: their sums do not depend on an
 // order, and a token or a cut differs from the exact one only where the given number is as
-// near to a border.
+// near to a border.  (The sum that top-p of a whole row is taken of has its far entries in
+// float32, off by at most 2^-18 of themselves: up to 2^17 entries with forty instructions each
+// would cost more than the rest.)
 //
 // A cluster of CTAs holds a row in shared memory, a slice each, and nearly always only the entries
 // near the maximum matter:
@@ -577,7 +579,10 @@ __global__ void __launch_bounds__(LS_THREADS, 2) logits_sample_kernel(const __gr
         if (!(use_k || use_p || min_p > 0.f)) return ALL;
         // The entries within each reach, a byte for each (a thread has at most 96 entries).  For top-p of the
         // whole row also the weights of the entries between the last two and beyond, in 2^-34 and 2^-38
-        // of the largest: below 2^23 of them each, so rounded by adding 2^23.
+        // of the largest: below 2^23 of them each, so rounded by adding 2^23.  (The exponent t < 32 is off by
+        // 2^-24 t for d and three roundings of 2^-20 at most, 3.3e-6 of the weight with ln 2; ex2 by 2^-22;
+        // and half a step, of the weights between, 2^-13.3 to 2^-15.3, 2^-19.7: below 2^-18 in all, beyond
+        // with 2^-39 for the step.)
         const bool weights = use_p && !use_k;
         uint32_t between = 0u, beyond = 0u, many = 0u;
         if (weights) {

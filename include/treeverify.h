@@ -729,9 +729,9 @@ tv_status tree_logits_process(const void* logits, tv_dtype dt, int B, int N, int
  *   probs[b][i][x] = w_x / (the sum W of the kept ones), 0 for the others
  *   tokens[b][i] = the smallest x with w_0 + .. + w_x (kept ones) > uniform[b][i] * W
  * The w of 1 and 2 and the sums are in fixed point, steps of 2^-42, each w off by at
- * most 2^-38 of itself and half a step (one below 2^-19, in the sum over a whole row, by
- * 2^-18 of itself): cuts and tokens differ from the exact ones only where a sum comes
- * that near to its border.  probs are float32, off by at most 2^-20
+ * most 2^-38 of itself and half a step (one below 2^-13, in the sum over a whole row that
+ * top_p is taken of where top_k does not limit it, by 2^-18 of itself and 2^-39): cuts and
+ * tokens differ from the exact ones only where a sum comes that near to its border.  probs are float32, off by at most 2^-20
  * of themselves and of the exponent's rounding, 2^-23 (logit - largest) / temperature.
  * temperature, top_p, min_p float32 [B], top_k int32 [B]: each may be NULL (1; 1; 0; all).
  * uniform float32 [B][N], in [0, 1): the random numbers are the caller's.  probs float32
