@@ -674,12 +674,16 @@ __device__ __forceinline__ void load_stream(const Params& p, const CUtensorMap& 
 // the power of two that brings its largest element to 2^7 .. 2^8, the nearest code and what is
 // left.  Eight significant bits go into two codes of four exactly, down to 2^-18 of the largest
 // element (the codes' smallest step, 2^-9; elements below lose bits).  Its exponent is noted.
-// A row with an infinity or NaN is NaN, as its scores are.
+// A row with a NaN is NaN, as its scores are; so is one with an infinity, whose scores are NaN or
+// infinite and, with one above -infinity among them, its output NaN.  Not with a cap, which makes
+// them finite: then such a row is zeros here (its products 0, or NaN where a key is), and noted as
+// QX_INF for the softmax to put its scores in place (infinite_scores).
 // Step k takes columns 16 k .. 16 k + 15, the pieces 2 k and 2 k + 1 of the row's sixteen, and writes
 // piece k of the first part, in the first half, and of the second part, in the second.  First the
 // first half upwards, with its four pieces of the second part held; then the second half
 // downwards: what is written has been read.
-template <class L>
+constexpr uint32_t QX_INF = 254u;      // (exponents: 20 .. 253)
+template <class L, bool CAP>
 __device__ __forceinline__ void split_queries(const Params& p, uint8_t* smem, const Item& it, int r, uint32_t buf) {
     const int nq = (it.flags & ITEM_TWO) ? 2 : 1;
 #pragma unroll 1
@@ -697,16 +701,17 @@ __device__ __forceinline__ void split_queries(const Params& p, uint8_t* smem, co
             top = max_u16x2(max_u16x2(top, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
             top = max_u16x2(max_u16x2(top, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
         }
-        const uint32_t e = max(top >> 16, top & 0xffffu) >> 7;
-        const uint32_t ex = min(max(e, 20u), 253u), odd = e == 255u ? 0x7f7f7f7fu : 0u;
+        const uint32_t most = max(top >> 16, top & 0xffffu), e = most >> 7;
+        const bool inf = CAP && most == 0x7f80u;           // an infinity, no NaN
+        const uint32_t ex = min(max(e, 20u), 253u), odd = e == 255u && !inf ? 0x7f7f7f7fu : 0u, kept = inf ? 0u : 0xffffffffu;
         const float up = __uint_as_float(min(261u - ex, 254u) << 23);      // 2^(7 - exponent)
-        smem[L::OFF_QX + (buf * 2 + t) * MT + r] = (uint8_t)ex;
+        smem[L::OFF_QX + (buf * 2 + t) * MT + r] = (uint8_t)(inf ? QX_INF : ex);
         auto split = [&](int k, uint4& hi, uint4& lo) {
             uint32_t h[4], l[4];
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
                 const uint4 x = *piece(2 * k + v);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                const uint32_t w[4] = {x.x & kept, x.y & kept, x.z & kept, x.w & kept};
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                     // exact in float16, as is what is left
@@ -751,7 +756,7 @@ __device__ __forceinline__ void split_queries(const Params& p, uint8_t* smem, co
 // byte permutation and two logical operations (value 2^-120, exact for subnormal codes too)
 // and a product with 2^120 times the scale.  V rows that must not reach O are cleared here
 // (see warp 10 of the other kernels).
-template <class L, int D, class Take>
+template <class L, int D, bool CAP, class Take>
 __device__ __forceinline__ void widen_codes(const Params& p, uint8_t* smem, uint64_t* full, uint64_t* empty,
                                             uint64_t* rfull, uint64_t* rempty, uint64_t* qfull, uint64_t* qready,
                                             uint32_t* bad, volatile int* abort_flag, Take& take, bool& alive) {
@@ -776,7 +781,7 @@ __device__ __forceinline__ void widen_codes(const Params& p, uint8_t* smem, uint
         if constexpr (L::K8) {
             alive = wait_all<64>(qfull, (live - 1) & 1u);
             if (!alive) break;
-            split_queries<L>(p, smem, it, r, (live - 1) & 1u);
+            split_queries<L, CAP>(p, smem, it, r, (live - 1) & 1u);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(qready);
@@ -937,6 +942,36 @@ __device__ __noinline__ void add_noted(const Params& p, const Item& it, const ui
                 tmem_wait_st();
             }
         }
+    }
+}
+
+// The scores of query rows with an infinity (see split_queries), in place (tensor memory, this warp's
+// lanes): of each key what the row's infinite columns give, beside what is there (0, or NaN).  here: the
+// lane's row is one, q; v0: the item's number of the first of `keys` keys.  Rare, so out of line.
+template <int D>
+__device__ __noinline__ void infinite_scores(const Params& p, const Item& it, int v0, int keys, uint32_t tS, bool here,
+                                             const __nv_bfloat16* q) {
+    const int vend = it.hi - it.kbase;
+#pragma unroll 1
+    for (int c = 0; c < keys; c += 16) {                   // a page: keys of one block
+        uint32_t r[16];
+        tmem_ld16(tS + c, r);
+        tmem_wait_ld();
+        if (here && v0 + c < vend) {
+            const int key = item_key(it, v0 + c);
+            const int64_t blk = p.c.table[(int64_t)it.b * p.c.max_blocks + key / p.c.bs];
+            const uint8_t* k = static_cast<const uint8_t*>(p.k) + ((blk * p.Hkv + it.g) * p.c.bs + key % p.c.bs) * D;
+#pragma unroll 1
+            for (int x = 0; x < D; ++x) {
+                const float a = __bfloat162float(q[x]);
+                if (!isinf(a)) continue;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(fmaf(a, e4m3_float(k[e * D + x]), __uint_as_float(r[e])));
+            }
+        }
+        __syncwarp();
+        tmem_st16(tS + c, r);
+        tmem_wait_st();
     }
 }
 
@@ -1281,7 +1316,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         }
         }
     } else if (E8 && warp >= CONV_WARP) {
-        widen_codes<L, D>(p, smem, full, empty, rfull, rempty, qfull, qready, bad, abort_flag, take, alive);
+        widen_codes<L, D, CAP>(p, smem, full, empty, rfull, rempty, qfull, qready, bad, abort_flag, take, alive);
     } else if (warp == MMA_WARP) {
         // ============================== products ==============================
         uint32_t slot = 0, par = 0;                    // next ring position: slot, parity of its round
@@ -1616,6 +1651,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 const float csc = CAP || L::K8 ? 1.f : p.scale_log2;
                 // loads a part, caps and masks it; its maximum
                 auto part_max = [&](int h0) -> float {
+                    if constexpr (CAP && L::K8) {
+                        const bool inf = mine && smem[L::OFF_QX + ((live & 1u) * 2 + (two ? i : 0)) * MT + row] == QX_INF;
+                        if (__any_sync(0xffffffffu, inf))
+                            infinite_scores<D>(p, it, (it.t_lo + j) * KT + h0, PART, tS + h0, inf,
+                                               p.q + (int64_t)(it.row0 + tok) * p.q_stride + (int64_t)(it.g * p.G + head) * D);
+                    }
                     load_s(h0);
                     if constexpr (CAP && L::K8) {
 #pragma unroll
