@@ -495,6 +495,11 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t a) {   // infinities to the largest number
+    uint32_t d;
+    asm("{\n\t.reg .b32 t;\n\tmin.bf16x2 t, %1, %2;\n\tmax.bf16x2 %0, t, %3;\n\t}" : "=r"(d) : "r"(a), "r"(0x7f7f7f7fu), "r"(0xff7fff7fu));
+    return d;
+}
 // Bytes that are NaN codes, as their top bits (no carries: a byte is at most 0x7f + 1).
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
 
@@ -850,7 +855,9 @@ __device__ __forceinline__ void widen_codes(const Params& p, uint8_t* smem, uint
             }
             const bool nan = !clear && (acc & 0x80808080u) != 0u;
             if (__any_sync(0xffffffffu, nan || e > 134u)) {
-                // NaN codes, and scales that need two factors: once more
+                // NaN codes, and scales that need two factors: once more.  (256 times 2^120, which the largest
+                // numbers are rounded to, is no bfloat16 and counts as the largest: as infinity it would
+                // reach the rows with weight zero.)
                 const uint32_t f1 = (max(e + 120u, 254u) - 127u) << 7, m3 = f1 | f1 << 16;
 #pragma unroll 1
                 for (int u = 0; u < NCH; ++u) {
@@ -860,7 +867,7 @@ __device__ __forceinline__ void widen_codes(const Params& p, uint8_t* smem, uint
                     widen(c, o);
 #pragma unroll
                     for (int y = 0; y < 8; ++y)
-                        if (e > 134u) o[y] = mul_bf16x2(o[y], m3);
+                        if (e > 134u) o[y] = finite_bf16x2(mul_bf16x2(o[y], m3));
                     if (nan)
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {

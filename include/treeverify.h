@@ -545,8 +545,9 @@ tv_status chunk_attention(const void* q, int64_t q_stride, const void* k_cache,
  * stands for code * scale.  Scales are powers of two from 2^-100 on, as
  * chunk_kv_append_q8 writes them (of any other number the exponent alone counts, and
  * smaller ones may count as 2^-100), so that what a code stands for is a bfloat16
- * number exactly, and a code moves to a larger scale without rounding until it falls
- * below the smallest normal code (2^-6).  block_size is a multiple of 16; d is 64 or
+ * number exactly (but for 256 times 2^120: numbers from 1.9375 2^127 on are rounded to 2^128,
+ * and attention may take that for the largest bfloat16 number), and a code moves to a larger
+ * scale without rounding until it falls below the smallest normal code (2^-6).  block_size is a multiple of 16; d is 64 or
  * 128; queries, new keys and values and outputs are bfloat16.  Half the bytes of the
  * stream that bounds decoding and verification, for a relative error of 2^-4 an
  * element.
@@ -603,6 +604,8 @@ tv_status chunk_kv_append_q8(const void* q, int64_t q_stride, const void* k, int
  * to bfloat16 or (few rows per sequence: those below 2^-27 of a row's largest weight x
  * scale of V by 2^-38 of that) float16; with d = 128, elements of a query row below 2^-10 of
  * its largest, to steps of 2^-17 of that.
+ * Sums beyond float32 are infinite, or NaN: q . k_t, and (unless there are few rows per
+ * sequence) 2^8 times the sum of weights up to 1 times values.
  * status int32 [B]: as chunk_attention (with sinks, the blocks of the first sinks
  * positions are needed too), and TV_ERR_OUT_OF_RANGE for more than 64 rows with a
  * mask.  Cache contents outside K reach no row, NaN included.
