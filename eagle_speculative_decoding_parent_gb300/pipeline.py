@@ -147,6 +147,18 @@ class VerifyStep:
             self.drawn = torch.zeros((B, N), **i32)
             self.st_filter = torch.zeros((B, N), **i32)
 
+    def _refuse(self, mode, sampling, node_counts, k_scale, v_scale):
+        """What a later call of the step would refuse, before the first one is issued."""
+        if sampling is not None and self.target is None:
+            raise ValueError("sampling needs a step made with process=True")
+        if sampling is not None and any(sampling.get(x) is not None for x in FILTERS) and \
+                (self.filtered is None or mode != STOCHASTIC):
+            raise ValueError("filters need a step made with filters=True, and mode STOCHASTIC")
+        if self.q8 and node_counts is not None:
+            raise ValueError("with an 8-bit cache the trees have N nodes each")
+        if self.q8 and (k_scale is None or v_scale is None):
+            raise ValueError("an 8-bit cache has k_scale and v_scale")
+
     def mask_build(self, parents, stream=None, node_counts=None):
         tree_mask_build(parents, self.mask, self.depth, self.st_mask, stream=stream,
                         node_counts=node_counts)
@@ -214,8 +226,7 @@ class VerifyStep:
         the step emits are added to counts.  A sequence that cannot be processed, or whose
         grammar leaves nothing where a token is to be chosen, emits none (st_process,
         st_accept; out_tokens -1): its counts stay, and its cache keeps the root."""
-        if sampling is not None and self.target is None:
-            raise ValueError("sampling needs a step made with process=True")
+        self._refuse(mode, sampling, node_counts, k_scale, v_scale)
         self.mask_build(parents, stream, node_counts)
         scales = dict(k_scale=k_scale, v_scale=v_scale) if self.q8 else {}
         self.attention(q, k_cache, v_cache, block_table, prefix_lens, stream, node_counts, **scales)
