@@ -609,6 +609,10 @@ tv_status chunk_kv_append_q8(const void* q, int64_t q_stride, const void* k, int
  * status int32 [B]: as chunk_attention (with sinks, the blocks of the first sinks
  * positions are needed too), and TV_ERR_OUT_OF_RANGE for more than 64 rows with a
  * mask.  Cache contents outside K reach no row, NaN included.
+ * One of two kernels serves a whole call, chosen by the average of rows per sequence (T / B
+ * times Hq / Hkv: up to 24, or more): a long chunk among many decoding sequences is better
+ * given a call of its own (512 rows after 16,000 keys and 128 single rows after 512-8,192, 32/8
+ * heads of 128: 910 us together, 146 and 214 apart).
  * workspace: chunk_attention_q8_workspace() bytes, 16-byte aligned, any contents.
  * Host errors: as chunk_attention; TV_ERR_INVALID_ARG for sinks outside [0, 64], mask
  * with a window, NULL scales; TV_ERR_UNSUPPORTED for d other than 64 and 128, a block
