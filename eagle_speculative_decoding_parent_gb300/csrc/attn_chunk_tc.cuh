@@ -152,7 +152,7 @@ struct Lay {
     static constexpr int OFF_ITEMS = OFF_Q + 2 * Q_BYTES;  // [GQ]
     static constexpr int OFF_MISC = OFF_ITEMS + GQ * 64;   // tensor memory's address, abort flag
     static constexpr int OFF_BARS = OFF_MISC + 16;
-    static constexpr int NBARS = (E8 ? 2 * SLOTS + 2 * RAWS + 2 * KSLOTS + (K8 ? 1 : 0) : 3 * SLOTS) + 8 + 4 + 2 * GQ + 2;
+    static constexpr int NBARS = (E8 ? 2 * SLOTS + 2 * RAWS + 2 * KSLOTS + (K8 ? 2 : 0) : 3 * SLOTS) + 8 + 4 + 2 * GQ + 2;
     static constexpr int OFF_EXP = OFF_BARS + NBARS * 8;   // [RAWS][8 pages], K8: and [KEXPS][8]
     static constexpr int OFF_BAD = (OFF_EXP + (RAWS + (K8 ? KEXPS : 0)) * 8 + 15) / 16 * 16;  // [FIX_BUFS][FIX_TILES][4]
     static constexpr int OFF_END = OFF_BAD + FIX_BUFS * FIX_TILES * 16;
@@ -599,10 +599,9 @@ __device__ __forceinline__ void load_codes(const Params& p, uint8_t* smem, uint6
 // d = 128: K and V have rings of their own, so a warp each: warp 9 loads K, and an item's queries
 // before it; warp 10 loads V.  A tile's scales follow its copies by one tile.  (Four slots of K and two
 // of V's codes, which are widened as they come: 32 trees of 26 nodes 88 us, two and four 91.)
-template <class L, int D, bool V, class Take, class Before, class Last>
+template <class L, int D, bool V, class Take, class Before>
 __device__ __forceinline__ void load_stream(const Params& p, const CUtensorMap& kmap, uint8_t* smem, uint64_t* filled,
-                                            uint64_t* freed, volatile int* abort_flag, Take& take, bool& alive, Before before,
-                                            Last last) {
+                                            uint64_t* freed, volatile int* abort_flag, Take& take, bool& alive, Before before) {
     constexpr int PAGE = 16 * D, WT = 32 / (KT / 16), RING = V ? L::RAWS : L::KSLOTS, EXPS = V ? L::RAWS : L::KEXPS;
     constexpr int OFF = V ? L::OFF_RAW : L::OFF_K, EXP = L::OFF_EXP + (V ? 0 : L::RAWS * 8);
     const int lane = threadIdx.x & 31;
@@ -666,9 +665,7 @@ __device__ __forceinline__ void load_stream(const Params& p, const CUtensorMap& 
             }
         }
         // (after a timeout no tile under way is without its scales)
-        const bool go = !alive || last(it);
         if (j == it.n) send(it.n - 1, sc);
-        if (!go) break;
     }
     if (!alive && lane == 0) *abort_flag = 1;
     // copies in flight end before the CTA does
@@ -1003,8 +1000,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     uint64_t* ofree = ofull + 2;          // [2] O(i) read by the epilogue
     uint64_t* qfull = ofree + 2;
     uint64_t* qempty = qfull + 1;
-    uint64_t* xdone = qempty + 1;         // an epilogue's use of the second Q tile is over
-    uint64_t* drain = xdone + 1;
+    uint64_t* xdone = qempty + 1;         // an epilogue's use of the second Q tile is over (K8: two, in turn)
+    uint64_t* drain = xdone + (L::K8 ? 2 : 1);
     uint64_t* gq_full = drain + 1;        // [GQ]
     uint64_t* gq_empty = gq_full + GQ;    // [GQ]
     uint64_t* xall = gq_empty + GQ;       // [2] every softmax warp has written xo, has read xo
@@ -1044,6 +1041,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         mbar_init(qfull, 1);
         mbar_init(qempty, 1);
         mbar_init(xdone, 1);
+        if constexpr (L::K8) mbar_init(xdone + 1, 1);
         mbar_init(drain, 1);
         mbar_init(&xall[0], 8);
         mbar_init(&xall[1], 8);
@@ -1121,8 +1119,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     auto load_q = [&](const Item& it) -> bool {
         const bool two = (it.flags & ITEM_TWO) != 0;
         alive = wait_all(qempty, (qi & 1u) ^ 1u);
-        // the second Q tile also serves the epilogues of single row tiles before
-        if (alive && two && xi > 0) alive = wait_all(xdone, (xi - 1) & 1u);
+        // The second Q tile also serves the epilogues of single row tiles before.  K8: two of them may be
+        // outstanding, not three: this item's Q may be loaded once the last S of the item before is done, which
+        // was issued behind the last P of the one before that, written behind the epilogues before it.  So they
+        // have two barriers in turn, of which the phase waited for is the next.
+        if constexpr (L::K8) {
+            if (alive && two && xi > 1) alive = wait_all(&xdone[xi & 1u], ((xi - 2) >> 1) & 1u);
+            if (alive && two && xi > 0) alive = wait_all(&xdone[(xi - 1) & 1u], ((xi - 1) >> 1) & 1u);
+        } else {
+            if (alive && two && xi > 0) alive = wait_all(xdone, (xi - 1) & 1u);
+        }
         if (!alive) return false;
         ++qi;
         const int nq = two ? 2 : 1;
@@ -1135,9 +1141,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         xi += (L::K8 && !two) ? 1 : 0;
         return true;
     };
-    // The second Q tile's use by the epilogue of a single row tile: one outstanding at most, or the
-    // barrier's phases could not be told apart.  (K8: warp 10, before the last tile of V is released,
-    // without which there is no epilogue.)
+    // The second Q tile's use by the epilogue of a single row tile (not K8): one outstanding at most, or the
+    // barrier's phases could not be told apart.
     auto single = [&](const Item& it) -> bool {
         if ((it.flags & ITEM_TWO) != 0) return true;
         if (xi > 0) alive = wait_all(xdone, (xi - 1) & 1u);
@@ -1238,7 +1243,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     tma_prefetch_desc(&kmap);
                     tma_prefetch_desc(&qmap);
                 }
-                load_stream<L, D, false>(p, kmap, smem, kfull, kempty, abort_flag, take, alive, load_q, [](const Item&) { return true; });
+                load_stream<L, D, false>(p, kmap, smem, kfull, kempty, abort_flag, take, alive, load_q);
                 if (!alive && lane == 0) *abort_flag = 1;
                 if (qi > 0) wait_own(qfull, (qi - 1) & 1u);
             } else {
@@ -1497,7 +1502,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     } else if (warp == FIX_WARP) {
         // ==================== Q tiles, V rows that must not reach O ====================
         if constexpr (L::K8) {
-            load_stream<L, D, true>(p, kmap, smem, rfull, rempty, abort_flag, take, alive, [](const Item&) { return true; }, single);
+            load_stream<L, D, true>(p, kmap, smem, rfull, rempty, abort_flag, take, alive, [](const Item&) { return true; });
         } else {
         if (lane == 0) tma_prefetch_desc(&qmap);
         uint32_t ld = 0, ph = 0;                              // ph: vraw's parity per slot
@@ -1578,6 +1583,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         float* xo = reinterpret_cast<float*>(smem + L::OFF_X);  // [columns][rows]
         float* ml = reinterpret_cast<float*>(smem + L::OFF_ML);
         uint32_t sc = 0, oc = 0, live = 0, xc = 0, kc = 0;    // kc: tiles of the items before
+        uint32_t xs = 0;                                       // epilogues of single row tiles before
         // every softmax warp has written xo (0), has read it (1): with a bounded wait, unlike
         // bar.sync
         auto all_x = [&](int which) {
@@ -2094,7 +2100,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 }
                 o_read();
             }
-            if (!two && it.n > 0 && tid == 0) mbar_arrive(xdone);
+            if (!two && it.n > 0) {
+                if (tid == 0) mbar_arrive(&xdone[L::K8 ? xs & 1u : 0u]);
+                ++xs;
+            }
             __syncwarp();
             if (lane == 0) remote_arrive_relaxed_after(&gq_empty[k % GQ], 0, it.b);
         }
