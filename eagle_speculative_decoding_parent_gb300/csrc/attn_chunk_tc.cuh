@@ -1879,7 +1879,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     }
                 }
                 o_read();
-                if (wrows) {
+                // (a bad sequence leaves nothing here: K8's ml lies in the second Q tile, which it has not)
+                if (wrows && it.n > 0) {
                     ml[i * 64 + row] = m_used;
                     ml[i * 64 + 32 + row] = l;
                 }
@@ -1887,7 +1888,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
 #pragma unroll 1
                 for (int e = tid; e < rows * (D / 8); e += 256) {
                     const int r = e / (D / 8), c = e % (D / 8) * 8;
-                    float m = ml[r], sum = ml[32 + r], w0 = 1.f, w1 = 0.f;
+                    float m = it.n > 0 ? ml[r] : 0.f, sum = it.n > 0 ? ml[32 + r] : 1.f, w0 = 1.f, w1 = 0.f;
                     float f[8];
 #pragma unroll
                     for (int x = 0; x < 8; ++x) f[x] = it.n > 0 ? xo[r * PITCH + c + x] : 0.f;

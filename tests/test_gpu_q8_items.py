@@ -50,3 +50,35 @@ def test_short_items_between_pairs_of_row_tiles(tv, heads, d, keys):
     c = Q.cache_case(n, P, Hq=heads[0], Hkv=heads[1], d=d, bs=16, seed=keys)
     same_and_right(tv, c)
     same_and_right(tv, c, window=5, sinks=2, softcap=20.0)
+
+
+@pytest.mark.parametrize("heads", [(16, 4), (2, 2), (64, 2)])
+@pytest.mark.parametrize("d", [128, 64])
+def test_refused_short_sequences_between_pairs_of_row_tiles(tv, heads, d):
+    """Short sequences that are refused, among chunks of two row tiles, whose queries may be there already."""
+    r = random.Random(d + heads[0])
+    tile = 128 // (heads[0] // heads[1])
+    n, bad = [], []
+    while len(n) < 150:
+        for _ in range(r.randrange(1, 4)):
+            bad.append(len(n))
+            n.append(r.randrange(1, 4))
+        n += [2 * tile] * r.randrange(1, 3)
+    P = [r.randrange(16, 200) for _ in n]
+    c = Q.cache_case(n, P, Hq=heads[0], Hkv=heads[1], d=d, bs=16, seed=d)
+    c["table"] = c["table"].clone()
+    for b in bad:
+        c["table"][b, 0] = -1
+    good = [b for b in range(len(n)) if b not in bad]
+    whole = dict(c, n=[0 if b in bad else a for b, a in enumerate(n)])
+    out, status = attend(tv, c)
+    ref, A, S = Q.attention(whole)
+    tol = R.attention_tolerance(c, ref, A, S, d)
+    start = c["q_start"].tolist()
+    for b in range(len(n)):
+        rows = slice(start[b], start[b + 1])
+        if b in bad:
+            assert status[b] == 3 and bool((out[rows] == 0).all()), b
+        else:
+            assert status[b] == 0 and bool(((out[rows].double() - ref[rows]).abs() <= tol[rows]).all()), b
+    assert good and torch.equal(attend(tv, c)[0], out)
