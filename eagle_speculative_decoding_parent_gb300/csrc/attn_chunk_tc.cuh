@@ -1583,7 +1583,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         float* xo = reinterpret_cast<float*>(smem + L::OFF_X);  // [columns][rows]
         float* ml = reinterpret_cast<float*>(smem + L::OFF_ML);
         uint32_t sc = 0, oc = 0, live = 0, xc = 0, kc = 0;    // kc: tiles of the items before
-        uint32_t xs = 0;                                       // epilogues of single row tiles before
+        // (live: items before; its top bit, K8: of xdone's two the next one)
         // every softmax warp has written xo (0), has read it (1): with a bounded wait, unlike
         // bar.sync
         auto all_x = [&](int which) {
@@ -2102,8 +2102,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 o_read();
             }
             if (!two && it.n > 0) {
-                if (tid == 0) mbar_arrive(&xdone[L::K8 ? xs & 1u : 0u]);
-                ++xs;
+                if (tid == 0) mbar_arrive(&xdone[L::K8 ? live >> 31 : 0u]);
+                if constexpr (L::K8) live ^= 1u << 31;
             }
             __syncwarp();
             if (lane == 0) remote_arrive_relaxed_after(&gq_empty[k % GQ], 0, it.b);
