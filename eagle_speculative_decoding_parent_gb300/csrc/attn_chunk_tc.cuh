@@ -56,15 +56,15 @@
 //            in the other kernels.
 //   d = 128  K's codes go to the tensor core as they are (f8f6f4), times the queries in two e4m3 parts
 //            whose sum they are; K's scales multiply the scores, 16 columns at a time.  Only V is
-//            widened: both were 1,333 us for the long chunk below, which 713 are now.  Warp 9
+//            widened: both were 1,333 us for the long chunk below, which 711 are now.  Warp 9
 //            loads K and the queries, warp 10 V; warps 12-15 split the queries.
 //   d = 64   both are widened; warp 9 loads them, warp 10 the queries.
 //   The softmax takes a tile's scores in halves of 64 columns; the running maximum is a whole
 //   number, so that the half before is rescaled exactly.
 // What bounds them is the issue of instructions, and fetching them: the sixteen warps run six
 // different loops, and unrolling any of them further costs more than it gives.  Measured: 4,096 rows after
-// 12,281 keys (28/4 heads of 128) 713 us = 1,180 TFLOP/s; 32 trees of 26 nodes after 512-8,192
-// keys (32/8 heads of 128) 84 us, 1.5 us per tile of 104 rows and some 18 us around a CTA's
+// 12,281 keys (28/4 heads of 128) 711 us = 1,183 TFLOP/s; 32 trees of 26 nodes after 512-8,192
+// keys (32/8 heads of 128) 85 us, 1.5 us per tile of 104 rows and some 18 us around a CTA's
 // tiles; 5 chunks with a window of 1,024 and a cap (16/2 heads of 64) 40 us.
 // Every wait is bounded; one that runs out sets the abort flag, which ends the other
 // roles' waits, and the roles leave after their copies and products in flight are done.
